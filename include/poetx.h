@@ -613,6 +613,71 @@ typedef struct {
 poetx_status poetx_adam_step_batch(int32_t count, const int64_t* len, float* const* q, const float* const* dq,
                                    float* const* m1, float* const* m2, const poetx_adam_params* hp, void* stream);
 
+/* ------------------------------------- norm of token rows (layer, RMS) -- */
+
+/*
+ * The normalisation that feeds a layer's linears, and its backward.  With S
+ * the row that is normalised (X, or X plus a residual stream):
+ *     mu = mean(S) (0 for POETX_NORM_RMS),  rs = 1 / sqrt(mean((S - mu)^2) + eps)
+ *     Y  = (S - mu) rs w + bias
+ * Every sum is taken in fp32, the variance around the mean.  w and bias are
+ * fp32 parameters (poetx_adam_step_batch steps them like any fp32 array).
+ */
+typedef enum { POETX_NORM_LAYER = 0, POETX_NORM_RMS = 1 } poetx_norm_kind;
+
+typedef struct {
+  int32_t d;         /* columns, 1 .. 32768 */
+  int32_t kind;      /* poetx_norm_kind */
+  int32_t act_dtype; /* POETX_F32 or POETX_BF16: X, the residual, S, Y and their gradients */
+  float eps;         /* added to the variance, finite and > 0 */
+} poetx_norm_desc;
+
+/* Bytes of the row statistics the forward saves, fp32: the means [T] then the
+ * reciprocal deviations rs [T] (POETX_NORM_LAYER), or rs [T] (POETX_NORM_RMS);
+ * 0 for invalid arguments. */
+size_t poetx_norm_stats_bytes(const poetx_norm_desc* desc, int64_t T);
+/* Workspace bytes of poetx_norm_bwd (the partial column sums of dw and db);
+ * 0 for T = 0 or invalid arguments. */
+size_t poetx_norm_workspace_size(const poetx_norm_desc* desc, int64_t T);
+
+/*
+ * Forward over T rows.  Matrices are rows of d elements with the row pitch
+ * stated (>= d, any value: rows need no alignment beyond the element's).
+ *   X      [T] pitch ldx, act_dtype
+ *   R      NULL, or the residual stream [T] pitch ldr: S = X + R, rounded to
+ *          act_dtype, is written to S and is what is normalised
+ *   w      [d] fp32, or NULL for ones;  bias  [d] fp32, or NULL for zeros
+ *          (must be NULL for POETX_NORM_RMS)
+ *   S      out [T] pitch lds with R, NULL without; may be X or R (same pitch)
+ *   Y      out [T] pitch ldy; overlaps no other operand
+ *   stats  out, poetx_norm_stats_bytes(desc, T) bytes
+ * T = 0 is a valid no-op.
+ * Errors: POETX_E_NULL, POETX_E_SHAPE, POETX_E_DTYPE, POETX_E_HIP.
+ */
+poetx_status poetx_norm_fwd(const poetx_norm_desc* desc, int64_t T, const void* X, int64_t ldx, const void* R,
+                            int64_t ldr, const float* w, const float* bias, void* S, int64_t lds, void* Y, int64_t ldy,
+                            float* stats, void* stream);
+
+/*
+ * Backward for upstream gradient dY, with xh = (S - mu) rs and g = dY w:
+ *     dX = rs (g - mean(g) - xh mean(g xh)) + dS   (no mean(g) for RMS)
+ *     dw = sum_t dY xh,  dbias = sum_t dY
+ * dX is the gradient of X and, where the forward added one, of the residual
+ * stream too; dS is the gradient that reaches S past the norm.  The sums over
+ * rows are taken in a fixed order (deterministic).
+ *   S      the rows the forward normalised: its S, or its X without a residual
+ *   stats  written by the forward of these rows
+ *   dS     NULL, or [T] pitch ldds
+ *   dX     out [T] pitch lddx; may be dY, or dS (same pitch)
+ *   dw, dbias  out fp32 [d], overwritten (zeros for T = 0); either may be
+ *          NULL, dbias must be for POETX_NORM_RMS
+ *   ws     >= poetx_norm_workspace_size(desc, T)
+ * Errors: POETX_E_NULL, POETX_E_SHAPE, POETX_E_DTYPE, POETX_E_WORKSPACE, POETX_E_HIP.
+ */
+poetx_status poetx_norm_bwd(const poetx_norm_desc* desc, int64_t T, const void* dY, int64_t lddy, const void* S,
+                            int64_t lds, const float* w, const float* stats, const void* dS, int64_t ldds, void* dX,
+                            int64_t lddx, float* dw, float* dbias, void* ws, size_t ws_bytes, void* stream);
+
 /* ----------------------------------- weight-centric baseline (comparison) -- */
 
 /*

@@ -645,3 +645,30 @@ def spo_block_grads(X: np.ndarray, dY: np.ndarray, f: SpoFactor, blocks: Sequenc
         cols = np.asarray(f.idx[s : s + r])
         out[k] = pack_skew_grad(cnp_adjoint(Q[k], X[:, cols].T @ dY[:, cols]), f.b)
     return out
+
+
+# ----------------------------------------------------------------------------
+# norm of token rows and its gradient
+# ----------------------------------------------------------------------------
+
+
+def norm_forward(S, w, bias, kind: str, eps: float):
+    """Row norm of S: (Y, mean, rs); kind "layer" or "rms" (mean 0)."""
+    mean = S.mean(1) if kind == "layer" else np.zeros(len(S))
+    c = S - mean[:, None]
+    rs = 1.0 / np.sqrt((c * c).mean(1) + eps)
+    Y = c * rs[:, None]
+    if w is not None:
+        Y = Y * w
+    return (Y if bias is None else Y + bias), mean, rs
+
+
+def norm_backward(S, dY, w, mean, rs, kind: str):
+    """(dS, dw, dbias) of norm_forward at its statistics: the Jacobian of one row is
+    rs (I - 1 1^T / d - xh xh^T / d) diag(w), without the 1 1^T term for "rms"."""
+    xh = (S - mean[:, None]) * rs[:, None]
+    g = dY if w is None else dY * w
+    t = g - xh * (g * xh).mean(1, keepdims=True)
+    if kind == "layer":
+        t = t - g.mean(1, keepdims=True)
+    return t * rs[:, None], (dY * xh).sum(0), dY.sum(0)

@@ -108,6 +108,19 @@ class BwdCall(ctypes.Structure):
     ]
 
 
+POETX_NORM_LAYER, POETX_NORM_RMS = 0, 1
+NORM_KINDS = {"layer": POETX_NORM_LAYER, "rms": POETX_NORM_RMS}
+
+
+class NormDesc(ctypes.Structure):
+    _fields_ = [
+        ("d", ctypes.c_int32),
+        ("kind", ctypes.c_int32),
+        ("act_dtype", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+    ]
+
+
 class AdamParams(ctypes.Structure):
     _fields_ = [
         ("lr", ctypes.c_float),
@@ -207,6 +220,18 @@ _SIG = {
     "poetx_wc_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(LayerDesc), ctypes.c_int64, ctypes.c_int32]),
     "poetx_wc_fwd": (ctypes.c_int, [ctypes.POINTER(LayerDesc), ctypes.c_int64] + [_P] * 9 + [ctypes.c_size_t, _P]),
     "poetx_wc_bwd": (ctypes.c_int, [ctypes.POINTER(LayerDesc), ctypes.c_int64] + [_P] * 12 + [ctypes.c_size_t, _P]),
+    "poetx_norm_stats_bytes": (ctypes.c_size_t, [ctypes.POINTER(NormDesc), ctypes.c_int64]),
+    "poetx_norm_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(NormDesc), ctypes.c_int64]),
+    "poetx_norm_fwd": (
+        ctypes.c_int,
+        [ctypes.POINTER(NormDesc), ctypes.c_int64, _P, ctypes.c_int64, _P, ctypes.c_int64, _P, _P, _P, ctypes.c_int64, _P,
+         ctypes.c_int64, _P, _P],
+    ),
+    "poetx_norm_bwd": (
+        ctypes.c_int,
+        [ctypes.POINTER(NormDesc), ctypes.c_int64, _P, ctypes.c_int64, _P, ctypes.c_int64, _P, _P, _P, ctypes.c_int64, _P,
+         ctypes.c_int64, _P, _P, _P, ctypes.c_size_t, _P],
+    ),
     "poetx_adam_step_batch": (
         ctypes.c_int,
         [ctypes.c_int32, ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(_P), ctypes.POINTER(_P), ctypes.POINTER(_P),
@@ -466,6 +491,31 @@ def poetx_adam_step_batch(q, dq, m1, m2, lr: float, beta1: float, beta2: float, 
     hp = AdamParams(lr, beta1, beta2, eps, weight_decay, t)
     _check(lib().poetx_adam_step_batch(len(lens), (ctypes.c_int64 * len(lens))(*lens), _ptr_array(q), _ptr_array(dq),
                                        _ptr_array(m1), _ptr_array(m2), ctypes.byref(hp), _stream(stream)))
+
+
+# ------------------------------------------------------- norm of token rows ---
+def norm_desc(d: int, kind: str, act: str, eps: float = 1e-5) -> NormDesc:
+    return NormDesc(d, NORM_KINDS[kind], DTYPES[act], eps)
+
+
+def poetx_norm_stats_bytes(dsc: NormDesc, T: int) -> int:
+    return lib().poetx_norm_stats_bytes(ctypes.byref(dsc), T)
+
+
+def poetx_norm_workspace_size(dsc: NormDesc, T: int) -> int:
+    return lib().poetx_norm_workspace_size(ctypes.byref(dsc), T)
+
+
+def poetx_norm_fwd(dsc: NormDesc, T: int, X, ldx: int, R, ldr: int, w, bias, S, lds: int, Y, ldy: int, stats,
+                   stream=None):
+    _check(lib().poetx_norm_fwd(ctypes.byref(dsc), T, _ptr(X), ldx, _ptr(R), ldr, _ptr(w), _ptr(bias), _ptr(S), lds,
+                                _ptr(Y), ldy, _ptr(stats), _stream(stream)))
+
+
+def poetx_norm_bwd(dsc: NormDesc, T: int, dY, lddy: int, S, lds: int, w, stats, dS, ldds: int, dX, lddx: int, dw,
+                   dbias, ws, ws_bytes: int, stream=None):
+    _check(lib().poetx_norm_bwd(ctypes.byref(dsc), T, _ptr(dY), lddy, _ptr(S), lds, _ptr(w), _ptr(stats), _ptr(dS),
+                                ldds, _ptr(dX), lddx, _ptr(dw), _ptr(dbias), _ptr(ws), ws_bytes, _stream(stream)))
 
 
 # ------------------------------------------------------------ one SPO factor ---

@@ -92,6 +92,7 @@ poetx_status fail(poetx_status st, const std::string& msg) {
 
 constexpr int64_t kMaxDim = int64_t(1) << 20;
 constexpr int64_t kMaxT = (int64_t(1) << 31) - 1;
+constexpr int64_t kMaxNormT = int64_t(1) << 30;  // row numbers stay 32-bit with a grid's step added
 
 poetx_status check_desc(const poetx_layer_desc* d) {
   if (!d) return fail(POETX_E_NULL, "desc is NULL");
@@ -1553,6 +1554,95 @@ poetx_status poetx_store_weight(const poetx_layer_desc* desc, const float* W, in
   PX_HIP(zero_cols(wt, Wt, lead(n), m, n, (int)lead(n), s));
   if (has_weight_t(desc))
     PX_HIP(transpose(wt, Wt, lead(n), m, n, reinterpret_cast<char*>(Wt) + weight_t_offset(desc), lead(m), s));
+  return POETX_OK;
+}
+
+}  // extern "C"
+
+// ---------------------------------------------------------------------------
+// norm of token rows
+// ---------------------------------------------------------------------------
+namespace {
+
+poetx_status check_norm(const poetx_norm_desc* d, int64_t T) {
+  if (!d) return fail(POETX_E_NULL, "desc is NULL");
+  if (d->d < 1 || d->d > kNormMaxD) return fail(POETX_E_SHAPE, "d must be in [1, 32768]");
+  if (d->kind != POETX_NORM_LAYER && d->kind != POETX_NORM_RMS)
+    return fail(POETX_E_SHAPE, "kind must be POETX_NORM_LAYER or POETX_NORM_RMS");
+  if (d->act_dtype != POETX_F32 && d->act_dtype != POETX_BF16)
+    return fail(POETX_E_DTYPE, "act_dtype must be F32 or BF16");
+  if (!(std::isfinite(d->eps) && d->eps > 0.f)) return fail(POETX_E_SHAPE, "eps must be finite and > 0");
+  if (T < 0 || T > kMaxNormT) return fail(POETX_E_SHAPE, "T must be in [0, 2^30]");
+  return POETX_OK;
+}
+
+int norm_vecs(const poetx_norm_desc* d) { return d->kind == POETX_NORM_RMS ? 1 : 2; }
+
+// a matrix operand of T rows: its row pitch, and its base on an element boundary
+poetx_status check_pitch(const char* name, const void* p, int64_t ld, const poetx_norm_desc* d) {
+  if (ld < d->d) return fail(POETX_E_SHAPE, std::string(name) + ": the row pitch must be at least d");
+  if (reinterpret_cast<uintptr_t>(p) % dt_size(d->act_dtype))
+    return fail(POETX_E_SHAPE, std::string(name) + " must be aligned to its element");
+  return POETX_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t poetx_norm_stats_bytes(const poetx_norm_desc* desc, int64_t T) {
+  if (check_norm(desc, T) != POETX_OK) return 0;
+  return (size_t)norm_vecs(desc) * T * 4;
+}
+
+size_t poetx_norm_workspace_size(const poetx_norm_desc* desc, int64_t T) {
+  if (check_norm(desc, T) != POETX_OK) return 0;
+  return (size_t)norm_bwd_parts(T, desc->d) * norm_vecs(desc) * desc->d * 4;
+}
+
+poetx_status poetx_norm_fwd(const poetx_norm_desc* desc, int64_t T, const void* X, int64_t ldx, const void* R,
+                            int64_t ldr, const float* w, const float* bias, void* S, int64_t lds, void* Y, int64_t ldy,
+                            float* stats, void* stream) {
+  poetx_status st = check_norm(desc, T);
+  if (st != POETX_OK) return st;
+  const bool rms = desc->kind == POETX_NORM_RMS;
+  if (rms && bias) return fail(POETX_E_SHAPE, "an RMS norm takes no bias");
+  if (T == 0) return POETX_OK;
+  if (!X || !Y || !stats) return fail(POETX_E_NULL, "X, Y and stats must be non-NULL");
+  if ((R != nullptr) != (S != nullptr)) return fail(POETX_E_NULL, "S is written with a residual R, and only then");
+  if ((st = check_pitch("X", X, ldx, desc)) != POETX_OK) return st;
+  if ((st = check_pitch("Y", Y, ldy, desc)) != POETX_OK) return st;
+  if (R && (st = check_pitch("R", R, ldr, desc)) != POETX_OK) return st;
+  if (S && (st = check_pitch("S", S, lds, desc)) != POETX_OK) return st;
+  if (Y == X || (R && (Y == R || Y == S))) return fail(POETX_E_SHAPE, "Y must not be X, R or S");
+  if (S && ((S == X && lds != ldx) || (S == R && lds != ldr)))
+    return fail(POETX_E_SHAPE, "S in place of X or R must have its pitch");
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  PX_HIP(norm_fwd(desc->act_dtype, rms, T, desc->d, desc->eps, X, ldx, R, ldr, w, bias, S, lds, Y, ldy, stats, s));
+  return POETX_OK;
+}
+
+poetx_status poetx_norm_bwd(const poetx_norm_desc* desc, int64_t T, const void* dY, int64_t lddy, const void* S,
+                            int64_t lds, const float* w, const float* stats, const void* dS, int64_t ldds, void* dX,
+                            int64_t lddx, float* dw, float* dbias, void* ws, size_t ws_bytes, void* stream) {
+  poetx_status st = check_norm(desc, T);
+  if (st != POETX_OK) return st;
+  const bool rms = desc->kind == POETX_NORM_RMS;
+  if (rms && dbias) return fail(POETX_E_SHAPE, "an RMS norm has no bias");
+  if (T > 0) {
+    if (!dY || !S || !stats || !dX) return fail(POETX_E_NULL, "dY, S, stats and dX must be non-NULL");
+    if ((st = check_pitch("dY", dY, lddy, desc)) != POETX_OK) return st;
+    if ((st = check_pitch("S", S, lds, desc)) != POETX_OK) return st;
+    if ((st = check_pitch("dX", dX, lddx, desc)) != POETX_OK) return st;
+    if (dS && (st = check_pitch("dS", dS, ldds, desc)) != POETX_OK) return st;
+    if ((dX == dY && lddx != lddy) || (dX == dS && lddx != ldds))
+      return fail(POETX_E_SHAPE, "dX in place of dY or dS must have its pitch");
+    if (dX == S) return fail(POETX_E_SHAPE, "dX must not be S");
+    if ((st = check_ws(ws, ws_bytes, poetx_norm_workspace_size(desc, T))) != POETX_OK) return st;
+  }
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  PX_HIP(norm_bwd(desc->act_dtype, rms, T, desc->d, dY, lddy, S, lds, w, stats, dS, ldds, dX, lddx, dw, dbias,
+                  reinterpret_cast<float*>(ws), s));
   return POETX_OK;
 }
 

@@ -170,4 +170,15 @@ struct AdamHyper {
 hipError_t adam_batch(int count, const int64_t* len, float* const* q, const float* const* g, float* const* m1,
                       float* const* m2, const AdamHyper& hp, hipStream_t s);
 
+// Layer norm (rms: RMS norm) of T rows of d, and its backward (poetx_norm.hip).  R, w, b, dS, dw and db may be
+// null.  part: norm_bwd_parts(T, d) rows of (rms ? 1 : 2) d floats.
+constexpr int kNormMaxD = 32768;
+int norm_bwd_parts(int64_t T, int d);
+hipError_t norm_fwd(int dt, bool rms, int64_t T, int d, float eps, const void* X, int64_t ldx, const void* R,
+                    int64_t ldr, const float* w, const float* b, void* S, int64_t lds, void* Y, int64_t ldy,
+                    float* stats, hipStream_t s);
+hipError_t norm_bwd(int dt, bool rms, int64_t T, int d, const void* dY, int64_t ldy, const void* S, int64_t lds,
+                    const float* w, const float* stats, const void* dS, int64_t ldds, void* dX, int64_t ldx, float* dw,
+                    float* db, float* part, hipStream_t s);
+
 }  // namespace pxk

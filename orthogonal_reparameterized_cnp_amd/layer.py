@@ -653,3 +653,121 @@ class PoetxWeightCentric:
         B.poetx_wc_bwd(L.desc, T, dZ, L.perm_R, L.perm_P, L.g_R, L.g_P, L.q_R, L.q_P, self.state, dX, dq_R, dq_P,
                        self.ws, self.ws.numel(), stream)
         return dX, dq_R, dq_P
+
+
+@contextlib.contextmanager
+def _on(device: torch.device, stream):
+    """The layer's device current and, where one is given, the stream: allocations and launches inside
+    belong to it.  Raises TypeError for anything but a torch.cuda.Stream or None."""
+    if stream is not None and not isinstance(stream, torch.cuda.Stream):
+        raise TypeError("stream must be a torch.cuda.Stream or None")
+    with torch.cuda.device(device):
+        if stream is None:
+            yield
+        else:
+            if stream.device_index != torch.cuda.current_device():
+                raise ValueError(f"stream is on cuda:{stream.device_index}, the operands on {device}")
+            with torch.cuda.stream(stream):
+                yield
+
+
+def _pitch(t, name: str, T: int, d: int, dtype: torch.dtype, device: torch.device) -> int:
+    """Row pitch of a [T, d] matrix whose rows are contiguous; ValueError for any other tensor."""
+    if not isinstance(t, torch.Tensor):
+        raise ValueError(f"{name} must be a torch.Tensor")
+    if tuple(t.shape) != (T, d):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {(T, d)}")
+    if t.dtype != dtype:
+        raise ValueError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if d > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    _check_device(device, **{name: t})
+    ld = t.stride(0) if T > 1 else d
+    if ld < d:
+        raise ValueError(f"{name} has overlapping rows (row stride {ld} < {d})")
+    return ld
+
+
+class PoetxNorm:
+    """Layer norm (kind "layer") or RMS norm (kind "rms") of token rows, with fp32 weight and, for
+    "layer", bias (poetx_norm_fwd / poetx_norm_bwd).  forward(X) returns Y; forward(X, residual) returns
+    (Y, S) with S = X + residual, the stream the next residual is added to.  The norm keeps S (X without a
+    residual) and the row statistics for the backward: neither may be overwritten before it.
+
+    weight and bias are plain fp32 tensors; their gradients are what poetx_adam_step_batch takes."""
+
+    def __init__(self, d: int, kind: str = "layer", act: str = "bf16", eps: float = 1e-5, bias: bool = True,
+                 device: str = "cuda"):
+        if kind not in B.NORM_KINDS:
+            raise ValueError(f"kind must be one of {sorted(B.NORM_KINDS)}")
+        if act not in ("f32", "bf16"):
+            raise ValueError("act must be f32 or bf16")
+        self.d, self.kind, self.act, self.eps = d, kind, act, eps
+        self.device = torch.device(device)
+        self.desc = B.norm_desc(d, kind, act, eps)
+        self.weight = torch.ones(d, dtype=torch.float32, device=self.device)
+        self.bias = torch.zeros(d, dtype=torch.float32, device=self.device) if bias and kind == "layer" else None
+        self.S: Optional[torch.Tensor] = None  # the rows of the last forward
+        self.stats: Optional[torch.Tensor] = None
+
+    def _params(self):
+        _check(self.weight, "weight", (self.d,), torch.float32)
+        if self.bias is not None:
+            _check(self.bias, "bias", (self.d,), torch.float32)
+        _check_device(self.device, weight=self.weight, bias=self.bias)
+
+    def forward(self, X: torch.Tensor, residual: Optional[torch.Tensor] = None, Y: Optional[torch.Tensor] = None,
+                S: Optional[torch.Tensor] = None, stream=None):
+        if not isinstance(X, torch.Tensor) or X.dim() != 2:
+            raise ValueError("X must be a 2-D tensor [T, d]")
+        T, d, dt, dev = X.shape[0], self.d, _TORCH_DT[self.act], self.device
+        ldx = _pitch(X, "X", T, d, dt, dev)
+        ldr = _pitch(residual, "residual", T, d, dt, dev) if residual is not None else d
+        if S is not None and residual is None:
+            raise ValueError("S is the sum with a residual: pass the residual")
+        ldy = _pitch(Y, "Y", T, d, dt, dev) if Y is not None else d
+        lds = _pitch(S, "S", T, d, dt, dev) if S is not None else d
+        self._params()
+        with _on(dev, stream):
+            if Y is None:
+                Y = torch.empty(T, d, dtype=dt, device=dev)
+            if S is None and residual is not None:
+                S = torch.empty(T, d, dtype=dt, device=dev)
+            stats = torch.empty(2 if self.kind == "layer" else 1, T, dtype=torch.float32, device=dev)
+            B.poetx_norm_fwd(self.desc, T, X, ldx, residual, ldr, self.weight, self.bias, S, lds, Y, ldy, stats)
+        self.S, self.stats = (X if S is None else S), stats
+        return Y if residual is None else (Y, S)
+
+    def backward(self, dY: torch.Tensor, dS: Optional[torch.Tensor] = None, dX: Optional[torch.Tensor] = None,
+                 dw: Optional[torch.Tensor] = None, db: Optional[torch.Tensor] = None, stream=None):
+        """(dX, dw, db) for the rows of the last forward (db None without a bias).  dS: the gradient that
+        reaches S past the norm, added to dX, which is then the gradient of X and of the residual."""
+        if self.S is None:
+            raise ValueError("backward before a forward: there is no saved state")
+        if not isinstance(dY, torch.Tensor) or dY.dim() != 2:
+            raise ValueError("dY must be a 2-D tensor [T, d]")
+        T, d, dt, dev = dY.shape[0], self.d, _TORCH_DT[self.act], self.device
+        if T != self.S.shape[0]:
+            raise ValueError(f"backward over {T} rows, but the saved state is from a forward of {self.S.shape[0]}")
+        ldy = _pitch(dY, "dY", T, d, dt, dev)
+        lds = _pitch(self.S, "S", T, d, dt, dev)
+        ldds = _pitch(dS, "dS", T, d, dt, dev) if dS is not None else d
+        ldx = _pitch(dX, "dX", T, d, dt, dev) if dX is not None else d
+        for name, t in (("dw", dw), ("db", db)):
+            if t is not None:
+                _check(t, name, (d,), torch.float32)
+        if db is not None and self.bias is None:
+            raise ValueError("db given, but the norm has no bias")
+        _check_device(dev, dw=dw, db=db)
+        self._params()
+        with _on(dev, stream):
+            if dX is None:
+                dX = torch.empty(T, d, dtype=dt, device=dev)
+            if dw is None:
+                dw = torch.empty(d, dtype=torch.float32, device=dev)
+            if db is None and self.bias is not None:
+                db = torch.empty(d, dtype=torch.float32, device=dev)
+            ws = torch.empty(B.poetx_norm_workspace_size(self.desc, T), dtype=torch.uint8, device=dev)
+            B.poetx_norm_bwd(self.desc, T, dY, ldy, self.S, lds, self.weight, self.stats, dS, ldds, dX, ldx, dw, db, ws,
+                             ws.numel())
+        return dX, dw, db
