@@ -613,6 +613,83 @@ typedef struct {
 poetx_status poetx_adam_step_batch(int32_t count, const int64_t* len, float* const* q, const float* const* dq,
                                    float* const* m1, float* const* m2, const poetx_adam_params* hp, void* stream);
 
+/* --------------------- orthogonalised updates (Newton-Schulz products) -- */
+
+/*
+ * The orthogonalisation of an update matrix M (r x k, r <= k): every singular
+ * value is brought near 1 with the singular vectors kept, by `steps` products
+ *     X_0 = M / (|M|_F + eps),  A = X X^T,  X <- a X + (b A + c A^2) X
+ * (Newton-Schulz iterations of the polynomial p(s) = a s + b s^3 + c s^5 on the
+ * singular values).  p must keep singular values in [0, 1] within a bounded
+ * range over all steps: with S_0 = 1 and S_{i+1} = max |p| on [0, S_i], the
+ * calls refuse coefficients with S_i > 4 or |b| S_i^2 + |c| S_i^4 > 200.
+ * A zero matrix gives zeros.
+ */
+typedef struct {
+  int32_t steps; /* 1 .. 20 */
+  float a, b, c; /* finite; 3.4445, -4.7750, 2.0315 take [2e-3, 1] into [0.68, 1.21] in 5 steps */
+  float eps;     /* added to the Frobenius norm, finite and > 0 */
+  float rms;     /* > 0: the result is multiplied by rms sqrt(max(rows, cols)), which makes rms the
+                    root mean square of an orthogonal result's entries; 0: it is not */
+} poetx_ns_params;
+
+typedef struct {
+  float lr;           /* step size, finite and >= 0 */
+  float beta;         /* decay of the momentum, in [0, 1) */
+  float weight_decay; /* decoupled decay rate, finite (0 disables it) */
+  int32_t nesterov;   /* 0 or 1 */
+  poetx_ns_params ns;
+} poetx_muon_params;
+
+/* Workspace bytes of poetx_muon_step_batch for `count` sides of lengths d[i]
+ * (host array) and block size b (0 for b <= 128, which needs none); 0 for
+ * invalid arguments. */
+size_t poetx_muon_workspace_size(int32_t count, const int32_t* d, int32_t b);
+
+/*
+ * One optimiser step on the packed skew parameters of `count` sides, in place,
+ * with the update of every block orthogonalised (the momentum of a block is
+ * the packed half of a skew r x r matrix, r = min(b, d - k b), and so is its
+ * orthogonalised form):
+ *     m = beta m + (1 - beta) dq;  u = nesterov ? beta m + (1 - beta) dq : m
+ *     O = orthogonalisation of the skew matrix of u, per block
+ *     q = q - lr (O + weight_decay q)
+ * The products are as exact as fp32 products, all else is fp32 (the norms
+ * 64 bits).  The slots that a partial block does not use (j >= r) are neither
+ * read nor written.
+ *   q, m   HOST arrays [count] of device pointers to fp32
+ *          [ceil(d[i]/b)][b(b-1)/2], read and overwritten (m: momentum)
+ *   dq     HOST array [count] of device pointers to the gradients, read only
+ *   ws     >= poetx_muon_workspace_size(count, d, b), 256-byte aligned
+ * The arrays must not overlap.  count 1 .. POETX_MAX_SIDES; b 2 .. 1024.
+ * Errors: POETX_E_NULL, POETX_E_SHAPE (a size or parameter out of range),
+ * POETX_E_WORKSPACE, POETX_E_HIP.
+ */
+poetx_status poetx_muon_step_batch(int32_t count, float* const* q, const float* const* dq, float* const* m,
+                                   const int32_t* d, int32_t b, const poetx_muon_params* hp, void* ws, size_t ws_bytes,
+                                   void* stream);
+
+/* Workspace bytes of poetx_orthogonalize; 0 for invalid arguments. */
+size_t poetx_orthogonalize_workspace_size(int32_t count, int32_t rows, int32_t cols, int32_t dtype);
+
+/*
+ * The orthogonalisation of `count` dense matrices of one shape, for the
+ * parameters of a model that stay dense.
+ *   rows, cols  1 .. 131072;  count  1 .. 1024;  dtype  POETX_F32 or POETX_BF16
+ *   G      matrix i at G + i stride_g elements, rows ld_g >= cols apart
+ *   O      out, likewise with stride_o and ld_o; may be G itself (same ld and
+ *          stride), else they must not overlap.  The strides matter for
+ *          count > 1 only, where they must be at least (rows - 1) ld + cols.
+ *   ws     >= poetx_orthogonalize_workspace_size(count, rows, cols, dtype)
+ * POETX_F32: products as exact as fp32 products.  POETX_BF16: fp16 operands
+ * (11 bits) with fp32 sums, about 2e-3 of the result's norm, and the result
+ * rounded to bf16 once.
+ * Errors: POETX_E_NULL, POETX_E_SHAPE, POETX_E_DTYPE, POETX_E_WORKSPACE, POETX_E_HIP.
+ */
+poetx_status poetx_orthogonalize(int32_t count, int32_t rows, int32_t cols, int32_t dtype, const void* G, int64_t ld_g,
+                                 int64_t stride_g, void* O, int64_t ld_o, int64_t stride_o, const poetx_ns_params* hp,
+                                 void* ws, size_t ws_bytes, void* stream);
+
 /* ------------------------------------- norm of token rows (layer, RMS) -- */
 
 /*

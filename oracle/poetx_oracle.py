@@ -672,3 +672,68 @@ def norm_backward(S, dY, w, mean, rs, kind: str):
     if kind == "layer":
         t = t - g.mean(1, keepdims=True)
     return t * rs[:, None], (dY * xh).sum(0), dY.sum(0)
+
+
+# ----------------------------------------------------------------------------
+# orthogonalised updates (Newton-Schulz products)
+# ----------------------------------------------------------------------------
+
+
+@dataclass
+class NsHP:
+    steps: int = 5
+    a: float = 3.4445
+    b: float = -4.7750
+    c: float = 2.0315
+    eps: float = 1e-7
+    rms: float = 0.2
+
+
+def ns_iterates(M: np.ndarray, hp: NsHP) -> List[np.ndarray]:
+    """X_0 = M / (|M|_F + eps), X_{k+1} = a X_k + (b A + c A^2) X_k with A = X_k X_k^T."""
+    X = [M / (np.linalg.norm(M) + hp.eps)]
+    for _ in range(hp.steps):
+        A = X[-1] @ X[-1].T
+        X.append(hp.a * X[-1] + (hp.b * A + hp.c * (A @ A)) @ X[-1])
+    return X
+
+
+def ns_scale(rows: int, cols: int, hp: NsHP) -> float:
+    return hp.rms * np.sqrt(max(rows, cols)) if hp.rms > 0 else 1.0
+
+
+def orthogonalize(M: np.ndarray, hp: NsHP) -> np.ndarray:
+    W = M if M.shape[0] <= M.shape[1] else M.T
+    O = ns_iterates(W, hp)[-1] * ns_scale(*M.shape, hp)
+    return O if M.shape[0] <= M.shape[1] else O.T
+
+
+@dataclass
+class MuonHP:
+    lr: float = 1e-3
+    beta: float = 0.95
+    weight_decay: float = 0.0
+    nesterov: bool = True
+    ns: NsHP = None
+
+
+def muon_update(g, m, hp: MuonHP):
+    """(momentum, update) of one step, elementwise."""
+    m = hp.beta * m + (1 - hp.beta) * g
+    return m, (hp.beta * m + (1 - hp.beta) * g if hp.nesterov else m)
+
+
+def muon_step(q, g, m, d: int, b: int, hp: MuonHP):
+    """One step on the packed parameters [nb][b(b-1)/2] of a side; the slots a partial block does not use keep
+    their q and m."""
+    q, m = q.copy(), m.copy()
+    i, j = np.triu_indices(b, 1)
+    for k, r in enumerate(min(b, d - k * b) for k in range(-(-d // b))):
+        live = j < r
+        mk, u = muon_update(g[k][live], m[k][live], hp)
+        M = np.zeros((r, r))
+        M[i[live], j[live]] = u
+        O = orthogonalize(M - M.T, hp.ns)
+        m[k][live] = mk
+        q[k][live] = q[k][live] - hp.lr * (O[i[live], j[live]] + hp.weight_decay * q[k][live])
+    return q, m

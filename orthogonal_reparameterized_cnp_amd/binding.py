@@ -132,6 +132,27 @@ class AdamParams(ctypes.Structure):
     ]
 
 
+class NsParams(ctypes.Structure):
+    _fields_ = [
+        ("steps", ctypes.c_int32),
+        ("a", ctypes.c_float),
+        ("b", ctypes.c_float),
+        ("c", ctypes.c_float),
+        ("eps", ctypes.c_float),
+        ("rms", ctypes.c_float),
+    ]
+
+
+class MuonParams(ctypes.Structure):
+    _fields_ = [
+        ("lr", ctypes.c_float),
+        ("beta", ctypes.c_float),
+        ("weight_decay", ctypes.c_float),
+        ("nesterov", ctypes.c_int32),
+        ("ns", NsParams),
+    ]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 _P = ctypes.c_void_p
@@ -220,6 +241,20 @@ _SIG = {
     "poetx_wc_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(LayerDesc), ctypes.c_int64, ctypes.c_int32]),
     "poetx_wc_fwd": (ctypes.c_int, [ctypes.POINTER(LayerDesc), ctypes.c_int64] + [_P] * 9 + [ctypes.c_size_t, _P]),
     "poetx_wc_bwd": (ctypes.c_int, [ctypes.POINTER(LayerDesc), ctypes.c_int64] + [_P] * 12 + [ctypes.c_size_t, _P]),
+    "poetx_muon_workspace_size": (ctypes.c_size_t, [ctypes.c_int32, ctypes.POINTER(ctypes.c_int32), ctypes.c_int32]),
+    "poetx_muon_step_batch": (
+        ctypes.c_int,
+        [ctypes.c_int32, ctypes.POINTER(_P), ctypes.POINTER(_P), ctypes.POINTER(_P), ctypes.POINTER(ctypes.c_int32),
+         ctypes.c_int32, ctypes.POINTER(MuonParams), _P, ctypes.c_size_t, _P],
+    ),
+    "poetx_orthogonalize_workspace_size": (
+        ctypes.c_size_t, [ctypes.c_int32, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32]
+    ),
+    "poetx_orthogonalize": (
+        ctypes.c_int,
+        [ctypes.c_int32] * 4 + [_P, ctypes.c_int64, ctypes.c_int64, _P, ctypes.c_int64, ctypes.c_int64,
+                                ctypes.POINTER(NsParams), _P, ctypes.c_size_t, _P],
+    ),
     "poetx_norm_stats_bytes": (ctypes.c_size_t, [ctypes.POINTER(NormDesc), ctypes.c_int64]),
     "poetx_norm_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(NormDesc), ctypes.c_int64]),
     "poetx_norm_fwd": (
@@ -491,6 +526,37 @@ def poetx_adam_step_batch(q, dq, m1, m2, lr: float, beta1: float, beta2: float, 
     hp = AdamParams(lr, beta1, beta2, eps, weight_decay, t)
     _check(lib().poetx_adam_step_batch(len(lens), (ctypes.c_int64 * len(lens))(*lens), _ptr_array(q), _ptr_array(dq),
                                        _ptr_array(m1), _ptr_array(m2), ctypes.byref(hp), _stream(stream)))
+
+
+# ------------------------------------------------------ orthogonalised updates ---
+def ns_params(steps: int = 5, a: float = 3.4445, b: float = -4.7750, c: float = 2.0315, eps: float = 1e-7,
+              rms: float = 0.2) -> NsParams:
+    return NsParams(steps, a, b, c, eps, rms)
+
+
+def muon_params(lr: float, beta: float = 0.95, weight_decay: float = 0.0, nesterov: bool = True, **ns) -> MuonParams:
+    """ns: the keyword arguments of ns_params."""
+    return MuonParams(lr, beta, weight_decay, int(nesterov), ns_params(**ns))
+
+
+def poetx_muon_workspace_size(d, b: int) -> int:
+    return lib().poetx_muon_workspace_size(len(d), _i32_array(d), b)
+
+
+def poetx_muon_step_batch(q, dq, m, d, b: int, hp: MuonParams, ws, ws_bytes: int, stream=None):
+    """q, dq, m, d: per-side lists (fp32 device tensors / ints), marshalled into host arrays."""
+    _check(lib().poetx_muon_step_batch(len(d), _ptr_array(q), _ptr_array(dq), _ptr_array(m), _i32_array(d), b,
+                                       ctypes.byref(hp), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def poetx_orthogonalize_workspace_size(count: int, rows: int, cols: int, dtype: int) -> int:
+    return lib().poetx_orthogonalize_workspace_size(count, rows, cols, dtype)
+
+
+def poetx_orthogonalize(count: int, rows: int, cols: int, dtype: int, G, ld_g: int, stride_g: int, O, ld_o: int,
+                        stride_o: int, hp: NsParams, ws, ws_bytes: int, stream=None):
+    _check(lib().poetx_orthogonalize(count, rows, cols, dtype, _ptr(G), ld_g, stride_g, _ptr(O), ld_o, stride_o,
+                                     ctypes.byref(hp), _ptr(ws), ws_bytes, _stream(stream)))
 
 
 # ------------------------------------------------------- norm of token rows ---

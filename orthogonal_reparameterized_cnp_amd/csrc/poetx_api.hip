@@ -1647,3 +1647,119 @@ poetx_status poetx_norm_bwd(const poetx_norm_desc* desc, int64_t T, const void* 
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------------------
+// orthogonalised updates
+// ---------------------------------------------------------------------------
+namespace {
+
+poetx_status check_ns(const poetx_ns_params& n) {
+  if (n.steps < 1 || n.steps > 20) return fail(POETX_E_SHAPE, "steps must be in [1, 20]");
+  if (!std::isfinite(n.a) || !std::isfinite(n.b) || !std::isfinite(n.c))
+    return fail(POETX_E_SHAPE, "a, b and c must be finite");
+  if (!(std::isfinite(n.eps) && n.eps > 0.f)) return fail(POETX_E_SHAPE, "eps of the norm must be finite and > 0");
+  if (!(std::isfinite(n.rms) && n.rms >= 0.f)) return fail(POETX_E_SHAPE, "rms must be finite and >= 0");
+  // the largest singular value over the steps: p's extremes on [0, S] are at S and where p' = a + 3 b x + 5 c x^2 = 0
+  const double a = n.a, b = n.b, c = n.c;
+  auto p = [&](double s) { return std::fabs(s * (a + s * s * (b + s * s * c))); };
+  double S = 1.0;
+  for (int i = 0; i < n.steps; ++i) {
+    if (std::fabs(b) * S * S + std::fabs(c) * S * S * S * S > 200.0)
+      return fail(POETX_E_SHAPE, "a, b, c: the polynomial's terms leave the range of the products");
+    double x[2] = {-1.0, -1.0};  // s^2 of the interior extremes
+    if (c == 0.0) {
+      if (b != 0.0) x[0] = -a / (3.0 * b);
+    } else {
+      const double disc = 9.0 * b * b - 20.0 * a * c;
+      if (disc >= 0.0) {
+        x[0] = (-3.0 * b + std::sqrt(disc)) / (10.0 * c);
+        x[1] = (-3.0 * b - std::sqrt(disc)) / (10.0 * c);
+      }
+    }
+    double next = p(S);
+    for (double v : x)
+      if (v > 0.0 && v < S * S) next = std::max(next, p(std::sqrt(v)));
+    S = next;
+    if (!(S <= 4.0)) return fail(POETX_E_SHAPE, "a, b, c: the steps do not keep the singular values bounded");
+  }
+  return POETX_OK;
+}
+
+NsHyper ns_hyper(const poetx_ns_params& n) { return NsHyper{n.steps, n.a, n.b, n.c, n.eps, n.rms}; }
+
+poetx_status check_orth(int32_t count, int32_t rows, int32_t cols, int32_t dtype) {
+  if (count < 1 || count > 1024) return fail(POETX_E_SHAPE, "count must be in [1, 1024]");
+  if (rows < 1 || cols < 1 || rows > (1 << 17) || cols > (1 << 17))
+    return fail(POETX_E_SHAPE, "rows and cols must be in [1, 131072]");
+  // one launch's tiles (of 128 x 128, by up to 32 splits) stay within a grid dimension
+  if ((double)count * (rows / 128 + 1) * (cols / 128 + 1) > (double)(1 << 25))
+    return fail(POETX_E_SHAPE, "count * rows * cols is too large for one call");
+  if (dtype != POETX_F32 && dtype != POETX_BF16) return fail(POETX_E_DTYPE, "dtype must be F32 or BF16");
+  return POETX_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t poetx_muon_workspace_size(int32_t count, const int32_t* d, int32_t b) {
+  int64_t nb;
+  if (check_sides(count, d, b, POETX_F32, &nb) != POETX_OK) return 0;
+  return muon_ws_bytes(nb, b);
+}
+
+poetx_status poetx_muon_step_batch(int32_t count, float* const* q, const float* const* dq, float* const* m,
+                                   const int32_t* d, int32_t b, const poetx_muon_params* hp, void* ws, size_t ws_bytes,
+                                   void* stream) {
+  int64_t nb;
+  poetx_status st = check_sides(count, d, b, POETX_F32, &nb);
+  if (st != POETX_OK) return st;
+  if (!q || !dq || !m || !hp) return fail(POETX_E_NULL, "q, dq, m and hp must be non-NULL");
+  if (!(std::isfinite(hp->lr) && hp->lr >= 0.f)) return fail(POETX_E_SHAPE, "lr must be finite and >= 0");
+  if (!(hp->beta >= 0.f && hp->beta < 1.f)) return fail(POETX_E_SHAPE, "beta must be in [0, 1)");
+  if (!std::isfinite(hp->weight_decay)) return fail(POETX_E_SHAPE, "weight_decay must be finite");
+  if (hp->nesterov != 0 && hp->nesterov != 1) return fail(POETX_E_SHAPE, "nesterov must be 0 or 1");
+  if ((st = check_ns(hp->ns)) != POETX_OK) return st;
+  for (int i = 0; i < count; ++i)
+    if (!q[i] || !dq[i] || !m[i]) return fail(POETX_E_NULL, "q[i], dq[i] and m[i] must be non-NULL");
+  if ((st = check_ws(ws, ws_bytes, muon_ws_bytes(nb, b))) != POETX_OK) return st;
+  double slots = 0, cubes = 0;
+  for (int i = 0; i < count; ++i) {
+    slots += 0.5 * (sum_r2(d[i], b) - d[i]);
+    cubes += sum_r3(d[i], b);
+  }
+  const MuonHyper h{hp->lr, hp->beta, hp->weight_decay, hp->nesterov, ns_hyper(hp->ns)};
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  PX_TIMED(POETX_KC_OPTIM, 3.0 * hp->ns.steps * cubes, 20.0 * slots, muon_batch(count, q, dq, m, d, b, h, ws, s));
+  return POETX_OK;
+}
+
+size_t poetx_orthogonalize_workspace_size(int32_t count, int32_t rows, int32_t cols, int32_t dtype) {
+  if (check_orth(count, rows, cols, dtype) != POETX_OK) return 0;
+  return orth_ws_bytes(count, rows, cols, dtype);
+}
+
+poetx_status poetx_orthogonalize(int32_t count, int32_t rows, int32_t cols, int32_t dtype, const void* G, int64_t ld_g,
+                                 int64_t stride_g, void* O, int64_t ld_o, int64_t stride_o, const poetx_ns_params* hp,
+                                 void* ws, size_t ws_bytes, void* stream) {
+  poetx_status st = check_orth(count, rows, cols, dtype);
+  if (st != POETX_OK) return st;
+  if (!G || !O || !hp) return fail(POETX_E_NULL, "G, O and hp must be non-NULL");
+  if (ld_g < cols || ld_o < cols) return fail(POETX_E_SHAPE, "ld_g and ld_o must be at least cols");
+  if (count > 1 && (stride_g < (rows - 1) * ld_g + cols || stride_o < (rows - 1) * ld_o + cols))
+    return fail(POETX_E_SHAPE, "the matrices of a batch must not overlap");
+  if (O == G && (ld_o != ld_g || (count > 1 && stride_o != stride_g)))
+    return fail(POETX_E_SHAPE, "O in place of G must have its ld and stride");
+  const size_t es = dt_size(dtype);
+  if (reinterpret_cast<uintptr_t>(G) % es || reinterpret_cast<uintptr_t>(O) % es)
+    return fail(POETX_E_SHAPE, "G and O must be aligned to their element");
+  if ((st = check_ns(*hp)) != POETX_OK) return st;
+  if ((st = check_ws(ws, ws_bytes, orth_ws_bytes(count, rows, cols, dtype))) != POETX_OK) return st;
+  const double r = std::min(rows, cols), k = std::max(rows, cols);
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  PX_TIMED(POETX_KC_OPTIM, count * hp->steps * (3.0 * r * r * k + r * r * r), 2.0 * count * r * k * es,
+           orthogonalize(count, rows, cols, dtype, G, ld_g, stride_g, O, ld_o, stride_o, ns_hyper(*hp), ws, s));
+  return POETX_OK;
+}
+
+}  // extern "C"

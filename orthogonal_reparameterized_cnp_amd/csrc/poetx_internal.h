@@ -181,4 +181,22 @@ hipError_t norm_bwd(int dt, bool rms, int64_t T, int d, const void* dY, int64_t 
                     const float* w, const float* stats, const void* dS, int64_t ldds, void* dX, int64_t ldx, float* dw,
                     float* db, float* part, hipStream_t s);
 
+// Newton-Schulz orthogonalisation (poetx_ns.hip): the optimiser step on the packed skew blocks of `count` sides, and
+// dense matrices.
+struct NsHyper {
+  int steps;
+  double a, b, c, eps, rms;
+};
+struct MuonHyper {
+  double lr, beta, weight_decay;
+  int nesterov;
+  NsHyper ns;
+};
+size_t muon_ws_bytes(int64_t blocks, int b);
+hipError_t muon_batch(int count, float* const* q, const float* const* g, float* const* m, const int* d, int b,
+                      const MuonHyper& hp, void* ws, hipStream_t s);
+size_t orth_ws_bytes(int count, int rows, int cols, int dt);
+hipError_t orthogonalize(int count, int rows, int cols, int dt, const void* G, int64_t ldg, int64_t sg, void* O,
+                         int64_t ldo, int64_t so, const NsHyper& n, void* ws, hipStream_t s);
+
 }  // namespace pxk

@@ -379,6 +379,20 @@ class PoetxGroup:
         return dqs
 
 
+def _default_merge_seeds(step, i):
+    return ((step << 16) | (2 * i), (step << 16) | (2 * i + 1))
+
+
+def _merge_all(layers, merge_seeds, steps: int, stream):
+    """Merge the factors of every linear's updated q into its weight and restart them (the cadence of the
+    optimisers below)."""
+    for i, lay in enumerate(layers):
+        lay.build(stream)
+        seed_R, seed_P = merge_seeds(steps, i)
+        lay.merge_reinit(seed_R, seed_P, stream)
+        lay.build(stream)  # G of the restarted q (the identity), so the layer is usable at once
+
+
 class PoetxAdam:
     """Optimiser state for the packed q of several linears, and the training
     cadence around it: each step() moves every side's q by one Adam step with
@@ -402,7 +416,7 @@ class PoetxAdam:
         self.layers = list(layers)
         self.lr, self.beta1, self.beta2, self.eps, self.weight_decay = lr, betas[0], betas[1], eps, weight_decay
         self.merge_every = merge_every
-        self.merge_seeds = merge_seeds or (lambda step, i: ((step << 16) | (2 * i), (step << 16) | (2 * i + 1)))
+        self.merge_seeds = merge_seeds or _default_merge_seeds
         qs = self.params()
         self.m1 = [torch.zeros_like(q) for q in qs]
         self.m2 = [torch.zeros_like(q) for q in qs]
@@ -425,11 +439,7 @@ class PoetxAdam:
                                 self.weight_decay, self.t, stream=stream)
         if not (self.merge_every and self.steps % self.merge_every == 0):
             return False
-        for i, lay in enumerate(self.layers):
-            lay.build(stream)
-            seed_R, seed_P = self.merge_seeds(self.steps, i)
-            lay.merge_reinit(seed_R, seed_P, stream)
-            lay.build(stream)  # G of the restarted q (the identity), so the layer is usable at once
+        _merge_all(self.layers, self.merge_seeds, self.steps, stream)
         with torch.cuda.stream(stream) if stream is not None else contextlib.nullcontext():
             for m in self.m1 + self.m2:
                 m.zero_()
@@ -771,3 +781,109 @@ class PoetxNorm:
             B.poetx_norm_bwd(self.desc, T, dY, ldy, self.S, lds, self.weight, self.stats, dS, ldds, dX, ldx, dw, db, ws,
                              ws.numel())
         return dX, dw, db
+
+
+class PoetxMuon:
+    """Optimiser state for the packed q of several linears, as PoetxAdam, with the momentum of every block
+    orthogonalised (poetx_muon_step_batch; one call for the linears of one block size, up to POETX_MAX_SIDES sides
+    each): q <- q - lr (rms sqrt(r) O + weight_decay q), O the Newton-Schulz orthogonalisation of the r x r block of
+    the momentum, so that every step moves the entries of q by lr rms on the average.
+
+    Every `merge_every` steps (0: never) the factors are merged as PoetxAdam does, and the momentum restarts from
+    zero.  step() takes a torch.cuda.Stream or None (the current stream).  A step without a merge uses no step
+    count, so it can be captured into a graph; the steps share one workspace and must not overlap in time."""
+
+    def __init__(self, layers, lr: float = 1e-3, beta: float = 0.95, nesterov: bool = True, weight_decay: float = 0.0,
+                 rms: float = 0.2, ns_steps: int = 5, merge_every: int = 0, merge_seeds=None):
+        if not layers:
+            raise ValueError("no linears")
+        self.layers = list(layers)
+        self.device = self.layers[0].device
+        if any(l.device != self.device for l in self.layers):
+            raise ValueError("the linears of one optimiser must share a device")
+        self.lr, self.beta, self.nesterov, self.weight_decay = lr, beta, nesterov, weight_decay
+        self.rms, self.ns_steps = rms, ns_steps
+        self.merge_every = merge_every
+        self.merge_seeds = merge_seeds or _default_merge_seeds
+        qs = self.params()
+        self.m = [torch.zeros_like(q) for q in qs]
+        self.d = [x for l in self.layers for x in (l.m, l.n)]
+        # the calls of a step: sides of one block size, at most POETX_MAX_SIDES of them
+        self.calls = []
+        for b in sorted({l.b for l in self.layers}):
+            idx = [2 * i + k for i, l in enumerate(self.layers) if l.b == b for k in (0, 1)]
+            self.calls += [(b, idx[k:k + B.POETX_MAX_SIDES]) for k in range(0, len(idx), B.POETX_MAX_SIDES)]
+        need = max(B.poetx_muon_workspace_size([self.d[i] for i in idx], b) for b, idx in self.calls)
+        self.ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
+        self.steps = 0
+
+    def params(self):
+        return [x for l in self.layers for x in (l.q_R, l.q_P)]
+
+    def step(self, dqs, stream=None) -> bool:
+        """dqs: [(dq_R, dq_P)] per linear.  Returns True when this step ended with a merge."""
+        dq, qs = [x for pair in dqs for x in pair], self.params()
+        if len(dq) != len(qs):
+            raise ValueError("one (dq_R, dq_P) pair per linear")
+        for i, (g, q) in enumerate(zip(dq, qs)):
+            _check(g, f"dq of side {i}", tuple(q.shape), torch.float32)
+            _check_device(self.device, **{f"dq of side {i}": g, f"q of side {i}": q})
+        hp = B.muon_params(self.lr, self.beta, self.weight_decay, self.nesterov, steps=self.ns_steps, rms=self.rms)
+        with _on(self.device, stream):
+            for b, idx in self.calls:
+                pick = lambda xs: [xs[i] for i in idx]
+                B.poetx_muon_step_batch(pick(qs), pick(dq), pick(self.m), pick(self.d), b, hp, self.ws, self.ws.numel())
+            self.steps += 1
+            if not (self.merge_every and self.steps % self.merge_every == 0):
+                return False
+            _merge_all(self.layers, self.merge_seeds, self.steps, None)
+            for m in self.m:
+                m.zero_()
+        return True
+
+
+class PoetxOrthogonalizer:
+    """Newton-Schulz orthogonalisation of dense update matrices of one shape (poetx_orthogonalize): owns the
+    workspace.  G is [rows, cols] or [count, rows, cols] in `dtype`, with contiguous rows of any pitch."""
+
+    def __init__(self, rows: int, cols: int, dtype: str = "f32", count: int = 1, steps: int = 5, rms: float = 0.2,
+                 device: str = "cuda"):
+        if dtype not in ("f32", "bf16"):
+            raise ValueError("dtype must be f32 or bf16")
+        self.rows, self.cols, self.dtype, self.count = rows, cols, dtype, count
+        self.device = torch.device(device)
+        self.hp = B.ns_params(steps=steps, rms=rms)
+        need = B.poetx_orthogonalize_workspace_size(count, rows, cols, B.DTYPES[dtype])
+        if need == 0:
+            raise ValueError(f"no workspace for {count} x {rows} x {cols}: {B.poetx_last_error()}")
+        self.ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+
+    def _strides(self, t, name: str):
+        shape = (self.count, self.rows, self.cols)
+        if not isinstance(t, torch.Tensor):
+            raise ValueError(f"{name} must be a torch.Tensor")
+        if tuple(t.shape) != shape and not (self.count == 1 and tuple(t.shape) == shape[1:]):
+            raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {shape}")
+        if t.dtype != _TORCH_DT[self.dtype]:
+            raise ValueError(f"{name} has dtype {t.dtype}, expected {_TORCH_DT[self.dtype]}")
+        if self.cols > 1 and t.stride(-1) != 1:
+            raise ValueError(f"{name} must have contiguous rows")
+        _check_device(self.device, **{name: t})
+        ld = t.stride(-2) if self.rows > 1 else self.cols
+        stride = t.stride(0) if self.count > 1 else self.rows * ld
+        if ld < self.cols or stride < (self.rows - 1) * ld + self.cols:
+            raise ValueError(f"{name} has overlapping rows or matrices")
+        return ld, stride
+
+    def __call__(self, G: torch.Tensor, out: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """The orthogonalised G, in `out` (which may be G) or a new tensor."""
+        ldg, sg = self._strides(G, "G")
+        if out is not None:
+            ldo, so = self._strides(out, "out")
+        with _on(self.device, stream):
+            if out is None:
+                out = torch.empty(G.shape, dtype=G.dtype, device=self.device)
+                ldo, so = self.cols, self.rows * self.cols
+            B.poetx_orthogonalize(self.count, self.rows, self.cols, B.DTYPES[self.dtype], G, ldg, sg, out, ldo, so,
+                                  self.hp, self.ws, self.ws.numel())
+        return out
