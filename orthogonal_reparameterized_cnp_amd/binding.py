@@ -306,21 +306,27 @@ def _check(st: int):
 
 
 def _ptr(t) -> Optional[int]:
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return t
-    return t.data_ptr()
+    return t if t is None or isinstance(t, int) else t.data_ptr()
 
 
 def _stream(stream) -> Optional[int]:
     if stream is None:
-        import torch
-
-        return torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
+
+
+def _current_stream() -> int:
+    """The current stream's handle.  The first call picks torch's raw accessor where it has one: building the Stream
+    object that torch.cuda.current_stream() returns costs more than the rest of a call's marshalling."""
+    global _current_stream
+    import torch
+
+    raw, dev = getattr(torch._C, "_cuda_getCurrentRawStream", None), getattr(torch._C, "_cuda_getDevice", None)
+    torch.cuda.current_stream()  # initialises the GPU, or raises
+    _current_stream = (lambda: raw(dev())) if raw and dev else (lambda: torch.cuda.current_stream().cuda_stream)
+    return _current_stream()
 
 
 def desc(m: int, n: int, b: int, act: str, w: str, mode: str = "xfast") -> LayerDesc:

@@ -78,9 +78,10 @@ PX_DEV void load_param(const float* p, float none, int lane, int d, float (&w)[E
 }
 
 // The sums of N values over the TPR threads of a row, in a fixed order.  Rows
-// of more than one wave use `red` (TPR / 64 x N floats); two calls that follow
-// each other take different buffers, and a buffer is used again only after a
-// barrier that every reader of it has passed.
+// of more than one wave use `red` (TPR / 64 x N floats a row) and a barrier of
+// the workgroup; two calls that follow each other take different buffers, and
+// a buffer is used again only after a barrier that every reader of it has
+// passed.
 template <int TPR, int N> PX_DEV void row_sum(float (&s)[N], float* red) {
 #pragma unroll
   for (int m = 32; m >= 1; m >>= 1)
@@ -88,7 +89,7 @@ template <int TPR, int N> PX_DEV void row_sum(float (&s)[N], float* red) {
     for (int i = 0; i < N; ++i) s[i] += __shfl_xor(s[i], m);
   if constexpr (TPR > 64) {
     constexpr int W = TPR / 64;
-    const int wave = threadIdx.x >> 6;
+    const int wave = (threadIdx.x >> 6) % W;
     if ((threadIdx.x & 63) == 0)
 #pragma unroll
       for (int i = 0; i < N; ++i) red[wave * N + i] = s[i];
@@ -117,6 +118,7 @@ struct FwdArgs {
 template <typename T, bool RMS, bool RES, int TPR, int E>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_fwd(const FwdArgs a) {
   constexpr int NT = TPR < 256 ? 256 : TPR, RPW = NT / TPR, W = TPR / 64;
+  static_assert(TPR == 64 || RPW == 1, "rows of several waves have the workgroup's barriers to themselves");
   using R = Row<T, TPR, E>;
   __shared__ float red[4 * W];
   const int lane = threadIdx.x % TPR, sub = threadIdx.x / TPR, d = a.d;
@@ -203,11 +205,16 @@ struct BwdArgs {
   int T, d;
 };
 
+// A workgroup of 1024 threads holds RPW rows at a time: 16 waves keep enough loads in flight for one workgroup a CU,
+// and its rows' column sums leave as one row of partial sums (four times the workgroups of a quarter the size, each
+// with its partial sums, ran 16384 x 2048 in 65.6 us and 3001 x 1376 in 23.9).
+constexpr int kBwdThreads = 1024;
 template <typename T, bool RMS, bool RES, int TPR, int E>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_bwd(const BwdArgs a) {
-  constexpr int NT = TPR < 256 ? 256 : TPR, RPW = NT / TPR, W = TPR / 64, VECS = RMS ? 1 : 2;
+__global__ __launch_bounds__(kBwdThreads) void k_norm_bwd(const BwdArgs a) {
+  constexpr int RPW = kBwdThreads / TPR, W = TPR / 64, VECS = RMS ? 1 : 2;
   using R = Row<T, TPR, E>;
-  __shared__ float red[4 * W];
+  __shared__ float red[2][RPW][2 * W];
+  __shared__ float acc[RPW > 1 ? VECS : 1][RPW > 1 ? TPR * E : 1];
   const int lane = threadIdx.x % TPR, sub = threadIdx.x / TPR, d = a.d;
   const T* dY = reinterpret_cast<const T*>(a.dY);
   const T* S = reinterpret_cast<const T*>(a.S);
@@ -215,12 +222,14 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_bwd(const BwdArg
   T* dX = reinterpret_cast<T*>(a.dX);
   const float* st_rs = RMS ? a.stats : a.stats + a.T;
   const float fd = (float)d;
-  float w[E], dw[E], db[E];
+  float w[E], dw[E], db[RMS ? 1 : E];
   load_param<T, TPR, E>(a.w, 1.f, lane, d, w);
 #pragma unroll
-  for (int i = 0; i < E; ++i) dw[i] = db[i] = 0.f;
+  for (int i = 0; i < E; ++i) dw[i] = 0.f;
+  if constexpr (!RMS)
+#pragma unroll
+    for (int i = 0; i < E; ++i) db[i] = 0.f;
   const int step = gridDim.x * RPW;
-  int t = blockIdx.x * RPW + sub;
   R y, x, r;
   float mean = 0.f, rs = 0.f;
   auto fetch = [&](int u) {
@@ -230,37 +239,37 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_bwd(const BwdArg
     if constexpr (!RMS) mean = a.stats[u];
     rs = st_rs[u];
   };
+  int t = blockIdx.x * RPW + sub;
   if (t < a.T) fetch(t);
-  for (int par = 0; t < a.T; t += step, par ^= 1) {
+  // every row group of the workgroup takes part in its barriers: the loop runs while the first one has rows
+  for (int t0 = blockIdx.x * RPW, par = 0; t0 < a.T; t0 += step, t += step, par ^= 1) {
+    const bool live = t < a.T;
     float g[E], xh[E], add[RES ? E : 1];
     const float rst = rs;
-    float s[2] = {0.f, 0.f};
+    float s[VECS] = {};
+    if (live) {
 #pragma unroll
-    for (int k = 0; k < R::NC; ++k)
+      for (int k = 0; k < R::NC; ++k)
 #pragma unroll
-      for (int e = 0; e < R::V; ++e) {
-        const int i = k * R::V + e;
-        const float dy = to_f32<T>(y.v[k][e]);
-        xh[i] = (to_f32<T>(x.v[k][e]) - mean) * rs;
-        if constexpr (RES) add[i] = to_f32<T>(r.v[k][e]);
-        g[i] = dy * w[i];
-        dw[i] += dy * xh[i];
-        if constexpr (!RMS) {
-          db[i] += dy;
-          s[1] += g[i];
+        for (int e = 0; e < R::V; ++e) {
+          const int i = k * R::V + e;
+          const float dy = to_f32<T>(y.v[k][e]);
+          xh[i] = (to_f32<T>(x.v[k][e]) - mean) * rs;
+          if constexpr (RES) add[i] = to_f32<T>(r.v[k][e]);
+          g[i] = dy * w[i];
+          dw[i] += dy * xh[i];
+          if constexpr (!RMS) {
+            db[i] += dy;
+            s[1] += g[i];
+          }
+          s[0] += g[i] * xh[i];
         }
-        s[0] += g[i] * xh[i];
-      }
+    }
     const int nt = t + step;
     if (nt < a.T) fetch(nt);
-    if constexpr (RMS) {
-      float s1[1] = {s[0]};
-      row_sum<TPR, 1>(s1, red + 2 * par * W);
-      s[0] = s1[0];
-    } else {
-      row_sum<TPR, 2>(s, red + 2 * par * W);
-    }
-    const float m0 = s[0] / fd, m1 = s[1] / fd;
+    row_sum<TPR, VECS>(s, red[par][sub]);
+    if (!live) continue;
+    const float m0 = s[0] / fd, m1 = RMS ? 0.f : s[VECS - 1] / fd;
     R o;
 #pragma unroll
     for (int k = 0; k < R::NC; ++k)
@@ -274,16 +283,14 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_bwd(const BwdArg
     o.store(dX + (int64_t)t * a.ldx, lane, d);
   }
   // the workgroup's column sums: its rows' partial sums added in the order of `sub`
-  float* P = a.part + (int64_t)blockIdx.x * VECS * d;
   if constexpr (RPW > 1) {
-    __shared__ float acc[2][TPR * E];
     for (int q = 0; q < RPW; ++q) {
       if (sub == q)
 #pragma unroll
         for (int i = 0; i < E; ++i) {
           const int c = i * TPR + lane;  // a place of its own per thread and element
           acc[0][c] = q == 0 ? dw[i] : acc[0][c] + dw[i];
-          if constexpr (!RMS) acc[1][c] = q == 0 ? db[i] : acc[1][c] + db[i];
+          if constexpr (!RMS) acc[VECS - 1][c] = q == 0 ? db[i] : acc[VECS - 1][c] + db[i];
         }
       __syncthreads();
     }
@@ -291,9 +298,10 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_bwd(const BwdArg
 #pragma unroll
     for (int i = 0; i < E; ++i) {
       dw[i] = acc[0][i * TPR + lane];
-      if constexpr (!RMS) db[i] = acc[1][i * TPR + lane];
+      if constexpr (!RMS) db[i] = acc[VECS - 1][i * TPR + lane];
     }
   }
+  float* P = a.part + (int64_t)blockIdx.x * VECS * d;
 #pragma unroll
   for (int k = 0; k < R::NC; ++k)
 #pragma unroll
@@ -335,19 +343,31 @@ __global__ __launch_bounds__(256) void k_norm_colsum(const float* __restrict__ p
   }
 }
 
-// The threads and elements per thread of a row of d: the narrowest that holds it.
-template <typename F> hipError_t by_width(int d, F&& f) {
-  if (d <= 64 * 8) return f(std::integral_constant<int, 64>(), std::integral_constant<int, 8>());
-  if (d <= 64 * 16) return f(std::integral_constant<int, 64>(), std::integral_constant<int, 16>());
-  if (d <= 256 * 8) return f(std::integral_constant<int, 256>(), std::integral_constant<int, 8>());
-  if (d <= 256 * 16) return f(std::integral_constant<int, 256>(), std::integral_constant<int, 16>());
-  if (d <= 512 * 16) return f(std::integral_constant<int, 512>(), std::integral_constant<int, 16>());
-  if (d <= 1024 * 16) return f(std::integral_constant<int, 1024>(), std::integral_constant<int, 16>());
-  return f(std::integral_constant<int, 1024>(), std::integral_constant<int, 32>());
+// The threads and elements per thread of a row of d: 8 elements while 1024 threads hold the row (with 16 a thread,
+// half the waves to keep loads in flight, 8192 x 4096 bf16 took 60.3 us forward instead of 54.2).
+template <int V> using Int = std::integral_constant<int, V>;
+template <bool BWD, typename F> hipError_t by_width(int d, F&& f) {
+  if (d <= 64 * 8) return f(Int<64>(), Int<8>());
+  if constexpr (BWD)  // rows of two waves share a workgroup (and its barriers) in the backward only
+    if (d <= 128 * 8) return f(Int<128>(), Int<8>());
+  if (d <= 256 * 8) return f(Int<256>(), Int<8>());
+  if (d <= 512 * 8) return f(Int<512>(), Int<8>());
+  if (d <= 1024 * 8) return f(Int<1024>(), Int<8>());
+  if (d <= 1024 * 16) return f(Int<1024>(), Int<16>());
+  return f(Int<1024>(), Int<32>());
+}
+// rows that a workgroup of the backward holds at a time
+int bwd_rows(int d) {
+  int n = 1;
+  by_width<true>(d, [&](auto tpr, auto) {
+    n = kBwdThreads / decltype(tpr)::value;
+    return hipSuccess;
+  });
+  return n;
 }
 
 template <typename T, bool RMS, bool RES> hipError_t fwd_t(const FwdArgs& a, hipStream_t s) {
-  return by_width(a.d, [&](auto tpr, auto el) {
+  return by_width<false>(a.d, [&](auto tpr, auto el) {
     constexpr int TPR = decltype(tpr)::value, E = decltype(el)::value, NT = TPR < 256 ? 256 : TPR, RPW = NT / TPR;
     const int64_t groups = ((int64_t)a.T + RPW - 1) / RPW;
     const unsigned grid = (unsigned)std::min<int64_t>(groups, 256 * (2048 / NT));
@@ -357,9 +377,9 @@ template <typename T, bool RMS, bool RES> hipError_t fwd_t(const FwdArgs& a, hip
 }
 
 template <typename T, bool RMS, bool RES> hipError_t bwd_t(const BwdArgs& a, int parts, hipStream_t s) {
-  return by_width(a.d, [&](auto tpr, auto el) {
-    constexpr int TPR = decltype(tpr)::value, E = decltype(el)::value, NT = TPR < 256 ? 256 : TPR;
-    k_norm_bwd<T, RMS, RES, TPR, E><<<(unsigned)parts, NT, 0, s>>>(a);
+  return by_width<true>(a.d, [&](auto tpr, auto el) {
+    constexpr int TPR = decltype(tpr)::value, E = decltype(el)::value;
+    k_norm_bwd<T, RMS, RES, TPR, E><<<(unsigned)parts, kBwdThreads, 0, s>>>(a);
     return hipGetLastError();
   });
 }
@@ -378,9 +398,8 @@ template <typename F> hipError_t by_kind(int dt, bool rms, bool res, F&& f) {
 namespace pxk {
 
 int norm_bwd_parts(int64_t T, int d) {
-  // one row per workgroup and step, four for rows of one wave
-  const int rpw = d <= 1024 ? 4 : 1;
-  return (int)std::min<int64_t>((T + rpw - 1) / rpw, d <= 8192 ? 512 : 256);
+  const int rows = bwd_rows(d);
+  return (int)std::min<int64_t>((T + rows - 1) / rows, 256);  // one workgroup a CU
 }
 
 hipError_t norm_fwd(int dt, bool rms, int64_t T, int d, float eps, const void* X, int64_t ldx, const void* R,

@@ -45,22 +45,26 @@ typedef _Float16 f16x8_v __attribute__((ext_vector_type(8)));
 
 constexpr float kSA = 256.f;  // scale of A and B
 
-// Tile configuration of the product kernels.  PL planes per operand.
-template <int BM_, int BN_, int BK_, int WM_, int WN_, int NP_> struct NCfg {
-  static constexpr int BM = BM_, BN = BN_, BK = BK_, WM = WM_, WN = WN_, NP = NP_, PL = NP_ == 3 ? 2 : 1;
+// Tile configuration of the product kernels: PL planes per operand, a ring of S stages of BK columns.
+template <int BM_, int BN_, int BK_, int WM_, int WN_, int S_, int NP_> struct NCfg {
+  static constexpr int BM = BM_, BN = BN_, BK = BK_, WM = WM_, WN = WN_, STAGES = S_, NP = NP_, PL = NP_ == 3 ? 2 : 1;
   static constexpr int NW = WM * WN, NT = NW * 64;
   static constexpr int WTM = BM / WM, WTN = BN / WN, TM = WTM / 32, TN = WTN / 32;
-  static constexpr int A_BYTES = BM * BK * 2, B_BYTES = BN * BK * 2;  // one plane of one stage
-  static constexpr int STAGE = PL * (A_BYTES + B_BYTES);
+  static constexpr int A_BYTES = PL * BM * BK * 2, B_BYTES = PL * BN * BK * 2;  // one stage
+  static constexpr int STAGE = A_BYTES + B_BYTES;
+  static constexpr int LA = A_BYTES / 1024 / NW, LB = B_BYTES / 1024 / NW;  // copies per wave and stage
   // the epilogue stages RS rows of (hi, lo) words; a pitch of 5 mod 64 words spreads both the reads
   // along its rows and those down its columns over the banks
-  static constexpr int RS = 128, PITCH = BN + 5, EPI = RS * PITCH * 4;
-  static constexpr int LDS = 2 * STAGE > EPI ? 2 * STAGE : EPI;
+  static constexpr int RS = BM < 128 ? BM : 128, PITCH = BN + 5, EPI = RS * PITCH * 4;
+  static constexpr int LDS = S_ * STAGE > EPI ? S_ * STAGE : EPI;
   static_assert(A_BYTES % (1024 * NW) == 0 && B_BYTES % (1024 * NW) == 0, "tile must split into 1 KB per wave");
   static_assert(BM % RS == 0 && RS % WTM == 0 && PITCH % 64 == 5, "epilogue stage");
 };
-template <int NP> using NSmall = NCfg<128, 128, NP == 3 ? 32 : 64, 2, 2, NP>;  // 4 waves of 64 x 64, two workgroups a CU
-template <int NP> using NBig = NCfg<256, 256, NP == 3 ? 32 : 64, 4, 2, NP>;    // 8 waves of 64 x 128
+// 4 waves of 32 x 32, two workgroups a CU, three stages in flight: products too small to fill the GPU with larger
+// tiles, bound by latency
+template <int NP> using NTiny = NCfg<64, 64, NP == 3 ? 32 : 64, 2, 2, 4, NP>;
+template <int NP> using NSmall = NCfg<128, 128, NP == 3 ? 32 : 64, 2, 2, 2, NP>;  // 4 waves of 64 x 64, two workgroups a CU
+template <int NP> using NBig = NCfg<256, 256, NP == 3 ? 32 : 64, 4, 2, 2, NP>;    // 8 waves of 64 x 128
 
 PX_DEV f16x8_v as_f16(const bf16x8_v& x) {
   f16x8_v y;
@@ -76,68 +80,87 @@ PX_DEV uint32_t pack_hilo(float v) {
   return (uint32_t)hb | ((uint32_t)lb << 16);
 }
 
-// One operand: K-contiguous rows of hi (and lo) values, ld elements apart.
+// One operand: K-contiguous rows of hi (and lo) values, ld fp16 elements apart.  Where the products read both planes
+// (NP = 3) they alternate along the rows, the hi values of a K step of `inter` (16 or 32) and then their lo values
+// (l = h + inter), so that a stage is one run of 64 or 128 bytes of every row.
 struct Planes {
   f16 *h = nullptr, *l = nullptr;
-  int64_t ld = 0, stride = 0;  // stride: elements from one matrix of the batch to the next
-  PX_DEV Planes at(int z, int64_t row) const {
-    const int64_t o = z * stride + row * ld;
-    return Planes{h + o, l ? l + o : nullptr, ld, stride};
+  int64_t ld = 0, stride = 0;  // stride: fp16 elements from one matrix of the batch to the next
+  int inter = 0;
+  // the planes from (row, col) of matrix z on; col a multiple of 32
+  PX_DEV Planes tile(int z, int64_t row, int64_t col) const {
+    if (!h) return *this;
+    const int64_t o = z * stride + row * ld + (inter ? 2 * col : col);
+    return Planes{h + o, l ? l + o : nullptr, ld, stride, inter};
   }
-  PX_DEV Planes tile(int z, int row, int col) const { return h ? at(z, row).right(col) : *this; }
-  PX_DEV Planes right(int col) const { return Planes{h + col, l ? l + col : nullptr, ld, stride}; }
 };
+// column of a row's element from its planes' origin
+PX_DEV int plane_col(int inter, int j) { return inter ? j / inter * 2 * inter + j % inter : j; }
 
 // acc = sum over KT tiles of K of a's tile rows times b's tile rows.  `same`: the two tiles are one.
 template <class C> PX_DEV void ns_loop(char* lds, const Planes& a, const Planes& b, int KT, bool same, Acc<C>& acc) {
+  constexpr int PK = C::BK * C::PL;  // fp16 elements of a row in a stage
   const AccPos<C> p = acc_pos<C>();
   const int wave = threadIdx.x >> 6, lane = p.lane;
   auto issue = [&](int kt, char* st) {
-    const int k0 = kt * C::BK;
-    dma_kmaj<C::BM, C::BK, C::NW>(reinterpret_cast<const bf16_t*>(a.h), a.ld, k0, st, wave, lane);
-    if constexpr (C::PL == 2)
-      dma_kmaj<C::BM, C::BK, C::NW>(reinterpret_cast<const bf16_t*>(a.l), a.ld, k0, st + C::A_BYTES, wave, lane);
+    dma_kmaj<C::BM, PK, C::NW>(reinterpret_cast<const bf16_t*>(a.h), a.ld, kt * PK, st, wave, lane);
     if (same) return;
-    st += C::PL * C::A_BYTES;
-    dma_kmaj<C::BN, C::BK, C::NW>(reinterpret_cast<const bf16_t*>(b.h), b.ld, k0, st, wave, lane);
-    if constexpr (C::PL == 2)
-      dma_kmaj<C::BN, C::BK, C::NW>(reinterpret_cast<const bf16_t*>(b.l), b.ld, k0, st + C::B_BYTES, wave, lane);
+    dma_kmaj<C::BN, PK, C::NW>(reinterpret_cast<const bf16_t*>(b.h), b.ld, kt * PK, st + C::A_BYTES, wave, lane);
   };
   acc.zero();
-  if (KT > 0) issue(0, lds);
+#pragma unroll
+  for (int t = 0; t < C::STAGES - 1; ++t)
+    if (t < KT) issue(t, lds + t * C::STAGE);
+  struct Frags {
+    f16x8_v ah[C::TM], bh[C::TN], al[C::PL == 2 ? C::TM : 1], bl[C::PL == 2 ? C::TN : 1];
+  };
   for (int kt = 0; kt < KT; ++kt) {
-    wait_vm<0>();
+    // the copies of up to STAGES - 2 later stages may stay in flight; stage kt must have landed
+    if (C::STAGES == 2 || KT - 1 - kt < C::STAGES - 2)
+      wait_vm<0>();
+    else if (same)
+      wait_vm<(C::STAGES - 2) * C::LA>();
+    else
+      wait_vm<(C::STAGES - 2) * (C::LA + C::LB)>();
     wait_lgkm0();
     barrier_raw();
-    if (kt + 1 < KT) issue(kt + 1, lds + ((kt + 1) & 1) * C::STAGE);
-    const char* As = lds + (kt & 1) * C::STAGE;
-    const char* Bs = same ? As : As + C::PL * C::A_BYTES;
-    const int bpl = same ? C::A_BYTES : C::B_BYTES;
-#pragma unroll
-    for (int ks = 0; ks < C::BK / 16; ++ks) {
-      f16x8_v ah[C::TM], bh[C::TN], al[C::PL == 2 ? C::TM : 1], bl[C::PL == 2 ? C::TN : 1];
+    const int nxt = kt + C::STAGES - 1;
+    if (nxt < KT) issue(nxt, lds + nxt % C::STAGES * C::STAGE);
+    const char* As = lds + kt % C::STAGES * C::STAGE;
+    const char* Bs = same ? As : As + C::A_BYTES;
+    auto load = [&](int ks, Frags& f) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < C::TM; ++i) {
         const int t0 = p.wm * C::WTM + i * 32;
-        ah[i] = as_f16(frag_kmaj<C::BK>(As, t0, ks * 16, lane));
-        if constexpr (C::PL == 2) al[i] = as_f16(frag_kmaj<C::BK>(As + C::A_BYTES, t0, ks * 16, lane));
+        f.ah[i] = as_f16(frag_kmaj<PK>(As, t0, ks * 16, lane));
+        if constexpr (C::PL == 2) f.al[i] = as_f16(frag_kmaj<PK>(As, t0, C::BK + ks * 16, lane));
       }
 #pragma unroll
       for (int j = 0; j < C::TN; ++j) {
         const int t0 = p.wn * C::WTN + j * 32;
-        bh[j] = as_f16(frag_kmaj<C::BK>(Bs, t0, ks * 16, lane));
-        if constexpr (C::PL == 2) bl[j] = as_f16(frag_kmaj<C::BK>(Bs + bpl, t0, ks * 16, lane));
+        f.bh[j] = as_f16(frag_kmaj<PK>(Bs, t0, ks * 16, lane));
+        if constexpr (C::PL == 2) f.bl[j] = as_f16(frag_kmaj<PK>(Bs, t0, C::BK + ks * 16, lane));
       }
+    };
+    constexpr int KS = C::BK / 16;
+    Frags f[2];
+    load(0, f[0]);
+#pragma unroll
+    for (int ks = 0; ks < KS; ++ks) {
+      const Frags& c = f[ks & 1];
+      if (ks + 1 < KS) load(ks + 1, f[(ks + 1) & 1]);
 #pragma unroll
       for (int i = 0; i < C::TM; ++i)
 #pragma unroll
         for (int j = 0; j < C::TN; ++j) {
           if constexpr (C::PL == 2) {
-            acc.v[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(al[i], bh[j], acc.v[i][j], 0, 0, 0);
-            acc.v[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ah[i], bl[j], acc.v[i][j], 0, 0, 0);
+            acc.v[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(c.al[i], c.bh[j], acc.v[i][j], 0, 0, 0);
+            acc.v[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(c.ah[i], c.bl[j], acc.v[i][j], 0, 0, 0);
           }
-          acc.v[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(ah[i], bh[j], acc.v[i][j], 0, 0, 0);
+          acc.v[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(c.ah[i], c.bh[j], acc.v[i][j], 0, 0, 0);
         }
+      // ask the compiler to interleave the reads with the matrix instructions
+      __builtin_amdgcn_iglp_opt(1);
     }
   }
   wait_lgkm0();
@@ -158,17 +181,50 @@ PX_DEV void split_words(const uint32_t (&w)[8], uint32_t x, uint4& h, uint4& l) 
   l = make_uint4(ll[0], ll[1], ll[2], ll[3]);
 }
 
+typedef uint32_t u32x4_v __attribute__((ext_vector_type(4)));
+// 16 bytes to memory.  Small products (NT) write past the L2: what they leave dirty there is written back after their
+// last wave, before the next launch may start (muon step of 40 blocks of 256: 153 -> 144 us; of 160 blocks of 512,
+// whose write-back runs under other tiles, 1882 -> 1926 us).
+template <bool NT> PX_DEV void put16(f16* p, const uint4& v) {
+  if constexpr (NT)
+    __builtin_nontemporal_store(u32x4_v{v.x, v.y, v.z, v.w}, reinterpret_cast<u32x4_v*>(p));
+  else
+    *reinterpret_cast<uint4*>(p) = v;
+}
+
 // The epilogue of a tile, v = alpha aux + beta acc, RS rows at a time through LDS: the accumulators are staged in
 // fp32, then each thread takes 8 consecutive values of a row, adds the aux planes' (16-byte loads; null: none),
 // writes them to the planes `o` (null: none) and leaves them in LDS, as (hi, lo) words where `t` (the transposed
 // tile's planes; null: none) is written from there with `flip` (0x8000 negates), as floats for emit(r0, stage).
-// All planes are at the tile's origin; null lo planes are skipped.
+// All planes are at the tile's origin; null lo planes are skipped.  `diag` (with `t` the tile itself): the tile lies on
+// the diagonal of a skew matrix, and its values below the diagonal are the negated mirrors of those above.  A computed
+// skew matrix would be off by its roundings there, and the products that read X^T as -X, from rows alone, would see
+// the sign of that symmetric part turned over: it grows by about 5 a step where a rounding otherwise grows by 3.4.
 template <class C, class Emit>
 PX_DEV void ns_store(char* lds, const Acc<C>& acc, const Planes& aux, float alpha, float beta, const Planes& o,
-                     const Planes& t, uint32_t flip, const Emit& emit) {
+                     const Planes& t, uint32_t flip, const Emit& emit, bool diag = false) {
   constexpr bool EMIT = !std::is_same<Emit, std::nullptr_t>::value;
+  constexpr int INTER = C::PL == 2 ? C::BK : 0;
+  constexpr int NIT = C::RS * C::BN / 8 / C::NT;  // a thread's share of the pieces of 8
   uint32_t* st = reinterpret_cast<uint32_t*>(lds);
   const AccPos<C> p = acc_pos<C>();
+  // the aux values: a thread's whole share is on its way before the stage is written, or for the 256 tile, whose
+  // accumulators leave no room for it, 4 pieces at a time
+  constexpr int NX = C::BM == C::RS ? NIT : 4;
+  static_assert(C::RS * C::BN / 8 % C::NT == 0 && NIT % NX == 0, "whole shares");
+  f16x8_v xh[NX], xl[NX];
+  auto load_aux = [&](int r0, int it0, int n) __attribute__((always_inline)) {
+    if (!aux.h) return;
+#pragma unroll
+    for (int x = 0; x < n; ++x) {
+      const int c = threadIdx.x + (it0 + x) * C::NT, i = c / (C::BN / 8), j = c % (C::BN / 8) * 8;
+      const int64_t at = (r0 + i) * aux.ld + plane_col(INTER, j);
+      xh[x] = *reinterpret_cast<const f16x8_v*>(aux.h + at);
+      xl[x] = f16x8_v{};
+      if (aux.l) xl[x] = *reinterpret_cast<const f16x8_v*>(aux.l + at);
+    }
+  };
+  if constexpr (C::BM == C::RS) load_aux(0, 0, NIT);
 #pragma unroll 1
   for (int r0 = 0; r0 < C::BM; r0 += C::RS) {
     __syncthreads();
@@ -182,20 +238,18 @@ PX_DEV void ns_store(char* lds, const Acc<C>& acc, const Planes& aux, float alph
             st[(p.row(i, e) - r0) * C::PITCH + p.col(j)] = __float_as_uint(beta * acc.v[i][j][e]);
     }
     __syncthreads();
-#pragma unroll 2
-    for (int c = threadIdx.x; c < C::RS * C::BN / 8; c += C::NT) {
-      const int i = c / (C::BN / 8), j = c % (C::BN / 8) * 8;
+#pragma unroll
+    for (int it = 0; it < NIT; ++it) {
+      if constexpr (C::BM != C::RS)
+        if (it % 4 == 0) load_aux(r0, it, 4);
+      const int c = threadIdx.x + it * C::NT, i = c / (C::BN / 8), j = c % (C::BN / 8) * 8;
       uint32_t* w = st + i * C::PITCH + j;
       float v[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(w[e]);
       if (aux.h) {
-        const int64_t at = (r0 + i) * aux.ld + j;
-        const f16x8_v xh = *reinterpret_cast<const f16x8_v*>(aux.h + at);
-        f16x8_v xl = {};
-        if (aux.l) xl = *reinterpret_cast<const f16x8_v*>(aux.l + at);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += alpha * plane_value(xh[e], xl[e]);
+        for (int e = 0; e < 8; ++e) v[e] += alpha * plane_value(xh[it % NX][e], xl[it % NX][e]);
       }
       if constexpr (EMIT) {
 #pragma unroll
@@ -204,12 +258,14 @@ PX_DEV void ns_store(char* lds, const Acc<C>& acc, const Planes& aux, float alph
         uint32_t x[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = pack_hilo(v[e]);
-        uint4 h, l;
-        split_words(x, 0, h, l);
-        const int64_t at = (r0 + i) * o.ld + j;
-        *reinterpret_cast<uint4*>(o.h + at) = h;
-        if (o.l) *reinterpret_cast<uint4*>(o.l + at) = l;
-        if (t.h)
+        if (!diag || j >= r0 + C::RS) {
+          uint4 h, l;
+          split_words(x, 0, h, l);
+          const int64_t at = (r0 + i) * o.ld + plane_col(INTER, j);
+          put16<C::BM == 64>(o.h + at, h);
+          if (o.l) put16<C::BM == 64>(o.l + at, l);
+        }
+        if (t.h || diag)
 #pragma unroll
           for (int e = 0; e < 8; ++e) w[e] = x[e];
       }
@@ -217,21 +273,57 @@ PX_DEV void ns_store(char* lds, const Acc<C>& acc, const Planes& aux, float alph
     if constexpr (EMIT) {
       __syncthreads();
       emit(r0, reinterpret_cast<const float*>(st));
-    } else if (t.h) {
+    } else if (t.h || diag) {
       __syncthreads();
+      if (diag) {
+        // the square on the diagonal, of these rows and the same columns
+#pragma unroll 2
+        for (int c = threadIdx.x; c < C::RS * C::RS / 8; c += C::NT) {
+          const int i = c / (C::RS / 8), j = c % (C::RS / 8) * 8;
+          uint32_t x[8];
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const uint32_t up = st[min(i, j + e) * C::PITCH + r0 + max(i, j + e)];
+            x[e] = j + e > i ? up : j + e < i ? up ^ 0x80008000u : 0u;
+          }
+          uint4 h, l;
+          split_words(x, 0, h, l);
+          const int64_t at = (r0 + i) * o.ld + plane_col(INTER, r0 + j);
+          put16<C::BM == 64>(o.h + at, h);
+          if (o.l) put16<C::BM == 64>(o.l + at, l);
+        }
+      }
 #pragma unroll 2
       for (int c = threadIdx.x; c < C::RS * C::BN / 8; c += C::NT) {
         const int j = c / (C::RS / 8), i = c % (C::RS / 8) * 8;
+        if (diag && j < r0 + C::RS) continue;
         uint32_t x[8];
 #pragma unroll
         for (int e = 0; e < 8; ++e) x[e] = st[(i + e) * C::PITCH + j];
         uint4 h, l;
         split_words(x, flip | (flip << 16), h, l);
-        const int64_t at = j * t.ld + r0 + i;
-        *reinterpret_cast<uint4*>(t.h + at) = h;
-        if (t.l) *reinterpret_cast<uint4*>(t.l + at) = l;
+        const int64_t at = j * t.ld + plane_col(INTER, r0 + i);
+        put16<C::BM == 64>(t.h + at, h);
+        if (t.l) put16<C::BM == 64>(t.l + at, l);
       }
     }
+  }
+}
+
+// one 64 x 64 tile of floats, value(row, col), to matrix z's planes at (row0, col0); 256 threads
+template <class F> PX_DEV void put64(const Planes& p, int z, int64_t row0, int64_t col0, const F& value) {
+  const Planes o = p.tile(z, row0, col0);
+#pragma unroll
+  for (int w = threadIdx.x; w < 64 * 8; w += 256) {
+    const int row = w / 8, col = w % 8 * 8;
+    uint32_t x[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) x[e] = pack_hilo(value(row, col + e));
+    uint4 h, l;
+    split_words(x, 0, h, l);
+    const int64_t at = row * o.ld + plane_col(o.inter, col);
+    *reinterpret_cast<uint4*>(o.h + at) = h;
+    if (o.l) *reinterpret_cast<uint4*>(o.l + at) = l;
   }
 }
 
@@ -256,8 +348,10 @@ struct MuonTable {
   int d[pxk::kMaxSides];
   int first[pxk::kMaxSides + 1];
   int count;
-  // block z: its side, the first packed slot of it in the side's arrays, its live size
+  int z0;  // number of the launch's first block
+  // block z of the launch: its side, the first packed slot of it in the side's arrays, its live size
   PX_DEV void at(int z, int b, int& s, int64_t& off, int& r) const {
+    z += z0;
     s = 0;
     while (s + 1 < count && z >= first[s + 1]) ++s;
     const int blk = z - first[s];
@@ -278,123 +372,189 @@ struct MuonK {
 
 // ------------------------------------------------------------ skew blocks ---
 
-// Momentum of every live slot, and each workgroup's sum of the squared updates
-// in 64 bits: workgroup c of block z takes the packed rows c, c + gridDim.x, ...
-// of waves.  A dead slot (j >= r of a partial block) is neither read nor written.
-__global__ __launch_bounds__(256) void k_muon_momentum(MuonTable tab, int b, MuonK k, double* __restrict__ part) {
+// Row and column of a packed slot (b <= 1024): row i starts at slot i b - i (i + 1) / 2; the root's rounding is put right
+// by at most a step.
+PX_DEV int slot_start(int i, int b) { return i * b - i * (i + 1) / 2; }
+PX_DEV int slot_i(int x, int b) {
+  const float t = (float)(2 * b - 1);
+  int i = (int)((t - __builtin_sqrtf(fmaxf(t * t - 8.f * (float)x, 0.f))) * 0.5f);
+  i = max(0, min(i, b - 2));
+  while (i > 0 && slot_start(i, b) > x) --i;
+  while (slot_start(i + 1, b) <= x) ++i;
+  return i;
+}
+PX_DEV int slot_j(int x, int b) {
+  const int i = slot_i(x, b);
+  return x - slot_start(i, b) + i + 1;
+}
+
+// What the products need of a block of the launch, in the workspace.
+struct BlockInfo {
+  float* q;  // its packed parameters
+  int r;     // its live size
+};
+
+// Momentum of every live slot, and each workgroup's sum of the squared updates in 64 bits: workgroup c of block z
+// takes the packed slots from 2048 c on, 8 consecutive ones a thread (of any alignment).  A dead slot (j >= r of a
+// partial block) is neither read nor written.
+constexpr int kMomentumSlots = 2048;
+__global__ __launch_bounds__(256) void k_muon_momentum(MuonTable tab, int b, MuonK k, double* __restrict__ part,
+                                                       BlockInfo* __restrict__ info) {
   __shared__ double red[4];
-  const int z = blockIdx.y, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int z = blockIdx.y, slots = b * (b - 1) / 2;
   int s, r;
   int64_t off;
   tab.at(z, b, s, off, r);
-  const float* g = tab.g[s] + off;
-  float* m = tab.m[s] + off;
+  if (blockIdx.x == 0 && threadIdx.x == 0) info[z] = BlockInfo{tab.q[s] + off, r};
+  const int x0 = blockIdx.x * kMomentumSlots + threadIdx.x * 8;
+  const float* g = tab.g[s] + off + x0;
+  float* m = tab.m[s] + off + x0;
   double sum = 0.0;
-  for (int i = blockIdx.x * 4 + wave; i < r - 1; i += gridDim.x * 4) {
-    const int64_t row = packed_slot(i, i + 1, b) - (i + 1);
-    for (int j = i + 1 + lane; j < r; j += 64) {
-      const float gv = g[row + j], mv = k.moment(m[row + j], gv);
-      m[row + j] = mv;
-      const float u = k.update(mv, gv);
+  if (r == b && x0 + 8 <= slots) {
+    float gv[8], mv[8];
+    __builtin_memcpy(gv, g, 32);
+    __builtin_memcpy(mv, m, 32);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      mv[e] = k.moment(mv[e], gv[e]);
+      const float u = k.update(mv[e], gv[e]);
       sum += (double)u * u;
+    }
+    __builtin_memcpy(m, mv, 32);
+  } else if (x0 < slots) {
+    int i = slot_i(x0, b), j = x0 - slot_start(i, b) + i + 1;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (x0 + e < slots && j < r) {
+        const float mv = k.moment(m[e], g[e]), u = k.update(mv, g[e]);
+        m[e] = mv;
+        sum += (double)u * u;
+      }
+      if (++j == b) j = ++i + 1;
     }
   }
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o);
-  if (lane == 0) red[wave] = sum;
+  if ((threadIdx.x & 63) == 0) red[threadIdx.x >> 6] = sum;
   __syncthreads();
   if (threadIdx.x == 0) part[(int64_t)z * gridDim.x + blockIdx.x] = (red[0] + red[1]) + (red[2] + red[3]);
 }
 
+// the sum of n partial sums, the same in every wave of the grid
+PX_DEV double sum_parts(const double* part, int n) {
+  double s = 0.0;
+  for (int p = threadIdx.x & 63; p < n; p += 64) s += part[p];
+#pragma unroll
+  for (int o = 32; o >= 1; o >>= 1) s += __shfl_xor(s, o);
+  return s;
+}
+
 // X planes of every block from its update, scaled by sx / (|M|_F + eps): one 64 x 64 tile on or above the
-// diagonal per workgroup and, off the diagonal, its negated mirror; zeros from r to the padded size.
+// diagonal per workgroup and, off the diagonal, its negated mirror; zeros from r to the end of its last tile.
 __global__ __launch_bounds__(256) void k_muon_unpack(MuonTable tab, int b, MuonK k, const double* __restrict__ part,
-                                                     int parts, float sx, Planes X) {
+                                                     int parts, float sx, int n64, Planes X) {
   __shared__ float t[64][65];
   const int z = blockIdx.y;
   int s, r;
   int64_t off;
   tab.at(z, b, s, off, r);
   int ti, tj;
-  upper_tile(blockIdx.x, (int)(X.ld / 64), ti, tj);
+  upper_tile(blockIdx.x, n64, ti, tj);
   const int i0 = ti * 64, j0 = tj * 64, live = (r + 127) / 128 * 128;
   if (j0 >= live) return;  // tiles that no product reads
-  double ss = 0.0;
-  for (int p = 0; p < parts; ++p) ss += part[(int64_t)z * parts + p];
-  const double f = (double)sx / (__builtin_sqrt(2.0 * ss) + (double)k.eps);  // both halves of M
   const int c = threadIdx.x & 63, rr = threadIdx.x >> 6;
   const float* g = tab.g[s] + off;
   const float* m = tab.m[s] + off;
+  // dead and mirrored places read slot 0 (a live one wherever a block has any) in their stead, so that all loads are
+  // under way together
+  float gv[16], mv[16];
 #pragma unroll
   for (int e = 0; e < 16; ++e) {
     const int i = i0 + rr + 4 * e, j = j0 + c;
-    float v = 0.f;
-    if (i < j && j < r) {
-      const int64_t x = packed_slot(i, j, b);
-      v = (float)((double)k.update(m[x], g[x]) * f);
-    }
-    t[rr + 4 * e][c] = v;
+    const int64_t x = i < j && j < r ? packed_slot(i, j, b) : 0;
+    gv[e] = r > 1 ? g[x] : 0.f;
+    mv[e] = r > 1 ? m[x] : 0.f;
+  }
+  const double f = (double)sx / (__builtin_sqrt(2.0 * sum_parts(part + (int64_t)z * parts, parts)) + (double)k.eps);
+#pragma unroll
+  for (int e = 0; e < 16; ++e) {
+    const int i = i0 + rr + 4 * e, j = j0 + c;
+    t[rr + 4 * e][c] = i < j && j < r ? (float)((double)k.update(mv[e], gv[e]) * f) : 0.f;  // (both halves of M: 2 sum)
   }
   __syncthreads();
-  const Planes o = X.at(z, 0);
-  auto put = [&](int row0, int col0, auto value) {
-#pragma unroll
-    for (int w = threadIdx.x; w < 64 * 8; w += 256) {
-      const int row = w / 8, col = w % 8 * 8;
-      uint32_t h[4], l[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t a = pack_hilo(value(row, col + 2 * e)), c2 = pack_hilo(value(row, col + 2 * e + 1));
-        h[e] = (a & 0xffff) | (c2 << 16);
-        l[e] = (a >> 16) | (c2 & 0xffff0000u);
-      }
-      const int64_t at = (row0 + row) * o.ld + col0 + col;
-      *reinterpret_cast<uint4*>(o.h + at) = make_uint4(h[0], h[1], h[2], h[3]);
-      *reinterpret_cast<uint4*>(o.l + at) = make_uint4(l[0], l[1], l[2], l[3]);
-    }
-  };
   if (ti == tj) {
-    put(i0, j0, [&](int i, int j) { return i < j ? t[i][j] : i > j ? -t[j][i] : 0.f; });
+    put64(X, z, i0, j0, [&](int i, int j) { return i < j ? t[i][j] : i > j ? -t[j][i] : 0.f; });
   } else {
-    put(i0, j0, [&](int i, int j) { return t[i][j]; });
-    put(j0, i0, [&](int j, int i) { return -t[i][j]; });
+    put64(X, z, i0, j0, [&](int i, int j) { return t[i][j]; });
+    put64(X, z, j0, i0, [&](int j, int i) { return -t[i][j]; });
   }
 }
 
-// One product of the batch on its tiles on and above the diagonal: out = alpha aux + beta a b^T, its mirror
-// flipped by `flip`; with LAST the step of q instead of an output.
+struct SkewArgs {
+  Planes a, b, aux, out;
+  float alpha, beta;
+  uint32_t flip;
+};
+
+// One tile (ti, tj) of block z
 template <class C, bool AUX, bool LAST>
-__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2))) void k_ns_skew(MuonTable tab, int b, int tiles, Planes a, Planes bb, Planes aux,
-                                                   Planes out, float alpha, float beta, uint32_t flip, MuonK k) {
-  extern __shared__ __align__(16) unsigned char smem[];
-  char* lds = reinterpret_cast<char*>(smem);
-  const int per = tiles * (tiles + 1) / 2;
-  const int u = xcd_unit(blockIdx.x, gridDim.x), z = u / per;
-  int s, r, ti, tj;
-  int64_t off;
-  tab.at(z, b, s, off, r);
-  upper_tile(u % per, tiles, ti, tj);
-  const int m0 = ti * C::BM, n0 = tj * C::BN;
+PX_DEV void skew_tile(char* lds, const SkewArgs& g, const BlockInfo* info, int b, int z, int ti, int tj, const MuonK& k) {
+  const int r = info[z].r, m0 = ti * C::BM, n0 = tj * C::BN;
   if (n0 >= r) return;  // past the live corner: read by no product
   Acc<C> acc;
-  ns_loop<C>(lds, a.at(z, m0), bb.at(z, n0), (r + C::BK - 1) / C::BK, ti == tj && a.h == bb.h, acc);
+  ns_loop<C>(lds, g.a.tile(z, m0, 0), g.b.tile(z, n0, 0), (r + C::BK - 1) / C::BK, ti == tj && g.a.h == g.b.h, acc);
   const Planes none{};
-  const Planes x = AUX ? aux.tile(z, m0, n0) : none;
+  const Planes x = AUX ? g.aux.tile(z, m0, n0) : none;
   if constexpr (!LAST) {
-    ns_store<C>(lds, acc, x, alpha, beta, out.tile(z, m0, n0), ti == tj ? none : out.tile(z, n0, m0), flip, nullptr);
+    ns_store<C>(lds, acc, x, g.alpha, g.beta, g.out.tile(z, m0, n0),
+                ti == tj && g.flip == 0 ? none : g.out.tile(z, n0, m0), g.flip, nullptr, g.flip != 0 && ti == tj);
   } else {
-    float* q = tab.q[s] + off;
+    float* q = info[z].q;
     const float sc = k.scale(r);
-    ns_store<C>(lds, acc, x, alpha, beta, none, none, 0, [&](int r0, const float* st) {
-#pragma unroll 4
-      for (int c = threadIdx.x; c < C::RS * C::BN; c += C::NT) {
-        const int i = c / C::BN, j = c % C::BN, row = m0 + r0 + i, col = n0 + j;
-        if (row < col && col < r) {
-          float* p = q + packed_slot(row, col, b);
-          *p = k.step(*p, st[i * C::PITCH + j], sc);
+    ns_store<C>(lds, acc, x, g.alpha, g.beta, none, none, 0, [&](int r0, const float* st) {
+      // runs of 8 slots of a packed row (of any alignment)
+#pragma unroll 2
+      for (int c = threadIdx.x; c < C::RS * C::BN / 8; c += C::NT) {
+        const int i = c / (C::BN / 8), j = c % (C::BN / 8) * 8, row = m0 + r0 + i, col = n0 + j;
+        if (col + 7 <= row || col >= r) continue;
+        float* p = q + packed_slot(row, col, b);
+        const float* v = st + i * C::PITCH + j;
+        if (col > row && col + 8 <= r) {
+          float f[8];
+          __builtin_memcpy(f, p, 32);
+#pragma unroll
+          for (int e = 0; e < 8; ++e) f[e] = k.step(f[e], v[e], sc);
+          __builtin_memcpy(p, f, 32);
+        } else {
+          for (int e = 0; e < 8; ++e)
+            if (col + e > row && col + e < r) p[e] = k.step(p[e], v[e], sc);
         }
       }
     });
+  }
+}
+
+// One product of the batch on the tiles on and above the diagonal of its blocks: out = alpha aux + beta a b^T, its
+// mirror flipped by `flip`; with LAST the step of q instead of an output.  The first `wide` blocks run on 128 x 128
+// tiles, the rest, which would leave most of the last round of workgroups empty, on 64 x 64 ones.
+template <bool AUX, bool LAST>
+__global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void k_ns_skew(
+    SkewArgs g, const BlockInfo* __restrict__ info, int b, int n128, int wide, MuonK k) {
+  using C1 = NSmall<3>;
+  using C2 = NTiny<3>;
+  static_assert(C1::NT == 256 && C2::NT == 256 && C1::BK == C2::BK, "one launch, one layout");
+  extern __shared__ __align__(16) unsigned char smem[];
+  char* lds = reinterpret_cast<char*>(smem);
+  const int per1 = n128 * (n128 + 1) / 2, per2 = n128 * (2 * n128 + 1), units1 = wide * per1;
+  int ti, tj;
+  if ((int)blockIdx.x < units1) {
+    const int u = xcd_unit(blockIdx.x, units1);
+    upper_tile(u % per1, n128, ti, tj);
+    skew_tile<C1, AUX, LAST>(lds, g, info, b, u / per1, ti, tj, k);
+  } else {
+    const int u = xcd_unit(blockIdx.x - units1, gridDim.x - units1);
+    upper_tile(u % per2, 2 * n128, ti, tj);
+    skew_tile<C2, AUX, LAST>(lds, g, info, b, wide + u / per2, ti, tj, k);
   }
 }
 
@@ -417,36 +577,53 @@ __global__ __launch_bounds__(W * 64) void k_muon_small(MuonTable tab, int b, Muo
   const float* g = tab.g[s] + off;
   float* m = tab.m[s] + off;
   float* q = tab.q[s] + off;
+  // the thread's slots: their updates stay in registers until the norm is known
+  constexpr int NU = (P * (P - 1) / 2 + W * 64 - 1) / (W * 64);
+  const int slots = b * (b - 1) / 2;
+  float u[NU];
   double sum = 0.0;
-  for (int i = wave; i < r - 1; i += W) {
-    const int64_t row = packed_slot(i, i + 1, b) - (i + 1);
-    for (int j = i + 1 + lane; j < r; j += 64) {
-      const float gv = g[row + j], mv = k.moment(m[row + j], gv);
-      m[row + j] = mv;
-      const float u = k.update(mv, gv);
-      sum += (double)u * u;
+#pragma unroll
+  for (int e0 = 0; e0 < NU; e0 += 8) {
+    float gv[8], mv[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int x = (e0 + e) * W * 64 + threadIdx.x;
+      const bool ok = x < slots && slot_j(x, b) < r;
+      gv[e] = ok ? g[x] : 0.f;
+      mv[e] = ok ? m[x] : 0.f;
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      if (e0 + e >= NU) continue;
+      const int x = (e0 + e) * W * 64 + threadIdx.x;
+      mv[e] = k.moment(mv[e], gv[e]);
+      if (x < slots && slot_j(x, b) < r) m[x] = mv[e];
+      u[e0 + e] = k.update(mv[e], gv[e]);
+      sum += (double)u[e0 + e] * u[e0 + e];
     }
   }
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o);
   if (lane == 0) red[wave] = sum;
-  // X planes start as zeros
+  // X planes start as zeros: the diagonal, and all past the live corner, stay so
   for (int c = threadIdx.x; c < 2 * P * LD / 8; c += W * 64) reinterpret_cast<uint4*>(Xh)[c] = make_uint4(0, 0, 0, 0);
   __syncthreads();
   sum = red[0];
 #pragma unroll
   for (int w = 1; w < W; ++w) sum += red[w];
   const double f = (double)sx / (__builtin_sqrt(2.0 * sum) + (double)k.eps);
-  for (int i = wave; i < r - 1; i += W) {
-    const int64_t row = packed_slot(i, i + 1, b) - (i + 1);
-    for (int j = i + 1 + lane; j < r; j += 64) {  // the slots this thread wrote
-      const float v = (float)((double)k.update(m[row + j], g[row + j]) * f);
-      const f16 h = (f16)v, l = (f16)(v - (float)h);
-      Xh[i * LD + j] = h;
-      Xl[i * LD + j] = l;
-      Xh[j * LD + i] = -h;
-      Xl[j * LD + i] = -l;
-    }
+#pragma unroll
+  for (int e = 0; e < NU; ++e) {
+    const int x = e * W * 64 + threadIdx.x;
+    if (x >= slots) continue;
+    const int i = slot_i(x, b), j = x - slot_start(i, b) + i + 1;
+    if (j >= r) continue;
+    const float v = (float)((double)u[e] * f);
+    const f16 h = (f16)v, l = (f16)(v - (float)h);
+    Xh[i * LD + j] = h;
+    Xl[i * LD + j] = l;
+    Xh[j * LD + i] = -h;
+    Xl[j * LD + i] = -l;
   }
   __syncthreads();
   const int m0 = wave / WN * TM * 32, n0 = wave % WN * TM * 32;
@@ -529,7 +706,17 @@ __global__ __launch_bounds__(W * 64) void k_muon_small(MuonTable tab, int b, Muo
       return;
     }
     __syncthreads();
-    put(Xh, Xl);
+    // X stays exactly skew (see ns_store): its upper half, and the negated mirror
+    each([&](int row, int col, float v) {
+      if (row < col) {
+        const f16 hv = (f16)v, lv = (f16)(v - (float)hv);
+        Xh[row * LD + col] = hv;
+        Xl[row * LD + col] = lv;
+        Xh[col * LD + row] = -hv;
+        Xl[col * LD + row] = -lv;
+      }
+      return v;
+    });
     __syncthreads();
   }
 }
@@ -544,18 +731,33 @@ template <typename T> struct Dense {
   PX_DEV T* at(int z, int64_t i, int64_t kk) const { return p + z * stride + (flip ? kk * ld + i : i * ld + kk); }
 };
 
-// each workgroup's sum of squares in 64 bits over rows blockIdx.x, + gridDim.x, ... of the stored matrix
+// 8 elements from c of a stored row of n, zeros past its end; rows need no alignment beyond the element's
+template <typename T> PX_DEV void load8(const T* row, int64_t c, int64_t n, float (&v)[8]) {
+  T t[8];
+  if (c + 8 <= n) {
+    __builtin_memcpy(t, row + c, 8 * sizeof(T));
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t[e] = c + e < n ? row[c + e] : T(0);
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = to_f32<T>(t[e]);
+}
+
+// each workgroup's sum of squares in 64 bits: the runs of 8 elements of the stored rows, dealt to the grid's threads
 template <typename T>
 __global__ __launch_bounds__(256) void k_orth_norm(Dense<const T> G, double* __restrict__ part) {
   __shared__ double red[4];
-  const int z = blockIdx.y, rows = G.flip ? G.k : G.r, cols = G.flip ? G.r : G.k;
+  const int z = blockIdx.y;
+  const int64_t rows = G.flip ? G.k : G.r, cols = G.flip ? G.r : G.k, per = (cols + 7) / 8, n = rows * per;
+  const T* base = G.p + z * G.stride;
   double sum = 0.0;
-  for (int i = blockIdx.x; i < rows; i += gridDim.x) {
-    const T* row = G.p + z * G.stride + i * G.ld;
-    for (int j = threadIdx.x; j < cols; j += 256) {
-      const double v = to_f32<T>(row[j]);
-      sum += v * v;
-    }
+#pragma unroll 4
+  for (int64_t c = (int64_t)blockIdx.x * 256 + threadIdx.x; c < n; c += (int64_t)gridDim.x * 256) {
+    float v[8];
+    load8<T>(base + c / per * G.ld, c % per * 8, cols, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum += (double)v[e] * v[e];
   }
 #pragma unroll
   for (int o = 32; o >= 1; o >>= 1) sum += __shfl_xor(sum, o);
@@ -567,37 +769,25 @@ __global__ __launch_bounds__(256) void k_orth_norm(Dense<const T> G, double* __r
 // X and X^T planes from the matrix, scaled by sx / (|G|_F + eps), zeros past its ends: one 64 x 64 tile a workgroup.
 template <typename T>
 __global__ __launch_bounds__(256) void k_orth_load(Dense<const T> G, const double* __restrict__ part, int parts, float sx,
-                                                   float eps, Planes X, Planes Xt) {
+                                                   float eps, int tk, Planes X, Planes Xt) {
   __shared__ float t[64][65];
-  const int z = blockIdx.y, tk = (int)(X.ld / 64), i0 = blockIdx.x / tk * 64, k0 = blockIdx.x % tk * 64;
-  double ss = 0.0;
-  for (int p = 0; p < parts; ++p) ss += part[(int64_t)z * parts + p];
-  const double f = (double)sx / (__builtin_sqrt(ss) + (double)eps);
-  const int c = threadIdx.x & 63, rr = threadIdx.x >> 6;
+  const int z = blockIdx.y, i0 = blockIdx.x / tk * 64, k0 = blockIdx.x % tk * 64;
+  const double f = (double)sx / (__builtin_sqrt(sum_parts(part + (int64_t)z * parts, parts)) + (double)eps);
+  // the stored tile, rows a0 and columns c0
+  const int a0 = G.flip ? k0 : i0, c0 = G.flip ? i0 : k0, rows = G.flip ? G.k : G.r, cols = G.flip ? G.r : G.k;
 #pragma unroll
-  for (int e = 0; e < 16; ++e) {
-    // lanes run along the stored rows
-    const int a = rr + 4 * e, i = i0 + (G.flip ? c : a), k = k0 + (G.flip ? a : c);
-    t[i - i0][k - k0] = i < G.r && k < G.k ? (float)((double)to_f32<T>(*G.at(z, i, k)) * f) : 0.f;
+  for (int w = threadIdx.x; w < 64 * 8; w += 256) {
+    const int a = w / 8, c = w % 8 * 8;
+    float v[8];
+    const bool in = a0 + a < rows && c0 + c < cols;
+    load8<T>(G.p + z * G.stride + (in ? (a0 + a) * G.ld : 0), in ? c0 + c : cols, cols, v);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t[a][c + e] = (float)((double)v[e] * f);
   }
   __syncthreads();
-  auto put = [&](const Planes& o, int row0, int col0, auto value) {
-    for (int w = threadIdx.x; w < 64 * 8; w += 256) {
-      const int row = w / 8, col = w % 8 * 8;
-      uint32_t h[4], l[4];
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const uint32_t a = pack_hilo(value(row, col + 2 * e)), b = pack_hilo(value(row, col + 2 * e + 1));
-        h[e] = (a & 0xffff) | (b << 16);
-        l[e] = (a >> 16) | (b & 0xffff0000u);
-      }
-      const int64_t at = (row0 + row) * o.ld + col0 + col;
-      *reinterpret_cast<uint4*>(o.h + at) = make_uint4(h[0], h[1], h[2], h[3]);
-      if (o.l) *reinterpret_cast<uint4*>(o.l + at) = make_uint4(l[0], l[1], l[2], l[3]);
-    }
-  };
-  put(X.at(z, 0), i0, k0, [&](int i, int k) { return t[i][k]; });
-  put(Xt.at(z, 0), k0, i0, [&](int k, int i) { return t[i][k]; });
+  const bool flip = G.flip;
+  put64(X, z, i0, k0, [&](int i, int k) { return flip ? t[k][i] : t[i][k]; });
+  put64(Xt, z, k0, i0, [&](int k, int i) { return flip ? t[k][i] : t[i][k]; });
 }
 
 template <class C>
@@ -617,93 +807,119 @@ PX_DEV void x_tile(int id, int tm, int tn, int& bm, int& bn) {
   bn = id % (8 * tn) / gs;
 }
 
-// Where the partial sums of a split product go: unit-major, then the accumulators in register order, 4 of them for
-// every thread in turn, so that every access is 16 bytes a lane of whole lines.
-template <class C> PX_DEV f32x4_v* part_at(float* part, int64_t unit, int i, int j, int g) {
-  return reinterpret_cast<f32x4_v*>(part) + (((unit * C::TM + i) * C::TN + j) * 4 + g) * C::NT + threadIdx.x;
-}
-
-// out = alpha aux + beta a a^T, symmetric: its tiles on and above the diagonal.  With S > 1 splits of the K loop
-// the workgroups write partial sums, which k_ns_join adds in order.
-template <class C, bool SPLIT>
-__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2))) void k_ns_sym(int tiles, int KT, int S, Planes a, Planes aux, Planes out, float alpha,
-                                                  float beta, float* __restrict__ part) {
+// out = alpha aux + beta a a^T, symmetric: the tiles on and above the diagonal of every matrix of the batch, `per` of
+// them a matrix.  The last `rest` of them run as S splits of the K loop each, which write their sums to `part` for
+// k_ns_join (they would leave most of a round of workgroups empty).
+template <class C>
+__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2))) void k_ns_sym(
+    int tiles, int KT, int full, int rest, int S, Planes a, Planes aux, Planes out, float alpha, float beta,
+    float* __restrict__ part) {
   extern __shared__ __align__(16) unsigned char smem[];
   char* lds = reinterpret_cast<char*>(smem);
   const int per = tiles * (tiles + 1) / 2;
-  const int u = xcd_unit(blockIdx.x, gridDim.x), z = u / (per * S), sp = u / per % S;
+  const bool whole = (int)blockIdx.x < full;
+  const int u = whole ? xcd_unit(blockIdx.x, full) : xcd_unit(blockIdx.x - full, rest * S);
+  const int tile = whole ? u : full + u % rest, sp = whole ? 0 : u / rest, z = tile / per;
   int ti, tj;
-  upper_tile(u % per, tiles, ti, tj);
-  const int k0 = (int)((int64_t)sp * KT / S), k1 = (int)((int64_t)(sp + 1) * KT / S);
+  upper_tile(tile % per, tiles, ti, tj);
+  const int k0 = whole ? 0 : (int)((int64_t)sp * KT / S), k1 = whole ? KT : (int)((int64_t)(sp + 1) * KT / S);
   Acc<C> acc;
-  ns_loop<C>(lds, a.tile(z, ti * C::BM, k0 * C::BK), a.tile(z, tj * C::BN, k0 * C::BK), k1 - k0, C::BM == 128 && ti == tj,
-             acc);  // (the 256 tile's registers leave no room for the second set of addresses)
-  if constexpr (SPLIT) {
-#pragma unroll
-    for (int i = 0; i < C::TM; ++i)
-#pragma unroll
-      for (int j = 0; j < C::TN; ++j)
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-          *part_at<C>(part, u, i, j, g) = f32x4_v{acc.v[i][j][4 * g], acc.v[i][j][4 * g + 1], acc.v[i][j][4 * g + 2],
-                                                  acc.v[i][j][4 * g + 3]};
-  } else {
+  ns_loop<C>(lds, a.tile(z, ti * C::BM, k0 * C::BK), a.tile(z, tj * C::BN, k0 * C::BK), k1 - k0, ti == tj, acc);
+  if (whole) {
     finish_sym<C>(lds, acc, z, ti, tj, aux, out, alpha, beta);
+  } else {
+    const Planes none{};
+    float* o = part + (int64_t)u * C::BM * C::BN;
+    ns_store<C>(lds, acc, none, 0.f, 1.f, none, none, 0, [&](int r0, const float* st) {
+      for (int c = threadIdx.x; c < C::RS * C::BN; c += C::NT)
+        o[(int64_t)r0 * C::BN + c] = st[c / C::BN * C::PITCH + c % C::BN];
+    });
   }
 }
 
-// the partial sums of one tile, in split order
-template <class C>
-__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2))) void k_ns_join(int tiles, int S, Planes aux, Planes out, float alpha, float beta,
-                                                   float* __restrict__ part) {
-  extern __shared__ __align__(16) unsigned char smem[];
-  const int per = tiles * (tiles + 1) / 2, z = blockIdx.x / per, ut = blockIdx.x % per;
+// alpha aux + beta times the sum over the splits (in order) of a 16 x 64 strip of one of the split BM x BM tiles, and
+// its mirror
+__global__ __launch_bounds__(256) void k_ns_join(int BM, int tiles, int full, int rest, int S, Planes aux, Planes out,
+                                                 float alpha, float beta, const float* __restrict__ part) {
+  __shared__ float t[16][65];
+  const int per = tiles * (tiles + 1) / 2, cols = BM / 64, strips = BM / 16 * cols, v = blockIdx.x / strips;
+  const int si = blockIdx.x % strips / cols * 16, sj = blockIdx.x % cols * 64, z = (full + v) / per;
   int ti, tj;
-  upper_tile(ut, tiles, ti, tj);
-  Acc<C> acc;
-  acc.zero();
-  for (int sp = 0; sp < S; ++sp)
+  upper_tile((full + v) % per, tiles, ti, tj);
+  const int c = threadIdx.x % 16 * 4, r = threadIdx.x / 16;
+  const int64_t i0 = (int64_t)ti * BM + si, j0 = (int64_t)tj * BM + sj, one = (int64_t)rest * BM * BM;
+  const float* P = part + (int64_t)v * BM * BM + (int64_t)(si + r) * BM + sj + c;
+  f32x4_v s = {}, x = {};
+  int sp = 0;
+  for (; sp + 8 <= S; sp += 8) {
+    f32x4_v w[8];
 #pragma unroll
-    for (int i = 0; i < C::TM; ++i)
+    for (int e = 0; e < 8; ++e) w[e] = *reinterpret_cast<const f32x4_v*>(P + (sp + e) * one);
 #pragma unroll
-      for (int j = 0; j < C::TN; ++j)
+    for (int e = 0; e < 8; ++e) s += w[e];
+  }
+  for (; sp < S; ++sp) s += *reinterpret_cast<const f32x4_v*>(P + sp * one);
+  if (aux.h) {
+    // strips start at multiples of 16 rows, tiles at multiples of 64 columns
+    const Planes p = aux.tile(z, i0, j0);
+    const int64_t at = r * p.ld + plane_col(p.inter, c);
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const f32x4_v v = *part_at<C>(part, ((int64_t)z * S + sp) * per + ut, i, j, g);
+    for (int q = 0; q < 4; ++q) x[q] = plane_value(p.h[at + q], p.l ? p.l[at + q] : f16(0));
+  }
 #pragma unroll
-          for (int e = 0; e < 4; ++e) acc.v[i][j][4 * g + e] += v[e];
-        }
-  finish_sym<C>(reinterpret_cast<char*>(smem), acc, z, ti, tj, aux, out, alpha, beta);
+  for (int q = 0; q < 4; ++q) t[r][c + q] = alpha * x[q] + beta * s[q];
+  __syncthreads();
+  // half the threads write the strip in rows, the others its mirror (a column of the strip is a run of 16)
+  const bool mirror = threadIdx.x >= 128;
+  if (mirror && ti == tj) return;
+  const int w = threadIdx.x % 128, row = mirror ? w / 2 : w / 8, col = mirror ? w % 2 * 8 : w % 8 * 8;
+  uint32_t y[8];
+#pragma unroll
+  for (int e = 0; e < 8; ++e) y[e] = pack_hilo(mirror ? t[col + e][row] : t[row][col + e]);
+  uint4 h, l;
+  split_words(y, 0, h, l);
+  // (the mirror's first column, i0, is a multiple of 16: its planes are taken from the 32 below)
+  const Planes o = mirror ? out.tile(z, j0, i0 / 32 * 32) : out.tile(z, i0, j0);
+  const int64_t at = row * o.ld + plane_col(o.inter, col + (mirror ? (int)(i0 % 32) : 0));
+  put16<true>(o.h + at, h);
+  if (o.l) put16<true>(o.l + at, l);
+}
+
+// The tile of unit u of a launch on parent tiles `first` and on (numbered through the batch, tm x tn of them a matrix),
+// each cut into sub x sub tiles: matrix, first row, first column.
+template <class C> PX_DEV void x_unit(int u, int tm, int tn, int first, int sub, int& z, int& m0, int& n0) {
+  const int p = first + u / (sub * sub), w = u % (sub * sub);
+  z = p / (tm * tn);
+  int bm, bn;
+  x_tile(p % (tm * tn), tm, tn, bm, bn);
+  m0 = (bm * sub + w / sub) * C::BM;
+  n0 = (bn * sub + w % sub) * C::BN;
 }
 
 // X <- alpha X + beta B X on every tile; X is updated in place (a tile is read by its own workgroup only) and its
 // transpose written to the other of two buffers, for the other workgroups still read this one.
 template <class C>
-__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2))) void k_ns_x(int tm, int tn, int KT, Planes B, Planes Xt, Planes X, Planes Xt_out,
+__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2))) void k_ns_x(int tm, int tn, int first, int sub, int KT, Planes B, Planes Xt, Planes X, Planes Xt_out,
                                                 float alpha, float beta) {
   extern __shared__ __align__(16) unsigned char smem[];
   char* lds = reinterpret_cast<char*>(smem);
-  const int u = xcd_unit(blockIdx.x, gridDim.x), z = u / (tm * tn);
-  int bm, bn;
-  x_tile(u % (tm * tn), tm, tn, bm, bn);
-  const int m0 = bm * C::BM, n0 = bn * C::BN;
+  int z, m0, n0;
+  x_unit<C>(xcd_unit(blockIdx.x, gridDim.x), tm, tn, first, sub, z, m0, n0);
   Acc<C> acc;
-  ns_loop<C>(lds, B.at(z, m0), Xt.at(z, n0), KT, false, acc);
+  ns_loop<C>(lds, B.tile(z, m0, 0), Xt.tile(z, n0, 0), KT, false, acc);
   const Planes o = X.tile(z, m0, n0);
   ns_store<C>(lds, acc, o, alpha, beta, o, Xt_out.tile(z, n0, m0), 0, nullptr);
 }
 
 // The last step: alpha X + beta B X to the caller's matrix.
 template <class C, typename T>
-__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2))) void k_ns_out(int tm, int tn, int KT, Planes B, Planes Xt, Planes X, Dense<T> O,
+__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2))) void k_ns_out(int tm, int tn, int first, int sub, int KT, Planes B, Planes Xt, Planes X, Dense<T> O,
                                                   float alpha, float beta) {
   extern __shared__ __align__(16) unsigned char smem[];
-  const int u = xcd_unit(blockIdx.x, gridDim.x), z = u / (tm * tn);
-  int bm, bn;
-  x_tile(u % (tm * tn), tm, tn, bm, bn);
-  const int m0 = bm * C::BM, n0 = bn * C::BN;
+  int z, m0, n0;
+  x_unit<C>(xcd_unit(blockIdx.x, gridDim.x), tm, tn, first, sub, z, m0, n0);
   Acc<C> acc;
-  ns_loop<C>(reinterpret_cast<char*>(smem), B.at(z, m0), Xt.at(z, n0), KT, false, acc);
+  ns_loop<C>(reinterpret_cast<char*>(smem), B.tile(z, m0, 0), Xt.tile(z, n0, 0), KT, false, acc);
   const Planes none{};
   ns_store<C>(reinterpret_cast<char*>(smem), acc, X.tile(z, m0, n0), alpha, beta, none, none, 0,
               [&](int r0, const float* st) {
@@ -717,7 +933,8 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2))) void
   });
 }
 
-constexpr int kNormParts = 256;  // workgroups (and 64-bit partial sums) of one matrix's norm
+// workgroups (and 64-bit partial sums) of one matrix's norm: 4 runs of 8 elements a thread, and no more than fill the GPU
+inline int norm_parts(int64_t elems) { return (int)std::max<int64_t>(1, std::min<int64_t>(1024, elems / (256 * 8 * 4))); }
 
 inline float pow2_near(double x) { return (float)std::exp2(std::round(std::log2(x))); }
 
@@ -738,28 +955,83 @@ struct Carve {
     off += al256(n * sizeof(T));
     return p;
   }
-  Planes planes(int count, int64_t rows, int64_t ld, bool lo) {
+  // planes of count matrices of rows x cols; lo: 0 none, 1 its own buffer, else alternating with hi by `lo`
+  Planes planes(int count, int64_t rows, int64_t cols, int lo) {
     Planes p;
-    p.ld = ld;
-    p.stride = rows * ld;
+    p.inter = lo > 1 ? lo : 0;
+    p.ld = p.inter ? 2 * cols : cols;
+    p.stride = rows * p.ld;
     p.h = take<f16>((size_t)count * p.stride);
-    p.l = lo ? take<f16>((size_t)count * p.stride) : nullptr;
+    p.l = lo == 0 ? nullptr : lo == 1 ? take<f16>((size_t)count * p.stride) : p.h + lo;
     return p;
   }
 };
 
+// The blocks of a step are taken in chunks that bound the workspace, each through all its products.  (Chunks whose
+// three buffers would stay in the 256 MB Infinity Cache ran slower, by the rounds of workgroups that they leave
+// unfilled: 2.45 ms with 160 MB chunks against 2.10 for 160 blocks of 512 at once.)
+constexpr size_t kChunkBytes = size_t(1) << 30;
+constexpr int kInter = NSmall<3>::BK;  // the K step by which hi and lo values alternate
 struct MuonWs {
+  int chunk;  // blocks
   double* part;
+  BlockInfo* info;
   Planes buf[3];
 };
-constexpr int kMomentumParts = 8;
+int momentum_parts(int b) { return (int)cdiv((int64_t)b * (b - 1) / 2, kMomentumSlots); }
 MuonWs muon_plan(Carve& c, int blocks, int b) {
   MuonWs w{};
   if (b <= 128) return w;
   const int P = (int)round_up(b, 128);
-  w.part = c.take<double>((size_t)blocks * kMomentumParts);
-  for (Planes& p : w.buf) p = c.planes(blocks, P, P, true);
+  const int most = (int)std::max<size_t>(1, kChunkBytes / ((size_t)P * P * 12)), chunks = (int)cdiv(blocks, most);
+  w.chunk = (int)cdiv(blocks, chunks);
+  w.part = c.take<double>((size_t)w.chunk * momentum_parts(b));
+  w.info = c.take<BlockInfo>(w.chunk);
+  for (Planes& p : w.buf) p = c.planes(w.chunk, P, P, kInter);
   return w;
+}
+
+// How many of nz blocks of `per` 128 x 128 tiles run on those: whole rounds of workgroups (two a CU), and what is left
+// of them too where it fills more than 0.6 of a round; below 0.8 of one round 64 x 64 tiles are faster throughout.
+int muon_wide(int nz, int per) {
+  constexpr int slots = 512;
+  const int64_t tiles = (int64_t)nz * per, left = tiles % slots;
+  if (tiles < slots) return tiles >= 0.8 * slots ? nz : 0;
+  return left > 0.6 * slots ? nz : (int)((tiles - left) / per);
+}
+
+hipError_t muon_big(MuonTable& t, int b, const MuonK& k, const NsHyper& n, const MuonWs& w, hipStream_t s) {
+  constexpr int lds = std::max(NSmall<3>::LDS, NTiny<3>::LDS);
+  const int NB = t.first[t.count], n128 = (int)cdiv(b, 128);
+  hipError_t e = allow_lds(k_ns_skew<false, false>, lds);
+  if (e == hipSuccess) e = allow_lds(k_ns_skew<true, false>, lds);
+  if (e == hipSuccess) e = allow_lds(k_ns_skew<true, true>, lds);
+  if (e != hipSuccess) return e;
+  const float sx = 8.f * pow2_near(std::sqrt((double)b)), ca = (float)n.a, cb = (float)n.b, cc = (float)n.c;
+  const unsigned t64 = (unsigned)(2 * n128);
+  const int parts = momentum_parts(b);
+  for (t.z0 = 0; t.z0 < NB; t.z0 += w.chunk) {
+    const int nz = std::min(w.chunk, NB - t.z0);
+    k_muon_momentum<<<dim3(parts, nz), 256, 0, s>>>(t, b, k, w.part, w.info);
+    k_muon_unpack<<<dim3(t64 * (t64 + 1) / 2, nz), 256, 0, s>>>(t, b, k, w.part, parts, sx, (int)t64, w.buf[0]);
+    const int per1 = n128 * (n128 + 1) / 2, per2 = n128 * (2 * n128 + 1), wide = muon_wide(nz, per1);
+    const unsigned grid = (unsigned)wide * per1 + (unsigned)(nz - wide) * per2;
+    Planes X = w.buf[0], A = w.buf[1];
+    const Planes B = w.buf[2], none{};
+    for (int it = 0; it < n.steps; ++it) {
+      const SkewArgs ga{X, X, none, A, 0.f, kSA / (sx * sx), 0}, gb{A, A, A, B, cb, cc / kSA, 0};
+      // X' goes over A, which no product reads any more
+      const SkewArgs gx{B, X, X, A, ca, -1.f / kSA, 0x8000u}, gq{B, X, X, none, ca / sx, -1.f / (kSA * sx), 0};
+      k_ns_skew<false, false><<<grid, 256, lds, s>>>(ga, w.info, b, n128, wide, k);
+      k_ns_skew<true, false><<<grid, 256, lds, s>>>(gb, w.info, b, n128, wide, k);
+      if (it + 1 < n.steps)
+        k_ns_skew<true, false><<<grid, 256, lds, s>>>(gx, w.info, b, n128, wide, k);
+      else
+        k_ns_skew<true, true><<<grid, 256, lds, s>>>(gq, w.info, b, n128, wide, k);
+      std::swap(X, A);
+    }
+  }
+  return hipGetLastError();
 }
 
 template <int P, int W> hipError_t muon_small(const MuonTable& t, int b, const MuonK& k, const NsHyper& n, hipStream_t s) {
@@ -797,108 +1069,146 @@ hipError_t muon_batch(int count, float* const* q, const float* const* g, float* 
   if (b <= 32) return muon_small<32, 1>(t, b, k, n, s);
   if (b <= 64) return muon_small<64, 4>(t, b, k, n, s);
   if (b <= 128) return muon_small<128, 4>(t, b, k, n, s);
-  using C = NSmall<3>;
-  const int NB = t.first[count], P = (int)round_up(b, 128), tiles = P / C::BM;
   Carve c{reinterpret_cast<char*>(ws)};
-  MuonWs w = muon_plan(c, NB, b);
-  hipError_t e = allow_lds(k_ns_skew<C, false, false>, C::LDS);
-  if (e == hipSuccess) e = allow_lds(k_ns_skew<C, true, false>, C::LDS);
-  if (e == hipSuccess) e = allow_lds(k_ns_skew<C, true, true>, C::LDS);
-  if (e != hipSuccess) return e;
-  const float sx = 8.f * pow2_near(std::sqrt((double)b)), a = (float)n.a, bb = (float)n.b, cc = (float)n.c;
-  k_muon_momentum<<<dim3(kMomentumParts, NB), 256, 0, s>>>(t, b, k, w.part);
-  const unsigned t64 = (unsigned)(P / 64);
-  k_muon_unpack<<<dim3(t64 * (t64 + 1) / 2, NB), 256, 0, s>>>(t, b, k, w.part, kMomentumParts, sx, w.buf[0]);
-  const unsigned grid = (unsigned)(tiles * (tiles + 1) / 2) * NB;
-  Planes X = w.buf[0], A = w.buf[1];
-  const Planes B = w.buf[2];
-  for (int it = 0; it < n.steps; ++it) {
-    k_ns_skew<C, false, false><<<grid, C::NT, C::LDS, s>>>(t, b, tiles, X, X, X, A, 0.f, kSA / (sx * sx), 0, k);
-    k_ns_skew<C, true, false><<<grid, C::NT, C::LDS, s>>>(t, b, tiles, A, A, A, B, bb, cc / kSA, 0, k);
-    if (it + 1 < n.steps) {
-      // X' over A, which no product reads any more
-      k_ns_skew<C, true, false><<<grid, C::NT, C::LDS, s>>>(t, b, tiles, B, X, X, A, a, -1.f / kSA, 0x8000u, k);
-      std::swap(X, A);
-    } else {
-      k_ns_skew<C, true, true><<<grid, C::NT, C::LDS, s>>>(t, b, tiles, B, X, X, A, a / sx, -1.f / (kSA * sx), 0, k);
-    }
-  }
-  return hipGetLastError();
+  return muon_big(t, b, k, n, muon_plan(c, t.first[count], b), s);
 }
 
 namespace {
 
+// How the tiles of one symmetric product run: `full` of them whole, the other `rest` in S splits.
+struct SymPlan {
+  int tile, tiles;  // tile size, tiles a side
+  int full, rest, S;
+  size_t part() const { return (size_t)rest * S * tile * tile; }
+};
+SymPlan sym_plan(int count, int r, int k, int bk) {
+  SymPlan p{};
+  const auto units = [&](int t) { const int64_t n = cdiv(r, t); return count * n * (n + 1) / 2; };
+  constexpr int slots = 512;  // two workgroups a CU
+  p.tile = units(128) >= 0.8 * slots ? 128 : 64;
+  p.tiles = (int)cdiv(r, p.tile);
+  const int64_t n = units(p.tile);
+  const int KT = (int)cdiv(k, bk), left = (int)(n % slots);
+  p.S = 1;
+  if (left > 0 && left <= 0.6 * slots) {
+    // rounds of workgroups times the K tiles of one, and what the launch that joins them (about 16 K tiles' time) and
+    // the partial sums cost
+    double best = KT;
+    for (int S = 2; S <= 32 && S * 4 <= KT; ++S) {
+      const double cost = (double)cdiv((int64_t)left * S, slots) * cdiv(KT, S) + 16.0 + 4.0 * S * left / slots + 0.25 * S;
+      if (cost < best) {
+        best = cost;
+        p.S = S;
+      }
+    }
+  }
+  p.rest = p.S > 1 ? left : 0;
+  p.full = (int)(n - p.rest);
+  return p;
+}
+
 struct OrthPlan {
-  int r, k, np, tile, rp, kp, splits;
+  int r, k, np, rp, kp;
+  SymPlan a, b;
+  int xtile;     // tile size of X's products, and
+  int xn, xwide;  // of 256: tiles, and how many run whole (the rest as 128 x 128)
   double* part;
   float* sums;
   Planes X, Xt[2], A, B;
 };
 
-// The tile, the products per product and the split of the A product's K loop.
 OrthPlan orth_plan(Carve& c, int count, int rows, int cols, int dt) {
   OrthPlan p{};
   p.r = std::min(rows, cols);
   p.k = std::max(rows, cols);
   // a short side of up to 128 leaves so few roundings to average over that fp16 products alone lose digits
   p.np = dt == F32 || p.r <= 128 ? 3 : 1;
-  p.tile = (int64_t)count * cdiv(p.r, 256) * cdiv(p.k, 256) >= 256 ? 256 : 128;
-  p.rp = (int)round_up(p.r, p.tile);
-  p.kp = (int)round_up(p.k, p.tile);
-  const int64_t tiles = p.rp / p.tile, units = tiles * (tiles + 1) / 2 * count;
-  const int KT = (int)cdiv(p.k, p.np == 3 ? 32 : 64), slots = p.tile == 256 ? 256 : 512;
-  p.splits = 1;
-  double best = 0;
-  for (int S = 1; S <= 32 && S * 4 <= KT; ++S) {
-    // rounds of workgroups times the K tiles of one, and what S partial sums of every tile cost in K tiles
-    const double cost = (double)cdiv(units * S, slots) * cdiv(KT, S) + (S > 1 ? 2.0 + 2.0 * S * units / slots : 0.0);
-    if (S == 1 || cost < best) {
-      p.splits = S;
-      best = cost;
-    }
+  const int bk = p.np == 3 ? NSmall<3>::BK : NSmall<1>::BK;
+  p.a = sym_plan(count, p.r, p.k, bk);
+  p.b = sym_plan(count, p.r, p.r, bk);
+  const auto units = [&](int t) { return (int64_t)count * cdiv(p.r, t) * cdiv(p.k, t); };
+  p.xtile = units(256) >= 256 ? 256 : units(128) >= 400 ? 128 : 64;
+  if (p.xtile == 256) {
+    // whole rounds of 256 workgroups, and what is left of them too where it fills more than 0.7 of a round
+    p.xn = (int)units(256);
+    p.xwide = p.xn % 256 > 0.7 * 256 ? p.xn : p.xn / 256 * 256;
   }
-  const bool lo = p.np == 3;
-  p.part = c.take<double>((size_t)count * kNormParts);
-  p.X = c.planes(count, p.rp, p.kp, true);
+  p.rp = (int)round_up(p.r, std::max(p.xtile, p.a.tile));
+  p.kp = (int)round_up(p.k, p.xtile);
+  const int lo = p.np == 3 ? kInter : 0;
+  p.part = c.take<double>((size_t)count * norm_parts((int64_t)rows * cols));
+  p.X = c.planes(count, p.rp, p.kp, lo ? lo : 1);
   for (Planes& t : p.Xt) t = c.planes(count, p.kp, p.rp, lo);
   p.A = c.planes(count, p.rp, p.rp, lo);
   p.B = c.planes(count, p.rp, p.rp, lo);
-  p.sums = p.splits > 1 ? c.take<float>((size_t)p.splits * units * p.tile * p.tile) : nullptr;
+  p.sums = c.take<float>(std::max(p.a.part(), p.b.part()));
   return p;
 }
 
+// out = alpha aux + beta a a^T over K columns
+template <class C>
+hipError_t sym_launch(const SymPlan& p, int K, const Planes& a, const Planes& aux, const Planes& out, float alpha,
+                      float beta, float* sums, hipStream_t s) {
+  const hipError_t e = allow_lds(k_ns_sym<C>, C::LDS);
+  if (e != hipSuccess) return e;
+  k_ns_sym<C><<<p.full + p.rest * p.S, C::NT, C::LDS, s>>>(p.tiles, (int)cdiv(K, C::BK), p.full, p.rest, p.S, a, aux, out,
+                                                            alpha, beta, sums);
+  if (p.rest > 0)
+    k_ns_join<<<p.rest * (C::BM / 16) * (C::BM / 64), 256, 0, s>>>(C::BM, p.tiles, p.full, p.rest, p.S, aux, out, alpha,
+                                                                 beta, sums);
+  return hipGetLastError();
+}
+template <int NP>
+hipError_t sym_run(const SymPlan& p, int K, const Planes& a, const Planes& aux, const Planes& out, float alpha, float beta,
+                   float* sums, hipStream_t s) {
+  if (p.tile == 128) return sym_launch<NSmall<NP>>(p, K, a, aux, out, alpha, beta, sums, s);
+  return sym_launch<NTiny<NP>>(p, K, a, aux, out, alpha, beta, sums, s);
+}
+
+// X' (or with `last` the caller's matrix) on parent tiles first .. first + n of sub x sub tiles
 template <class C, typename T>
+hipError_t x_launch(const OrthPlan& p, int first, int n, int sub, const Planes& cur, const Planes& nxt, bool last,
+                    const Dense<T>& O, float alpha, float beta, hipStream_t s) {
+  hipError_t e = allow_lds(k_ns_x<C>, C::LDS);
+  if (e == hipSuccess) e = allow_lds(k_ns_out<C, T>, C::LDS);
+  if (e != hipSuccess || n == 0) return e;
+  const int tm = (int)cdiv(p.r, C::BM * sub), tn = (int)cdiv(p.k, C::BN * sub), KR = (int)cdiv(p.r, C::BK);
+  const unsigned grid = (unsigned)n * sub * sub;
+  if (last)
+    k_ns_out<C, T><<<grid, C::NT, C::LDS, s>>>(tm, tn, first, sub, KR, p.B, cur, p.X, O, alpha, beta);
+  else
+    k_ns_x<C><<<grid, C::NT, C::LDS, s>>>(tm, tn, first, sub, KR, p.B, cur, p.X, nxt, alpha, beta);
+  return hipGetLastError();
+}
+
+template <int NP, typename T>
 hipError_t orth_run(const OrthPlan& p, int count, const Dense<const T>& G, const Dense<T>& O, const NsHyper& n,
                     hipStream_t s) {
-  hipError_t e = allow_lds(k_ns_sym<C, false>, C::LDS);
-  if (e == hipSuccess) e = allow_lds(k_ns_sym<C, true>, C::LDS);
-  if (e == hipSuccess) e = allow_lds(k_ns_join<C>, C::EPI);
-  if (e == hipSuccess) e = allow_lds(k_ns_x<C>, C::LDS);
-  if (e == hipSuccess) e = allow_lds(k_ns_out<C, T>, C::LDS);
-  if (e != hipSuccess) return e;
   const float sx = 8.f * pow2_near(std::sqrt((double)p.k)), a = (float)n.a, b = (float)n.b, c = (float)n.c;
   const float scale = n.rms > 0 ? (float)(n.rms * std::sqrt((double)p.k)) : 1.f;
-  const int tm = p.rp / C::BM, tn = p.kp / C::BN, KT = (int)cdiv(p.k, C::BK), KR = (int)cdiv(p.r, C::BK);
-  const unsigned sym = (unsigned)(tm * (tm + 1) / 2) * count, full = (unsigned)(tm * tn) * count;
   const Planes none{};
-  k_orth_norm<T><<<dim3(kNormParts, count), 256, 0, s>>>(G, p.part);
-  k_orth_load<T><<<dim3((unsigned)(p.rp / 64) * (p.kp / 64), count), 256, 0, s>>>(G, p.part, kNormParts, sx, (float)n.eps,
-                                                                              p.X, p.Xt[0]);
+  const int parts = norm_parts((int64_t)p.r * p.k);
+  k_orth_norm<T><<<dim3(parts, count), 256, 0, s>>>(G, p.part);
+  k_orth_load<T><<<dim3((unsigned)(p.rp / 64) * (p.kp / 64), count), 256, 0, s>>>(G, p.part, parts, sx, (float)n.eps,
+                                                                                p.kp / 64, p.X, p.Xt[0]);
   for (int it = 0; it < n.steps; ++it) {
     const Planes &cur = p.Xt[it & 1], &nxt = p.Xt[(it + 1) & 1];
-    if (p.splits > 1)
-      k_ns_sym<C, true><<<sym * p.splits, C::NT, C::LDS, s>>>(tm, KT, p.splits, p.X, none, p.A, 0.f, kSA / (sx * sx), p.sums);
-    else
-      k_ns_sym<C, false><<<sym, C::NT, C::LDS, s>>>(tm, KT, 1, p.X, none, p.A, 0.f, kSA / (sx * sx), nullptr);
-    if (p.splits > 1)
-      k_ns_join<C><<<sym, C::NT, C::EPI, s>>>(tm, p.splits, none, p.A, 0.f, kSA / (sx * sx), p.sums);
-    k_ns_sym<C, false><<<sym, C::NT, C::LDS, s>>>(tm, KR, 1, p.A, p.A, p.B, b, c / kSA, nullptr);
-    if (it + 1 < n.steps)
-      k_ns_x<C><<<full, C::NT, C::LDS, s>>>(tm, tn, KR, p.B, cur, p.X, nxt, a, 1.f / kSA);
-    else
-      k_ns_out<C, T><<<full, C::NT, C::LDS, s>>>(tm, tn, KR, p.B, cur, p.X, O, a * scale / sx, scale / (kSA * sx));
+    hipError_t e = sym_run<NP>(p.a, p.k, p.X, none, p.A, 0.f, kSA / (sx * sx), p.sums, s);
+    if (e == hipSuccess) e = sym_run<NP>(p.b, p.r, p.A, p.A, p.B, b, c / kSA, p.sums, s);
+    const bool last = it + 1 == n.steps;
+    const float al = last ? a * scale / sx : a, be = last ? scale / (kSA * sx) : 1.f / kSA;
+    if (e != hipSuccess) return e;
+    if (p.xtile == 256) {
+      e = x_launch<NBig<NP>, T>(p, 0, p.xwide, 1, cur, nxt, last, O, al, be, s);
+      if (e == hipSuccess) e = x_launch<NSmall<NP>, T>(p, p.xwide, p.xn - p.xwide, 2, cur, nxt, last, O, al, be, s);
+    } else {
+      const int t = p.xtile, nx = (int)(count * cdiv(p.r, t) * cdiv(p.k, t));
+      e = t == 128 ? x_launch<NSmall<NP>, T>(p, 0, nx, 1, cur, nxt, last, O, al, be, s)
+                   : x_launch<NTiny<NP>, T>(p, 0, nx, 1, cur, nxt, last, O, al, be, s);
+    }
+    if (e != hipSuccess) return e;
   }
-  return hipGetLastError();
+  return hipSuccess;
 }
 
 template <typename T>
@@ -909,9 +1219,7 @@ hipError_t orth_t(int count, int rows, int cols, int dt, const void* G, int64_t 
   const int flip = rows > cols;
   const Dense<const T> g{reinterpret_cast<const T*>(G), ldg, sg, p.r, p.k, flip};
   const Dense<T> o{reinterpret_cast<T*>(O), ldo, so, p.r, p.k, flip};
-  if (p.tile == 256)
-    return p.np == 3 ? orth_run<NBig<3>, T>(p, count, g, o, n, s) : orth_run<NBig<1>, T>(p, count, g, o, n, s);
-  return p.np == 3 ? orth_run<NSmall<3>, T>(p, count, g, o, n, s) : orth_run<NSmall<1>, T>(p, count, g, o, n, s);
+  return p.np == 3 ? orth_run<3, T>(p, count, g, o, n, s) : orth_run<1, T>(p, count, g, o, n, s);
 }
 
 }  // namespace

@@ -278,7 +278,7 @@ def test_orthogonalize_matches_oracle(count, rows, cols, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("count,rows,cols", [(7, 700, 2300), (16, 1024, 1024), (8, 2300, 700)])
+@pytest.mark.parametrize("count,rows,cols", [(7, 700, 2300), (16, 1024, 1024), (8, 2300, 700), (4, 1950, 2100)])
 def test_orthogonalize_large_tiles(count, rows, cols, dtype):
     """Enough 256 x 256 tiles for the wide kernels; the first and the last matrix against the oracle."""
     print(f"orth {count}x{rows}x{cols} {dtype}", flush=True)
