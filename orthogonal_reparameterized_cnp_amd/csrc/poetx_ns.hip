@@ -31,6 +31,7 @@
 //
 // Every buffer is padded with zeros to whole tiles, so the K loop copies 16
 // bytes a lane straight into LDS with no bounds.
+#include <atomic>
 #include <cmath>
 #include <cstddef>
 
@@ -42,8 +43,10 @@ namespace {
 
 typedef _Float16 f16;
 typedef _Float16 f16x8_v __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x4_v __attribute__((ext_vector_type(4)));
 
 constexpr float kSA = 256.f;  // scale of A and B
+constexpr int kInter = 32;    // run of hi values between runs of lo values
 
 // Tile configuration of the product kernels: PL planes per operand, a ring of S stages of BK columns.
 template <int BM_, int BN_, int BK_, int WM_, int WN_, int S_, int NP_> struct NCfg {
@@ -58,11 +61,13 @@ template <int BM_, int BN_, int BK_, int WM_, int WN_, int S_, int NP_> struct N
   static constexpr int RS = BM < 128 ? BM : 128, PITCH = BN + 5, EPI = RS * PITCH * 4;
   static constexpr int LDS = S_ * STAGE > EPI ? S_ * STAGE : EPI;
   static_assert(A_BYTES % (1024 * NW) == 0 && B_BYTES % (1024 * NW) == 0, "tile must split into 1 KB per wave");
+  // the K loops run to the next multiple of BK past the last column: no further than the tiles of 64 that hold it
+  static_assert(64 % BK == 0, "K steps stay within written tiles");
   static_assert(BM % RS == 0 && RS % WTM == 0 && PITCH % 64 == 5, "epilogue stage");
 };
-// 4 waves of 32 x 32, two workgroups a CU, three stages in flight: products too small to fill the GPU with larger
-// tiles, bound by latency
-template <int NP> using NTiny = NCfg<64, 64, NP == 3 ? 32 : 64, 2, 2, 4, NP>;
+// 4 waves of 32 x 32, two workgroups a CU: products too small to fill the GPU with larger tiles, bound by latency (for
+// NP = 3 two stages of 64 columns, with half the barriers of four of 32: 40 blocks of 256 in 137 us instead of 142)
+template <int NP> using NTiny = NCfg<64, 64, 64, 2, 2, NP == 3 ? 2 : 4, NP>;
 template <int NP> using NSmall = NCfg<128, 128, NP == 3 ? 32 : 64, 2, 2, 2, NP>;  // 4 waves of 64 x 64, two workgroups a CU
 template <int NP> using NBig = NCfg<256, 256, NP == 3 ? 32 : 64, 4, 2, 2, NP>;    // 8 waves of 64 x 128
 
@@ -81,12 +86,12 @@ PX_DEV uint32_t pack_hilo(float v) {
 }
 
 // One operand: K-contiguous rows of hi (and lo) values, ld fp16 elements apart.  Where the products read both planes
-// (NP = 3) they alternate along the rows, the hi values of a K step of `inter` (16 or 32) and then their lo values
-// (l = h + inter), so that a stage is one run of 64 or 128 bytes of every row.
+// (NP = 3) they alternate along the rows, kInter hi values and then their lo values (l = h + kInter), so that a K step
+// of 32 is one 128-byte line of every row.
 struct Planes {
   f16 *h = nullptr, *l = nullptr;
   int64_t ld = 0, stride = 0;  // stride: fp16 elements from one matrix of the batch to the next
-  int inter = 0;
+  int inter = 0;  // kInter, or 0 for planes of their own
   // the planes from (row, col) of matrix z on; col a multiple of 32
   PX_DEV Planes tile(int z, int64_t row, int64_t col) const {
     if (!h) return *this;
@@ -95,7 +100,7 @@ struct Planes {
   }
 };
 // column of a row's element from its planes' origin
-PX_DEV int plane_col(int inter, int j) { return inter ? j / inter * 2 * inter + j % inter : j; }
+PX_DEV constexpr int plane_col(int inter, int j) { return inter ? j / inter * 2 * inter + j % inter : j; }
 
 // acc = sum over KT tiles of K of a's tile rows times b's tile rows.  `same`: the two tiles are one.
 template <class C> PX_DEV void ns_loop(char* lds, const Planes& a, const Planes& b, int KT, bool same, Acc<C>& acc) {
@@ -128,18 +133,20 @@ template <class C> PX_DEV void ns_loop(char* lds, const Planes& a, const Planes&
     if (nxt < KT) issue(nxt, lds + nxt % C::STAGES * C::STAGE);
     const char* As = lds + kt % C::STAGES * C::STAGE;
     const char* Bs = same ? As : As + C::A_BYTES;
+    // place of k-step ks's hi values in a staged row
+    auto hi = [](int ks) { return C::PL == 2 ? plane_col(kInter, ks * 16) : ks * 16; };
     auto load = [&](int ks, Frags& f) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < C::TM; ++i) {
         const int t0 = p.wm * C::WTM + i * 32;
-        f.ah[i] = as_f16(frag_kmaj<PK>(As, t0, ks * 16, lane));
-        if constexpr (C::PL == 2) f.al[i] = as_f16(frag_kmaj<PK>(As, t0, C::BK + ks * 16, lane));
+        f.ah[i] = as_f16(frag_kmaj<PK>(As, t0, hi(ks), lane));
+        if constexpr (C::PL == 2) f.al[i] = as_f16(frag_kmaj<PK>(As, t0, hi(ks) + kInter, lane));
       }
 #pragma unroll
       for (int j = 0; j < C::TN; ++j) {
         const int t0 = p.wn * C::WTN + j * 32;
-        f.bh[j] = as_f16(frag_kmaj<PK>(Bs, t0, ks * 16, lane));
-        if constexpr (C::PL == 2) f.bl[j] = as_f16(frag_kmaj<PK>(Bs, t0, C::BK + ks * 16, lane));
+        f.bh[j] = as_f16(frag_kmaj<PK>(Bs, t0, hi(ks), lane));
+        if constexpr (C::PL == 2) f.bl[j] = as_f16(frag_kmaj<PK>(Bs, t0, hi(ks) + kInter, lane));
       }
     };
     constexpr int KS = C::BK / 16;
@@ -204,7 +211,7 @@ template <class C, class Emit>
 PX_DEV void ns_store(char* lds, const Acc<C>& acc, const Planes& aux, float alpha, float beta, const Planes& o,
                      const Planes& t, uint32_t flip, const Emit& emit, bool diag = false) {
   constexpr bool EMIT = !std::is_same<Emit, std::nullptr_t>::value;
-  constexpr int INTER = C::PL == 2 ? C::BK : 0;
+  constexpr int INTER = C::PL == 2 ? kInter : 0;
   constexpr int NIT = C::RS * C::BN / 8 / C::NT;  // a thread's share of the pieces of 8
   uint32_t* st = reinterpret_cast<uint32_t*>(lds);
   const AccPos<C> p = acc_pos<C>();
@@ -542,7 +549,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void k
     SkewArgs g, const BlockInfo* __restrict__ info, int b, int n128, int wide, MuonK k) {
   using C1 = NSmall<3>;
   using C2 = NTiny<3>;
-  static_assert(C1::NT == 256 && C2::NT == 256 && C1::BK == C2::BK, "one launch, one layout");
+  static_assert(C1::NT == 256 && C2::NT == 256 && C1::PL == C2::PL, "one launch, one layout");
   extern __shared__ __align__(16) unsigned char smem[];
   char* lds = reinterpret_cast<char*>(smem);
   const int per1 = n128 * (n128 + 1) / 2, per2 = n128 * (2 * n128 + 1), units1 = wide * per1;
@@ -577,29 +584,35 @@ __global__ __launch_bounds__(W * 64) void k_muon_small(MuonTable tab, int b, Muo
   const float* g = tab.g[s] + off;
   float* m = tab.m[s] + off;
   float* q = tab.q[s] + off;
-  // the thread's slots: their updates stay in registers until the norm is known
-  constexpr int NU = (P * (P - 1) / 2 + W * 64 - 1) / (W * 64);
+  // the thread's slots threadIdx.x, + 64 W, ...: their places (i, j), packed, and their updates stay in registers
+  // until the norm is known
+  constexpr int NU = ((P * (P - 1) / 2 + W * 64 - 1) / (W * 64) + 7) / 8 * 8;
   const int slots = b * (b - 1) / 2;
   float u[NU];
+  uint32_t ij[NU];
   double sum = 0.0;
+  {
+    int x = min((int)threadIdx.x, slots - 1), i = slot_i(x, b), j = x - slot_start(i, b) + i + 1;
+    x = threadIdx.x;
 #pragma unroll
-  for (int e0 = 0; e0 < NU; e0 += 8) {
-    float gv[8], mv[8];
+    for (int e0 = 0; e0 < NU; e0 += 8) {
+      float gv[8], mv[8];
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const int x = (e0 + e) * W * 64 + threadIdx.x;
-      const bool ok = x < slots && slot_j(x, b) < r;
-      gv[e] = ok ? g[x] : 0.f;
-      mv[e] = ok ? m[x] : 0.f;
-    }
+      for (int e = 0; e < 8; ++e, x += W * 64) {
+        const bool ok = x < slots && j < r;
+        ij[e0 + e] = ok ? (uint32_t)(i << 16 | j) : 0u;  // (0, 0) is no slot's place
+        gv[e] = ok ? g[x] : 0.f;
+        mv[e] = ok ? m[x] : 0.f;
+        j += W * 64;
+        while (j >= b && i < b) j += ++i + 1 - b;  // the rows get shorter
+      }
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if (e0 + e >= NU) continue;
-      const int x = (e0 + e) * W * 64 + threadIdx.x;
-      mv[e] = k.moment(mv[e], gv[e]);
-      if (x < slots && slot_j(x, b) < r) m[x] = mv[e];
-      u[e0 + e] = k.update(mv[e], gv[e]);
-      sum += (double)u[e0 + e] * u[e0 + e];
+      for (int e = 0; e < 8; ++e) {
+        mv[e] = k.moment(mv[e], gv[e]);
+        if (ij[e0 + e]) m[(e0 + e) * W * 64 + threadIdx.x] = mv[e];
+        u[e0 + e] = k.update(mv[e], gv[e]);
+        sum += (double)u[e0 + e] * u[e0 + e];
+      }
     }
   }
 #pragma unroll
@@ -614,10 +627,8 @@ __global__ __launch_bounds__(W * 64) void k_muon_small(MuonTable tab, int b, Muo
   const double f = (double)sx / (__builtin_sqrt(2.0 * sum) + (double)k.eps);
 #pragma unroll
   for (int e = 0; e < NU; ++e) {
-    const int x = e * W * 64 + threadIdx.x;
-    if (x >= slots) continue;
-    const int i = slot_i(x, b), j = x - slot_start(i, b) + i + 1;
-    if (j >= r) continue;
+    const int i = ij[e] >> 16, j = ij[e] & 0xffff;
+    if (ij[e] == 0) continue;
     const float v = (float)((double)u[e] * f);
     const f16 h = (f16)v, l = (f16)(v - (float)h);
     Xh[i * LD + j] = h;
@@ -658,64 +669,91 @@ __global__ __launch_bounds__(W * 64) void k_muon_small(MuonTable tab, int b, Muo
         }
     }
   };
-  // element = fn(row, col, element) over the wave's part
-  auto each = [&](auto&& fn) __attribute__((always_inline)) {
+  // fn(row, col, values) over the wave's part in runs of 4 rows of one column, the unit a lane owns.  A and B are
+  // symmetric and X is skew, so a run of a column is read and written as the run of the row col: 8 bytes, not 4 times 2
+  auto each4 = [&](auto&& fn) __attribute__((always_inline)) {
     if (idle) return;
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TM; ++j)
 #pragma unroll
-        for (int e = 0; e < 16; ++e)
-          acc[i][j][e] =
-              fn(m0 + i * 32 + 8 * (e >> 2) + 4 * (lane >> 5) + (e & 3), n0 + j * 32 + (lane & 31), (float)acc[i][j][e]);
+        for (int q = 0; q < 4; ++q) {
+          float v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = acc[i][j][4 * q + e];
+          fn(m0 + i * 32 + 8 * q + 4 * (lane >> 5), n0 + j * 32 + (lane & 31), v);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[i][j][4 * q + e] = v[e];
+        }
   };
-  auto put = [&](f16* h, f16* l) __attribute__((always_inline)) {
-    each([&](int row, int col, float v) {
-      const f16 hv = (f16)v;
-      h[row * LD + col] = hv;
-      l[row * LD + col] = (f16)(v - (float)hv);
-      return v;
-    });
+  auto put4 = [&](f16* h, f16* l, int at, const float (&v)[4]) __attribute__((always_inline)) {
+    f16x4_v hv, lv;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      hv[e] = (f16)v[e];
+      lv[e] = (f16)(v[e] - (float)hv[e]);
+    }
+    *reinterpret_cast<f16x4_v*>(h + at) = hv;
+    *reinterpret_cast<f16x4_v*>(l + at) = lv;
+  };
+  auto add4 = [&](const f16* h, const f16* l, int at, float f, float (&v)[4]) __attribute__((always_inline)) {
+    const f16x4_v hv = *reinterpret_cast<const f16x4_v*>(h + at), lv = *reinterpret_cast<const f16x4_v*>(l + at);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) v[e] += f * plane_value(hv[e], lv[e]);
   };
   const float sc = k.scale(r);
   for (int it = 0; it < steps; ++it) {
-    product(Xh, Xl, Xh, Xl);  // A = X X^T
-    each([&](int, int, float v) { return v * (kSA / (sx * sx)); });
-    put(Ah, Al);  // its readers of the last step are past the barrier
+    product(Xh, Xl, Xh, Xl);  // A = X X^T; its place's readers of the last step are past the barrier
+    each4([&](int row, int col, float(&v)[4]) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] *= kSA / (sx * sx);
+      put4(Ah, Al, col * LD + row, v);
+    });
     __syncthreads();
     product(Ah, Al, Ah, Al);  // B = b A + c A A
-    each([&](int row, int col, float v) {
-      return cb * ((float)Ah[row * LD + col] + (float)Al[row * LD + col]) + cc / kSA * v;
+    each4([&](int row, int col, float(&v)[4]) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] *= cc / kSA;
+      add4(Ah, Al, col * LD + row, cb, v);
     });
     __syncthreads();
-    put(Ah, Al);
+    each4([&](int row, int col, float(&v)[4]) { put4(Ah, Al, col * LD + row, v); });
     __syncthreads();
-    product(Ah, Al, Xh, Xl);  // a X - B X^T
-    each([&](int row, int col, float v) {
-      return ca * ((float)Xh[row * LD + col] + (float)Xl[row * LD + col]) - v / kSA;
+    product(Ah, Al, Xh, Xl);  // a X - B X^T, with X[row][col] read as -X[col][row]
+    each4([&](int row, int col, float(&v)[4]) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) v[e] *= -1.f / kSA;
+      add4(Xh, Xl, col * LD + row, -ca, v);
     });
     if (it + 1 == steps) {
-      each([&](int row, int col, float v) {
-        if (row < col && col < r) {
-          float* p = q + packed_slot(row, col, b);
-          *p = k.step(*p, v / sx, sc);
-        }
-        return v;
+      each4([&](int row, int col, float(&v)[4]) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+          if (row + e < col && col < r) {
+            float* p = q + packed_slot(row + e, col, b);
+            *p = k.step(*p, v[e] / sx, sc);
+          }
       });
       return;
     }
     __syncthreads();
     // X stays exactly skew (see ns_store): its upper half, and the negated mirror
-    each([&](int row, int col, float v) {
-      if (row < col) {
-        const f16 hv = (f16)v, lv = (f16)(v - (float)hv);
-        Xh[row * LD + col] = hv;
-        Xl[row * LD + col] = lv;
-        Xh[col * LD + row] = -hv;
-        Xl[col * LD + row] = -lv;
-      }
-      return v;
+    each4([&](int row, int col, float(&v)[4]) {
+      if (row >= col) return;
+      const float n[4] = {-v[0], -v[1], -v[2], -v[3]};
+      if (row + 3 < col) put4(Xh, Xl, col * LD + row, n);
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        if (row + e < col) {
+          const f16 hv = (f16)v[e], lv = (f16)(v[e] - (float)hv);
+          Xh[(row + e) * LD + col] = hv;
+          Xl[(row + e) * LD + col] = lv;
+          if (row + 3 >= col) {
+            Xh[col * LD + row + e] = -hv;
+            Xl[col * LD + row + e] = -lv;
+          }
+        }
     });
     __syncthreads();
   }
@@ -936,6 +974,19 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2))) void
 // workgroups (and 64-bit partial sums) of one matrix's norm: 4 runs of 8 elements a thread, and no more than fill the GPU
 inline int norm_parts(int64_t elems) { return (int)std::max<int64_t>(1, std::min<int64_t>(1024, elems / (256 * 8 * 4))); }
 
+// allow_lds, once per kernel and GPU: a call makes about 20 launches
+template <auto K> hipError_t lds_once(int bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  hipError_t e = hipGetDevice(&dev);
+  if (e != hipSuccess) return e;
+  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
+  if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
+  e = allow_lds(K, bytes);
+  if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 inline float pow2_near(double x) { return (float)std::exp2(std::round(std::log2(x))); }
 
 }  // namespace
@@ -971,7 +1022,6 @@ struct Carve {
 // three buffers would stay in the 256 MB Infinity Cache ran slower, by the rounds of workgroups that they leave
 // unfilled: 2.45 ms with 160 MB chunks against 2.10 for 160 blocks of 512 at once.)
 constexpr size_t kChunkBytes = size_t(1) << 30;
-constexpr int kInter = NSmall<3>::BK;  // the K step by which hi and lo values alternate
 struct MuonWs {
   int chunk;  // blocks
   double* part;
@@ -1003,9 +1053,9 @@ int muon_wide(int nz, int per) {
 hipError_t muon_big(MuonTable& t, int b, const MuonK& k, const NsHyper& n, const MuonWs& w, hipStream_t s) {
   constexpr int lds = std::max(NSmall<3>::LDS, NTiny<3>::LDS);
   const int NB = t.first[t.count], n128 = (int)cdiv(b, 128);
-  hipError_t e = allow_lds(k_ns_skew<false, false>, lds);
-  if (e == hipSuccess) e = allow_lds(k_ns_skew<true, false>, lds);
-  if (e == hipSuccess) e = allow_lds(k_ns_skew<true, true>, lds);
+  hipError_t e = lds_once<k_ns_skew<false, false>>(lds);
+  if (e == hipSuccess) e = lds_once<k_ns_skew<true, false>>(lds);
+  if (e == hipSuccess) e = lds_once<k_ns_skew<true, true>>(lds);
   if (e != hipSuccess) return e;
   const float sx = 8.f * pow2_near(std::sqrt((double)b)), ca = (float)n.a, cb = (float)n.b, cc = (float)n.c;
   const unsigned t64 = (unsigned)(2 * n128);
@@ -1036,7 +1086,7 @@ hipError_t muon_big(MuonTable& t, int b, const MuonK& k, const NsHyper& n, const
 
 template <int P, int W> hipError_t muon_small(const MuonTable& t, int b, const MuonK& k, const NsHyper& n, hipStream_t s) {
   constexpr int lds = 4 * P * (P + 8) * 2;
-  const hipError_t e = allow_lds(k_muon_small<P, W>, lds);
+  const hipError_t e = lds_once<k_muon_small<P, W>>(lds);
   if (e != hipSuccess) return e;
   k_muon_small<P, W><<<t.first[t.count], W * 64, lds, s>>>(t, b, k, n.steps, (float)n.a, (float)n.b, (float)n.c,
                                                            8.f * pow2_near(std::sqrt((double)b)));
@@ -1123,7 +1173,7 @@ OrthPlan orth_plan(Carve& c, int count, int rows, int cols, int dt) {
   p.k = std::max(rows, cols);
   // a short side of up to 128 leaves so few roundings to average over that fp16 products alone lose digits
   p.np = dt == F32 || p.r <= 128 ? 3 : 1;
-  const int bk = p.np == 3 ? NSmall<3>::BK : NSmall<1>::BK;
+  const int bk = p.np == 3 ? 32 : 64;  // one line of a row
   p.a = sym_plan(count, p.r, p.k, bk);
   p.b = sym_plan(count, p.r, p.r, bk);
   const auto units = [&](int t) { return (int64_t)count * cdiv(p.r, t) * cdiv(p.k, t); };
@@ -1149,7 +1199,7 @@ OrthPlan orth_plan(Carve& c, int count, int rows, int cols, int dt) {
 template <class C>
 hipError_t sym_launch(const SymPlan& p, int K, const Planes& a, const Planes& aux, const Planes& out, float alpha,
                       float beta, float* sums, hipStream_t s) {
-  const hipError_t e = allow_lds(k_ns_sym<C>, C::LDS);
+  const hipError_t e = lds_once<k_ns_sym<C>>(C::LDS);
   if (e != hipSuccess) return e;
   k_ns_sym<C><<<p.full + p.rest * p.S, C::NT, C::LDS, s>>>(p.tiles, (int)cdiv(K, C::BK), p.full, p.rest, p.S, a, aux, out,
                                                             alpha, beta, sums);
@@ -1169,8 +1219,8 @@ hipError_t sym_run(const SymPlan& p, int K, const Planes& a, const Planes& aux, 
 template <class C, typename T>
 hipError_t x_launch(const OrthPlan& p, int first, int n, int sub, const Planes& cur, const Planes& nxt, bool last,
                     const Dense<T>& O, float alpha, float beta, hipStream_t s) {
-  hipError_t e = allow_lds(k_ns_x<C>, C::LDS);
-  if (e == hipSuccess) e = allow_lds(k_ns_out<C, T>, C::LDS);
+  hipError_t e = lds_once<k_ns_x<C>>(C::LDS);
+  if (e == hipSuccess) e = lds_once<k_ns_out<C, T>>(C::LDS);
   if (e != hipSuccess || n == 0) return e;
   const int tm = (int)cdiv(p.r, C::BM * sub), tn = (int)cdiv(p.k, C::BN * sub), KR = (int)cdiv(p.r, C::BK);
   const unsigned grid = (unsigned)n * sub * sub;
