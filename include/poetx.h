@@ -642,8 +642,9 @@ typedef struct {
 } poetx_muon_params;
 
 /* Workspace bytes of poetx_muon_step_batch for `count` sides of lengths d[i]
- * (host array) and block size b (0 for b <= 128, which needs none); 0 for
- * invalid arguments. */
+ * (host array) and block size b: about 12 bytes for each of a block's
+ * round_up(b, 128)^2 entries, for as many blocks as fit 1 GiB (one at least);
+ * 0 for b <= 128, which needs none, and for invalid arguments. */
 size_t poetx_muon_workspace_size(int32_t count, const int32_t* d, int32_t b);
 
 /*
@@ -661,8 +662,10 @@ size_t poetx_muon_workspace_size(int32_t count, const int32_t* d, int32_t b);
  *          [ceil(d[i]/b)][b(b-1)/2], read and overwritten (m: momentum)
  *   dq     HOST array [count] of device pointers to the gradients, read only
  *   ws     >= poetx_muon_workspace_size(count, d, b), 256-byte aligned
- * The arrays must not overlap.  count 1 .. POETX_MAX_SIDES; b 2 .. 1024.
- * Errors: POETX_E_NULL, POETX_E_SHAPE (a size or parameter out of range),
+ * An array of q or m must not overlap any other array.  count 1 ..
+ * POETX_MAX_SIDES; b 2 .. 1024.
+ * Errors: POETX_E_NULL, POETX_E_SHAPE (a size or parameter out of range, arrays
+ * that overlap),
  * POETX_E_WORKSPACE, POETX_E_HIP.
  */
 poetx_status poetx_muon_step_batch(int32_t count, float* const* q, const float* const* dq, float* const* m,
@@ -675,7 +678,8 @@ size_t poetx_orthogonalize_workspace_size(int32_t count, int32_t rows, int32_t c
 /*
  * The orthogonalisation of `count` dense matrices of one shape, for the
  * parameters of a model that stay dense.
- *   rows, cols  1 .. 131072;  count  1 .. 1024;  dtype  POETX_F32 or POETX_BF16
+ *   rows, cols  1 .. 131072;  count  1 .. 1024, with count (rows / 128 + 1)
+ *          (cols / 128 + 1) at most 2^23;  dtype  POETX_F32 or POETX_BF16
  *   G      matrix i at G + i stride_g elements, rows ld_g >= cols apart
  *   O      out, likewise with stride_o and ld_o; may be G itself (same ld and
  *          stride), else they must not overlap.  The strides matter for

@@ -1685,14 +1685,30 @@ poetx_status check_ns(const poetx_ns_params& n) {
   return POETX_OK;
 }
 
+// Whether an array that a step writes shares memory with another of its arrays (arrays that are only read may).
+struct Extent {
+  uintptr_t at, end;
+  bool written;
+};
+bool overlap(std::vector<Extent>& v) {
+  std::sort(v.begin(), v.end(), [](const Extent& a, const Extent& b) { return a.at < b.at; });
+  uintptr_t end = 0, end_written = 0;  // of the extents so far
+  for (const Extent& e : v) {
+    if (e.at < (e.written ? end : end_written)) return true;
+    end = std::max(end, e.end);
+    if (e.written) end_written = std::max(end_written, e.end);
+  }
+  return false;
+}
+
 NsHyper ns_hyper(const poetx_ns_params& n) { return NsHyper{n.steps, n.a, n.b, n.c, n.eps, n.rms}; }
 
 poetx_status check_orth(int32_t count, int32_t rows, int32_t cols, int32_t dtype) {
   if (count < 1 || count > 1024) return fail(POETX_E_SHAPE, "count must be in [1, 1024]");
   if (rows < 1 || cols < 1 || rows > (1 << 17) || cols > (1 << 17))
     return fail(POETX_E_SHAPE, "rows and cols must be in [1, 131072]");
-  // one launch's tiles (of 128 x 128, by up to 32 splits) stay within a grid dimension
-  if ((double)count * (rows / 128 + 1) * (cols / 128 + 1) > (double)(1 << 25))
+  // one launch's threads (256 for every 128 x 128 tile) stay within a grid dimension
+  if ((double)count * (rows / 128 + 1) * (cols / 128 + 1) > (double)(1 << 23))
     return fail(POETX_E_SHAPE, "count * rows * cols is too large for one call");
   if (dtype != POETX_F32 && dtype != POETX_BF16) return fail(POETX_E_DTYPE, "dtype must be F32 or BF16");
   return POETX_OK;
@@ -1722,6 +1738,13 @@ poetx_status poetx_muon_step_batch(int32_t count, float* const* q, const float* 
   if ((st = check_ns(hp->ns)) != POETX_OK) return st;
   for (int i = 0; i < count; ++i)
     if (!q[i] || !dq[i] || !m[i]) return fail(POETX_E_NULL, "q[i], dq[i] and m[i] must be non-NULL");
+  std::vector<Extent> arrays;
+  for (int i = 0; i < count; ++i) {
+    const uintptr_t bytes = (uintptr_t)nblocks(d[i], b) * packed_len(b) * 4;
+    for (const float* p : {(const float*)q[i], (const float*)m[i], dq[i]})
+      arrays.push_back(Extent{reinterpret_cast<uintptr_t>(p), reinterpret_cast<uintptr_t>(p) + bytes, p != dq[i]});
+  }
+  if (overlap(arrays)) return fail(POETX_E_SHAPE, "q, dq and m must not overlap");
   if ((st = check_ws(ws, ws_bytes, muon_ws_bytes(nb, b))) != POETX_OK) return st;
   double slots = 0, cubes = 0;
   for (int i = 0; i < count; ++i) {

@@ -102,8 +102,11 @@ struct Planes {
 // column of a row's element from its planes' origin
 PX_DEV constexpr int plane_col(int inter, int j) { return inter ? j / inter * 2 * inter + j % inter : j; }
 
-// acc = sum over KT tiles of K of a's tile rows times b's tile rows.  `same`: the two tiles are one.
-template <class C> PX_DEV void ns_loop(char* lds, const Planes& a, const Planes& b, int KT, bool same, Acc<C>& acc) {
+// acc = sum over KT tiles of K of a's tile rows times b's tile rows.  `same`: the two tiles are one.  `upper`: only
+// what lies on and above the tile's diagonal is wanted, so that waves whose part lies below it multiply nothing (and
+// results do not depend on the tile a block ran on: what is below a diagonal is always a mirror).
+template <class C>
+PX_DEV void ns_loop(char* lds, const Planes& a, const Planes& b, int KT, bool same, Acc<C>& acc, bool upper = false) {
   constexpr int PK = C::BK * C::PL;  // fp16 elements of a row in a stage
   const AccPos<C> p = acc_pos<C>();
   const int wave = threadIdx.x >> 6, lane = p.lane;
@@ -131,6 +134,7 @@ template <class C> PX_DEV void ns_loop(char* lds, const Planes& a, const Planes&
     barrier_raw();
     const int nxt = kt + C::STAGES - 1;
     if (nxt < KT) issue(nxt, lds + nxt % C::STAGES * C::STAGE);
+    if (upper && p.wm > p.wn) continue;
     const char* As = lds + kt % C::STAGES * C::STAGE;
     const char* Bs = same ? As : As + C::A_BYTES;
     // place of k-step ks's hi values in a staged row
@@ -204,8 +208,8 @@ template <bool NT> PX_DEV void put16(f16* p, const uint4& v) {
 // writes them to the planes `o` (null: none) and leaves them in LDS, as (hi, lo) words where `t` (the transposed
 // tile's planes; null: none) is written from there with `flip` (0x8000 negates), as floats for emit(r0, stage).
 // All planes are at the tile's origin; null lo planes are skipped.  `diag` (with `t` the tile itself): the tile lies on
-// the diagonal of a skew matrix, and its values below the diagonal are the negated mirrors of those above.  A computed
-// skew matrix would be off by its roundings there, and the products that read X^T as -X, from rows alone, would see
+// the diagonal of a symmetric or, with `flip`, skew matrix, and its values below the diagonal are the mirrors of those
+// above.  A computed skew matrix would be off by its roundings there, and the products that read X^T as -X, from rows alone, would see
 // the sign of that symmetric part turned over: it grows by about 5 a step where a rounding otherwise grows by 3.4.
 template <class C, class Emit>
 PX_DEV void ns_store(char* lds, const Acc<C>& acc, const Planes& aux, float alpha, float beta, const Planes& o,
@@ -291,7 +295,7 @@ PX_DEV void ns_store(char* lds, const Acc<C>& acc, const Planes& aux, float alph
 #pragma unroll
           for (int e = 0; e < 8; ++e) {
             const uint32_t up = st[min(i, j + e) * C::PITCH + r0 + max(i, j + e)];
-            x[e] = j + e > i ? up : j + e < i ? up ^ 0x80008000u : 0u;
+            x[e] = j + e > i ? up : j + e < i ? up ^ (flip | flip << 16) : flip ? 0u : up;
           }
           uint4 h, l;
           split_words(x, 0, h, l);
@@ -509,12 +513,12 @@ PX_DEV void skew_tile(char* lds, const SkewArgs& g, const BlockInfo* info, int b
   const int r = info[z].r, m0 = ti * C::BM, n0 = tj * C::BN;
   if (n0 >= r) return;  // past the live corner: read by no product
   Acc<C> acc;
-  ns_loop<C>(lds, g.a.tile(z, m0, 0), g.b.tile(z, n0, 0), (r + C::BK - 1) / C::BK, ti == tj && g.a.h == g.b.h, acc);
+  ns_loop<C>(lds, g.a.tile(z, m0, 0), g.b.tile(z, n0, 0), (r + C::BK - 1) / C::BK, ti == tj && g.a.h == g.b.h, acc,
+             ti == tj);
   const Planes none{};
   const Planes x = AUX ? g.aux.tile(z, m0, n0) : none;
   if constexpr (!LAST) {
-    ns_store<C>(lds, acc, x, g.alpha, g.beta, g.out.tile(z, m0, n0),
-                ti == tj && g.flip == 0 ? none : g.out.tile(z, n0, m0), g.flip, nullptr, g.flip != 0 && ti == tj);
+    ns_store<C>(lds, acc, x, g.alpha, g.beta, g.out.tile(z, m0, n0), g.out.tile(z, n0, m0), g.flip, nullptr, ti == tj);
   } else {
     float* q = info[z].q;
     const float sc = k.scale(r);

@@ -232,6 +232,36 @@ def test_many_sides_and_repeats(b):
         check_step(s, hp)
 
 
+def test_more_blocks_than_one_chunk():
+    """1400 blocks of 129 take two passes through the workspace (1 GiB holds 1365), most of them on the wide tiles;
+    blocks on either side of the seam equal calls of their own, and the last one, of 100, its own call and the oracle."""
+    b, nb, last = 129, 1400, 100
+    d, L = b * (nb - 1) + last, b * (b - 1) // 2
+    g = torch.Generator(device="cuda").manual_seed(4)
+    Q, G, M = (torch.randn(nb, L, device="cuda", generator=g) for _ in range(3))
+    q0, g0, m0 = (t[[0, 700, 1364, 1365, 1398, 1399]].clone() for t in (Q, G, M))
+    assert B.poetx_muon_workspace_size([d], b) < 1200 << 20
+    hp = muon_hp()
+    whole = Side.__new__(Side)
+    whole.d, whole.b, whole.Q, whole.G, whole.M = d, b, Q, G, M
+    run_step([whole], b, hp)
+    for i, k in enumerate([0, 700, 1364, 1365, 1398, 1399]):
+        one = Side(np.random.default_rng(0), b if k < nb - 1 else last, b)
+        one.q, one.g, one.m = (t[i:i + 1].cpu().numpy().copy() for t in (q0, g0, m0))
+        one.upload()
+        run_step([one], b, hp)
+        torch.cuda.synchronize()
+        live = torch.from_numpy(~one.dead).cuda() if k == nb - 1 else slice(None)
+        assert torch.equal(one.Q[0], Q[k]) and torch.equal(one.M[0], M[k]), k
+        if k == nb - 1:
+            assert torch.equal(Q[k][~live], q0[i][~live]) and torch.equal(M[k][~live], m0[i][~live])
+            for a in (one.q, one.m):
+                a[-1][one.dead] = np.nan
+            for t in (one.Q, one.M):
+                t[-1][~live] = float("nan")
+        check_step(one, hp) if k in (0, nb - 1) else None
+
+
 def _matrices(rng, count, rows, cols, dtype, pitch=None):
     r = max(1, min(rows, cols) // 8)
     M = rng.standard_normal((count, rows, r)) @ rng.standard_normal((count, r, cols)) / np.sqrt(r)

@@ -24,7 +24,10 @@ def _hp(lr=1e-3, **kw):
     return B.muon_params(lr=lr, **kw)
 
 
-def _step(n=2, q=_pp(FAKE, FAKE), dq=_pp(FAKE, FAKE), m=_pp(FAKE, FAKE), d=_ii(300, 200), b=256, hp=None, ws=FAKE, size=1 << 40):
+MB = 1 << 20  # more than one of these arrays holds
+
+
+def _step(n=2, q=_pp(FAKE, 2 * MB), dq=_pp(3 * MB, 3 * MB), m=_pp(5 * MB, 6 * MB), d=_ii(300, 200), b=256, hp=None, ws=FAKE, size=1 << 40):
     hp = _hp() if hp is None else hp
     return B.lib().poetx_muon_step_batch(n, q, dq, m, d, b, ctypes.byref(hp) if hp else None, ws, size, None)
 
@@ -58,7 +61,7 @@ def test_workspace_sizes():
 
 def test_step_refusals():
     for kw in (dict(q=None), dict(dq=None), dict(m=None), dict(hp=False), dict(d=None), dict(q=_pp(FAKE, None)),
-               dict(dq=_pp(None, FAKE)), dict(m=_pp(FAKE, None)), dict(ws=None)):
+               dict(dq=_pp(None, FAKE)), dict(m=_pp(5 * MB, None)), dict(ws=None)):
         assert _step(**kw) == B.POETX_E_NULL, kw
     for kw in (dict(n=0), dict(n=65), dict(b=1), dict(b=1025), dict(d=_ii(0, 5)), dict(d=_ii(5, (1 << 20) + 1)),
                dict(hp=_hp(lr=-1.0)), dict(hp=_hp(lr=float("nan"))), dict(hp=_hp(beta=1.0)), dict(hp=_hp(beta=-0.1)),
@@ -70,6 +73,23 @@ def test_step_refusals():
     for ns in BAD_NS:
         assert _step(hp=_hp(**ns)) == B.POETX_E_SHAPE, ns
     assert _step(size=16) == B.POETX_E_WORKSPACE and _step(ws=FAKE + 8) == B.POETX_E_WORKSPACE
+
+
+def test_step_refuses_arrays_that_overlap():
+    """b = 4: a side of 8 holds 2 blocks of 6 slots, 48 bytes."""
+    hp = _hp(lr=-1.0)  # checked before the arrays: a call that passes the array check would end as this does
+    A = FAKE
+    call = lambda q, dq, m: _step(2, _pp(*q), _pp(*dq), _pp(*m), _ii(8, 8), 4)
+    for q, dq, m in (((A, A), (A + 800, A + 900), (A + 1000, A + 1100)),  # one side twice
+                     ((A, A + 44), (A + 800, A + 900), (A + 1000, A + 1100)),
+                     ((A, A + 48), (A + 800, A + 900), (A + 95, A + 1100)),  # m into q
+                     ((A, A + 48), (A + 40, A + 900), (A + 1000, A + 1100)),  # dq in q
+                     ((A, A + 48), (A + 800, A + 1140), (A + 1000, A + 1100))):
+        assert call(q, dq, m) == B.POETX_E_SHAPE and "overlap" in B.poetx_last_error()
+    assert _step(hp=hp) == B.POETX_E_SHAPE and "lr" in B.poetx_last_error()
+    # side by side, and one gradient for both: past the array check (the workspace is what is wrong)
+    assert _step(2, _pp(A, A + 40 * MB), _pp(A + 10 * MB, A + 10 * MB), _pp(A + 20 * MB, A + 30 * MB), _ii(300, 300), 256,
+                 size=16) == B.POETX_E_WORKSPACE
 
 
 def test_orthogonalize_refusals():
