@@ -575,6 +575,9 @@ def main():
                          "report it amortised over the workload's merge period")
     ap.add_argument("--optimizer", action="store_true",
                     help="end every step with the Adam step on all packed q (poetx_adam_step_batch)")
+    ap.add_argument("--muon", action="store_true",
+                    help="also time the orthogonalised step of every side (poetx_muon_step_batch), outside the timed "
+                         "region")
     ap.add_argument("--graph", action="store_true",
                     help="capture one step into a HIP graph and time its replays (the W~ contraction rate then "
                          "comes from an eager pass of the same length)")
@@ -737,6 +740,15 @@ def main():
         "gb_per_s": o_bytes / (o_ms * 1e-3) / 1e9 if o_ms > 0 else None,
         "hbm_frac": o_bytes / (o_ms * 1e-3) / 8.0e12 if o_ms > 0 else None,
     }
+
+    if args.muon:
+        from orthogonal_reparameterized_cnp_amd.layer import PoetxMuon
+
+        muon = PoetxMuon(layers, lr=1e-5)
+        muon.step(dqs)
+        ms, _ = timed(lambda: muon.step(dqs), max(3, args.steps // 2))
+        result["muon_step"] = {"kernel": "momentum, 5 Newton-Schulz steps per block, decay (all sides)", "ms": ms}
+        del muon
 
     if args.breakdown:
         for name, kc in (("gemm", B.POETX_KC_GEMM), ("apply", B.POETX_KC_APPLY), ("dgrad", B.POETX_KC_DGRAD),
