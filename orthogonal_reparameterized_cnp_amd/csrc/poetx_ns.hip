@@ -68,8 +68,10 @@ template <int BM_, int BN_, int BK_, int WM_, int WN_, int S_, int NP_> struct N
 // 4 waves of 32 x 32, two workgroups a CU: products too small to fill the GPU with larger tiles, bound by latency (for
 // NP = 3 two stages of 64 columns, with half the barriers of four of 32: 40 blocks of 256 in 137 us instead of 142)
 template <int NP> using NTiny = NCfg<64, 64, 64, 2, 2, NP == 3 ? 2 : 4, NP>;
-template <int NP> using NSmall = NCfg<128, 128, NP == 3 ? 32 : 64, 2, 2, 2, NP>;  // 4 waves of 64 x 64, two workgroups a CU
-template <int NP> using NBig = NCfg<256, 256, NP == 3 ? 32 : 64, 4, 2, 2, NP>;    // 8 waves of 64 x 128
+// 4 waves of 64 x 64, two workgroups a CU
+template <int NP> using NSmall = NCfg<128, 128, NP == 3 ? 32 : 64, 2, 2, 2, NP>;
+// 8 waves of 64 x 128
+template <int NP> using NBig = NCfg<256, 256, NP == 3 ? 32 : 64, 4, 2, 2, NP>;
 
 PX_DEV f16x8_v as_f16(const bf16x8_v& x) {
   f16x8_v y;
@@ -209,8 +211,9 @@ template <bool NT> PX_DEV void put16(f16* p, const uint4& v) {
 // tile's planes; null: none) is written from there with `flip` (0x8000 negates), as floats for emit(r0, stage).
 // All planes are at the tile's origin; null lo planes are skipped.  `diag` (with `t` the tile itself): the tile lies on
 // the diagonal of a symmetric or, with `flip`, skew matrix, and its values below the diagonal are the mirrors of those
-// above.  A computed skew matrix would be off by its roundings there, and the products that read X^T as -X, from rows alone, would see
-// the sign of that symmetric part turned over: it grows by about 5 a step where a rounding otherwise grows by 3.4.
+// above.  A computed skew matrix would be off by its roundings there, and the products that read X^T as -X, from rows
+// alone, would see the sign of that symmetric part turned over: it grows by about 5 a step where a rounding otherwise
+// grows by 3.4.
 template <class C, class Emit>
 PX_DEV void ns_store(char* lds, const Acc<C>& acc, const Planes& aux, float alpha, float beta, const Planes& o,
                      const Planes& t, uint32_t flip, const Emit& emit, bool diag = false) {
@@ -383,8 +386,8 @@ struct MuonK {
 
 // ------------------------------------------------------------ skew blocks ---
 
-// Row and column of a packed slot (b <= 1024): row i starts at slot i b - i (i + 1) / 2; the root's rounding is put right
-// by at most a step.
+// Row and column of a packed slot (b <= 1024): row i starts at slot i b - i (i + 1) / 2; the root's rounding is put
+// right by at most a step.
 PX_DEV int slot_start(int i, int b) { return i * b - i * (i + 1) / 2; }
 PX_DEV int slot_i(int x, int b) {
   const float t = (float)(2 * b - 1);
@@ -407,7 +410,7 @@ struct BlockInfo {
 
 // Momentum of every live slot, and each workgroup's sum of the squared updates in 64 bits: workgroup c of block z
 // takes the packed slots from 2048 c on, 8 consecutive ones a thread (of any alignment).  A dead slot (j >= r of a
-// partial block) is neither read nor written.
+// partial block) is neither read nor written.  Bound by bytes: 160 blocks of 512, 251 MB in 41.9 us, 6.0 TB/s.
 constexpr int kMomentumSlots = 2048;
 __global__ __launch_bounds__(256) void k_muon_momentum(MuonTable tab, int b, MuonK k, double* __restrict__ part,
                                                        BlockInfo* __restrict__ info) {
@@ -462,6 +465,7 @@ PX_DEV double sum_parts(const double* part, int n) {
 
 // X planes of every block from its update, scaled by sx / (|M|_F + eps): one 64 x 64 tile on or above the
 // diagonal per workgroup and, off the diagonal, its negated mirror; zeros from r to the end of its last tile.
+// 160 blocks of 512: 168 MB read and as much written in 74 us, 4.5 TB/s.
 __global__ __launch_bounds__(256) void k_muon_unpack(MuonTable tab, int b, MuonK k, const double* __restrict__ part,
                                                      int parts, float sx, int n64, Planes X) {
   __shared__ float t[64][65];
@@ -509,7 +513,8 @@ struct SkewArgs {
 
 // One tile (ti, tj) of block z
 template <class C, bool AUX, bool LAST>
-PX_DEV void skew_tile(char* lds, const SkewArgs& g, const BlockInfo* info, int b, int z, int ti, int tj, const MuonK& k) {
+PX_DEV void skew_tile(char* lds, const SkewArgs& g, const BlockInfo* info, int b, int z, int ti, int tj,
+                      const MuonK& k) {
   const int r = info[z].r, m0 = ti * C::BM, n0 = tj * C::BN;
   if (n0 >= r) return;  // past the live corner: read by no product
   Acc<C> acc;
@@ -547,7 +552,9 @@ PX_DEV void skew_tile(char* lds, const SkewArgs& g, const BlockInfo* info, int b
 
 // One product of the batch on the tiles on and above the diagonal of its blocks: out = alpha aux + beta a b^T, its
 // mirror flipped by `flip`; with LAST the step of q instead of an output.  The first `wide` blocks run on 128 x 128
-// tiles, the rest, which would leave most of the last round of workgroups empty, on 64 x 64 ones.
+// tiles, the rest, which would leave most of the last round of workgroups empty, on 64 x 64 ones.  160 blocks of 512:
+// 114 us for A and 132 with the term of the planes, three rounds of workgroups, 710 and 610 TFLOP/s of the matrix
+// instructions, bound by them and the clock they leave; 40 blocks of 256: 9 to 10 us, bound by latency.
 template <bool AUX, bool LAST>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void k_ns_skew(
     SkewArgs g, const BlockInfo* __restrict__ info, int b, int n128, int wide, MuonK k) {
@@ -572,7 +579,8 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void k
 // Blocks of b <= 128: one workgroup keeps X and A (then B) of its block in LDS
 // for the whole step, from the momentum to the step of q, so that a call is one
 // launch.  W waves share the P x P tile; a block of r < P runs its k-steps to r
-// only, and waves whose part lies past r only keep the barriers.
+// only, and waves whose part lies past r only keep the barriers.  Bound by latency: 16 blocks of 32 take 21.7 us, of
+// which 15 dependent products about 0.75 us each.
 template <int P, int W>
 __global__ __launch_bounds__(W * 64) void k_muon_small(MuonTable tab, int b, MuonK k, int steps, float ca, float cb,
                                                        float cc, float sx) {
@@ -809,9 +817,10 @@ __global__ __launch_bounds__(256) void k_orth_norm(Dense<const T> G, double* __r
 }
 
 // X and X^T planes from the matrix, scaled by sx / (|G|_F + eps), zeros past its ends: one 64 x 64 tile a workgroup.
+// 4096 x 14336 bf16: 117 MB read and 352 MB written in 125 us, 3.8 TB/s, once a call of 4.9 ms.
 template <typename T>
-__global__ __launch_bounds__(256) void k_orth_load(Dense<const T> G, const double* __restrict__ part, int parts, float sx,
-                                                   float eps, int tk, Planes X, Planes Xt) {
+__global__ __launch_bounds__(256) void k_orth_load(Dense<const T> G, const double* __restrict__ part, int parts,
+                                                   float sx, float eps, int tk, Planes X, Planes Xt) {
   __shared__ float t[64][65];
   const int z = blockIdx.y, i0 = blockIdx.x / tk * 64, k0 = blockIdx.x % tk * 64;
   const double f = (double)sx / (__builtin_sqrt(sum_parts(part + (int64_t)z * parts, parts)) + (double)eps);
@@ -851,7 +860,8 @@ PX_DEV void x_tile(int id, int tm, int tn, int& bm, int& bn) {
 
 // out = alpha aux + beta a a^T, symmetric: the tiles on and above the diagonal of every matrix of the batch, `per` of
 // them a matrix.  The last `rest` of them run as S splits of the K loop each, which write their sums to `part` for
-// k_ns_join (they would leave most of a round of workgroups empty).
+// k_ns_join (they would leave most of a round of workgroups empty).  4096 x 14336 bf16: A in 282 us, 880 TFLOP/s, bound
+// by the matrix instructions (8192^3 of the library: 1130); 512 x 1376 fp32: 7 to 11 us, bound by latency.
 template <class C>
 __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2))) void k_ns_sym(
     int tiles, int KT, int full, int rest, int S, Planes a, Planes aux, Planes out, float alpha, float beta,
@@ -939,10 +949,11 @@ template <class C> PX_DEV void x_unit(int u, int tm, int tn, int first, int sub,
 }
 
 // X <- alpha X + beta B X on every tile; X is updated in place (a tile is read by its own workgroup only) and its
-// transpose written to the other of two buffers, for the other workgroups still read this one.
+// transpose written to the other of two buffers, for the other workgroups still read this one.  4096 x 14336 bf16: 768
+// tiles of 256 x 256 in 463 us, 890 TFLOP/s, and the other 128 as 512 of 128 x 128 in 97 us.
 template <class C>
-__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2))) void k_ns_x(int tm, int tn, int first, int sub, int KT, Planes B, Planes Xt, Planes X, Planes Xt_out,
-                                                float alpha, float beta) {
+__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2))) void k_ns_x(
+    int tm, int tn, int first, int sub, int KT, Planes B, Planes Xt, Planes X, Planes Xt_out, float alpha, float beta) {
   extern __shared__ __align__(16) unsigned char smem[];
   char* lds = reinterpret_cast<char*>(smem);
   int z, m0, n0;
@@ -955,8 +966,8 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2))) void
 
 // The last step: alpha X + beta B X to the caller's matrix.
 template <class C, typename T>
-__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2))) void k_ns_out(int tm, int tn, int first, int sub, int KT, Planes B, Planes Xt, Planes X, Dense<T> O,
-                                                  float alpha, float beta) {
+__global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2))) void k_ns_out(
+    int tm, int tn, int first, int sub, int KT, Planes B, Planes Xt, Planes X, Dense<T> O, float alpha, float beta) {
   extern __shared__ __align__(16) unsigned char smem[];
   int z, m0, n0;
   x_unit<C>(xcd_unit(blockIdx.x, gridDim.x), tm, tn, first, sub, z, m0, n0);
@@ -975,8 +986,11 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2))) void
   });
 }
 
-// workgroups (and 64-bit partial sums) of one matrix's norm: 4 runs of 8 elements a thread, and no more than fill the GPU
-inline int norm_parts(int64_t elems) { return (int)std::max<int64_t>(1, std::min<int64_t>(1024, elems / (256 * 8 * 4))); }
+// workgroups (and 64-bit partial sums) of one matrix's norm: 4 runs of 8 elements a thread, and no more than fill the
+// GPU
+inline int norm_parts(int64_t elems) {
+  return (int)std::max<int64_t>(1, std::min<int64_t>(1024, elems / (256 * 8 * 4)));
+}
 
 // allow_lds, once per kernel and GPU: a call makes about 20 launches
 template <auto K> hipError_t lds_once(int bytes) {
@@ -1045,12 +1059,16 @@ MuonWs muon_plan(Carve& c, int blocks, int b) {
   return w;
 }
 
-// How many of nz blocks of `per` 128 x 128 tiles run on those: whole rounds of workgroups (two a CU), and what is left
-// of them too where it fills more than 0.6 of a round; below 0.8 of one round 64 x 64 tiles are faster throughout.
+// How many of nz blocks of `per` 128 x 128 tiles run on those, the others on 64 x 64 ones: whole rounds of workgroups
+// (two a CU), and what is left over of them too where it fills more than 0.6 of a round.  A step in us, the rest on
+// 64 x 64 tiles / on 128 x 128: blocks of 512, 0.17 of a round left 756 / 828, 0.46 973 / 1003, 0.73 1758 / 1731, 0.95
+// 1330 / 1205; blocks of 256, 0.35 648 / 674, 0.76 825 / 807.  Less than one round runs on 64 x 64 tiles up to 0.75 of
+// it: blocks of 256, 0.59 312 / 393, 0.82 416 / 427, 0.94 509 / 445; blocks of 512, 0.23 208 / 352, 0.47 398 / 395,
+// 0.70 577 / 545.
 int muon_wide(int nz, int per) {
   constexpr int slots = 512;
   const int64_t tiles = (int64_t)nz * per, left = tiles % slots;
-  if (tiles < slots) return tiles >= 0.8 * slots ? nz : 0;
+  if (tiles < slots) return tiles >= 0.75 * slots ? nz : 0;
   return left > 0.6 * slots ? nz : (int)((tiles - left) / per);
 }
 
@@ -1088,7 +1106,8 @@ hipError_t muon_big(MuonTable& t, int b, const MuonK& k, const NsHyper& n, const
   return hipGetLastError();
 }
 
-template <int P, int W> hipError_t muon_small(const MuonTable& t, int b, const MuonK& k, const NsHyper& n, hipStream_t s) {
+template <int P, int W>
+hipError_t muon_small(const MuonTable& t, int b, const MuonK& k, const NsHyper& n, hipStream_t s) {
   constexpr int lds = 4 * P * (P + 8) * 2;
   const hipError_t e = lds_once<k_muon_small<P, W>>(lds);
   if (e != hipSuccess) return e;
@@ -1139,7 +1158,10 @@ SymPlan sym_plan(int count, int r, int k, int bk) {
   SymPlan p{};
   const auto units = [&](int t) { const int64_t n = cdiv(r, t); return count * n * (n + 1) / 2; };
   constexpr int slots = 512;  // two workgroups a CU
-  p.tile = units(128) >= 0.8 * slots ? 128 : 64;
+  // the whole call in us with tiles of 128 / 64, bf16 and fp32: 36 of 128 (1024 x 4096) 352 / 280, 515 / 460; 136
+  // (2048 x 5461) 806 / 843, 1603 / 1563; 210 (2560 x 4096) 933 / 1032, 1974 / 2002; 528 (4096 x 4096) 1729 / 2384,
+  // 3980 / 4991
+  p.tile = units(128) >= 200 ? 128 : 64;
   p.tiles = (int)cdiv(r, p.tile);
   const int64_t n = units(p.tile);
   const int KT = (int)cdiv(k, bk), left = (int)(n % slots);
@@ -1149,7 +1171,8 @@ SymPlan sym_plan(int count, int r, int k, int bk) {
     // the partial sums cost
     double best = KT;
     for (int S = 2; S <= 32 && S * 4 <= KT; ++S) {
-      const double cost = (double)cdiv((int64_t)left * S, slots) * cdiv(KT, S) + 16.0 + 4.0 * S * left / slots + 0.25 * S;
+      const double cost =
+          (double)cdiv((int64_t)left * S, slots) * cdiv(KT, S) + 16.0 + 4.0 * S * left / slots + 0.25 * S;
       if (cost < best) {
         best = cost;
         p.S = S;
@@ -1175,17 +1198,25 @@ OrthPlan orth_plan(Carve& c, int count, int rows, int cols, int dt) {
   OrthPlan p{};
   p.r = std::min(rows, cols);
   p.k = std::max(rows, cols);
-  // a short side of up to 128 leaves so few roundings to average over that fp16 products alone lose digits
+  // a short side of up to 128 leaves few roundings to average over: with fp16 products alone the result is up to 5e-3
+  // of its norm off there (2 x 7; 4e-3 for 1 x 1000; both from a model of the roundings in 64 bits).  The digits cost
+  // time: 121 us against 99 for 128 x 4096, 757 against 529 for 256 of 128 x 512
   p.np = dt == F32 || p.r <= 128 ? 3 : 1;
   const int bk = p.np == 3 ? 32 : 64;  // one line of a row
   p.a = sym_plan(count, p.r, p.k, bk);
   p.b = sym_plan(count, p.r, p.r, bk);
   const auto units = [&](int t) { return (int64_t)count * cdiv(p.r, t) * cdiv(p.k, t); };
-  p.xtile = units(256) >= 256 ? 256 : units(128) >= 400 ? 128 : 64;
+  // the whole call in us, bf16 and fp32, with tiles of 128 / 64: 64 of 128 (1024 x 1024) 223 / 166, 345 / 265; 144
+  // (1536 x 1536) 309 / 289, 504 / 497; 256 (1024 x 4096) 278 / 280, 446 / 463, (2048 x 2048) 482 / 482, 822 / 849;
+  // 640 (2560 x 4096) 1029 / 1139, 2007 / 2160.  Tiles of 256 / 128: 160 of 256 (2560 x 4096) 1027 / 1029, 2066 /
+  // 2007; 176 (2048 x 5461) 818 / 844, 1619 / 1561; 256 (4096 x 4096) 1734 / 1811, 3983 / 4194
+  p.xtile = units(256) >= 256 ? 256 : units(128) >= 256 ? 128 : 64;
   if (p.xtile == 256) {
-    // whole rounds of 256 workgroups, and what is left of them too where it fills more than 0.7 of a round
+    // whole rounds of 256 workgroups, and what is left of them too where it fills more than 0.6 of a round: 4096 rows,
+    // the whole call in us with the rest on 128 / 256, bf16 and fp32: 0.5 of a round left 2401 / 2543, 5591 / 5896;
+    // 0.62 2649 / 2643, 6150 / 6109; 0.75 2793 / 2706, 6453 / 6359
     p.xn = (int)units(256);
-    p.xwide = p.xn % 256 > 0.7 * 256 ? p.xn : p.xn / 256 * 256;
+    p.xwide = p.xn % 256 > 0.6 * 256 ? p.xn : p.xn / 256 * 256;
   }
   p.rp = (int)round_up(p.r, std::max(p.xtile, p.a.tile));
   p.kp = (int)round_up(p.k, p.xtile);
@@ -1205,16 +1236,16 @@ hipError_t sym_launch(const SymPlan& p, int K, const Planes& a, const Planes& au
                       float beta, float* sums, hipStream_t s) {
   const hipError_t e = lds_once<k_ns_sym<C>>(C::LDS);
   if (e != hipSuccess) return e;
-  k_ns_sym<C><<<p.full + p.rest * p.S, C::NT, C::LDS, s>>>(p.tiles, (int)cdiv(K, C::BK), p.full, p.rest, p.S, a, aux, out,
-                                                            alpha, beta, sums);
+  k_ns_sym<C><<<p.full + p.rest * p.S, C::NT, C::LDS, s>>>(p.tiles, (int)cdiv(K, C::BK), p.full, p.rest, p.S, a, aux,
+                                                           out, alpha, beta, sums);
   if (p.rest > 0)
     k_ns_join<<<p.rest * (C::BM / 16) * (C::BM / 64), 256, 0, s>>>(C::BM, p.tiles, p.full, p.rest, p.S, aux, out, alpha,
                                                                  beta, sums);
   return hipGetLastError();
 }
 template <int NP>
-hipError_t sym_run(const SymPlan& p, int K, const Planes& a, const Planes& aux, const Planes& out, float alpha, float beta,
-                   float* sums, hipStream_t s) {
+hipError_t sym_run(const SymPlan& p, int K, const Planes& a, const Planes& aux, const Planes& out, float alpha,
+                   float beta, float* sums, hipStream_t s) {
   if (p.tile == 128) return sym_launch<NSmall<NP>>(p, K, a, aux, out, alpha, beta, sums, s);
   return sym_launch<NTiny<NP>>(p, K, a, aux, out, alpha, beta, sums, s);
 }

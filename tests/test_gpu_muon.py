@@ -308,9 +308,10 @@ def test_orthogonalize_matches_oracle(count, rows, cols, dtype):
 
 
 @pytest.mark.parametrize("dtype", ["f32", "bf16"])
-@pytest.mark.parametrize("count,rows,cols", [(7, 700, 2300), (16, 1024, 1024), (8, 2300, 700), (4, 1950, 2100)])
+@pytest.mark.parametrize("count,rows,cols", [(7, 700, 2300), (16, 1024, 1024), (8, 2300, 700), (4, 1950, 2100),
+                                             (6, 1000, 1100), (3, 1300, 1250)])
 def test_orthogonalize_large_tiles(count, rows, cols, dtype):
-    """Enough 256 x 256 tiles for the wide kernels; the first and the last matrix against the oracle."""
+    """Enough tiles of 256 x 256 or 128 x 128 for the wide kernels; the first and the last matrix against the oracle."""
     print(f"orth {count}x{rows}x{cols} {dtype}", flush=True)
     G = _matrices(np.random.default_rng(9), count, rows, cols, dtype)
     out = PoetxOrthogonalizer(rows, cols, dtype, count)(G)
