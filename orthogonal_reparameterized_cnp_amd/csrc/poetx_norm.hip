@@ -27,54 +27,90 @@ namespace {
 
 template <typename T> constexpr int kVecOf = 16 / (int)sizeof(T);
 
-// Elements [c0, c0 + V) of a row of d; zeros past its end.
-template <typename T> PX_DEV void load_chunk(const T* __restrict__ row, int c0, int d, T (&v)[kVecOf<T>]) {
-  constexpr int V = kVecOf<T>;
-  if (c0 + V <= d) {
-    __builtin_memcpy(v, row + c0, 16);
-  } else {
-#pragma unroll
-    for (int e = 0; e < V; ++e) v[e] = c0 + e < d ? row[c0 + e] : T(0);
-  }
-}
-template <typename T> PX_DEV void store_chunk(T* __restrict__ row, int c0, int d, const T (&v)[kVecOf<T>]) {
-  constexpr int V = kVecOf<T>;
-  if (c0 + V <= d) {
-    __builtin_memcpy(row + c0, v, 16);
-  } else {
-#pragma unroll
-    for (int e = 0; e < V; ++e)
-      if (c0 + e < d) row[c0 + e] = v[e];
-  }
-}
+typedef uint32_t u32x4_v __attribute__((ext_vector_type(4)));
 
-// A thread's share of a row: NC chunks of V elements, chunk k at column (k TPR + lane) V.
-template <typename T, int TPR, int E> struct Row {
+// The columns of a thread: NC chunks of V, chunk k at min((k TPR + lane) V, d - V).  Only the row's last chunk is moved
+// back by the minimum (and those past the row, which hold nothing): its first `skip` columns are its neighbour's,
+// loaded and left out.  So loads have no branch of their own for the row's end, and a next row's stay in flight while
+// this one is summed.  (With one, every row waited where its paths joined for the loads just issued: backward of 16384
+// x 2048 bf16 66 us instead of 53, forward of 1021 x 5461 bf16 21 instead of 13.)
+template <typename T, int TPR, int E> struct Cols {
   static constexpr int V = kVecOf<T>, NC = E / V;
   static_assert(E % V == 0, "whole chunks");
-  T v[NC][V];
-  static PX_DEV int col(int k, int lane) { return (k * TPR + lane) * V; }
-  PX_DEV void load(const T* row, int lane, int d) {
+  int at[NC], skip[NC], d;
+  PX_DEV bool whole() const { return TPR > 64 || d >= V; }  // rows of a chunk at least
+  PX_DEV Cols(int lane, int d_) : d(d_) {
 #pragma unroll
-    for (int k = 0; k < NC; ++k) load_chunk<T>(row, col(k, lane), d, v[k]);
+    for (int k = 0; k < NC; ++k) {
+      const int c0 = (k * TPR + lane) * V;
+      at[k] = max(0, min(c0, d - V));
+      skip[k] = c0 - at[k];
+    }
   }
-  PX_DEV void store(T* row, int lane, int d) const {
+  PX_DEV bool own(int k, int e) const { return e >= skip[k] && (whole() || e < d); }
+};
+
+// A thread's share of a row, as loaded.
+template <typename T, int TPR, int E> struct Row {
+  using C = Cols<T, TPR, E>;
+  static constexpr int V = C::V, NC = C::NC;
+  u32x4_v v[NC];
+  PX_DEV void load(const T* row, const C& c) {
 #pragma unroll
-    for (int k = 0; k < NC; ++k) store_chunk<T>(row, col(k, lane), d, v[k]);
+    for (int k = 0; k < NC; ++k) {
+      if (c.whole()) {
+        __builtin_memcpy(&v[k], row + c.at[k], 16);
+      } else {
+        T t[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) t[e] = row[min(e, c.d - 1)];
+        __builtin_memcpy(&v[k], t, 16);
+      }
+    }
+  }
+  PX_DEV void store(T* row, const C& c) const {
+#pragma unroll
+    for (int k = 0; k < NC; ++k) {
+      if (c.skip[k] == 0 && c.whole()) {
+        __builtin_memcpy(row + c.at[k], &v[k], 16);
+      } else if (c.skip[k] < V) {
+        T t[V];
+        __builtin_memcpy(t, &v[k], 16);
+#pragma unroll
+        for (int e = 0; e < V; ++e)
+          if (c.own(k, e)) row[c.at[k] + e] = t[e];
+      }
+    }
+  }
+  PX_DEV void get(int k, float (&f)[V]) const {
+    // the compiler would take 16-bit elements apart where they are loaded, and wait for them there
+    u32x4_v w = v[k];
+    asm volatile("" : "+v"(w));
+    T t[V];
+    __builtin_memcpy(t, &w, 16);
+#pragma unroll
+    for (int e = 0; e < V; ++e) f[e] = to_f32<T>(t[e]);
+  }
+  PX_DEV void set(int k, const float (&f)[V]) {
+    T t[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) t[e] = from_f32<T>(f[e]);
+    __builtin_memcpy(&v[k], t, 16);
   }
 };
 
 // fp32 parameters of the thread's columns (`none` where the caller has none)
 template <typename T, int TPR, int E>
-PX_DEV void load_param(const float* p, float none, int lane, int d, float (&w)[E]) {
-  using R = Row<T, TPR, E>;
+PX_DEV void load_param(const float* p, float none, const Cols<T, TPR, E>& c, float (&w)[E]) {
+  using C = Cols<T, TPR, E>;
 #pragma unroll
-  for (int k = 0; k < R::NC; ++k)
+  for (int k = 0; k < C::NC; ++k) {
+    if (p && c.whole())
+      __builtin_memcpy(w + k * C::V, p + c.at[k], C::V * 4);
+    else
 #pragma unroll
-    for (int e = 0; e < R::V; ++e) {
-      const int c = R::col(k, lane) + e;
-      w[k * R::V + e] = p && c < d ? p[c] : none;
-    }
+      for (int e = 0; e < C::V; ++e) w[k * C::V + e] = p ? p[min(e, c.d - 1)] : none;
+  }
 }
 
 // The sums of N values over the TPR threads of a row, in a fixed order.  Rows
@@ -115,8 +151,8 @@ struct FwdArgs {
 };
 
 // NT threads hold NT / TPR rows at a time; workgroup g takes rows g RPW + sub, + gridDim RPW, ...  Bound by bytes in
-// long calls (8192 x 4096 bf16, RMS with a residual: 268 MB in 46.9 us, 5.7 TB/s), by the launch and the two dependent
-// sums of a row in short ones (2048 x 512 bf16, layer: 6.9 us; one row of 4096: 4.0 us).
+// long calls (8192 x 4096 bf16, RMS with a residual: 268 MB from memory in 51.7 us, 5.2 TB/s), by the launch and the
+// two dependent sums of a row in short ones (2048 x 512 bf16, layer: 4.1 us; one row of 4096: 2.5 us).
 template <typename T, bool RMS, bool RES, int TPR, int E>
 __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_fwd(const FwdArgs a) {
   constexpr int NT = TPR < 256 ? 256 : TPR, RPW = NT / TPR, W = TPR / 64;
@@ -131,32 +167,38 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_fwd(const FwdArg
   const float fd = (float)d;  // the means are quotients, so that a constant row's is exact
   const int step = gridDim.x * RPW;
   int t = blockIdx.x * RPW + sub;
+  const Cols<T, TPR, E> cols(lane, d);
   R x, r;
   // a workgroup's barriers are uniform: TPR > 64 has one row per workgroup
   if (t < a.T) {
-    x.load(X + (int64_t)t * a.ldx, lane, d);
-    if constexpr (RES) r.load(Rs + (int64_t)t * a.ldr, lane, d);
+    x.load(X + (int64_t)t * a.ldx, cols);
+    if constexpr (RES) r.load(Rs + (int64_t)t * a.ldr, cols);
   }
   float w[E], b[E];
-  load_param<T, TPR, E>(a.w, 1.f, lane, d, w);
-  if constexpr (!RMS) load_param<T, TPR, E>(a.b, 0.f, lane, d, b);
+  load_param<T, TPR, E>(a.w, 1.f, cols, w);
+  if constexpr (!RMS) load_param<T, TPR, E>(a.b, 0.f, cols, b);
   for (int par = 0; t < a.T; t += step, par ^= 1) {
     float f[E];
 #pragma unroll
-    for (int k = 0; k < R::NC; ++k)
+    for (int k = 0; k < R::NC; ++k) {
+      float v[R::V], q[R::V];
+      x.get(k, v);
+      if constexpr (RES) {
+        r.get(k, q);
 #pragma unroll
-      for (int e = 0; e < R::V; ++e) {
-        if constexpr (RES) x.v[k][e] = from_f32<T>(to_f32<T>(x.v[k][e]) + to_f32<T>(r.v[k][e]));
-        f[k * R::V + e] = to_f32<T>(x.v[k][e]);
+        for (int e = 0; e < R::V; ++e) v[e] += q[e];
+        x.set(k, v);
+        x.get(k, v);
       }
-    if constexpr (RES) {
-      x.store(S + (int64_t)t * a.lds, lane, d);
+#pragma unroll
+      for (int e = 0; e < R::V; ++e) f[k * R::V + e] = cols.own(k, e) ? v[e] : 0.f;
     }
+    if constexpr (RES) x.store(S + (int64_t)t * a.lds, cols);
     // the next row's loads fly while this row is summed
     const int nt = t + step;
     if (nt < a.T) {
-      x.load(X + (int64_t)nt * a.ldx, lane, d);
-      if constexpr (RES) r.load(Rs + (int64_t)nt * a.ldr, lane, d);
+      x.load(X + (int64_t)nt * a.ldx, cols);
+      if constexpr (RES) r.load(Rs + (int64_t)nt * a.ldr, cols);
     }
     float mean = 0.f;
     if constexpr (!RMS) {
@@ -168,8 +210,8 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_fwd(const FwdArg
 #pragma unroll
       for (int k = 0; k < R::NC; ++k)
 #pragma unroll
-        for (int e = 0; e < R::V; ++e)  // columns past the row's end stay out of the variance
-          f[k * R::V + e] = R::col(k, lane) + e < d ? f[k * R::V + e] - mean : 0.f;
+        for (int e = 0; e < R::V; ++e)  // columns that are not the thread's stay out of the variance
+          f[k * R::V + e] = cols.own(k, e) ? f[k * R::V + e] - mean : 0.f;
     }
     float s[1] = {0.f};
 #pragma unroll
@@ -178,15 +220,17 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void k_norm_fwd(const FwdArg
     const float rs = 1.f / __builtin_sqrtf(s[0] / fd + a.eps);
     R y;
 #pragma unroll
-    for (int k = 0; k < R::NC; ++k)
+    for (int k = 0; k < R::NC; ++k) {
+      float v[R::V];
 #pragma unroll
       for (int e = 0; e < R::V; ++e) {
         const int i = k * R::V + e;
-        float v = f[i] * rs * w[i];
-        if constexpr (!RMS) v += b[i];
-        y.v[k][e] = from_f32<T>(v);
+        v[e] = f[i] * rs * w[i];
+        if constexpr (!RMS) v[e] += b[i];
       }
-    y.store(Y + (int64_t)t * a.ldy, lane, d);
+      y.set(k, v);
+    }
+    y.store(Y + (int64_t)t * a.ldy, cols);
     if (lane == 0) {
       if constexpr (RMS) {
         a.stats[t] = rs;
@@ -208,16 +252,16 @@ struct BwdArgs {
 };
 
 // A workgroup of 1024 threads holds RPW rows at a time: 16 waves keep enough loads in flight for one workgroup a CU,
-// and its rows' column sums leave as one row of partial sums (four times the workgroups of a quarter the size, each
-// with its partial sums, ran 16384 x 2048 in 65.6 us and 3001 x 1376 in 23.9).  Bound by bytes: 16384 x 2048 bf16 with
-// dS, 268 MB in 53.4 us, 5.0 TB/s; 3001 x 1376 bf16, three rows a workgroup, 16.0 us.
-constexpr int kBwdThreads = 1024;
+// and its rows' column sums leave as one row of partial sums (workgroups of 256 / 512 / 1024, four, two or one a CU,
+// the whole call: 16384 x 2048 bf16 with dS 59.1 / 54.6 / 51.9 us, 3001 x 1376 bf16 23.8 / 18.1 / 14.1).  Bound by
+// bytes: 16384 x 2048, 268 MB at 5.2 TB/s; 3001 x 1376 bf16, three rows a workgroup one after the other, by their sums.
+constexpr int bwd_threads(int tpr, int e) { return e > 8 ? tpr : 1024 / tpr * tpr; }
 template <typename T, bool RMS, bool RES, int TPR, int E>
-__global__ __launch_bounds__(kBwdThreads) void k_norm_bwd(const BwdArgs a) {
-  constexpr int RPW = kBwdThreads / TPR, W = TPR / 64, VECS = RMS ? 1 : 2;
+__global__ __launch_bounds__(bwd_threads(TPR, E)) void k_norm_bwd(const BwdArgs a) {
+  constexpr int NT = bwd_threads(TPR, E), RPW = NT / TPR, W = TPR / 64, VECS = RMS ? 1 : 2;
   using R = Row<T, TPR, E>;
   __shared__ float red[2][RPW][2 * W];
-  __shared__ float acc[RPW > 1 ? VECS : 1][RPW > 1 ? TPR * E : 1];
+  __shared__ float acc[RPW > 1 ? RPW : 1][RPW > 1 ? E : 1][TPR + 8];
   const int lane = threadIdx.x % TPR, sub = threadIdx.x / TPR, d = a.d;
   const T* dY = reinterpret_cast<const T*>(a.dY);
   const T* S = reinterpret_cast<const T*>(a.S);
@@ -226,7 +270,8 @@ __global__ __launch_bounds__(kBwdThreads) void k_norm_bwd(const BwdArgs a) {
   const float* st_rs = RMS ? a.stats : a.stats + a.T;
   const float fd = (float)d;
   float w[E], dw[E], db[RMS ? 1 : E];
-  load_param<T, TPR, E>(a.w, 1.f, lane, d, w);
+  const Cols<T, TPR, E> cols(lane, d);
+  load_param<T, TPR, E>(a.w, 1.f, cols, w);
 #pragma unroll
   for (int i = 0; i < E; ++i) dw[i] = 0.f;
   if constexpr (!RMS)
@@ -236,9 +281,9 @@ __global__ __launch_bounds__(kBwdThreads) void k_norm_bwd(const BwdArgs a) {
   R y, x, r;
   float mean = 0.f, rs = 0.f;
   auto fetch = [&](int u) {
-    y.load(dY + (int64_t)u * a.ldy, lane, d);
-    x.load(S + (int64_t)u * a.lds, lane, d);
-    if constexpr (RES) r.load(dS + (int64_t)u * a.ldds, lane, d);
+    y.load(dY + (int64_t)u * a.ldy, cols);
+    x.load(S + (int64_t)u * a.lds, cols);
+    if constexpr (RES) r.load(dS + (int64_t)u * a.ldds, cols);
     if constexpr (!RMS) mean = a.stats[u];
     rs = st_rs[u];
   };
@@ -252,13 +297,18 @@ __global__ __launch_bounds__(kBwdThreads) void k_norm_bwd(const BwdArgs a) {
     float s[VECS] = {};
     if (live) {
 #pragma unroll
-      for (int k = 0; k < R::NC; ++k)
+      for (int k = 0; k < R::NC; ++k) {
+        float vy[R::V], vx[R::V], vr[R::V];
+        y.get(k, vy);
+        x.get(k, vx);
+        if constexpr (RES) r.get(k, vr);
 #pragma unroll
         for (int e = 0; e < R::V; ++e) {
           const int i = k * R::V + e;
-          const float dy = to_f32<T>(y.v[k][e]);
-          xh[i] = (to_f32<T>(x.v[k][e]) - mean) * rs;
-          if constexpr (RES) add[i] = to_f32<T>(r.v[k][e]);
+          const bool own = cols.own(k, e);
+          const float dy = own ? vy[e] : 0.f;
+          xh[i] = own ? (vx[e] - mean) * rs : 0.f;
+          if constexpr (RES) add[i] = vr[e];
           g[i] = dy * w[i];
           dw[i] += dy * xh[i];
           if constexpr (!RMS) {
@@ -267,6 +317,7 @@ __global__ __launch_bounds__(kBwdThreads) void k_norm_bwd(const BwdArgs a) {
           }
           s[0] += g[i] * xh[i];
         }
+      }
     }
     const int nt = t + step;
     if (nt < a.T) fetch(nt);
@@ -275,46 +326,49 @@ __global__ __launch_bounds__(kBwdThreads) void k_norm_bwd(const BwdArgs a) {
     const float m0 = s[0] / fd, m1 = RMS ? 0.f : s[VECS - 1] / fd;
     R o;
 #pragma unroll
-    for (int k = 0; k < R::NC; ++k)
+    for (int k = 0; k < R::NC; ++k) {
+      float v[R::V];
 #pragma unroll
       for (int e = 0; e < R::V; ++e) {
         const int i = k * R::V + e;
-        float v = rst * (g[i] - m1 - xh[i] * m0);
-        if constexpr (RES) v += add[i];
-        o.v[k][e] = from_f32<T>(v);
+        v[e] = rst * (g[i] - m1 - xh[i] * m0);
+        if constexpr (RES) v[e] += add[i];
       }
-    o.store(dX + (int64_t)t * a.ldx, lane, d);
-  }
-  // the workgroup's column sums: its rows' partial sums added in the order of `sub`
-  if constexpr (RPW > 1) {
-    for (int q = 0; q < RPW; ++q) {
-      if (sub == q)
-#pragma unroll
-        for (int i = 0; i < E; ++i) {
-          const int c = i * TPR + lane;  // a place of its own per thread and element
-          acc[0][c] = q == 0 ? dw[i] : acc[0][c] + dw[i];
-          if constexpr (!RMS) acc[VECS - 1][c] = q == 0 ? db[i] : acc[VECS - 1][c] + db[i];
-        }
-      __syncthreads();
+      o.set(k, v);
     }
-    if (sub != 0) return;
-#pragma unroll
-    for (int i = 0; i < E; ++i) {
-      dw[i] = acc[0][i * TPR + lane];
-      if constexpr (!RMS) db[i] = acc[VECS - 1][i * TPR + lane];
-    }
+    o.store(dX + (int64_t)t * a.ldx, cols);
   }
   float* P = a.part + (int64_t)blockIdx.x * VECS * d;
+  if constexpr (RPW > 1) {
+    // the workgroup's column sums: its row groups' added in their order, a column a thread (8 words between the rows of
+    // `acc` spread a thread's neighbours over the banks)
+    auto join = [&](const float* v, float* out) {
+      __syncthreads();
 #pragma unroll
-  for (int k = 0; k < R::NC; ++k)
+      for (int i = 0; i < E; ++i) acc[sub][i][lane] = v[i];
+      __syncthreads();
+      for (int c = threadIdx.x; c < d; c += NT) {
+        const int chunk = c / R::V, k = chunk / TPR, e = c - max(0, min(chunk * R::V, d - R::V));
+        float t = 0.f;
 #pragma unroll
-    for (int e = 0; e < R::V; ++e) {
-      const int c = R::col(k, lane) + e;
-      if (c < d) {
-        P[c] = dw[k * R::V + e];
-        if constexpr (!RMS) P[d + c] = db[k * R::V + e];
+        for (int q = 0; q < RPW; ++q) t += acc[q][k * R::V + e][chunk % TPR];
+        out[c] = t;
       }
-    }
+    };
+    join(dw, P);
+    if constexpr (!RMS) join(db, P + d);
+  } else {
+#pragma unroll
+    for (int k = 0; k < R::NC; ++k)
+#pragma unroll
+      for (int e = 0; e < R::V; ++e) {
+        const int c = cols.at[k] + e;
+        if (cols.own(k, e)) {
+          P[c] = dw[k * R::V + e];
+          if constexpr (!RMS) P[d + c] = db[k * R::V + e];
+        }
+      }
+  }
 }
 
 // dw and db: the sums of `parts` rows of n = vecs d columns, 16 columns by 16
@@ -346,31 +400,46 @@ __global__ __launch_bounds__(256) void k_norm_colsum(const float* __restrict__ p
   }
 }
 
-// The threads and elements per thread of a row of d: 8 elements while 1024 threads hold the row (with 16 a thread,
-// half the waves to keep loads in flight, 8192 x 4096 bf16 took 60.3 us forward instead of 54.2).
+// The threads and elements per thread of a row of d: 8 elements while 1024 threads hold the row (with 16 and half the
+// threads, forward, 8192 x 4096 bf16 with a residual takes 53.2 us instead of 52.0, 8192 x 5461 bf16 63.9 instead of
+// 54.2).  768 threads leave two workgroups a CU all the registers they ask for (4096 x 5461 fp32, layer: 44.5 us
+// forward instead of 51.8 on 1024, 60 backward instead of 66); the layer norm's forward takes more than 64 registers,
+// so that workgroups of 1024 would run one a CU: 16 elements up to 8192 (8192 x 8192 bf16 59 us instead of 80; RMS,
+// which fits, fp32 104 instead of 100).  Past 8192 the backward's rows, sums and weights do not fit the 128 registers
+// of a workgroup of 1024: 768 threads have 168, 512 have 256 (1000 x 10000 fp32, layer, 1024 / 768 / 512 threads: 111 /
+// 45 / 62 us; 2048 x 14336 bf16, RMS with dS, 1024 / 512: 99 / 68).
 template <int V> using Int = std::integral_constant<int, V>;
-template <bool BWD, typename F> hipError_t by_width(int d, F&& f) {
+template <bool BWD, bool RMS, typename F> hipError_t by_width(int d, F&& f) {
   if (d <= 64 * 8) return f(Int<64>(), Int<8>());
   if constexpr (BWD)  // rows of two waves share a workgroup (and its barriers) in the backward only
     if (d <= 128 * 8) return f(Int<128>(), Int<8>());
   if (d <= 256 * 8) return f(Int<256>(), Int<8>());
   if (d <= 512 * 8) return f(Int<512>(), Int<8>());
+  if (d <= 768 * 8) return f(Int<768>(), Int<8>());
+  if constexpr (!BWD && !RMS)
+    if (d <= 512 * 16) return f(Int<512>(), Int<16>());
   if (d <= 1024 * 8) return f(Int<1024>(), Int<8>());
-  if (d <= 1024 * 16) return f(Int<1024>(), Int<16>());
+  if constexpr (BWD) {
+    if (d <= 768 * 16) return f(Int<768>(), Int<16>());
+    if (d <= 512 * 32) return f(Int<512>(), Int<32>());
+  } else {
+    if (d <= 1024 * 16) return f(Int<1024>(), Int<16>());
+  }
   return f(Int<1024>(), Int<32>());
 }
 // rows that a workgroup of the backward holds at a time
 int bwd_rows(int d) {
   int n = 1;
-  by_width<true>(d, [&](auto tpr, auto) {
-    n = kBwdThreads / decltype(tpr)::value;
+  by_width<true, false>(d, [&](auto tpr, auto el) {
+    constexpr int TPR = decltype(tpr)::value;
+    n = bwd_threads(TPR, decltype(el)::value) / TPR;
     return hipSuccess;
   });
   return n;
 }
 
 template <typename T, bool RMS, bool RES> hipError_t fwd_t(const FwdArgs& a, hipStream_t s) {
-  return by_width<false>(a.d, [&](auto tpr, auto el) {
+  return by_width<false, RMS>(a.d, [&](auto tpr, auto el) {
     constexpr int TPR = decltype(tpr)::value, E = decltype(el)::value, NT = TPR < 256 ? 256 : TPR, RPW = NT / TPR;
     const int64_t groups = ((int64_t)a.T + RPW - 1) / RPW;
     const unsigned grid = (unsigned)std::min<int64_t>(groups, 256 * (2048 / NT));
@@ -380,9 +449,9 @@ template <typename T, bool RMS, bool RES> hipError_t fwd_t(const FwdArgs& a, hip
 }
 
 template <typename T, bool RMS, bool RES> hipError_t bwd_t(const BwdArgs& a, int parts, hipStream_t s) {
-  return by_width<true>(a.d, [&](auto tpr, auto el) {
+  return by_width<true, RMS>(a.d, [&](auto tpr, auto el) {
     constexpr int TPR = decltype(tpr)::value, E = decltype(el)::value;
-    k_norm_bwd<T, RMS, RES, TPR, E><<<(unsigned)parts, kBwdThreads, 0, s>>>(a);
+    k_norm_bwd<T, RMS, RES, TPR, E><<<(unsigned)parts, bwd_threads(TPR, E), 0, s>>>(a);
     return hipGetLastError();
   });
 }
