@@ -729,7 +729,8 @@ size_t poetx_norm_workspace_size(const poetx_norm_desc* desc, int64_t T);
  *          act_dtype, is written to S and is what is normalised
  *   w      [d] fp32, or NULL for ones;  bias  [d] fp32, or NULL for zeros
  *          (must be NULL for POETX_NORM_RMS)
- *   S      out [T] pitch lds with R, NULL without; may be X or R (same pitch)
+ *   S      out [T] pitch lds with R, NULL without; may be X or R (same pitch),
+ *          else overlaps neither
  *   Y      out [T] pitch ldy; overlaps no other operand
  *   stats  out, poetx_norm_stats_bytes(desc, T) bytes
  * T = 0 is a valid no-op.
@@ -749,7 +750,8 @@ poetx_status poetx_norm_fwd(const poetx_norm_desc* desc, int64_t T, const void* 
  *   S      the rows the forward normalised: its S, or its X without a residual
  *   stats  written by the forward of these rows
  *   dS     NULL, or [T] pitch ldds
- *   dX     out [T] pitch lddx; may be dY, or dS (same pitch)
+ *   dX     out [T] pitch lddx; may be dY, or dS (same pitch), else overlaps
+ *          neither, nor S
  *   dw, dbias  out fp32 [d], overwritten (zeros for T = 0); either may be
  *          NULL, dbias must be for POETX_NORM_RMS
  *   ws     >= poetx_norm_workspace_size(desc, T)

@@ -1578,6 +1578,29 @@ poetx_status check_norm(const poetx_norm_desc* d, int64_t T) {
 
 int norm_vecs(const poetx_norm_desc* d) { return d->kind == POETX_NORM_RMS ? 1 : 2; }
 
+// `count` matrices of `rows` rows of `width` bytes, all sizes in bytes.
+struct Span {
+  const void* p;
+  uint64_t pitch, stride = 0;
+};
+// Whether two of them share a cell.  Matrices of one pitch may lie in each other's gaps; of two pitches they must lie
+// apart.
+bool meet(const Span& a, const Span& b, uint64_t rows, uint64_t width, uint64_t count = 1) {
+  const uint64_t pa = reinterpret_cast<uintptr_t>(a.p), pb = reinterpret_cast<uintptr_t>(b.p);
+  const auto one = [&](const Span& s) { return (rows - 1) * s.pitch + width; };
+  const auto all = [&](const Span& s) { return (count - 1) * s.stride + one(s); };
+  if (pa >= pb + all(b) || pb >= pa + all(a)) return false;
+  if ((rows > 1 && a.pitch != b.pitch) || (count > 1 && a.stride != b.stride)) return true;
+  // one matrix `off` past another
+  const auto rows_meet = [&](uint64_t off) {
+    if (off >= one(a)) return false;
+    return rows == 1 || off % a.pitch < width || a.pitch - off % a.pitch < width;
+  };
+  const uint64_t off = pa > pb ? pa - pb : pb - pa;
+  if (count == 1) return rows_meet(off);
+  return rows_meet(off % a.stride) || (off / a.stride + 1 < count && rows_meet(a.stride - off % a.stride));
+}
+
 // a matrix operand of T rows: its row pitch, and its base on an element boundary
 poetx_status check_pitch(const char* name, const void* p, int64_t ld, const poetx_norm_desc* d) {
   if (ld < d->d) return fail(POETX_E_SHAPE, std::string(name) + ": the row pitch must be at least d");
@@ -1614,9 +1637,14 @@ poetx_status poetx_norm_fwd(const poetx_norm_desc* desc, int64_t T, const void* 
   if ((st = check_pitch("Y", Y, ldy, desc)) != POETX_OK) return st;
   if (R && (st = check_pitch("R", R, ldr, desc)) != POETX_OK) return st;
   if (S && (st = check_pitch("S", S, lds, desc)) != POETX_OK) return st;
-  if (Y == X || (R && (Y == R || Y == S))) return fail(POETX_E_SHAPE, "Y must not be X, R or S");
+  const size_t es = dt_size(desc->act_dtype);
+  const Span x{X, ldx * es}, r{R, ldr * es}, sum{S, lds * es}, y{Y, ldy * es};
+  const auto apart = [&](const Span& a, const Span& b) { return !b.p || !meet(a, b, T, desc->d * es); };
+  if (!apart(y, x) || !apart(y, r) || !apart(y, sum)) return fail(POETX_E_SHAPE, "Y must not overlap X, R or S");
   if (S && ((S == X && lds != ldx) || (S == R && lds != ldr)))
     return fail(POETX_E_SHAPE, "S in place of X or R must have its pitch");
+  if (S && ((S != X && !apart(sum, x)) || (S != R && !apart(sum, r))))
+    return fail(POETX_E_SHAPE, "S must be X or R or overlap neither");
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   PX_HIP(norm_fwd(desc->act_dtype, rms, T, desc->d, desc->eps, X, ldx, R, ldr, w, bias, S, lds, Y, ldy, stats, s));
   return POETX_OK;
@@ -1637,7 +1665,12 @@ poetx_status poetx_norm_bwd(const poetx_norm_desc* desc, int64_t T, const void* 
     if (dS && (st = check_pitch("dS", dS, ldds, desc)) != POETX_OK) return st;
     if ((dX == dY && lddx != lddy) || (dX == dS && lddx != ldds))
       return fail(POETX_E_SHAPE, "dX in place of dY or dS must have its pitch");
-    if (dX == S) return fail(POETX_E_SHAPE, "dX must not be S");
+    const size_t es = dt_size(desc->act_dtype);
+    const Span dx{dX, lddx * es};
+    const auto apart = [&](const void* p, int64_t ld) { return !p || !meet(dx, Span{p, ld * es}, T, desc->d * es); };
+    if (!apart(S, lds)) return fail(POETX_E_SHAPE, "dX must not overlap S");
+    if ((dX != dY && !apart(dY, lddy)) || (dX != dS && !apart(dS, ldds)))
+      return fail(POETX_E_SHAPE, "dX must be dY or dS or overlap neither");
     if ((st = check_ws(ws, ws_bytes, poetx_norm_workspace_size(desc, T))) != POETX_OK) return st;
   }
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
@@ -1776,6 +1809,8 @@ poetx_status poetx_orthogonalize(int32_t count, int32_t rows, int32_t cols, int3
   const size_t es = dt_size(dtype);
   if (reinterpret_cast<uintptr_t>(G) % es || reinterpret_cast<uintptr_t>(O) % es)
     return fail(POETX_E_SHAPE, "G and O must be aligned to their element");
+  if (O != G && meet(Span{G, ld_g * es, stride_g * es}, Span{O, ld_o * es, stride_o * es}, rows, cols * es, count))
+    return fail(POETX_E_SHAPE, "O must be G or not overlap it");
   if ((st = check_ns(*hp)) != POETX_OK) return st;
   if ((st = check_ws(ws, ws_bytes, orth_ws_bytes(count, rows, cols, dtype))) != POETX_OK) return st;
   const double r = std::min(rows, cols), k = std::max(rows, cols);

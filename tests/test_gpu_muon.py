@@ -480,3 +480,15 @@ def test_training_step_end_to_end():
         check_step(s, hp)
     w1, _, _ = O.adam_step(w0.astype(np.float64), f64(dw), 0.0, 0.0, 1, O.AdamHP(*(f32(x) for x in (1e-3, 0.9, 0.99, 1e-3, 0.0))))
     np.testing.assert_allclose(f64(norm.weight), w1, rtol=2e-6)
+
+
+def test_orthogonalize_between_its_operands():
+    """G and O as the halves of one array, matrix by matrix: the results of separate arrays, bit for bit."""
+    count, rows, cols = 3, 100, 130
+    G = _matrices(np.random.default_rng(5), count, rows, cols, "f32")
+    op = PoetxOrthogonalizer(rows, cols, "f32", count)
+    want = op(G)
+    both = torch.stack([G, torch.zeros_like(G)], 1)
+    assert torch.equal(op(both[:, 0], out=both[:, 1]), want) and torch.equal(both[:, 0], G)
+    wide = torch.cat([G, torch.zeros_like(G)], 2)
+    assert torch.equal(op(wide[:, :, :cols], out=wide[:, :, cols:]), want) and torch.equal(wide[:, :, :cols], G)

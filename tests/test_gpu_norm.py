@@ -156,6 +156,24 @@ def test_in_place(act, T, d):
         assert torch.equal(got, dX) and torch.equal(dw2, dw) and torch.equal(db2, db)
 
 
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+def test_operands_in_each_others_gaps(act):
+    """Y beside X, and dX beside dY, as columns of one array: the results of separate arrays, bit for bit."""
+    T, d = 70, 513
+    norm = PoetxNorm(d, "layer", act)
+    X, dY = _rows(T, d, act, 1), _rows(T, d, act, 2)
+    Y = norm.forward(X)
+    dX, dw, db = norm.backward(dY)
+    both = torch.cat([X, torch.zeros_like(X)], 1)
+    assert torch.equal(norm.forward(both[:, :d], Y=both[:, d:]), Y) and torch.equal(both[:, :d], X)
+    both = torch.cat([torch.zeros_like(dY), dY], 1)
+    norm.forward(X)
+    got = norm.backward(both[:, d:], dX=both[:, :d])
+    assert all(torch.equal(a, b) for a, b in zip(got, (dX, dw, db))) and torch.equal(both[:, d:], dY)
+    with pytest.raises(B.PoetxError):
+        norm.forward(both[:, :d], Y=both[:, 1:d + 1])
+
+
 def test_rows_that_degenerate():
     """A constant row and a zero row have variance 0; a NaN or an infinity stays in its own row and in the column sums."""
     d = 300

@@ -99,6 +99,13 @@ def test_orthogonalize_refusals():
                dict(count=2, sg=19999), dict(count=2, so=0), dict(O=FAKE, ldo=201), dict(count=2, O=FAKE, so=20001),
                dict(G=FAKE + 2), dict(count=1024, rows=1 << 17, cols=1 << 17, ldg=1 << 17, ldo=1 << 17)):
         assert _orth(**kw) == B.POETX_E_SHAPE, kw
+    # arrays that share a cell: rows 100 x 200 fp32, in one piece, with gaps, and in a batch
+    for O in (FAKE + 4, FAKE - 4, FAKE + 80000 - 4, FAKE - 80000 + 4):
+        assert _orth(O=O) == B.POETX_E_SHAPE, O
+    for off in (4, 796, 1200 * 4 - 796, 99 * 1200 * 4 + 796):
+        assert _orth(O=FAKE + off, ldg=1200, ldo=1200) == B.POETX_E_SHAPE, off
+    for off in (80000 - 4, 160000, 240000 - 4, 160000 + 80000 - 4, 320000 + 80000 - 4):
+        assert _orth(count=3, O=FAKE + off, sg=40000, so=40000) == B.POETX_E_SHAPE, off
     assert _orth(dt=B.POETX_I8) == B.POETX_E_DTYPE
     for ns in BAD_NS:
         assert _orth(hp=B.ns_params(**ns)) == B.POETX_E_SHAPE, ns

@@ -54,6 +54,24 @@ def test_forward_refusals():
     assert _fwd(_d(kind="rms"), b=FAKE) == B.POETX_E_SHAPE
 
 
+def test_overlap_refusals():
+    """Operands that share a cell are refused unless they are one array; rows in each other's gaps share none."""
+    apart, row = 16 * FAKE, 64 * 2
+    for Y in (FAKE + 2, FAKE - 2, FAKE + 3 * row, FAKE + row * 4 - 2, FAKE - row * 4 + 2):
+        assert _fwd(_d(), Y=Y) == B.POETX_E_SHAPE, Y
+        assert _fwd(_d(), X=apart, R=FAKE, S=2 * apart, Y=Y) == B.POETX_E_SHAPE, Y
+        assert _fwd(_d(), X=apart, R=3 * apart, S=FAKE, Y=Y) == B.POETX_E_SHAPE, Y
+        assert _fwd(_d(), X=FAKE, R=apart, S=Y, Y=2 * apart) == B.POETX_E_SHAPE, Y
+        assert _fwd(_d(), X=apart, R=FAKE, S=Y, Y=2 * apart) == B.POETX_E_SHAPE, Y
+        assert _bwd(_d(), dX=Y) == B.POETX_E_SHAPE, Y
+        assert _bwd(_d(), dY=apart, S=FAKE, dX=Y) == B.POETX_E_SHAPE, Y
+        assert _bwd(_d(), dY=apart, dS=FAKE, dX=Y) == B.POETX_E_SHAPE, Y
+    wide = dict(ldx=200, ldy=200)
+    for off in (0, 2, row - 2, 2 * 200 - row + 2, 2 * 200, 3 * 2 * 200 + row - 2):
+        assert _fwd(_d(), Y=FAKE + off, **wide) == B.POETX_E_SHAPE, off
+    assert _fwd(_d(), Y=FAKE + row, ldx=200, ldy=201) == B.POETX_E_SHAPE
+
+
 def test_backward_refusals():
     for kw in (dict(dY=None), dict(S=None), dict(stats=None), dict(dX=None), dict(ws=None)):
         assert _bwd(_d(), **kw) == B.POETX_E_NULL, kw
