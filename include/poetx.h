@@ -685,9 +685,8 @@ size_t poetx_orthogonalize_workspace_size(int32_t count, int32_t rows, int32_t c
  *          stride), else they must not overlap.  The strides matter for
  *          count > 1 only, where they must be at least (rows - 1) ld + cols.
  *   ws     >= poetx_orthogonalize_workspace_size(count, rows, cols, dtype)
- * POETX_F32: products as exact as fp32 products.  POETX_BF16: fp16 operands
- * (11 bits) with fp32 sums, about 2e-3 of the result's norm, and the result
- * rounded to bf16 once.
+ * The products are as exact as fp32 products for both types, and the result is
+ * rounded to dtype once.
  * Errors: POETX_E_NULL, POETX_E_SHAPE, POETX_E_DTYPE, POETX_E_WORKSPACE, POETX_E_HIP.
  */
 poetx_status poetx_orthogonalize(int32_t count, int32_t rows, int32_t cols, int32_t dtype, const void* G, int64_t ld_g,

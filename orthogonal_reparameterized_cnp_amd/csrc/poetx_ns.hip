@@ -9,14 +9,13 @@
 //
 // Operands.  X, A and B live in the workspace as fp16 "planes" at a fixed power
 // of two: hi = fp16(x), lo = fp16(x - hi), 22 bits together.  The products run
-// on the fp16 matrix instructions with fp32 accumulation.  With NP = 3 a
-// product is hi hi + hi lo + lo hi: as exact as fp32 products (the low-by-low
-// part is 2^-22 of the whole) at three times the cost of one, about 5x the rate
-// of the fp32 matrix instructions; packed parameters and fp32 matrices take it.
-// With NP = 1 (bf16 matrices) it is hi hi, and only the term a X is carried in
-// both planes: measured against the definition in 64 bits the result is off by
-// 1.2 to 2.4e-3 of its norm before the rounding to bf16, which is off by 1.7e-3
-// itself (bf16 products would be off by 1 to 2e-2).
+// on the fp16 matrix instructions with fp32 accumulation, hi hi + hi lo + lo hi:
+// as exact as fp32 products (the low-by-low part is 2^-22 of the whole) at three
+// times the cost of one, about 5x the rate of the fp32 matrix instructions.
+// bf16 matrices take the same products and are rounded once, at the end.  (hi hi
+// alone is 2.5 times as fast, but its roundings of 2^-12 pass through all steps:
+// a matrix of low rank and noise comes out 1.2 to 2.4e-3 of its norm off, a
+// diagonal of four entries, where nothing averages them, 1.3e-2.)
 //
 // Scales: X is held times SX, a power of two near 8 sqrt(K) for rows of length
 // K (an orthogonal result has entries near K^-1/2), A and B times SA = 2^8.
@@ -48,12 +47,12 @@ typedef _Float16 f16x4_v __attribute__((ext_vector_type(4)));
 constexpr float kSA = 256.f;  // scale of A and B
 constexpr int kInter = 32;    // run of hi values between runs of lo values
 
-// Tile configuration of the product kernels: PL planes per operand, a ring of S stages of BK columns.
-template <int BM_, int BN_, int BK_, int WM_, int WN_, int S_, int NP_> struct NCfg {
-  static constexpr int BM = BM_, BN = BN_, BK = BK_, WM = WM_, WN = WN_, STAGES = S_, NP = NP_, PL = NP_ == 3 ? 2 : 1;
+// Tile configuration of the product kernels: two planes per operand, a ring of S stages of BK columns.
+template <int BM_, int BN_, int BK_, int WM_, int WN_, int S_> struct NCfg {
+  static constexpr int BM = BM_, BN = BN_, BK = BK_, WM = WM_, WN = WN_, STAGES = S_;
   static constexpr int NW = WM * WN, NT = NW * 64;
   static constexpr int WTM = BM / WM, WTN = BN / WN, TM = WTM / 32, TN = WTN / 32;
-  static constexpr int A_BYTES = PL * BM * BK * 2, B_BYTES = PL * BN * BK * 2;  // one stage
+  static constexpr int A_BYTES = 2 * BM * BK * 2, B_BYTES = 2 * BN * BK * 2;  // one stage
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int LA = A_BYTES / 1024 / NW, LB = B_BYTES / 1024 / NW;  // copies per wave and stage
   // the epilogue stages RS rows of (hi, lo) words; a pitch of 5 mod 64 words spreads both the reads
@@ -65,13 +64,13 @@ template <int BM_, int BN_, int BK_, int WM_, int WN_, int S_, int NP_> struct N
   static_assert(64 % BK == 0, "K steps stay within written tiles");
   static_assert(BM % RS == 0 && RS % WTM == 0 && PITCH % 64 == 5, "epilogue stage");
 };
-// 4 waves of 32 x 32, two workgroups a CU: products too small to fill the GPU with larger tiles, bound by latency (for
-// NP = 3 two stages of 64 columns, with half the barriers of four of 32: 40 blocks of 256 in 137 us instead of 142)
-template <int NP> using NTiny = NCfg<64, 64, 64, 2, 2, NP == 3 ? 2 : 4, NP>;
+// 4 waves of 32 x 32, two workgroups a CU: products too small to fill the GPU with larger tiles, bound by latency (two
+// stages of 64 columns, with half the barriers of four of 32: 40 blocks of 256 in 137 us instead of 142)
+using NTiny = NCfg<64, 64, 64, 2, 2, 2>;
 // 4 waves of 64 x 64, two workgroups a CU
-template <int NP> using NSmall = NCfg<128, 128, NP == 3 ? 32 : 64, 2, 2, 2, NP>;
+using NSmall = NCfg<128, 128, 32, 2, 2, 2>;
 // 8 waves of 64 x 128
-template <int NP> using NBig = NCfg<256, 256, NP == 3 ? 32 : 64, 4, 2, 2, NP>;
+using NBig = NCfg<256, 256, 32, 4, 2, 2>;
 
 PX_DEV f16x8_v as_f16(const bf16x8_v& x) {
   f16x8_v y;
@@ -87,29 +86,26 @@ PX_DEV uint32_t pack_hilo(float v) {
   return (uint32_t)hb | ((uint32_t)lb << 16);
 }
 
-// One operand: K-contiguous rows of hi (and lo) values, ld fp16 elements apart.  Where the products read both planes
-// (NP = 3) they alternate along the rows, kInter hi values and then their lo values (l = h + kInter), so that a K step
-// of 32 is one 128-byte line of every row.
+// One operand: K-contiguous rows, ld fp16 elements apart, in which kInter hi values and then their lo values alternate,
+// so that a K step of 32 is one 128-byte line of every row.
 struct Planes {
-  f16 *h = nullptr, *l = nullptr;
+  f16* h = nullptr;
   int64_t ld = 0, stride = 0;  // stride: fp16 elements from one matrix of the batch to the next
-  int inter = 0;  // kInter, or 0 for planes of their own
   // the planes from (row, col) of matrix z on; col a multiple of 32
   PX_DEV Planes tile(int z, int64_t row, int64_t col) const {
     if (!h) return *this;
-    const int64_t o = z * stride + row * ld + (inter ? 2 * col : col);
-    return Planes{h + o, l ? l + o : nullptr, ld, stride, inter};
+    return Planes{h + z * stride + row * ld + 2 * col, ld, stride};
   }
 };
-// column of a row's element from its planes' origin
-PX_DEV constexpr int plane_col(int inter, int j) { return inter ? j / inter * 2 * inter + j % inter : j; }
+// place of a row's hi value from its planes' origin; its lo value is kInter further
+PX_DEV constexpr int plane_col(int j) { return j / kInter * 2 * kInter + j % kInter; }
 
 // acc = sum over KT tiles of K of a's tile rows times b's tile rows.  `same`: the two tiles are one.  `upper`: only
 // what lies on and above the tile's diagonal is wanted, so that waves whose part lies below it multiply nothing (and
 // results do not depend on the tile a block ran on: what is below a diagonal is always a mirror).
 template <class C>
 PX_DEV void ns_loop(char* lds, const Planes& a, const Planes& b, int KT, bool same, Acc<C>& acc, bool upper = false) {
-  constexpr int PK = C::BK * C::PL;  // fp16 elements of a row in a stage
+  constexpr int PK = C::BK * 2;  // fp16 elements of a row in a stage
   const AccPos<C> p = acc_pos<C>();
   const int wave = threadIdx.x >> 6, lane = p.lane;
   auto issue = [&](int kt, char* st) {
@@ -122,7 +118,7 @@ PX_DEV void ns_loop(char* lds, const Planes& a, const Planes& b, int KT, bool sa
   for (int t = 0; t < C::STAGES - 1; ++t)
     if (t < KT) issue(t, lds + t * C::STAGE);
   struct Frags {
-    f16x8_v ah[C::TM], bh[C::TN], al[C::PL == 2 ? C::TM : 1], bl[C::PL == 2 ? C::TN : 1];
+    f16x8_v ah[C::TM], bh[C::TN], al[C::TM], bl[C::TN];
   };
   for (int kt = 0; kt < KT; ++kt) {
     // the copies of up to STAGES - 2 later stages may stay in flight; stage kt must have landed
@@ -140,19 +136,19 @@ PX_DEV void ns_loop(char* lds, const Planes& a, const Planes& b, int KT, bool sa
     const char* As = lds + kt % C::STAGES * C::STAGE;
     const char* Bs = same ? As : As + C::A_BYTES;
     // place of k-step ks's hi values in a staged row
-    auto hi = [](int ks) { return C::PL == 2 ? plane_col(kInter, ks * 16) : ks * 16; };
+    auto hi = [](int ks) { return plane_col(ks * 16); };
     auto load = [&](int ks, Frags& f) __attribute__((always_inline)) {
 #pragma unroll
       for (int i = 0; i < C::TM; ++i) {
         const int t0 = p.wm * C::WTM + i * 32;
         f.ah[i] = as_f16(frag_kmaj<PK>(As, t0, hi(ks), lane));
-        if constexpr (C::PL == 2) f.al[i] = as_f16(frag_kmaj<PK>(As, t0, hi(ks) + kInter, lane));
+        f.al[i] = as_f16(frag_kmaj<PK>(As, t0, hi(ks) + kInter, lane));
       }
 #pragma unroll
       for (int j = 0; j < C::TN; ++j) {
         const int t0 = p.wn * C::WTN + j * 32;
         f.bh[j] = as_f16(frag_kmaj<PK>(Bs, t0, hi(ks), lane));
-        if constexpr (C::PL == 2) f.bl[j] = as_f16(frag_kmaj<PK>(Bs, t0, hi(ks) + kInter, lane));
+        f.bl[j] = as_f16(frag_kmaj<PK>(Bs, t0, hi(ks) + kInter, lane));
       }
     };
     constexpr int KS = C::BK / 16;
@@ -166,10 +162,8 @@ PX_DEV void ns_loop(char* lds, const Planes& a, const Planes& b, int KT, bool sa
       for (int i = 0; i < C::TM; ++i)
 #pragma unroll
         for (int j = 0; j < C::TN; ++j) {
-          if constexpr (C::PL == 2) {
-            acc.v[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(c.al[i], c.bh[j], acc.v[i][j], 0, 0, 0);
-            acc.v[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(c.ah[i], c.bl[j], acc.v[i][j], 0, 0, 0);
-          }
+          acc.v[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(c.al[i], c.bh[j], acc.v[i][j], 0, 0, 0);
+          acc.v[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(c.ah[i], c.bl[j], acc.v[i][j], 0, 0, 0);
           acc.v[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(c.ah[i], c.bh[j], acc.v[i][j], 0, 0, 0);
         }
       // ask the compiler to interleave the reads with the matrix instructions
@@ -209,7 +203,7 @@ template <bool NT> PX_DEV void put16(f16* p, const uint4& v) {
 // fp32, then each thread takes 8 consecutive values of a row, adds the aux planes' (16-byte loads; null: none),
 // writes them to the planes `o` (null: none) and leaves them in LDS, as (hi, lo) words where `t` (the transposed
 // tile's planes; null: none) is written from there with `flip` (0x8000 negates), as floats for emit(r0, stage).
-// All planes are at the tile's origin; null lo planes are skipped.  `diag` (with `t` the tile itself): the tile lies on
+// All planes are at the tile's origin.  `diag` (with `t` the tile itself): the tile lies on
 // the diagonal of a symmetric or, with `flip`, skew matrix, and its values below the diagonal are the mirrors of those
 // above.  A computed skew matrix would be off by its roundings there, and the products that read X^T as -X, from rows
 // alone, would see the sign of that symmetric part turned over: it grows by about 5 a step where a rounding otherwise
@@ -218,7 +212,6 @@ template <class C, class Emit>
 PX_DEV void ns_store(char* lds, const Acc<C>& acc, const Planes& aux, float alpha, float beta, const Planes& o,
                      const Planes& t, uint32_t flip, const Emit& emit, bool diag = false) {
   constexpr bool EMIT = !std::is_same<Emit, std::nullptr_t>::value;
-  constexpr int INTER = C::PL == 2 ? kInter : 0;
   constexpr int NIT = C::RS * C::BN / 8 / C::NT;  // a thread's share of the pieces of 8
   uint32_t* st = reinterpret_cast<uint32_t*>(lds);
   const AccPos<C> p = acc_pos<C>();
@@ -232,10 +225,9 @@ PX_DEV void ns_store(char* lds, const Acc<C>& acc, const Planes& aux, float alph
 #pragma unroll
     for (int x = 0; x < n; ++x) {
       const int c = threadIdx.x + (it0 + x) * C::NT, i = c / (C::BN / 8), j = c % (C::BN / 8) * 8;
-      const int64_t at = (r0 + i) * aux.ld + plane_col(INTER, j);
+      const int64_t at = (r0 + i) * aux.ld + plane_col(j);
       xh[x] = *reinterpret_cast<const f16x8_v*>(aux.h + at);
-      xl[x] = f16x8_v{};
-      if (aux.l) xl[x] = *reinterpret_cast<const f16x8_v*>(aux.l + at);
+      xl[x] = *reinterpret_cast<const f16x8_v*>(aux.h + at + kInter);
     }
   };
   if constexpr (C::BM == C::RS) load_aux(0, 0, NIT);
@@ -275,9 +267,9 @@ PX_DEV void ns_store(char* lds, const Acc<C>& acc, const Planes& aux, float alph
         if (!diag || j >= r0 + C::RS) {
           uint4 h, l;
           split_words(x, 0, h, l);
-          const int64_t at = (r0 + i) * o.ld + plane_col(INTER, j);
+          const int64_t at = (r0 + i) * o.ld + plane_col(j);
           put16<C::BM == 64>(o.h + at, h);
-          if (o.l) put16<C::BM == 64>(o.l + at, l);
+          put16<C::BM == 64>(o.h + at + kInter, l);
         }
         if (t.h || diag)
 #pragma unroll
@@ -302,9 +294,9 @@ PX_DEV void ns_store(char* lds, const Acc<C>& acc, const Planes& aux, float alph
           }
           uint4 h, l;
           split_words(x, 0, h, l);
-          const int64_t at = (r0 + i) * o.ld + plane_col(INTER, r0 + j);
+          const int64_t at = (r0 + i) * o.ld + plane_col(r0 + j);
           put16<C::BM == 64>(o.h + at, h);
-          if (o.l) put16<C::BM == 64>(o.l + at, l);
+          put16<C::BM == 64>(o.h + at + kInter, l);
         }
       }
 #pragma unroll 2
@@ -316,9 +308,9 @@ PX_DEV void ns_store(char* lds, const Acc<C>& acc, const Planes& aux, float alph
         for (int e = 0; e < 8; ++e) x[e] = st[(i + e) * C::PITCH + j];
         uint4 h, l;
         split_words(x, flip | (flip << 16), h, l);
-        const int64_t at = j * t.ld + plane_col(INTER, r0 + i);
+        const int64_t at = j * t.ld + plane_col(r0 + i);
         put16<C::BM == 64>(t.h + at, h);
-        if (t.l) put16<C::BM == 64>(t.l + at, l);
+        put16<C::BM == 64>(t.h + at + kInter, l);
       }
     }
   }
@@ -335,9 +327,9 @@ template <class F> PX_DEV void put64(const Planes& p, int z, int64_t row0, int64
     for (int e = 0; e < 8; ++e) x[e] = pack_hilo(value(row, col + e));
     uint4 h, l;
     split_words(x, 0, h, l);
-    const int64_t at = row * o.ld + plane_col(o.inter, col);
+    const int64_t at = row * o.ld + plane_col(col);
     *reinterpret_cast<uint4*>(o.h + at) = h;
-    if (o.l) *reinterpret_cast<uint4*>(o.l + at) = l;
+    *reinterpret_cast<uint4*>(o.h + at + kInter) = l;
   }
 }
 
@@ -558,9 +550,9 @@ PX_DEV void skew_tile(char* lds, const SkewArgs& g, const BlockInfo* info, int b
 template <bool AUX, bool LAST>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void k_ns_skew(
     SkewArgs g, const BlockInfo* __restrict__ info, int b, int n128, int wide, MuonK k) {
-  using C1 = NSmall<3>;
-  using C2 = NTiny<3>;
-  static_assert(C1::NT == 256 && C2::NT == 256 && C1::PL == C2::PL, "one launch, one layout");
+  using C1 = NSmall;
+  using C2 = NTiny;
+  static_assert(C1::NT == 256 && C2::NT == 256, "one launch");
   extern __shared__ __align__(16) unsigned char smem[];
   char* lds = reinterpret_cast<char*>(smem);
   const int per1 = n128 * (n128 + 1) / 2, per2 = n128 * (2 * n128 + 1), units1 = wide * per1;
@@ -811,9 +803,11 @@ template <typename T> struct Run8 {
 };
 
 // each workgroup's sum of squares in 64 bits: the runs of 8 elements of the stored rows, dealt to the grid's threads,
-// four of them under way at a time (4096 x 14336 bf16: 117 MB in 26.6 us, 4.4 TB/s)
+// kNormBytes of them under way at a time (4096 x 14336 bf16: 117 MB in 26.6 us, 4.4 TB/s)
+constexpr int kNormBytes = 128;
 template <typename T>
 __global__ __launch_bounds__(256) void k_orth_norm(Dense<const T> G, double* __restrict__ part) {
+  constexpr int NR = kNormBytes / (8 * (int)sizeof(T));
   __shared__ double red[4];
   const int z = blockIdx.y;
   // rows and columns up to 2^17: at most 2^31 runs
@@ -821,15 +815,15 @@ __global__ __launch_bounds__(256) void k_orth_norm(Dense<const T> G, double* __r
   const uint32_t per = (uint32_t)(cols + 7) / 8, n = (uint32_t)(G.flip ? G.k : G.r) * per, step = gridDim.x * 256;
   const T* base = G.p + z * G.stride;
   double sum = 0.0;
-  for (uint32_t c0 = blockIdx.x * 256 + threadIdx.x; c0 < n; c0 += 4 * step) {
-    Run8<T> r[4];
+  for (uint32_t c0 = blockIdx.x * 256 + threadIdx.x; c0 < n; c0 += NR * step) {
+    Run8<T> r[NR];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < NR; ++q) {
       const uint32_t c = c0 + q * step;
       r[q].load(base + (c < n ? c / per * G.ld : 0), c < n ? c % per * 8 : cols, cols);
     }
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
+    for (int q = 0; q < NR; ++q) {
       float v[8];
       r[q].get(v);
 #pragma unroll
@@ -947,9 +941,9 @@ __global__ __launch_bounds__(256) void k_ns_join(int BM, int tiles, int full, in
   if (aux.h) {
     // strips start at multiples of 16 rows, tiles at multiples of 64 columns
     const Planes p = aux.tile(z, i0, j0);
-    const int64_t at = r * p.ld + plane_col(p.inter, c);
+    const int64_t at = r * p.ld + plane_col(c);
 #pragma unroll
-    for (int q = 0; q < 4; ++q) x[q] = plane_value(p.h[at + q], p.l ? p.l[at + q] : f16(0));
+    for (int q = 0; q < 4; ++q) x[q] = plane_value(p.h[at + q], p.h[at + kInter + q]);
   }
 #pragma unroll
   for (int q = 0; q < 4; ++q) t[r][c + q] = alpha * x[q] + beta * s[q];
@@ -965,9 +959,9 @@ __global__ __launch_bounds__(256) void k_ns_join(int BM, int tiles, int full, in
   split_words(y, 0, h, l);
   // (the mirror's first column, i0, is a multiple of 16: its planes are taken from the 32 below)
   const Planes o = mirror ? out.tile(z, j0, i0 / 32 * 32) : out.tile(z, i0, j0);
-  const int64_t at = row * o.ld + plane_col(o.inter, col + (mirror ? (int)(i0 % 32) : 0));
+  const int64_t at = row * o.ld + plane_col(col + (mirror ? (int)(i0 % 32) : 0));
   put16<true>(o.h + at, h);
-  if (o.l) put16<true>(o.l + at, l);
+  put16<true>(o.h + at + kInter, l);
 }
 
 // The tile of unit u of a launch on parent tiles `first` and on (numbered through the batch, tm x tn of them a matrix),
@@ -1019,10 +1013,9 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2))) void
   });
 }
 
-// workgroups (and 64-bit partial sums) of one matrix's norm: 4 runs of 8 elements a thread, and no more than fill the
-// GPU
-inline int norm_parts(int64_t elems) {
-  return (int)std::max<int64_t>(1, std::min<int64_t>(1024, elems / (256 * 8 * 4)));
+// workgroups (and 64-bit partial sums) of one matrix's norm: kNormBytes a thread, and no more than fill the GPU
+inline int norm_parts(int64_t elems, int es) {
+  return (int)std::max<int64_t>(1, std::min<int64_t>(1024, elems * es / (256 * kNormBytes)));
 }
 
 // allow_lds, once per kernel and GPU: a call makes about 20 launches
@@ -1057,14 +1050,12 @@ struct Carve {
     off += al256(n * sizeof(T));
     return p;
   }
-  // planes of count matrices of rows x cols; lo: 0 none, 1 its own buffer, else alternating with hi by `lo`
-  Planes planes(int count, int64_t rows, int64_t cols, int lo) {
+  // planes of count matrices of rows x cols
+  Planes planes(int count, int64_t rows, int64_t cols) {
     Planes p;
-    p.inter = lo > 1 ? lo : 0;
-    p.ld = p.inter ? 2 * cols : cols;
+    p.ld = 2 * cols;
     p.stride = rows * p.ld;
     p.h = take<f16>((size_t)count * p.stride);
-    p.l = lo == 0 ? nullptr : lo == 1 ? take<f16>((size_t)count * p.stride) : p.h + lo;
     return p;
   }
 };
@@ -1088,7 +1079,7 @@ MuonWs muon_plan(Carve& c, int blocks, int b) {
   w.chunk = (int)cdiv(blocks, chunks);
   w.part = c.take<double>((size_t)w.chunk * momentum_parts(b));
   w.info = c.take<BlockInfo>(w.chunk);
-  for (Planes& p : w.buf) p = c.planes(w.chunk, P, P, kInter);
+  for (Planes& p : w.buf) p = c.planes(w.chunk, P, P);
   return w;
 }
 
@@ -1106,7 +1097,7 @@ int muon_wide(int nz, int per) {
 }
 
 hipError_t muon_big(MuonTable& t, int b, const MuonK& k, const NsHyper& n, const MuonWs& w, hipStream_t s) {
-  constexpr int lds = std::max(NSmall<3>::LDS, NTiny<3>::LDS);
+  constexpr int lds = std::max(NSmall::LDS, NTiny::LDS);
   const int NB = t.first[t.count], n128 = (int)cdiv(b, 128);
   hipError_t e = lds_once<k_ns_skew<false, false>>(lds);
   if (e == hipSuccess) e = lds_once<k_ns_skew<true, false>>(lds);
@@ -1187,7 +1178,7 @@ struct SymPlan {
   int full, rest, S;
   size_t part() const { return (size_t)rest * S * tile * tile; }
 };
-SymPlan sym_plan(int count, int r, int k, int bk) {
+SymPlan sym_plan(int count, int r, int k) {
   SymPlan p{};
   const auto units = [&](int t) { const int64_t n = cdiv(r, t); return count * n * (n + 1) / 2; };
   constexpr int slots = 512;  // two workgroups a CU
@@ -1197,7 +1188,7 @@ SymPlan sym_plan(int count, int r, int k, int bk) {
   p.tile = units(128) >= 200 ? 128 : 64;
   p.tiles = (int)cdiv(r, p.tile);
   const int64_t n = units(p.tile);
-  const int KT = (int)cdiv(k, bk), left = (int)(n % slots);
+  const int KT = (int)cdiv(k, 32), left = (int)(n % slots);
   p.S = 1;
   if (left > 0 && left <= 0.6 * slots) {
     // rounds of workgroups times the K tiles of one, and what the launch that joins them (about 16 K tiles' time) and
@@ -1218,7 +1209,7 @@ SymPlan sym_plan(int count, int r, int k, int bk) {
 }
 
 struct OrthPlan {
-  int r, k, np, rp, kp;
+  int r, k, rp, kp;
   SymPlan a, b;
   int xtile;     // tile size of X's products, and
   int xn, xwide;  // of 256: tiles, and how many run whole (the rest as 128 x 128)
@@ -1231,13 +1222,8 @@ OrthPlan orth_plan(Carve& c, int count, int rows, int cols, int dt) {
   OrthPlan p{};
   p.r = std::min(rows, cols);
   p.k = std::max(rows, cols);
-  // a short side of up to 128 leaves few roundings to average over: with fp16 products alone the result is up to 5e-3
-  // of its norm off there (2 x 7; 4e-3 for 1 x 1000; both from a model of the roundings in 64 bits).  The digits cost
-  // time: 121 us against 99 for 128 x 4096, 757 against 529 for 256 of 128 x 512
-  p.np = dt == F32 || p.r <= 128 ? 3 : 1;
-  const int bk = p.np == 3 ? 32 : 64;  // one line of a row
-  p.a = sym_plan(count, p.r, p.k, bk);
-  p.b = sym_plan(count, p.r, p.r, bk);
+  p.a = sym_plan(count, p.r, p.k);
+  p.b = sym_plan(count, p.r, p.r);
   const auto units = [&](int t) { return (int64_t)count * cdiv(p.r, t) * cdiv(p.k, t); };
   // the whole call in us, bf16 and fp32, with tiles of 128 / 64: 64 of 128 (1024 x 1024) 223 / 166, 345 / 265; 144
   // (1536 x 1536) 309 / 289, 504 / 497; 256 (1024 x 4096) 278 / 280, 446 / 463, (2048 x 2048) 482 / 482, 822 / 849;
@@ -1253,12 +1239,11 @@ OrthPlan orth_plan(Carve& c, int count, int rows, int cols, int dt) {
   }
   p.rp = (int)round_up(p.r, std::max(p.xtile, p.a.tile));
   p.kp = (int)round_up(p.k, p.xtile);
-  const int lo = p.np == 3 ? kInter : 0;
-  p.part = c.take<double>((size_t)count * norm_parts((int64_t)rows * cols));
-  p.X = c.planes(count, p.rp, p.kp, lo ? lo : 1);
-  for (Planes& t : p.Xt) t = c.planes(count, p.kp, p.rp, lo);
-  p.A = c.planes(count, p.rp, p.rp, lo);
-  p.B = c.planes(count, p.rp, p.rp, lo);
+  p.part = c.take<double>((size_t)count * norm_parts((int64_t)rows * cols, dt == F32 ? 4 : 2));
+  p.X = c.planes(count, p.rp, p.kp);
+  for (Planes& t : p.Xt) t = c.planes(count, p.kp, p.rp);
+  p.A = c.planes(count, p.rp, p.rp);
+  p.B = c.planes(count, p.rp, p.rp);
   p.sums = c.take<float>(std::max(p.a.part(), p.b.part()));
   return p;
 }
@@ -1276,11 +1261,10 @@ hipError_t sym_launch(const SymPlan& p, int K, const Planes& a, const Planes& au
                                                                  beta, sums);
   return hipGetLastError();
 }
-template <int NP>
 hipError_t sym_run(const SymPlan& p, int K, const Planes& a, const Planes& aux, const Planes& out, float alpha,
                    float beta, float* sums, hipStream_t s) {
-  if (p.tile == 128) return sym_launch<NSmall<NP>>(p, K, a, aux, out, alpha, beta, sums, s);
-  return sym_launch<NTiny<NP>>(p, K, a, aux, out, alpha, beta, sums, s);
+  if (p.tile == 128) return sym_launch<NSmall>(p, K, a, aux, out, alpha, beta, sums, s);
+  return sym_launch<NTiny>(p, K, a, aux, out, alpha, beta, sums, s);
 }
 
 // X' (or with `last` the caller's matrix) on parent tiles first .. first + n of sub x sub tiles
@@ -1299,30 +1283,30 @@ hipError_t x_launch(const OrthPlan& p, int first, int n, int sub, const Planes& 
   return hipGetLastError();
 }
 
-template <int NP, typename T>
+template <typename T>
 hipError_t orth_run(const OrthPlan& p, int count, const Dense<const T>& G, const Dense<T>& O, const NsHyper& n,
                     hipStream_t s) {
   const float sx = 8.f * pow2_near(std::sqrt((double)p.k)), a = (float)n.a, b = (float)n.b, c = (float)n.c;
   const float scale = n.rms > 0 ? (float)(n.rms * std::sqrt((double)p.k)) : 1.f;
   const Planes none{};
-  const int parts = norm_parts((int64_t)p.r * p.k);
+  const int parts = norm_parts((int64_t)p.r * p.k, sizeof(T));
   k_orth_norm<T><<<dim3(parts, count), 256, 0, s>>>(G, p.part);
   k_orth_load<T><<<dim3((unsigned)(p.rp / 64) * (p.kp / 64), count), 256, 0, s>>>(G, p.part, parts, sx, (float)n.eps,
                                                                                 p.kp / 64, p.X, p.Xt[0]);
   for (int it = 0; it < n.steps; ++it) {
     const Planes &cur = p.Xt[it & 1], &nxt = p.Xt[(it + 1) & 1];
-    hipError_t e = sym_run<NP>(p.a, p.k, p.X, none, p.A, 0.f, kSA / (sx * sx), p.sums, s);
-    if (e == hipSuccess) e = sym_run<NP>(p.b, p.r, p.A, p.A, p.B, b, c / kSA, p.sums, s);
+    hipError_t e = sym_run(p.a, p.k, p.X, none, p.A, 0.f, kSA / (sx * sx), p.sums, s);
+    if (e == hipSuccess) e = sym_run(p.b, p.r, p.A, p.A, p.B, b, c / kSA, p.sums, s);
     const bool last = it + 1 == n.steps;
     const float al = last ? a * scale / sx : a, be = last ? scale / (kSA * sx) : 1.f / kSA;
     if (e != hipSuccess) return e;
     if (p.xtile == 256) {
-      e = x_launch<NBig<NP>, T>(p, 0, p.xwide, 1, cur, nxt, last, O, al, be, s);
-      if (e == hipSuccess) e = x_launch<NSmall<NP>, T>(p, p.xwide, p.xn - p.xwide, 2, cur, nxt, last, O, al, be, s);
+      e = x_launch<NBig, T>(p, 0, p.xwide, 1, cur, nxt, last, O, al, be, s);
+      if (e == hipSuccess) e = x_launch<NSmall, T>(p, p.xwide, p.xn - p.xwide, 2, cur, nxt, last, O, al, be, s);
     } else {
       const int t = p.xtile, nx = (int)(count * cdiv(p.r, t) * cdiv(p.k, t));
-      e = t == 128 ? x_launch<NSmall<NP>, T>(p, 0, nx, 1, cur, nxt, last, O, al, be, s)
-                   : x_launch<NTiny<NP>, T>(p, 0, nx, 1, cur, nxt, last, O, al, be, s);
+      e = t == 128 ? x_launch<NSmall, T>(p, 0, nx, 1, cur, nxt, last, O, al, be, s)
+                   : x_launch<NTiny, T>(p, 0, nx, 1, cur, nxt, last, O, al, be, s);
     }
     if (e != hipSuccess) return e;
   }
@@ -1337,7 +1321,7 @@ hipError_t orth_t(int count, int rows, int cols, int dt, const void* G, int64_t 
   const int flip = rows > cols;
   const Dense<const T> g{reinterpret_cast<const T*>(G), ldg, sg, p.r, p.k, flip};
   const Dense<T> o{reinterpret_cast<T*>(O), ldo, so, p.r, p.k, flip};
-  return p.np == 3 ? orth_run<3, T>(p, count, g, o, n, s) : orth_run<1, T>(p, count, g, o, n, s);
+  return orth_run<T>(p, count, g, o, n, s);
 }
 
 }  // namespace
