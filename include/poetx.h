@@ -624,6 +624,13 @@ poetx_status poetx_adam_step_batch(int32_t count, const int64_t* len, float* con
  * range over all steps: with S_0 = 1 and S_{i+1} = max |p| on [0, S_i], the
  * calls refuse coefficients with S_i > 4 or |b| S_i^2 + |c| S_i^4 > 200.
  * A zero matrix gives zeros.
+ *
+ * X, A and c A^2 + b A are held in 23 bits, and their products summed in fp32:
+ * the result is as far from the definition as one computed in fp32.  This holds
+ * for entries of X down to about 2^-17 / sqrt(k), 2^-17 of an orthogonal
+ * matrix's; smaller ones are held to 2^-39 / sqrt(k), so that rows at 1e-5 of
+ * the others, or |M|_F at 1e-5 eps, lose the last digits of fp32 (they come out
+ * to about 5e-6 of themselves).
  */
 typedef struct {
   int32_t steps; /* 1 .. 20 */
@@ -655,8 +662,8 @@ size_t poetx_muon_workspace_size(int32_t count, const int32_t* d, int32_t b);
  *     m = beta m + (1 - beta) dq;  u = nesterov ? beta m + (1 - beta) dq : m
  *     O = orthogonalisation of the skew matrix of u, per block
  *     q = q - lr (O + weight_decay q)
- * The products are as exact as fp32 products, all else is fp32 (the norms
- * 64 bits).  The slots that a partial block does not use (j >= r) are neither
+ * The products are as exact as fp32 products (see above), all else is fp32
+ * (the norms 64 bits).  The slots that a partial block does not use (j >= r) are neither
  * read nor written.
  *   q, m   HOST arrays [count] of device pointers to fp32
  *          [ceil(d[i]/b)][b(b-1)/2], read and overwritten (m: momentum)
@@ -685,8 +692,8 @@ size_t poetx_orthogonalize_workspace_size(int32_t count, int32_t rows, int32_t c
  *          stride), else they must not overlap.  The strides matter for
  *          count > 1 only, where they must be at least (rows - 1) ld + cols.
  *   ws     >= poetx_orthogonalize_workspace_size(count, rows, cols, dtype)
- * The products are as exact as fp32 products for both types, and the result is
- * rounded to dtype once.
+ * The products are as exact as fp32 products (see above) for both types, and
+ * the result is rounded to dtype once.
  * Errors: POETX_E_NULL, POETX_E_SHAPE, POETX_E_DTYPE, POETX_E_WORKSPACE, POETX_E_HIP.
  */
 poetx_status poetx_orthogonalize(int32_t count, int32_t rows, int32_t cols, int32_t dtype, const void* G, int64_t ld_g,

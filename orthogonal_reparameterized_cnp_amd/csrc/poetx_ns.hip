@@ -8,10 +8,14 @@
 // singular vectors, so a few steps with a suitable p bring all of them near 1.
 //
 // Operands.  X, A and B live in the workspace as fp16 "planes" at a fixed power
-// of two: hi = fp16(x), lo = fp16(x - hi), 22 bits together.  The products run
-// on the fp16 matrix instructions with fp32 accumulation, hi hi + hi lo + lo hi:
-// as exact as fp32 products (the low-by-low part is 2^-22 of the whole) at three
-// times the cost of one, about 5x the rate of the fp32 matrix instructions.
+// of two: hi = fp16(x), lo = fp16(2^11 (x - hi)), together x to 2^-23 of itself
+// down to 2^-14 and to 2^-36 below (a lo of x - hi itself would lose digits from
+// 2^-3 down, where it is subnormal: rows at 1e-3 of the others came out 1e-4 of
+// themselves off, a matrix with a row 1e4 times the others 2e-5 of its norm).
+// The products run on the fp16 matrix instructions with fp32 accumulation, hi hi
+// + 2^-11 (hi lo + lo hi), the two sums in accumulators of their own: as exact
+// as fp32 products (the low-by-low part is 2^-22 of the whole) at three times
+// the cost of one, about 5x the rate of the fp32 matrix instructions.
 // bf16 matrices take the same products and are rounded once, at the end.  (hi hi
 // alone is 2.5 times as fast, but its roundings of 2^-12 pass through all steps:
 // a matrix of low rank and noise comes out 1.2 to 2.4e-3 of its norm off, a
@@ -46,6 +50,7 @@ typedef _Float16 f16x4_v __attribute__((ext_vector_type(4)));
 
 constexpr float kSA = 256.f;  // scale of A and B
 constexpr int kInter = 32;    // run of hi values between runs of lo values
+constexpr float kLo = 2048.f;  // scale of the lo values
 
 // Tile configuration of the product kernels: two planes per operand, a ring of S stages of BK columns.
 template <int BM_, int BN_, int BK_, int WM_, int WN_, int S_> struct NCfg {
@@ -55,22 +60,20 @@ template <int BM_, int BN_, int BK_, int WM_, int WN_, int S_> struct NCfg {
   static constexpr int A_BYTES = 2 * BM * BK * 2, B_BYTES = 2 * BN * BK * 2;  // one stage
   static constexpr int STAGE = A_BYTES + B_BYTES;
   static constexpr int LA = A_BYTES / 1024 / NW, LB = B_BYTES / 1024 / NW;  // copies per wave and stage
-  // the epilogue stages RS rows of (hi, lo) words; a pitch of 5 mod 64 words spreads both the reads
-  // along its rows and those down its columns over the banks
-  static constexpr int RS = BM < 128 ? BM : 128, PITCH = BN + 5, EPI = RS * PITCH * 4;
+  // the epilogue stages the tile as (hi, lo) words; a pitch of 5 mod 64 words spreads both the reads along its rows
+  // and those down its columns over the banks
+  static constexpr int PITCH = BN + 5, EPI = BM * PITCH * 4;
   static constexpr int LDS = S_ * STAGE > EPI ? S_ * STAGE : EPI;
   static_assert(A_BYTES % (1024 * NW) == 0 && B_BYTES % (1024 * NW) == 0, "tile must split into 1 KB per wave");
   // the K loops run to the next multiple of BK past the last column: no further than the tiles of 64 that hold it
   static_assert(64 % BK == 0, "K steps stay within written tiles");
-  static_assert(BM % RS == 0 && RS % WTM == 0 && PITCH % 64 == 5, "epilogue stage");
+  static_assert(BM == BN && PITCH % 64 == 5, "epilogue stage");
 };
 // 4 waves of 32 x 32, two workgroups a CU: products too small to fill the GPU with larger tiles, bound by latency (two
 // stages of 64 columns, with half the barriers of four of 32: 40 blocks of 256 in 137 us instead of 142)
 using NTiny = NCfg<64, 64, 64, 2, 2, 2>;
 // 4 waves of 64 x 64, two workgroups a CU
 using NSmall = NCfg<128, 128, 32, 2, 2, 2>;
-// 8 waves of 64 x 128
-using NBig = NCfg<256, 256, 32, 4, 2, 2>;
 
 PX_DEV f16x8_v as_f16(const bf16x8_v& x) {
   f16x8_v y;
@@ -78,8 +81,10 @@ PX_DEV f16x8_v as_f16(const bf16x8_v& x) {
   return y;
 }
 
+PX_DEV f16 low_half(float v, f16 h) { return (f16)((v - (float)h) * kLo); }
+
 PX_DEV uint32_t pack_hilo(float v) {
-  const f16 h = (f16)v, l = (f16)(v - (float)h);
+  const f16 h = (f16)v, l = low_half(v, h);
   uint16_t hb, lb;
   __builtin_memcpy(&hb, &h, 2);
   __builtin_memcpy(&lb, &l, 2);
@@ -113,7 +118,9 @@ PX_DEV void ns_loop(char* lds, const Planes& a, const Planes& b, int KT, bool sa
     if (same) return;
     dma_kmaj<C::BN, PK, C::NW>(reinterpret_cast<const bf16_t*>(b.h), b.ld, kt * PK, st + C::A_BYTES, wave, lane);
   };
+  Acc<C> cross;  // kLo times the products of hi and lo values
   acc.zero();
+  cross.zero();
 #pragma unroll
   for (int t = 0; t < C::STAGES - 1; ++t)
     if (t < KT) issue(t, lds + t * C::STAGE);
@@ -162,19 +169,25 @@ PX_DEV void ns_loop(char* lds, const Planes& a, const Planes& b, int KT, bool sa
       for (int i = 0; i < C::TM; ++i)
 #pragma unroll
         for (int j = 0; j < C::TN; ++j) {
-          acc.v[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(c.al[i], c.bh[j], acc.v[i][j], 0, 0, 0);
-          acc.v[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(c.ah[i], c.bl[j], acc.v[i][j], 0, 0, 0);
+          cross.v[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(c.al[i], c.bh[j], cross.v[i][j], 0, 0, 0);
+          cross.v[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(c.ah[i], c.bl[j], cross.v[i][j], 0, 0, 0);
           acc.v[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(c.ah[i], c.bh[j], acc.v[i][j], 0, 0, 0);
         }
       // ask the compiler to interleave the reads with the matrix instructions
       __builtin_amdgcn_iglp_opt(1);
     }
   }
+#pragma unroll
+  for (int i = 0; i < C::TM; ++i)
+#pragma unroll
+    for (int j = 0; j < C::TN; ++j)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc.v[i][j][e] += cross.v[i][j][e] * (1.f / kLo);
   wait_lgkm0();
   barrier_raw();
 }
 
-PX_DEV float plane_value(f16 h, f16 l) { return (float)h + (float)l; }
+PX_DEV float plane_value(f16 h, f16 l) { return (float)h + (float)l * (1.f / kLo); }
 
 // 8 (hi, lo) words -> their hi and their lo halves, each flipped by x
 PX_DEV void split_words(const uint32_t (&w)[8], uint32_t x, uint4& h, uint4& l) {
@@ -199,119 +212,104 @@ template <bool NT> PX_DEV void put16(f16* p, const uint4& v) {
     *reinterpret_cast<uint4*>(p) = v;
 }
 
-// The epilogue of a tile, v = alpha aux + beta acc, RS rows at a time through LDS: the accumulators are staged in
-// fp32, then each thread takes 8 consecutive values of a row, adds the aux planes' (16-byte loads; null: none),
-// writes them to the planes `o` (null: none) and leaves them in LDS, as (hi, lo) words where `t` (the transposed
-// tile's planes; null: none) is written from there with `flip` (0x8000 negates), as floats for emit(r0, stage).
-// All planes are at the tile's origin.  `diag` (with `t` the tile itself): the tile lies on
-// the diagonal of a symmetric or, with `flip`, skew matrix, and its values below the diagonal are the mirrors of those
-// above.  A computed skew matrix would be off by its roundings there, and the products that read X^T as -X, from rows
-// alone, would see the sign of that symmetric part turned over: it grows by about 5 a step where a rounding otherwise
-// grows by 3.4.
+// The epilogue of a tile, v = alpha aux + beta acc, through LDS: the accumulators are staged in fp32, then each thread
+// takes 8 consecutive values of a row, adds the aux planes' (16-byte loads; null: none), writes them to the planes `o`
+// (null: none) and leaves them in LDS, as (hi, lo) words where `t` (the transposed tile's planes; null: none) is
+// written from there with `flip` (0x8000 negates), as floats for emit(stage).  All planes are at the tile's origin.
+// `diag` (with `t` the tile itself): the tile lies on the diagonal of a symmetric or, with `flip`, skew matrix, and its
+// values below the diagonal are the mirrors of those above.  A computed skew matrix would be off by its roundings
+// there, and the products that read X^T as -X, from rows alone, would see the sign of that symmetric part turned over:
+// it grows by about 5 a step where a rounding otherwise grows by 3.4.
 template <class C, class Emit>
 PX_DEV void ns_store(char* lds, const Acc<C>& acc, const Planes& aux, float alpha, float beta, const Planes& o,
                      const Planes& t, uint32_t flip, const Emit& emit, bool diag = false) {
   constexpr bool EMIT = !std::is_same<Emit, std::nullptr_t>::value;
-  constexpr int NIT = C::RS * C::BN / 8 / C::NT;  // a thread's share of the pieces of 8
+  constexpr int NIT = C::BM * C::BN / 8 / C::NT;  // a thread's share of the pieces of 8
+  static_assert(C::BM * C::BN / 8 % C::NT == 0, "whole shares");
   uint32_t* st = reinterpret_cast<uint32_t*>(lds);
   const AccPos<C> p = acc_pos<C>();
-  // the aux values: a thread's whole share is on its way before the stage is written, or for the 256 tile, whose
-  // accumulators leave no room for it, 4 pieces at a time
-  constexpr int NX = C::BM == C::RS ? NIT : 4;
-  static_assert(C::RS * C::BN / 8 % C::NT == 0 && NIT % NX == 0, "whole shares");
-  f16x8_v xh[NX], xl[NX];
-  auto load_aux = [&](int r0, int it0, int n) __attribute__((always_inline)) {
-    if (!aux.h) return;
+  // the aux values: a thread's whole share is on its way before the stage is written
+  f16x8_v xh[NIT], xl[NIT];
+  if (aux.h) {
 #pragma unroll
-    for (int x = 0; x < n; ++x) {
-      const int c = threadIdx.x + (it0 + x) * C::NT, i = c / (C::BN / 8), j = c % (C::BN / 8) * 8;
-      const int64_t at = (r0 + i) * aux.ld + plane_col(j);
+    for (int x = 0; x < NIT; ++x) {
+      const int c = threadIdx.x + x * C::NT, i = c / (C::BN / 8), j = c % (C::BN / 8) * 8;
+      const int64_t at = i * aux.ld + plane_col(j);
       xh[x] = *reinterpret_cast<const f16x8_v*>(aux.h + at);
       xl[x] = *reinterpret_cast<const f16x8_v*>(aux.h + at + kInter);
     }
-  };
-  if constexpr (C::BM == C::RS) load_aux(0, 0, NIT);
-#pragma unroll 1
-  for (int r0 = 0; r0 < C::BM; r0 += C::RS) {
-    __syncthreads();
-    if (p.wm * C::WTM / C::RS * C::RS == r0) {
+  }
+  __syncthreads();
 #pragma unroll
-      for (int i = 0; i < C::TM; ++i)
+  for (int i = 0; i < C::TM; ++i)
 #pragma unroll
-        for (int j = 0; j < C::TN; ++j)
+    for (int j = 0; j < C::TN; ++j)
 #pragma unroll
-          for (int e = 0; e < 16; ++e)
-            st[(p.row(i, e) - r0) * C::PITCH + p.col(j)] = __float_as_uint(beta * acc.v[i][j][e]);
-    }
-    __syncthreads();
+      for (int e = 0; e < 16; ++e) st[p.row(i, e) * C::PITCH + p.col(j)] = __float_as_uint(beta * acc.v[i][j][e]);
+  __syncthreads();
 #pragma unroll
-    for (int it = 0; it < NIT; ++it) {
-      if constexpr (C::BM != C::RS)
-        if (it % 4 == 0) load_aux(r0, it, 4);
-      const int c = threadIdx.x + it * C::NT, i = c / (C::BN / 8), j = c % (C::BN / 8) * 8;
-      uint32_t* w = st + i * C::PITCH + j;
-      float v[8];
+  for (int it = 0; it < NIT; ++it) {
+    const int c = threadIdx.x + it * C::NT, i = c / (C::BN / 8), j = c % (C::BN / 8) * 8;
+    uint32_t* w = st + i * C::PITCH + j;
+    float v[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(w[e]);
-      if (aux.h) {
+    for (int e = 0; e < 8; ++e) v[e] = __uint_as_float(w[e]);
+    if (aux.h) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[e] += alpha * plane_value(xh[it % NX][e], xl[it % NX][e]);
-      }
-      if constexpr (EMIT) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(v[e]);
-      } else {
-        uint32_t x[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = pack_hilo(v[e]);
-        if (!diag || j >= r0 + C::RS) {
-          uint4 h, l;
-          split_words(x, 0, h, l);
-          const int64_t at = (r0 + i) * o.ld + plane_col(j);
-          put16<C::BM == 64>(o.h + at, h);
-          put16<C::BM == 64>(o.h + at + kInter, l);
-        }
-        if (t.h || diag)
-#pragma unroll
-          for (int e = 0; e < 8; ++e) w[e] = x[e];
-      }
+      for (int e = 0; e < 8; ++e) v[e] += alpha * plane_value(xh[it][e], xl[it][e]);
     }
     if constexpr (EMIT) {
-      __syncthreads();
-      emit(r0, reinterpret_cast<const float*>(st));
-    } else if (t.h || diag) {
-      __syncthreads();
-      if (diag) {
-        // the square on the diagonal, of these rows and the same columns
-#pragma unroll 2
-        for (int c = threadIdx.x; c < C::RS * C::RS / 8; c += C::NT) {
-          const int i = c / (C::RS / 8), j = c % (C::RS / 8) * 8;
-          uint32_t x[8];
 #pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            const uint32_t up = st[min(i, j + e) * C::PITCH + r0 + max(i, j + e)];
-            x[e] = j + e > i ? up : j + e < i ? up ^ (flip | flip << 16) : flip ? 0u : up;
-          }
-          uint4 h, l;
-          split_words(x, 0, h, l);
-          const int64_t at = (r0 + i) * o.ld + plane_col(r0 + j);
-          put16<C::BM == 64>(o.h + at, h);
-          put16<C::BM == 64>(o.h + at + kInter, l);
-        }
-      }
-#pragma unroll 2
-      for (int c = threadIdx.x; c < C::RS * C::BN / 8; c += C::NT) {
-        const int j = c / (C::RS / 8), i = c % (C::RS / 8) * 8;
-        if (diag && j < r0 + C::RS) continue;
-        uint32_t x[8];
+      for (int e = 0; e < 8; ++e) w[e] = __float_as_uint(v[e]);
+    } else {
+      uint32_t x[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[e] = st[(i + e) * C::PITCH + j];
+      for (int e = 0; e < 8; ++e) x[e] = pack_hilo(v[e]);
+      if (!diag) {
         uint4 h, l;
-        split_words(x, flip | (flip << 16), h, l);
-        const int64_t at = j * t.ld + plane_col(r0 + i);
-        put16<C::BM == 64>(t.h + at, h);
-        put16<C::BM == 64>(t.h + at + kInter, l);
+        split_words(x, 0, h, l);
+        const int64_t at = i * o.ld + plane_col(j);
+        put16<C::BM == 64>(o.h + at, h);
+        put16<C::BM == 64>(o.h + at + kInter, l);
       }
+      if (t.h || diag)
+#pragma unroll
+        for (int e = 0; e < 8; ++e) w[e] = x[e];
+    }
+  }
+  if constexpr (EMIT) {
+    __syncthreads();
+    emit(reinterpret_cast<const float*>(st));
+  } else if (diag) {
+    __syncthreads();
+#pragma unroll 2
+    for (int c = threadIdx.x; c < C::BM * C::BN / 8; c += C::NT) {
+      const int i = c / (C::BN / 8), j = c % (C::BN / 8) * 8;
+      uint32_t x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const uint32_t up = st[min(i, j + e) * C::PITCH + max(i, j + e)];
+        x[e] = j + e > i ? up : j + e < i ? up ^ (flip | flip << 16) : flip ? 0u : up;
+      }
+      uint4 h, l;
+      split_words(x, 0, h, l);
+      const int64_t at = i * o.ld + plane_col(j);
+      put16<C::BM == 64>(o.h + at, h);
+      put16<C::BM == 64>(o.h + at + kInter, l);
+    }
+  } else if (t.h) {
+    __syncthreads();
+#pragma unroll 2
+    for (int c = threadIdx.x; c < C::BM * C::BN / 8; c += C::NT) {
+      const int j = c / (C::BM / 8), i = c % (C::BM / 8) * 8;
+      uint32_t x[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) x[e] = st[(i + e) * C::PITCH + j];
+      uint4 h, l;
+      split_words(x, flip | (flip << 16), h, l);
+      const int64_t at = j * t.ld + plane_col(i);
+      put16<C::BM == 64>(t.h + at, h);
+      put16<C::BM == 64>(t.h + at + kInter, l);
     }
   }
 }
@@ -519,11 +517,11 @@ PX_DEV void skew_tile(char* lds, const SkewArgs& g, const BlockInfo* info, int b
   } else {
     float* q = info[z].q;
     const float sc = k.scale(r);
-    ns_store<C>(lds, acc, x, g.alpha, g.beta, none, none, 0, [&](int r0, const float* st) {
+    ns_store<C>(lds, acc, x, g.alpha, g.beta, none, none, 0, [&](const float* st) {
       // runs of 8 slots of a packed row (of any alignment)
 #pragma unroll 2
-      for (int c = threadIdx.x; c < C::RS * C::BN / 8; c += C::NT) {
-        const int i = c / (C::BN / 8), j = c % (C::BN / 8) * 8, row = m0 + r0 + i, col = n0 + j;
+      for (int c = threadIdx.x; c < C::BM * C::BN / 8; c += C::NT) {
+        const int i = c / (C::BN / 8), j = c % (C::BN / 8) * 8, row = m0 + i, col = n0 + j;
         if (col + 7 <= row || col >= r) continue;
         float* p = q + packed_slot(row, col, b);
         const float* v = st + i * C::PITCH + j;
@@ -634,7 +632,7 @@ __global__ __launch_bounds__(W * 64) void k_muon_small(MuonTable tab, int b, Muo
     const int i = ij[e] >> 16, j = ij[e] & 0xffff;
     if (ij[e] == 0) continue;
     const float v = (float)((double)u[e] * f);
-    const f16 h = (f16)v, l = (f16)(v - (float)h);
+    const f16 h = (f16)v, l = low_half(v, h);
     Xh[i * LD + j] = h;
     Xl[i * LD + j] = l;
     Xh[j * LD + i] = -h;
@@ -644,14 +642,14 @@ __global__ __launch_bounds__(W * 64) void k_muon_small(MuonTable tab, int b, Muo
   const int m0 = wave / WN * TM * 32, n0 = wave % WN * TM * 32;
   const bool idle = m0 >= r || n0 >= r;
   const int ks_n = (r + 15) / 16, fr = lane & 31, fk = (lane >> 5) * 8;
-  f32x16_v acc[TM][TM];
+  f32x16_v acc[TM][TM], cross[TM][TM];
   auto product = [&](const f16* ah, const f16* al, const f16* bh, const f16* bl) __attribute__((always_inline)) {
 #pragma unroll
     for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TM; ++j)
 #pragma unroll
-        for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.f;
+        for (int e = 0; e < 16; ++e) acc[i][j][e] = cross[i][j][e] = 0.f;
     if (idle) return;
     for (int ks = 0; ks < ks_n; ++ks) {
       f16x8_v fah[TM], fal[TM], fbh[TM], fbl[TM];
@@ -667,11 +665,17 @@ __global__ __launch_bounds__(W * 64) void k_muon_small(MuonTable tab, int b, Muo
       for (int i = 0; i < TM; ++i)
 #pragma unroll
         for (int j = 0; j < TM; ++j) {
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fal[i], fbh[j], acc[i][j], 0, 0, 0);
-          acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fah[i], fbl[j], acc[i][j], 0, 0, 0);
+          cross[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fal[i], fbh[j], cross[i][j], 0, 0, 0);
+          cross[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fah[i], fbl[j], cross[i][j], 0, 0, 0);
           acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fah[i], fbh[j], acc[i][j], 0, 0, 0);
         }
     }
+#pragma unroll
+    for (int i = 0; i < TM; ++i)
+#pragma unroll
+      for (int j = 0; j < TM; ++j)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) acc[i][j][e] += cross[i][j][e] * (1.f / kLo);
   };
   // fn(row, col, values) over the wave's part in runs of 4 rows of one column, the unit a lane owns.  A and B are
   // symmetric and X is skew, so a run of a column is read and written as the run of the row col: 8 bytes, not 4 times 2
@@ -696,7 +700,7 @@ __global__ __launch_bounds__(W * 64) void k_muon_small(MuonTable tab, int b, Muo
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       hv[e] = (f16)v[e];
-      lv[e] = (f16)(v[e] - (float)hv[e]);
+      lv[e] = low_half(v[e], hv[e]);
     }
     *reinterpret_cast<f16x4_v*>(h + at) = hv;
     *reinterpret_cast<f16x4_v*>(l + at) = lv;
@@ -750,7 +754,7 @@ __global__ __launch_bounds__(W * 64) void k_muon_small(MuonTable tab, int b, Muo
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         if (row + e < col) {
-          const f16 hv = (f16)v[e], lv = (f16)(v[e] - (float)hv);
+          const f16 hv = (f16)v[e], lv = low_half(v[e], hv);
           Xh[(row + e) * LD + col] = hv;
           Xl[(row + e) * LD + col] = lv;
           if (row + 3 >= col) {
@@ -909,9 +913,8 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2))) void
   } else {
     const Planes none{};
     float* o = part + (int64_t)u * C::BM * C::BN;
-    ns_store<C>(lds, acc, none, 0.f, 1.f, none, none, 0, [&](int r0, const float* st) {
-      for (int c = threadIdx.x; c < C::RS * C::BN; c += C::NT)
-        o[(int64_t)r0 * C::BN + c] = st[c / C::BN * C::PITCH + c % C::BN];
+    ns_store<C>(lds, acc, none, 0.f, 1.f, none, none, 0, [&](const float* st) {
+      for (int c = threadIdx.x; c < C::BM * C::BN; c += C::NT) o[c] = st[c / C::BN * C::PITCH + c % C::BN];
     });
   }
 }
@@ -964,15 +967,13 @@ __global__ __launch_bounds__(256) void k_ns_join(int BM, int tiles, int full, in
   put16<true>(o.h + at + kInter, l);
 }
 
-// The tile of unit u of a launch on parent tiles `first` and on (numbered through the batch, tm x tn of them a matrix),
-// each cut into sub x sub tiles: matrix, first row, first column.
-template <class C> PX_DEV void x_unit(int u, int tm, int tn, int first, int sub, int& z, int& m0, int& n0) {
-  const int p = first + u / (sub * sub), w = u % (sub * sub);
-  z = p / (tm * tn);
+// The tile of unit u of the batch's tm x tn tiles a matrix: matrix, first row, first column.
+template <class C> PX_DEV void x_unit(int u, int tm, int tn, int& z, int& m0, int& n0) {
+  z = u / (tm * tn);
   int bm, bn;
-  x_tile(p % (tm * tn), tm, tn, bm, bn);
-  m0 = (bm * sub + w / sub) * C::BM;
-  n0 = (bn * sub + w % sub) * C::BN;
+  x_tile(u % (tm * tn), tm, tn, bm, bn);
+  m0 = bm * C::BM;
+  n0 = bn * C::BN;
 }
 
 // X <- alpha X + beta B X on every tile; X is updated in place (a tile is read by its own workgroup only) and its
@@ -980,11 +981,11 @@ template <class C> PX_DEV void x_unit(int u, int tm, int tn, int first, int sub,
 // tiles of 256 x 256 in 463 us, 890 TFLOP/s, and the other 128 as 512 of 128 x 128 in 97 us.
 template <class C>
 __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2))) void k_ns_x(
-    int tm, int tn, int first, int sub, int KT, Planes B, Planes Xt, Planes X, Planes Xt_out, float alpha, float beta) {
+    int tm, int tn, int KT, Planes B, Planes Xt, Planes X, Planes Xt_out, float alpha, float beta) {
   extern __shared__ __align__(16) unsigned char smem[];
   char* lds = reinterpret_cast<char*>(smem);
   int z, m0, n0;
-  x_unit<C>(xcd_unit(blockIdx.x, gridDim.x), tm, tn, first, sub, z, m0, n0);
+  x_unit<C>(xcd_unit(blockIdx.x, gridDim.x), tm, tn, z, m0, n0);
   Acc<C> acc;
   ns_loop<C>(lds, B.tile(z, m0, 0), Xt.tile(z, n0, 0), KT, false, acc);
   const Planes o = X.tile(z, m0, n0);
@@ -994,20 +995,20 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2))) void
 // The last step: alpha X + beta B X to the caller's matrix.
 template <class C, typename T>
 __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2))) void k_ns_out(
-    int tm, int tn, int first, int sub, int KT, Planes B, Planes Xt, Planes X, Dense<T> O, float alpha, float beta) {
+    int tm, int tn, int KT, Planes B, Planes Xt, Planes X, Dense<T> O, float alpha, float beta) {
   extern __shared__ __align__(16) unsigned char smem[];
   int z, m0, n0;
-  x_unit<C>(xcd_unit(blockIdx.x, gridDim.x), tm, tn, first, sub, z, m0, n0);
+  x_unit<C>(xcd_unit(blockIdx.x, gridDim.x), tm, tn, z, m0, n0);
   Acc<C> acc;
   ns_loop<C>(reinterpret_cast<char*>(smem), B.tile(z, m0, 0), Xt.tile(z, n0, 0), KT, false, acc);
   const Planes none{};
   ns_store<C>(reinterpret_cast<char*>(smem), acc, X.tile(z, m0, n0), alpha, beta, none, none, 0,
-              [&](int r0, const float* st) {
+              [&](const float* st) {
     // lanes run along the stored rows
 #pragma unroll 4
-    for (int c = threadIdx.x; c < C::RS * C::BN; c += C::NT) {
-      const int i = O.flip ? c % C::RS : c / C::BN, j = O.flip ? c / C::RS : c % C::BN;
-      const int row = m0 + r0 + i, col = n0 + j;
+    for (int c = threadIdx.x; c < C::BM * C::BN; c += C::NT) {
+      const int i = O.flip ? c % C::BM : c / C::BN, j = O.flip ? c / C::BM : c % C::BN;
+      const int row = m0 + i, col = n0 + j;
       if (row < O.r && col < O.k) *O.at(z, row, col) = from_f32<T>(st[i * C::PITCH + j]);
     }
   });
@@ -1085,10 +1086,10 @@ MuonWs muon_plan(Carve& c, int blocks, int b) {
 
 // How many of nz blocks of `per` 128 x 128 tiles run on those, the others on 64 x 64 ones: whole rounds of workgroups
 // (two a CU), and what is left over of them too where it fills more than 0.6 of a round.  A step in us, the rest on
-// 64 x 64 tiles / on 128 x 128: blocks of 512, 0.17 of a round left 756 / 828, 0.46 973 / 1003, 0.73 1758 / 1731, 0.95
-// 1330 / 1205; blocks of 256, 0.35 648 / 674, 0.76 825 / 807.  Less than one round runs on 64 x 64 tiles up to 0.75 of
-// it: blocks of 256, 0.59 312 / 393, 0.82 416 / 427, 0.94 509 / 445; blocks of 512, 0.23 208 / 352, 0.47 398 / 395,
-// 0.70 577 / 545.
+// 64 x 64 tiles / on 128 x 128: blocks of 512, 0.17 of a round left 770 / 843, 0.46 978 / 1020, 0.73 1759 / 1740, 0.95
+// 1312 / 1207; blocks of 256, 0.35 672 / 713, 0.76 838 / 834.  Less than one round runs on 64 x 64 tiles up to 0.75 of
+// it: blocks of 256, 0.59 320 / 401, 0.82 417 / 437, 0.94 545 / 466; blocks of 512, 0.23 210 / 355, 0.70 567 / 555,
+// 0.78 596 / 580, 0.88 709 / 596.
 int muon_wide(int nz, int per) {
   constexpr int slots = 512;
   const int64_t tiles = (int64_t)nz * per, left = tiles % slots;
@@ -1182,9 +1183,8 @@ SymPlan sym_plan(int count, int r, int k) {
   SymPlan p{};
   const auto units = [&](int t) { const int64_t n = cdiv(r, t); return count * n * (n + 1) / 2; };
   constexpr int slots = 512;  // two workgroups a CU
-  // the whole call in us with tiles of 128 / 64, bf16 and fp32: 36 of 128 (1024 x 4096) 352 / 280, 515 / 460; 136
-  // (2048 x 5461) 806 / 843, 1603 / 1563; 210 (2560 x 4096) 933 / 1032, 1974 / 2002; 528 (4096 x 4096) 1729 / 2384,
-  // 3980 / 4991
+  // the whole call in us with tiles of 128 / 64: 36 of 128 (1024 x 4096) 503 / 447; 120 (1920 x 2048) 806 / 707; 136
+  // (2048 x 2048) 853 / 829, (2048 x 5461) 1597 / 1597; 210 (2560 x 4096) 1974 / 2065; 528 (4096 x 4096) 4247 / 5219
   p.tile = units(128) >= 200 ? 128 : 64;
   p.tiles = (int)cdiv(r, p.tile);
   const int64_t n = units(p.tile);
@@ -1211,8 +1211,7 @@ SymPlan sym_plan(int count, int r, int k) {
 struct OrthPlan {
   int r, k, rp, kp;
   SymPlan a, b;
-  int xtile;     // tile size of X's products, and
-  int xn, xwide;  // of 256: tiles, and how many run whole (the rest as 128 x 128)
+  int xtile;  // tile size of X's products
   double* part;
   float* sums;
   Planes X, Xt[2], A, B;
@@ -1225,18 +1224,11 @@ OrthPlan orth_plan(Carve& c, int count, int rows, int cols, int dt) {
   p.a = sym_plan(count, p.r, p.k);
   p.b = sym_plan(count, p.r, p.r);
   const auto units = [&](int t) { return (int64_t)count * cdiv(p.r, t) * cdiv(p.k, t); };
-  // the whole call in us, bf16 and fp32, with tiles of 128 / 64: 64 of 128 (1024 x 1024) 223 / 166, 345 / 265; 144
-  // (1536 x 1536) 309 / 289, 504 / 497; 256 (1024 x 4096) 278 / 280, 446 / 463, (2048 x 2048) 482 / 482, 822 / 849;
-  // 640 (2560 x 4096) 1029 / 1139, 2007 / 2160.  Tiles of 256 / 128: 160 of 256 (2560 x 4096) 1027 / 1029, 2066 /
-  // 2007; 176 (2048 x 5461) 818 / 844, 1619 / 1561; 256 (4096 x 4096) 1734 / 1811, 3983 / 4194
-  p.xtile = units(256) >= 256 ? 256 : units(128) >= 256 ? 128 : 64;
-  if (p.xtile == 256) {
-    // whole rounds of 256 workgroups, and what is left of them too where it fills more than 0.6 of a round: 4096 rows,
-    // the whole call in us with the rest on 128 / 256, bf16 and fp32: 0.5 of a round left 2401 / 2543, 5591 / 5896;
-    // 0.62 2649 / 2643, 6150 / 6109; 0.75 2793 / 2706, 6453 / 6359
-    p.xn = (int)units(256);
-    p.xwide = p.xn % 256 > 0.6 * 256 ? p.xn : p.xn / 256 * 256;
-  }
+  // the whole call in us with tiles of 128 / 64: 64 of 128 (1024 x 1024) 342 / 261; 144 (1536 x 1536) 506 / 501; 240
+  // (1920 x 2048) 689 / 714; 256 (1024 x 4096) 447 / 452; 640 (2560 x 4096) 1970 / 2078; 1024 (4096 x 4096) 4236 /
+  // 4940
+  // (Tiles of 256 x 256 on 8 waves would need two sets of 128 accumulators a thread, all the registers there are.)
+  p.xtile = units(128) >= 200 ? 128 : 64;
   p.rp = (int)round_up(p.r, std::max(p.xtile, p.a.tile));
   p.kp = (int)round_up(p.k, p.xtile);
   p.part = c.take<double>((size_t)count * norm_parts((int64_t)rows * cols, dt == F32 ? 4 : 2));
@@ -1267,19 +1259,19 @@ hipError_t sym_run(const SymPlan& p, int K, const Planes& a, const Planes& aux, 
   return sym_launch<NTiny>(p, K, a, aux, out, alpha, beta, sums, s);
 }
 
-// X' (or with `last` the caller's matrix) on parent tiles first .. first + n of sub x sub tiles
+// X', or with `last` the caller's matrix
 template <class C, typename T>
-hipError_t x_launch(const OrthPlan& p, int first, int n, int sub, const Planes& cur, const Planes& nxt, bool last,
-                    const Dense<T>& O, float alpha, float beta, hipStream_t s) {
+hipError_t x_launch(const OrthPlan& p, int count, const Planes& cur, const Planes& nxt, bool last, const Dense<T>& O,
+                    float alpha, float beta, hipStream_t s) {
   hipError_t e = lds_once<k_ns_x<C>>(C::LDS);
   if (e == hipSuccess) e = lds_once<k_ns_out<C, T>>(C::LDS);
-  if (e != hipSuccess || n == 0) return e;
-  const int tm = (int)cdiv(p.r, C::BM * sub), tn = (int)cdiv(p.k, C::BN * sub), KR = (int)cdiv(p.r, C::BK);
-  const unsigned grid = (unsigned)n * sub * sub;
+  if (e != hipSuccess) return e;
+  const int tm = (int)cdiv(p.r, C::BM), tn = (int)cdiv(p.k, C::BN), KR = (int)cdiv(p.r, C::BK);
+  const unsigned grid = (unsigned)(count * tm * tn);
   if (last)
-    k_ns_out<C, T><<<grid, C::NT, C::LDS, s>>>(tm, tn, first, sub, KR, p.B, cur, p.X, O, alpha, beta);
+    k_ns_out<C, T><<<grid, C::NT, C::LDS, s>>>(tm, tn, KR, p.B, cur, p.X, O, alpha, beta);
   else
-    k_ns_x<C><<<grid, C::NT, C::LDS, s>>>(tm, tn, first, sub, KR, p.B, cur, p.X, nxt, alpha, beta);
+    k_ns_x<C><<<grid, C::NT, C::LDS, s>>>(tm, tn, KR, p.B, cur, p.X, nxt, alpha, beta);
   return hipGetLastError();
 }
 
@@ -1300,14 +1292,8 @@ hipError_t orth_run(const OrthPlan& p, int count, const Dense<const T>& G, const
     const bool last = it + 1 == n.steps;
     const float al = last ? a * scale / sx : a, be = last ? scale / (kSA * sx) : 1.f / kSA;
     if (e != hipSuccess) return e;
-    if (p.xtile == 256) {
-      e = x_launch<NBig, T>(p, 0, p.xwide, 1, cur, nxt, last, O, al, be, s);
-      if (e == hipSuccess) e = x_launch<NSmall, T>(p, p.xwide, p.xn - p.xwide, 2, cur, nxt, last, O, al, be, s);
-    } else {
-      const int t = p.xtile, nx = (int)(count * cdiv(p.r, t) * cdiv(p.k, t));
-      e = t == 128 ? x_launch<NSmall, T>(p, 0, nx, 1, cur, nxt, last, O, al, be, s)
-                   : x_launch<NTiny, T>(p, 0, nx, 1, cur, nxt, last, O, al, be, s);
-    }
+    e = p.xtile == 128 ? x_launch<NSmall, T>(p, count, cur, nxt, last, O, al, be, s)
+                       : x_launch<NTiny, T>(p, count, cur, nxt, last, O, al, be, s);
     if (e != hipSuccess) return e;
   }
   return hipSuccess;
