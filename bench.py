@@ -746,8 +746,8 @@ def main():
 
         muon = PoetxMuon(layers, lr=1e-5)
         muon.step(dqs)
-        ms, _ = timed(lambda: muon.step(dqs), max(3, args.steps // 2))
-        result["muon_step"] = {"kernel": "momentum, 5 Newton-Schulz steps per block, decay (all sides)", "ms": ms}
+        muon_ms, _ = timed(lambda: muon.step(dqs), max(3, args.steps // 2))
+        result["muon_step"] = {"kernel": "momentum, 5 Newton-Schulz steps per block, decay (all sides)", "ms": muon_ms}
         del muon
 
     if args.breakdown:
