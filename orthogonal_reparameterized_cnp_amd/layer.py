@@ -798,8 +798,8 @@ class PoetxMuon:
         if not layers:
             raise ValueError("no linears")
         self.layers = list(layers)
-        self.device = self.layers[0].device
-        if any(l.device != self.device for l in self.layers):
+        self.device = self.layers[0].q_R.device  # "cuda" and "cuda:0" name one device: the parameters say which
+        if any(q.device != self.device for q in self.params()):
             raise ValueError("the linears of one optimiser must share a device")
         self.lr, self.beta, self.nesterov, self.weight_decay = lr, beta, nesterov, weight_decay
         self.rms, self.ns_steps = rms, ns_steps
