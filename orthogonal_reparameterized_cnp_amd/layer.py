@@ -681,6 +681,25 @@ def _on(device: torch.device, stream):
                 yield
 
 
+def _keep(made_on: Optional[int], *tensors):
+    """To be called after a launch that reads or writes `tensors`, which were allocated with the stream of handle
+    `made_on` current: on another stream, their memory is not given out again before the launch is done, even if
+    their owner drops them at once."""
+    if B._current_stream() == made_on:
+        return
+    s = torch.cuda.current_stream()
+    for t in tensors:
+        t.record_stream(s)
+
+
+def _made_on(device: torch.device) -> Optional[int]:
+    """The handle of the stream that allocations on `device` belong to now (None on the CPU)."""
+    if device.type != "cuda":
+        return None
+    with torch.cuda.device(device):
+        return B._current_stream()
+
+
 def _pitch(t, name: str, T: int, d: int, dtype: torch.dtype, device: torch.device) -> int:
     """Row pitch of a [T, d] matrix whose rows are contiguous; ValueError for any other tensor."""
     if not isinstance(t, torch.Tensor):
@@ -702,7 +721,8 @@ class PoetxNorm:
     """Layer norm (kind "layer") or RMS norm (kind "rms") of token rows, with fp32 weight and, for
     "layer", bias (poetx_norm_fwd / poetx_norm_bwd).  forward(X) returns Y; forward(X, residual) returns
     (Y, S) with S = X + residual, the stream the next residual is added to.  The norm keeps S (X without a
-    residual) and the row statistics for the backward: neither may be overwritten before it.
+    residual) and the row statistics for the backward: neither may be overwritten before it.  The backward may run on
+    another stream than the forward, once that stream waits for the forward's.
 
     weight and bias are plain fp32 tensors; their gradients are what poetx_adam_step_batch takes."""
 
@@ -719,6 +739,7 @@ class PoetxNorm:
         self.bias = torch.zeros(d, dtype=torch.float32, device=self.device) if bias and kind == "layer" else None
         self.S: Optional[torch.Tensor] = None  # the rows of the last forward
         self.stats: Optional[torch.Tensor] = None
+        self._saved_on: Optional[int] = None  # the stream of the last forward
 
     def _params(self):
         _check(self.weight, "weight", (self.d,), torch.float32)
@@ -745,6 +766,7 @@ class PoetxNorm:
                 S = torch.empty(T, d, dtype=dt, device=dev)
             stats = torch.empty(2 if self.kind == "layer" else 1, T, dtype=torch.float32, device=dev)
             B.poetx_norm_fwd(self.desc, T, X, ldx, residual, ldr, self.weight, self.bias, S, lds, Y, ldy, stats)
+            self._saved_on = B._current_stream()
         self.S, self.stats = (X if S is None else S), stats
         return Y if residual is None else (Y, S)
 
@@ -780,6 +802,7 @@ class PoetxNorm:
             ws = torch.empty(B.poetx_norm_workspace_size(self.desc, T), dtype=torch.uint8, device=dev)
             B.poetx_norm_bwd(self.desc, T, dY, ldy, self.S, lds, self.weight, self.stats, dS, ldds, dX, ldx, dw, db, ws,
                              ws.numel())
+            _keep(self._saved_on, self.S, self.stats)
         return dX, dw, db
 
 
@@ -815,6 +838,7 @@ class PoetxMuon:
             self.calls += [(b, idx[k:k + B.POETX_MAX_SIDES]) for k in range(0, len(idx), B.POETX_MAX_SIDES)]
         need = max(B.poetx_muon_workspace_size([self.d[i] for i in idx], b) for b, idx in self.calls)
         self.ws = torch.empty(max(need, 256), dtype=torch.uint8, device=self.device)
+        self._made_on = _made_on(self.device)
         self.steps = 0
 
     def params(self):
@@ -833,6 +857,7 @@ class PoetxMuon:
             for b, idx in self.calls:
                 pick = lambda xs: [xs[i] for i in idx]
                 B.poetx_muon_step_batch(pick(qs), pick(dq), pick(self.m), pick(self.d), b, hp, self.ws, self.ws.numel())
+            _keep(self._made_on, self.ws, *self.m)
             self.steps += 1
             if not (self.merge_every and self.steps % self.merge_every == 0):
                 return False
@@ -844,7 +869,9 @@ class PoetxMuon:
 
 class PoetxOrthogonalizer:
     """Newton-Schulz orthogonalisation of dense update matrices of one shape (poetx_orthogonalize): owns the
-    workspace.  G is [rows, cols] or [count, rows, cols] in `dtype`, with contiguous rows of any pitch."""
+    workspace, which its calls share: they must not overlap in time (calls on two streams take two objects), and a
+    graph captured from one needs it alive.  G is [rows, cols] or [count, rows, cols] in `dtype`, with contiguous rows
+    of any pitch."""
 
     def __init__(self, rows: int, cols: int, dtype: str = "f32", count: int = 1, steps: int = 5, rms: float = 0.2,
                  device: str = "cuda"):
@@ -857,6 +884,7 @@ class PoetxOrthogonalizer:
         if need == 0:
             raise ValueError(f"no workspace for {count} x {rows} x {cols}: {B.poetx_last_error()}")
         self.ws = torch.empty(need, dtype=torch.uint8, device=self.device)
+        self._made_on = _made_on(self.device)
 
     def _strides(self, t, name: str):
         shape = (self.count, self.rows, self.cols)
@@ -886,4 +914,5 @@ class PoetxOrthogonalizer:
                 ldo, so = self.cols, self.rows * self.cols
             B.poetx_orthogonalize(self.count, self.rows, self.cols, B.DTYPES[self.dtype], G, ldg, sg, out, ldo, so,
                                   self.hp, self.ws, self.ws.numel())
+            _keep(self._made_on, self.ws)
         return out
