@@ -758,8 +758,8 @@ poetx_status poetx_norm_fwd(const poetx_norm_desc* desc, int64_t T, const void* 
  *   dS     NULL, or [T] pitch ldds
  *   dX     out [T] pitch lddx; may be dY, or dS (same pitch), else overlaps
  *          neither, nor S
- *   dw, dbias  out fp32 [d], overwritten (zeros for T = 0); either may be
- *          NULL, dbias must be for POETX_NORM_RMS
+ *   dw, dbias  out fp32 [d], overwritten (zeros for T = 0), two arrays; either
+ *          may be NULL, dbias must be for POETX_NORM_RMS
  *   ws     >= poetx_norm_workspace_size(desc, T)
  * Errors: POETX_E_NULL, POETX_E_SHAPE, POETX_E_DTYPE, POETX_E_WORKSPACE, POETX_E_HIP.
  */

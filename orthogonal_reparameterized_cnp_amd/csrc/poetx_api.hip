@@ -1673,6 +1673,8 @@ poetx_status poetx_norm_bwd(const poetx_norm_desc* desc, int64_t T, const void* 
       return fail(POETX_E_SHAPE, "dX must be dY or dS or overlap neither");
     if ((st = check_ws(ws, ws_bytes, poetx_norm_workspace_size(desc, T))) != POETX_OK) return st;
   }
+  if (dw && dbias && meet(Span{dw, desc->d * 4u}, Span{dbias, desc->d * 4u}, 1, desc->d * 4u))
+    return fail(POETX_E_SHAPE, "dw and dbias must not overlap");
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   PX_HIP(norm_bwd(desc->act_dtype, rms, T, desc->d, dY, lddy, S, lds, w, stats, dS, ldds, dX, lddx, dw, dbias,
                   reinterpret_cast<float*>(ws), s));
