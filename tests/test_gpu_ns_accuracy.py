@@ -75,3 +75,22 @@ def test_structured_matrices(name, dtype):
     # for y within t of x, |RN(y) - y| <= |RN(x) - y| <= |RN(x) - x| + t, so |RN(y) - x| <= |RN(x) - x| + 2 t
     off = np.maximum(np.abs(got - ref) - np.abs(rounded(ref) - ref), 0.0)
     assert np.linalg.norm(off) <= 2 * tol
+
+
+@pytest.mark.parametrize("count,rows,cols", [(1, 16, 131072), (1, 131072, 5), (1024, 20, 24)])
+def test_largest_sizes(count, rows, cols):
+    """The longest rows and the largest batch that the call takes; of the batch the first and the last matrix."""
+    print(f"orth {count}x{rows}x{cols}", flush=True)
+    rng = np.random.default_rng(rows)
+    G = torch.from_numpy(rng.standard_normal((count, rows, cols))).cuda().float()
+    out = PoetxOrthogonalizer(rows, cols, "f32", count)(G)
+    torch.cuda.synchronize()
+    hp = ns32()
+    for k in sorted({0, count - 1}):
+        G64, got = G[k].double().cpu().numpy(), out[k].double().cpu().numpy()
+        ref = O.orthogonalize(G64, hp)
+        W = G64 if rows <= cols else G64.T
+        tol = tolerance(W, hp) * O.ns_scale(rows, cols, hp) + 2.0**-24 * np.linalg.norm(ref)
+        d = np.linalg.norm(got - ref)
+        print(f"  off by {d / np.linalg.norm(ref):.2e}, bound {tol / np.linalg.norm(ref):.2e}", flush=True)
+        assert d <= tol
