@@ -7,8 +7,9 @@
 //   dw = sum_t dY xh;  db = sum_t dY
 //
 // Both directions are bound by HBM: every activation is read once into
-// registers, where the row stays until its outputs are written.  A row belongs
-// to TPR threads with E elements each (a wave, or a workgroup whose waves
+// registers, where the row stays until its outputs are written (of the widest
+// rows a part spills, see by_width).  A row belongs to TPR threads with E
+// elements each (a wave, or a workgroup whose waves
 // exchange their sums through LDS), each thread owning the same columns of
 // every row it meets: the weights, and in the backward the column sums dw and
 // db, live in its registers over all rows.  The variance is a second sum over
@@ -33,7 +34,7 @@ typedef uint32_t u32x4_v __attribute__((ext_vector_type(4)));
 // back by the minimum (and those past the row, which hold nothing): its first `skip` columns are its neighbour's,
 // loaded and left out.  So loads have no branch of their own for the row's end, and a next row's stay in flight while
 // this one is summed.  (With one, every row waited where its paths joined for the loads just issued: backward of 16384
-// x 2048 bf16 66 us instead of 53, forward of 1021 x 5461 bf16 21 instead of 13.)
+// x 2048 bf16 66 us instead of 52, forward of 1021 x 5461 bf16 21 instead of 13.)
 template <typename T, int TPR, int E> struct Cols {
   static constexpr int V = kVecOf<T>, NC = E / V;
   static_assert(E % V == 0, "whole chunks");
@@ -253,8 +254,9 @@ struct BwdArgs {
 
 // A workgroup of 1024 threads holds RPW rows at a time: 16 waves keep enough loads in flight for one workgroup a CU,
 // and its rows' column sums leave as one row of partial sums (workgroups of 256 / 512 / 1024, four, two or one a CU,
-// the whole call: 16384 x 2048 bf16 with dS 59.1 / 54.6 / 52.4 us, 3001 x 1376 bf16 23.8 / 18.1 / 15.3).  Bound by
-// bytes: 16384 x 2048, 268 MB at 5.2 TB/s; 3001 x 1376 bf16, three rows a workgroup one after the other, by their sums.
+// whole calls back to back: 16384 x 2048 bf16 with dS 60.8 / 55.1 / 52.9 us, 3001 x 1376 bf16 23.8 / 16.4 / 14.4).
+// Bound by bytes: 16384 x 2048, 268 MB at 5.2 TB/s; 3001 x 1376 bf16, three rows a workgroup one after the other, by
+// their sums.
 constexpr int bwd_threads(int tpr, int e) { return e > 8 ? tpr : 1024 / tpr * tpr; }
 template <typename T, bool RMS, bool RES, int TPR, int E>
 __global__ __launch_bounds__(bwd_threads(TPR, E)) void k_norm_bwd(const BwdArgs a) {
@@ -341,7 +343,7 @@ __global__ __launch_bounds__(bwd_threads(TPR, E)) void k_norm_bwd(const BwdArgs 
   float* P = a.part + (int64_t)blockIdx.x * VECS * d;
   if constexpr (RPW > 1) {
     // the workgroup's column sums: its row groups' added in their order, a column a thread (8 words between the rows of
-    // `acc` spread a thread's neighbours over the banks; group after group 3001 x 1376 took 15.3 us instead of 14.1)
+    // `acc` spread a thread's neighbours over the banks; group after group 3001 x 1376 took 1.2 us longer)
     auto join = [&](const float* v, float* out) {
       __syncthreads();
 #pragma unroll
@@ -407,7 +409,11 @@ __global__ __launch_bounds__(256) void k_norm_colsum(const float* __restrict__ p
 // so that workgroups of 1024 would run one a CU: 16 elements up to 8192 (8192 x 8192 bf16 59 us instead of 80; RMS,
 // which fits, fp32 104 instead of 100).  Past 8192 the backward's rows, sums and weights do not fit the 128 registers
 // of a workgroup of 1024: 768 threads have 168, 512 have 256 (1000 x 10000 fp32, layer, 1024 / 768 / 512 threads: 111 /
-// 45 / 62 us; 2048 x 14336 bf16, RMS with dS, 1024 / 512: 99 / 68).
+// 45 / 62 us; 2048 x 14336 bf16, RMS with dS, 1024 / 512: 99 / 68).  What still spills on 768 / 512 threads, in
+// registers of a thread: layer norm with dS 59 / 191 in fp32 and 6 / 91 in bf16, RMS with dS 12 / 115 and 0 / 13,
+// without dS at most 7 / 78 (fp32, layer, with dS: 2048 x 10000 in 132 us, 2.5 TB/s; 2048 x 14336 in 263, 1.8 TB/s).
+// Past 16384 the 32 columns of a thread spill in both directions, up to 147 registers in the forward and 181 to 501 in
+// the backward (512 x 20000 bf16, layer, backward: 172 us, 0.36 TB/s).
 template <int V> using Int = std::integral_constant<int, V>;
 template <bool BWD, bool RMS, typename F> hipError_t by_width(int d, F&& f) {
   if (d <= 64 * 8) return f(Int<64>(), Int<8>());

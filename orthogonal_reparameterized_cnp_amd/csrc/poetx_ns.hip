@@ -70,7 +70,7 @@ template <int BM_, int BN_, int BK_, int WM_, int WN_, int S_> struct NCfg {
   static_assert(BM == BN && PITCH % 64 == 5, "epilogue stage");
 };
 // 4 waves of 32 x 32, two workgroups a CU: products too small to fill the GPU with larger tiles, bound by latency (two
-// stages of 64 columns, with half the barriers of four of 32: 40 blocks of 256 in 137 us instead of 142)
+// stages of 64 columns have half the barriers of four of 32, which took 4 % longer on 40 blocks of 256)
 using NTiny = NCfg<64, 64, 64, 2, 2, 2>;
 // 4 waves of 64 x 64, two workgroups a CU
 using NSmall = NCfg<128, 128, 32, 2, 2, 2>;
@@ -203,8 +203,8 @@ PX_DEV void split_words(const uint32_t (&w)[8], uint32_t x, uint4& h, uint4& l) 
 
 typedef uint32_t u32x4_v __attribute__((ext_vector_type(4)));
 // 16 bytes to memory.  Small products (NT) write past the L2: what they leave dirty there is written back after their
-// last wave, before the next launch may start (muon step of 40 blocks of 256: 153 -> 144 us; of 160 blocks of 512,
-// whose write-back runs under other tiles, 1882 -> 1926 us).
+// last wave, before the next launch may start (it took a step of 40 blocks of 256 from 153 to 144 us; one of 160 blocks
+// of 512, whose write-back runs under other tiles, would go from 1882 to 1926).
 template <bool NT> PX_DEV void put16(f16* p, const uint4& v) {
   if constexpr (NT)
     __builtin_nontemporal_store(u32x4_v{v.x, v.y, v.z, v.w}, reinterpret_cast<u32x4_v*>(p));
@@ -455,7 +455,7 @@ PX_DEV double sum_parts(const double* part, int n) {
 
 // X planes of every block from its update, scaled by sx / (|M|_F + eps): one 64 x 64 tile on or above the
 // diagonal per workgroup and, off the diagonal, its negated mirror; zeros from r to the end of its last tile.
-// 160 blocks of 512: 168 MB read and as much written in 74 us, 4.5 TB/s.
+// 160 blocks of 512: 257 MB fetched (packed rows start anywhere in a line) and 168 MB written in 73 us, 5.8 TB/s.
 __global__ __launch_bounds__(256) void k_muon_unpack(MuonTable tab, int b, MuonK k, const double* __restrict__ part,
                                                      int parts, float sx, int n64, Planes X) {
   __shared__ float t[64][65];
@@ -543,8 +543,9 @@ PX_DEV void skew_tile(char* lds, const SkewArgs& g, const BlockInfo* info, int b
 // One product of the batch on the tiles on and above the diagonal of its blocks: out = alpha aux + beta a b^T, its
 // mirror flipped by `flip`; with LAST the step of q instead of an output.  The first `wide` blocks run on 128 x 128
 // tiles, the rest, which would leave most of the last round of workgroups empty, on 64 x 64 ones.  160 blocks of 512:
-// 114 us for A and 132 with the term of the planes, three rounds of workgroups, 710 and 610 TFLOP/s of the matrix
-// instructions, bound by them and the clock they leave; 40 blocks of 256: 9 to 10 us, bound by latency.
+// 113 us for A and 129 with the term of the planes, three rounds of workgroups, 715 and 625 TFLOP/s of the matrix
+// instructions, which are busy 30 and 26 % of the time, while 0.36 and 0.49 GB pass the L2s (3.2 and 3.8 TB/s): a
+// tile's copies, products and stores come in part one after the other; 40 blocks of 256: 8 to 9 us, bound by latency.
 template <bool AUX, bool LAST>
 __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void k_ns_skew(
     SkewArgs g, const BlockInfo* __restrict__ info, int b, int n128, int wide, MuonK k) {
@@ -569,7 +570,7 @@ __global__ __launch_bounds__(256) __attribute__((amdgpu_waves_per_eu(2))) void k
 // Blocks of b <= 128: one workgroup keeps X and A (then B) of its block in LDS
 // for the whole step, from the momentum to the step of q, so that a call is one
 // launch.  W waves share the P x P tile; a block of r < P runs its k-steps to r
-// only, and waves whose part lies past r only keep the barriers.  Bound by latency: 16 blocks of 32 take 21.7 us, of
+// only, and waves whose part lies past r only keep the barriers.  Bound by latency: 16 blocks of 32 take 22.2 us, of
 // which 15 dependent products about 0.75 us each.
 template <int P, int W>
 __global__ __launch_bounds__(W * 64) void k_muon_small(MuonTable tab, int b, MuonK k, int steps, float ca, float cb,
@@ -807,11 +808,9 @@ template <typename T> struct Run8 {
 };
 
 // each workgroup's sum of squares in 64 bits: the runs of 8 elements of the stored rows, dealt to the grid's threads,
-// kNormBytes of them under way at a time (4096 x 14336 bf16: 117 MB in 26.6 us, 4.4 TB/s)
-constexpr int kNormBytes = 128;
+// four of them under way at a time (4096 x 14336 bf16: 117 MB in 24.1 us, 4.9 TB/s; eight at a time 28.1)
 template <typename T>
 __global__ __launch_bounds__(256) void k_orth_norm(Dense<const T> G, double* __restrict__ part) {
-  constexpr int NR = kNormBytes / (8 * (int)sizeof(T));
   __shared__ double red[4];
   const int z = blockIdx.y;
   // rows and columns up to 2^17: at most 2^31 runs
@@ -819,15 +818,15 @@ __global__ __launch_bounds__(256) void k_orth_norm(Dense<const T> G, double* __r
   const uint32_t per = (uint32_t)(cols + 7) / 8, n = (uint32_t)(G.flip ? G.k : G.r) * per, step = gridDim.x * 256;
   const T* base = G.p + z * G.stride;
   double sum = 0.0;
-  for (uint32_t c0 = blockIdx.x * 256 + threadIdx.x; c0 < n; c0 += NR * step) {
-    Run8<T> r[NR];
+  for (uint32_t c0 = blockIdx.x * 256 + threadIdx.x; c0 < n; c0 += 4 * step) {
+    Run8<T> r[4];
 #pragma unroll
-    for (int q = 0; q < NR; ++q) {
+    for (int q = 0; q < 4; ++q) {
       const uint32_t c = c0 + q * step;
       r[q].load(base + (c < n ? c / per * G.ld : 0), c < n ? c % per * 8 : cols, cols);
     }
 #pragma unroll
-    for (int q = 0; q < NR; ++q) {
+    for (int q = 0; q < 4; ++q) {
       float v[8];
       r[q].get(v);
 #pragma unroll
@@ -842,7 +841,7 @@ __global__ __launch_bounds__(256) void k_orth_norm(Dense<const T> G, double* __r
 }
 
 // X and X^T planes from the matrix, scaled by sx / (|G|_F + eps), zeros past its ends: one 64 x 64 tile a workgroup.
-// 4096 x 14336 bf16: 117 MB read and 352 MB written in 116 us, 4.1 TB/s, once a call of 4.9 ms.
+// 4096 x 14336 bf16: 117 MB read and 470 MB written in 138 us, 4.3 TB/s, once a call of 11.8 ms.
 template <typename T>
 __global__ __launch_bounds__(256) void k_orth_load(Dense<const T> G, const double* __restrict__ part, int parts,
                                                    float sx, float eps, int tk, Planes X, Planes Xt) {
@@ -891,8 +890,9 @@ PX_DEV void x_tile(int id, int tm, int tn, int& bm, int& bn) {
 
 // out = alpha aux + beta a a^T, symmetric: the tiles on and above the diagonal of every matrix of the batch, `per` of
 // them a matrix.  The last `rest` of them run as S splits of the K loop each, which write their sums to `part` for
-// k_ns_join (they would leave most of a round of workgroups empty).  4096 x 14336 bf16: A in 282 us, 880 TFLOP/s, bound
-// by the matrix instructions (8192^3 of the library: 1130); 512 x 1376 fp32: 7 to 11 us, bound by latency.
+// k_ns_join (they would leave most of a round of workgroups empty).  4096 x 14336: A in 689 us, 1080 TFLOP/s, bound by
+// the matrix instructions (busy 61 % at a clock of 1.65 GHz; 8192^3 of the library: 1130); 512 x 1376 fp32: 8 to 11 us,
+// bound by latency.
 template <class C>
 __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2))) void k_ns_sym(
     int tiles, int KT, int full, int rest, int S, Planes a, Planes aux, Planes out, float alpha, float beta,
@@ -977,8 +977,8 @@ template <class C> PX_DEV void x_unit(int u, int tm, int tn, int& z, int& m0, in
 }
 
 // X <- alpha X + beta B X on every tile; X is updated in place (a tile is read by its own workgroup only) and its
-// transpose written to the other of two buffers, for the other workgroups still read this one.  4096 x 14336 bf16: 768
-// tiles of 256 x 256 in 463 us, 890 TFLOP/s, and the other 128 as 512 of 128 x 128 in 97 us.
+// transpose written to the other of two buffers, for the other workgroups still read this one.  4096 x 14336: 1374 us,
+// 1050 TFLOP/s, bound by the matrix instructions.
 template <class C>
 __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2))) void k_ns_x(
     int tm, int tn, int KT, Planes B, Planes Xt, Planes X, Planes Xt_out, float alpha, float beta) {
@@ -1014,9 +1014,9 @@ __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2))) void
   });
 }
 
-// workgroups (and 64-bit partial sums) of one matrix's norm: kNormBytes a thread, and no more than fill the GPU
+// workgroups (and 64-bit partial sums) of one matrix's norm: 128 bytes a thread, and no more than fill the GPU
 inline int norm_parts(int64_t elems, int es) {
-  return (int)std::max<int64_t>(1, std::min<int64_t>(1024, elems * es / (256 * kNormBytes)));
+  return (int)std::max<int64_t>(1, std::min<int64_t>(1024, elems * es / (256 * 128)));
 }
 
 // allow_lds, once per kernel and GPU: a call makes about 20 launches
