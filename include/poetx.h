@@ -146,7 +146,7 @@ size_t poetx_workspace_size(const poetx_layer_desc* desc, int64_t T, int32_t op)
  * Errors: POETX_E_NULL, POETX_E_SHAPE (d < 1). */
 poetx_status poetx_perm_from_seed(uint64_t seed, int32_t d, int32_t* host_out);
 
-/* Kernel classes for the measurement timer. */
+/* Kernel classes for the measurement timer (the norm of token rows has none). */
 typedef enum {
   POETX_KC_NONE = 0,
   POETX_KC_GEMM = 1,    /* the W~ contractions (forward and backward) */
