@@ -663,8 +663,8 @@ size_t poetx_muon_workspace_size(int32_t count, const int32_t* d, int32_t b);
  *     O = orthogonalisation of the skew matrix of u, per block
  *     q = q - lr (O + weight_decay q)
  * The products are as exact as fp32 products (see above), all else is fp32
- * (the norms 64 bits).  The slots that a partial block does not use (j >= r) are neither
- * read nor written.
+ * (the norms 64 bits).  The slots that a partial block does not use (j >= r)
+ * are neither read nor written.
  *   q, m   HOST arrays [count] of device pointers to fp32
  *          [ceil(d[i]/b)][b(b-1)/2], read and overwritten (m: momentum)
  *   dq     HOST array [count] of device pointers to the gradients, read only

@@ -891,8 +891,8 @@ PX_DEV void x_tile(int id, int tm, int tn, int& bm, int& bn) {
 // out = alpha aux + beta a a^T, symmetric: the tiles on and above the diagonal of every matrix of the batch, `per` of
 // them a matrix.  The last `rest` of them run as S splits of the K loop each, which write their sums to `part` for
 // k_ns_join (they would leave most of a round of workgroups empty).  4096 x 14336: A in 689 us, 1080 TFLOP/s, bound by
-// the matrix instructions (busy 61 % at a clock of 1.65 GHz; 8192^3 of the library: 1130); 512 x 1376 fp32: 8 to 11 us,
-// bound by latency.
+// the matrix instructions (busy 61 % at a clock of 1.65 GHz, with 3.2 GB past the L2s; 8192^3 of the library: 1130); 512
+// x 1376 fp32: 8 to 11 us, bound by latency.
 template <class C>
 __global__ __launch_bounds__(C::NT) __attribute__((amdgpu_waves_per_eu(2))) void k_ns_sym(
     int tiles, int KT, int full, int rest, int S, Planes a, Planes aux, Planes out, float alpha, float beta,
