@@ -146,7 +146,8 @@ size_t poetx_workspace_size(const poetx_layer_desc* desc, int64_t T, int32_t op)
  * Errors: POETX_E_NULL, POETX_E_SHAPE (d < 1). */
 poetx_status poetx_perm_from_seed(uint64_t seed, int32_t d, int32_t* host_out);
 
-/* Kernel classes for the measurement timer (the norm of token rows has none). */
+/* Kernel classes for the measurement timer (the norm of token rows, rotary positions, attention and the log
+ * probabilities have none). */
 typedef enum {
   POETX_KC_NONE = 0,
   POETX_KC_GEMM = 1,    /* the W~ contractions (forward and backward) */
@@ -766,6 +767,203 @@ poetx_status poetx_norm_fwd(const poetx_norm_desc* desc, int64_t T, const void* 
 poetx_status poetx_norm_bwd(const poetx_norm_desc* desc, int64_t T, const void* dY, int64_t lddy, const void* S,
                             int64_t lds, const float* w, const float* stats, const void* dS, int64_t ldds, void* dX,
                             int64_t lddx, float* dw, float* dbias, void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------- rotary positions (queries, keys) -- */
+
+/*
+ * Rotary positions of token rows that hold heads one after another: of every
+ * head, the first rot_dim elements are rot_dim / 2 pairs, and pair j of a token
+ * at position pos turns by the angle pos f[j]:
+ *     (x, y) -> amplitude (x cos - y sin, y cos + x sin)
+ * The elements behind rot_dim are copied.  With `inverse` the angles change
+ * sign, which is the transposed matrix: it takes the gradient of the result to
+ * the gradient of the rows.
+ */
+typedef enum {
+  POETX_ROPE_HALF = 0, /* pair j is elements j and j + rot_dim / 2 */
+  POETX_ROPE_PAIRS = 1 /* pair j is elements 2 j and 2 j + 1 */
+} poetx_rope_layout;
+
+typedef struct {
+  int32_t head_dim;  /* 2 .. 1024 */
+  int32_t rot_dim;   /* even, 2 .. head_dim */
+  int32_t layout;    /* poetx_rope_layout */
+  int32_t act_dtype; /* POETX_F32 or POETX_BF16 */
+} poetx_rope_desc;
+
+/* How the frequencies f[j] = base^(-2 j / rot_dim) are changed for sequences
+ * `factor` times as long as the `original` ones. */
+typedef enum {
+  POETX_ROPE_NONE = 0,
+  POETX_ROPE_LINEAR = 1, /* f / factor */
+  POETX_ROPE_BASE = 2,   /* base factor^(rot_dim / (rot_dim - 2)) in place of base (rot_dim > 2) */
+  POETX_ROPE_BANDS = 3,  /* with r = original f / (2 pi), the turns within the original length: f / factor for r <= low,
+                            f for r >= high, and in between the mix that is linear in r */
+  POETX_ROPE_RAMP = 4    /* the same with the mix linear in j, between the (real) j that make `low` and `high` turns,
+                            rounded down for high and up for low; amplitude 1 + 0.1 ln(factor) */
+} poetx_rope_scaling;
+
+typedef struct {
+  double base;      /* > 1, finite */
+  int32_t scaling;  /* poetx_rope_scaling */
+  double factor;    /* >= 1, finite (read unless NONE) */
+  double original;  /* original length, >= 1, finite (BANDS, RAMP) */
+  double low, high; /* turns, 0 < low < high, finite (BANDS, RAMP) */
+} poetx_rope_params;
+
+/* Host helper: the frequencies in radians per position and the amplitude that
+ * poetx_rope takes.  host_freqs: [rot_dim / 2] host memory; host_amplitude: one
+ * float.  Errors: POETX_E_NULL, POETX_E_SHAPE. */
+poetx_status poetx_rope_freqs(int32_t rot_dim, const poetx_rope_params* p, double* host_freqs, float* host_amplitude);
+
+/*
+ * Rotates the rows of `count` matrices (the queries and the keys) that share
+ * their positions, in one launch.
+ *   pos    [T] int32 device, any value, or NULL: row t is at position t
+ *   freqs  [rot_dim / 2] fp64 device, radians per position.  The angle is
+ *          formed and reduced to one turn in fp64, so far positions lose
+ *          nothing; the rotation is fp32, rounded to act_dtype once.
+ *   amplitude  finite
+ *   X, Y   HOST arrays [count] of device pointers to rows of heads[i] head_dim
+ *          elements, pitches ldx[i], ldy[i] (HOST arrays, >= heads[i] head_dim).
+ *          Y[i] may be X[i] (same pitch); else no Y may share a cell with any
+ *          other operand of the call.
+ *   heads  HOST array [count], each 1 .. 2^20 / head_dim
+ *   count  1 .. 8;  T  0 (a no-op) .. 2^30;  inverse  0 or 1
+ * Errors: POETX_E_NULL, POETX_E_SHAPE, POETX_E_DTYPE, POETX_E_HIP.
+ */
+poetx_status poetx_rope(const poetx_rope_desc* desc, int64_t T, const int32_t* pos, const double* freqs,
+                        float amplitude, int32_t inverse, int32_t count, const void* const* X, const int64_t* ldx,
+                        const int32_t* heads, void* const* Y, const int64_t* ldy, void* stream);
+
+/* --------------------------------------- attention of packed sequences -- */
+
+/*
+ * Attention over `batch` sequences packed one after another into token rows.
+ * For query head h, which reads key head h / (heads / kv_heads), and within
+ * each sequence of nq queries and nk keys:
+ *     x[i][j] = scale q_i . k_j            for the keys j that query i sees
+ *     lse[i]  = log sum_j exp(x[i][j]),  O[i] = sum_j exp(x[i][j] - lse[i]) v_j
+ * A query i stands at place i + nk - nq of the keys (the last query at the last
+ * key).  It sees the keys j of its sequence
+ *   - with causal: j <= place;
+ *   - with window w > 0: place - j < w, and j - place < w.
+ * A query that sees no key gets O = 0 and lse = -infinity, and no gradient.
+ * The scores, the softmax and all sums are fp32.  In bf16 the probabilities
+ * (and in the backward their gradients) are rounded to bf16 as operands of the
+ * products, O and the gradients once at the end; POETX_F32 rounds nothing.
+ * An infinity or NaN in a sequence's rows may reach any row of that sequence,
+ * and none of another.
+ */
+typedef struct {
+  int32_t heads;     /* query heads, 1 .. 1024 */
+  int32_t kv_heads;  /* key and value heads, a divisor of heads */
+  int32_t head_dim;  /* 1 .. 128 */
+  int32_t act_dtype; /* POETX_F32 or POETX_BF16: Q, K, V, O and their gradients */
+  int32_t causal;    /* 0 or 1 */
+  int32_t window;    /* 0: none, else 1 .. 2^30 */
+  float scale;       /* finite and > 0 */
+} poetx_attn_desc;
+
+/* Workspace bytes of poetx_attn_fwd (op = POETX_OP_FWD) or poetx_attn_bwd
+ * (POETX_OP_BWD); may be 0, and is 0 for invalid arguments. */
+size_t poetx_attn_workspace_size(const poetx_attn_desc* desc, int32_t batch, int64_t Tq, int64_t Tk, int32_t op);
+
+/*
+ * Forward.  Rows hold heads one after another (head h at columns h head_dim and
+ * up); pitches are in elements, at least the row's length, of any value (rows
+ * need no alignment beyond the element's).
+ *   cu_q   [batch + 1] int32 device: sequence s is query rows cu_q[s] ..
+ *          cu_q[s + 1] - 1, not decreasing, within 0 .. Tq; rows outside all of
+ *          them are neither read nor written.  NULL: equal sequences of
+ *          Tq / batch rows (which must be whole).
+ *   cu_k   the same for the Tk key rows
+ *   Q      [Tq] rows of heads head_dim;  K, V  [Tk] rows of kv_heads head_dim
+ *   O      out [Tq] rows of heads head_dim; shares no cell with Q, K or V
+ *   lse    out fp32 [heads][Tq]
+ *   ws     >= poetx_attn_workspace_size(desc, batch, Tq, Tk, POETX_OP_FWD)
+ *   batch  1 .. 65536;  Tq, Tk  0 .. 2^30.  Tq = 0 is a no-op.
+ * Errors: POETX_E_NULL, POETX_E_SHAPE, POETX_E_DTYPE, POETX_E_WORKSPACE, POETX_E_HIP.
+ */
+poetx_status poetx_attn_fwd(const poetx_attn_desc* desc, int32_t batch, int64_t Tq, int64_t Tk, const int32_t* cu_q,
+                            const int32_t* cu_k, const void* Q, int64_t ldq, const void* K, int64_t ldk, const void* V,
+                            int64_t ldv, void* O, int64_t ldo, float* lse, void* ws, size_t ws_bytes, void* stream);
+
+/*
+ * Backward for upstream gradient dO.  The probabilities are formed again from Q,
+ * K and the forward's lse:
+ *     p[i][j] = exp(x[i][j] - lse[i]),  D[i] = dO_i . O_i
+ *     dV_j = sum_i p[i][j] dO_i,  g[i][j] = scale p[i][j] (dO_i . v_j - D[i])
+ *     dQ_i = sum_j g[i][j] k_j,   dK_j = sum_i g[i][j] q_i
+ * with the sums of dK and dV over the query heads of a key head too.  Every sum
+ * is taken in a fixed order (deterministic).
+ *   O, lse  written by the forward of these operands
+ *   dQ      out [Tq] rows of heads head_dim;  dK, dV  out [Tk] rows of kv_heads
+ *           head_dim.  They share no cell with an operand or one another; rows
+ *           outside all sequences are left as they were.
+ *   ws      >= poetx_attn_workspace_size(desc, batch, Tq, Tk, POETX_OP_BWD)
+ * The rest as for poetx_attn_fwd; Tq = 0 zeroes the sequences' dK and dV.
+ * Errors: as for poetx_attn_fwd.
+ */
+poetx_status poetx_attn_bwd(const poetx_attn_desc* desc, int32_t batch, int64_t Tq, int64_t Tk, const int32_t* cu_q,
+                            const int32_t* cu_k, const void* dO, int64_t lddo, const void* Q, int64_t ldq,
+                            const void* K, int64_t ldk, const void* V, int64_t ldv, const void* O, int64_t ldo,
+                            const float* lse, void* dQ, int64_t lddq, void* dK, int64_t lddk, void* dV, int64_t lddv,
+                            void* ws, size_t ws_bytes, void* stream);
+
+/* ------------------------------------ log probabilities of given tokens -- */
+
+/*
+ * For every row X of logits, with x = scale X:
+ *     lse = log sum_j exp(x_j),  logp = x_target - lse
+ *     H = -sum_j p_j log p_j,  p_j = exp(x_j - lse)
+ * A logit of -infinity has p = 0 and adds nothing.  A target outside 0 ..
+ * vocab - 1 asks for nothing: logp = 0, and no gradient through it.  A row of
+ * -infinities has lse = -infinity, logp = -infinity (or 0), H = 0 and no gradient;
+ * one with a NaN or +infinity gives NaN.  All sums are fp32.
+ */
+typedef struct {
+  int32_t vocab;     /* columns, 1 .. 2^20 */
+  int32_t act_dtype; /* POETX_F32 or POETX_BF16: X and dX */
+  int32_t top;       /* alternatives per row, 0 .. min(64, vocab) */
+  float scale;       /* the reciprocal temperature, finite and > 0 */
+} poetx_logp_desc;
+
+/* Workspace bytes of poetx_logp_fwd; may be 0, and is 0 for invalid arguments. */
+size_t poetx_logp_workspace_size(const poetx_logp_desc* desc, int64_t T);
+
+/*
+ * Forward over T rows.
+ *   X        [T] rows of vocab, pitch ldx (>= vocab, any value)
+ *   target   [T] int32 device, or NULL with logp NULL
+ *   logp     out fp32 [T], or NULL
+ *   lse      out fp32 [T]
+ *   entropy  out fp32 [T], or NULL
+ *   top_ids, top_logp  out int32 and fp32 [T][top]: the `top` largest logits of
+ *            each row from the largest down, the lower index first among equal
+ *            ones, with x - lse (NaN counts as the largest); NULL with top = 0
+ *   ws       >= poetx_logp_workspace_size(desc, T)
+ * T 0 (a no-op) .. 2^30.
+ * Errors: POETX_E_NULL, POETX_E_SHAPE, POETX_E_DTYPE, POETX_E_WORKSPACE, POETX_E_HIP.
+ */
+poetx_status poetx_logp_fwd(const poetx_logp_desc* desc, int64_t T, const void* X, int64_t ldx, const int32_t* target,
+                            float* logp, float* lse, float* entropy, int32_t* top_ids, float* top_logp, void* ws,
+                            size_t ws_bytes, void* stream);
+
+/*
+ * Backward: the gradient of the logits for upstream gradients of logp and H,
+ *     dX_j = scale (dlogp (1[j = target] - p_j) - dentropy p_j (log p_j + H))
+ *   lse, entropy  of the forward of these rows (entropy: NULL without dentropy).
+ *            log p_j is taken as x_j - lse here: in a row whose largest logit is
+ *            2^20 and more in size, p loses the digits that lse has lost.
+ *   target, dlogp      NULL for none (both)
+ *   dentropy           fp32 [T], or NULL
+ *   dX       out [T] pitch lddx; may be X (same pitch), else shares no cell with it
+ * desc->top is not used.  Errors: POETX_E_NULL, POETX_E_SHAPE, POETX_E_DTYPE, POETX_E_HIP.
+ */
+poetx_status poetx_logp_bwd(const poetx_logp_desc* desc, int64_t T, const void* X, int64_t ldx, const int32_t* target,
+                            const float* lse, const float* entropy, const float* dlogp, const float* dentropy,
+                            void* dX, int64_t lddx, void* stream);
 
 /* ----------------------------------- weight-centric baseline (comparison) -- */
 

@@ -737,3 +737,149 @@ def muon_step(q, g, m, d: int, b: int, hp: MuonHP):
         m[k][live] = mk
         q[k][live] = q[k][live] - hp.lr * (O[i[live], j[live]] + hp.weight_decay * q[k][live])
     return q, m
+
+
+# ----------------------------------------------------------------------------
+# rotary positions
+# ----------------------------------------------------------------------------
+
+
+def rope_freqs(rot_dim: int, base: float = 10000.0, scaling: str = "none", factor: float = 1.0, original: float = 0.0,
+               low: float = 1.0, high: float = 4.0):
+    """(radians per position of every pair, amplitude)."""
+    j = np.arange(rot_dim // 2)
+    if scaling == "base":
+        base = base * factor ** (rot_dim / (rot_dim - 2))
+    f = base ** (-2 * j / rot_dim)
+    if scaling in ("none", "base"):
+        return f, 1.0
+    if scaling == "linear":
+        return f / factor, 1.0
+    if scaling == "bands":
+        turns = original * f / (2 * np.pi)
+        share = np.interp(turns, [low, high], [0.0, 1.0])  # of the unscaled frequency
+        return share * f + (1 - share) * f / factor, 1.0
+    # ramp: the pairs where f makes `high` and `low` turns, on whole numbers
+    at = lambda turns: rot_dim * np.log(original / (2 * np.pi * turns)) / (2 * np.log(base))
+    first, last = max(np.floor(at(high)), 0), min(np.ceil(at(low)), rot_dim // 2 - 1)
+    last = max(last, first + 1e-3)
+    share = 1 - np.clip((j - first) / (last - first), 0, 1)
+    return share * f + (1 - share) * f / factor, 1 + 0.1 * np.log(factor)
+
+
+def rope(X, pos, freqs, head_dim: int, layout: str = "half", amplitude: float = 1.0, inverse: bool = False):
+    """Rows of heads with pair j of each head times amplitude exp(i pos freqs[j])."""
+    half = len(freqs)
+    Y = X.reshape(len(X), -1, head_dim).copy()
+    first = np.arange(half) if layout == "half" else 2 * np.arange(half)
+    second = first + (half if layout == "half" else 1)
+    turn = amplitude * np.exp((-1j if inverse else 1j) * pos[:, None] * freqs)[:, None]
+    z = (Y[..., first] + 1j * Y[..., second]) * turn
+    Y[..., first], Y[..., second] = z.real, z.imag
+    return Y.reshape(X.shape)
+
+
+# ----------------------------------------------------------------------------
+# attention of packed sequences
+# ----------------------------------------------------------------------------
+
+
+@dataclass
+class Attn:
+    heads: int
+    kv_heads: int
+    head_dim: int
+    scale: float
+    causal: bool = True
+    window: int = 0
+
+    def sees(self, nq: int, nk: int):
+        """[nq, nk]: whether query i sees key j."""
+        back = np.arange(nq)[:, None] + nk - nq - np.arange(nk)
+        on = np.ones((nq, nk), dtype=bool)
+        if self.causal:
+            on &= back >= 0
+        if self.window:
+            on &= abs(back) < self.window
+        return on
+
+    def split(self, X, cu, heads):
+        """Every sequence's rows as [heads, rows, head_dim], key heads repeated for their query heads."""
+        for a, b in zip(cu[:-1], cu[1:]):
+            x = X[a:b].reshape(b - a, heads, self.head_dim).transpose(1, 0, 2)
+            yield np.repeat(x, self.heads // heads, 0)
+
+    @staticmethod
+    def join(x):
+        """The inverse of split() for one sequence of [heads, rows, head_dim]."""
+        return x.transpose(1, 0, 2).reshape(x.shape[1], x.shape[0] * x.shape[2])
+
+    def scores(self, Q, K, cu_q, cu_k):
+        for q, k in zip(self.split(Q, cu_q, self.heads), self.split(K, cu_k, self.kv_heads)):
+            x = np.where(self.sees(q.shape[1], k.shape[1]), self.scale * (q @ k.transpose(0, 2, 1)), -np.inf)
+            yield q, k, x
+
+
+def attention(c: Attn, Q, K, V, cu_q, cu_k):
+    """(O, lse [heads, Tq]); rows of no sequence are 0."""
+    O, lse = np.zeros_like(Q), np.zeros((c.heads, len(Q)))
+    for (q, k, x), v, a, b in zip(c.scores(Q, K, cu_q, cu_k), c.split(V, cu_k, c.kv_heads), cu_q[:-1], cu_q[1:]):
+        m = np.max(x, axis=2, initial=-np.inf)
+        e = np.exp(x - np.where(np.isneginf(m), 0.0, m)[..., None])
+        z = e.sum(2)
+        with np.errstate(divide="ignore"):
+            lse[:, a:b] = m + np.log(z)
+        o = (e / np.where(z == 0, 1.0, z)[..., None]) @ v
+        O[a:b] = c.join(o)
+    return O, lse
+
+
+def attention_backward(c: Attn, dO, Q, K, V, O, lse, cu_q, cu_k):
+    """(dQ, dK, dV) at the given O and lse."""
+    dQ, dK, dV = np.zeros_like(Q), np.zeros_like(K), np.zeros_like(V)
+    group = c.heads // c.kv_heads
+    fold = lambda g: c.join(g.reshape(c.kv_heads, group, *g.shape[1:]).sum(1))
+    for (q, k, x), v, do, o, a, b, e, f in zip(c.scores(Q, K, cu_q, cu_k), c.split(V, cu_k, c.kv_heads),
+                                               c.split(dO, cu_q, c.heads), c.split(O, cu_q, c.heads),
+                                               cu_q[:-1], cu_q[1:], cu_k[:-1], cu_k[1:]):
+        l = lse[:, a:b, None]
+        p = np.exp(x - np.where(np.isneginf(l), 0.0, l))
+        g = c.scale * p * (do @ v.transpose(0, 2, 1) - (do * o).sum(2, keepdims=True))
+        dQ[a:b] = c.join(g @ k)
+        dK[e:f] = fold(g.transpose(0, 2, 1) @ q)
+        dV[e:f] = fold(p.transpose(0, 2, 1) @ do)
+    return dQ, dK, dV
+
+
+# ----------------------------------------------------------------------------
+# log probabilities of given tokens
+# ----------------------------------------------------------------------------
+
+
+def token_logprobs(X, target, scale: float = 1.0, top: int = 0):
+    """(logp, lse, entropy, top ids, top log probabilities) of rows of logits."""
+    x = X * scale
+    m = x.max(1)
+    y = x - np.where(np.isneginf(m), 0.0, m)[:, None]  # exact differences, however large the logits
+    with np.errstate(divide="ignore", invalid="ignore"):
+        log_sum = np.log(np.exp(y).sum(1))
+        lse = m + log_sum
+        lx = np.where(np.isneginf(x), -np.inf, y - log_sum[:, None])
+        p = np.exp(lx)
+        H = -np.where(p > 0, p * lx, 0.0).sum(1)
+    given = (target >= 0) & (target < X.shape[1])
+    logp = np.where(given, lx[np.arange(len(X)), np.where(given, target, 0)], 0.0)
+    ids = np.argsort(-X, axis=1, kind="stable")[:, :top]
+    return logp, lse, H, ids, np.take_along_axis(lx, ids, 1)
+
+
+def token_logprobs_backward(X, target, lse, H, dlogp, dH, scale: float = 1.0):
+    """The gradient of X at the given lse and entropy."""
+    with np.errstate(invalid="ignore"):
+        lx = np.where(np.isneginf(X) | np.isneginf(lse)[:, None], -np.inf, X * scale - lse[:, None])
+    p = np.exp(lx)
+    given = (target >= 0) & (target < X.shape[1]) & ~np.isneginf(lse)
+    hit = np.zeros_like(X)
+    hit[np.arange(len(X))[given], target[given]] = 1
+    g = (dlogp * given)[:, None] * (hit - p) - dH[:, None] * np.where(p > 0, p * (np.where(p > 0, lx, 0) + H[:, None]), 0)
+    return scale * g

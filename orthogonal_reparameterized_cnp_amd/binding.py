@@ -121,6 +121,54 @@ class NormDesc(ctypes.Structure):
     ]
 
 
+POETX_ROPE_HALF, POETX_ROPE_PAIRS = 0, 1
+ROPE_LAYOUTS = {"half": POETX_ROPE_HALF, "pairs": POETX_ROPE_PAIRS}
+POETX_ROPE_NONE, POETX_ROPE_LINEAR, POETX_ROPE_BASE, POETX_ROPE_BANDS, POETX_ROPE_RAMP = range(5)
+ROPE_SCALINGS = {"none": POETX_ROPE_NONE, "linear": POETX_ROPE_LINEAR, "base": POETX_ROPE_BASE,
+                 "bands": POETX_ROPE_BANDS, "ramp": POETX_ROPE_RAMP}
+
+
+class RopeDesc(ctypes.Structure):
+    _fields_ = [
+        ("head_dim", ctypes.c_int32),
+        ("rot_dim", ctypes.c_int32),
+        ("layout", ctypes.c_int32),
+        ("act_dtype", ctypes.c_int32),
+    ]
+
+
+class RopeParams(ctypes.Structure):
+    _fields_ = [
+        ("base", ctypes.c_double),
+        ("scaling", ctypes.c_int32),
+        ("factor", ctypes.c_double),
+        ("original", ctypes.c_double),
+        ("low", ctypes.c_double),
+        ("high", ctypes.c_double),
+    ]
+
+
+class AttnDesc(ctypes.Structure):
+    _fields_ = [
+        ("heads", ctypes.c_int32),
+        ("kv_heads", ctypes.c_int32),
+        ("head_dim", ctypes.c_int32),
+        ("act_dtype", ctypes.c_int32),
+        ("causal", ctypes.c_int32),
+        ("window", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
+class LogpDesc(ctypes.Structure):
+    _fields_ = [
+        ("vocab", ctypes.c_int32),
+        ("act_dtype", ctypes.c_int32),
+        ("top", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+    ]
+
+
 class AdamParams(ctypes.Structure):
     _fields_ = [
         ("lr", ctypes.c_float),
@@ -266,6 +314,39 @@ _SIG = {
         ctypes.c_int,
         [ctypes.POINTER(NormDesc), ctypes.c_int64, _P, ctypes.c_int64, _P, ctypes.c_int64, _P, _P, _P, ctypes.c_int64, _P,
          ctypes.c_int64, _P, _P, _P, ctypes.c_size_t, _P],
+    ),
+    "poetx_rope_freqs": (
+        ctypes.c_int,
+        [ctypes.c_int32, ctypes.POINTER(RopeParams), ctypes.POINTER(ctypes.c_double), ctypes.POINTER(ctypes.c_float)],
+    ),
+    "poetx_rope": (
+        ctypes.c_int,
+        [ctypes.POINTER(RopeDesc), ctypes.c_int64, _P, _P, ctypes.c_float, ctypes.c_int32, ctypes.c_int32,
+         ctypes.POINTER(_P), ctypes.POINTER(ctypes.c_int64), ctypes.POINTER(ctypes.c_int32), ctypes.POINTER(_P),
+         ctypes.POINTER(ctypes.c_int64), _P],
+    ),
+    "poetx_attn_workspace_size": (
+        ctypes.c_size_t,
+        [ctypes.POINTER(AttnDesc), ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, ctypes.c_int32],
+    ),
+    "poetx_attn_fwd": (
+        ctypes.c_int,
+        [ctypes.POINTER(AttnDesc), ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, _P, _P] + [_P, ctypes.c_int64] * 4
+        + [_P, _P, ctypes.c_size_t, _P],
+    ),
+    "poetx_attn_bwd": (
+        ctypes.c_int,
+        [ctypes.POINTER(AttnDesc), ctypes.c_int32, ctypes.c_int64, ctypes.c_int64, _P, _P] + [_P, ctypes.c_int64] * 5
+        + [_P] + [_P, ctypes.c_int64] * 3 + [_P, ctypes.c_size_t, _P],
+    ),
+    "poetx_logp_workspace_size": (ctypes.c_size_t, [ctypes.POINTER(LogpDesc), ctypes.c_int64]),
+    "poetx_logp_fwd": (
+        ctypes.c_int,
+        [ctypes.POINTER(LogpDesc), ctypes.c_int64, _P, ctypes.c_int64] + [_P] * 7 + [ctypes.c_size_t, _P],
+    ),
+    "poetx_logp_bwd": (
+        ctypes.c_int,
+        [ctypes.POINTER(LogpDesc), ctypes.c_int64, _P, ctypes.c_int64] + [_P] * 6 + [ctypes.c_int64, _P],
     ),
     "poetx_adam_step_batch": (
         ctypes.c_int,
@@ -588,6 +669,82 @@ def poetx_norm_bwd(dsc: NormDesc, T: int, dY, lddy: int, S, lds: int, w, stats, 
                    dbias, ws, ws_bytes: int, stream=None):
     _check(lib().poetx_norm_bwd(ctypes.byref(dsc), T, _ptr(dY), lddy, _ptr(S), lds, _ptr(w), _ptr(stats), _ptr(dS),
                                 ldds, _ptr(dX), lddx, _ptr(dw), _ptr(dbias), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+# ---------------------------------------------------------- rotary positions ---
+def rope_desc(head_dim: int, rot_dim: int, layout: str, act: str) -> RopeDesc:
+    return RopeDesc(head_dim, rot_dim, ROPE_LAYOUTS[layout], DTYPES[act])
+
+
+def rope_params(base: float = 10000.0, scaling: str = "none", factor: float = 1.0, original: float = 0.0,
+                low: float = 1.0, high: float = 4.0) -> RopeParams:
+    return RopeParams(base, ROPE_SCALINGS[scaling], factor, original, low, high)
+
+
+def poetx_rope_freqs(rot_dim: int, params: RopeParams):
+    """(frequencies [rot_dim / 2] float64, amplitude) on the host."""
+    import numpy as np
+
+    out, amp = np.empty(max(rot_dim // 2, 1), dtype=np.float64), ctypes.c_float()
+    _check(lib().poetx_rope_freqs(rot_dim, ctypes.byref(params), out.ctypes.data_as(ctypes.POINTER(ctypes.c_double)),
+                                  ctypes.byref(amp)))
+    return out, amp.value
+
+
+def poetx_rope(dsc: RopeDesc, T: int, pos, freqs, amplitude: float, inverse: bool, Xs, ldx, heads, Ys, ldy, stream=None):
+    n = len(Xs)
+    _check(lib().poetx_rope(ctypes.byref(dsc), T, _ptr(pos), _ptr(freqs), amplitude, int(inverse), n,
+                            (ctypes.c_void_p * n)(*[_ptr(x) for x in Xs]), (ctypes.c_int64 * n)(*ldx),
+                            (ctypes.c_int32 * n)(*heads), (ctypes.c_void_p * n)(*[_ptr(y) for y in Ys]),
+                            (ctypes.c_int64 * n)(*ldy), _stream(stream)))
+
+
+# ------------------------------------------------ attention of packed sequences ---
+def attn_desc(heads: int, kv_heads: int, head_dim: int, act: str, causal: bool = True, window: int = 0,
+              scale: Optional[float] = None) -> AttnDesc:
+    """scale: 1 / sqrt(head_dim) where it is None."""
+    if scale is None:
+        scale = head_dim**-0.5
+    return AttnDesc(heads, kv_heads, head_dim, DTYPES[act], int(causal), window, scale)
+
+
+def poetx_attn_workspace_size(dsc: AttnDesc, batch: int, Tq: int, Tk: int, op: int) -> int:
+    return lib().poetx_attn_workspace_size(ctypes.byref(dsc), batch, Tq, Tk, op)
+
+
+def poetx_attn_fwd(dsc: AttnDesc, batch: int, Tq: int, Tk: int, cu_q, cu_k, Q, ldq: int, K, ldk: int, V, ldv: int, O,
+                   ldo: int, lse, ws, ws_bytes: int, stream=None):
+    _check(lib().poetx_attn_fwd(ctypes.byref(dsc), batch, Tq, Tk, _ptr(cu_q), _ptr(cu_k), _ptr(Q), ldq, _ptr(K), ldk,
+                                _ptr(V), ldv, _ptr(O), ldo, _ptr(lse), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def poetx_attn_bwd(dsc: AttnDesc, batch: int, Tq: int, Tk: int, cu_q, cu_k, dO, lddo: int, Q, ldq: int, K, ldk: int, V,
+                   ldv: int, O, ldo: int, lse, dQ, lddq: int, dK, lddk: int, dV, lddv: int, ws, ws_bytes: int,
+                   stream=None):
+    _check(lib().poetx_attn_bwd(ctypes.byref(dsc), batch, Tq, Tk, _ptr(cu_q), _ptr(cu_k), _ptr(dO), lddo, _ptr(Q), ldq,
+                                _ptr(K), ldk, _ptr(V), ldv, _ptr(O), ldo, _ptr(lse), _ptr(dQ), lddq, _ptr(dK), lddk,
+                                _ptr(dV), lddv, _ptr(ws), ws_bytes, _stream(stream)))
+
+
+# ---------------------------------------------- log probabilities of given tokens ---
+def logp_desc(vocab: int, act: str, top: int = 0, scale: float = 1.0) -> LogpDesc:
+    return LogpDesc(vocab, DTYPES[act], top, scale)
+
+
+def poetx_logp_workspace_size(dsc: LogpDesc, T: int) -> int:
+    return lib().poetx_logp_workspace_size(ctypes.byref(dsc), T)
+
+
+def poetx_logp_fwd(dsc: LogpDesc, T: int, X, ldx: int, target, logp, lse, entropy, top_ids, top_logp, ws, ws_bytes: int,
+                   stream=None):
+    _check(lib().poetx_logp_fwd(ctypes.byref(dsc), T, _ptr(X), ldx, _ptr(target), _ptr(logp), _ptr(lse), _ptr(entropy),
+                                _ptr(top_ids), _ptr(top_logp), _ptr(ws), ws_bytes, _stream(stream)))
+
+
+def poetx_logp_bwd(dsc: LogpDesc, T: int, X, ldx: int, target, lse, entropy, dlogp, dentropy, dX, lddx: int,
+                   stream=None):
+    _check(lib().poetx_logp_bwd(ctypes.byref(dsc), T, _ptr(X), ldx, _ptr(target), _ptr(lse), _ptr(entropy), _ptr(dlogp),
+                                _ptr(dentropy), _ptr(dX), lddx, _stream(stream)))
 
 
 # ------------------------------------------------------------ one SPO factor ---

@@ -1823,3 +1823,298 @@ poetx_status poetx_orthogonalize(int32_t count, int32_t rows, int32_t cols, int3
 }
 
 }  // extern "C"
+
+// ---------------------------------------------------------------------------
+// rotary positions, attention, log probabilities
+// ---------------------------------------------------------------------------
+namespace {
+
+// `rows` rows of `width` bytes, `pitch` apart
+struct Mat {
+  const void* p;
+  uint64_t rows, width, pitch;
+};
+// Whether two matrices share a cell.  With one pitch they may lie in each other's gaps (columns of one buffer); with two
+// they must lie apart.
+bool share(const Mat& x, const Mat& y) {
+  if (!x.p || !y.p || !x.rows || !y.rows) return false;
+  const bool swap = reinterpret_cast<uintptr_t>(x.p) > reinterpret_cast<uintptr_t>(y.p);
+  const Mat &a = swap ? y : x, &b = swap ? x : y;
+  const uint64_t off = reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p);
+  if (off >= (a.rows - 1) * a.pitch + a.width) return false;
+  if (a.pitch != b.pitch) return true;
+  // row j of b begins r behind the beginning of a's row q + j
+  const uint64_t q = off / a.pitch, r = off % a.pitch;
+  return r < a.width || (r + b.width > a.pitch && q + 1 < a.rows);
+}
+
+poetx_status check_rows(const char* name, const void* p, int64_t ld, int64_t cols, int dt) {
+  if (!p) return fail(POETX_E_NULL, std::string(name) + " is NULL");
+  if (ld < cols) return fail(POETX_E_SHAPE, std::string(name) + ": the row pitch must be at least the row's length");
+  if (ld > (int64_t(1) << 31)) return fail(POETX_E_SHAPE, std::string(name) + ": the row pitch must be at most 2^31");
+  if (reinterpret_cast<uintptr_t>(p) % dt_size(dt))
+    return fail(POETX_E_SHAPE, std::string(name) + " must be aligned to its element");
+  return POETX_OK;
+}
+
+bool float_dtype(int32_t dt) { return dt == POETX_F32 || dt == POETX_BF16; }
+
+poetx_status check_rope(const poetx_rope_desc* d, int64_t T) {
+  if (!d) return fail(POETX_E_NULL, "desc is NULL");
+  if (d->head_dim < 2 || d->head_dim > 1024) return fail(POETX_E_SHAPE, "head_dim must be in [2, 1024]");
+  if (d->rot_dim < 2 || d->rot_dim > d->head_dim || d->rot_dim % 2)
+    return fail(POETX_E_SHAPE, "rot_dim must be even and in [2, head_dim]");
+  if (d->layout != POETX_ROPE_HALF && d->layout != POETX_ROPE_PAIRS)
+    return fail(POETX_E_SHAPE, "layout must be POETX_ROPE_HALF or POETX_ROPE_PAIRS");
+  if (!float_dtype(d->act_dtype)) return fail(POETX_E_DTYPE, "act_dtype must be F32 or BF16");
+  if (T < 0 || T > kMaxNormT) return fail(POETX_E_SHAPE, "T must be in [0, 2^30]");
+  return POETX_OK;
+}
+
+poetx_status check_attn(const poetx_attn_desc* d, int32_t batch, int64_t Tq, int64_t Tk) {
+  if (!d) return fail(POETX_E_NULL, "desc is NULL");
+  if (d->heads < 1 || d->heads > 1024) return fail(POETX_E_SHAPE, "heads must be in [1, 1024]");
+  if (d->kv_heads < 1 || d->heads % d->kv_heads) return fail(POETX_E_SHAPE, "kv_heads must divide heads");
+  if (d->head_dim < 1 || d->head_dim > kAttnMaxD) return fail(POETX_E_SHAPE, "head_dim must be in [1, 128]");
+  if (!float_dtype(d->act_dtype)) return fail(POETX_E_DTYPE, "act_dtype must be F32 or BF16");
+  if (d->causal != 0 && d->causal != 1) return fail(POETX_E_SHAPE, "causal must be 0 or 1");
+  if (d->window < 0 || d->window > (1 << 30)) return fail(POETX_E_SHAPE, "window must be in [0, 2^30]");
+  if (!(std::isfinite(d->scale) && d->scale > 0.f)) return fail(POETX_E_SHAPE, "scale must be finite and > 0");
+  if (batch < 1 || batch > 65536) return fail(POETX_E_SHAPE, "batch must be in [1, 65536]");
+  if (Tq < 0 || Tq > kMaxNormT || Tk < 0 || Tk > kMaxNormT) return fail(POETX_E_SHAPE, "Tq and Tk must be in [0, 2^30]");
+  return POETX_OK;
+}
+AttnDesc attn_desc(const poetx_attn_desc* d, int32_t batch, int64_t Tq, int64_t Tk, const int32_t* cu_q,
+                   const int32_t* cu_k) {
+  return AttnDesc{d->act_dtype, d->heads, d->kv_heads, d->head_dim, d->causal != 0, d->window,
+                  d->scale, batch, Tq, Tk, cu_q, cu_k};
+}
+poetx_status check_seqs(const AttnDesc& a) {
+  if (!a.cu_q && a.Tq % a.batch) return fail(POETX_E_SHAPE, "without cu_q, Tq must be a multiple of batch");
+  if (!a.cu_k && a.Tk % a.batch) return fail(POETX_E_SHAPE, "without cu_k, Tk must be a multiple of batch");
+  if (!attn_fits(a)) return fail(POETX_E_SHAPE, "too many rows and heads for one call");
+  return POETX_OK;
+}
+
+poetx_status check_logp(const poetx_logp_desc* d, int64_t T) {
+  if (!d) return fail(POETX_E_NULL, "desc is NULL");
+  if (d->vocab < 1 || d->vocab > kLogpMaxV) return fail(POETX_E_SHAPE, "vocab must be in [1, 2^20]");
+  if (!float_dtype(d->act_dtype)) return fail(POETX_E_DTYPE, "act_dtype must be F32 or BF16");
+  if (d->top < 0 || d->top > kLogpTop || d->top > d->vocab) return fail(POETX_E_SHAPE, "top must be in [0, min(64, vocab)]");
+  if (!(std::isfinite(d->scale) && d->scale > 0.f)) return fail(POETX_E_SHAPE, "scale must be finite and > 0");
+  if (T < 0 || T > kMaxNormT) return fail(POETX_E_SHAPE, "T must be in [0, 2^30]");
+  return POETX_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+poetx_status poetx_rope_freqs(int32_t rot_dim, const poetx_rope_params* p, double* host_freqs, float* host_amplitude) {
+  if (!p || !host_freqs || !host_amplitude) return fail(POETX_E_NULL, "p, host_freqs and host_amplitude must be non-NULL");
+  if (rot_dim < 2 || rot_dim > 1024 || rot_dim % 2) return fail(POETX_E_SHAPE, "rot_dim must be even and in [2, 1024]");
+  if (!(std::isfinite(p->base) && p->base > 1.0)) return fail(POETX_E_SHAPE, "base must be finite and > 1");
+  const bool none = p->scaling == POETX_ROPE_NONE, bands = p->scaling == POETX_ROPE_BANDS,
+             ramp = p->scaling == POETX_ROPE_RAMP;
+  if (!none && !bands && !ramp && p->scaling != POETX_ROPE_LINEAR && p->scaling != POETX_ROPE_BASE)
+    return fail(POETX_E_SHAPE, "unknown scaling");
+  if (!none && !(std::isfinite(p->factor) && p->factor >= 1.0))
+    return fail(POETX_E_SHAPE, "factor must be finite and >= 1");
+  if (p->scaling == POETX_ROPE_BASE && rot_dim == 2) return fail(POETX_E_SHAPE, "POETX_ROPE_BASE needs rot_dim > 2");
+  if (bands || ramp) {
+    if (!(std::isfinite(p->original) && p->original >= 1.0))
+      return fail(POETX_E_SHAPE, "original must be finite and >= 1");
+    if (!(p->low > 0.0 && p->high > p->low && std::isfinite(p->high)))
+      return fail(POETX_E_SHAPE, "low and high must satisfy 0 < low < high");
+  }
+  const double two_pi = 6.28318530717958647693;
+  double base = p->base;
+  if (p->scaling == POETX_ROPE_BASE) base *= std::pow(p->factor, rot_dim / (rot_dim - 2.0));
+  // the (real) pair that makes `turns` turns within the original length: original base^(-2 j / rot_dim) = 2 pi turns
+  const auto pair_of = [&](double turns) {
+    return 0.5 * rot_dim * std::log(p->original / (two_pi * turns)) / std::log(base);
+  };
+  double j0 = 0.0, j1 = 0.0;
+  if (ramp) {
+    j0 = std::max(std::floor(pair_of(p->high)), 0.0);
+    j1 = std::min(std::ceil(pair_of(p->low)), rot_dim / 2 - 1.0);
+    j1 = std::max(j1, j0 + 1e-3);  // a step where the two meet
+  }
+  for (int j = 0; j < rot_dim / 2; ++j) {
+    const double f = std::pow(base, -2.0 * j / rot_dim);
+    double keep = 1.0;  // the share of f that is left unscaled
+    if (p->scaling == POETX_ROPE_LINEAR) keep = 0.0;
+    if (bands) keep = (p->original * f / two_pi - p->low) / (p->high - p->low);
+    if (ramp) keep = 1.0 - (j - j0) / (j1 - j0);
+    keep = std::min(std::max(keep, 0.0), 1.0);
+    host_freqs[j] = p->scaling == POETX_ROPE_BASE || none ? f : keep * f + (1.0 - keep) * f / p->factor;
+  }
+  *host_amplitude = ramp ? (float)(1.0 + 0.1 * std::log(p->factor)) : 1.f;
+  return POETX_OK;
+}
+
+poetx_status poetx_rope(const poetx_rope_desc* desc, int64_t T, const int32_t* pos, const double* freqs,
+                        float amplitude, int32_t inverse, int32_t count, const void* const* X, const int64_t* ldx,
+                        const int32_t* heads, void* const* Y, const int64_t* ldy, void* stream) {
+  poetx_status st = check_rope(desc, T);
+  if (st != POETX_OK) return st;
+  if (count < 1 || count > kRopeSides) return fail(POETX_E_SHAPE, "count must be in [1, 8]");
+  if (!std::isfinite(amplitude)) return fail(POETX_E_SHAPE, "amplitude must be finite");
+  if (inverse != 0 && inverse != 1) return fail(POETX_E_SHAPE, "inverse must be 0 or 1");
+  if (!X || !ldx || !heads || !Y || !ldy) return fail(POETX_E_NULL, "X, ldx, heads, Y and ldy must be non-NULL");
+  for (int i = 0; i < count; ++i)
+    if (heads[i] < 1 || heads[i] > (1 << 20) / desc->head_dim)
+      return fail(POETX_E_SHAPE, "heads[i] must be in [1, 2^20 / head_dim]");
+  if (T == 0) return POETX_OK;
+  if (!freqs) return fail(POETX_E_NULL, "freqs is NULL");
+  if (reinterpret_cast<uintptr_t>(freqs) % 8 || reinterpret_cast<uintptr_t>(pos) % 4)
+    return fail(POETX_E_SHAPE, "freqs and pos must be aligned to their elements");
+  const int dt = desc->act_dtype;
+  const uint64_t es = dt_size(dt);
+  RopeSide sides[kRopeSides];
+  std::vector<Mat> in, out;
+  for (int i = 0; i < count; ++i) {
+    const int64_t cols = (int64_t)heads[i] * desc->head_dim;
+    if ((st = check_rows("X[i]", X[i], ldx[i], cols, dt)) != POETX_OK) return st;
+    if ((st = check_rows("Y[i]", Y[i], ldy[i], cols, dt)) != POETX_OK) return st;
+    if (X[i] == Y[i] && ldx[i] != ldy[i]) return fail(POETX_E_SHAPE, "Y[i] in place of X[i] must have its pitch");
+    sides[i] = RopeSide{X[i], Y[i], ldx[i], ldy[i], heads[i]};
+    in.push_back(Mat{X[i], (uint64_t)T, cols * es, ldx[i] * es});
+    out.push_back(Mat{Y[i], (uint64_t)T, cols * es, ldy[i] * es});
+  }
+  const uint64_t pos_bytes = (uint64_t)T * 4, table_bytes = (uint64_t)desc->rot_dim * 4;
+  const Mat places{pos, 1, pos_bytes, pos_bytes}, table{freqs, 1, table_bytes, table_bytes};
+  for (int i = 0; i < count; ++i) {
+    bool bad = share(out[i], places) || share(out[i], table);
+    for (int j = 0; j < count; ++j) {
+      if (j != i) bad |= share(out[i], out[j]);
+      if (j != i || X[i] != Y[i]) bad |= share(out[i], in[j]);
+    }
+    if (bad) return fail(POETX_E_SHAPE, "Y[i] must be X[i] or share no cell with another operand");
+  }
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  PX_HIP(rope(dt, desc->layout == POETX_ROPE_PAIRS, T, desc->head_dim, desc->rot_dim, pos, freqs, amplitude,
+              inverse != 0, count, sides, s));
+  return POETX_OK;
+}
+
+size_t poetx_attn_workspace_size(const poetx_attn_desc* desc, int32_t batch, int64_t Tq, int64_t Tk, int32_t op) {
+  if (check_attn(desc, batch, Tq, Tk) != POETX_OK) return 0;
+  const AttnDesc a = attn_desc(desc, batch, Tq, Tk, nullptr, nullptr);
+  if (!attn_fits(a)) return 0;
+  return op == POETX_OP_FWD ? attn_fwd_ws_bytes(a) : op == POETX_OP_BWD ? attn_bwd_ws_bytes(a) : 0;
+}
+
+poetx_status poetx_attn_fwd(const poetx_attn_desc* desc, int32_t batch, int64_t Tq, int64_t Tk, const int32_t* cu_q,
+                            const int32_t* cu_k, const void* Q, int64_t ldq, const void* K, int64_t ldk, const void* V,
+                            int64_t ldv, void* O, int64_t ldo, float* lse, void* ws, size_t ws_bytes, void* stream) {
+  poetx_status st = check_attn(desc, batch, Tq, Tk);
+  if (st != POETX_OK) return st;
+  const AttnDesc a = attn_desc(desc, batch, Tq, Tk, cu_q, cu_k);
+  if ((st = check_seqs(a)) != POETX_OK) return st;
+  if (Tq == 0) return POETX_OK;
+  const int dt = a.dt;
+  const uint64_t es = dt_size(dt), nq = (uint64_t)a.heads * a.hd, nk = (uint64_t)a.kv_heads * a.hd;
+  if ((st = check_rows("Q", Q, ldq, nq, dt)) != POETX_OK) return st;
+  if ((st = check_rows("O", O, ldo, nq, dt)) != POETX_OK) return st;
+  if (Tk > 0) {
+    if ((st = check_rows("K", K, ldk, nk, dt)) != POETX_OK) return st;
+    if ((st = check_rows("V", V, ldv, nk, dt)) != POETX_OK) return st;
+  }
+  if (!lse) return fail(POETX_E_NULL, "lse is NULL");
+  const Mat o{O, (uint64_t)Tq, nq * es, ldo * es};
+  if (share(o, Mat{Q, (uint64_t)Tq, nq * es, ldq * es}) || share(o, Mat{K, (uint64_t)Tk, nk * es, ldk * es}) ||
+      share(o, Mat{V, (uint64_t)Tk, nk * es, ldv * es}))
+    return fail(POETX_E_SHAPE, "O must share no cell with Q, K or V");
+  if ((st = check_ws(ws, ws_bytes, attn_fwd_ws_bytes(a))) != POETX_OK) return st;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  PX_HIP(attn_fwd(a, AttnMat{Q, ldq}, AttnMat{K, ldk}, AttnMat{V, ldv}, O, ldo, lse, ws, s));
+  return POETX_OK;
+}
+
+poetx_status poetx_attn_bwd(const poetx_attn_desc* desc, int32_t batch, int64_t Tq, int64_t Tk, const int32_t* cu_q,
+                            const int32_t* cu_k, const void* dO, int64_t lddo, const void* Q, int64_t ldq,
+                            const void* K, int64_t ldk, const void* V, int64_t ldv, const void* O, int64_t ldo,
+                            const float* lse, void* dQ, int64_t lddq, void* dK, int64_t lddk, void* dV, int64_t lddv,
+                            void* ws, size_t ws_bytes, void* stream) {
+  poetx_status st = check_attn(desc, batch, Tq, Tk);
+  if (st != POETX_OK) return st;
+  const AttnDesc a = attn_desc(desc, batch, Tq, Tk, cu_q, cu_k);
+  if ((st = check_seqs(a)) != POETX_OK) return st;
+  const int dt = a.dt;
+  const uint64_t es = dt_size(dt), nq = (uint64_t)a.heads * a.hd, nk = (uint64_t)a.kv_heads * a.hd;
+  std::vector<Mat> in, out;
+  struct Op {
+    const char* name;
+    const void* p;
+    int64_t ld;
+    bool key, written;
+  };
+  const Op ops[] = {{"dO", dO, lddo, false, false}, {"Q", Q, ldq, false, false}, {"O", O, ldo, false, false},
+                    {"K", K, ldk, true, false},     {"V", V, ldv, true, false},  {"dQ", dQ, lddq, false, true},
+                    {"dK", dK, lddk, true, true},   {"dV", dV, lddv, true, true}};
+  for (const Op& o : ops) {
+    const int64_t rows = o.key ? Tk : Tq, cols = o.key ? nk : nq;
+    if (rows == 0) continue;
+    if ((st = check_rows(o.name, o.p, o.ld, cols, dt)) != POETX_OK) return st;
+    (o.written ? out : in).push_back(Mat{o.p, (uint64_t)rows, cols * es, o.ld * es});
+  }
+  if (Tq > 0 && !lse) return fail(POETX_E_NULL, "lse is NULL");
+  for (size_t i = 0; i < out.size(); ++i) {
+    bool bad = false;
+    for (const Mat& m : in) bad |= share(out[i], m);
+    for (size_t j = 0; j < i; ++j) bad |= share(out[i], out[j]);
+    if (bad) return fail(POETX_E_SHAPE, "dQ, dK and dV must share no cell with an operand or one another");
+  }
+  if ((st = check_ws(ws, ws_bytes, attn_bwd_ws_bytes(a))) != POETX_OK) return st;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  PX_HIP(attn_bwd(a, AttnMat{dO, lddo}, AttnMat{Q, ldq}, AttnMat{K, ldk}, AttnMat{V, ldv}, AttnMat{O, ldo}, lse, dQ, lddq,
+                  dK, lddk, dV, lddv, ws, s));
+  return POETX_OK;
+}
+
+size_t poetx_logp_workspace_size(const poetx_logp_desc* desc, int64_t T) {
+  if (check_logp(desc, T) != POETX_OK) return 0;
+  return logp_ws_bytes(desc->act_dtype, T, desc->vocab, desc->top);
+}
+
+poetx_status poetx_logp_fwd(const poetx_logp_desc* desc, int64_t T, const void* X, int64_t ldx, const int32_t* target,
+                            float* logp, float* lse, float* entropy, int32_t* top_ids, float* top_logp, void* ws,
+                            size_t ws_bytes, void* stream) {
+  poetx_status st = check_logp(desc, T);
+  if (st != POETX_OK) return st;
+  if (T == 0) return POETX_OK;
+  if ((st = check_rows("X", X, ldx, desc->vocab, desc->act_dtype)) != POETX_OK) return st;
+  if (!lse) return fail(POETX_E_NULL, "lse is NULL");
+  if ((target != nullptr) != (logp != nullptr)) return fail(POETX_E_NULL, "logp is written with targets, and only then");
+  if ((desc->top > 0) != (top_ids != nullptr) || (desc->top > 0) != (top_logp != nullptr))
+    return fail(POETX_E_NULL, "top_ids and top_logp are written with top > 0, and only then");
+  if ((st = check_ws(ws, ws_bytes, poetx_logp_workspace_size(desc, T))) != POETX_OK) return st;
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  PX_HIP(logp_fwd(desc->act_dtype, T, desc->vocab, desc->top, desc->scale, X, ldx, target, logp, lse, entropy, top_ids,
+                  top_logp, ws, s));
+  return POETX_OK;
+}
+
+poetx_status poetx_logp_bwd(const poetx_logp_desc* desc, int64_t T, const void* X, int64_t ldx, const int32_t* target,
+                            const float* lse, const float* entropy, const float* dlogp, const float* dentropy,
+                            void* dX, int64_t lddx, void* stream) {
+  poetx_status st = check_logp(desc, T);
+  if (st != POETX_OK) return st;
+  if (T == 0) return POETX_OK;
+  if ((st = check_rows("X", X, ldx, desc->vocab, desc->act_dtype)) != POETX_OK) return st;
+  if ((st = check_rows("dX", dX, lddx, desc->vocab, desc->act_dtype)) != POETX_OK) return st;
+  if (!lse) return fail(POETX_E_NULL, "lse is NULL");
+  if ((target != nullptr) != (dlogp != nullptr)) return fail(POETX_E_NULL, "target and dlogp go together");
+  if (dentropy && !entropy) return fail(POETX_E_NULL, "dentropy needs the forward's entropy");
+  const uint64_t es = dt_size(desc->act_dtype), width = desc->vocab * es;
+  if (X == dX && ldx != lddx) return fail(POETX_E_SHAPE, "dX in place of X must have its pitch");
+  if (X != dX && share(Mat{X, (uint64_t)T, width, ldx * es}, Mat{dX, (uint64_t)T, width, lddx * es}))
+    return fail(POETX_E_SHAPE, "dX must be X or share no cell with it");
+  hipStream_t s = reinterpret_cast<hipStream_t>(stream);
+  PX_HIP(logp_bwd(desc->act_dtype, T, desc->vocab, desc->scale, X, ldx, target, lse, entropy, dlogp, dentropy, dX, lddx,
+                  s));
+  return POETX_OK;
+}
+
+}  // extern "C"

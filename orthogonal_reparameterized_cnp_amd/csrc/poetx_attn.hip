@@ -1,0 +1,541 @@
+// Attention of packed sequences and its backward (poetx_attn_fwd, poetx_attn_bwd).
+//
+// Every product runs on the 32 x 32 MFMA instructions, oriented so that a lane owns one query (forward, dQ) or one key
+// (dK, dV) in all of them.  An accumulator of these instructions holds, in lane l, column l % 32 at the rows
+//     row(e) = 8 (e / 4) + 4 (l / 32) + e % 4,   e < 16,
+// and the second operand of the next product wants 8 values of the summed index per lane, column l % 32.  A sum does
+// not mind the order of its terms: elements 8 c .. 8 c + 7 of the accumulator are used as they stand, and the first
+// operand's fragment is read for the same rows (16 c + 4 (l / 32) + {0 .. 3, 8 .. 11}).  So probabilities and score
+// gradients go from one product to the next without leaving their lane:
+//     forward   S^T = K Q^T       O^T += V^T P^T
+//     dQ        S^T = K Q^T,  dP^T = V dO^T       dQ^T += K^T G^T
+//     dK, dV    S = Q K^T,    dP = dO V^T         dV^T += dO^T P,  dK^T += Q^T G
+// and the softmax's maximum, sum and rescaling are a lane's own, with one exchange between the wave's halves.
+//
+// bf16 takes v_mfma_f32_32x32x16_bf16; fp32 takes eight v_mfma_f32_32x32x2_f32 for the same 16 terms, on the same
+// fragments, so that both types share the kernels.
+#include <algorithm>
+
+#include "common.h"
+#include "poetx_internal.h"
+
+namespace {
+
+using namespace pxk;
+
+constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr int kWaves = 4, kThreads = 64 * kWaves;
+constexpr int kRows = 32 * kWaves;  // rows of a workgroup: queries (forward, dQ) or keys (dK, dV), 32 a wave
+
+PX_DEV float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
+PX_DEV float other_half(float x) { return __shfl_xor(x, 32); }
+
+// ---- types -----------------------------------------------------------------
+typedef float f32x8_v __attribute__((ext_vector_type(8)));
+typedef short v4i16_t __attribute__((ext_vector_type(4)));
+template <typename T> struct FragOf;
+template <> struct FragOf<bf16_t> { typedef bf16x8_v type; };
+template <> struct FragOf<float> { typedef f32x8_v type; };
+template <typename T> using Frag = typename FragOf<T>::type;
+
+PX_DEV void mma(f32x16_v& acc, const bf16x8_v& a, const bf16x8_v& b) {
+  acc = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, acc, 0, 0, 0);
+}
+PX_DEV void mma(f32x16_v& acc, const f32x8_v& a, const f32x8_v& b) {
+#pragma unroll
+  for (int e = 0; e < 8; ++e) acc = __builtin_amdgcn_mfma_f32_32x32x2f32(a[e], b[e], acc, 0, 0, 0);
+}
+
+// elements 8 c .. 8 c + 7 of an accumulator as an operand
+template <typename T> PX_DEV Frag<T> to_frag(const f32x16_v& v, int c);
+template <> PX_DEV bf16x8_v to_frag<bf16_t>(const f32x16_v& v, int c) {
+  uint32_t w[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) w[i] = f2bf2(v[8 * c + 2 * i], v[8 * c + 2 * i + 1]);
+  bf16x8_v f;
+  __builtin_memcpy(&f, w, 16);
+  return f;
+}
+template <> PX_DEV f32x8_v to_frag<float>(const f32x16_v& v, int c) {
+  f32x8_v f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) f[i] = v[8 * c + i];
+  return f;
+}
+
+// row of accumulator element e
+PX_DEV int acc_row(int e, int lane) { return 8 * (e / 4) + 4 * (lane >> 5) + e % 4; }
+
+// ---- tiles of token rows in LDS --------------------------------------------
+// bf16: [rows][D] in 16-byte chunks, chunk c of row r at c ^ swz(r).  The two low bits of the row choose among the
+// 64-byte groups of a row (four of them for D = 128, two and the row's parity for D = 64), so that both the 16-byte
+// reads of 16 rows and the transposing reads of 4 rows x 64 bytes touch every bank once.
+// fp32: [rows][D + 4] (reads of 32 bytes from 16 rows touch every bank equally).
+template <typename T, int D> struct Rows;
+template <int D> struct Rows<bf16_t, D> {
+  static constexpr int CPR = D / 8;
+  static PX_DEV int chunk(int r, int c) {
+    const int x = D == 128 ? ((r & 3) << 2) | ((r >> 2) & 3) : (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+    return r * CPR + (c ^ x);
+  }
+  static constexpr int bytes(int rows) { return rows * D * 2; }
+  static PX_DEV void put(char* t, int r, int c, const bf16_t (&v)[8]) { __builtin_memcpy(t + 16 * chunk(r, c), v, 16); }
+  // columns 16 kk + 8 (lane / 32) .. + 7 of row r0 + lane % 32
+  static PX_DEV bf16x8_v along(const char* t, int r0, int kk, int lane) {
+    return *reinterpret_cast<const bf16x8_v*>(t + 16 * chunk(r0 + (lane & 31), 2 * kk + (lane >> 5)));
+  }
+  // column c0 + lane % 32 of rows r0 + 4 (lane / 32) + {0 .. 3, 8 .. 11}
+  static PX_DEV bf16x8_v across(const char* t, int r0, int c0, int lane) {
+    const int s = lane & 15, col = c0 + 16 * ((lane >> 4) & 1) + 4 * (s & 3);
+    v4i16_t p[2];
+#pragma unroll
+    for (int q = 0; q < 2; ++q) {
+      const char* a = t + 16 * chunk(r0 + 4 * (lane >> 5) + 8 * q + (s >> 2), col >> 3) + 2 * (col & 7);
+      p[q] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4i16_t*)(a));
+    }
+    bf16x8_v f;
+    __builtin_memcpy(&f, p, 16);
+    return f;
+  }
+};
+template <int D> struct Rows<float, D> {
+  static constexpr int P = D + 4;
+  static constexpr int bytes(int rows) { return rows * P * 4; }
+  static PX_DEV void put(char* t, int r, int c, const float (&v)[8]) {
+    float* p = reinterpret_cast<float*>(t) + r * P + 8 * c;
+    *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
+  }
+  static PX_DEV f32x8_v along(const char* t, int r0, int kk, int lane) {
+    const float* p = reinterpret_cast<const float*>(t) + (r0 + (lane & 31)) * P + 16 * kk + 8 * (lane >> 5);
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+    return f32x8_v{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
+  }
+  static PX_DEV f32x8_v across(const char* t, int r0, int c0, int lane) {
+    const float* p = reinterpret_cast<const float*>(t) + (r0 + 4 * (lane >> 5)) * P + c0 + (lane & 31);
+    f32x8_v f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = p[(i + (i & 4)) * P];
+    return f;
+  }
+};
+
+// 8 elements from column c of a head's row, zeros behind its end and for absent rows
+template <typename T> PX_DEV void load8(T (&v)[8], const T* row, bool there, int c, int hd) {
+  if (there && c + 8 <= hd) {
+    __builtin_memcpy(v, row + c, sizeof(v));
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) v[i] = there && c + i < hd ? row[c + i] : T(0);
+  }
+}
+// rows [r0, r0 + N) of a sequence's `n`, into an LDS tile
+template <typename T, int D, int N>
+PX_DEV void copy_rows(char* tile, const T* base, int64_t ld, int r0, int n, int hd) {
+  constexpr int C = D / 8;
+#pragma unroll
+  for (int i = 0; i < N * C / kThreads; ++i) {
+    const int x = i * kThreads + (int)threadIdx.x, r = x / C, c = x % C;
+    T v[8];
+    load8<T>(v, base + (int64_t)(r0 + r) * ld, r0 + r < n, 8 * c, hd);
+    Rows<T, D>::put(tile, r, c, v);
+  }
+}
+// the operand fragments of one row, held in registers
+template <typename T, int D>
+PX_DEV void row_frags(Frag<T> (&f)[D / 16], const T* row, bool there, int hd, int lane) {
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    T v[8];
+    load8<T>(v, row, there, 16 * kk + 8 * (lane >> 5), hd);
+    __builtin_memcpy(&f[kk], v, sizeof(v));
+  }
+}
+// a lane's accumulator column as row elements: 4 consecutive of them at a time
+template <typename T, int D>
+PX_DEV void store_row(T* row, const f32x16_v (&acc)[D / 32], float scale, int hd, int lane) {
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+    for (int g = 0; g < 4; ++g) {
+      const int c = 32 * d + 8 * g + 4 * (lane >> 5);
+      T v[4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) v[i] = from_f32<T>(acc[d][4 * g + i] * scale);
+      if (c + 4 <= hd) {
+        __builtin_memcpy(row + c, v, sizeof(v));
+      } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+          if (c + i < hd) row[c + i] = v[i];
+      }
+    }
+}
+
+// ---- sequences -------------------------------------------------------------
+struct Side {
+  const int32_t* cu;
+  int64_t rows;
+};
+struct AttnArgs {
+  const void *Q, *K, *V, *O, *dO;
+  int64_t ldq, ldk, ldv, ldo, lddo;
+  void *out, *out2;  // O; dQ; dK and dV
+  int64_t ldout, ldout2;
+  float *lse, *delta;
+  Side q, k;
+  int batch, heads, group, hd, window;
+  bool causal;
+  float scale;
+  int64_t slots;
+};
+// first row of sequence s (s = batch: behind the last), held within the rows whatever the offsets say
+PX_DEV int64_t first_row(const Side& x, int batch, int s) {
+  if (!x.cu) return x.rows / batch * s;
+  return min(max((int64_t)x.cu[s], (int64_t)0), x.rows);
+}
+struct Seq {
+  int64_t q0, k0;
+  int nq, nk;
+};
+PX_DEV Seq sequence(const AttnArgs& a, int s) {
+  Seq r;
+  r.q0 = first_row(a.q, a.batch, s);
+  r.k0 = first_row(a.k, a.batch, s);
+  r.nq = (int)max(first_row(a.q, a.batch, s + 1) - r.q0, (int64_t)0);
+  r.nk = (int)max(first_row(a.k, a.batch, s + 1) - r.k0, (int64_t)0);
+  return r;
+}
+// The sequence and the tile of `slot`: sequence s of rows [a, b) has the slots from a / R + s on, and the ones up to
+// b / R + s are enough for its ceil((b - a) / R) tiles.  So the host needs no length, and a workgroup no prefix sum.
+PX_DEV int find_seq(const Side& x, int batch, int64_t slot, int R, int* tile) {
+  int lo = 0, hi = batch;  // the last s < batch with first_row / R + s <= slot
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (first_row(x, batch, mid) / R + mid <= slot) lo = mid;
+    else hi = mid;
+  }
+  *tile = (int)(slot - (first_row(x, batch, lo) / R + lo));
+  return lo;
+}
+
+// The keys [lo, hi) that the query at `place` sees.
+struct Sees {
+  int lo, hi;
+};
+PX_DEV Sees keys_of(const AttnArgs& a, int place, int nk) {
+  Sees r;
+  r.lo = a.window ? max(place - a.window + 1, 0) : 0;
+  r.hi = a.causal ? min(place + 1, nk) : a.window ? (int)min((int64_t)place + a.window, (int64_t)nk) : nk;
+  return r;
+}
+// The places [lo, hi) of the queries that see key j, within [p0, p1).
+PX_DEV Sees places_of(const AttnArgs& a, int j, int p0, int p1) {
+  Sees r;
+  r.lo = a.causal ? max(j, p0) : a.window ? max(j - a.window + 1, p0) : p0;
+  r.hi = a.window ? (int)min((int64_t)j + a.window, (int64_t)p1) : p1;
+  return r;
+}
+
+// ---- forward ---------------------------------------------------------------
+template <typename T> constexpr int kTile = sizeof(T) == 2 ? 64 : 32;  // keys (queries for dK, dV) of an LDS tile
+
+template <typename T, int D> __global__ __launch_bounds__(kThreads) void k_attn_fwd(AttnArgs a) {
+  constexpr int KT = kTile<T>, NB = KT / 32;
+  typedef Rows<T, D> R;
+  __shared__ __align__(16) char lds[2 * R::bytes(KT)];
+  char *const tk = lds, *const tv = lds + R::bytes(KT);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int head = (int)(blockIdx.x % a.heads);
+  const int64_t slot = a.slots - 1 - blockIdx.x / a.heads;
+  int tile;
+  const Seq sq = sequence(a, find_seq(a.q, a.batch, slot, kRows, &tile));
+  const int w0 = tile * kRows;
+  if (tile < 0 || w0 >= sq.nq) return;
+  const int shift = sq.nk - sq.nq, i = w0 + 32 * wave + (lane & 31);  // this lane's query
+  const bool live = i < sq.nq;
+  const T* K = static_cast<const T*>(a.K) + sq.k0 * a.ldk + (int64_t)(head / a.group) * a.hd;
+  const T* V = static_cast<const T*>(a.V) + sq.k0 * a.ldv + (int64_t)(head / a.group) * a.hd;
+  Frag<T> q[D / 16];
+  row_frags<T, D>(q, static_cast<const T*>(a.Q) + (sq.q0 + i) * a.ldq + (int64_t)head * a.hd, live, a.hd, lane);
+  const Sees see = live ? keys_of(a, i + shift, sq.nk) : Sees{0, 0};
+  const int last = min(w0 + kRows, sq.nq) - 1;
+  const int j0 = keys_of(a, w0 + shift, sq.nk).lo / KT * KT, j1 = keys_of(a, last + shift, sq.nk).hi;
+  const float c = a.scale * kLog2e;
+  f32x16_v acc[D / 32] = {};
+  float m = -INFINITY, l = 0.f;
+  for (int j = j0; j < j1; j += KT) {
+    __syncthreads();
+    copy_rows<T, D, KT>(tk, K, a.ldk, j, sq.nk, a.hd);
+    copy_rows<T, D, KT>(tv, V, a.ldv, j, sq.nk, a.hd);
+    __syncthreads();
+    f32x16_v s[NB] = {};
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) mma(s[b], R::along(tk, 32 * b, kk, lane), q[kk]);
+    float top = -INFINITY;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int key = j + 32 * b + acc_row(e, lane);
+        s[b][e] = key >= see.lo && key < see.hi ? s[b][e] : -INFINITY;
+        top = fmaxf(top, s[b][e]);
+      }
+    top = fmaxf(top, other_half(top));
+    const float was = m;
+    m = fmaxf(m, top);
+    const float base = m == -INFINITY ? 0.f : m;  // no key so far
+    const float keep = exp2_of((was - base) * c);
+    l *= keep;
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d) acc[d] *= keep;
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        s[b][e] = exp2_of((s[b][e] - base) * c);
+        l += s[b][e];
+      }
+#pragma unroll
+    for (int b = 0; b < NB; ++b)
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const Frag<T> p = to_frag<T>(s[b], h);
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d) mma(acc[d], R::across(tv, 32 * b + 16 * h, 32 * d, lane), p);
+      }
+  }
+  if (!live) return;
+  l += other_half(l);
+  store_row<T, D>(static_cast<T*>(a.out) + (sq.q0 + i) * a.ldout + (int64_t)head * a.hd, acc, l == 0.f ? 0.f : 1.f / l,
+                  a.hd, lane);
+  if (lane < 32) a.lse[(int64_t)head * a.q.rows + sq.q0 + i] = l == 0.f ? -INFINITY : m * a.scale + kLn2 * log2f(l);
+}
+
+// ---- backward --------------------------------------------------------------
+// dQ of 128 queries of one head, and D = dO . O of them, which the second launch reads.
+template <typename T, int D> __global__ __launch_bounds__(kThreads) void k_attn_dq(AttnArgs a) {
+  constexpr int KT = kTile<T>, NB = KT / 32;
+  typedef Rows<T, D> R;
+  __shared__ __align__(16) char lds[2 * R::bytes(KT)];
+  char *const tk = lds, *const tv = lds + R::bytes(KT);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int head = (int)(blockIdx.x % a.heads);
+  const int64_t slot = a.slots - 1 - blockIdx.x / a.heads;
+  int tile;
+  const Seq sq = sequence(a, find_seq(a.q, a.batch, slot, kRows, &tile));
+  const int w0 = tile * kRows;
+  if (tile < 0 || w0 >= sq.nq) return;
+  const int shift = sq.nk - sq.nq, i = w0 + 32 * wave + (lane & 31);
+  const bool live = i < sq.nq;
+  const T* K = static_cast<const T*>(a.K) + sq.k0 * a.ldk + (int64_t)(head / a.group) * a.hd;
+  const T* V = static_cast<const T*>(a.V) + sq.k0 * a.ldv + (int64_t)(head / a.group) * a.hd;
+  Frag<T> q[D / 16], g[D / 16];
+  row_frags<T, D>(q, static_cast<const T*>(a.Q) + (sq.q0 + i) * a.ldq + (int64_t)head * a.hd, live, a.hd, lane);
+  float delta = 0.f;
+  {
+    Frag<T> o[D / 16];
+    row_frags<T, D>(g, static_cast<const T*>(a.dO) + (sq.q0 + i) * a.lddo + (int64_t)head * a.hd, live, a.hd, lane);
+    row_frags<T, D>(o, static_cast<const T*>(a.O) + (sq.q0 + i) * a.ldo + (int64_t)head * a.hd, live, a.hd, lane);
+#pragma unroll
+    for (int kk = 0; kk < D / 16; ++kk)
+#pragma unroll
+      for (int e = 0; e < 8; ++e) delta += (float)g[kk][e] * (float)o[kk][e];
+  }
+  delta += other_half(delta);
+  const int64_t at = (int64_t)head * a.q.rows + sq.q0 + i;
+  float lse = live ? a.lse[at] : -INFINITY;
+  if (live && lane < 32) a.delta[at] = delta;
+  const Sees see = live && lse != -INFINITY ? keys_of(a, i + shift, sq.nk) : Sees{0, 0};
+  const int last = min(w0 + kRows, sq.nq) - 1;
+  const int j0 = keys_of(a, w0 + shift, sq.nk).lo / KT * KT, j1 = keys_of(a, last + shift, sq.nk).hi;
+  f32x16_v acc[D / 32] = {};
+  for (int j = j0; j < j1; j += KT) {
+    __syncthreads();
+    copy_rows<T, D, KT>(tk, K, a.ldk, j, sq.nk, a.hd);
+    copy_rows<T, D, KT>(tv, V, a.ldv, j, sq.nk, a.hd);
+    __syncthreads();
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      f32x16_v s = {}, dp = {};
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        mma(s, R::along(tk, 32 * b, kk, lane), q[kk]);
+        mma(dp, R::along(tv, 32 * b, kk, lane), g[kk]);
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        const int key = j + 32 * b + acc_row(e, lane);
+        const float p = exp2_of((s[e] * a.scale - lse) * kLog2e) * (dp[e] - delta);
+        s[e] = key >= see.lo && key < see.hi ? p : 0.f;
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const Frag<T> p = to_frag<T>(s, h);
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d) mma(acc[d], R::across(tk, 32 * b + 16 * h, 32 * d, lane), p);
+      }
+    }
+  }
+  if (live)
+    store_row<T, D>(static_cast<T*>(a.out) + (sq.q0 + i) * a.ldout + (int64_t)head * a.hd, acc, a.scale, a.hd, lane);
+}
+
+// dK and dV of 128 keys of one key head: its query heads one after another, so that their sum has one order.
+template <typename T, int D> __global__ __launch_bounds__(kThreads) void k_attn_dkv(AttnArgs a) {
+  constexpr int QT = kTile<T>, NB = QT / 32;
+  typedef Rows<T, D> R;
+  __shared__ __align__(16) char lds[2 * R::bytes(QT)];
+  __shared__ float rows[2][QT];  // lse, D
+  char *const tq = lds, *const tg = lds + R::bytes(QT);
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int kv_heads = a.heads / a.group, head = (int)(blockIdx.x % kv_heads);
+  const int64_t slot = blockIdx.x / kv_heads;
+  int tile;
+  const Seq sq = sequence(a, find_seq(a.k, a.batch, slot, kRows, &tile));
+  const int w0 = tile * kRows;
+  if (tile < 0 || w0 >= sq.nk) return;
+  const int shift = sq.nk - sq.nq, j = w0 + 32 * wave + (lane & 31);  // this lane's key
+  const bool live = j < sq.nk;
+  Frag<T> k[D / 16], v[D / 16];
+  row_frags<T, D>(k, static_cast<const T*>(a.K) + (sq.k0 + j) * a.ldk + (int64_t)head * a.hd, live, a.hd, lane);
+  row_frags<T, D>(v, static_cast<const T*>(a.V) + (sq.k0 + j) * a.ldv + (int64_t)head * a.hd, live, a.hd, lane);
+  const Sees see = live ? places_of(a, j, shift, sq.nk) : Sees{0, 0};
+  const int last = min(w0 + kRows, sq.nk) - 1;
+  // queries [i0, i1) see some of these keys
+  const int i0 = max(places_of(a, w0, shift, sq.nk).lo - shift, 0) / QT * QT;
+  const int i1 = places_of(a, last, shift, sq.nk).hi - shift;
+  f32x16_v dk[D / 32] = {}, dv[D / 32] = {};
+  for (int h = head * a.group; h < (head + 1) * a.group; ++h) {
+    const T* Q = static_cast<const T*>(a.Q) + sq.q0 * a.ldq + (int64_t)h * a.hd;
+    const T* G = static_cast<const T*>(a.dO) + sq.q0 * a.lddo + (int64_t)h * a.hd;
+    const int64_t at = (int64_t)h * a.q.rows + sq.q0;
+    for (int i = i0; i < i1; i += QT) {
+      __syncthreads();
+      copy_rows<T, D, QT>(tq, Q, a.ldq, i, sq.nq, a.hd);
+      copy_rows<T, D, QT>(tg, G, a.lddo, i, sq.nq, a.hd);
+      if ((int)threadIdx.x < QT) {
+        const int r = i + (int)threadIdx.x;
+        // a query that sees nothing: p = 2^-infinity
+        const float x = r < sq.nq ? a.lse[at + r] : -INFINITY;
+        rows[0][threadIdx.x] = x == -INFINITY ? INFINITY : x;
+        rows[1][threadIdx.x] = r < sq.nq ? a.delta[at + r] : 0.f;
+      }
+      __syncthreads();
+#pragma unroll
+      for (int b = 0; b < NB; ++b) {
+        f32x16_v s = {}, dp = {};
+#pragma unroll
+        for (int kk = 0; kk < D / 16; ++kk) {
+          mma(s, R::along(tq, 32 * b, kk, lane), k[kk]);
+          mma(dp, R::along(tg, 32 * b, kk, lane), v[kk]);
+        }
+#pragma unroll
+        for (int e = 0; e < 16; ++e) {
+          const int r = 32 * b + acc_row(e, lane), place = i + r + shift;
+          const float p = exp2_of((s[e] * a.scale - rows[0][r]) * kLog2e);
+          const bool on = place >= see.lo && place < see.hi;
+          s[e] = on ? p : 0.f;
+          dp[e] = on ? p * (dp[e] - rows[1][r]) : 0.f;
+        }
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const Frag<T> p = to_frag<T>(s, x), g = to_frag<T>(dp, x);
+#pragma unroll
+          for (int d = 0; d < D / 32; ++d) {
+            mma(dv[d], R::across(tg, 32 * b + 16 * x, 32 * d, lane), p);
+            mma(dk[d], R::across(tq, 32 * b + 16 * x, 32 * d, lane), g);
+          }
+        }
+      }
+    }
+  }
+  if (!live) return;
+  store_row<T, D>(static_cast<T*>(a.out) + (sq.k0 + j) * a.ldout + (int64_t)head * a.hd, dk, a.scale, a.hd, lane);
+  store_row<T, D>(static_cast<T*>(a.out2) + (sq.k0 + j) * a.ldout2 + (int64_t)head * a.hd, dv, 1.f, a.hd, lane);
+}
+
+int64_t slots_of(int64_t rows, int batch) { return rows / kRows + batch; }
+
+AttnArgs args_of(const AttnDesc& d) {
+  AttnArgs a = {};
+  a.q = Side{d.cu_q, d.Tq};
+  a.k = Side{d.cu_k, d.Tk};
+  a.batch = d.batch;
+  a.heads = d.heads;
+  a.group = d.heads / d.kv_heads;
+  a.hd = d.hd;
+  a.window = d.window;
+  a.causal = d.causal;
+  a.scale = d.scale;
+  return a;
+}
+
+// f.operator()<T, D>() for the type and the head's tile width
+template <class F> void pick(const AttnDesc& d, F&& f) {
+  if (d.dt == BF16) {
+    if (d.hd <= 64) f(bf16_t(), std::integral_constant<int, 64>());
+    else f(bf16_t(), std::integral_constant<int, 128>());
+  } else {
+    if (d.hd <= 64) f(float(), std::integral_constant<int, 64>());
+    else f(float(), std::integral_constant<int, 128>());
+  }
+}
+
+}  // namespace
+
+namespace pxk {
+
+bool attn_fits(const AttnDesc& d) {
+  const double most = (double)((int64_t(1) << 31) - 1);
+  return (double)slots_of(d.Tq, d.batch) * d.heads <= most && (double)slots_of(d.Tk, d.batch) * d.kv_heads <= most;
+}
+
+size_t attn_fwd_ws_bytes(const AttnDesc& d) {
+  (void)d;
+  return 0;
+}
+size_t attn_bwd_ws_bytes(const AttnDesc& d) { return (size_t)d.heads * d.Tq * 4; }
+
+hipError_t attn_fwd(const AttnDesc& d, const AttnMat& Q, const AttnMat& K, const AttnMat& V, void* O, int64_t ldo,
+                    float* lse, void* ws, hipStream_t s) {
+  (void)ws;
+  if (d.Tq == 0) return hipSuccess;
+  AttnArgs a = args_of(d);
+  a.Q = Q.p, a.ldq = Q.ld, a.K = K.p, a.ldk = K.ld, a.V = V.p, a.ldv = V.ld;
+  a.out = O, a.ldout = ldo, a.lse = lse;
+  a.slots = slots_of(d.Tq, d.batch);
+  pick(d, [&](auto t, auto D) {
+    k_attn_fwd<decltype(t), decltype(D)::value><<<dim3((unsigned)(a.slots * d.heads)), kThreads, 0, s>>>(a);
+  });
+  return hipGetLastError();
+}
+
+hipError_t attn_bwd(const AttnDesc& d, const AttnMat& dO, const AttnMat& Q, const AttnMat& K, const AttnMat& V,
+                    const AttnMat& O, const float* lse, void* dQ, int64_t lddq, void* dK, int64_t lddk, void* dV,
+                    int64_t lddv, void* ws, hipStream_t s) {
+  AttnArgs a = args_of(d);
+  a.Q = Q.p, a.ldq = Q.ld, a.K = K.p, a.ldk = K.ld, a.V = V.p, a.ldv = V.ld, a.O = O.p, a.ldo = O.ld;
+  a.dO = dO.p, a.lddo = dO.ld;
+  a.lse = const_cast<float*>(lse), a.delta = static_cast<float*>(ws);
+  if (d.Tq > 0) {
+    a.out = dQ, a.ldout = lddq;
+    a.slots = slots_of(d.Tq, d.batch);
+    pick(d, [&](auto t, auto D) {
+      k_attn_dq<decltype(t), decltype(D)::value><<<dim3((unsigned)(a.slots * d.heads)), kThreads, 0, s>>>(a);
+    });
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  if (d.Tk == 0) return hipSuccess;
+  a.out = dK, a.ldout = lddk, a.out2 = dV, a.ldout2 = lddv;
+  a.slots = slots_of(d.Tk, d.batch);
+  pick(d, [&](auto t, auto D) {
+    k_attn_dkv<decltype(t), decltype(D)::value><<<dim3((unsigned)(a.slots * d.kv_heads)), kThreads, 0, s>>>(a);
+  });
+  return hipGetLastError();
+}
+
+}  // namespace pxk

@@ -199,4 +199,49 @@ size_t orth_ws_bytes(int count, int rows, int cols, int dt);
 hipError_t orthogonalize(int count, int rows, int cols, int dt, const void* G, int64_t ldg, int64_t sg, void* O,
                          int64_t ldo, int64_t so, const NsHyper& n, void* ws, hipStream_t s);
 
+// Rotary positions of `count` matrices (poetx_rope.hip); pos may be null.
+constexpr int kRopeSides = 8;
+struct RopeSide {
+  const void* X;
+  void* Y;
+  int64_t ldx, ldy;
+  int heads;
+};
+hipError_t rope(int dt, bool pairs, int64_t T, int hd, int rot, const int32_t* pos, const double* freqs,
+                float amplitude, bool inverse, int count, const RopeSide* sides, hipStream_t s);
+
+// Attention of packed sequences (poetx_attn.hip); cu_q and cu_k may be null.
+constexpr int kAttnMaxD = 128;
+struct AttnDesc {
+  int dt, heads, kv_heads, hd;
+  bool causal;
+  int window;
+  float scale;
+  int batch;
+  int64_t Tq, Tk;
+  const int32_t *cu_q, *cu_k;
+};
+struct AttnMat {
+  const void* p;
+  int64_t ld;
+};
+bool attn_fits(const AttnDesc& d);  // whether the grids of its launches stay within their limits
+size_t attn_fwd_ws_bytes(const AttnDesc& d);
+size_t attn_bwd_ws_bytes(const AttnDesc& d);
+hipError_t attn_fwd(const AttnDesc& d, const AttnMat& Q, const AttnMat& K, const AttnMat& V, void* O, int64_t ldo,
+                    float* lse, void* ws, hipStream_t s);
+hipError_t attn_bwd(const AttnDesc& d, const AttnMat& dO, const AttnMat& Q, const AttnMat& K, const AttnMat& V,
+                    const AttnMat& O, const float* lse, void* dQ, int64_t lddq, void* dK, int64_t lddk, void* dV,
+                    int64_t lddv, void* ws, hipStream_t s);
+
+// Log probabilities of given tokens (poetx_logp.hip).  logp, entropy, the targets and the gradients may be null.
+constexpr int kLogpTop = 64, kLogpMaxV = 1 << 20;
+size_t logp_ws_bytes(int dt, int64_t T, int V, int top);
+hipError_t logp_fwd(int dt, int64_t T, int V, int top, float scale, const void* X, int64_t ldx, const int32_t* target,
+                    float* logp, float* lse, float* entropy, int32_t* top_ids, float* top_logp, void* ws,
+                    hipStream_t s);
+hipError_t logp_bwd(int dt, int64_t T, int V, float scale, const void* X, int64_t ldx, const int32_t* target,
+                    const float* lse, const float* entropy, const float* dlogp, const float* dentropy, void* dX,
+                    int64_t lddx, hipStream_t s);
+
 }  // namespace pxk

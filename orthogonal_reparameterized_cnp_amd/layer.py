@@ -7,7 +7,7 @@ done by libpoetx kernels.
 from __future__ import annotations
 
 import contextlib
-from typing import Optional
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -916,3 +916,210 @@ class PoetxOrthogonalizer:
                                   self.hp, self.ws, self.ws.numel())
             _keep(self._made_on, self.ws)
         return out
+
+
+class PoetxRope:
+    """Rotary positions of query and key rows (poetx_rope): every head's first rot_dim elements turn by the angles of
+    the token's position.  `layout` "half" pairs element j with j + rot_dim / 2, "pairs" 2 j with 2 j + 1.  `scaling`
+    ("none", "linear", "base", "bands", "ramp") changes the frequencies for sequences `factor` times as long as the
+    `original` ones (see poetx_rope_scaling).  The backward is the inverse rotation; nothing is saved between them."""
+
+    def __init__(self, head_dim: int, rot_dim: Optional[int] = None, layout: str = "half", act: str = "bf16",
+                 base: float = 10000.0, scaling: str = "none", factor: float = 1.0, original: float = 0.0,
+                 low: float = 1.0, high: float = 4.0, device: str = "cuda"):
+        if layout not in B.ROPE_LAYOUTS:
+            raise ValueError(f"layout must be one of {sorted(B.ROPE_LAYOUTS)}")
+        if scaling not in B.ROPE_SCALINGS:
+            raise ValueError(f"scaling must be one of {sorted(B.ROPE_SCALINGS)}")
+        if act not in ("f32", "bf16"):
+            raise ValueError("act must be f32 or bf16")
+        self.head_dim, self.rot_dim = head_dim, head_dim if rot_dim is None else rot_dim
+        self.layout, self.act, self.device = layout, act, torch.device(device)
+        self.desc = B.rope_desc(self.head_dim, self.rot_dim, layout, act)
+        freqs, self.amplitude = B.poetx_rope_freqs(self.rot_dim, B.rope_params(base, scaling, factor, original, low, high))
+        self._made_on = _made_on(self.device)
+        self.freqs = torch.from_numpy(freqs).to(self.device)
+
+    def _turn(self, Xs, pos, Ys, inverse: bool, stream):
+        Xs = list(Xs)
+        Ys = [None] * len(Xs) if Ys is None else list(Ys)
+        if not Xs or len(Ys) != len(Xs):
+            raise ValueError("one or more matrices, and an output or None for each")
+        dt, dev, hd = _TORCH_DT[self.act], self.device, self.head_dim
+        for x in Xs:
+            if not isinstance(x, torch.Tensor) or x.dim() != 2 or x.shape[1] == 0 or x.shape[1] % hd:
+                raise ValueError("every matrix must be a 2-D tensor [T, heads * head_dim]")
+        T = Xs[0].shape[0]
+        if pos is not None:
+            _check(pos, "pos", (T,), torch.int32)
+            _check_device(dev, pos=pos)
+        cols = [x.shape[1] for x in Xs]
+        ldx = [_pitch(x, f"matrix {i}", T, n, dt, dev) for i, (x, n) in enumerate(zip(Xs, cols))]
+        ldy = [n if y is None else _pitch(y, f"output {i}", T, n, dt, dev) for i, (y, n) in enumerate(zip(Ys, cols))]
+        with _on(dev, stream):
+            Ys = [torch.empty(T, n, dtype=dt, device=dev) if y is None else y for y, n in zip(Ys, cols)]
+            B.poetx_rope(self.desc, T, pos, self.freqs, self.amplitude, inverse, Xs, ldx, [n // hd for n in cols], Ys, ldy)
+            _keep(self._made_on, self.freqs)
+        return Ys
+
+    def forward(self, Xs, pos: Optional[torch.Tensor] = None, Ys=None, stream=None):
+        """The rotated matrices [T, heads * head_dim] (each into its own of Ys, which may be the matrix itself, or a new
+        tensor).  pos: int32 [T]; None: row t is at position t."""
+        return self._turn(Xs, pos, Ys, False, stream)
+
+    def backward(self, dYs, pos: Optional[torch.Tensor] = None, dXs=None, stream=None):
+        """The gradients of the matrices from those of the rotated ones, at the forward's positions."""
+        return self._turn(dYs, pos, dXs, True, stream)
+
+
+class PoetxAttention:
+    """Attention of packed sequences (poetx_attn_fwd / poetx_attn_bwd) on token rows Q [Tq, heads * head_dim] and K, V
+    [Tk, kv_heads * head_dim].  forward keeps its operands, O and the row sums for the backward, which forms the
+    probabilities again: none of them may be overwritten before it.  The backward may run on another stream than the
+    forward, once that stream waits for the forward's.
+
+    cu_q, cu_k: int32 [sequences + 1], the first rows of the sequences (cu_k None: those of cu_q); or neither, and
+    `batch` equal sequences.  Rows that belong to no sequence are not written; a new tensor holds zeros there."""
+
+    def __init__(self, heads: int, kv_heads: int, head_dim: int, act: str = "bf16", causal: bool = True, window: int = 0,
+                 scale: Optional[float] = None, device: str = "cuda"):
+        if act not in ("f32", "bf16"):
+            raise ValueError("act must be f32 or bf16")
+        if heads < 1 or kv_heads < 1 or heads % kv_heads:
+            raise ValueError("kv_heads must divide heads")
+        if not 1 <= head_dim <= 128:
+            raise ValueError("head_dim must be in [1, 128]")
+        self.heads, self.kv_heads, self.head_dim, self.act = heads, kv_heads, head_dim, act
+        self.device = torch.device(device)
+        self.desc = B.attn_desc(heads, kv_heads, head_dim, act, causal, window, scale)
+        self.saved = None  # Q, K, V, O, lse, cu_q, cu_k, batch of the last forward
+        self._saved_on: Optional[int] = None
+
+    def _cu(self, cu, name: str):
+        if not isinstance(cu, torch.Tensor) or cu.dim() != 1 or cu.numel() < 2:
+            raise ValueError(f"{name} must be a 1-D tensor of the sequences' first rows and the last one's end")
+        _check(cu, name, tuple(cu.shape), torch.int32)
+        _check_device(self.device, **{name: cu})
+        return cu.numel() - 1
+
+    def forward(self, Q: torch.Tensor, K: torch.Tensor, V: torch.Tensor, cu_q: Optional[torch.Tensor] = None,
+                cu_k: Optional[torch.Tensor] = None, batch: int = 1, O: Optional[torch.Tensor] = None, stream=None):
+        for name, t in (("Q", Q), ("K", K)):
+            if not isinstance(t, torch.Tensor) or t.dim() != 2:
+                raise ValueError(f"{name} must be a 2-D tensor of token rows")
+        Tq, Tk, dt, dev = Q.shape[0], K.shape[0], _TORCH_DT[self.act], self.device
+        nq, nk = self.heads * self.head_dim, self.kv_heads * self.head_dim
+        ldq, ldk = _pitch(Q, "Q", Tq, nq, dt, dev), _pitch(K, "K", Tk, nk, dt, dev)
+        ldv = _pitch(V, "V", Tk, nk, dt, dev)
+        ldo = _pitch(O, "O", Tq, nq, dt, dev) if O is not None else nq
+        if cu_q is not None:
+            batch = self._cu(cu_q, "cu_q")
+            cu_k = cu_q if cu_k is None else cu_k
+            if self._cu(cu_k, "cu_k") != batch:
+                raise ValueError("cu_q and cu_k must have one entry per sequence and one more")
+        elif cu_k is not None:
+            raise ValueError("cu_k without cu_q")
+        with _on(dev, stream):
+            if O is None:
+                O = (torch.empty if cu_q is None else torch.zeros)(Tq, nq, dtype=dt, device=dev)
+            lse = torch.empty(self.heads, Tq, dtype=torch.float32, device=dev)
+            ws = torch.empty(B.poetx_attn_workspace_size(self.desc, batch, Tq, Tk, B.POETX_OP_FWD), dtype=torch.uint8,
+                             device=dev)
+            B.poetx_attn_fwd(self.desc, batch, Tq, Tk, cu_q, cu_k, Q, ldq, K, ldk, V, ldv, O, ldo, lse, ws, ws.numel())
+            self._saved_on = B._current_stream()
+        self.saved = (Q, K, V, O, lse, cu_q, cu_k, batch)
+        return O
+
+    def backward(self, dO: torch.Tensor, dQ: Optional[torch.Tensor] = None, dK: Optional[torch.Tensor] = None,
+                 dV: Optional[torch.Tensor] = None, stream=None):
+        """(dQ, dK, dV) for the operands of the last forward."""
+        if self.saved is None:
+            raise ValueError("backward before a forward: there is no saved state")
+        Q, K, V, O, lse, cu_q, cu_k, batch = self.saved
+        Tq, Tk, dt, dev = Q.shape[0], K.shape[0], _TORCH_DT[self.act], self.device
+        nq, nk = self.heads * self.head_dim, self.kv_heads * self.head_dim
+        ld = [_pitch(t, name, T, n, dt, dev) for t, name, T, n in
+              ((dO, "dO", Tq, nq), (Q, "Q", Tq, nq), (K, "K", Tk, nk), (V, "V", Tk, nk), (O, "O", Tq, nq))]
+        lddq = _pitch(dQ, "dQ", Tq, nq, dt, dev) if dQ is not None else nq
+        lddk = _pitch(dK, "dK", Tk, nk, dt, dev) if dK is not None else nk
+        lddv = _pitch(dV, "dV", Tk, nk, dt, dev) if dV is not None else nk
+        with _on(dev, stream):
+            new = torch.empty if cu_q is None else torch.zeros  # equal sequences hold every row
+            dQ = new(Tq, nq, dtype=dt, device=dev) if dQ is None else dQ
+            dK = new(Tk, nk, dtype=dt, device=dev) if dK is None else dK
+            dV = new(Tk, nk, dtype=dt, device=dev) if dV is None else dV
+            ws = torch.empty(B.poetx_attn_workspace_size(self.desc, batch, Tq, Tk, B.POETX_OP_BWD), dtype=torch.uint8,
+                             device=dev)
+            B.poetx_attn_bwd(self.desc, batch, Tq, Tk, cu_q, cu_k, dO, ld[0], Q, ld[1], K, ld[2], V, ld[3], O, ld[4], lse,
+                             dQ, lddq, dK, lddk, dV, lddv, ws, ws.numel())
+            _keep(self._saved_on, *[t for t in (Q, K, V, O, lse, cu_q, cu_k) if t is not None])
+        return dQ, dK, dV
+
+
+class LogProbs(NamedTuple):
+    logp: Optional[torch.Tensor]  # [T] fp32, 0 where the target asks for nothing
+    lse: torch.Tensor  # [T] fp32
+    entropy: torch.Tensor  # [T] fp32
+    top_ids: Optional[torch.Tensor]  # [T, top] int32
+    top_logp: Optional[torch.Tensor]  # [T, top] fp32
+
+
+class PoetxLogProb:
+    """Log probabilities of given tokens under rows of logits, with the rows' entropy and, with `top`, their most likely
+    tokens (poetx_logp_fwd), and the gradient of the logits (poetx_logp_bwd).  `scale` is the reciprocal temperature.
+    forward keeps the logits, the targets and the row sums for the backward."""
+
+    def __init__(self, vocab: int, act: str = "bf16", top: int = 0, scale: float = 1.0, device: str = "cuda"):
+        if act not in ("f32", "bf16"):
+            raise ValueError("act must be f32 or bf16")
+        if not 0 <= top <= min(64, vocab):
+            raise ValueError("top must be in [0, min(64, vocab)]")
+        self.vocab, self.act, self.top, self.scale = vocab, act, top, scale
+        self.device = torch.device(device)
+        self.desc = B.logp_desc(vocab, act, top, scale)
+        self.saved = None  # X, target, lse, entropy of the last forward
+        self._saved_on: Optional[int] = None
+
+    def forward(self, X: torch.Tensor, target: Optional[torch.Tensor] = None, stream=None) -> LogProbs:
+        """target: int32 [T]; a value outside 0 .. vocab - 1 asks for nothing."""
+        if not isinstance(X, torch.Tensor) or X.dim() != 2:
+            raise ValueError("X must be a 2-D tensor [T, vocab]")
+        T, dev = X.shape[0], self.device
+        ldx = _pitch(X, "X", T, self.vocab, _TORCH_DT[self.act], dev)
+        if target is not None:
+            _check(target, "target", (T,), torch.int32)
+            _check_device(dev, target=target)
+        with _on(dev, stream):
+            new = lambda *n, dtype=torch.float32: torch.empty(*n, dtype=dtype, device=dev)
+            out = LogProbs(None if target is None else new(T), new(T), new(T),
+                           new(T, self.top, dtype=torch.int32) if self.top else None,
+                           new(T, self.top) if self.top else None)
+            ws = new(B.poetx_logp_workspace_size(self.desc, T), dtype=torch.uint8)
+            B.poetx_logp_fwd(self.desc, T, X, ldx, target, out.logp, out.lse, out.entropy, out.top_ids, out.top_logp, ws,
+                             ws.numel())
+            self._saved_on = B._current_stream()
+        self.saved = (X, target, out.lse, out.entropy)
+        return out
+
+    def backward(self, dlogp: Optional[torch.Tensor] = None, dentropy: Optional[torch.Tensor] = None,
+                 dX: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
+        """The gradient of the last forward's logits, in dX (which may be the logits) or a new tensor."""
+        if self.saved is None:
+            raise ValueError("backward before a forward: there is no saved state")
+        X, target, lse, entropy = self.saved
+        T, dt, dev = X.shape[0], _TORCH_DT[self.act], self.device
+        if dlogp is not None and target is None:
+            raise ValueError("dlogp given, but the forward had no targets")
+        for name, t in (("dlogp", dlogp), ("dentropy", dentropy)):
+            if t is not None:
+                _check(t, name, (T,), torch.float32)
+        _check_device(dev, dlogp=dlogp, dentropy=dentropy)
+        ldx = _pitch(X, "X", T, self.vocab, dt, dev)
+        lddx = _pitch(dX, "dX", T, self.vocab, dt, dev) if dX is not None else self.vocab
+        with _on(dev, stream):
+            if dX is None:
+                dX = torch.empty(T, self.vocab, dtype=dt, device=dev)
+            B.poetx_logp_bwd(self.desc, T, X, ldx, None if dlogp is None else target, lse, entropy, dlogp, dentropy, dX,
+                             lddx)
+            _keep(self._saved_on, *[t for t in (X, target, lse, entropy) if t is not None])
+        return dX
