@@ -141,6 +141,28 @@ PX_DEV void copy_rows(char* tile, const T* base, int64_t ld, int r0, int n, int 
     Rows<T, D>::put(tile, r, c, v);
   }
 }
+// The same by direct global -> LDS copies, 16 bytes a lane, for heads that fill the tile (bf16, hd = D, rows aligned to
+// 16 bytes).  Rows behind the last repeat it; what is computed from them is masked.
+template <int D, int N> struct DmaRows {
+  static constexpr int C = D / 8, RPW = 64 / C, STEP = kWaves * RPW;  // rows of a wave's copy, of the workgroup's
+  const bf16_t* base;
+  int64_t ld;
+  int r, c, n;  // this lane's row and column in the workgroup's first copy
+  PX_DEV DmaRows(const bf16_t* base_, int64_t ld_, int n_) : base(base_), ld(ld_), n(n_) {
+    const int lane = threadIdx.x & 63;
+    r = ((int)threadIdx.x >> 6) * RPW + lane / C;
+    c = 8 * (Rows<bf16_t, D>::chunk(r, lane % C) - r * C);  // STEP is a multiple of the swizzle's period
+  }
+  PX_DEV void copy(char* tile, int r0) const {
+    static_assert(STEP % 16 == 0 && N % STEP == 0, "swizzle period");
+    char* t = tile + ((int)threadIdx.x >> 6) * 1024;
+#pragma unroll
+    for (int i = 0; i < N / STEP; ++i) {
+      const bf16_t* g = base + (int64_t)min(r0 + r + i * STEP, n - 1) * ld + c;
+      __builtin_amdgcn_global_load_lds(g, (__attribute__((address_space(3))) void*)(t + i * kWaves * 1024), 16, 0, 0);
+    }
+  }
+};
 // the operand fragments of one row, held in registers
 template <typename T, int D>
 PX_DEV void row_frags(Frag<T> (&f)[D / 16], const T* row, bool there, int hd, int lane) {
@@ -175,7 +197,7 @@ PX_DEV void store_row(T* row, const f32x16_v (&acc)[D / 32], float scale, int hd
 // ---- sequences -------------------------------------------------------------
 struct Side {
   const int32_t* cu;
-  int64_t rows;
+  int64_t rows, each;  // each: rows of a sequence where cu is null
 };
 struct AttnArgs {
   const void *Q, *K, *V, *O, *dO;
@@ -190,8 +212,8 @@ struct AttnArgs {
   int64_t slots;
 };
 // first row of sequence s (s = batch: behind the last), held within the rows whatever the offsets say
-PX_DEV int64_t first_row(const Side& x, int batch, int s) {
-  if (!x.cu) return x.rows / batch * s;
+PX_DEV int64_t first_row(const Side& x, int s) {
+  if (!x.cu) return x.each * s;
   return min(max((int64_t)x.cu[s], (int64_t)0), x.rows);
 }
 struct Seq {
@@ -200,23 +222,34 @@ struct Seq {
 };
 PX_DEV Seq sequence(const AttnArgs& a, int s) {
   Seq r;
-  r.q0 = first_row(a.q, a.batch, s);
-  r.k0 = first_row(a.k, a.batch, s);
-  r.nq = (int)max(first_row(a.q, a.batch, s + 1) - r.q0, (int64_t)0);
-  r.nk = (int)max(first_row(a.k, a.batch, s + 1) - r.k0, (int64_t)0);
+  r.q0 = first_row(a.q, s);
+  r.k0 = first_row(a.k, s);
+  r.nq = (int)max(first_row(a.q, s + 1) - r.q0, (int64_t)0);
+  r.nk = (int)max(first_row(a.k, s + 1) - r.k0, (int64_t)0);
   return r;
 }
 // The sequence and the tile of `slot`: sequence s of rows [a, b) has the slots from a / R + s on, and the ones up to
 // b / R + s are enough for its ceil((b - a) / R) tiles.  So the host needs no length, and a workgroup no prefix sum.
 PX_DEV int find_seq(const Side& x, int batch, int64_t slot, int R, int* tile) {
-  int lo = 0, hi = batch;  // the last s < batch with first_row / R + s <= slot
-  while (hi - lo > 1) {
-    const int mid = (lo + hi) / 2;
-    if (first_row(x, batch, mid) / R + mid <= slot) lo = mid;
-    else hi = mid;
+  const int lane = threadIdx.x & 63;
+  int lo = 0, n = batch;  // the last s of [lo, lo + n) with first_row / R + s <= slot, 64 candidates at a time
+  while (n > 1) {
+    const int step = (n + 63) / 64, s = lo + lane * step;
+    const bool at = lane * step < n && first_row(x, s) / R + s <= slot;
+    const int k = max((int)__popcll(__ballot(at)) - 1, 0);
+    lo += k * step;
+    n = min(step, n - k * step);
   }
-  *tile = (int)(slot - (first_row(x, batch, lo) / R + lo));
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  *tile = (int)(slot - (first_row(x, lo) / R + lo));
   return lo;
+}
+
+// The head of workgroup p of a tile's: the query heads of a key head are kv_heads apart, so that with the 8 or 16 key heads
+// of usual models they run on one XCD, whose L2 they read the keys from.
+PX_DEV int head_of(const AttnArgs& a, int p) {
+  const int kv_heads = a.heads / a.group;
+  return p % kv_heads * a.group + p / kv_heads;
 }
 
 // The keys [lo, hi) that the query at `place` sees.
@@ -240,13 +273,17 @@ PX_DEV Sees places_of(const AttnArgs& a, int j, int p0, int p1) {
 // ---- forward ---------------------------------------------------------------
 template <typename T> constexpr int kTile = sizeof(T) == 2 ? 64 : 32;  // keys (queries for dK, dV) of an LDS tile
 
-template <typename T, int D> __global__ __launch_bounds__(kThreads) void k_attn_fwd(AttnArgs a) {
-  constexpr int KT = kTile<T>, NB = KT / 32;
+// Softmax of one wave's queries over the tiles so far: maximum m (of the raw scores), sum l of this half's keys.  The
+// maximum is only taken over where it has grown by more than kSlack (in units of log2 p): until then p may reach
+// 2^kSlack, which costs no digits, and the accumulators need no rescaling.
+constexpr float kSlack = 8.f;
+
+template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DMA ? 2 : 1) void k_attn_fwd(AttnArgs a) {
+  constexpr int KT = kTile<T>, NB = KT / 32, BUFS = DMA ? 2 : 1;
   typedef Rows<T, D> R;
-  __shared__ __align__(16) char lds[2 * R::bytes(KT)];
-  char *const tk = lds, *const tv = lds + R::bytes(KT);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int head = (int)(blockIdx.x % a.heads);
+  __shared__ __align__(16) char lds[BUFS * 2 * R::bytes(KT)];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, hd = DMA ? D : a.hd;
+  const int head = head_of(a, blockIdx.x % a.heads);
   const int64_t slot = a.slots - 1 - blockIdx.x / a.heads;
   int tile;
   const Seq sq = sequence(a, find_seq(a.q, a.batch, slot, kRows, &tile));
@@ -254,48 +291,52 @@ template <typename T, int D> __global__ __launch_bounds__(kThreads) void k_attn_
   if (tile < 0 || w0 >= sq.nq) return;
   const int shift = sq.nk - sq.nq, i = w0 + 32 * wave + (lane & 31);  // this lane's query
   const bool live = i < sq.nq;
-  const T* K = static_cast<const T*>(a.K) + sq.k0 * a.ldk + (int64_t)(head / a.group) * a.hd;
-  const T* V = static_cast<const T*>(a.V) + sq.k0 * a.ldv + (int64_t)(head / a.group) * a.hd;
+  const T* K = static_cast<const T*>(a.K) + sq.k0 * a.ldk + (int64_t)(head / a.group) * hd;
+  const T* V = static_cast<const T*>(a.V) + sq.k0 * a.ldv + (int64_t)(head / a.group) * hd;
   Frag<T> q[D / 16];
-  row_frags<T, D>(q, static_cast<const T*>(a.Q) + (sq.q0 + i) * a.ldq + (int64_t)head * a.hd, live, a.hd, lane);
+  row_frags<T, D>(q, static_cast<const T*>(a.Q) + (sq.q0 + i) * a.ldq + (int64_t)head * hd, live, hd, lane);
   const Sees see = live ? keys_of(a, i + shift, sq.nk) : Sees{0, 0};
   const int last = min(w0 + kRows, sq.nq) - 1;
   const int j0 = keys_of(a, w0 + shift, sq.nk).lo / KT * KT, j1 = keys_of(a, last + shift, sq.nk).hi;
+  // the keys that every query of this wave sees
+  const int f = w0 + 32 * wave, g = f + 31;
+  const Sees all = g < sq.nq ? Sees{keys_of(a, g + shift, sq.nk).lo, keys_of(a, f + shift, sq.nk).hi} : Sees{0, 0};
   const float c = a.scale * kLog2e;
   f32x16_v acc[D / 32] = {};
   float m = -INFINITY, l = 0.f;
-  for (int j = j0; j < j1; j += KT) {
-    __syncthreads();
-    copy_rows<T, D, KT>(tk, K, a.ldk, j, sq.nk, a.hd);
-    copy_rows<T, D, KT>(tv, V, a.ldv, j, sq.nk, a.hd);
-    __syncthreads();
+  const auto step = [&](const char* tk, const char* tv, int j, auto masked) __attribute__((always_inline)) {
     f32x16_v s[NB] = {};
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
+    for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) mma(s[b], R::along(tk, 32 * b, kk, lane), q[kk]);
+      for (int b = 0; b < NB; ++b) mma(s[b], R::along(tk, 32 * b, kk, lane), q[kk]);
     float top = -INFINITY;
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        const int key = j + 32 * b + acc_row(e, lane);
-        s[b][e] = key >= see.lo && key < see.hi ? s[b][e] : -INFINITY;
+        if constexpr (decltype(masked)::value) {
+          const int key = j + 32 * b + acc_row(e, lane);
+          s[b][e] = key >= see.lo && key < see.hi ? s[b][e] : -INFINITY;
+        }
         top = fmaxf(top, s[b][e]);
       }
     top = fmaxf(top, other_half(top));
-    const float was = m;
-    m = fmaxf(m, top);
-    const float base = m == -INFINITY ? 0.f : m;  // no key so far
-    const float keep = exp2_of((was - base) * c);
-    l *= keep;
+    if (__any((top - m) * c > kSlack)) {  // a first key: top - m is infinite
+      const float was = m;
+      m = fmaxf(m, top);
+      const float keep = exp2_of((was - (m == -INFINITY ? 0.f : m)) * c);
+      l *= keep;
 #pragma unroll
-    for (int d = 0; d < D / 32; ++d) acc[d] *= keep;
+      for (int d = 0; d < D / 32; ++d) acc[d] *= keep;
+    }
+    const float base = m == -INFINITY ? 0.f : m;  // no key so far
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        s[b][e] = exp2_of((s[b][e] - base) * c);
+        // fp32 keeps the exact difference; bf16's p has fewer digits than one fma leaves
+        s[b][e] = sizeof(T) == 4 ? exp2_of((s[b][e] - base) * c) : exp2_of(fmaf(s[b][e], c, -base * c));
         l += s[b][e];
       }
 #pragma unroll
@@ -306,11 +347,44 @@ template <typename T, int D> __global__ __launch_bounds__(kThreads) void k_attn_
 #pragma unroll
         for (int d = 0; d < D / 32; ++d) mma(acc[d], R::across(tv, 32 * b + 16 * h, 32 * d, lane), p);
       }
+  };
+  const auto tile_at = [&](int x) { return lds + x * R::bytes(KT); };
+  const auto compute = [&](const char* tk, const char* tv, int j) __attribute__((always_inline)) {
+    if (j >= all.lo && j + KT <= all.hi) step(tk, tv, j, std::false_type());
+    else step(tk, tv, j, std::true_type());
+  };
+  if constexpr (DMA) {
+    if (j0 < j1) {
+      const DmaRows<D, KT> ck(K, a.ldk, sq.nk), cv(V, a.ldv, sq.nk);
+      ck.copy(tile_at(0), j0);
+      cv.copy(tile_at(1), j0);
+      for (int j = j0; j < j1; j += 2 * KT) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int at = j + x * KT;
+          if (at >= j1) break;
+          __syncthreads();  // this tile is there, and the other buffer is done with
+          if (at + KT < j1) {
+            ck.copy(tile_at(2 - 2 * x), at + KT);
+            cv.copy(tile_at(3 - 2 * x), at + KT);
+          }
+          compute(tile_at(2 * x), tile_at(2 * x + 1), at);
+        }
+      }
+    }
+  } else {
+    for (int j = j0; j < j1; j += KT) {
+      __syncthreads();
+      copy_rows<T, D, KT>(tile_at(0), K, a.ldk, j, sq.nk, hd);
+      copy_rows<T, D, KT>(tile_at(1), V, a.ldv, j, sq.nk, hd);
+      __syncthreads();
+      compute(tile_at(0), tile_at(1), j);
+    }
   }
   if (!live) return;
   l += other_half(l);
-  store_row<T, D>(static_cast<T*>(a.out) + (sq.q0 + i) * a.ldout + (int64_t)head * a.hd, acc, l == 0.f ? 0.f : 1.f / l,
-                  a.hd, lane);
+  store_row<T, D>(static_cast<T*>(a.out) + (sq.q0 + i) * a.ldout + (int64_t)head * hd, acc, l == 0.f ? 0.f : 1.f / l,
+                  hd, lane);
   if (lane < 32) a.lse[(int64_t)head * a.q.rows + sq.q0 + i] = l == 0.f ? -INFINITY : m * a.scale + kLn2 * log2f(l);
 }
 
@@ -322,7 +396,7 @@ template <typename T, int D> __global__ __launch_bounds__(kThreads) void k_attn_
   __shared__ __align__(16) char lds[2 * R::bytes(KT)];
   char *const tk = lds, *const tv = lds + R::bytes(KT);
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int head = (int)(blockIdx.x % a.heads);
+  const int head = head_of(a, blockIdx.x % a.heads);
   const int64_t slot = a.slots - 1 - blockIdx.x / a.heads;
   int tile;
   const Seq sq = sequence(a, find_seq(a.q, a.batch, slot, kRows, &tile));
@@ -461,8 +535,8 @@ int64_t slots_of(int64_t rows, int batch) { return rows / kRows + batch; }
 
 AttnArgs args_of(const AttnDesc& d) {
   AttnArgs a = {};
-  a.q = Side{d.cu_q, d.Tq};
-  a.k = Side{d.cu_k, d.Tk};
+  a.q = Side{d.cu_q, d.Tq, d.Tq / d.batch};
+  a.k = Side{d.cu_k, d.Tk, d.Tk / d.batch};
   a.batch = d.batch;
   a.heads = d.heads;
   a.group = d.heads / d.kv_heads;
@@ -483,6 +557,9 @@ template <class F> void pick(const AttnDesc& d, F&& f) {
     else f(float(), std::integral_constant<int, 128>());
   }
 }
+
+// whether rows can be copied 16 bytes at a time
+bool dma_rows(const AttnMat& m) { return reinterpret_cast<uintptr_t>(m.p) % 16 == 0 && m.ld % 8 == 0; }
 
 }  // namespace
 
@@ -507,8 +584,14 @@ hipError_t attn_fwd(const AttnDesc& d, const AttnMat& Q, const AttnMat& K, const
   a.Q = Q.p, a.ldq = Q.ld, a.K = K.p, a.ldk = K.ld, a.V = V.p, a.ldv = V.ld;
   a.out = O, a.ldout = ldo, a.lse = lse;
   a.slots = slots_of(d.Tq, d.batch);
+  const bool dma = d.dt == BF16 && (d.hd == 64 || d.hd == 128) && dma_rows(K) && dma_rows(V);
   pick(d, [&](auto t, auto D) {
-    k_attn_fwd<decltype(t), decltype(D)::value><<<dim3((unsigned)(a.slots * d.heads)), kThreads, 0, s>>>(a);
+    typedef decltype(t) T;
+    const dim3 grid((unsigned)(a.slots * d.heads));
+    if constexpr (sizeof(T) == 2) {
+      if (dma) return k_attn_fwd<T, decltype(D)::value, true><<<grid, kThreads, 0, s>>>(a);
+    }
+    k_attn_fwd<T, decltype(D)::value, false><<<grid, kThreads, 0, s>>>(a);
   });
   return hipGetLastError();
 }
