@@ -16,8 +16,7 @@
 // fragments, so that both types share the kernels.
 #include <algorithm>
 
-#include "common.h"
-#include "poetx_internal.h"
+#include "kernel_util.h"
 
 namespace {
 
@@ -204,7 +203,7 @@ struct AttnArgs {
   int64_t ldq, ldk, ldv, ldo, lddo;
   void *out, *out2;  // O; dQ; dK and dV
   int64_t ldout, ldout2;
-  float *lse, *delta;
+  float *lse, *rows;  // rows: the backward's lse and D of every query, [2][heads][Tq]
   Side q, k;
   int batch, heads, group, hd, window;
   bool causal;
@@ -270,6 +269,65 @@ PX_DEV Sees places_of(const AttnArgs& a, int j, int p0, int p1) {
   return r;
 }
 
+// What the 32 rows of a wave see together: some of them, and each of them.
+struct Span {
+  Sees some, each;
+  PX_DEV bool any(int lo, int hi) const { return lo < some.hi && hi > some.lo; }
+  PX_DEV bool all(int lo, int hi) const { return lo >= each.lo && hi <= each.hi; }
+};
+// Keys of the queries first .. first + 31.
+PX_DEV Span keys_of_wave(const AttnArgs& a, int first, const Seq& sq) {
+  const int shift = sq.nk - sq.nq, end = first + 31;
+  Span w = {{0, 0}, {0, 0}};
+  if (first < sq.nq)
+    w.some = Sees{keys_of(a, first + shift, sq.nk).lo, keys_of(a, min(end, sq.nq - 1) + shift, sq.nk).hi};
+  if (end < sq.nq) w.each = Sees{keys_of(a, end + shift, sq.nk).lo, keys_of(a, first + shift, sq.nk).hi};
+  return w;
+}
+
+// The slots in the order in which their workgroups start: the tiles of equal sequences side by side, the ones with the
+// most work first (of a causal sequence the last queries, or the first keys), so that the short ones fill the end.
+PX_DEV int64_t slot_of(const AttnArgs& a, int64_t n, bool last_first) {
+  const int64_t per = a.slots / a.batch, t = n / a.batch;
+  if (t < per) n = n % a.batch * per + t;
+  return last_first ? a.slots - 1 - n : n;
+}
+
+// f(K tile, V tile, first key) over the tiles of the keys [j0, j1), which are the same for the whole workgroup
+template <typename T, int D, bool DMA, int KT, class F>
+PX_DEV void over_tiles(char* lds, const T* K, int64_t ldk, const T* V, int64_t ldv, int n, int hd, int j0, int j1,
+                       const F& f) {
+  typedef Rows<T, D> R;
+  const auto at = [&](int x) { return lds + x * R::bytes(KT); };
+  if constexpr (DMA) {
+    if (j0 >= j1) return;
+    const DmaRows<D, KT> ck(K, ldk, n), cv(V, ldv, n);
+    ck.copy(at(0), j0);
+    cv.copy(at(1), j0);
+    for (int j = j0; j < j1; j += 2 * KT) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int now = j + x * KT;
+        if (now >= j1) break;
+        __syncthreads();  // this tile is there, and the other buffer is done with
+        if (now + KT < j1) {
+          ck.copy(at(2 - 2 * x), now + KT);
+          cv.copy(at(3 - 2 * x), now + KT);
+        }
+        f(at(2 * x), at(2 * x + 1), now);
+      }
+    }
+  } else {
+    for (int j = j0; j < j1; j += KT) {
+      __syncthreads();
+      copy_rows<T, D, KT>(at(0), K, ldk, j, n, hd);
+      copy_rows<T, D, KT>(at(1), V, ldv, j, n, hd);
+      __syncthreads();
+      f(at(0), at(1), j);
+    }
+  }
+}
+
 // ---- forward ---------------------------------------------------------------
 template <typename T> constexpr int kTile = sizeof(T) == 2 ? 64 : 32;  // keys (queries for dK, dV) of an LDS tile
 
@@ -284,9 +342,8 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
   __shared__ __align__(16) char lds[BUFS * 2 * R::bytes(KT)];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, hd = DMA ? D : a.hd;
   const int head = head_of(a, blockIdx.x % a.heads);
-  const int64_t slot = a.slots - 1 - blockIdx.x / a.heads;
   int tile;
-  const Seq sq = sequence(a, find_seq(a.q, a.batch, slot, kRows, &tile));
+  const Seq sq = sequence(a, find_seq(a.q, a.batch, slot_of(a, blockIdx.x / a.heads, true), kRows, &tile));
   const int w0 = tile * kRows;
   if (tile < 0 || w0 >= sq.nq) return;
   const int shift = sq.nk - sq.nq, i = w0 + 32 * wave + (lane & 31);  // this lane's query
@@ -298,9 +355,7 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
   const Sees see = live ? keys_of(a, i + shift, sq.nk) : Sees{0, 0};
   const int last = min(w0 + kRows, sq.nq) - 1;
   const int j0 = keys_of(a, w0 + shift, sq.nk).lo / KT * KT, j1 = keys_of(a, last + shift, sq.nk).hi;
-  // the keys that every query of this wave sees
-  const int f = w0 + 32 * wave, g = f + 31;
-  const Sees all = g < sq.nq ? Sees{keys_of(a, g + shift, sq.nk).lo, keys_of(a, f + shift, sq.nk).hi} : Sees{0, 0};
+  const Span w = keys_of_wave(a, w0 + 32 * wave, sq);
   const float c = a.scale * kLog2e;
   f32x16_v acc[D / 32] = {};
   float m = -INFINITY, l = 0.f;
@@ -348,39 +403,11 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
         for (int d = 0; d < D / 32; ++d) mma(acc[d], R::across(tv, 32 * b + 16 * h, 32 * d, lane), p);
       }
   };
-  const auto tile_at = [&](int x) { return lds + x * R::bytes(KT); };
-  const auto compute = [&](const char* tk, const char* tv, int j) __attribute__((always_inline)) {
-    if (j >= all.lo && j + KT <= all.hi) step(tk, tv, j, std::false_type());
-    else step(tk, tv, j, std::true_type());
-  };
-  if constexpr (DMA) {
-    if (j0 < j1) {
-      const DmaRows<D, KT> ck(K, a.ldk, sq.nk), cv(V, a.ldv, sq.nk);
-      ck.copy(tile_at(0), j0);
-      cv.copy(tile_at(1), j0);
-      for (int j = j0; j < j1; j += 2 * KT) {
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int at = j + x * KT;
-          if (at >= j1) break;
-          __syncthreads();  // this tile is there, and the other buffer is done with
-          if (at + KT < j1) {
-            ck.copy(tile_at(2 - 2 * x), at + KT);
-            cv.copy(tile_at(3 - 2 * x), at + KT);
-          }
-          compute(tile_at(2 * x), tile_at(2 * x + 1), at);
-        }
-      }
-    }
-  } else {
-    for (int j = j0; j < j1; j += KT) {
-      __syncthreads();
-      copy_rows<T, D, KT>(tile_at(0), K, a.ldk, j, sq.nk, hd);
-      copy_rows<T, D, KT>(tile_at(1), V, a.ldv, j, sq.nk, hd);
-      __syncthreads();
-      compute(tile_at(0), tile_at(1), j);
-    }
-  }
+  over_tiles<T, D, DMA, KT>(lds, K, a.ldk, V, a.ldv, sq.nk, hd, j0, j1,
+                            [&](const char* tk, const char* tv, int j) __attribute__((always_inline)) {
+                              if (w.all(j, j + KT)) step(tk, tv, j, std::false_type());
+                              else if (w.any(j, j + KT)) step(tk, tv, j, std::true_type());
+                            });
   if (!live) return;
   l += other_half(l);
   store_row<T, D>(static_cast<T*>(a.out) + (sq.q0 + i) * a.ldout + (int64_t)head * hd, acc, l == 0.f ? 0.f : 1.f / l,
@@ -389,30 +416,33 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
 }
 
 // ---- backward --------------------------------------------------------------
-// dQ of 128 queries of one head, and D = dO . O of them, which the second launch reads.
-template <typename T, int D> __global__ __launch_bounds__(kThreads) void k_attn_dq(AttnArgs a) {
-  constexpr int KT = kTile<T>, NB = KT / 32;
+// dQ of 128 queries of one head.  It also leaves, for the second launch, D = dO . O and the lse as its exponent takes it:
+// in units of log2 for bf16, +infinity for a query that sees nothing (p = 2^-infinity).
+template <typename T> PX_DEV float prob(float s, float lse, float scale, float c) {
+  // fp32 keeps the digits of a difference of logarithms; bf16's p has fewer than one fma leaves
+  return sizeof(T) == 4 ? exp2_of((s * scale - lse) * kLog2e) : exp2_of(fmaf(s, c, -lse));
+}
+template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DMA ? 2 : 1) void k_attn_dq(AttnArgs a) {
+  constexpr int KT = kTile<T>, NB = KT / 32, BUFS = DMA ? 2 : 1;
   typedef Rows<T, D> R;
-  __shared__ __align__(16) char lds[2 * R::bytes(KT)];
-  char *const tk = lds, *const tv = lds + R::bytes(KT);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  __shared__ __align__(16) char lds[BUFS * 2 * R::bytes(KT)];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, hd = DMA ? D : a.hd;
   const int head = head_of(a, blockIdx.x % a.heads);
-  const int64_t slot = a.slots - 1 - blockIdx.x / a.heads;
   int tile;
-  const Seq sq = sequence(a, find_seq(a.q, a.batch, slot, kRows, &tile));
+  const Seq sq = sequence(a, find_seq(a.q, a.batch, slot_of(a, blockIdx.x / a.heads, true), kRows, &tile));
   const int w0 = tile * kRows;
   if (tile < 0 || w0 >= sq.nq) return;
   const int shift = sq.nk - sq.nq, i = w0 + 32 * wave + (lane & 31);
   const bool live = i < sq.nq;
-  const T* K = static_cast<const T*>(a.K) + sq.k0 * a.ldk + (int64_t)(head / a.group) * a.hd;
-  const T* V = static_cast<const T*>(a.V) + sq.k0 * a.ldv + (int64_t)(head / a.group) * a.hd;
+  const T* K = static_cast<const T*>(a.K) + sq.k0 * a.ldk + (int64_t)(head / a.group) * hd;
+  const T* V = static_cast<const T*>(a.V) + sq.k0 * a.ldv + (int64_t)(head / a.group) * hd;
   Frag<T> q[D / 16], g[D / 16];
-  row_frags<T, D>(q, static_cast<const T*>(a.Q) + (sq.q0 + i) * a.ldq + (int64_t)head * a.hd, live, a.hd, lane);
+  row_frags<T, D>(q, static_cast<const T*>(a.Q) + (sq.q0 + i) * a.ldq + (int64_t)head * hd, live, hd, lane);
   float delta = 0.f;
   {
     Frag<T> o[D / 16];
-    row_frags<T, D>(g, static_cast<const T*>(a.dO) + (sq.q0 + i) * a.lddo + (int64_t)head * a.hd, live, a.hd, lane);
-    row_frags<T, D>(o, static_cast<const T*>(a.O) + (sq.q0 + i) * a.ldo + (int64_t)head * a.hd, live, a.hd, lane);
+    row_frags<T, D>(g, static_cast<const T*>(a.dO) + (sq.q0 + i) * a.lddo + (int64_t)head * hd, live, hd, lane);
+    row_frags<T, D>(o, static_cast<const T*>(a.O) + (sq.q0 + i) * a.ldo + (int64_t)head * hd, live, hd, lane);
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
@@ -421,16 +451,18 @@ template <typename T, int D> __global__ __launch_bounds__(kThreads) void k_attn_
   delta += other_half(delta);
   const int64_t at = (int64_t)head * a.q.rows + sq.q0 + i;
   float lse = live ? a.lse[at] : -INFINITY;
-  if (live && lane < 32) a.delta[at] = delta;
   const Sees see = live && lse != -INFINITY ? keys_of(a, i + shift, sq.nk) : Sees{0, 0};
+  lse = lse == -INFINITY ? INFINITY : sizeof(T) == 4 ? lse : lse * kLog2e;
+  if (live && lane < 32) {
+    a.rows[at] = lse;
+    a.rows[(int64_t)a.heads * a.q.rows + at] = delta;
+  }
+  const Span w = keys_of_wave(a, w0 + 32 * wave, sq);
   const int last = min(w0 + kRows, sq.nq) - 1;
   const int j0 = keys_of(a, w0 + shift, sq.nk).lo / KT * KT, j1 = keys_of(a, last + shift, sq.nk).hi;
+  const float c = a.scale * kLog2e;
   f32x16_v acc[D / 32] = {};
-  for (int j = j0; j < j1; j += KT) {
-    __syncthreads();
-    copy_rows<T, D, KT>(tk, K, a.ldk, j, sq.nk, a.hd);
-    copy_rows<T, D, KT>(tv, V, a.ldv, j, sq.nk, a.hd);
-    __syncthreads();
+  const auto step = [&](const char* tk, const char* tv, int j, auto masked) __attribute__((always_inline)) {
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       f32x16_v s = {}, dp = {};
@@ -441,9 +473,11 @@ template <typename T, int D> __global__ __launch_bounds__(kThreads) void k_attn_
       }
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        const int key = j + 32 * b + acc_row(e, lane);
-        const float p = exp2_of((s[e] * a.scale - lse) * kLog2e) * (dp[e] - delta);
-        s[e] = key >= see.lo && key < see.hi ? p : 0.f;
+        s[e] = prob<T>(s[e], lse, a.scale, c) * (dp[e] - delta);
+        if constexpr (decltype(masked)::value) {
+          const int key = j + 32 * b + acc_row(e, lane);
+          s[e] = key >= see.lo && key < see.hi ? s[e] : 0.f;
+        }
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -452,83 +486,133 @@ template <typename T, int D> __global__ __launch_bounds__(kThreads) void k_attn_
         for (int d = 0; d < D / 32; ++d) mma(acc[d], R::across(tk, 32 * b + 16 * h, 32 * d, lane), p);
       }
     }
-  }
+  };
+  over_tiles<T, D, DMA, KT>(lds, K, a.ldk, V, a.ldv, sq.nk, hd, j0, j1,
+                            [&](const char* tk, const char* tv, int j) __attribute__((always_inline)) {
+                              if (w.all(j, j + KT)) step(tk, tv, j, std::false_type());
+                              else if (w.any(j, j + KT)) step(tk, tv, j, std::true_type());
+                            });
   if (live)
-    store_row<T, D>(static_cast<T*>(a.out) + (sq.q0 + i) * a.ldout + (int64_t)head * a.hd, acc, a.scale, a.hd, lane);
+    store_row<T, D>(static_cast<T*>(a.out) + (sq.q0 + i) * a.ldout + (int64_t)head * hd, acc, a.scale, hd, lane);
 }
 
 // dK and dV of 128 keys of one key head: its query heads one after another, so that their sum has one order.
-template <typename T, int D> __global__ __launch_bounds__(kThreads) void k_attn_dkv(AttnArgs a) {
-  constexpr int QT = kTile<T>, NB = QT / 32;
+template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads) void k_attn_dkv(AttnArgs a) {
+  constexpr int QT = kTile<T>, NB = QT / 32, BUFS = DMA ? 2 : 1, PAIR = 2 * Rows<T, D>::bytes(QT) + 2 * QT * 4;
   typedef Rows<T, D> R;
-  __shared__ __align__(16) char lds[2 * R::bytes(QT)];
-  __shared__ float rows[2][QT];  // lse, D
-  char *const tq = lds, *const tg = lds + R::bytes(QT);
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  extern __shared__ __align__(16) char lds[];  // BUFS times: queries, dO, lse, D
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, hd = DMA ? D : a.hd;
   const int kv_heads = a.heads / a.group, head = (int)(blockIdx.x % kv_heads);
-  const int64_t slot = blockIdx.x / kv_heads;
   int tile;
-  const Seq sq = sequence(a, find_seq(a.k, a.batch, slot, kRows, &tile));
+  const Seq sq = sequence(a, find_seq(a.k, a.batch, slot_of(a, blockIdx.x / kv_heads, false), kRows, &tile));
   const int w0 = tile * kRows;
   if (tile < 0 || w0 >= sq.nk) return;
   const int shift = sq.nk - sq.nq, j = w0 + 32 * wave + (lane & 31);  // this lane's key
   const bool live = j < sq.nk;
   Frag<T> k[D / 16], v[D / 16];
-  row_frags<T, D>(k, static_cast<const T*>(a.K) + (sq.k0 + j) * a.ldk + (int64_t)head * a.hd, live, a.hd, lane);
-  row_frags<T, D>(v, static_cast<const T*>(a.V) + (sq.k0 + j) * a.ldv + (int64_t)head * a.hd, live, a.hd, lane);
+  row_frags<T, D>(k, static_cast<const T*>(a.K) + (sq.k0 + j) * a.ldk + (int64_t)head * hd, live, hd, lane);
+  row_frags<T, D>(v, static_cast<const T*>(a.V) + (sq.k0 + j) * a.ldv + (int64_t)head * hd, live, hd, lane);
   const Sees see = live ? places_of(a, j, shift, sq.nk) : Sees{0, 0};
+  // places that see some, and all, of this wave's keys
+  Span w = {{0, 0}, {0, 0}};
+  {
+    const int f = w0 + 32 * wave, g = f + 31;
+    if (f < sq.nk) w.some = Sees{places_of(a, f, shift, sq.nk).lo, places_of(a, min(g, sq.nk - 1), shift, sq.nk).hi};
+    if (g < sq.nk) w.each = Sees{places_of(a, g, shift, sq.nk).lo, places_of(a, f, shift, sq.nk).hi};
+  }
   const int last = min(w0 + kRows, sq.nk) - 1;
   // queries [i0, i1) see some of these keys
   const int i0 = max(places_of(a, w0, shift, sq.nk).lo - shift, 0) / QT * QT;
   const int i1 = places_of(a, last, shift, sq.nk).hi - shift;
+  const float c = a.scale * kLog2e;
   f32x16_v dk[D / 32] = {}, dv[D / 32] = {};
-  for (int h = head * a.group; h < (head + 1) * a.group; ++h) {
-    const T* Q = static_cast<const T*>(a.Q) + sq.q0 * a.ldq + (int64_t)h * a.hd;
-    const T* G = static_cast<const T*>(a.dO) + sq.q0 * a.lddo + (int64_t)h * a.hd;
-    const int64_t at = (int64_t)h * a.q.rows + sq.q0;
-    for (int i = i0; i < i1; i += QT) {
-      __syncthreads();
-      copy_rows<T, D, QT>(tq, Q, a.ldq, i, sq.nq, a.hd);
-      copy_rows<T, D, QT>(tg, G, a.lddo, i, sq.nq, a.hd);
-      if ((int)threadIdx.x < QT) {
-        const int r = i + (int)threadIdx.x;
-        // a query that sees nothing: p = 2^-infinity
-        const float x = r < sq.nq ? a.lse[at + r] : -INFINITY;
-        rows[0][threadIdx.x] = x == -INFINITY ? INFINITY : x;
-        rows[1][threadIdx.x] = r < sq.nq ? a.delta[at + r] : 0.f;
+  const auto step = [&](const char* t, int i, auto masked) __attribute__((always_inline)) {
+    const char *tq = t, *tg = t + R::bytes(QT);
+    const float* rows = reinterpret_cast<const float*>(t + 2 * R::bytes(QT));
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      f32x16_v s = {}, dp = {};
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) {
+        mma(s, R::along(tq, 32 * b, kk, lane), k[kk]);
+        mma(dp, R::along(tg, 32 * b, kk, lane), v[kk]);
       }
-      __syncthreads();
 #pragma unroll
-      for (int b = 0; b < NB; ++b) {
-        f32x16_v s = {}, dp = {};
-#pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
-          mma(s, R::along(tq, 32 * b, kk, lane), k[kk]);
-          mma(dp, R::along(tg, 32 * b, kk, lane), v[kk]);
-        }
-#pragma unroll
-        for (int e = 0; e < 16; ++e) {
-          const int r = 32 * b + acc_row(e, lane), place = i + r + shift;
-          const float p = exp2_of((s[e] * a.scale - rows[0][r]) * kLog2e);
+      for (int e = 0; e < 16; ++e) {
+        const int r = 32 * b + acc_row(e, lane), place = i + r + shift;
+        s[e] = prob<T>(s[e], rows[r], a.scale, c);
+        if constexpr (decltype(masked)::value) {
           const bool on = place >= see.lo && place < see.hi;
-          s[e] = on ? p : 0.f;
-          dp[e] = on ? p * (dp[e] - rows[1][r]) : 0.f;
+          s[e] = on ? s[e] : 0.f;
+          dp[e] = on ? s[e] * (dp[e] - rows[QT + r]) : 0.f;
+        } else {
+          dp[e] = s[e] * (dp[e] - rows[QT + r]);
         }
+      }
 #pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const Frag<T> p = to_frag<T>(s, x), g = to_frag<T>(dp, x);
+      for (int x = 0; x < 2; ++x) {
+        const Frag<T> p = to_frag<T>(s, x), g = to_frag<T>(dp, x);
 #pragma unroll
-          for (int d = 0; d < D / 32; ++d) {
-            mma(dv[d], R::across(tg, 32 * b + 16 * x, 32 * d, lane), p);
-            mma(dk[d], R::across(tq, 32 * b + 16 * x, 32 * d, lane), g);
-          }
+        for (int d = 0; d < D / 32; ++d) {
+          mma(dv[d], R::across(tg, 32 * b + 16 * x, 32 * d, lane), p);
+          mma(dk[d], R::across(tq, 32 * b + 16 * x, 32 * d, lane), g);
         }
       }
     }
+  };
+  const auto compute = [&](const char* t, int i) __attribute__((always_inline)) {
+    const int p = i + shift;
+    if (w.all(p, p + QT)) step(t, i, std::false_type());
+    else if (w.any(p, p + QT)) step(t, i, std::true_type());
+  };
+  const T* Q = static_cast<const T*>(a.Q) + sq.q0 * a.ldq;
+  const T* G = static_cast<const T*>(a.dO) + sq.q0 * a.lddo;
+  const int64_t at = sq.q0 + (int64_t)head * a.group * a.q.rows, more = (int64_t)a.heads * a.q.rows;
+  const int per = i1 > i0 ? (i1 - i0 + QT - 1) / QT : 0, count = per * a.group;  // tiles: heads x queries
+  if constexpr (DMA) {
+    const auto fetch = [&](char* t, int h, int i) __attribute__((always_inline)) {
+      const int64_t col = (int64_t)(head * a.group + h) * hd;
+      DmaRows<D, QT>(Q + col, a.ldq, sq.nq).copy(t, i);
+      DmaRows<D, QT>(G + col, a.lddo, sq.nq).copy(t + R::bytes(QT), i);
+      if (wave < 2) {  // 64 values each: wave 0 the lse, wave 1 D
+        const float* x = a.rows + at + wave * more + (int64_t)h * a.q.rows + min(i + lane, sq.nq - 1);
+        char* to = t + 2 * R::bytes(QT) + wave * QT * 4;
+        __builtin_amdgcn_global_load_lds(x, (__attribute__((address_space(3))) void*)to, 4, 0, 0);
+      }
+    };
+    int h = 0, i = i0;
+    if (count > 0) fetch(lds, 0, i0);
+    for (int n = 0; n < count; n += 2) {
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (n + x >= count) break;
+        __syncthreads();  // this tile is there, and the other buffer is done with
+        const int now = i;
+        i += QT;
+        if (i >= i1) i = i0, ++h;
+        if (n + x + 1 < count) fetch(lds + (1 - x) * PAIR, h, i);
+        compute(lds + x * PAIR, now);
+      }
+    }
+  } else {
+    float* rows = reinterpret_cast<float*>(lds + 2 * R::bytes(QT));
+    for (int n = 0; n < count; ++n) {
+      const int h = n / per, i = i0 + (n - h * per) * QT;
+      const int64_t col = (int64_t)(head * a.group + h) * hd;
+      __syncthreads();
+      copy_rows<T, D, QT>(lds, Q + col, a.ldq, i, sq.nq, hd);
+      copy_rows<T, D, QT>(lds + R::bytes(QT), G + col, a.lddo, i, sq.nq, hd);
+      if ((int)threadIdx.x < 2 * QT) {
+        const int which = (int)threadIdx.x / QT, r = i + (int)threadIdx.x % QT;
+        rows[threadIdx.x] = a.rows[at + which * more + (int64_t)h * a.q.rows + min(r, sq.nq - 1)];
+      }
+      __syncthreads();
+      compute(lds, i);
+    }
   }
   if (!live) return;
-  store_row<T, D>(static_cast<T*>(a.out) + (sq.k0 + j) * a.ldout + (int64_t)head * a.hd, dk, a.scale, a.hd, lane);
-  store_row<T, D>(static_cast<T*>(a.out2) + (sq.k0 + j) * a.ldout2 + (int64_t)head * a.hd, dv, 1.f, a.hd, lane);
+  store_row<T, D>(static_cast<T*>(a.out) + (sq.k0 + j) * a.ldout + (int64_t)head * hd, dk, a.scale, hd, lane);
+  store_row<T, D>(static_cast<T*>(a.out2) + (sq.k0 + j) * a.ldout2 + (int64_t)head * hd, dv, 1.f, hd, lane);
 }
 
 int64_t slots_of(int64_t rows, int batch) { return rows / kRows + batch; }
@@ -558,7 +642,8 @@ template <class F> void pick(const AttnDesc& d, F&& f) {
   }
 }
 
-// whether rows can be copied 16 bytes at a time
+// whether the direct-to-LDS copies take these heads, and these rows
+bool fills_tile(const AttnDesc& d) { return d.dt == BF16 && (d.hd == 64 || d.hd == 128); }
 bool dma_rows(const AttnMat& m) { return reinterpret_cast<uintptr_t>(m.p) % 16 == 0 && m.ld % 8 == 0; }
 
 }  // namespace
@@ -574,7 +659,7 @@ size_t attn_fwd_ws_bytes(const AttnDesc& d) {
   (void)d;
   return 0;
 }
-size_t attn_bwd_ws_bytes(const AttnDesc& d) { return (size_t)d.heads * d.Tq * 4; }
+size_t attn_bwd_ws_bytes(const AttnDesc& d) { return (size_t)d.heads * d.Tq * 8; }
 
 hipError_t attn_fwd(const AttnDesc& d, const AttnMat& Q, const AttnMat& K, const AttnMat& V, void* O, int64_t ldo,
                     float* lse, void* ws, hipStream_t s) {
@@ -584,7 +669,7 @@ hipError_t attn_fwd(const AttnDesc& d, const AttnMat& Q, const AttnMat& K, const
   a.Q = Q.p, a.ldq = Q.ld, a.K = K.p, a.ldk = K.ld, a.V = V.p, a.ldv = V.ld;
   a.out = O, a.ldout = ldo, a.lse = lse;
   a.slots = slots_of(d.Tq, d.batch);
-  const bool dma = d.dt == BF16 && (d.hd == 64 || d.hd == 128) && dma_rows(K) && dma_rows(V);
+  const bool dma = fills_tile(d) && dma_rows(K) && dma_rows(V);
   pick(d, [&](auto t, auto D) {
     typedef decltype(t) T;
     const dim3 grid((unsigned)(a.slots * d.heads));
@@ -599,15 +684,22 @@ hipError_t attn_fwd(const AttnDesc& d, const AttnMat& Q, const AttnMat& K, const
 hipError_t attn_bwd(const AttnDesc& d, const AttnMat& dO, const AttnMat& Q, const AttnMat& K, const AttnMat& V,
                     const AttnMat& O, const float* lse, void* dQ, int64_t lddq, void* dK, int64_t lddk, void* dV,
                     int64_t lddv, void* ws, hipStream_t s) {
+  const bool full = fills_tile(d);
   AttnArgs a = args_of(d);
   a.Q = Q.p, a.ldq = Q.ld, a.K = K.p, a.ldk = K.ld, a.V = V.p, a.ldv = V.ld, a.O = O.p, a.ldo = O.ld;
   a.dO = dO.p, a.lddo = dO.ld;
-  a.lse = const_cast<float*>(lse), a.delta = static_cast<float*>(ws);
+  a.lse = const_cast<float*>(lse), a.rows = static_cast<float*>(ws);
   if (d.Tq > 0) {
     a.out = dQ, a.ldout = lddq;
     a.slots = slots_of(d.Tq, d.batch);
     pick(d, [&](auto t, auto D) {
-      k_attn_dq<decltype(t), decltype(D)::value><<<dim3((unsigned)(a.slots * d.heads)), kThreads, 0, s>>>(a);
+      typedef decltype(t) T;
+      constexpr int W = decltype(D)::value;
+      const dim3 grid((unsigned)(a.slots * d.heads));
+      if constexpr (sizeof(T) == 2) {
+        if (full && dma_rows(K) && dma_rows(V)) return k_attn_dq<T, W, true><<<grid, kThreads, 0, s>>>(a);
+      }
+      k_attn_dq<T, W, false><<<grid, kThreads, 0, s>>>(a);
     });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -615,10 +707,21 @@ hipError_t attn_bwd(const AttnDesc& d, const AttnMat& dO, const AttnMat& Q, cons
   if (d.Tk == 0) return hipSuccess;
   a.out = dK, a.ldout = lddk, a.out2 = dV, a.ldout2 = lddv;
   a.slots = slots_of(d.Tk, d.batch);
+  hipError_t e = hipSuccess;
   pick(d, [&](auto t, auto D) {
-    k_attn_dkv<decltype(t), decltype(D)::value><<<dim3((unsigned)(a.slots * d.kv_heads)), kThreads, 0, s>>>(a);
+    typedef decltype(t) T;
+    constexpr int W = decltype(D)::value, QT = kTile<T>, lds = 2 * Rows<T, W>::bytes(QT) + 2 * QT * 4;
+    const dim3 grid((unsigned)(a.slots * d.kv_heads));
+    if constexpr (sizeof(T) == 2) {
+      if (full && dma_rows(Q) && dma_rows(dO)) {
+        e = px::lds_once<k_attn_dkv<T, W, true>>(2 * lds);
+        if (e == hipSuccess) k_attn_dkv<T, W, true><<<grid, kThreads, 2 * lds, s>>>(a);
+        return;
+      }
+    }
+    k_attn_dkv<T, W, false><<<grid, kThreads, lds, s>>>(a);
   });
-  return hipGetLastError();
+  return e != hipSuccess ? e : hipGetLastError();
 }
 
 }  // namespace pxk

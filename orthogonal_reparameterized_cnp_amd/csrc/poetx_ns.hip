@@ -1019,19 +1019,6 @@ inline int norm_parts(int64_t elems, int es) {
   return (int)std::max<int64_t>(1, std::min<int64_t>(1024, elems * es / (256 * 128)));
 }
 
-// allow_lds, once per kernel and GPU: a call makes about 20 launches
-template <auto K> hipError_t lds_once(int bytes) {
-  static std::atomic<uint64_t> done{0};
-  int dev = 0;
-  hipError_t e = hipGetDevice(&dev);
-  if (e != hipSuccess) return e;
-  const uint64_t bit = dev < 64 ? uint64_t(1) << dev : 0;
-  if (done.load(std::memory_order_relaxed) & bit) return hipSuccess;
-  e = allow_lds(K, bytes);
-  if (e == hipSuccess) done.fetch_or(bit, std::memory_order_relaxed);
-  return e;
-}
-
 inline float pow2_near(double x) { return (float)std::exp2(std::round(std::log2(x))); }
 
 }  // namespace
