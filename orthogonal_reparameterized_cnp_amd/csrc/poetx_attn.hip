@@ -27,7 +27,15 @@ constexpr int kWaves = 4, kThreads = 64 * kWaves;
 constexpr int kRows = 32 * kWaves;  // rows of a workgroup: queries (forward, dQ) or keys (dK, dV), 32 a wave
 
 PX_DEV float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
-PX_DEV float other_half(float x) { return __shfl_xor(x, 32); }
+// a wave's number, known to be the same in all its lanes
+PX_DEV int wave_id() { return __builtin_amdgcn_readfirstlane(threadIdx.x >> 6); }
+// f of the values of lanes l and l ^ 32
+template <class F> PX_DEV float both_halves(float x, const F& f) {
+  const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(x), __float_as_uint(x), false, false);
+  return f(__uint_as_float(r[0]), __uint_as_float(r[1]));
+}
+PX_DEV float sum_halves(float x) { return both_halves(x, [](float a, float b) { return a + b; }); }
+PX_DEV float max_halves(float x) { return both_halves(x, [](float a, float b) { return fmaxf(a, b); }); }
 
 // ---- types -----------------------------------------------------------------
 typedef float f32x8_v __attribute__((ext_vector_type(8)));
@@ -62,8 +70,8 @@ template <> PX_DEV f32x8_v to_frag<float>(const f32x16_v& v, int c) {
   return f;
 }
 
-// row of accumulator element e
-PX_DEV int acc_row(int e, int lane) { return 8 * (e / 4) + 4 * (lane >> 5) + e % 4; }
+// row of accumulator element e, in the half of lanes that begins with row 0 (the other's is 4 higher)
+constexpr int acc_row(int e) { return 8 * (e / 4) + e % 4; }
 
 // ---- tiles of token rows in LDS --------------------------------------------
 // bf16: [rows][D] in 16-byte chunks, chunk c of row r at c ^ swz(r).  The two low bits of the row choose among the
@@ -141,25 +149,34 @@ PX_DEV void copy_rows(char* tile, const T* base, int64_t ld, int r0, int n, int 
   }
 }
 // The same by direct global -> LDS copies, 16 bytes a lane, for heads that fill the tile (bf16, hd = D, rows aligned to
-// 16 bytes).  Rows behind the last repeat it; what is computed from them is masked.
+// 16 bytes, pitches of up to kDmaLd).  Rows behind the last repeat it; what is computed from them is masked.
+constexpr int64_t kDmaLd = 1 << 24;  // a tile's rows lie within 32 bits
 template <int D, int N> struct DmaRows {
   static constexpr int C = D / 8, RPW = 64 / C, STEP = kWaves * RPW;  // rows of a wave's copy, of the workgroup's
-  const bf16_t* base;
-  int64_t ld;
-  int r, c, n;  // this lane's row and column in the workgroup's first copy
-  PX_DEV DmaRows(const bf16_t* base_, int64_t ld_, int n_) : base(base_), ld(ld_), n(n_) {
+  int r, c;  // this lane's row in the workgroup's first copy, its column in bytes
+  PX_DEV DmaRows() {
     const int lane = threadIdx.x & 63;
-    r = ((int)threadIdx.x >> 6) * RPW + lane / C;
-    c = 8 * (Rows<bf16_t, D>::chunk(r, lane % C) - r * C);  // STEP is a multiple of the swizzle's period
+    r = wave_id() * RPW + lane / C;
+    c = 16 * (Rows<bf16_t, D>::chunk(r, lane % C) - r * C);  // STEP is a multiple of the swizzle's period
   }
-  PX_DEV void copy(char* tile, int r0) const {
+  // rows [r0, r0 + N) of the `n` at base
+  PX_DEV void copy(char* tile, const bf16_t* base, int64_t ld, int r0, int n) const {
     static_assert(STEP % 16 == 0 && N % STEP == 0, "swizzle period");
-    char* t = tile + ((int)threadIdx.x >> 6) * 1024;
+    char* t = tile + wave_id() * 1024;
+    const char* g = reinterpret_cast<const char*>(base + r0 * ld);
+    const int pitch = 2 * (int)ld, last = n - 1 - r0;
+    if (last >= N - 1) {
+      const uint32_t at = (uint32_t)(r * pitch + c);
 #pragma unroll
-    for (int i = 0; i < N / STEP; ++i) {
-      const bf16_t* g = base + (int64_t)min(r0 + r + i * STEP, n - 1) * ld + c;
-      __builtin_amdgcn_global_load_lds(g, (__attribute__((address_space(3))) void*)(t + i * kWaves * 1024), 16, 0, 0);
+      for (int i = 0; i < N / STEP; ++i) put(t + i * kWaves * 1024, g + (int64_t)i * STEP * pitch, at);
+    } else {
+#pragma unroll
+      for (int i = 0; i < N / STEP; ++i)
+        put(t + i * kWaves * 1024, g, (uint32_t)(min(r + i * STEP, last) * pitch + c));
     }
+  }
+  static PX_DEV void put(char* t, const char* base, uint32_t at) {
+    __builtin_amdgcn_global_load_lds(base + at, (__attribute__((address_space(3))) void*)t, 16, 0, 0);
   }
 };
 // the operand fragments of one row, held in registers
@@ -254,6 +271,12 @@ PX_DEV int head_of(const AttnArgs& a, int p) {
 // The keys [lo, hi) that the query at `place` sees.
 struct Sees {
   int lo, hi;
+  // the same relative to this lane's row 0 of a tile that begins at j, to compare constants with
+  PX_DEV Sees from(int j) const {
+    const int at = j + 4 * (((int)threadIdx.x >> 5) & 1);
+    return Sees{lo - at, hi - at};
+  }
+  PX_DEV bool has(int x) const { return x >= lo && x < hi; }
 };
 PX_DEV Sees keys_of(const AttnArgs& a, int place, int nk) {
   Sees r;
@@ -301,9 +324,9 @@ PX_DEV void over_tiles(char* lds, const T* K, int64_t ldk, const T* V, int64_t l
   const auto at = [&](int x) { return lds + x * R::bytes(KT); };
   if constexpr (DMA) {
     if (j0 >= j1) return;
-    const DmaRows<D, KT> ck(K, ldk, n), cv(V, ldv, n);
-    ck.copy(at(0), j0);
-    cv.copy(at(1), j0);
+    const DmaRows<D, KT> dma;
+    dma.copy(at(0), K, ldk, j0, n);
+    dma.copy(at(1), V, ldv, j0, n);
     for (int j = j0; j < j1; j += 2 * KT) {
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
@@ -311,8 +334,8 @@ PX_DEV void over_tiles(char* lds, const T* K, int64_t ldk, const T* V, int64_t l
         if (now >= j1) break;
         __syncthreads();  // this tile is there, and the other buffer is done with
         if (now + KT < j1) {
-          ck.copy(at(2 - 2 * x), now + KT);
-          cv.copy(at(3 - 2 * x), now + KT);
+          dma.copy(at(2 - 2 * x), K, ldk, now + KT, n);
+          dma.copy(at(3 - 2 * x), V, ldv, now + KT, n);
         }
         f(at(2 * x), at(2 * x + 1), now);
       }
@@ -340,7 +363,7 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
   constexpr int KT = kTile<T>, NB = KT / 32, BUFS = DMA ? 2 : 1;
   typedef Rows<T, D> R;
   __shared__ __align__(16) char lds[BUFS * 2 * R::bytes(KT)];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, hd = DMA ? D : a.hd;
+  const int lane = threadIdx.x & 63, wave = wave_id(), hd = DMA ? D : a.hd;
   const int head = head_of(a, blockIdx.x % a.heads);
   int tile;
   const Seq sq = sequence(a, find_seq(a.q, a.batch, slot_of(a, blockIdx.x / a.heads, true), kRows, &tile));
@@ -366,17 +389,15 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
 #pragma unroll
       for (int b = 0; b < NB; ++b) mma(s[b], R::along(tk, 32 * b, kk, lane), q[kk]);
     float top = -INFINITY;
+    const Sees on = see.from(j);
 #pragma unroll
     for (int b = 0; b < NB; ++b)
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
-        if constexpr (decltype(masked)::value) {
-          const int key = j + 32 * b + acc_row(e, lane);
-          s[b][e] = key >= see.lo && key < see.hi ? s[b][e] : -INFINITY;
-        }
+        if constexpr (decltype(masked)::value) s[b][e] = on.has(32 * b + acc_row(e)) ? s[b][e] : -INFINITY;
         top = fmaxf(top, s[b][e]);
       }
-    top = fmaxf(top, other_half(top));
+    top = max_halves(top);
     if (__any((top - m) * c > kSlack)) {  // a first key: top - m is infinite
       const float was = m;
       m = fmaxf(m, top);
@@ -409,7 +430,7 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
                               else if (w.any(j, j + KT)) step(tk, tv, j, std::true_type());
                             });
   if (!live) return;
-  l += other_half(l);
+  l = sum_halves(l);
   store_row<T, D>(static_cast<T*>(a.out) + (sq.q0 + i) * a.ldout + (int64_t)head * hd, acc, l == 0.f ? 0.f : 1.f / l,
                   hd, lane);
   if (lane < 32) a.lse[(int64_t)head * a.q.rows + sq.q0 + i] = l == 0.f ? -INFINITY : m * a.scale + kLn2 * log2f(l);
@@ -426,7 +447,7 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
   constexpr int KT = kTile<T>, NB = KT / 32, BUFS = DMA ? 2 : 1;
   typedef Rows<T, D> R;
   __shared__ __align__(16) char lds[BUFS * 2 * R::bytes(KT)];
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, hd = DMA ? D : a.hd;
+  const int lane = threadIdx.x & 63, wave = wave_id(), hd = DMA ? D : a.hd;
   const int head = head_of(a, blockIdx.x % a.heads);
   int tile;
   const Seq sq = sequence(a, find_seq(a.q, a.batch, slot_of(a, blockIdx.x / a.heads, true), kRows, &tile));
@@ -448,7 +469,7 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
 #pragma unroll
       for (int e = 0; e < 8; ++e) delta += (float)g[kk][e] * (float)o[kk][e];
   }
-  delta += other_half(delta);
+  delta = sum_halves(delta);
   const int64_t at = (int64_t)head * a.q.rows + sq.q0 + i;
   float lse = live ? a.lse[at] : -INFINITY;
   const Sees see = live && lse != -INFINITY ? keys_of(a, i + shift, sq.nk) : Sees{0, 0};
@@ -463,6 +484,7 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
   const float c = a.scale * kLog2e;
   f32x16_v acc[D / 32] = {};
   const auto step = [&](const char* tk, const char* tv, int j, auto masked) __attribute__((always_inline)) {
+    const Sees on = see.from(j);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       f32x16_v s = {}, dp = {};
@@ -474,10 +496,7 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
 #pragma unroll
       for (int e = 0; e < 16; ++e) {
         s[e] = prob<T>(s[e], lse, a.scale, c) * (dp[e] - delta);
-        if constexpr (decltype(masked)::value) {
-          const int key = j + 32 * b + acc_row(e, lane);
-          s[e] = key >= see.lo && key < see.hi ? s[e] : 0.f;
-        }
+        if constexpr (decltype(masked)::value) s[e] = on.has(32 * b + acc_row(e)) ? s[e] : 0.f;
       }
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
@@ -501,7 +520,7 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads) vo
   constexpr int QT = kTile<T>, NB = QT / 32, BUFS = DMA ? 2 : 1, PAIR = 2 * Rows<T, D>::bytes(QT) + 2 * QT * 4;
   typedef Rows<T, D> R;
   extern __shared__ __align__(16) char lds[];  // BUFS times: queries, dO, lse, D
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, hd = DMA ? D : a.hd;
+  const int lane = threadIdx.x & 63, wave = wave_id(), hd = DMA ? D : a.hd;
   const int kv_heads = a.heads / a.group, head = (int)(blockIdx.x % kv_heads);
   int tile;
   const Seq sq = sequence(a, find_seq(a.k, a.batch, slot_of(a, blockIdx.x / kv_heads, false), kRows, &tile));
@@ -528,7 +547,8 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads) vo
   f32x16_v dk[D / 32] = {}, dv[D / 32] = {};
   const auto step = [&](const char* t, int i, auto masked) __attribute__((always_inline)) {
     const char *tq = t, *tg = t + R::bytes(QT);
-    const float* rows = reinterpret_cast<const float*>(t + 2 * R::bytes(QT));
+    const float* rows = reinterpret_cast<const float*>(t + 2 * R::bytes(QT)) + 4 * (lane >> 5);
+    const Sees on = see.from(i + shift);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       f32x16_v s = {}, dp = {};
@@ -538,15 +558,20 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads) vo
         mma(dp, R::along(tg, 32 * b, kk, lane), v[kk]);
       }
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        const int r = 32 * b + acc_row(e, lane), place = i + r + shift;
-        s[e] = prob<T>(s[e], rows[r], a.scale, c);
-        if constexpr (decltype(masked)::value) {
-          const bool on = place >= see.lo && place < see.hi;
-          s[e] = on ? s[e] : 0.f;
-          dp[e] = on ? s[e] * (dp[e] - rows[QT + r]) : 0.f;
-        } else {
-          dp[e] = s[e] * (dp[e] - rows[QT + r]);
+      for (int u = 0; u < 4; ++u) {
+        const int r = 32 * b + acc_row(4 * u);  // four rows of a lane lie side by side
+        const float4 l4 = *reinterpret_cast<const float4*>(rows + r), d4 = *reinterpret_cast<const float4*>(rows + QT + r);
+        const float l[4] = {l4.x, l4.y, l4.z, l4.w}, dl[4] = {d4.x, d4.y, d4.z, d4.w};
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          const int e = 4 * u + x;
+          float p = prob<T>(s[e], l[x], a.scale, c), g = p * (dp[e] - dl[x]);
+          if constexpr (decltype(masked)::value) {
+            p = on.has(r + x) ? p : 0.f;
+            g = on.has(r + x) ? g : 0.f;
+          }
+          s[e] = p;
+          dp[e] = g;
         }
       }
 #pragma unroll
@@ -570,10 +595,11 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads) vo
   const int64_t at = sq.q0 + (int64_t)head * a.group * a.q.rows, more = (int64_t)a.heads * a.q.rows;
   const int per = i1 > i0 ? (i1 - i0 + QT - 1) / QT : 0, count = per * a.group;  // tiles: heads x queries
   if constexpr (DMA) {
+    const DmaRows<D, QT> dma;
     const auto fetch = [&](char* t, int h, int i) __attribute__((always_inline)) {
       const int64_t col = (int64_t)(head * a.group + h) * hd;
-      DmaRows<D, QT>(Q + col, a.ldq, sq.nq).copy(t, i);
-      DmaRows<D, QT>(G + col, a.lddo, sq.nq).copy(t + R::bytes(QT), i);
+      dma.copy(t, Q + col, a.ldq, i, sq.nq);
+      dma.copy(t + R::bytes(QT), G + col, a.lddo, i, sq.nq);
       if (wave < 2) {  // 64 values each: wave 0 the lse, wave 1 D
         const float* x = a.rows + at + wave * more + (int64_t)h * a.q.rows + min(i + lane, sq.nq - 1);
         char* to = t + 2 * R::bytes(QT) + wave * QT * 4;
@@ -644,7 +670,9 @@ template <class F> void pick(const AttnDesc& d, F&& f) {
 
 // whether the direct-to-LDS copies take these heads, and these rows
 bool fills_tile(const AttnDesc& d) { return d.dt == BF16 && (d.hd == 64 || d.hd == 128); }
-bool dma_rows(const AttnMat& m) { return reinterpret_cast<uintptr_t>(m.p) % 16 == 0 && m.ld % 8 == 0; }
+bool dma_rows(const AttnMat& m) {
+  return reinterpret_cast<uintptr_t>(m.p) % 16 == 0 && m.ld % 8 == 0 && m.ld <= kDmaLd;
+}
 
 }  // namespace
 
