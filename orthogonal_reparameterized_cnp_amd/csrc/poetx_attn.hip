@@ -78,26 +78,45 @@ constexpr int acc_row(int e) { return 8 * (e / 4) + e % 4; }
 // 64-byte groups of a row (four of them for D = 128, two and the row's parity for D = 64), so that both the 16-byte
 // reads of 16 rows and the transposing reads of 4 rows x 64 bytes touch every bank once.
 // fp32: [rows][D + 4] (reads of 32 bytes from 16 rows touch every bank equally).
+//
+// A lane reads at offsets that it keeps in two registers (Lane) and that every fragment changes by constants: bits of the
+// chunk by exclusive or, rows of 16 and tiles by an immediate.
+struct Lane {
+  int along, across;
+  PX_DEV Lane operator+(int bytes) const { return Lane{along + bytes, across + bytes}; }  // bytes: a multiple of 256
+  // the same to the compiler as if it changed here: the fragments' offsets are formed where they are used (an operation
+  // each) instead of being held in a register each over the whole loop
+  PX_DEV Lane here() const {
+    Lane l = *this;
+    asm volatile("" : "+v"(l.along), "+v"(l.across));
+    return l;
+  }
+};
 template <typename T, int D> struct Rows;
 template <int D> struct Rows<bf16_t, D> {
   static constexpr int CPR = D / 8;
-  static PX_DEV int chunk(int r, int c) {
-    const int x = D == 128 ? ((r & 3) << 2) | ((r >> 2) & 3) : (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
-    return r * CPR + (c ^ x);
+  static PX_DEV int swz(int r) {
+    return D == 128 ? ((r & 3) << 2) | ((r >> 2) & 3) : (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
   }
   static constexpr int bytes(int rows) { return rows * D * 2; }
-  static PX_DEV void put(char* t, int r, int c, const bf16_t (&v)[8]) { __builtin_memcpy(t + 16 * chunk(r, c), v, 16); }
+  static PX_DEV void put(char* t, int r, int c, const bf16_t (&v)[8]) {
+    __builtin_memcpy(t + 16 * (r * CPR + (c ^ swz(r))), v, 16);
+  }
+  static PX_DEV Lane lane_at() {
+    const int lane = threadIdx.x & 63, h = lane >> 5, r = lane & 31, s = lane & 15;
+    const int row = 4 * h + (s >> 2), chunk = 2 * ((lane >> 4) & 1) + ((s & 3) >> 1);
+    return Lane{2 * D * r + 16 * (h ^ swz(r)), 2 * D * row + 16 * (chunk ^ swz(row)) + 8 * (s & 1)};
+  }
   // columns 16 kk + 8 (lane / 32) .. + 7 of row r0 + lane % 32
-  static PX_DEV bf16x8_v along(const char* t, int r0, int kk, int lane) {
-    return *reinterpret_cast<const bf16x8_v*>(t + 16 * chunk(r0 + (lane & 31), 2 * kk + (lane >> 5)));
+  static PX_DEV bf16x8_v along(const char* t, const Lane& l, int r0, int kk) {
+    return *reinterpret_cast<const bf16x8_v*>(t + (l.along ^ (32 * kk)) + 2 * D * r0);
   }
   // column c0 + lane % 32 of rows r0 + 4 (lane / 32) + {0 .. 3, 8 .. 11}
-  static PX_DEV bf16x8_v across(const char* t, int r0, int c0, int lane) {
-    const int s = lane & 15, col = c0 + 16 * ((lane >> 4) & 1) + 4 * (s & 3);
+  static PX_DEV bf16x8_v across(const char* t, const Lane& l, int r0, int c0) {
     v4i16_t p[2];
 #pragma unroll
     for (int q = 0; q < 2; ++q) {
-      const char* a = t + 16 * chunk(r0 + 4 * (lane >> 5) + 8 * q + (s >> 2), col >> 3) + 2 * (col & 7);
+      const char* a = t + (l.across ^ (2 * c0) ^ (32 * q)) + 2 * D * (r0 + 8 * q);
       p[q] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4i16_t*)(a));
     }
     bf16x8_v f;
@@ -113,13 +132,17 @@ template <int D> struct Rows<float, D> {
     *reinterpret_cast<float4*>(p) = make_float4(v[0], v[1], v[2], v[3]);
     *reinterpret_cast<float4*>(p + 4) = make_float4(v[4], v[5], v[6], v[7]);
   }
-  static PX_DEV f32x8_v along(const char* t, int r0, int kk, int lane) {
-    const float* p = reinterpret_cast<const float*>(t) + (r0 + (lane & 31)) * P + 16 * kk + 8 * (lane >> 5);
-    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+  static PX_DEV Lane lane_at() {
+    const int lane = threadIdx.x & 63, h = lane >> 5, r = lane & 31;
+    return Lane{4 * (r * P + 8 * h), 4 * (4 * h * P + r)};
+  }
+  static PX_DEV f32x8_v along(const char* t, const Lane& l, int r0, int kk) {
+    const float4* p = reinterpret_cast<const float4*>(t + l.along + 4 * (r0 * P + 16 * kk));
+    const float4 a = p[0], b = p[1];
     return f32x8_v{a.x, a.y, a.z, a.w, b.x, b.y, b.z, b.w};
   }
-  static PX_DEV f32x8_v across(const char* t, int r0, int c0, int lane) {
-    const float* p = reinterpret_cast<const float*>(t) + (r0 + 4 * (lane >> 5)) * P + c0 + (lane & 31);
+  static PX_DEV f32x8_v across(const char* t, const Lane& l, int r0, int c0) {
+    const float* p = reinterpret_cast<const float*>(t + l.across + 4 * (r0 * P + c0));
     f32x8_v f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) f[i] = p[(i + (i & 4)) * P];
@@ -151,13 +174,13 @@ PX_DEV void copy_rows(char* tile, const T* base, int64_t ld, int r0, int n, int 
 // The same by direct global -> LDS copies, 16 bytes a lane, for heads that fill the tile (bf16, hd = D, rows aligned to
 // 16 bytes, pitches of up to kDmaLd).  Rows behind the last repeat it; what is computed from them is masked.
 constexpr int64_t kDmaLd = 1 << 24;  // a tile's rows lie within 32 bits
-template <int D, int N> struct DmaRows {
-  static constexpr int C = D / 8, RPW = 64 / C, STEP = kWaves * RPW;  // rows of a wave's copy, of the workgroup's
+template <int D, int N, int W> struct DmaRows {
+  static constexpr int C = D / 8, RPW = 64 / C, STEP = W * RPW;  // rows of a wave's copy, of the workgroup's
   int r, c;  // this lane's row in the workgroup's first copy, its column in bytes
   PX_DEV DmaRows() {
     const int lane = threadIdx.x & 63;
     r = wave_id() * RPW + lane / C;
-    c = 16 * (Rows<bf16_t, D>::chunk(r, lane % C) - r * C);  // STEP is a multiple of the swizzle's period
+    c = 16 * (lane % C ^ Rows<bf16_t, D>::swz(r));  // STEP is a multiple of the swizzle's period
   }
   // rows [r0, r0 + N) of the `n` at base
   PX_DEV void copy(char* tile, const bf16_t* base, int64_t ld, int r0, int n) const {
@@ -168,11 +191,11 @@ template <int D, int N> struct DmaRows {
     if (last >= N - 1) {
       const uint32_t at = (uint32_t)(r * pitch + c);
 #pragma unroll
-      for (int i = 0; i < N / STEP; ++i) put(t + i * kWaves * 1024, g + (int64_t)i * STEP * pitch, at);
+      for (int i = 0; i < N / STEP; ++i) put(t + i * W * 1024, g + (int64_t)i * STEP * pitch, at);
     } else {
 #pragma unroll
       for (int i = 0; i < N / STEP; ++i)
-        put(t + i * kWaves * 1024, g, (uint32_t)(min(r + i * STEP, last) * pitch + c));
+        put(t + i * W * 1024, g, (uint32_t)(min(r + i * STEP, last) * pitch + c));
     }
   }
   static PX_DEV void put(char* t, const char* base, uint32_t at) {
@@ -277,7 +300,16 @@ struct Sees {
     return Sees{lo - at, hi - at};
   }
   PX_DEV bool has(int x) const { return x >= lo && x < hi; }
+  // bit x: has(x), x < 32
+  PX_DEV uint32_t bits() const {
+    const auto below = [](int n) { return n <= 0 ? 0u : n >= 32 ? ~0u : (1u << n) - 1; };
+    return below(hi) & ~below(lo);
+  }
 };
+// x where bit n of `on` is set, else 0
+PX_DEV float where(uint32_t on, int n, float x) {
+  return __uint_as_float(__float_as_uint(x) & (uint32_t)__builtin_amdgcn_sbfe((int)on, n, 1));
+}
 PX_DEV Sees keys_of(const AttnArgs& a, int place, int nk) {
   Sees r;
   r.lo = a.window ? max(place - a.window + 1, 0) : 0;
@@ -316,7 +348,7 @@ PX_DEV int64_t slot_of(const AttnArgs& a, int64_t n, bool last_first) {
   return last_first ? a.slots - 1 - n : n;
 }
 
-// f(K tile, V tile, first key) over the tiles of the keys [j0, j1), which are the same for the whole workgroup
+// f(offset of the K tile, which the V tile follows, first key) over the tiles of the keys [j0, j1), which are the same for the whole workgroup
 template <typename T, int D, bool DMA, int KT, class F>
 PX_DEV void over_tiles(char* lds, const T* K, int64_t ldk, const T* V, int64_t ldv, int n, int hd, int j0, int j1,
                        const F& f) {
@@ -324,21 +356,16 @@ PX_DEV void over_tiles(char* lds, const T* K, int64_t ldk, const T* V, int64_t l
   const auto at = [&](int x) { return lds + x * R::bytes(KT); };
   if constexpr (DMA) {
     if (j0 >= j1) return;
-    const DmaRows<D, KT> dma;
+    const DmaRows<D, KT, kWaves> dma;
     dma.copy(at(0), K, ldk, j0, n);
     dma.copy(at(1), V, ldv, j0, n);
-    for (int j = j0; j < j1; j += 2 * KT) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const int now = j + x * KT;
-        if (now >= j1) break;
-        __syncthreads();  // this tile is there, and the other buffer is done with
-        if (now + KT < j1) {
-          dma.copy(at(2 - 2 * x), K, ldk, now + KT, n);
-          dma.copy(at(3 - 2 * x), V, ldv, now + KT, n);
-        }
-        f(at(2 * x), at(2 * x + 1), now);
+    for (int j = j0, x = 0; j < j1; j += KT, x ^= 2) {
+      __syncthreads();  // this tile is there, and the other buffer is done with
+      if (j + KT < j1) {
+        dma.copy(at(2 - x), K, ldk, j + KT, n);
+        dma.copy(at(3 - x), V, ldv, j + KT, n);
       }
+      f(x * R::bytes(KT), j);
     }
   } else {
     for (int j = j0; j < j1; j += KT) {
@@ -346,7 +373,7 @@ PX_DEV void over_tiles(char* lds, const T* K, int64_t ldk, const T* V, int64_t l
       copy_rows<T, D, KT>(at(0), K, ldk, j, n, hd);
       copy_rows<T, D, KT>(at(1), V, ldv, j, n, hd);
       __syncthreads();
-      f(at(0), at(1), j);
+      f(0, j);
     }
   }
 }
@@ -380,14 +407,17 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
   const int j0 = keys_of(a, w0 + shift, sq.nk).lo / KT * KT, j1 = keys_of(a, last + shift, sq.nk).hi;
   const Span w = keys_of_wave(a, w0 + 32 * wave, sq);
   const float c = a.scale * kLog2e;
+  const Lane lane_at = R::lane_at();
   f32x16_v acc[D / 32] = {};
   float m = -INFINITY, l = 0.f;
-  const auto step = [&](const char* tk, const char* tv, int j, auto masked) __attribute__((always_inline)) {
+  const auto step = [&](int tile, int j, auto masked) __attribute__((always_inline)) {
+    const Lane at = (lane_at + tile).here();
+    const char *const tk = lds, *const tv = lds + R::bytes(KT);
     f32x16_v s[NB] = {};
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk)
 #pragma unroll
-      for (int b = 0; b < NB; ++b) mma(s[b], R::along(tk, 32 * b, kk, lane), q[kk]);
+      for (int b = 0; b < NB; ++b) mma(s[b], R::along(tk, at, 32 * b, kk), q[kk]);
     float top = -INFINITY;
     const Sees on = see.from(j);
 #pragma unroll
@@ -421,13 +451,13 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
       for (int h = 0; h < 2; ++h) {
         const Frag<T> p = to_frag<T>(s[b], h);
 #pragma unroll
-        for (int d = 0; d < D / 32; ++d) mma(acc[d], R::across(tv, 32 * b + 16 * h, 32 * d, lane), p);
+        for (int d = 0; d < D / 32; ++d) mma(acc[d], R::across(tv, at, 32 * b + 16 * h, 32 * d), p);
       }
   };
   over_tiles<T, D, DMA, KT>(lds, K, a.ldk, V, a.ldv, sq.nk, hd, j0, j1,
-                            [&](const char* tk, const char* tv, int j) __attribute__((always_inline)) {
-                              if (w.all(j, j + KT)) step(tk, tv, j, std::false_type());
-                              else if (w.any(j, j + KT)) step(tk, tv, j, std::true_type());
+                            [&](int tile, int j) __attribute__((always_inline)) {
+                              if (w.all(j, j + KT)) step(tile, j, std::false_type());
+                              else if (w.any(j, j + KT)) step(tile, j, std::true_type());
                             });
   if (!live) return;
   l = sum_halves(l);
@@ -482,163 +512,240 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
   const int last = min(w0 + kRows, sq.nq) - 1;
   const int j0 = keys_of(a, w0 + shift, sq.nk).lo / KT * KT, j1 = keys_of(a, last + shift, sq.nk).hi;
   const float c = a.scale * kLog2e;
+  const Lane lane_at = R::lane_at();
   f32x16_v acc[D / 32] = {};
-  const auto step = [&](const char* tk, const char* tv, int j, auto masked) __attribute__((always_inline)) {
-    const Sees on = see.from(j);
+  const auto step = [&](int tile, int j) __attribute__((always_inline)) {
+    const Lane at = (lane_at + tile).here();
+    const char *const tk = lds, *const tv = lds + R::bytes(KT);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
+      const uint32_t on = see.from(j + 32 * b).bits();
       f32x16_v s = {}, dp = {};
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
-        mma(s, R::along(tk, 32 * b, kk, lane), q[kk]);
-        mma(dp, R::along(tv, 32 * b, kk, lane), g[kk]);
+        mma(s, R::along(tk, at, 32 * b, kk), q[kk]);
+        mma(dp, R::along(tv, at, 32 * b, kk), g[kk]);
       }
 #pragma unroll
-      for (int e = 0; e < 16; ++e) {
-        s[e] = prob<T>(s[e], lse, a.scale, c) * (dp[e] - delta);
-        if constexpr (decltype(masked)::value) s[e] = on.has(32 * b + acc_row(e)) ? s[e] : 0.f;
-      }
+      for (int e = 0; e < 16; ++e) s[e] = where(on, acc_row(e), prob<T>(s[e], lse, a.scale, c)) * (dp[e] - delta);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const Frag<T> p = to_frag<T>(s, h);
 #pragma unroll
-        for (int d = 0; d < D / 32; ++d) mma(acc[d], R::across(tk, 32 * b + 16 * h, 32 * d, lane), p);
+        for (int d = 0; d < D / 32; ++d) mma(acc[d], R::across(tk, at, 32 * b + 16 * h, 32 * d), p);
       }
     }
   };
-  over_tiles<T, D, DMA, KT>(lds, K, a.ldk, V, a.ldv, sq.nk, hd, j0, j1,
-                            [&](const char* tk, const char* tv, int j) __attribute__((always_inline)) {
-                              if (w.all(j, j + KT)) step(tk, tv, j, std::false_type());
-                              else if (w.any(j, j + KT)) step(tk, tv, j, std::true_type());
-                            });
+  over_tiles<T, D, DMA, KT>(lds, K, a.ldk, V, a.ldv, sq.nk, hd, j0, j1, [&](int tile, int j) __attribute__((always_inline)) {
+    if (w.any(j, j + KT)) step(tile, j);
+  });
   if (live)
     store_row<T, D>(static_cast<T*>(a.out) + (sq.q0 + i) * a.ldout + (int64_t)head * hd, acc, a.scale, hd, lane);
 }
 
-// dK and dV of 128 keys of one key head: its query heads one after another, so that their sum has one order.
-template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads) void k_attn_dkv(AttnArgs a) {
-  constexpr int QT = kTile<T>, NB = QT / 32, BUFS = DMA ? 2 : 1, PAIR = 2 * Rows<T, D>::bytes(QT) + 2 * QT * 4;
+// dK and dV of 128 keys of one key head: its query heads one after another, so that their sum has one order.  Of a block
+// of 32 queries (`tq`, `tg`: their rows and dO in LDS, `rows` and `deltas`: their lse and D), key(kk) and value(kk) are
+// the operands of the wave's keys.
+template <typename T, int D, class FK, class FV>
+PX_DEV void dkv_block(f32x16_v (&dk)[D / 32], f32x16_v (&dv)[D / 32], const char* tq, const char* tg, const Lane& at,
+                      const float* rows, const float* deltas, uint32_t on, float scale, float c, const FK& key,
+                      const FV& value) {
   typedef Rows<T, D> R;
-  extern __shared__ __align__(16) char lds[];  // BUFS times: queries, dO, lse, D
-  const int lane = threadIdx.x & 63, wave = wave_id(), hd = DMA ? D : a.hd;
-  const int kv_heads = a.heads / a.group, head = (int)(blockIdx.x % kv_heads);
+  f32x16_v s = {}, dp = {};
+#pragma unroll
+  for (int kk = 0; kk < D / 16; ++kk) {
+    mma(s, R::along(tq, at, 0, kk), key(kk));
+    mma(dp, R::along(tg, at, 0, kk), value(kk));
+  }
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    const int r = acc_row(4 * u);  // four rows of a lane lie side by side
+    const float4 l4 = *reinterpret_cast<const float4*>(rows + r), d4 = *reinterpret_cast<const float4*>(deltas + r);
+    const float l[4] = {l4.x, l4.y, l4.z, l4.w}, dl[4] = {d4.x, d4.y, d4.z, d4.w};
+#pragma unroll
+    for (int x = 0; x < 4; ++x) {
+      const int e = 4 * u + x;
+      s[e] = where(on, r + x, prob<T>(s[e], l[x], scale, c));
+      dp[e] = s[e] * (dp[e] - dl[x]);
+    }
+  }
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    const Frag<T> p = to_frag<T>(s, x), g = to_frag<T>(dp, x);
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d) {
+      mma(dv[d], R::across(tg, at, 16 * x, 32 * d), p);
+      mma(dk[d], R::across(tq, at, 16 * x, 32 * d), g);
+    }
+  }
+}
+
+// The keys of a workgroup, and the queries that see some of them.
+struct KeyTile {
+  Seq sq;
+  int head, w0, shift, i0, i1;
+  bool any;
+};
+PX_DEV KeyTile key_tile(const AttnArgs& a, int QT) {
+  KeyTile k;
+  const int kv_heads = a.heads / a.group;
+  k.head = (int)(blockIdx.x % kv_heads);
   int tile;
-  const Seq sq = sequence(a, find_seq(a.k, a.batch, slot_of(a, blockIdx.x / kv_heads, false), kRows, &tile));
-  const int w0 = tile * kRows;
-  if (tile < 0 || w0 >= sq.nk) return;
-  const int shift = sq.nk - sq.nq, j = w0 + 32 * wave + (lane & 31);  // this lane's key
+  k.sq = sequence(a, find_seq(a.k, a.batch, slot_of(a, blockIdx.x / kv_heads, false), kRows, &tile));
+  k.w0 = tile * kRows;
+  k.any = tile >= 0 && k.w0 < k.sq.nk;
+  k.shift = k.sq.nk - k.sq.nq;
+  const int last = min(k.w0 + kRows, k.sq.nk) - 1;
+  k.i0 = max(places_of(a, k.w0, k.shift, k.sq.nk).lo - k.shift, 0) / QT * QT;
+  k.i1 = places_of(a, last, k.shift, k.sq.nk).hi - k.shift;
+  return k;
+}
+// places that see some, and all, of the 32 keys from `first` on
+PX_DEV Span places_of_wave(const AttnArgs& a, int first, const KeyTile& k) {
+  const int end = first + 31, nk = k.sq.nk;
+  Span w = {{0, 0}, {0, 0}};
+  if (first < nk) w.some = Sees{places_of(a, first, k.shift, nk).lo, places_of(a, min(end, nk - 1), k.shift, nk).hi};
+  if (end < nk) w.each = Sees{places_of(a, end, k.shift, nk).lo, places_of(a, first, k.shift, nk).hi};
+  return w;
+}
+
+// Any type, head and alignment: 4 waves, which hold their keys and values in registers.
+template <typename T, int D> __global__ __launch_bounds__(kThreads) void k_attn_dkv(AttnArgs a) {
+  constexpr int QT = kTile<T>;
+  typedef Rows<T, D> R;
+  __shared__ __align__(16) char lds[2 * R::bytes(QT)];
+  __shared__ float rows[2][QT];  // lse, D
+  const int lane = threadIdx.x & 63, wave = wave_id();
+  const KeyTile t = key_tile(a, QT);
+  if (!t.any) return;
+  const Seq& sq = t.sq;
+  const int j = t.w0 + 32 * wave + (lane & 31);  // this lane's key
   const bool live = j < sq.nk;
   Frag<T> k[D / 16], v[D / 16];
-  row_frags<T, D>(k, static_cast<const T*>(a.K) + (sq.k0 + j) * a.ldk + (int64_t)head * hd, live, hd, lane);
-  row_frags<T, D>(v, static_cast<const T*>(a.V) + (sq.k0 + j) * a.ldv + (int64_t)head * hd, live, hd, lane);
-  const Sees see = live ? places_of(a, j, shift, sq.nk) : Sees{0, 0};
-  // places that see some, and all, of this wave's keys
-  Span w = {{0, 0}, {0, 0}};
-  {
-    const int f = w0 + 32 * wave, g = f + 31;
-    if (f < sq.nk) w.some = Sees{places_of(a, f, shift, sq.nk).lo, places_of(a, min(g, sq.nk - 1), shift, sq.nk).hi};
-    if (g < sq.nk) w.each = Sees{places_of(a, g, shift, sq.nk).lo, places_of(a, f, shift, sq.nk).hi};
-  }
-  const int last = min(w0 + kRows, sq.nk) - 1;
-  // queries [i0, i1) see some of these keys
-  const int i0 = max(places_of(a, w0, shift, sq.nk).lo - shift, 0) / QT * QT;
-  const int i1 = places_of(a, last, shift, sq.nk).hi - shift;
+  row_frags<T, D>(k, static_cast<const T*>(a.K) + (sq.k0 + j) * a.ldk + (int64_t)t.head * a.hd, live, a.hd, lane);
+  row_frags<T, D>(v, static_cast<const T*>(a.V) + (sq.k0 + j) * a.ldv + (int64_t)t.head * a.hd, live, a.hd, lane);
+  const Sees see = live ? places_of(a, j, t.shift, sq.nk) : Sees{0, 0};
+  const Span w = places_of_wave(a, t.w0 + 32 * wave, t);
   const float c = a.scale * kLog2e;
+  const Lane lane_at = R::lane_at();
   f32x16_v dk[D / 32] = {}, dv[D / 32] = {};
-  const auto step = [&](const char* t, int i, auto masked) __attribute__((always_inline)) {
-    const char *tq = t, *tg = t + R::bytes(QT);
-    const float* rows = reinterpret_cast<const float*>(t + 2 * R::bytes(QT)) + 4 * (lane >> 5);
-    const Sees on = see.from(i + shift);
-#pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      f32x16_v s = {}, dp = {};
-#pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        mma(s, R::along(tq, 32 * b, kk, lane), k[kk]);
-        mma(dp, R::along(tg, 32 * b, kk, lane), v[kk]);
-      }
-#pragma unroll
-      for (int u = 0; u < 4; ++u) {
-        const int r = 32 * b + acc_row(4 * u);  // four rows of a lane lie side by side
-        const float4 l4 = *reinterpret_cast<const float4*>(rows + r), d4 = *reinterpret_cast<const float4*>(rows + QT + r);
-        const float l[4] = {l4.x, l4.y, l4.z, l4.w}, dl[4] = {d4.x, d4.y, d4.z, d4.w};
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-          const int e = 4 * u + x;
-          float p = prob<T>(s[e], l[x], a.scale, c), g = p * (dp[e] - dl[x]);
-          if constexpr (decltype(masked)::value) {
-            p = on.has(r + x) ? p : 0.f;
-            g = on.has(r + x) ? g : 0.f;
-          }
-          s[e] = p;
-          dp[e] = g;
-        }
-      }
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        const Frag<T> p = to_frag<T>(s, x), g = to_frag<T>(dp, x);
-#pragma unroll
-        for (int d = 0; d < D / 32; ++d) {
-          mma(dv[d], R::across(tg, 32 * b + 16 * x, 32 * d, lane), p);
-          mma(dk[d], R::across(tq, 32 * b + 16 * x, 32 * d, lane), g);
-        }
-      }
-    }
-  };
-  const auto compute = [&](const char* t, int i) __attribute__((always_inline)) {
-    const int p = i + shift;
-    if (w.all(p, p + QT)) step(t, i, std::false_type());
-    else if (w.any(p, p + QT)) step(t, i, std::true_type());
-  };
-  const T* Q = static_cast<const T*>(a.Q) + sq.q0 * a.ldq;
-  const T* G = static_cast<const T*>(a.dO) + sq.q0 * a.lddo;
-  const int64_t at = sq.q0 + (int64_t)head * a.group * a.q.rows, more = (int64_t)a.heads * a.q.rows;
-  const int per = i1 > i0 ? (i1 - i0 + QT - 1) / QT : 0, count = per * a.group;  // tiles: heads x queries
-  if constexpr (DMA) {
-    const DmaRows<D, QT> dma;
-    const auto fetch = [&](char* t, int h, int i) __attribute__((always_inline)) {
-      const int64_t col = (int64_t)(head * a.group + h) * hd;
-      dma.copy(t, Q + col, a.ldq, i, sq.nq);
-      dma.copy(t + R::bytes(QT), G + col, a.lddo, i, sq.nq);
-      if (wave < 2) {  // 64 values each: wave 0 the lse, wave 1 D
-        const float* x = a.rows + at + wave * more + (int64_t)h * a.q.rows + min(i + lane, sq.nq - 1);
-        char* to = t + 2 * R::bytes(QT) + wave * QT * 4;
-        __builtin_amdgcn_global_load_lds(x, (__attribute__((address_space(3))) void*)to, 4, 0, 0);
-      }
-    };
-    int h = 0, i = i0;
-    if (count > 0) fetch(lds, 0, i0);
-    for (int n = 0; n < count; n += 2) {
-#pragma unroll
-      for (int x = 0; x < 2; ++x) {
-        if (n + x >= count) break;
-        __syncthreads();  // this tile is there, and the other buffer is done with
-        const int now = i;
-        i += QT;
-        if (i >= i1) i = i0, ++h;
-        if (n + x + 1 < count) fetch(lds + (1 - x) * PAIR, h, i);
-        compute(lds + x * PAIR, now);
-      }
-    }
-  } else {
-    float* rows = reinterpret_cast<float*>(lds + 2 * R::bytes(QT));
-    for (int n = 0; n < count; ++n) {
-      const int h = n / per, i = i0 + (n - h * per) * QT;
-      const int64_t col = (int64_t)(head * a.group + h) * hd;
+  const int64_t more = (int64_t)a.heads * a.q.rows;
+  for (int h = t.head * a.group; h < (t.head + 1) * a.group; ++h) {
+    const T* Q = static_cast<const T*>(a.Q) + sq.q0 * a.ldq + (int64_t)h * a.hd;
+    const T* G = static_cast<const T*>(a.dO) + sq.q0 * a.lddo + (int64_t)h * a.hd;
+    const float* x = a.rows + (int64_t)h * a.q.rows + sq.q0;
+    for (int i = t.i0; i < t.i1; i += QT) {
       __syncthreads();
-      copy_rows<T, D, QT>(lds, Q + col, a.ldq, i, sq.nq, hd);
-      copy_rows<T, D, QT>(lds + R::bytes(QT), G + col, a.lddo, i, sq.nq, hd);
+      copy_rows<T, D, QT>(lds, Q, a.ldq, i, sq.nq, a.hd);
+      copy_rows<T, D, QT>(lds + R::bytes(QT), G, a.lddo, i, sq.nq, a.hd);
       if ((int)threadIdx.x < 2 * QT) {
-        const int which = (int)threadIdx.x / QT, r = i + (int)threadIdx.x % QT;
-        rows[threadIdx.x] = a.rows[at + which * more + (int64_t)h * a.q.rows + min(r, sq.nq - 1)];
+        const int which = (int)threadIdx.x / QT, r = (int)threadIdx.x % QT;
+        rows[which][r] = x[which * more + min(i + r, sq.nq - 1)];
       }
       __syncthreads();
-      compute(lds, i);
+#pragma unroll
+      for (int b = 0; b < QT; b += 32) {
+        const int p = i + b + t.shift, r = b + 4 * (lane >> 5);
+        if (w.any(p, p + 32))
+          dkv_block<T, D>(dk, dv, lds, lds + R::bytes(QT), lane_at + R::bytes(b), rows[0] + r, rows[1] + r,
+                          see.from(p).bits(), a.scale, c, [&](int kk) { return k[kk]; }, [&](int kk) { return v[kk]; });
+      }
     }
   }
   if (!live) return;
-  store_row<T, D>(static_cast<T*>(a.out) + (sq.k0 + j) * a.ldout + (int64_t)head * hd, dk, a.scale, hd, lane);
-  store_row<T, D>(static_cast<T*>(a.out2) + (sq.k0 + j) * a.ldout2 + (int64_t)head * hd, dv, 1.f, hd, lane);
+  store_row<T, D>(static_cast<T*>(a.out) + (sq.k0 + j) * a.ldout + (int64_t)t.head * a.hd, dk, a.scale, a.hd, lane);
+  store_row<T, D>(static_cast<T*>(a.out2) + (sq.k0 + j) * a.ldout2 + (int64_t)t.head * a.hd, dv, 1.f, a.hd, lane);
+}
+
+// Heads that fill the tile, by direct copies.  The accumulators of 32 keys take 128 registers; with the keys and values
+// beside them a SIMD holds one wave, whose products and exponentials follow each other.  Here they stay in LDS, and 8
+// waves take the same 128 keys, four of them the first 32 queries of a tile of 64 and four the others: two waves a SIMD.
+// The halves' sums are added at the end, the first one's first.
+template <int D> struct Dkv {
+  static constexpr int W = 8, QT = 64;
+  static constexpr int KEYS = kRows * D * 2, TILE = QT * D * 2;
+  static constexpr int BUF = 2 * TILE + 2 * QT * 4;  // queries, dO, lse, D
+  static constexpr int EXCHANGE = W * 64 * (D / 32) * 16 * 4;
+  static constexpr int LDS = 2 * KEYS + 2 * BUF > EXCHANGE ? 2 * KEYS + 2 * BUF : EXCHANGE;
+};
+template <int D> __global__ __launch_bounds__(512, 2) void k_attn_dkv_dma(AttnArgs a) {
+  typedef bf16_t T;
+  typedef Rows<T, D> R;
+  typedef Dkv<D> C;
+  constexpr int QT = C::QT;
+  extern __shared__ __align__(16) char lds[];
+  char *const tk = lds, *const tv = lds + C::KEYS, *const bufs = lds + 2 * C::KEYS;
+  const int lane = threadIdx.x & 63, wave = wave_id(), keys = 32 * (wave & 3), half = wave >> 2;
+  const KeyTile t = key_tile(a, QT);
+  if (!t.any) return;
+  const Seq& sq = t.sq;
+  const int j = t.w0 + keys + (lane & 31);  // this lane's key
+  const bool live = j < sq.nk;
+  const Sees see = live ? places_of(a, j, t.shift, sq.nk) : Sees{0, 0};
+  const Span w = places_of_wave(a, t.w0 + keys, t);
+  const float c = a.scale * kLog2e;
+  f32x16_v dk[D / 32] = {}, dv[D / 32] = {};
+  const T* Q = static_cast<const T*>(a.Q) + sq.q0 * a.ldq;
+  const T* G = static_cast<const T*>(a.dO) + sq.q0 * a.lddo;
+  const int64_t at = sq.q0 + (int64_t)t.head * a.group * a.q.rows, more = (int64_t)a.heads * a.q.rows;
+  const int per = t.i1 > t.i0 ? (t.i1 - t.i0 + QT - 1) / QT : 0, count = per * a.group;  // tiles: heads x queries
+  const DmaRows<D, QT, C::W> dma;
+  const auto fetch = [&](char* b, int h, int i) __attribute__((always_inline)) {
+    const int64_t col = (int64_t)(t.head * a.group + h) * D;
+    dma.copy(b, Q + col, a.ldq, i, sq.nq);
+    dma.copy(b + C::TILE, G + col, a.lddo, i, sq.nq);
+    if (wave < 2) {  // 64 values each: wave 0 the lse, wave 1 D
+      const float* x = a.rows + at + wave * more + (int64_t)h * a.q.rows + min(i + lane, sq.nq - 1);
+      char* to = b + 2 * C::TILE + wave * QT * 4;
+      __builtin_amdgcn_global_load_lds(x, (__attribute__((address_space(3))) void*)to, 4, 0, 0);
+    }
+  };
+  const Lane lane_at = R::lane_at();
+  const auto compute = [&](int tile, int i) __attribute__((always_inline)) {
+    const int p = i + 32 * half + t.shift;
+    const float* rows = reinterpret_cast<const float*>(lds + tile + 2 * C::TILE) + 32 * half + 4 * (lane >> 5);
+    const Lane at = (lane_at + (tile + R::bytes(32 * half))).here(), keys_at = (lane_at + R::bytes(keys)).here();
+    if (w.any(p, p + 32))
+      dkv_block<T, D>(dk, dv, lds, lds + C::TILE, at, rows, rows + QT, see.from(p).bits(), a.scale, c,
+                      [&](int kk) { return R::along(tk, keys_at, 0, kk); },
+                      [&](int kk) { return R::along(tv, keys_at, 0, kk); });
+  };
+  if (count > 0) {
+    const DmaRows<D, kRows, C::W> whole;
+    whole.copy(tk, static_cast<const T*>(a.K) + sq.k0 * a.ldk + (int64_t)t.head * D, a.ldk, t.w0, sq.nk);
+    whole.copy(tv, static_cast<const T*>(a.V) + sq.k0 * a.ldv + (int64_t)t.head * D, a.ldv, t.w0, sq.nk);
+    fetch(bufs, 0, t.i0);
+  }
+  int h = 0, i = t.i0;
+  for (int n = 0, buf = 0; n < count; ++n, buf ^= C::BUF) {
+    __syncthreads();  // this tile is there, and the other buffer is done with
+    const int now = i;
+    i += QT;
+    if (i >= t.i1) i = t.i0, ++h;
+    if (n + 1 < count) fetch(bufs + (buf ^ C::BUF), h, i);
+    compute(2 * C::KEYS + buf, now);
+  }
+  // the waves of the first queries take the others' dK, those of the others the first ones' dV
+  __syncthreads();
+  float* mine = reinterpret_cast<float*>(lds) + wave * 64 * (D / 2) + lane;
+  const float* other = reinterpret_cast<const float*>(lds) + (wave ^ 4) * 64 * (D / 2) + lane;
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) mine[(16 * d + e) * 64] = half ? dk[d][e] : dv[d][e];
+  __syncthreads();
+#pragma unroll
+  for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+    for (int e = 0; e < 16; ++e) {
+      const float x = other[(16 * d + e) * 64];
+      dk[d][e] = half ? x + dv[d][e] : dk[d][e] + x;
+    }
+  if (!live) return;
+  if (half)
+    store_row<T, D>(static_cast<T*>(a.out2) + (sq.k0 + j) * a.ldout2 + (int64_t)t.head * D, dk, 1.f, D, lane);
+  else
+    store_row<T, D>(static_cast<T*>(a.out) + (sq.k0 + j) * a.ldout + (int64_t)t.head * D, dk, a.scale, D, lane);
 }
 
 int64_t slots_of(int64_t rows, int batch) { return rows / kRows + batch; }
@@ -738,16 +845,16 @@ hipError_t attn_bwd(const AttnDesc& d, const AttnMat& dO, const AttnMat& Q, cons
   hipError_t e = hipSuccess;
   pick(d, [&](auto t, auto D) {
     typedef decltype(t) T;
-    constexpr int W = decltype(D)::value, QT = kTile<T>, lds = 2 * Rows<T, W>::bytes(QT) + 2 * QT * 4;
+    constexpr int W = decltype(D)::value;
     const dim3 grid((unsigned)(a.slots * d.kv_heads));
     if constexpr (sizeof(T) == 2) {
-      if (full && dma_rows(Q) && dma_rows(dO)) {
-        e = px::lds_once<k_attn_dkv<T, W, true>>(2 * lds);
-        if (e == hipSuccess) k_attn_dkv<T, W, true><<<grid, kThreads, 2 * lds, s>>>(a);
+      if (full && dma_rows(Q) && dma_rows(dO) && dma_rows(K) && dma_rows(V)) {
+        e = px::lds_once<k_attn_dkv_dma<W>>(Dkv<W>::LDS);
+        if (e == hipSuccess) k_attn_dkv_dma<W><<<grid, 64 * Dkv<W>::W, Dkv<W>::LDS, s>>>(a);
         return;
       }
     }
-    k_attn_dkv<T, W, false><<<grid, kThreads, lds, s>>>(a);
+    k_attn_dkv<T, W><<<grid, kThreads, 0, s>>>(a);
   });
   return e != hipSuccess ? e : hipGetLastError();
 }

@@ -218,25 +218,23 @@ def test_nan_stays_in_its_sequence(act):
 @pytest.mark.parametrize("act", ["f32", "bf16"])
 @pytest.mark.parametrize("heads,kv,hd,offset,gap", [(4, 2, 64, 0, 0), (4, 2, 64, 1, 3), (2, 2, 128, 8, 8), (3, 1, 75, 1, 0)])
 def test_columns_of_one_buffer(act, heads, kv, hd, offset, gap):
-    """Q, K and V as columns of one buffer, their gradients as columns of another, at any pitch and element offset: the
-    results of separate matrices, and the cells around them as they were."""
+    """Q, K and V as columns of one buffer, their gradients as columns of another, at any pitch and element offset: within
+    the bounds, and the cells around them as they were."""
     T, n = 200, (heads + 2 * kv) * hd
     pitch = n + gap
     at = PoetxAttention(heads, kv, hd, act)
-    cu = dev(cu_of([64, 136]))
+    lens = cu_of([64, 136])
+    cu = dev(lens)
     buf = rows(T, n, act, 1, pitch, offset)
     cut = lambda m: (m[:, :heads * hd], m[:, heads * hd:(heads + kv) * hd], m[:, (heads + kv) * hd:])
-    dO = rows(T, heads * hd, act, 2)
-    ref = at.forward(*[x.contiguous() for x in cut(buf)], cu)
-    ref_g = at.backward(dO)
     whole = torch.full((offset + T * pitch + 8,), MARK, dtype=DT[act], device="cuda")
     grads = whole[offset:offset + T * pitch].view(T, pitch)
     out = rows(T, heads * hd, act, 3, heads * hd + gap, offset)
     at.forward(*cut(buf), cu, O=out)
-    at.backward(rows(T, heads * hd, act, 2, heads * hd + gap, offset), *cut(grads[:, :n]))
-    assert torch.equal(out, ref)
-    for g, r in zip(cut(grads[:, :n]), ref_g):
-        assert torch.equal(g, r)
+    dO = rows(T, heads * hd, act, 2, heads * hd + gap, offset)
+    at.backward(dO, *cut(grads[:, :n]))
+    c = O.Attn(heads, kv, hd, float(np.float32(at.desc.scale)))
+    check(at, c, act, cut(buf), dO, out, at.saved[4], cut(grads[:, :n]), lens, lens)
     assert (grads[:, n:] == MARK).all() and (whole[:offset] == MARK).all() and (whole[offset + T * pitch:] == MARK).all()
 
 
