@@ -175,27 +175,22 @@ PX_DEV void copy_rows(char* tile, const T* base, int64_t ld, int r0, int n, int 
 // 16 bytes, pitches of up to kDmaLd).  Rows behind the last repeat it; what is computed from them is masked.
 constexpr int64_t kDmaLd = 1 << 24;  // a tile's rows lie within 32 bits
 template <int D, int N, int W> struct DmaRows {
-  static constexpr int C = D / 8, RPW = 64 / C, STEP = W * RPW;  // rows of a wave's copy, of the workgroup's
-  int r, c;  // this lane's row in the workgroup's first copy, its column in bytes
-  PX_DEV DmaRows() {
-    const int lane = threadIdx.x & 63;
-    r = wave_id() * RPW + lane / C;
-    c = 16 * (lane % C ^ Rows<bf16_t, D>::swz(r));  // STEP is a multiple of the swizzle's period
-  }
-  // rows [r0, r0 + N) of the `n` at base
-  PX_DEV void copy(char* tile, const bf16_t* base, int64_t ld, int r0, int n) const {
-    static_assert(STEP % 16 == 0 && N % STEP == 0, "swizzle period");
-    char* t = tile + wave_id() * 1024;
+  static constexpr int C = D / 8, RPW = 64 / C, STEP = W * RPW;  // rows of a wave's copy, of the W waves'
+  int r, lane;  // this lane's row in the first copy
+  PX_DEV explicit DmaRows(int wave) : r(wave * RPW + ((int)threadIdx.x & 63) / C), lane((int)threadIdx.x & 63) {}
+  // rows [r0, r0 + N) of the `n` at base; `wave` as above
+  PX_DEV void copy(char* tile, const bf16_t* base, int64_t ld, int r0, int n, int wave) const {
+    static_assert(N % STEP == 0, "whole copies");
+    char* t = tile + wave * 1024;
     const char* g = reinterpret_cast<const char*>(base + r0 * ld);
     const int pitch = 2 * (int)ld, last = n - 1 - r0;
-    if (last >= N - 1) {
-      const uint32_t at = (uint32_t)(r * pitch + c);
 #pragma unroll
-      for (int i = 0; i < N / STEP; ++i) put(t + i * W * 1024, g + (int64_t)i * STEP * pitch, at);
-    } else {
-#pragma unroll
-      for (int i = 0; i < N / STEP; ++i)
-        put(t + i * W * 1024, g, (uint32_t)(min(r + i * STEP, last) * pitch + c));
+    for (int i = 0; i < N / STEP; ++i) {
+      const int row = r + i * STEP, c = 16 * (lane % C ^ Rows<bf16_t, D>::swz(row));
+      if (last >= N - 1)
+        put(t + i * W * 1024, g + (int64_t)i * STEP * pitch, (uint32_t)(r * pitch + c));
+      else
+        put(t + i * W * 1024, g, (uint32_t)(min(row, last) * pitch + c));
     }
   }
   static PX_DEV void put(char* t, const char* base, uint32_t at) {
@@ -243,12 +238,14 @@ struct AttnArgs {
   int64_t ldq, ldk, ldv, ldo, lddo;
   void *out, *out2;  // O; dQ; dK and dV
   int64_t ldout, ldout2;
-  float *lse, *rows;  // rows: the backward's lse and D of every query, [2][heads][Tq]
+  float *lse, *rows;  // rows: the backward's lse and D of every query, [2][heads][Tq]; the parts of few rows, pairs of
+                      // maximum and sum and from part_head on their O
   Side q, k;
   int batch, heads, group, hd, window;
+  int part;  // keys of a workgroup in the forward of few rows
   bool causal;
   float scale;
-  int64_t slots;
+  int64_t slots, part_head;
 };
 // first row of sequence s (s = batch: behind the last), held within the rows whatever the offsets say
 PX_DEV int64_t first_row(const Side& x, int s) {
@@ -270,17 +267,18 @@ PX_DEV Seq sequence(const AttnArgs& a, int s) {
 // The sequence and the tile of `slot`: sequence s of rows [a, b) has the slots from a / R + s on, and the ones up to
 // b / R + s are enough for its ceil((b - a) / R) tiles.  So the host needs no length, and a workgroup no prefix sum.
 PX_DEV int find_seq(const Side& x, int batch, int64_t slot, int R, int* tile) {
+  const auto begin = [&](int s) { return (int64_t)((uint32_t)first_row(x, s) / (uint32_t)R) + s; };
   const int lane = threadIdx.x & 63;
   int lo = 0, n = batch;  // the last s of [lo, lo + n) with first_row / R + s <= slot, 64 candidates at a time
   while (n > 1) {
     const int step = (n + 63) / 64, s = lo + lane * step;
-    const bool at = lane * step < n && first_row(x, s) / R + s <= slot;
+    const bool at = lane * step < n && begin(s) <= slot;
     const int k = max((int)__popcll(__ballot(at)) - 1, 0);
     lo += k * step;
     n = min(step, n - k * step);
   }
   lo = __builtin_amdgcn_readfirstlane(lo);
-  *tile = (int)(slot - (first_row(x, lo) / R + lo));
+  *tile = (int)(slot - begin(lo));
   return lo;
 }
 
@@ -330,13 +328,16 @@ struct Span {
   PX_DEV bool any(int lo, int hi) const { return lo < some.hi && hi > some.lo; }
   PX_DEV bool all(int lo, int hi) const { return lo >= each.lo && hi <= each.hi; }
 };
-// Keys of the queries first .. first + 31.
+// Keys of the queries first .. end, of which there are some.
+PX_DEV Span keys_of_rows(const AttnArgs& a, int first, int end, const Seq& sq) {
+  const Sees f = keys_of(a, first + sq.nk - sq.nq, sq.nk), e = keys_of(a, end + sq.nk - sq.nq, sq.nk);
+  return Span{{f.lo, e.hi}, {e.lo, f.hi}};
+}
+// Keys of the queries first .. first + 31 of a wave; no key for all of them where some do not exist.
 PX_DEV Span keys_of_wave(const AttnArgs& a, int first, const Seq& sq) {
-  const int shift = sq.nk - sq.nq, end = first + 31;
-  Span w = {{0, 0}, {0, 0}};
-  if (first < sq.nq)
-    w.some = Sees{keys_of(a, first + shift, sq.nk).lo, keys_of(a, min(end, sq.nq - 1) + shift, sq.nk).hi};
-  if (end < sq.nq) w.each = Sees{keys_of(a, end + shift, sq.nk).lo, keys_of(a, first + shift, sq.nk).hi};
+  if (first >= sq.nq) return Span{{0, 0}, {0, 0}};
+  Span w = keys_of_rows(a, first, min(first + 31, sq.nq - 1), sq);
+  if (first + 31 >= sq.nq) w.each = Sees{0, 0};
   return w;
 }
 
@@ -356,15 +357,16 @@ PX_DEV void over_tiles(char* lds, const T* K, int64_t ldk, const T* V, int64_t l
   const auto at = [&](int x) { return lds + x * R::bytes(KT); };
   if constexpr (DMA) {
     if (j0 >= j1) return;
-    const DmaRows<D, KT, kWaves> dma;
-    dma.copy(at(0), K, ldk, j0, n);
-    dma.copy(at(1), V, ldv, j0, n);
+    const int wave = wave_id();
+    const DmaRows<D, KT, kWaves> dma(wave);
+    const auto copy = [&](int x, int j) __attribute__((always_inline)) {
+      dma.copy(at(x), K, ldk, j, n, wave);
+      dma.copy(at(x + 1), V, ldv, j, n, wave);
+    };
+    copy(0, j0);
     for (int j = j0, x = 0; j < j1; j += KT, x ^= 2) {
       __syncthreads();  // this tile is there, and the other buffer is done with
-      if (j + KT < j1) {
-        dma.copy(at(2 - x), K, ldk, j + KT, n);
-        dma.copy(at(3 - x), V, ldv, j + KT, n);
-      }
+      if (j + KT < j1) copy(2 - x, j + KT);
       f(x * R::bytes(KT), j);
     }
   } else {
@@ -464,6 +466,205 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
   store_row<T, D>(static_cast<T*>(a.out) + (sq.q0 + i) * a.ldout + (int64_t)head * hd, acc, l == 0.f ? 0.f : 1.f / l,
                   hd, lane);
   if (lane < 32) a.lse[(int64_t)head * a.q.rows + sq.q0 + i] = l == 0.f ? -INFINITY : m * a.scale + kLn2 * log2f(l);
+}
+
+// ---- forward of few rows ---------------------------------------------------
+// With one or a few queries per sequence the keys are read for little work, and there are too few tiles of 128 queries for
+// the card.  Here a tile is 32 rows, a row one query of one of the query heads that share a key head (so that its keys are
+// read once for all of them), and the four waves take 32 keys each of a tile of 128.  By direct copies a wave has its own
+// piece of LDS and waits for nobody: what bounds the kernel is how many bytes are under way, and eight waves a CU that
+// load and compute at different times keep more of them there than two workgroups in step.  A workgroup stands for `part`
+// keys of a sequence.  It leaves the maximum, the sum and the unscaled O that they give the sequence's rows, and k_attn_join
+// adds the parts in their order.  Where a sequence has more rows than a tile all the same, its workgroups share the
+// tiles instead, each with all keys.
+constexpr int kFewRows = 32, kFewKeys = 32 * kWaves;
+template <typename T, int D, bool DMA> struct Few {
+  static constexpr int TILES = 2 * Rows<T, D>::bytes(kFewKeys);
+  static constexpr int JOIN = kWaves * 64 * (D / 2 + 2) * 4;
+  static constexpr int LDS = TILES > JOIN ? TILES : JOIN;
+};
+PX_DEV int parts_of(const AttnArgs& a, const Seq& sq) { return max((sq.nk + a.part - 1) / a.part, 1); }
+// where the O of part slot and key head `kv` is among the parts, in rows of D floats; its maxima and sums lie before
+// them all, as pairs
+PX_DEV int64_t part_row(const AttnArgs& a, int64_t slot, int kv) {
+  return (slot * (a.heads / a.group) + kv) * kFewRows;
+}
+template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads) void k_attn_few(AttnArgs a) {
+  constexpr int KT = kFewKeys;
+  typedef Rows<T, D> R;
+  extern __shared__ __align__(16) char lds[];
+  const int lane = threadIdx.x & 63, wave = wave_id(), hd = DMA ? D : a.hd, kv_heads = a.heads / a.group;
+  const int kv = (int)(blockIdx.x % kv_heads);
+  const int64_t slot = blockIdx.x / kv_heads;
+  int part;
+  const Seq sq = sequence(a, find_seq(a.k, a.batch, slot, a.part, &part));
+  const int parts = parts_of(a, sq), n = sq.nq * a.group, tiles = (n + kFewRows - 1) / kFewRows;
+  if (part < 0 || part >= parts || n == 0) return;
+  const bool cut = tiles == 1 && parts > 1;
+  const int shift = sq.nk - sq.nq;
+  const T* K = static_cast<const T*>(a.K) + sq.k0 * a.ldk + (int64_t)kv * hd;
+  const T* V = static_cast<const T*>(a.V) + sq.k0 * a.ldv + (int64_t)kv * hd;
+  const float c = a.scale * kLog2e;
+  const Lane lane_at = R::lane_at();
+  float2* const sums = reinterpret_cast<float2*>(a.rows) + part_row(a, slot, kv);
+  for (int tile = cut ? 0 : part; tile < tiles; tile += parts) {
+    const int row = tile * kFewRows + (lane & 31), i = row / a.group, head = kv * a.group + row % a.group;
+    const bool live = row < n;
+    // the keys that some row sees, and this workgroup's of them
+    const int last = (min((tile + 1) * kFewRows, n) - 1) / a.group;
+    int j0 = keys_of(a, tile * kFewRows / a.group + shift, sq.nk).lo, j1 = keys_of(a, last + shift, sq.nk).hi;
+    if (cut) {
+      j0 = max(j0, part * a.part);
+      j1 = min(j1, part * a.part + a.part);
+      if (j0 >= j1) {  // none: a part that the join passes over
+        if ((int)threadIdx.x < kFewRows) sums[threadIdx.x] = make_float2(-INFINITY, 0.f);
+        return;
+      }
+    }
+    Frag<T> q[D / 16];
+    row_frags<T, D>(q, static_cast<const T*>(a.Q) + (sq.q0 + i) * a.ldq + (int64_t)head * hd, live, hd, lane);
+    Sees see = live ? keys_of(a, i + shift, sq.nk) : Sees{0, 0};
+    see = Sees{max(see.lo, j0), min(see.hi, j1)};
+    f32x16_v acc[D / 32] = {};
+    float m = -INFINITY, l = 0.f;
+    const Span all = keys_of_rows(a, tile * kFewRows / a.group, last, sq);
+    // 32 keys from j on, whose K and V lie at lds + t and + v behind it
+    const auto step = [&](int t, int v, int j) __attribute__((always_inline)) {
+      const Lane at = lane_at + t;
+      f32x16_v s = {};
+#pragma unroll
+      for (int kk = 0; kk < D / 16; ++kk) mma(s, R::along(lds, at, 0, kk), q[kk]);
+      if (j + 32 > j1 || !all.all(j, j + 32)) {
+        const Sees on = see.from(j);
+#pragma unroll
+        for (int e = 0; e < 16; ++e) s[e] = on.has(acc_row(e)) ? s[e] : -INFINITY;
+      }
+      float top = s[0];
+#pragma unroll
+      for (int e = 1; e < 16; ++e) top = fmaxf(top, s[e]);
+      top = max_halves(top);
+      if (__any((top - m) * c > kSlack)) {
+        const float was = m;
+        m = fmaxf(m, top);
+        const float keep = exp2_of((was - (m == -INFINITY ? 0.f : m)) * c);
+        l *= keep;
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d) acc[d] *= keep;
+      }
+      const float base = m == -INFINITY ? 0.f : m;
+#pragma unroll
+      for (int e = 0; e < 16; ++e) {
+        s[e] = exp2_of((s[e] - base) * c);
+        l += s[e];
+      }
+#pragma unroll
+      for (int h = 0; h < 2; ++h) {
+        const Frag<T> p = to_frag<T>(s, h);
+#pragma unroll
+        for (int d = 0; d < D / 32; ++d) mma(acc[d], R::across(lds + v, at, 16 * h, 32 * d), p);
+      }
+    };
+    if constexpr (DMA) {
+      const int mine = wave * 2 * R::bytes(32);
+      const DmaRows<D, 32, 1> dma(0);
+      for (int j = j0 + 32 * wave; j < j1; j += KT) {
+        dma.copy(lds + mine, K, a.ldk, j, sq.nk, 0);
+        dma.copy(lds + mine + R::bytes(32), V, a.ldv, j, sq.nk, 0);
+        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's own copies
+        step(mine, R::bytes(32), j);
+      }
+    } else {
+      over_tiles<T, D, DMA, KT>(lds, K, a.ldk, V, a.ldv, sq.nk, hd, j0, j1, [&](int t, int j) __attribute__((always_inline)) {
+        if (j + 32 * wave < j1) step(t + R::bytes(32) * wave, R::bytes(KT), j + 32 * wave);
+      });
+    }
+    l = sum_halves(l);
+    // the waves' sums, added in their order: wave w takes columns 32 w and up
+    __syncthreads();
+    float* mine = reinterpret_cast<float*>(lds) + wave * 64 * (D / 2 + 2) + lane;
+#pragma unroll
+    for (int d = 0; d < D / 32; ++d)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) mine[(16 * d + e) * 64] = acc[d][e];
+    mine[(D / 2) * 64] = m;
+    mine[(D / 2 + 1) * 64] = l;
+    __syncthreads();
+    if (wave < D / 32) {
+      const float* all = reinterpret_cast<const float*>(lds) + lane;
+      float f[kWaves], sum = 0.f;
+      m = -INFINITY;
+#pragma unroll
+      for (int x = 0; x < kWaves; ++x) m = fmaxf(m, f[x] = all[(x * (D / 2 + 2) + D / 2) * 64]);
+      f32x16_v o = {};
+#pragma unroll
+      for (int x = 0; x < kWaves; ++x) {
+        f[x] = exp2_of((f[x] - (m == -INFINITY ? 0.f : m)) * c);
+        sum += f[x] * all[(x * (D / 2 + 2) + D / 2 + 1) * 64];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) o[e] += f[x] * all[(x * (D / 2 + 2) + 16 * wave + e) * 64];
+      }
+      if (cut) {
+        float* to = a.rows + a.part_head + (part_row(a, slot, kv) + (lane & 31)) * D + 32 * wave + 4 * (lane >> 5);
+#pragma unroll
+        for (int g = 0; g < 4; ++g)
+          *reinterpret_cast<float4*>(to + 8 * g) = make_float4(o[4 * g], o[4 * g + 1], o[4 * g + 2], o[4 * g + 3]);
+        if (wave == 0 && lane < 32) sums[lane] = make_float2(m, sum);
+      } else if (live) {
+        T* out = static_cast<T*>(a.out) + (sq.q0 + i) * a.ldout + (int64_t)head * hd + 32 * wave;
+        const f32x16_v columns[1] = {o};
+        store_row<T, 32>(out, columns, sum == 0.f ? 0.f : 1.f / sum, hd - 32 * wave, lane);
+        if (wave == 0 && lane < 32)
+          a.lse[(int64_t)head * a.q.rows + sq.q0 + i] = sum == 0.f ? -INFINITY : m * a.scale + kLn2 * log2f(sum);
+      }
+    }
+    __syncthreads();  // the next tile's copies
+  }
+}
+// The parts of one sequence's row and head, in their order, a wave each row.
+template <typename T, int D> __global__ __launch_bounds__(kThreads) void k_attn_join(AttnArgs a) {
+  const int lane = threadIdx.x & 63;
+  const int64_t at = (int64_t)blockIdx.x * kWaves + wave_id();
+  const int s = (int)(at / (a.heads / a.group * kFewRows)), r = (int)(at % (a.heads / a.group * kFewRows));
+  if (s >= a.batch) return;
+  const Seq sq = sequence(a, s);
+  const int kv = r / kFewRows, row = r % kFewRows, parts = parts_of(a, sq);
+  if (row >= sq.nq * a.group || sq.nq * a.group > kFewRows || parts == 1) return;
+  const int64_t slot = (int64_t)((uint32_t)sq.k0 / (uint32_t)a.part) + s;
+  const float c = a.scale * kLog2e;
+  // the largest maximum, a part a lane
+  float m = -INFINITY;
+  for (int x = lane; x < parts; x += 64) m = fmaxf(m, reinterpret_cast<const float2*>(a.rows)[part_row(a, slot + x, kv) + row].x);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+  float sum = 0.f, o[D / 64] = {};
+  for (int x0 = 0; x0 < parts; x0 += 64) {
+    // the factors of 64 parts, one a lane: 0 for a part that saw no key, whose O is not there
+    float f = 0.f;
+    if (x0 + lane < parts) {
+      const float2 ml = reinterpret_cast<const float2*>(a.rows)[part_row(a, slot + x0 + lane, kv) + row];
+      if (ml.x != -INFINITY || ml.y != 0.f) f = exp2_of((ml.x - (m == -INFINITY ? 0.f : m)) * c);
+      sum += f * ml.y;
+    }
+    const int there = __popcll(__ballot(x0 + lane < parts));
+#pragma unroll 8
+    for (int x = 0; x < there; ++x) {
+      const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), x));
+#pragma unroll
+      for (int e = 0; e < D / 64; ++e) {
+        const float v = a.rows[a.part_head + (part_row(a, slot + x0 + x, kv) + row) * D + 64 * e + lane];
+        o[e] += w == 0.f ? 0.f : w * v;
+      }
+    }
+  }
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
+  const int head = kv * a.group + row % a.group;
+  const int64_t i = sq.q0 + row / a.group;
+  T* out = static_cast<T*>(a.out) + i * a.ldout + (int64_t)head * a.hd;
+#pragma unroll
+  for (int e = 0; e < D / 64; ++e)
+    if (64 * e + lane < a.hd) out[64 * e + lane] = from_f32<T>(sum == 0.f ? 0.f : o[e] / sum);
+  if (lane == 0) a.lse[(int64_t)head * a.q.rows + i] = sum == 0.f ? -INFINITY : m * a.scale + kLn2 * log2f(sum);
 }
 
 // ---- backward --------------------------------------------------------------
@@ -689,11 +890,11 @@ template <int D> __global__ __launch_bounds__(512, 2) void k_attn_dkv_dma(AttnAr
   const T* G = static_cast<const T*>(a.dO) + sq.q0 * a.lddo;
   const int64_t at = sq.q0 + (int64_t)t.head * a.group * a.q.rows, more = (int64_t)a.heads * a.q.rows;
   const int per = t.i1 > t.i0 ? (t.i1 - t.i0 + QT - 1) / QT : 0, count = per * a.group;  // tiles: heads x queries
-  const DmaRows<D, QT, C::W> dma;
+  const DmaRows<D, QT, C::W> dma(wave);
   const auto fetch = [&](char* b, int h, int i) __attribute__((always_inline)) {
     const int64_t col = (int64_t)(t.head * a.group + h) * D;
-    dma.copy(b, Q + col, a.ldq, i, sq.nq);
-    dma.copy(b + C::TILE, G + col, a.lddo, i, sq.nq);
+    dma.copy(b, Q + col, a.ldq, i, sq.nq, wave);
+    dma.copy(b + C::TILE, G + col, a.lddo, i, sq.nq, wave);
     if (wave < 2) {  // 64 values each: wave 0 the lse, wave 1 D
       const float* x = a.rows + at + wave * more + (int64_t)h * a.q.rows + min(i + lane, sq.nq - 1);
       char* to = b + 2 * C::TILE + wave * QT * 4;
@@ -711,9 +912,9 @@ template <int D> __global__ __launch_bounds__(512, 2) void k_attn_dkv_dma(AttnAr
                       [&](int kk) { return R::along(tv, keys_at, 0, kk); });
   };
   if (count > 0) {
-    const DmaRows<D, kRows, C::W> whole;
-    whole.copy(tk, static_cast<const T*>(a.K) + sq.k0 * a.ldk + (int64_t)t.head * D, a.ldk, t.w0, sq.nk);
-    whole.copy(tv, static_cast<const T*>(a.V) + sq.k0 * a.ldv + (int64_t)t.head * D, a.ldv, t.w0, sq.nk);
+    const DmaRows<D, kRows, C::W> whole(wave);
+    whole.copy(tk, static_cast<const T*>(a.K) + sq.k0 * a.ldk + (int64_t)t.head * D, a.ldk, t.w0, sq.nk, wave);
+    whole.copy(tv, static_cast<const T*>(a.V) + sq.k0 * a.ldv + (int64_t)t.head * D, a.ldv, t.w0, sq.nk, wave);
     fetch(bufs, 0, t.i0);
   }
   int h = 0, i = t.i0;
@@ -748,7 +949,7 @@ template <int D> __global__ __launch_bounds__(512, 2) void k_attn_dkv_dma(AttnAr
     store_row<T, D>(static_cast<T*>(a.out) + (sq.k0 + j) * a.ldout + (int64_t)t.head * D, dk, a.scale, D, lane);
 }
 
-int64_t slots_of(int64_t rows, int batch) { return rows / kRows + batch; }
+int64_t slots_of(int64_t rows, int batch, int R = kRows) { return rows / R + batch; }
 
 AttnArgs args_of(const AttnDesc& d) {
   AttnArgs a = {};
@@ -781,6 +982,13 @@ bool dma_rows(const AttnMat& m) {
   return reinterpret_cast<uintptr_t>(m.p) % 16 == 0 && m.ld % 8 == 0 && m.ld <= kDmaLd;
 }
 
+// The keys of a workgroup in the forward of few rows; 0 where a tile of 32 rows does not hold a sequence's queries on the
+// average, and the tiles of 128 queries are taken.
+int few_part(const AttnDesc& d) {
+  if (d.Tq * (d.heads / d.kv_heads) > (int64_t)kFewRows * d.batch) return 0;
+  return (int)std::max<int64_t>(256, round_up(d.Tk * d.kv_heads / 512, kFewKeys));
+}
+
 }  // namespace
 
 namespace pxk {
@@ -791,18 +999,43 @@ bool attn_fits(const AttnDesc& d) {
 }
 
 size_t attn_fwd_ws_bytes(const AttnDesc& d) {
-  (void)d;
-  return 0;
+  const int part = few_part(d);
+  if (part == 0 || d.Tk <= part) return 0;  // the latter: no sequence has two parts
+  return (size_t)slots_of(d.Tk, d.batch, part) * d.kv_heads * kFewRows * (2 + (d.hd <= 64 ? 64 : 128)) * 4;
 }
 size_t attn_bwd_ws_bytes(const AttnDesc& d) { return (size_t)d.heads * d.Tq * 8; }
 
 hipError_t attn_fwd(const AttnDesc& d, const AttnMat& Q, const AttnMat& K, const AttnMat& V, void* O, int64_t ldo,
                     float* lse, void* ws, hipStream_t s) {
-  (void)ws;
   if (d.Tq == 0) return hipSuccess;
   AttnArgs a = args_of(d);
   a.Q = Q.p, a.ldq = Q.ld, a.K = K.p, a.ldk = K.ld, a.V = V.p, a.ldv = V.ld;
-  a.out = O, a.ldout = ldo, a.lse = lse;
+  a.out = O, a.ldout = ldo, a.lse = lse, a.rows = static_cast<float*>(ws);
+  a.part = few_part(d);
+  if (a.part) {
+    hipError_t e = hipSuccess;
+    const int64_t slots = slots_of(d.Tk, d.batch, a.part);
+    a.part_head = 2 * slots * d.kv_heads * kFewRows;
+    pick(d, [&](auto t, auto D) {
+      typedef decltype(t) T;
+      constexpr int W = decltype(D)::value;
+      const auto run = [&](auto dma) {
+        typedef Few<T, W, decltype(dma)::value> F;
+        e = px::lds_once<k_attn_few<T, W, decltype(dma)::value>>(F::LDS);
+        if (e != hipSuccess) return;
+        k_attn_few<T, W, decltype(dma)::value><<<dim3((unsigned)(slots * d.kv_heads)), kThreads, F::LDS, s>>>(a);
+      };
+      if constexpr (sizeof(T) == 2) {
+        if (fills_tile(d) && dma_rows(K) && dma_rows(V)) run(std::true_type());
+        else run(std::false_type());
+      } else {
+        run(std::false_type());
+      }
+      if (e == hipSuccess && d.Tk > a.part)
+        k_attn_join<T, W><<<dim3(px::cdiv((int64_t)d.batch * d.kv_heads * kFewRows, kWaves)), kThreads, 0, s>>>(a);
+    });
+    return e != hipSuccess ? e : hipGetLastError();
+  }
   a.slots = slots_of(d.Tq, d.batch);
   const bool dma = fills_tile(d) && dma_rows(K) && dma_rows(V);
   pick(d, [&](auto t, auto D) {
