@@ -264,22 +264,29 @@ PX_DEV Seq sequence(const AttnArgs& a, int s) {
   r.nk = (int)max(first_row(a.k, s + 1) - r.k0, (int64_t)0);
   return r;
 }
-// The sequence and the tile of `slot`: sequence s of rows [a, b) has the slots from a / R + s on, and the ones up to
-// b / R + s are enough for its ceil((b - a) / R) tiles.  So the host needs no length, and a workgroup no prefix sum.
-PX_DEV int find_seq(const Side& x, int batch, int64_t slot, int R, int* tile) {
-  const auto begin = [&](int s) { return (int64_t)((uint32_t)first_row(x, s) / (uint32_t)R) + s; };
+// The last sequence s that f(s) holds for, or the first; f holds up to some sequence.  64 candidates at a time.
+template <class F> PX_DEV int last_seq(int batch, const F& f) {
   const int lane = threadIdx.x & 63;
-  int lo = 0, n = batch;  // the last s of [lo, lo + n) with first_row / R + s <= slot, 64 candidates at a time
+  int lo = 0, n = batch;  // it is in [lo, lo + n)
   while (n > 1) {
-    const int step = (n + 63) / 64, s = lo + lane * step;
-    const bool at = lane * step < n && begin(s) <= slot;
+    const int step = (n + 63) / 64;
+    const bool at = lane * step < n && f(lo + lane * step);
     const int k = max((int)__popcll(__ballot(at)) - 1, 0);
     lo += k * step;
     n = min(step, n - k * step);
   }
-  lo = __builtin_amdgcn_readfirstlane(lo);
-  *tile = (int)(slot - begin(lo));
-  return lo;
+  return __builtin_amdgcn_readfirstlane(lo);
+}
+PX_DEV int seq_of_row(const Side& x, int batch, int64_t row) {
+  return last_seq(batch, [&](int s) { return first_row(x, s) <= row; });
+}
+// The sequence and the tile of `slot`: sequence s of rows [a, b) has the slots from a / R + s on, and the ones up to
+// b / R + s are enough for its ceil((b - a) / R) tiles.  So the host needs no length, and a workgroup no prefix sum.
+PX_DEV int find_seq(const Side& x, int batch, int64_t slot, int R, int* tile) {
+  const auto begin = [&](int s) { return (int64_t)((uint32_t)first_row(x, s) / (uint32_t)R) + s; };
+  const int s = last_seq(batch, [&](int s) { return begin(s) <= slot; });
+  *tile = (int)(slot - begin(s));
+  return s;
 }
 
 // The head of workgroup p of a tile's: the query heads of a key head are kv_heads apart, so that with the 8 or 16 key heads
@@ -514,8 +521,9 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads) vo
     const int last = (min((tile + 1) * kFewRows, n) - 1) / a.group;
     int j0 = keys_of(a, tile * kFewRows / a.group + shift, sq.nk).lo, j1 = keys_of(a, last + shift, sq.nk).hi;
     if (cut) {
-      j0 = max(j0, part * a.part);
-      j1 = min(j1, part * a.part + a.part);
+      const int each = ((sq.nk + parts - 1) / parts + 31) / 32 * 32;  // parts of one length
+      j0 = max(j0, part * each);
+      j1 = min(j1, part * each + each);
       if (j0 >= j1) {  // none: a part that the join passes over
         if ((int)threadIdx.x < kFewRows) sums[threadIdx.x] = make_float2(-INFINITY, 0.f);
         return;
@@ -620,46 +628,55 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads) vo
     __syncthreads();  // the next tile's copies
   }
 }
-// The parts of one sequence's row and head, in their order, a wave each row.
+// The parts of one query and head, in their order: a wave each.
 template <typename T, int D> __global__ __launch_bounds__(kThreads) void k_attn_join(AttnArgs a) {
   const int lane = threadIdx.x & 63;
   const int64_t at = (int64_t)blockIdx.x * kWaves + wave_id();
-  const int s = (int)(at / (a.heads / a.group * kFewRows)), r = (int)(at % (a.heads / a.group * kFewRows));
-  if (s >= a.batch) return;
+  const int64_t i = at / a.heads;
+  const int head = (int)(at % a.heads);
+  if (i >= a.q.rows || i < first_row(a.q, 0) || i >= first_row(a.q, a.batch)) return;
+  const int s = seq_of_row(a.q, a.batch, i);
   const Seq sq = sequence(a, s);
-  const int kv = r / kFewRows, row = r % kFewRows, parts = parts_of(a, sq);
-  if (row >= sq.nq * a.group || sq.nq * a.group > kFewRows || parts == 1) return;
+  const int kv = head / a.group, row = (int)(i - sq.q0) * a.group + head % a.group, parts = parts_of(a, sq);
+  if (sq.nq * a.group > kFewRows || parts == 1) return;  // complete
+  constexpr int kAtOnce = 16;
   const int64_t slot = (int64_t)((uint32_t)sq.k0 / (uint32_t)a.part) + s;
   const float c = a.scale * kLog2e;
-  // the largest maximum, a part a lane
-  float m = -INFINITY;
-  for (int x = lane; x < parts; x += 64) m = fmaxf(m, reinterpret_cast<const float2*>(a.rows)[part_row(a, slot + x, kv) + row].x);
+  const float2* const sums = reinterpret_cast<const float2*>(a.rows);
+  float m = -INFINITY, sum = 0.f, o[D / 64] = {};
+  for (int x0 = 0; x0 < parts; x0 += kAtOnce) {
+    // 16 parts: their maxima and sums a part a lane, their O a part a register, all on the way together
+    const int n = min(parts - x0, kAtOnce);
+    float2 ml = make_float2(-INFINITY, 0.f);
+    if (lane < n) ml = sums[part_row(a, slot + x0 + lane, kv) + row];
+    float v[kAtOnce][D / 64];
 #pragma unroll
-  for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-  float sum = 0.f, o[D / 64] = {};
-  for (int x0 = 0; x0 < parts; x0 += 64) {
-    // the factors of 64 parts, one a lane: 0 for a part that saw no key, whose O is not there
-    float f = 0.f;
-    if (x0 + lane < parts) {
-      const float2 ml = reinterpret_cast<const float2*>(a.rows)[part_row(a, slot + x0 + lane, kv) + row];
-      if (ml.x != -INFINITY || ml.y != 0.f) f = exp2_of((ml.x - (m == -INFINITY ? 0.f : m)) * c);
-      sum += f * ml.y;
-    }
-    const int there = __popcll(__ballot(x0 + lane < parts));
-#pragma unroll 8
-    for (int x = 0; x < there; ++x) {
+    for (int x = 0; x < kAtOnce; ++x)
+#pragma unroll
+      for (int e = 0; e < D / 64; ++e)
+        v[x][e] = a.rows[a.part_head + (part_row(a, slot + x0 + min(x, n - 1), kv) + row) * D + 64 * e + lane];
+    float top = fmaxf(m, ml.x);
+#pragma unroll
+    for (int d = 1; d < kAtOnce; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+    top = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(top), 0));
+    const float base = top == -INFINITY ? 0.f : top, keep = exp2_of((m - base) * c);
+    m = top;
+    // a part that saw no key has no O: whatever is read there counts 0
+    const bool none = ml.x == -INFINITY && ml.y == 0.f;
+    const float f = none ? 0.f : exp2_of((ml.x - base) * c);
+    sum = sum * keep + f * ml.y;
+#pragma unroll
+    for (int e = 0; e < D / 64; ++e) o[e] *= keep;
+    const uint64_t there = __ballot(!none);
+#pragma unroll
+    for (int x = 0; x < kAtOnce; ++x) {
       const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), x));
 #pragma unroll
-      for (int e = 0; e < D / 64; ++e) {
-        const float v = a.rows[a.part_head + (part_row(a, slot + x0 + x, kv) + row) * D + 64 * e + lane];
-        o[e] += w == 0.f ? 0.f : w * v;
-      }
+      for (int e = 0; e < D / 64; ++e) o[e] += there >> x & 1 ? w * v[x][e] : 0.f;
     }
   }
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
-  const int head = kv * a.group + row % a.group;
-  const int64_t i = sq.q0 + row / a.group;
   T* out = static_cast<T*>(a.out) + i * a.ldout + (int64_t)head * a.hd;
 #pragma unroll
   for (int e = 0; e < D / 64; ++e)
@@ -986,7 +1003,7 @@ bool dma_rows(const AttnMat& m) {
 // average, and the tiles of 128 queries are taken.
 int few_part(const AttnDesc& d) {
   if (d.Tq * (d.heads / d.kv_heads) > (int64_t)kFewRows * d.batch) return 0;
-  return (int)std::max<int64_t>(256, round_up(d.Tk * d.kv_heads / 512, kFewKeys));
+  return (int)std::max<int64_t>(256, round_up(std::min(d.Tk * d.kv_heads / 512, d.Tk / (2 * d.batch)), kFewKeys));
 }
 
 }  // namespace
@@ -1032,7 +1049,7 @@ hipError_t attn_fwd(const AttnDesc& d, const AttnMat& Q, const AttnMat& K, const
         run(std::false_type());
       }
       if (e == hipSuccess && d.Tk > a.part)
-        k_attn_join<T, W><<<dim3(px::cdiv((int64_t)d.batch * d.kv_heads * kFewRows, kWaves)), kThreads, 0, s>>>(a);
+        k_attn_join<T, W><<<dim3(px::cdiv((int64_t)d.Tq * d.heads, kWaves)), kThreads, 0, s>>>(a);
     });
     return e != hipSuccess ? e : hipGetLastError();
   }
