@@ -150,6 +150,9 @@ template <int D> struct Rows<float, D> {
   }
 };
 
+// whether column c is in the head: known where the head fills the tile
+template <bool FULL> PX_DEV bool within(int c, int hd) { return FULL || c < hd; }
+
 // 8 elements from column c of a head's row, zeros behind its end and for absent rows
 template <typename T> PX_DEV void load8(T (&v)[8], const T* row, bool there, int c, int hd) {
   if (there && c + 8 <= hd) {
@@ -159,18 +162,25 @@ template <typename T> PX_DEV void load8(T (&v)[8], const T* row, bool there, int
     for (int i = 0; i < 8; ++i) v[i] = there && c + i < hd ? row[c + i] : T(0);
   }
 }
-// rows [r0, r0 + N) of a sequence's `n`, into an LDS tile
-template <typename T, int D, int N>
-PX_DEV void copy_rows(char* tile, const T* base, int64_t ld, int r0, int n, int hd) {
-  constexpr int C = D / 8;
+// rows [r0, r0 + N) of a sequence's `n`, into an LDS tile by way of registers: any type, head and alignment
+template <typename T, int D, int N> struct Staged {
+  static constexpr int C = D / 8, EACH = N * C / kThreads;
+  T v[EACH][8];
+  PX_DEV void load(const T* base, int64_t ld, int r0, int n, int hd) {
 #pragma unroll
-  for (int i = 0; i < N * C / kThreads; ++i) {
-    const int x = i * kThreads + (int)threadIdx.x, r = x / C, c = x % C;
-    T v[8];
-    load8<T>(v, base + (int64_t)(r0 + r) * ld, r0 + r < n, 8 * c, hd);
-    Rows<T, D>::put(tile, r, c, v);
+    for (int i = 0; i < EACH; ++i) {
+      const int x = i * kThreads + (int)threadIdx.x, r = x / C, c = x % C;
+      load8<T>(v[i], base + (int64_t)(r0 + r) * ld, r0 + r < n, 8 * c, hd);
+    }
   }
-}
+  PX_DEV void put(char* tile) const {
+#pragma unroll
+    for (int i = 0; i < EACH; ++i) {
+      const int x = i * kThreads + (int)threadIdx.x;
+      Rows<T, D>::put(tile, x / C, x % C, v[i]);
+    }
+  }
+};
 // The same by direct global -> LDS copies, 16 bytes a lane, for heads that fill the tile (bf16, hd = D, rows aligned to
 // 16 bytes, pitches of up to kDmaLd).  Rows behind the last repeat it; what is computed from them is masked.
 constexpr int64_t kDmaLd = 1 << 24;  // a tile's rows lie within 32 bits
@@ -376,11 +386,32 @@ PX_DEV void over_tiles(char* lds, const T* K, int64_t ldk, const T* V, int64_t l
       if (j + KT < j1) copy(2 - x, j + KT);
       f(x * R::bytes(KT), j);
     }
-  } else {
+  } else if constexpr (KT <= 64) {
+    // the next tile's rows come into registers while this one is computed with
+    Staged<T, D, KT> k, v;
+    const auto load = [&](int j) __attribute__((always_inline)) {
+      k.load(K, ldk, j, n, hd);
+      v.load(V, ldv, j, n, hd);
+    };
+    if (j0 < j1) load(j0);
     for (int j = j0; j < j1; j += KT) {
       __syncthreads();
-      copy_rows<T, D, KT>(at(0), K, ldk, j, n, hd);
-      copy_rows<T, D, KT>(at(1), V, ldv, j, n, hd);
+      k.put(at(0));
+      v.put(at(1));
+      __syncthreads();
+      if (j + KT < j1) load(j + KT);
+      f(0, j);
+    }
+  } else {  // too many rows for that
+    for (int j = j0; j < j1; j += KT) {
+      __syncthreads();
+      for (int x = 0; x < KT; x += 32) {
+        Staged<T, D, 32> k, v;
+        k.load(K, ldk, j + x, n, hd);
+        v.load(V, ldv, j + x, n, hd);
+        k.put(at(0) + R::bytes(x));
+        v.put(at(1) + R::bytes(x));
+      }
       __syncthreads();
       f(0, j);
     }
@@ -425,8 +456,9 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
     f32x16_v s[NB] = {};
 #pragma unroll
     for (int kk = 0; kk < D / 16; ++kk)
+      if (within<DMA>(16 * kk, hd))
 #pragma unroll
-      for (int b = 0; b < NB; ++b) mma(s[b], R::along(tk, at, 32 * b, kk), q[kk]);
+        for (int b = 0; b < NB; ++b) mma(s[b], R::along(tk, at, 32 * b, kk), q[kk]);
     float top = -INFINITY;
     const Sees on = see.from(j);
 #pragma unroll
@@ -460,7 +492,8 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
       for (int h = 0; h < 2; ++h) {
         const Frag<T> p = to_frag<T>(s[b], h);
 #pragma unroll
-        for (int d = 0; d < D / 32; ++d) mma(acc[d], R::across(tv, at, 32 * b + 16 * h, 32 * d), p);
+        for (int d = 0; d < D / 32; ++d)
+          if (within<DMA>(32 * d, hd)) mma(acc[d], R::across(tv, at, 32 * b + 16 * h, 32 * d), p);
       }
   };
   over_tiles<T, D, DMA, KT>(lds, K, a.ldk, V, a.ldv, sq.nk, hd, j0, j1,
@@ -541,7 +574,8 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads) vo
       const Lane at = lane_at + t;
       f32x16_v s = {};
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) mma(s, R::along(lds, at, 0, kk), q[kk]);
+      for (int kk = 0; kk < D / 16; ++kk)
+        if (within<DMA>(16 * kk, hd)) mma(s, R::along(lds, at, 0, kk), q[kk]);
       if (j + 32 > j1 || !all.all(j, j + 32)) {
         const Sees on = see.from(j);
 #pragma unroll
@@ -569,7 +603,8 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads) vo
       for (int h = 0; h < 2; ++h) {
         const Frag<T> p = to_frag<T>(s, h);
 #pragma unroll
-        for (int d = 0; d < D / 32; ++d) mma(acc[d], R::across(lds + v, at, 16 * h, 32 * d), p);
+        for (int d = 0; d < D / 32; ++d)
+          if (within<DMA>(32 * d, hd)) mma(acc[d], R::across(lds + v, at, 16 * h, 32 * d), p);
       }
     };
     if constexpr (DMA) {
@@ -740,17 +775,19 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
       const uint32_t on = see.from(j + 32 * b).bits();
       f32x16_v s = {}, dp = {};
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk) {
-        mma(s, R::along(tk, at, 32 * b, kk), q[kk]);
-        mma(dp, R::along(tv, at, 32 * b, kk), g[kk]);
-      }
+      for (int kk = 0; kk < D / 16; ++kk)
+        if (within<DMA>(16 * kk, hd)) {
+          mma(s, R::along(tk, at, 32 * b, kk), q[kk]);
+          mma(dp, R::along(tv, at, 32 * b, kk), g[kk]);
+        }
 #pragma unroll
       for (int e = 0; e < 16; ++e) s[e] = where(on, acc_row(e), prob<T>(s[e], lse, a.scale, c)) * (dp[e] - delta);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const Frag<T> p = to_frag<T>(s, h);
 #pragma unroll
-        for (int d = 0; d < D / 32; ++d) mma(acc[d], R::across(tk, at, 32 * b + 16 * h, 32 * d), p);
+        for (int d = 0; d < D / 32; ++d)
+          if (within<DMA>(32 * d, hd)) mma(acc[d], R::across(tk, at, 32 * b + 16 * h, 32 * d), p);
       }
     }
   };
@@ -764,17 +801,18 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
 // dK and dV of 128 keys of one key head: its query heads one after another, so that their sum has one order.  Of a block
 // of 32 queries (`tq`, `tg`: their rows and dO in LDS, `rows` and `deltas`: their lse and D), key(kk) and value(kk) are
 // the operands of the wave's keys.
-template <typename T, int D, class FK, class FV>
+template <typename T, int D, bool FULL, class FK, class FV>
 PX_DEV void dkv_block(f32x16_v (&dk)[D / 32], f32x16_v (&dv)[D / 32], const char* tq, const char* tg, const Lane& at,
-                      const float* rows, const float* deltas, uint32_t on, float scale, float c, const FK& key,
+                      const float* rows, const float* deltas, uint32_t on, float scale, float c, int hd, const FK& key,
                       const FV& value) {
   typedef Rows<T, D> R;
   f32x16_v s = {}, dp = {};
 #pragma unroll
-  for (int kk = 0; kk < D / 16; ++kk) {
-    mma(s, R::along(tq, at, 0, kk), key(kk));
-    mma(dp, R::along(tg, at, 0, kk), value(kk));
-  }
+  for (int kk = 0; kk < D / 16; ++kk)
+    if (within<FULL>(16 * kk, hd)) {
+      mma(s, R::along(tq, at, 0, kk), key(kk));
+      mma(dp, R::along(tg, at, 0, kk), value(kk));
+    }
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int r = acc_row(4 * u);  // four rows of a lane lie side by side
@@ -791,10 +829,11 @@ PX_DEV void dkv_block(f32x16_v (&dk)[D / 32], f32x16_v (&dv)[D / 32], const char
   for (int x = 0; x < 2; ++x) {
     const Frag<T> p = to_frag<T>(s, x), g = to_frag<T>(dp, x);
 #pragma unroll
-    for (int d = 0; d < D / 32; ++d) {
-      mma(dv[d], R::across(tg, at, 16 * x, 32 * d), p);
-      mma(dk[d], R::across(tq, at, 16 * x, 32 * d), g);
-    }
+    for (int d = 0; d < D / 32; ++d)
+      if (within<FULL>(32 * d, hd)) {
+        mma(dv[d], R::across(tg, at, 16 * x, 32 * d), p);
+        mma(dk[d], R::across(tq, at, 16 * x, 32 * d), g);
+      }
   }
 }
 
@@ -848,26 +887,33 @@ template <typename T, int D> __global__ __launch_bounds__(kThreads) void k_attn_
   const Lane lane_at = R::lane_at();
   f32x16_v dk[D / 32] = {}, dv[D / 32] = {};
   const int64_t more = (int64_t)a.heads * a.q.rows;
-  for (int h = t.head * a.group; h < (t.head + 1) * a.group; ++h) {
-    const T* Q = static_cast<const T*>(a.Q) + sq.q0 * a.ldq + (int64_t)h * a.hd;
-    const T* G = static_cast<const T*>(a.dO) + sq.q0 * a.lddo + (int64_t)h * a.hd;
-    const float* x = a.rows + (int64_t)h * a.q.rows + sq.q0;
-    for (int i = t.i0; i < t.i1; i += QT) {
-      __syncthreads();
-      copy_rows<T, D, QT>(lds, Q, a.ldq, i, sq.nq, a.hd);
-      copy_rows<T, D, QT>(lds + R::bytes(QT), G, a.lddo, i, sq.nq, a.hd);
-      if ((int)threadIdx.x < 2 * QT) {
-        const int which = (int)threadIdx.x / QT, r = (int)threadIdx.x % QT;
-        rows[which][r] = x[which * more + min(i + r, sq.nq - 1)];
-      }
-      __syncthreads();
+  const int per = t.i1 > t.i0 ? (t.i1 - t.i0 + QT - 1) / QT : 0, count = per * a.group;  // tiles: heads x queries
+  Staged<T, D, QT> q, g;
+  float row_value = 0.f;  // of the first 2 QT threads: lse, D
+  const auto load = [&](int n) __attribute__((always_inline)) {
+    const int h = t.head * a.group + n / per, i = t.i0 + n % per * QT;
+    q.load(static_cast<const T*>(a.Q) + sq.q0 * a.ldq + (int64_t)h * a.hd, a.ldq, i, sq.nq, a.hd);
+    g.load(static_cast<const T*>(a.dO) + sq.q0 * a.lddo + (int64_t)h * a.hd, a.lddo, i, sq.nq, a.hd);
+    if ((int)threadIdx.x < 2 * QT)
+      row_value = a.rows[(int)threadIdx.x / QT * more + (int64_t)h * a.q.rows + sq.q0 +
+                         min(i + (int)threadIdx.x % QT, sq.nq - 1)];
+  };
+  if (count > 0) load(0);
+  for (int n = 0; n < count; ++n) {
+    const int i = t.i0 + n % per * QT;
+    __syncthreads();
+    q.put(lds);
+    g.put(lds + R::bytes(QT));
+    if ((int)threadIdx.x < 2 * QT) rows[0][threadIdx.x] = row_value;
+    __syncthreads();
+    if (n + 1 < count) load(n + 1);
 #pragma unroll
-      for (int b = 0; b < QT; b += 32) {
-        const int p = i + b + t.shift, r = b + 4 * (lane >> 5);
-        if (w.any(p, p + 32))
-          dkv_block<T, D>(dk, dv, lds, lds + R::bytes(QT), lane_at + R::bytes(b), rows[0] + r, rows[1] + r,
-                          see.from(p).bits(), a.scale, c, [&](int kk) { return k[kk]; }, [&](int kk) { return v[kk]; });
-      }
+    for (int b = 0; b < QT; b += 32) {
+      const int p = i + b + t.shift, r = b + 4 * (lane >> 5);
+      if (w.any(p, p + 32))
+        dkv_block<T, D, false>(dk, dv, lds, lds + R::bytes(QT), lane_at + R::bytes(b), rows[0] + r, rows[1] + r,
+                               see.from(p).bits(), a.scale, c, a.hd, [&](int kk) { return k[kk]; },
+                               [&](int kk) { return v[kk]; });
     }
   }
   if (!live) return;
@@ -924,7 +970,7 @@ template <int D> __global__ __launch_bounds__(512, 2) void k_attn_dkv_dma(AttnAr
     const float* rows = reinterpret_cast<const float*>(lds + tile + 2 * C::TILE) + 32 * half + 4 * (lane >> 5);
     const Lane at = (lane_at + (tile + R::bytes(32 * half))).here(), keys_at = (lane_at + R::bytes(keys)).here();
     if (w.any(p, p + 32))
-      dkv_block<T, D>(dk, dv, lds, lds + C::TILE, at, rows, rows + QT, see.from(p).bits(), a.scale, c,
+      dkv_block<T, D, true>(dk, dv, lds, lds + C::TILE, at, rows, rows + QT, see.from(p).bits(), a.scale, c, D,
                       [&](int kk) { return R::along(tk, keys_at, 0, kk); },
                       [&](int kk) { return R::along(tv, keys_at, 0, kk); });
   };
