@@ -250,9 +250,11 @@ struct AttnArgs {
   int64_t ldout, ldout2;
   float *lse, *rows;  // rows: the backward's lse and D of every query, [2][heads][Tq]; the parts of few rows, pairs of
                       // maximum and sum and from part_head on their O
+  float* parts;       // the shares' dK and dV, [shares][2][kv_heads][Tk][D]
   Side q, k;
   int batch, heads, group, hd, window;
-  int part;  // keys of a workgroup in the forward of few rows
+  int part;    // keys of a workgroup in the forward of few rows
+  int shares;  // workgroups that share the query heads of a key head in dK and dV
   bool causal;
   float scale;
   int64_t slots, part_head;
@@ -798,7 +800,9 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
     store_row<T, D>(static_cast<T*>(a.out) + (sq.q0 + i) * a.ldout + (int64_t)head * hd, acc, a.scale, hd, lane);
 }
 
-// dK and dV of 128 keys of one key head: its query heads one after another, so that their sum has one order.  Of a block
+// dK and dV of 128 keys of one key head: its query heads one after another, so that their sum has one order.  Where that
+// gives the card too few workgroups, they share the query heads: each leaves its sums in fp32, and k_attn_dkv_sum adds
+// them in the heads' order.  Of a block
 // of 32 queries (`tq`, `tg`: their rows and dO in LDS, `rows` and `deltas`: their lse and D), key(kk) and value(kk) are
 // the operands of the wave's keys.
 template <typename T, int D, bool FULL, class FK, class FV>
@@ -840,15 +844,19 @@ PX_DEV void dkv_block(f32x16_v (&dk)[D / 32], f32x16_v (&dv)[D / 32], const char
 // The keys of a workgroup, and the queries that see some of them.
 struct KeyTile {
   Seq sq;
-  int head, w0, shift, i0, i1;
+  int head, share, w0, shift, i0, i1;  // share: which of the workgroups that share the key head's query heads
+  int first, heads;                    // its query heads
   bool any;
 };
 PX_DEV KeyTile key_tile(const AttnArgs& a, int QT) {
   KeyTile k;
   const int kv_heads = a.heads / a.group;
   k.head = (int)(blockIdx.x % kv_heads);
+  k.share = (int)(blockIdx.x / kv_heads % a.shares);
+  k.heads = a.group / a.shares;
+  k.first = k.head * a.group + k.share * k.heads;
   int tile;
-  k.sq = sequence(a, find_seq(a.k, a.batch, slot_of(a, blockIdx.x / kv_heads, false), kRows, &tile));
+  k.sq = sequence(a, find_seq(a.k, a.batch, slot_of(a, blockIdx.x / kv_heads / a.shares, false), kRows, &tile));
   k.w0 = tile * kRows;
   k.any = tile >= 0 && k.w0 < k.sq.nk;
   k.shift = k.sq.nk - k.sq.nq;
@@ -864,6 +872,39 @@ PX_DEV Span places_of_wave(const AttnArgs& a, int first, const KeyTile& k) {
   if (first < nk) w.some = Sees{places_of(a, first, k.shift, nk).lo, places_of(a, min(end, nk - 1), k.shift, nk).hi};
   if (end < nk) w.each = Sees{places_of(a, end, k.shift, nk).lo, places_of(a, first, k.shift, nk).hi};
   return w;
+}
+
+// a key's row of dK (which = 0) or dV (1), or where this share's goes
+template <typename T, int D>
+PX_DEV void store_grad(const AttnArgs& a, const KeyTile& k, int which, int key, const f32x16_v (&acc)[D / 32], int hd, int lane) {
+  if (a.shares == 1) {
+    T* out = which ? static_cast<T*>(a.out2) + (k.sq.k0 + key) * a.ldout2 : static_cast<T*>(a.out) + (k.sq.k0 + key) * a.ldout;
+    store_row<T, D>(out + (int64_t)k.head * hd, acc, which ? 1.f : a.scale, hd, lane);
+  } else {
+    const int64_t row = ((int64_t)(2 * k.share + which) * (a.heads / a.group) + k.head) * a.k.rows + k.sq.k0 + key;
+    store_row<float, D>(a.parts + row * D, acc, which ? 1.f : a.scale, D, lane);
+  }
+}
+template <typename T, int D> __global__ __launch_bounds__(kThreads) void k_attn_dkv_sum(AttnArgs a) {
+  const int kv_heads = a.heads / a.group, c = (int)(threadIdx.x % (D / 4)) * 4;
+  const int64_t n = (int64_t)blockIdx.x * (kThreads / (D / 4)) + threadIdx.x / (D / 4);  // row and head of both
+  const int64_t row = n / kv_heads;
+  const int head = (int)(n % kv_heads);
+  if (row >= a.k.rows || row < first_row(a.k, 0) || row >= first_row(a.k, a.batch)) return;
+#pragma unroll
+  for (int which = 0; which < 2; ++which) {
+    float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int x = 0; x < a.shares; ++x) {
+      const int64_t at = (((int64_t)(2 * x + which) * kv_heads + head) * a.k.rows + row) * D + c;
+      const float4 f = *reinterpret_cast<const float4*>(a.parts + at);
+      sum = make_float4(sum.x + f.x, sum.y + f.y, sum.z + f.z, sum.w + f.w);
+    }
+    T* out = (which ? static_cast<T*>(a.out2) + row * a.ldout2 : static_cast<T*>(a.out) + row * a.ldout) + (int64_t)head * a.hd;
+    const float v[4] = {sum.x, sum.y, sum.z, sum.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (c + i < a.hd) out[c + i] = from_f32<T>(v[i]);
+  }
 }
 
 // Any type, head and alignment: 4 waves, which hold their keys and values in registers.
@@ -887,11 +928,11 @@ template <typename T, int D> __global__ __launch_bounds__(kThreads) void k_attn_
   const Lane lane_at = R::lane_at();
   f32x16_v dk[D / 32] = {}, dv[D / 32] = {};
   const int64_t more = (int64_t)a.heads * a.q.rows;
-  const int per = t.i1 > t.i0 ? (t.i1 - t.i0 + QT - 1) / QT : 0, count = per * a.group;  // tiles: heads x queries
+  const int per = t.i1 > t.i0 ? (t.i1 - t.i0 + QT - 1) / QT : 0, count = per * t.heads;  // tiles: heads x queries
   Staged<T, D, QT> q, g;
   float row_value = 0.f;  // of the first 2 QT threads: lse, D
   const auto load = [&](int n) __attribute__((always_inline)) {
-    const int h = t.head * a.group + n / per, i = t.i0 + n % per * QT;
+    const int h = t.first + n / per, i = t.i0 + n % per * QT;
     q.load(static_cast<const T*>(a.Q) + sq.q0 * a.ldq + (int64_t)h * a.hd, a.ldq, i, sq.nq, a.hd);
     g.load(static_cast<const T*>(a.dO) + sq.q0 * a.lddo + (int64_t)h * a.hd, a.lddo, i, sq.nq, a.hd);
     if ((int)threadIdx.x < 2 * QT)
@@ -917,8 +958,8 @@ template <typename T, int D> __global__ __launch_bounds__(kThreads) void k_attn_
     }
   }
   if (!live) return;
-  store_row<T, D>(static_cast<T*>(a.out) + (sq.k0 + j) * a.ldout + (int64_t)t.head * a.hd, dk, a.scale, a.hd, lane);
-  store_row<T, D>(static_cast<T*>(a.out2) + (sq.k0 + j) * a.ldout2 + (int64_t)t.head * a.hd, dv, 1.f, a.hd, lane);
+  store_grad<T, D>(a, t, 0, j, dk, a.hd, lane);
+  store_grad<T, D>(a, t, 1, j, dv, a.hd, lane);
 }
 
 // Heads that fill the tile, by direct copies.  The accumulators of 32 keys take 128 registers; with the keys and values
@@ -951,11 +992,11 @@ template <int D> __global__ __launch_bounds__(512, 2) void k_attn_dkv_dma(AttnAr
   f32x16_v dk[D / 32] = {}, dv[D / 32] = {};
   const T* Q = static_cast<const T*>(a.Q) + sq.q0 * a.ldq;
   const T* G = static_cast<const T*>(a.dO) + sq.q0 * a.lddo;
-  const int64_t at = sq.q0 + (int64_t)t.head * a.group * a.q.rows, more = (int64_t)a.heads * a.q.rows;
-  const int per = t.i1 > t.i0 ? (t.i1 - t.i0 + QT - 1) / QT : 0, count = per * a.group;  // tiles: heads x queries
+  const int64_t at = sq.q0 + (int64_t)t.first * a.q.rows, more = (int64_t)a.heads * a.q.rows;
+  const int per = t.i1 > t.i0 ? (t.i1 - t.i0 + QT - 1) / QT : 0, count = per * t.heads;  // tiles: heads x queries
   const DmaRows<D, QT, C::W> dma(wave);
   const auto fetch = [&](char* b, int h, int i) __attribute__((always_inline)) {
-    const int64_t col = (int64_t)(t.head * a.group + h) * D;
+    const int64_t col = (int64_t)(t.first + h) * D;
     dma.copy(b, Q + col, a.ldq, i, sq.nq, wave);
     dma.copy(b + C::TILE, G + col, a.lddo, i, sq.nq, wave);
     if (wave < 2) {  // 64 values each: wave 0 the lse, wave 1 D
@@ -1006,10 +1047,7 @@ template <int D> __global__ __launch_bounds__(512, 2) void k_attn_dkv_dma(AttnAr
       dk[d][e] = half ? x + dv[d][e] : dk[d][e] + x;
     }
   if (!live) return;
-  if (half)
-    store_row<T, D>(static_cast<T*>(a.out2) + (sq.k0 + j) * a.ldout2 + (int64_t)t.head * D, dk, 1.f, D, lane);
-  else
-    store_row<T, D>(static_cast<T*>(a.out) + (sq.k0 + j) * a.ldout + (int64_t)t.head * D, dk, a.scale, D, lane);
+  store_grad<T, D>(a, t, half, j, dk, D, lane);
 }
 
 int64_t slots_of(int64_t rows, int batch, int R = kRows) { return rows / R + batch; }
@@ -1052,6 +1090,16 @@ int few_part(const AttnDesc& d) {
   return (int)std::max<int64_t>(256, round_up(std::min(d.Tk * d.kv_heads / 512, d.Tk / (2 * d.batch)), kFewKeys));
 }
 
+// How many workgroups share the query heads of a key head in dK and dV: the fewest that divide them and give two
+// workgroups a CU, which their unequal work (causal keys) needs.
+int key_shares(const AttnDesc& d) {
+  const int group = d.heads / d.kv_heads;
+  const int64_t grid = slots_of(d.Tk, d.batch) * d.kv_heads;
+  int n = 1;
+  while (n < group && (group % n || grid * n < 512)) ++n;
+  return n;
+}
+
 }  // namespace
 
 namespace pxk {
@@ -1066,7 +1114,11 @@ size_t attn_fwd_ws_bytes(const AttnDesc& d) {
   if (part == 0 || d.Tk <= part) return 0;  // the latter: no sequence has two parts
   return (size_t)slots_of(d.Tk, d.batch, part) * d.kv_heads * kFewRows * (2 + (d.hd <= 64 ? 64 : 128)) * 4;
 }
-size_t attn_bwd_ws_bytes(const AttnDesc& d) { return (size_t)d.heads * d.Tq * 8; }
+static size_t shares_at(const AttnDesc& d) { return (size_t)round_up((int64_t)d.heads * d.Tq * 8, 256); }
+size_t attn_bwd_ws_bytes(const AttnDesc& d) {
+  const int n = key_shares(d);
+  return shares_at(d) + (n > 1 ? (size_t)n * 2 * d.kv_heads * d.Tk * (d.hd <= 64 ? 64 : 128) * 4 : 0);
+}
 
 hipError_t attn_fwd(const AttnDesc& d, const AttnMat& Q, const AttnMat& K, const AttnMat& V, void* O, int64_t ldo,
                     float* lse, void* ws, hipStream_t s) {
@@ -1137,20 +1189,28 @@ hipError_t attn_bwd(const AttnDesc& d, const AttnMat& dO, const AttnMat& Q, cons
   }
   if (d.Tk == 0) return hipSuccess;
   a.out = dK, a.ldout = lddk, a.out2 = dV, a.ldout2 = lddv;
+  a.shares = key_shares(d);
+  a.parts = reinterpret_cast<float*>(static_cast<char*>(ws) + shares_at(d));
   a.slots = slots_of(d.Tk, d.batch);
   hipError_t e = hipSuccess;
   pick(d, [&](auto t, auto D) {
     typedef decltype(t) T;
     constexpr int W = decltype(D)::value;
-    const dim3 grid((unsigned)(a.slots * d.kv_heads));
+    const dim3 grid((unsigned)(a.slots * d.kv_heads * a.shares));
+    const auto sum = [&] {
+      const int rows = kThreads / (W / 4);
+      if (e == hipSuccess && a.shares > 1)
+        k_attn_dkv_sum<T, W><<<dim3(px::cdiv(d.Tk * d.kv_heads, rows)), kThreads, 0, s>>>(a);
+    };
     if constexpr (sizeof(T) == 2) {
       if (full && dma_rows(Q) && dma_rows(dO) && dma_rows(K) && dma_rows(V)) {
         e = px::lds_once<k_attn_dkv_dma<W>>(Dkv<W>::LDS);
         if (e == hipSuccess) k_attn_dkv_dma<W><<<grid, 64 * Dkv<W>::W, Dkv<W>::LDS, s>>>(a);
-        return;
+        return sum();
       }
     }
     k_attn_dkv<T, W><<<grid, kThreads, 0, s>>>(a);
+    sum();
   });
   return e != hipSuccess ? e : hipGetLastError();
 }
