@@ -59,6 +59,29 @@ PX_DEV uint64_t lane_value(uint64_t v, int lane) {
          (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
 }
 
+// v of the lane below (lane 0: any value): one instruction a word, where a shuffle goes through LDS
+PX_DEV uint64_t from_lane_below(uint64_t v) {
+  constexpr int kWaveShr1 = 0x138;
+  const int lo = __builtin_amdgcn_update_dpp(0, (int)v, kWaveShr1, 0xf, 0xf, false);
+  const int hi = __builtin_amdgcn_update_dpp(0, (int)(v >> 32), kWaveShr1, 0xf, 0xf, false);
+  return ((uint64_t)(uint32_t)hi << 32) | (uint32_t)lo;
+}
+// The n-th largest of the lanes' values, bit by bit.
+PX_DEV uint32_t nth_largest(uint32_t v, int n) {
+  uint64_t in = ~0ull;  // the lanes that agree with the result in the bits so far
+  uint32_t r = 0;
+#pragma unroll
+  for (int b = 31; b >= 0; --b) {
+    const uint64_t ones = __ballot(v >> b & 1) & in;
+    const int k = __popcll(ones);
+    const bool one = k >= n;
+    in = one ? ones : in & ~ones;
+    n -= one ? 0 : k;
+    r |= (uint32_t)one << b;
+  }
+  return r;
+}
+
 // The wave's `top` largest keys, lane i the i-th; 0 (below every key) where there is none.
 struct TopList {
   uint64_t mine = 0, last = 0;  // this lane's; the smallest that is kept
@@ -67,14 +90,14 @@ struct TopList {
   // k is the same in every lane and above `last`
   PX_DEV void put(uint64_t k) {
     const int at = __popcll(__ballot(mine > k));
-    const uint64_t up = __shfl_up(mine, 1);
+    const uint64_t up = from_lane_below(mine);
     const int lane = threadIdx.x & 63;
-    if (lane == at) mine = k;
-    else if (lane > at) mine = up;
+    mine = lane < at ? mine : lane == at ? k : up;
     last = lane_value(mine, top - 1);
   }
-  // every lane's k, the lanes one after another
-  PX_DEV void offer(uint64_t k) {
+  // every lane's k, the lanes one after another; keys under `floor` are known to be too small
+  PX_DEV void offer(uint64_t k, uint64_t floor = 0) {
+    if (k < floor) k = 0;
     uint64_t better = __ballot(k > last);
     while (better) {
       put(lane_value(k, __builtin_ctzll(better)));
@@ -159,8 +182,17 @@ __global__ __launch_bounds__(kThreads) void k_logp_fwd(const T* X, int64_t ldx, 
 #pragma unroll
       for (int i = 0; i < W; ++i) any |= !(f[i] < bar);
       if (__ballot(any)) {
+        // While the list is not full: of the lanes' largest logits here the top-th, below which no logit can be among
+        // the `top` largest.  It spares most of the insertions that an empty list would take.
+        uint64_t floor = 0;
+        if (best.last == 0) {
+          uint32_t most = 0;
 #pragma unroll
-        for (int i = 0; i < W; ++i) best.offer(at + i < c1 ? key_of(f[i], at + i) : 0);
+          for (int i = 0; i < W; ++i) most = max(most, at + i < c1 ? order(f[i]) : 0u);
+          floor = (uint64_t)nth_largest(most, top) << 32;
+        }
+#pragma unroll
+        for (int i = 0; i < W; ++i) best.offer(at + i < c1 ? key_of(f[i], at + i) : 0, floor);
       }
     }
   };
@@ -211,7 +243,7 @@ __global__ __launch_bounds__(kThreads) void k_logp_fwd(const T* X, int64_t ldx, 
   if (TOP && lane < top) part_keys[(int64_t)blockIdx.x * top + lane] = best.mine;
 }
 
-// joins the parts of row blockIdx.x, in order within each wave and then over the waves
+// joins the parts of row blockIdx.x, their sums in one order
 template <typename T>
 __global__ __launch_bounds__(kThreads) void k_logp_join(const T* X, int64_t ldx, int V, int top, float scale,
                                                         int parts, const float4* part_sums, const uint64_t* part_keys,
@@ -219,8 +251,13 @@ __global__ __launch_bounds__(kThreads) void k_logp_join(const T* X, int64_t ldx,
   const int64_t row = blockIdx.x;
   const int wave = threadIdx.x >> 6, lane = threadIdx.x & 63;
   TopList best(top ? top : 1);
-  if (top)
-    for (int p = wave; p < parts; p += kWaves) best.offer_list(part_keys + (row * parts + p) * top);
+  // all parts' keys, 64 at a time; the first ones' top-th is a floor for the rest
+  const uint64_t* list = part_keys + row * parts * top;
+  for (int x = wave * 64; x < parts * top; x += kThreads) {
+    const uint64_t k = x + lane < parts * top ? list[x + lane] : 0;
+    const uint64_t floor = best.last ? 0 : (uint64_t)nth_largest((uint32_t)(k >> 32), top) << 32;
+    best.offer(k, floor);
+  }
   __shared__ uint64_t keys[kWaves][kLogpTop];
   if (lane < top) keys[wave][lane] = best.mine;
   __syncthreads();
