@@ -323,10 +323,6 @@ struct Sees {
     return below(hi) & ~below(lo);
   }
 };
-// x where bit n of `on` is set, else 0
-PX_DEV float where(uint32_t on, int n, float x) {
-  return __uint_as_float(__float_as_uint(x) & (uint32_t)__builtin_amdgcn_sbfe((int)on, n, 1));
-}
 PX_DEV Sees keys_of(const AttnArgs& a, int place, int nk) {
   Sees r;
   r.lo = a.window ? max(place - a.window + 1, 0) : 0;
@@ -772,9 +768,9 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
   const auto step = [&](int tile, int j) __attribute__((always_inline)) {
     const Lane at = (lane_at + tile).here();
     const char *const tk = lds, *const tv = lds + R::bytes(KT);
+    const bool masked = !w.all(j, j + KT);
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      const uint32_t on = see.from(j + 32 * b).bits();
       f32x16_v s = {}, dp = {};
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk)
@@ -782,8 +778,13 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
           mma(s, R::along(tk, at, 32 * b, kk), q[kk]);
           mma(dp, R::along(tv, at, 32 * b, kk), g[kk]);
         }
+      if (masked) {
+        const uint32_t on = see.from(j + 32 * b).bits();
 #pragma unroll
-      for (int e = 0; e < 16; ++e) s[e] = where(on, acc_row(e), prob<T>(s[e], lse, a.scale, c)) * (dp[e] - delta);
+        for (int e = 0; e < 16; ++e) s[e] = on >> acc_row(e) & 1 ? s[e] : -INFINITY;
+      }
+#pragma unroll
+      for (int e = 0; e < 16; ++e) s[e] = prob<T>(s[e], lse, a.scale, c) * (dp[e] - delta);
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const Frag<T> p = to_frag<T>(s, h);
@@ -807,7 +808,7 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
 // the operands of the wave's keys.
 template <typename T, int D, bool FULL, class FK, class FV>
 PX_DEV void dkv_block(f32x16_v (&dk)[D / 32], f32x16_v (&dv)[D / 32], const char* tq, const char* tg, const Lane& at,
-                      const float* rows, const float* deltas, uint32_t on, float scale, float c, int hd, const FK& key,
+                      const float* rows, const float* deltas, bool masked, const Sees& see, float scale, float c, int hd, const FK& key,
                       const FV& value) {
   typedef Rows<T, D> R;
   f32x16_v s = {}, dp = {};
@@ -817,6 +818,11 @@ PX_DEV void dkv_block(f32x16_v (&dk)[D / 32], f32x16_v (&dv)[D / 32], const char
       mma(s, R::along(tq, at, 0, kk), key(kk));
       mma(dp, R::along(tg, at, 0, kk), value(kk));
     }
+  if (masked) {
+    const uint32_t on = see.bits();
+#pragma unroll
+    for (int e = 0; e < 16; ++e) s[e] = on >> acc_row(e) & 1 ? s[e] : -INFINITY;
+  }
 #pragma unroll
   for (int u = 0; u < 4; ++u) {
     const int r = acc_row(4 * u);  // four rows of a lane lie side by side
@@ -825,7 +831,7 @@ PX_DEV void dkv_block(f32x16_v (&dk)[D / 32], f32x16_v (&dv)[D / 32], const char
 #pragma unroll
     for (int x = 0; x < 4; ++x) {
       const int e = 4 * u + x;
-      s[e] = where(on, r + x, prob<T>(s[e], l[x], scale, c));
+      s[e] = prob<T>(s[e], l[x], scale, c);
       dp[e] = s[e] * (dp[e] - dl[x]);
     }
   }
@@ -953,7 +959,7 @@ template <typename T, int D> __global__ __launch_bounds__(kThreads) void k_attn_
       const int p = i + b + t.shift, r = b + 4 * (lane >> 5);
       if (w.any(p, p + 32))
         dkv_block<T, D, false>(dk, dv, lds, lds + R::bytes(QT), lane_at + R::bytes(b), rows[0] + r, rows[1] + r,
-                               see.from(p).bits(), a.scale, c, a.hd, [&](int kk) { return k[kk]; },
+                               !w.all(p, p + 32), see.from(p), a.scale, c, a.hd, [&](int kk) { return k[kk]; },
                                [&](int kk) { return v[kk]; });
     }
   }
@@ -1011,7 +1017,8 @@ template <int D> __global__ __launch_bounds__(512, 2) void k_attn_dkv_dma(AttnAr
     const float* rows = reinterpret_cast<const float*>(lds + tile + 2 * C::TILE) + 32 * half + 4 * (lane >> 5);
     const Lane at = (lane_at + (tile + R::bytes(32 * half))).here(), keys_at = (lane_at + R::bytes(keys)).here();
     if (w.any(p, p + 32))
-      dkv_block<T, D, true>(dk, dv, lds, lds + C::TILE, at, rows, rows + QT, see.from(p).bits(), a.scale, c, D,
+      dkv_block<T, D, true>(dk, dv, lds, lds + C::TILE, at, rows, rows + QT, !w.all(p, p + 32), see.from(p), a.scale,
+                            c, D,
                       [&](int kk) { return R::along(tk, keys_at, 0, kk); },
                       [&](int kk) { return R::along(tv, keys_at, 0, kk); });
   };
