@@ -24,6 +24,7 @@ using namespace pxk;
 
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
+constexpr unsigned kAtOnce = 512;  // workgroups that the card holds of the larger kernels
 constexpr int kRows = 32 * kWaves;  // rows of a workgroup: queries (forward, dQ) or keys (dK, dV), 32 a wave
 
 PX_DEV float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -356,12 +357,45 @@ PX_DEV Span keys_of_wave(const AttnArgs& a, int first, const Seq& sq) {
   return w;
 }
 
-// The slots in the order in which their workgroups start: the tiles of equal sequences side by side, the ones with the
-// most work first (of a causal sequence the last queries, or the first keys), so that the short ones fill the end.
-PX_DEV int64_t slot_of(const AttnArgs& a, int64_t n, bool last_first) {
-  const int64_t per = a.slots / a.batch, t = n / a.batch;
-  if (t < per) n = n % a.batch * per + t;
-  return last_first ? a.slots - 1 - n : n;
+// The n-th tile of R rows in the order in which the workgroups start, which is that of falling work in causal sequences:
+// the k-th tile of a sequence (`ends`: counted from its first row; else from its last) attends to about k tiles, and the
+// tiles of equal k stand side by side.  So the short ones fill the card's end, however the lengths are mixed.  Of up to
+// 64 sequences the order is exact: with f(k) tiles of the k-th class and above, a lane a class,
+//     f(k) = sum over the sequences of max(tiles - k, 0);
+// more sequences are taken as equal ones, and so are those of a launch that the card takes at once (`order` false), which
+// has nothing to fill.  Returns the sequence, with *tile < 0 where there is none.
+PX_DEV int tile_of(const Side& x, int batch, int64_t slots, int64_t n, int R, bool order, bool ends, int* tile) {
+  if (!order || batch > 64) {
+    const int64_t per = slots / batch, t = n / batch;
+    if (t < per) n = n % batch * per + t;
+    return find_seq(x, batch, ends ? slots - 1 - n : n, R, tile);
+  }
+  const int lane = threadIdx.x & 63;
+  const int rows = lane < batch ? (int)max(first_row(x, lane + 1) - first_row(x, lane), (int64_t)0) : 0;
+  const int tiles = (rows + R - 1) / R;
+  int most = 0;
+  for (int s = 0; s < batch; ++s) most = max(most, __builtin_amdgcn_readlane(tiles, s));
+  const auto f = [&](int k) {
+    int sum = 0;
+    for (int s = 0; s < batch; ++s) sum += max(__builtin_amdgcn_readlane(tiles, s) - k, 0);
+    return sum;
+  };
+  int k = 0;  // the class: the last with f(k) > n
+  for (int step = (most + 63) / 64; step > 0; step = step > 1 ? (step + 63) / 64 : 0) {
+    const uint64_t in = __ballot(f(k + lane * step) > n);
+    *tile = -1;
+    if (!in) return 0;
+    k += (__popcll(in) - 1) * step;
+  }
+  if (most == 0) {
+    *tile = -1;
+    return 0;
+  }
+  const int nth = (int)n - f(k + 1);
+  const uint64_t in = __ballot(tiles > k);
+  const int s = __builtin_ctzll(__ballot(tiles > k && __popcll(in & ((1ull << lane) - 1)) == nth));
+  *tile = ends ? k : __builtin_amdgcn_readlane(tiles, s) - 1 - k;
+  return s;
 }
 
 // f(offset of the K tile, which the V tile follows, first key) over the tiles of the keys [j0, j1), which are the same for the whole workgroup
@@ -431,7 +465,7 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
   const int lane = threadIdx.x & 63, wave = wave_id(), hd = DMA ? D : a.hd;
   const int head = head_of(a, blockIdx.x % a.heads);
   int tile;
-  const Seq sq = sequence(a, find_seq(a.q, a.batch, slot_of(a, blockIdx.x / a.heads, true), kRows, &tile));
+  const Seq sq = sequence(a, tile_of(a.q, a.batch, a.slots, blockIdx.x / a.heads, kRows, gridDim.x > kAtOnce, true, &tile));
   const int w0 = tile * kRows;
   if (tile < 0 || w0 >= sq.nq) return;
   const int shift = sq.nk - sq.nq, i = w0 + 32 * wave + (lane & 31);  // this lane's query
@@ -672,25 +706,25 @@ template <typename T, int D> __global__ __launch_bounds__(kThreads) void k_attn_
   const Seq sq = sequence(a, s);
   const int kv = head / a.group, row = (int)(i - sq.q0) * a.group + head % a.group, parts = parts_of(a, sq);
   if (sq.nq * a.group > kFewRows || parts == 1) return;  // complete
-  constexpr int kAtOnce = 16;
+  constexpr int kGroup = 16;
   const int64_t slot = (int64_t)((uint32_t)sq.k0 / (uint32_t)a.part) + s;
   const float c = a.scale * kLog2e;
   const float2* const sums = reinterpret_cast<const float2*>(a.rows);
   float m = -INFINITY, sum = 0.f, o[D / 64] = {};
-  for (int x0 = 0; x0 < parts; x0 += kAtOnce) {
+  for (int x0 = 0; x0 < parts; x0 += kGroup) {
     // 16 parts: their maxima and sums a part a lane, their O a part a register, all on the way together
-    const int n = min(parts - x0, kAtOnce);
+    const int n = min(parts - x0, kGroup);
     float2 ml = make_float2(-INFINITY, 0.f);
     if (lane < n) ml = sums[part_row(a, slot + x0 + lane, kv) + row];
-    float v[kAtOnce][D / 64];
+    float v[kGroup][D / 64];
 #pragma unroll
-    for (int x = 0; x < kAtOnce; ++x)
+    for (int x = 0; x < kGroup; ++x)
 #pragma unroll
       for (int e = 0; e < D / 64; ++e)
         v[x][e] = a.rows[a.part_head + (part_row(a, slot + x0 + min(x, n - 1), kv) + row) * D + 64 * e + lane];
     float top = fmaxf(m, ml.x);
 #pragma unroll
-    for (int d = 1; d < kAtOnce; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
+    for (int d = 1; d < kGroup; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
     top = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(top), 0));
     const float base = top == -INFINITY ? 0.f : top, keep = exp2_of((m - base) * c);
     m = top;
@@ -702,7 +736,7 @@ template <typename T, int D> __global__ __launch_bounds__(kThreads) void k_attn_
     for (int e = 0; e < D / 64; ++e) o[e] *= keep;
     const uint64_t there = __ballot(!none);
 #pragma unroll
-    for (int x = 0; x < kAtOnce; ++x) {
+    for (int x = 0; x < kGroup; ++x) {
       const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), x));
 #pragma unroll
       for (int e = 0; e < D / 64; ++e) o[e] += there >> x & 1 ? w * v[x][e] : 0.f;
@@ -731,7 +765,7 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
   const int lane = threadIdx.x & 63, wave = wave_id(), hd = DMA ? D : a.hd;
   const int head = head_of(a, blockIdx.x % a.heads);
   int tile;
-  const Seq sq = sequence(a, find_seq(a.q, a.batch, slot_of(a, blockIdx.x / a.heads, true), kRows, &tile));
+  const Seq sq = sequence(a, tile_of(a.q, a.batch, a.slots, blockIdx.x / a.heads, kRows, gridDim.x > kAtOnce, true, &tile));
   const int w0 = tile * kRows;
   if (tile < 0 || w0 >= sq.nq) return;
   const int shift = sq.nk - sq.nq, i = w0 + 32 * wave + (lane & 31);
@@ -862,7 +896,8 @@ PX_DEV KeyTile key_tile(const AttnArgs& a, int QT) {
   k.heads = a.group / a.shares;
   k.first = k.head * a.group + k.share * k.heads;
   int tile;
-  k.sq = sequence(a, find_seq(a.k, a.batch, slot_of(a, blockIdx.x / kv_heads / a.shares, false), kRows, &tile));
+  k.sq = sequence(a, tile_of(a.k, a.batch, a.slots, blockIdx.x / kv_heads / a.shares, kRows, gridDim.x > kAtOnce, false,
+                            &tile));
   k.w0 = tile * kRows;
   k.any = tile >= 0 && k.w0 < k.sq.nk;
   k.shift = k.sq.nk - k.sq.nq;
