@@ -551,6 +551,44 @@ def time_secondary(key, to_dev, dev):
     return out
 
 
+def time_attention(wl, seq, dev, reps):
+    """Rotary positions and causal attention of a decoder-layer workload, forward and backward, on random rows."""
+    import torch
+
+    from orthogonal_reparameterized_cnp_amd.layer import PoetxAttention, PoetxRope
+
+    cols = {L.name: L.n for L in wl.linears}
+    if not {"q", "k", "v"} <= set(cols):
+        raise SystemExit("--attention takes a decoder-layer workload")
+    hd = 128 if cols["q"] >= 2048 else 64
+    seq = min(seq, wl.T)
+    if seq < 1 or wl.T % seq:
+        raise SystemExit(f"--attention: {wl.T} tokens are not whole sequences of {seq}")
+    heads, kv, n = cols["q"] // hd, cols["k"] // hd, wl.T // seq
+    new = lambda c: torch.randn(wl.T, c, device=dev).to({"f32": torch.float32, "bf16": torch.bfloat16}[wl.act])
+    Q, K, V, dO = new(cols["q"]), new(cols["k"]), new(cols["v"]), new(cols["q"])
+    pos = (torch.arange(wl.T, device=dev) % seq).int()
+    rope, attn = PoetxRope(hd, act=wl.act, device=str(dev)), PoetxAttention(heads, kv, hd, wl.act, device=str(dev))
+    r = {}
+
+    def fwd():
+        r["q"], r["k"] = rope.forward([Q, K], pos)
+        attn.forward(r["q"], r["k"], V, batch=n)
+
+    def bwd():
+        dQ, dK, r["dv"] = attn.backward(dO)
+        rope.backward([dQ, dK], pos, [dQ, dK])
+
+    out = {"heads": heads, "kv_heads": kv, "head_dim": hd, "sequences": n, "seq_len": seq}
+    fwd()
+    bwd()
+    for name, f, flops in (("forward", fwd, 4.0), ("backward", bwd, 10.0)):
+        ms, _ = timed(f, reps)
+        out[f"{name}_ms"] = ms
+        out[f"{name}_tflops"] = flops * hd * heads * n * seq * (seq + 1) / 2 / (ms * 1e-3) / 1e12
+    return out
+
+
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--gpus", type=int, default=1)
@@ -578,6 +616,10 @@ def main():
     ap.add_argument("--muon", action="store_true",
                     help="also time the orthogonalised step of every side (poetx_muon_step_batch), outside the timed "
                          "region")
+    ap.add_argument("--attention", metavar="SEQ", nargs="?", const=4096, type=int, default=None,
+                    help="also time what stands between the q, k, v linears and the o linear on the workload's tokens, as "
+                         "sequences of SEQ (default 4096): rotary positions and causal attention, forward and backward, "
+                         "outside the timed step (decoder-layer workloads)")
     ap.add_argument("--graph", action="store_true",
                     help="capture one step into a HIP graph and time its replays (the W~ contraction rate then "
                          "comes from an eager pass of the same length)")
@@ -749,6 +791,9 @@ def main():
         muon_ms, _ = timed(lambda: muon.step(dqs), max(3, args.steps // 2))
         result["muon_step"] = {"kernel": "momentum, 5 Newton-Schulz steps per block, decay (all sides)", "ms": muon_ms}
         del muon
+
+    if args.attention:
+        result["attention_step"] = time_attention(wl, args.attention, dev, max(3, args.steps // 2))
 
     if args.breakdown:
         for name, kc in (("gemm", B.POETX_KC_GEMM), ("apply", B.POETX_KC_APPLY), ("dgrad", B.POETX_KC_DGRAD),

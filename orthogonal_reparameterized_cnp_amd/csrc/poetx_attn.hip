@@ -184,7 +184,7 @@ template <typename T, int D, int N> struct Staged {
 };
 // The same by direct global -> LDS copies, 16 bytes a lane, for heads that fill the tile (bf16, hd = D, rows aligned to
 // 16 bytes, pitches of up to kDmaLd).  Rows behind the last repeat it; what is computed from them is masked.
-constexpr int64_t kDmaLd = 1 << 24;  // a tile's rows lie within 32 bits
+constexpr int64_t kDmaLd = 1 << 23;  // a tile's rows lie within 32 bits
 template <int D, int N, int W> struct DmaRows {
   static constexpr int C = D / 8, RPW = 64 / C, STEP = W * RPW;  // rows of a wave's copy, of the W waves'
   int r, lane;  // this lane's row in the first copy

@@ -1,0 +1,161 @@
+"""GPU parity of the attention where its calls take other ways than at small sizes: more workgroups than the card holds at
+once (their order, and key heads whose query heads one workgroup sums alone), the forward of few rows (rows of several
+heads in a tile, many parts, sequences of more than a tile), and offsets past 32 bits.  Bounds as in
+tests/test_gpu_attention.py."""
+
+import numpy as np
+import pytest
+import torch
+
+import oracle as O
+from orthogonal_reparameterized_cnp_amd import binding as B
+from orthogonal_reparameterized_cnp_amd.layer import PoetxAttention, PoetxLogProb, PoetxRope
+
+from . import test_gpu_attention as A
+from . import test_gpu_logp as LP
+from . import test_gpu_rope as R
+
+pytestmark = [
+    pytest.mark.gpu,
+    pytest.mark.skipif(not torch.cuda.is_available(), reason="needs a GPU"),
+]
+
+
+def _lens(n, most, seed):
+    rng = np.random.default_rng(seed)
+    lens = rng.integers(0, most, n)
+    lens[n // 2] = most
+    lens[n // 3] = 0
+    return [int(x) for x in lens]
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("causal", [True, False])
+def test_more_workgroups_than_the_card_holds(act, causal):
+    lens = _lens(20, 300, 1)
+    A.run(64, 16, 16, act, lens, lens, causal)
+    A.run(64, 16, 64, act, [256] * 9, [256] * 9, causal, seed=5)
+    # more sequences than a wave has lanes
+    lens = _lens(100, 60, 2)
+    A.run(16, 8, 64, act, lens, lens, causal, seed=9)
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+def test_queries_and_keys_of_other_lengths_in_order(act):
+    lq, lk = _lens(30, 200, 3), _lens(30, 400, 4)
+    A.run(32, 32, 32, act, lq, lk, True)
+    A.run(32, 32, 128, act, lq[:12], lk[:12], False, window=70, seed=7)
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("heads,kv,hd,lq,lk", [
+    (2, 1, 64, [1], [20000]),  # 79 parts
+    (32, 1, 128, [1, 1, 1], [3000, 600, 1]),  # a full tile of rows
+    (32, 1, 64, [2, 0, 0, 0], [2000, 5, 0, 700]),  # more rows than a tile: tiles shared, not keys
+    (24, 8, 128, [1, 0, 2, 3, 1], [1500, 9, 1300, 2, 0]),
+    (5, 5, 75, [1] * 70, list(range(0, 350, 5))),  # more sequences than a wave has lanes
+    (8, 2, 96, [1, 2], [4000, 900]),
+])
+def test_few_rows(act, heads, kv, hd, lq, lk):
+    A.run(heads, kv, hd, act, lq, lk)
+    A.run(heads, kv, hd, act, lq, lk, window=500, seed=3)  # parts that no row sees
+    A.run(heads, kv, hd, act, lq, lk, causal=False, seed=6, first=3, behind=2)
+
+
+def test_few_rows_leave_others_alone():
+    """Single tokens with rows between the last sequence and the end, an O of another pitch."""
+    at = PoetxAttention(8, 2, 64)
+    cu_q, cu_k = A.cu_of([1, 1, 1], 2), A.cu_of([900, 0, 1200], 1)
+    mats = [A.rows(9, 512, "bf16", 1), A.rows(2110, 128, "bf16", 2), A.rows(2110, 128, "bf16", 3)]
+    out = torch.full((9, 520), A.MARK, dtype=torch.bfloat16, device="cuda")
+    at.forward(*mats, A.dev(cu_q), A.dev(cu_k), O=out[:, :512])
+    assert (out[:2] == A.MARK).all() and (out[5:] == A.MARK).all() and (out[:, 512:] == A.MARK).all()
+    assert not out[3, :512].any() and torch.isneginf(at.saved[4][:, 3]).all() and out[2, :512].any()
+
+
+def test_few_rows_in_a_graph():
+    at, other = PoetxAttention(8, 2, 64), PoetxAttention(8, 2, 64)
+    mats = [A.rows(3, 512, "bf16", 1), A.rows(4000, 128, "bf16", 2), A.rows(4000, 128, "bf16", 3)]
+    cu_q, cu_k = A.dev(A.cu_of([1, 1, 1])), A.dev(A.cu_of([100, 3000, 900]))
+    at.forward(*mats, cu_q, cu_k)
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = at.forward(*mats, cu_q, cu_k)
+    for i in range(3):
+        for k, m in enumerate(mats):
+            m.copy_(A.rows(len(m), m.shape[1], "bf16", 20 + 3 * i + k))
+        # other lengths at replay: the offsets are read on the device
+        cu_k.copy_(A.dev(A.cu_of([100 + 500 * i, 3000 - 700 * i, 900 - 50 * i])))
+        ref = other.forward(*mats, cu_q, cu_k).clone()
+        torch.cuda.synchronize()
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out, ref)
+
+
+@pytest.mark.parametrize("pitch,T", [(1 << 20, 2200), ((1 << 24) + 8, 140)])
+def test_offsets_past_32_bits(pitch, T):
+    """Q, K and V as columns of one buffer of more than 2^31 elements, by direct copies and (the wider pitch) without."""
+    heads, kv, hd = 2, 1, 64
+    lens = [T - 100, 100]
+    cu = A.cu_of(lens)
+    buf = A.rows(T, 256, "bf16", 1, pitch)
+    mats = (buf[:, :128], buf[:, 128:192], buf[:, 192:])
+    at = PoetxAttention(heads, kv, hd)
+    c = O.Attn(heads, kv, hd, float(np.float32(at.desc.scale)))
+    dO = A.rows(T, 128, "bf16", 2, pitch)
+    out = at.forward(*mats, A.dev(cu))
+    grads = at.backward(dO)
+    A.check(at, c, "bf16", mats, dO, out, at.saved[4], grads, cu, cu)
+    # single tokens over the same keys
+    q = A.rows(2, 128, "bf16", 3)
+    cu1 = A.cu_of([1, 1])
+    out = at.forward(q, mats[1], mats[2], A.dev(cu1), A.dev(cu))
+    g1 = A.rows(2, 128, "bf16", 4)
+    grads = at.backward(g1)
+    A.check(at, c, "bf16", (q, *mats[1:]), g1, out, at.saved[4], grads, cu1, cu)
+
+
+def test_offsets_past_32_bits_of_the_others():
+    T, pitch = 2200, 1 << 20
+    X = R.rows(T, 256, "bf16", 1, pitch)
+    rope = PoetxRope(64)
+    pos = torch.arange(T, dtype=torch.int32, device="cuda")
+    R.check(rope, X, rope.forward([X], pos, [X.new_empty(T, 256)])[0], pos)
+    op = PoetxLogProb(256, "bf16", top=3)
+    t = LP.targets(T, 256, 1)
+    LP.check_forward(op, X, t, op.forward(X, t))
+    a = torch.randn(T, device="cuda")
+    LP.check_backward(op, X, t, op.saved, a, a, op.backward(a, a))
+
+
+def test_workspaces_hold_what_the_calls_write():
+    """A call with exactly the bytes that were asked for leaves the bytes behind them alone."""
+    for lq, lk, heads, kv, hd in (([1, 1], [3000, 700], 8, 2, 64), ([130, 70], [130, 70], 8, 2, 128), ([1], [2000], 3, 1, 75)):
+        cu_q, cu_k = A.cu_of(lq), A.cu_of(lk)
+        Tq, Tk = int(cu_q[-1]), int(cu_k[-1])
+        d = B.attn_desc(heads, kv, hd, "bf16")
+        nq, nk = heads * hd, kv * hd
+        q, k, v, g = (A.rows(T, n, "bf16", s) for T, n, s in ((Tq, nq, 1), (Tk, nk, 2), (Tk, nk, 3), (Tq, nq, 4)))
+        o, lse = torch.empty_like(q), torch.empty(heads, Tq, device="cuda")
+        args = (len(lq), Tq, Tk, A.dev(cu_q), A.dev(cu_k))
+        for op in (B.POETX_OP_FWD, B.POETX_OP_BWD):
+            n = B.poetx_attn_workspace_size(d, len(lq), Tq, Tk, op)
+            ws = torch.full((n + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+            if op == B.POETX_OP_FWD:
+                B.poetx_attn_fwd(d, *args, q, nq, k, nk, v, nk, o, nq, lse, ws, n)
+            else:
+                dq, dk, dv = torch.empty_like(q), torch.empty_like(k), torch.empty_like(v)
+                B.poetx_attn_bwd(d, *args, g, nq, q, nq, k, nk, v, nk, o, nq, lse, dq, nq, dk, nk, dv, nk, ws, n)
+            torch.cuda.synchronize()
+            assert (ws[n:] == 0x5A).all()
+    for T, V, top in ((1, 131072, 64), (3, 50001, 5), (600, 9000, 0)):
+        d = B.logp_desc(V, "bf16", top)
+        n = B.poetx_logp_workspace_size(d, T)
+        ws = torch.full((n + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+        X, t = LP.logits(T, V, "bf16", 1), LP.targets(T, V, 1)
+        new = lambda *s, dt=torch.float32: torch.empty(*s, dtype=dt, device="cuda")
+        B.poetx_logp_fwd(d, T, X, V, t, new(T), new(T), new(T), new(T, top, dt=torch.int32) if top else None,
+                         new(T, top) if top else None, ws, n)
+        torch.cuda.synchronize()
+        assert (ws[n:] == 0x5A).all()
