@@ -151,53 +151,66 @@ template <int D> struct Rows<float, D> {
   }
 };
 
-// whether column c is in the head: known where the head fills the tile
-template <bool FULL> PX_DEV bool within(int c, int hd) { return FULL || c < hd; }
+// Kernels are built for C columns, the head's rounded up.  bf16 has C = 32, 64, 96 and 128 and multiplies with as many,
+// in tiles whose rows hold 64 or 128 for the sake of the banks; fp32, whose products take longer than to ask for each
+// whether the head reaches it, has 64 and 128.
+template <typename T, int C> using RowsOf = Rows<T, sizeof(T) == 4 ? C : C <= 64 ? 64 : 128>;
+
+// whether the columns from c on are multiplied with
+template <typename T> PX_DEV bool within(int c, int hd) { return sizeof(T) == 2 || c < hd; }
+
+// How tiles come to LDS: through registers, by direct copies, which take heads of a multiple of 8 columns, and
+// by direct copies of heads that fill the rows, which need not ask where the head ends.
+enum How { kStaged, kDirect, kWhole };
 
 // 8 elements from column c of a head's row, zeros behind its end and for absent rows
-template <typename T> PX_DEV void load8(T (&v)[8], const T* row, bool there, int c, int hd) {
+template <int HOW, typename T> PX_DEV void load8(T (&v)[8], const T* row, bool there, int c, int hd) {
   if (there && c + 8 <= hd) {
     __builtin_memcpy(v, row + c, sizeof(v));
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = there && c + i < hd ? row[c + i] : T(0);
+    for (int i = 0; i < 8; ++i) v[i] = HOW == kStaged && there && c + i < hd ? row[c + i] : T(0);
   }
 }
 // rows [r0, r0 + N) of a sequence's `n`, into an LDS tile by way of registers: any type, head and alignment
-template <typename T, int D, int N> struct Staged {
-  static constexpr int C = D / 8, EACH = N * C / kThreads;
+template <typename T, int C, int N> struct Staged {
+  static constexpr int K = C / 8, ALL = N * K, EACH = (ALL + kThreads - 1) / kThreads;
+  static PX_DEV bool in(int x) { return ALL % kThreads == 0 || x < ALL; }
   T v[EACH][8];
   PX_DEV void load(const T* base, int64_t ld, int r0, int n, int hd) {
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
-      const int x = i * kThreads + (int)threadIdx.x, r = x / C, c = x % C;
-      load8<T>(v[i], base + (int64_t)(r0 + r) * ld, r0 + r < n, 8 * c, hd);
+      const int x = i * kThreads + (int)threadIdx.x, r = x / K, c = x % K;
+      load8<kStaged>(v[i], base + (int64_t)(r0 + r) * ld, in(x) && r0 + r < n, 8 * c, hd);
     }
   }
   PX_DEV void put(char* tile) const {
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
       const int x = i * kThreads + (int)threadIdx.x;
-      Rows<T, D>::put(tile, x / C, x % C, v[i]);
+      if (in(x)) RowsOf<T, C>::put(tile, x / K, x % K, v[i]);
     }
   }
 };
-// The same by direct global -> LDS copies, 16 bytes a lane, for heads that fill the tile (bf16, hd = D, rows aligned to
-// 16 bytes, pitches of up to kDmaLd).  Rows behind the last repeat it; what is computed from them is masked.
+// The same by direct global -> LDS copies, 16 bytes a lane, for bf16 heads of a multiple of 8 columns in rows aligned to
+// 16 bytes (pitches of up to kDmaLd).  Rows behind the last repeat it; what is computed from them is masked.  Columns
+// behind the head are left alone: zero_tail() clears them once.
 constexpr int64_t kDmaLd = 1 << 23;  // a tile's rows lie within 32 bits
-template <int D, int N, int W> struct DmaRows {
-  static constexpr int C = D / 8, RPW = 64 / C, STEP = W * RPW;  // rows of a wave's copy, of the W waves'
+template <int C, int N, int W> struct DmaRows {
+  typedef RowsOf<bf16_t, C> R;
+  static constexpr int K = R::CPR, RPW = 64 / K, STEP = W * RPW;  // rows of a wave's copy, of the W waves'
   int r, lane;  // this lane's row in the first copy
-  PX_DEV explicit DmaRows(int wave) : r(wave * RPW + ((int)threadIdx.x & 63) / C), lane((int)threadIdx.x & 63) {}
+  PX_DEV explicit DmaRows(int wave) : r(wave * RPW + ((int)threadIdx.x & 63) / K), lane((int)threadIdx.x & 63) {}
   // rows [r0, r0 + N) of the `n` at base; `wave` as above
-  PX_DEV void copy(char* tile, const bf16_t* base, int64_t ld, int r0, int n, int wave) const {
+  PX_DEV void copy(char* tile, const bf16_t* base, int64_t ld, int r0, int n, int hd, int wave) const {
     static_assert(N % STEP == 0, "whole copies");
     char* t = tile + wave * 1024;
     const char* g = reinterpret_cast<const char*>(base + r0 * ld);
     const int pitch = 2 * (int)ld, last = n - 1 - r0;
 #pragma unroll
     for (int i = 0; i < N / STEP; ++i) {
-      const int row = r + i * STEP, c = 16 * (lane % C ^ Rows<bf16_t, D>::swz(row));
+      const int row = r + i * STEP, c = 16 * (lane % K ^ R::swz(row));
+      if (hd < 8 * K && c >= 2 * hd) continue;
       if (last >= N - 1)
         put(t + i * W * 1024, g + (int64_t)i * STEP * pitch, (uint32_t)(r * pitch + c));
       else
@@ -208,21 +221,27 @@ template <int D, int N, int W> struct DmaRows {
     __builtin_amdgcn_global_load_lds(base + at, (__attribute__((address_space(3))) void*)t, 16, 0, 0);
   }
 };
+// the columns behind the head, of `rows` rows of an LDS tile, by `threads` threads of which this is the x-th
+template <int C> PX_DEV void zero_tail(char* tile, int rows, int hd, int x, int threads) {
+  const int k = (C - hd) / 8;  // chunks of 8
+  const bf16_t zeros[8] = {};
+  for (int i = x; i < rows * k; i += threads) RowsOf<bf16_t, C>::put(tile, i / k, hd / 8 + i % k, zeros);
+}
 // the operand fragments of one row, held in registers
-template <typename T, int D>
-PX_DEV void row_frags(Frag<T> (&f)[D / 16], const T* row, bool there, int hd, int lane) {
+template <typename T, int C, int HOW>
+PX_DEV void row_frags(Frag<T> (&f)[C / 16], const T* row, bool there, int hd, int lane) {
 #pragma unroll
-  for (int kk = 0; kk < D / 16; ++kk) {
+  for (int kk = 0; kk < C / 16; ++kk) {
     T v[8];
-    load8<T>(v, row, there, 16 * kk + 8 * (lane >> 5), hd);
+    load8<HOW>(v, row, there, 16 * kk + 8 * (lane >> 5), hd);
     __builtin_memcpy(&f[kk], v, sizeof(v));
   }
 }
 // a lane's accumulator column as row elements: 4 consecutive of them at a time
-template <typename T, int D>
-PX_DEV void store_row(T* row, const f32x16_v (&acc)[D / 32], float scale, int hd, int lane) {
+template <typename T, int C, int HOW>
+PX_DEV void store_row(T* row, const f32x16_v (&acc)[C / 32], float scale, int hd, int lane) {
 #pragma unroll
-  for (int d = 0; d < D / 32; ++d)
+  for (int d = 0; d < C / 32; ++d)
 #pragma unroll
     for (int g = 0; g < 4; ++g) {
       const int c = 32 * d + 8 * g + 4 * (lane >> 5);
@@ -231,7 +250,7 @@ PX_DEV void store_row(T* row, const f32x16_v (&acc)[D / 32], float scale, int hd
       for (int i = 0; i < 4; ++i) v[i] = from_f32<T>(acc[d][4 * g + i] * scale);
       if (c + 4 <= hd) {
         __builtin_memcpy(row + c, v, sizeof(v));
-      } else {
+      } else if constexpr (HOW == kStaged) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (c + i < hd) row[c + i] = v[i];
@@ -251,7 +270,7 @@ struct AttnArgs {
   int64_t ldout, ldout2;
   float *lse, *rows;  // rows: the backward's lse and D of every query, [2][heads][Tq]; the parts of few rows, pairs of
                       // maximum and sum and from part_head on their O
-  float* parts;       // the shares' dK and dV, [shares][2][kv_heads][Tk][D]
+  float* parts;       // the shares' dK and dV, [shares][2][kv_heads][Tk][C]
   Side q, k;
   int batch, heads, group, hd, window;
   int part;    // keys of a workgroup in the forward of few rows
@@ -399,20 +418,21 @@ PX_DEV int tile_of(const Side& x, int batch, int64_t slots, int64_t n, int R, bo
 }
 
 // f(offset of the K tile, which the V tile follows, first key) over the tiles of the keys [j0, j1), which are the same for the whole workgroup
-template <typename T, int D, bool DMA, int KT, class F>
+template <typename T, int C, int HOW, int KT, class F>
 PX_DEV void over_tiles(char* lds, const T* K, int64_t ldk, const T* V, int64_t ldv, int n, int hd, int j0, int j1,
                        const F& f) {
-  typedef Rows<T, D> R;
+  typedef RowsOf<T, C> R;
   const auto at = [&](int x) { return lds + x * R::bytes(KT); };
-  if constexpr (DMA) {
+  if constexpr (HOW != kStaged) {
     if (j0 >= j1) return;
     const int wave = wave_id();
-    const DmaRows<D, KT, kWaves> dma(wave);
+    const DmaRows<C, KT, kWaves> dma(wave);
     const auto copy = [&](int x, int j) __attribute__((always_inline)) {
-      dma.copy(at(x), K, ldk, j, n, wave);
-      dma.copy(at(x + 1), V, ldv, j, n, wave);
+      dma.copy(at(x), K, ldk, j, n, hd, wave);
+      dma.copy(at(x + 1), V, ldv, j, n, hd, wave);
     };
     copy(0, j0);
+    zero_tail<C>(lds, 4 * KT, hd, (int)threadIdx.x, kThreads);
     for (int j = j0, x = 0; j < j1; j += KT, x ^= 2) {
       __syncthreads();  // this tile is there, and the other buffer is done with
       if (j + KT < j1) copy(2 - x, j + KT);
@@ -420,7 +440,7 @@ PX_DEV void over_tiles(char* lds, const T* K, int64_t ldk, const T* V, int64_t l
     }
   } else if constexpr (KT <= 64) {
     // the next tile's rows come into registers while this one is computed with
-    Staged<T, D, KT> k, v;
+    Staged<T, C, KT> k, v;
     const auto load = [&](int j) __attribute__((always_inline)) {
       k.load(K, ldk, j, n, hd);
       v.load(V, ldv, j, n, hd);
@@ -438,7 +458,7 @@ PX_DEV void over_tiles(char* lds, const T* K, int64_t ldk, const T* V, int64_t l
     for (int j = j0; j < j1; j += KT) {
       __syncthreads();
       for (int x = 0; x < KT; x += 32) {
-        Staged<T, D, 32> k, v;
+        Staged<T, C, 32> k, v;
         k.load(K, ldk, j + x, n, hd);
         v.load(V, ldv, j + x, n, hd);
         k.put(at(0) + R::bytes(x));
@@ -458,11 +478,11 @@ template <typename T> constexpr int kTile = sizeof(T) == 2 ? 64 : 32;  // keys (
 // 2^kSlack, which costs no digits, and the accumulators need no rescaling.
 constexpr float kSlack = 8.f;
 
-template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DMA ? 2 : 1) void k_attn_fwd(AttnArgs a) {
-  constexpr int KT = kTile<T>, NB = KT / 32, BUFS = DMA ? 2 : 1;
-  typedef Rows<T, D> R;
+template <typename T, int C, int HOW> __global__ __launch_bounds__(kThreads, HOW ? 2 : 1) void k_attn_fwd(AttnArgs a) {
+  constexpr int KT = kTile<T>, NB = KT / 32, BUFS = HOW ? 2 : 1;
+  typedef RowsOf<T, C> R;
   __shared__ __align__(16) char lds[BUFS * 2 * R::bytes(KT)];
-  const int lane = threadIdx.x & 63, wave = wave_id(), hd = DMA ? D : a.hd;
+  const int lane = threadIdx.x & 63, wave = wave_id(), hd = HOW == kWhole ? C : a.hd;
   const int head = head_of(a, blockIdx.x % a.heads);
   int tile;
   const Seq sq = sequence(a, tile_of(a.q, a.batch, a.slots, blockIdx.x / a.heads, kRows, gridDim.x > kAtOnce, true, &tile));
@@ -472,23 +492,23 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
   const bool live = i < sq.nq;
   const T* K = static_cast<const T*>(a.K) + sq.k0 * a.ldk + (int64_t)(head / a.group) * hd;
   const T* V = static_cast<const T*>(a.V) + sq.k0 * a.ldv + (int64_t)(head / a.group) * hd;
-  Frag<T> q[D / 16];
-  row_frags<T, D>(q, static_cast<const T*>(a.Q) + (sq.q0 + i) * a.ldq + (int64_t)head * hd, live, hd, lane);
+  Frag<T> q[C / 16];
+  row_frags<T, C, HOW>(q, static_cast<const T*>(a.Q) + (sq.q0 + i) * a.ldq + (int64_t)head * hd, live, hd, lane);
   const Sees see = live ? keys_of(a, i + shift, sq.nk) : Sees{0, 0};
   const int last = min(w0 + kRows, sq.nq) - 1;
   const int j0 = keys_of(a, w0 + shift, sq.nk).lo / KT * KT, j1 = keys_of(a, last + shift, sq.nk).hi;
   const Span w = keys_of_wave(a, w0 + 32 * wave, sq);
   const float c = a.scale * kLog2e;
   const Lane lane_at = R::lane_at();
-  f32x16_v acc[D / 32] = {};
+  f32x16_v acc[C / 32] = {};
   float m = -INFINITY, l = 0.f;
   const auto step = [&](int tile, int j, auto masked) __attribute__((always_inline)) {
     const Lane at = (lane_at + tile).here();
     const char *const tk = lds, *const tv = lds + R::bytes(KT);
     f32x16_v s[NB] = {};
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk)
-      if (within<DMA>(16 * kk, hd))
+    for (int kk = 0; kk < C / 16; ++kk)
+      if (within<T>(16 * kk, hd))
 #pragma unroll
         for (int b = 0; b < NB; ++b) mma(s[b], R::along(tk, at, 32 * b, kk), q[kk]);
     float top = -INFINITY;
@@ -507,7 +527,7 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
       const float keep = exp2_of((was - (m == -INFINITY ? 0.f : m)) * c);
       l *= keep;
 #pragma unroll
-      for (int d = 0; d < D / 32; ++d) acc[d] *= keep;
+      for (int d = 0; d < C / 32; ++d) acc[d] *= keep;
     }
     const float base = m == -INFINITY ? 0.f : m;  // no key so far
 #pragma unroll
@@ -524,18 +544,18 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
       for (int h = 0; h < 2; ++h) {
         const Frag<T> p = to_frag<T>(s[b], h);
 #pragma unroll
-        for (int d = 0; d < D / 32; ++d)
-          if (within<DMA>(32 * d, hd)) mma(acc[d], R::across(tv, at, 32 * b + 16 * h, 32 * d), p);
+        for (int d = 0; d < C / 32; ++d)
+          if (within<T>(32 * d, hd)) mma(acc[d], R::across(tv, at, 32 * b + 16 * h, 32 * d), p);
       }
   };
-  over_tiles<T, D, DMA, KT>(lds, K, a.ldk, V, a.ldv, sq.nk, hd, j0, j1,
+  over_tiles<T, C, HOW, KT>(lds, K, a.ldk, V, a.ldv, sq.nk, hd, j0, j1,
                             [&](int tile, int j) __attribute__((always_inline)) {
                               if (w.all(j, j + KT)) step(tile, j, std::false_type());
                               else if (w.any(j, j + KT)) step(tile, j, std::true_type());
                             });
   if (!live) return;
   l = sum_halves(l);
-  store_row<T, D>(static_cast<T*>(a.out) + (sq.q0 + i) * a.ldout + (int64_t)head * hd, acc, l == 0.f ? 0.f : 1.f / l,
+  store_row<T, C, HOW>(static_cast<T*>(a.out) + (sq.q0 + i) * a.ldout + (int64_t)head * hd, acc, l == 0.f ? 0.f : 1.f / l,
                   hd, lane);
   if (lane < 32) a.lse[(int64_t)head * a.q.rows + sq.q0 + i] = l == 0.f ? -INFINITY : m * a.scale + kLn2 * log2f(l);
 }
@@ -550,22 +570,22 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
 // adds the parts in their order.  Where a sequence has more rows than a tile all the same, its workgroups share the
 // tiles instead, each with all keys.
 constexpr int kFewRows = 32, kFewKeys = 32 * kWaves;
-template <typename T, int D, bool DMA> struct Few {
-  static constexpr int TILES = 2 * Rows<T, D>::bytes(kFewKeys);
-  static constexpr int JOIN = kWaves * 64 * (D / 2 + 2) * 4;
+template <typename T, int C> struct Few {
+  static constexpr int TILES = 2 * RowsOf<T, C>::bytes(kFewKeys);
+  static constexpr int JOIN = kWaves * 64 * (C / 2 + 2) * 4;
   static constexpr int LDS = TILES > JOIN ? TILES : JOIN;
 };
 PX_DEV int parts_of(const AttnArgs& a, const Seq& sq) { return max((sq.nk + a.part - 1) / a.part, 1); }
-// where the O of part slot and key head `kv` is among the parts, in rows of D floats; its maxima and sums lie before
+// where the O of part slot and key head `kv` is among the parts, in rows of C floats; its maxima and sums lie before
 // them all, as pairs
 PX_DEV int64_t part_row(const AttnArgs& a, int64_t slot, int kv) {
   return (slot * (a.heads / a.group) + kv) * kFewRows;
 }
-template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads) void k_attn_few(AttnArgs a) {
+template <typename T, int C, int HOW> __global__ __launch_bounds__(kThreads) void k_attn_few(AttnArgs a) {
   constexpr int KT = kFewKeys;
-  typedef Rows<T, D> R;
+  typedef RowsOf<T, C> R;
   extern __shared__ __align__(16) char lds[];
-  const int lane = threadIdx.x & 63, wave = wave_id(), hd = DMA ? D : a.hd, kv_heads = a.heads / a.group;
+  const int lane = threadIdx.x & 63, wave = wave_id(), hd = HOW == kWhole ? C : a.hd, kv_heads = a.heads / a.group;
   const int kv = (int)(blockIdx.x % kv_heads);
   const int64_t slot = blockIdx.x / kv_heads;
   int part;
@@ -594,11 +614,11 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads) vo
         return;
       }
     }
-    Frag<T> q[D / 16];
-    row_frags<T, D>(q, static_cast<const T*>(a.Q) + (sq.q0 + i) * a.ldq + (int64_t)head * hd, live, hd, lane);
+    Frag<T> q[C / 16];
+    row_frags<T, C, HOW>(q, static_cast<const T*>(a.Q) + (sq.q0 + i) * a.ldq + (int64_t)head * hd, live, hd, lane);
     Sees see = live ? keys_of(a, i + shift, sq.nk) : Sees{0, 0};
     see = Sees{max(see.lo, j0), min(see.hi, j1)};
-    f32x16_v acc[D / 32] = {};
+    f32x16_v acc[C / 32] = {};
     float m = -INFINITY, l = 0.f;
     const Span all = keys_of_rows(a, tile * kFewRows / a.group, last, sq);
     // 32 keys from j on, whose K and V lie at lds + t and + v behind it
@@ -606,8 +626,8 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads) vo
       const Lane at = lane_at + t;
       f32x16_v s = {};
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-        if (within<DMA>(16 * kk, hd)) mma(s, R::along(lds, at, 0, kk), q[kk]);
+      for (int kk = 0; kk < C / 16; ++kk)
+        if (within<T>(16 * kk, hd)) mma(s, R::along(lds, at, 0, kk), q[kk]);
       if (j + 32 > j1 || !all.all(j, j + 32)) {
         const Sees on = see.from(j);
 #pragma unroll
@@ -623,7 +643,7 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads) vo
         const float keep = exp2_of((was - (m == -INFINITY ? 0.f : m)) * c);
         l *= keep;
 #pragma unroll
-        for (int d = 0; d < D / 32; ++d) acc[d] *= keep;
+        for (int d = 0; d < C / 32; ++d) acc[d] *= keep;
       }
       const float base = m == -INFINITY ? 0.f : m;
 #pragma unroll
@@ -635,51 +655,52 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads) vo
       for (int h = 0; h < 2; ++h) {
         const Frag<T> p = to_frag<T>(s, h);
 #pragma unroll
-        for (int d = 0; d < D / 32; ++d)
-          if (within<DMA>(32 * d, hd)) mma(acc[d], R::across(lds + v, at, 16 * h, 32 * d), p);
+        for (int d = 0; d < C / 32; ++d)
+          if (within<T>(32 * d, hd)) mma(acc[d], R::across(lds + v, at, 16 * h, 32 * d), p);
       }
     };
-    if constexpr (DMA) {
+    if constexpr (HOW != kStaged) {
       const int mine = wave * 2 * R::bytes(32);
-      const DmaRows<D, 32, 1> dma(0);
+      zero_tail<C>(lds + mine, 64, hd, lane, 64);
+      const DmaRows<C, 32, 1> dma(0);
       for (int j = j0 + 32 * wave; j < j1; j += KT) {
-        dma.copy(lds + mine, K, a.ldk, j, sq.nk, 0);
-        dma.copy(lds + mine + R::bytes(32), V, a.ldv, j, sq.nk, 0);
+        dma.copy(lds + mine, K, a.ldk, j, sq.nk, hd, 0);
+        dma.copy(lds + mine + R::bytes(32), V, a.ldv, j, sq.nk, hd, 0);
         asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's own copies
         step(mine, R::bytes(32), j);
       }
     } else {
-      over_tiles<T, D, DMA, KT>(lds, K, a.ldk, V, a.ldv, sq.nk, hd, j0, j1, [&](int t, int j) __attribute__((always_inline)) {
+      over_tiles<T, C, HOW, KT>(lds, K, a.ldk, V, a.ldv, sq.nk, hd, j0, j1, [&](int t, int j) __attribute__((always_inline)) {
         if (j + 32 * wave < j1) step(t + R::bytes(32) * wave, R::bytes(KT), j + 32 * wave);
       });
     }
     l = sum_halves(l);
     // the waves' sums, added in their order: wave w takes columns 32 w and up
     __syncthreads();
-    float* mine = reinterpret_cast<float*>(lds) + wave * 64 * (D / 2 + 2) + lane;
+    float* mine = reinterpret_cast<float*>(lds) + wave * 64 * (C / 2 + 2) + lane;
 #pragma unroll
-    for (int d = 0; d < D / 32; ++d)
+    for (int d = 0; d < C / 32; ++d)
 #pragma unroll
       for (int e = 0; e < 16; ++e) mine[(16 * d + e) * 64] = acc[d][e];
-    mine[(D / 2) * 64] = m;
-    mine[(D / 2 + 1) * 64] = l;
+    mine[(C / 2) * 64] = m;
+    mine[(C / 2 + 1) * 64] = l;
     __syncthreads();
-    if (wave < D / 32) {
+    if (wave < C / 32) {
       const float* all = reinterpret_cast<const float*>(lds) + lane;
       float f[kWaves], sum = 0.f;
       m = -INFINITY;
 #pragma unroll
-      for (int x = 0; x < kWaves; ++x) m = fmaxf(m, f[x] = all[(x * (D / 2 + 2) + D / 2) * 64]);
+      for (int x = 0; x < kWaves; ++x) m = fmaxf(m, f[x] = all[(x * (C / 2 + 2) + C / 2) * 64]);
       f32x16_v o = {};
 #pragma unroll
       for (int x = 0; x < kWaves; ++x) {
         f[x] = exp2_of((f[x] - (m == -INFINITY ? 0.f : m)) * c);
-        sum += f[x] * all[(x * (D / 2 + 2) + D / 2 + 1) * 64];
+        sum += f[x] * all[(x * (C / 2 + 2) + C / 2 + 1) * 64];
 #pragma unroll
-        for (int e = 0; e < 16; ++e) o[e] += f[x] * all[(x * (D / 2 + 2) + 16 * wave + e) * 64];
+        for (int e = 0; e < 16; ++e) o[e] += f[x] * all[(x * (C / 2 + 2) + 16 * wave + e) * 64];
       }
       if (cut) {
-        float* to = a.rows + a.part_head + (part_row(a, slot, kv) + (lane & 31)) * D + 32 * wave + 4 * (lane >> 5);
+        float* to = a.rows + a.part_head + (part_row(a, slot, kv) + (lane & 31)) * C + 32 * wave + 4 * (lane >> 5);
 #pragma unroll
         for (int g = 0; g < 4; ++g)
           *reinterpret_cast<float4*>(to + 8 * g) = make_float4(o[4 * g], o[4 * g + 1], o[4 * g + 2], o[4 * g + 3]);
@@ -687,7 +708,7 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads) vo
       } else if (live) {
         T* out = static_cast<T*>(a.out) + (sq.q0 + i) * a.ldout + (int64_t)head * hd + 32 * wave;
         const f32x16_v columns[1] = {o};
-        store_row<T, 32>(out, columns, sum == 0.f ? 0.f : 1.f / sum, hd - 32 * wave, lane);
+        store_row<T, 32, HOW>(out, columns, sum == 0.f ? 0.f : 1.f / sum, hd - 32 * wave, lane);
         if (wave == 0 && lane < 32)
           a.lse[(int64_t)head * a.q.rows + sq.q0 + i] = sum == 0.f ? -INFINITY : m * a.scale + kLn2 * log2f(sum);
       }
@@ -696,7 +717,7 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads) vo
   }
 }
 // The parts of one query and head, in their order: a wave each.
-template <typename T, int D> __global__ __launch_bounds__(kThreads) void k_attn_join(AttnArgs a) {
+template <typename T, int C> __global__ __launch_bounds__(kThreads) void k_attn_join(AttnArgs a) {
   const int lane = threadIdx.x & 63;
   const int64_t at = (int64_t)blockIdx.x * kWaves + wave_id();
   const int64_t i = at / a.heads;
@@ -706,22 +727,22 @@ template <typename T, int D> __global__ __launch_bounds__(kThreads) void k_attn_
   const Seq sq = sequence(a, s);
   const int kv = head / a.group, row = (int)(i - sq.q0) * a.group + head % a.group, parts = parts_of(a, sq);
   if (sq.nq * a.group > kFewRows || parts == 1) return;  // complete
-  constexpr int kGroup = 16;
+  constexpr int kGroup = 16, E = (C + 63) / 64;
   const int64_t slot = (int64_t)((uint32_t)sq.k0 / (uint32_t)a.part) + s;
   const float c = a.scale * kLog2e;
   const float2* const sums = reinterpret_cast<const float2*>(a.rows);
-  float m = -INFINITY, sum = 0.f, o[D / 64] = {};
+  float m = -INFINITY, sum = 0.f, o[E] = {};
   for (int x0 = 0; x0 < parts; x0 += kGroup) {
     // 16 parts: their maxima and sums a part a lane, their O a part a register, all on the way together
     const int n = min(parts - x0, kGroup);
     float2 ml = make_float2(-INFINITY, 0.f);
     if (lane < n) ml = sums[part_row(a, slot + x0 + lane, kv) + row];
-    float v[kGroup][D / 64];
+    float v[kGroup][E];
 #pragma unroll
     for (int x = 0; x < kGroup; ++x)
 #pragma unroll
-      for (int e = 0; e < D / 64; ++e)
-        v[x][e] = a.rows[a.part_head + (part_row(a, slot + x0 + min(x, n - 1), kv) + row) * D + 64 * e + lane];
+      for (int e = 0; e < E; ++e)
+        v[x][e] = a.rows[a.part_head + (part_row(a, slot + x0 + min(x, n - 1), kv) + row) * C + min(64 * e + lane, C - 1)];
     float top = fmaxf(m, ml.x);
 #pragma unroll
     for (int d = 1; d < kGroup; d <<= 1) top = fmaxf(top, __shfl_xor(top, d));
@@ -733,20 +754,20 @@ template <typename T, int D> __global__ __launch_bounds__(kThreads) void k_attn_
     const float f = none ? 0.f : exp2_of((ml.x - base) * c);
     sum = sum * keep + f * ml.y;
 #pragma unroll
-    for (int e = 0; e < D / 64; ++e) o[e] *= keep;
+    for (int e = 0; e < E; ++e) o[e] *= keep;
     const uint64_t there = __ballot(!none);
 #pragma unroll
     for (int x = 0; x < kGroup; ++x) {
       const float w = __uint_as_float(__builtin_amdgcn_readlane(__float_as_uint(f), x));
 #pragma unroll
-      for (int e = 0; e < D / 64; ++e) o[e] += there >> x & 1 ? w * v[x][e] : 0.f;
+      for (int e = 0; e < E; ++e) o[e] += there >> x & 1 ? w * v[x][e] : 0.f;
     }
   }
 #pragma unroll
   for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d);
   T* out = static_cast<T*>(a.out) + i * a.ldout + (int64_t)head * a.hd;
 #pragma unroll
-  for (int e = 0; e < D / 64; ++e)
+  for (int e = 0; e < E; ++e)
     if (64 * e + lane < a.hd) out[64 * e + lane] = from_f32<T>(sum == 0.f ? 0.f : o[e] / sum);
   if (lane == 0) a.lse[(int64_t)head * a.q.rows + i] = sum == 0.f ? -INFINITY : m * a.scale + kLn2 * log2f(sum);
 }
@@ -758,11 +779,11 @@ template <typename T> PX_DEV float prob(float s, float lse, float scale, float c
   // fp32 keeps the digits of a difference of logarithms; bf16's p has fewer than one fma leaves
   return sizeof(T) == 4 ? exp2_of((s * scale - lse) * kLog2e) : exp2_of(fmaf(s, c, -lse));
 }
-template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DMA ? 2 : 1) void k_attn_dq(AttnArgs a) {
-  constexpr int KT = kTile<T>, NB = KT / 32, BUFS = DMA ? 2 : 1;
-  typedef Rows<T, D> R;
+template <typename T, int C, int HOW> __global__ __launch_bounds__(kThreads, HOW ? 2 : 1) void k_attn_dq(AttnArgs a) {
+  constexpr int KT = kTile<T>, NB = KT / 32, BUFS = HOW ? 2 : 1;
+  typedef RowsOf<T, C> R;
   __shared__ __align__(16) char lds[BUFS * 2 * R::bytes(KT)];
-  const int lane = threadIdx.x & 63, wave = wave_id(), hd = DMA ? D : a.hd;
+  const int lane = threadIdx.x & 63, wave = wave_id(), hd = HOW == kWhole ? C : a.hd;
   const int head = head_of(a, blockIdx.x % a.heads);
   int tile;
   const Seq sq = sequence(a, tile_of(a.q, a.batch, a.slots, blockIdx.x / a.heads, kRows, gridDim.x > kAtOnce, true, &tile));
@@ -772,15 +793,15 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
   const bool live = i < sq.nq;
   const T* K = static_cast<const T*>(a.K) + sq.k0 * a.ldk + (int64_t)(head / a.group) * hd;
   const T* V = static_cast<const T*>(a.V) + sq.k0 * a.ldv + (int64_t)(head / a.group) * hd;
-  Frag<T> q[D / 16], g[D / 16];
-  row_frags<T, D>(q, static_cast<const T*>(a.Q) + (sq.q0 + i) * a.ldq + (int64_t)head * hd, live, hd, lane);
+  Frag<T> q[C / 16], g[C / 16];
+  row_frags<T, C, HOW>(q, static_cast<const T*>(a.Q) + (sq.q0 + i) * a.ldq + (int64_t)head * hd, live, hd, lane);
   float delta = 0.f;
   {
-    Frag<T> o[D / 16];
-    row_frags<T, D>(g, static_cast<const T*>(a.dO) + (sq.q0 + i) * a.lddo + (int64_t)head * hd, live, hd, lane);
-    row_frags<T, D>(o, static_cast<const T*>(a.O) + (sq.q0 + i) * a.ldo + (int64_t)head * hd, live, hd, lane);
+    Frag<T> o[C / 16];
+    row_frags<T, C, HOW>(g, static_cast<const T*>(a.dO) + (sq.q0 + i) * a.lddo + (int64_t)head * hd, live, hd, lane);
+    row_frags<T, C, HOW>(o, static_cast<const T*>(a.O) + (sq.q0 + i) * a.ldo + (int64_t)head * hd, live, hd, lane);
 #pragma unroll
-    for (int kk = 0; kk < D / 16; ++kk)
+    for (int kk = 0; kk < C / 16; ++kk)
 #pragma unroll
       for (int e = 0; e < 8; ++e) delta += (float)g[kk][e] * (float)o[kk][e];
   }
@@ -798,7 +819,7 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
   const int j0 = keys_of(a, w0 + shift, sq.nk).lo / KT * KT, j1 = keys_of(a, last + shift, sq.nk).hi;
   const float c = a.scale * kLog2e;
   const Lane lane_at = R::lane_at();
-  f32x16_v acc[D / 32] = {};
+  f32x16_v acc[C / 32] = {};
   const auto step = [&](int tile, int j) __attribute__((always_inline)) {
     const Lane at = (lane_at + tile).here();
     const char *const tk = lds, *const tv = lds + R::bytes(KT);
@@ -807,11 +828,11 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
     for (int b = 0; b < NB; ++b) {
       f32x16_v s = {}, dp = {};
 #pragma unroll
-      for (int kk = 0; kk < D / 16; ++kk)
-        if (within<DMA>(16 * kk, hd)) {
-          mma(s, R::along(tk, at, 32 * b, kk), q[kk]);
-          mma(dp, R::along(tv, at, 32 * b, kk), g[kk]);
-        }
+      for (int kk = 0; kk < C / 16; ++kk) {
+        if (!within<T>(16 * kk, hd)) continue;
+        mma(s, R::along(tk, at, 32 * b, kk), q[kk]);
+        mma(dp, R::along(tv, at, 32 * b, kk), g[kk]);
+      }
       if (masked) {
         const uint32_t on = see.from(j + 32 * b).bits();
 #pragma unroll
@@ -823,16 +844,16 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
       for (int h = 0; h < 2; ++h) {
         const Frag<T> p = to_frag<T>(s, h);
 #pragma unroll
-        for (int d = 0; d < D / 32; ++d)
-          if (within<DMA>(32 * d, hd)) mma(acc[d], R::across(tk, at, 32 * b + 16 * h, 32 * d), p);
+        for (int d = 0; d < C / 32; ++d)
+          if (within<T>(32 * d, hd)) mma(acc[d], R::across(tk, at, 32 * b + 16 * h, 32 * d), p);
       }
     }
   };
-  over_tiles<T, D, DMA, KT>(lds, K, a.ldk, V, a.ldv, sq.nk, hd, j0, j1, [&](int tile, int j) __attribute__((always_inline)) {
+  over_tiles<T, C, HOW, KT>(lds, K, a.ldk, V, a.ldv, sq.nk, hd, j0, j1, [&](int tile, int j) __attribute__((always_inline)) {
     if (w.any(j, j + KT)) step(tile, j);
   });
   if (live)
-    store_row<T, D>(static_cast<T*>(a.out) + (sq.q0 + i) * a.ldout + (int64_t)head * hd, acc, a.scale, hd, lane);
+    store_row<T, C, HOW>(static_cast<T*>(a.out) + (sq.q0 + i) * a.ldout + (int64_t)head * hd, acc, a.scale, hd, lane);
 }
 
 // dK and dV of 128 keys of one key head: its query heads one after another, so that their sum has one order.  Where that
@@ -840,18 +861,18 @@ template <typename T, int D, bool DMA> __global__ __launch_bounds__(kThreads, DM
 // them in the heads' order.  Of a block
 // of 32 queries (`tq`, `tg`: their rows and dO in LDS, `rows` and `deltas`: their lse and D), key(kk) and value(kk) are
 // the operands of the wave's keys.
-template <typename T, int D, bool FULL, class FK, class FV>
-PX_DEV void dkv_block(f32x16_v (&dk)[D / 32], f32x16_v (&dv)[D / 32], const char* tq, const char* tg, const Lane& at,
-                      const float* rows, const float* deltas, bool masked, const Sees& see, float scale, float c, int hd, const FK& key,
-                      const FV& value) {
-  typedef Rows<T, D> R;
+template <typename T, int C, class FK, class FV>
+PX_DEV void dkv_block(f32x16_v (&dk)[C / 32], f32x16_v (&dv)[C / 32], const char* tq, const char* tg, const Lane& at,
+                      const float* rows, const float* deltas, bool masked, const Sees& see, float scale, float c, int hd,
+                      const FK& key, const FV& value) {
+  typedef RowsOf<T, C> R;
   f32x16_v s = {}, dp = {};
 #pragma unroll
-  for (int kk = 0; kk < D / 16; ++kk)
-    if (within<FULL>(16 * kk, hd)) {
-      mma(s, R::along(tq, at, 0, kk), key(kk));
-      mma(dp, R::along(tg, at, 0, kk), value(kk));
-    }
+  for (int kk = 0; kk < C / 16; ++kk) {
+    if (!within<T>(16 * kk, hd)) continue;
+    mma(s, R::along(tq, at, 0, kk), key(kk));
+    mma(dp, R::along(tg, at, 0, kk), value(kk));
+  }
   if (masked) {
     const uint32_t on = see.bits();
 #pragma unroll
@@ -873,11 +894,11 @@ PX_DEV void dkv_block(f32x16_v (&dk)[D / 32], f32x16_v (&dv)[D / 32], const char
   for (int x = 0; x < 2; ++x) {
     const Frag<T> p = to_frag<T>(s, x), g = to_frag<T>(dp, x);
 #pragma unroll
-    for (int d = 0; d < D / 32; ++d)
-      if (within<FULL>(32 * d, hd)) {
-        mma(dv[d], R::across(tg, at, 16 * x, 32 * d), p);
-        mma(dk[d], R::across(tq, at, 16 * x, 32 * d), g);
-      }
+    for (int d = 0; d < C / 32; ++d) {
+      if (!within<T>(32 * d, hd)) continue;
+      mma(dv[d], R::across(tg, at, 16 * x, 32 * d), p);
+      mma(dk[d], R::across(tq, at, 16 * x, 32 * d), g);
+    }
   }
 }
 
@@ -916,19 +937,19 @@ PX_DEV Span places_of_wave(const AttnArgs& a, int first, const KeyTile& k) {
 }
 
 // a key's row of dK (which = 0) or dV (1), or where this share's goes
-template <typename T, int D>
-PX_DEV void store_grad(const AttnArgs& a, const KeyTile& k, int which, int key, const f32x16_v (&acc)[D / 32], int hd, int lane) {
+template <typename T, int C, int HOW>
+PX_DEV void store_grad(const AttnArgs& a, const KeyTile& k, int which, int key, const f32x16_v (&acc)[C / 32], int hd, int lane) {
   if (a.shares == 1) {
     T* out = which ? static_cast<T*>(a.out2) + (k.sq.k0 + key) * a.ldout2 : static_cast<T*>(a.out) + (k.sq.k0 + key) * a.ldout;
-    store_row<T, D>(out + (int64_t)k.head * hd, acc, which ? 1.f : a.scale, hd, lane);
+    store_row<T, C, HOW>(out + (int64_t)k.head * hd, acc, which ? 1.f : a.scale, hd, lane);
   } else {
     const int64_t row = ((int64_t)(2 * k.share + which) * (a.heads / a.group) + k.head) * a.k.rows + k.sq.k0 + key;
-    store_row<float, D>(a.parts + row * D, acc, which ? 1.f : a.scale, D, lane);
+    store_row<float, C, kWhole>(a.parts + row * C, acc, which ? 1.f : a.scale, C, lane);
   }
 }
-template <typename T, int D> __global__ __launch_bounds__(kThreads) void k_attn_dkv_sum(AttnArgs a) {
-  const int kv_heads = a.heads / a.group, c = (int)(threadIdx.x % (D / 4)) * 4;
-  const int64_t n = (int64_t)blockIdx.x * (kThreads / (D / 4)) + threadIdx.x / (D / 4);  // row and head of both
+template <typename T, int C> __global__ __launch_bounds__(kThreads) void k_attn_dkv_sum(AttnArgs a) {
+  const int kv_heads = a.heads / a.group, c = (int)(threadIdx.x % (C / 4)) * 4;
+  const int64_t n = (int64_t)blockIdx.x * (kThreads / (C / 4)) + threadIdx.x / (C / 4);  // row and head of both
   const int64_t row = n / kv_heads;
   const int head = (int)(n % kv_heads);
   if (row >= a.k.rows || row < first_row(a.k, 0) || row >= first_row(a.k, a.batch)) return;
@@ -936,7 +957,7 @@ template <typename T, int D> __global__ __launch_bounds__(kThreads) void k_attn_
   for (int which = 0; which < 2; ++which) {
     float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
     for (int x = 0; x < a.shares; ++x) {
-      const int64_t at = (((int64_t)(2 * x + which) * kv_heads + head) * a.k.rows + row) * D + c;
+      const int64_t at = (((int64_t)(2 * x + which) * kv_heads + head) * a.k.rows + row) * C + c;
       const float4 f = *reinterpret_cast<const float4*>(a.parts + at);
       sum = make_float4(sum.x + f.x, sum.y + f.y, sum.z + f.z, sum.w + f.w);
     }
@@ -949,9 +970,9 @@ template <typename T, int D> __global__ __launch_bounds__(kThreads) void k_attn_
 }
 
 // Any type, head and alignment: 4 waves, which hold their keys and values in registers.
-template <typename T, int D> __global__ __launch_bounds__(kThreads) void k_attn_dkv(AttnArgs a) {
+template <typename T, int C> __global__ __launch_bounds__(kThreads) void k_attn_dkv(AttnArgs a) {
   constexpr int QT = kTile<T>;
-  typedef Rows<T, D> R;
+  typedef RowsOf<T, C> R;
   __shared__ __align__(16) char lds[2 * R::bytes(QT)];
   __shared__ float rows[2][QT];  // lse, D
   const int lane = threadIdx.x & 63, wave = wave_id();
@@ -960,17 +981,17 @@ template <typename T, int D> __global__ __launch_bounds__(kThreads) void k_attn_
   const Seq& sq = t.sq;
   const int j = t.w0 + 32 * wave + (lane & 31);  // this lane's key
   const bool live = j < sq.nk;
-  Frag<T> k[D / 16], v[D / 16];
-  row_frags<T, D>(k, static_cast<const T*>(a.K) + (sq.k0 + j) * a.ldk + (int64_t)t.head * a.hd, live, a.hd, lane);
-  row_frags<T, D>(v, static_cast<const T*>(a.V) + (sq.k0 + j) * a.ldv + (int64_t)t.head * a.hd, live, a.hd, lane);
+  Frag<T> k[C / 16], v[C / 16];
+  row_frags<T, C, kStaged>(k, static_cast<const T*>(a.K) + (sq.k0 + j) * a.ldk + (int64_t)t.head * a.hd, live, a.hd, lane);
+  row_frags<T, C, kStaged>(v, static_cast<const T*>(a.V) + (sq.k0 + j) * a.ldv + (int64_t)t.head * a.hd, live, a.hd, lane);
   const Sees see = live ? places_of(a, j, t.shift, sq.nk) : Sees{0, 0};
   const Span w = places_of_wave(a, t.w0 + 32 * wave, t);
   const float c = a.scale * kLog2e;
   const Lane lane_at = R::lane_at();
-  f32x16_v dk[D / 32] = {}, dv[D / 32] = {};
+  f32x16_v dk[C / 32] = {}, dv[C / 32] = {};
   const int64_t more = (int64_t)a.heads * a.q.rows;
   const int per = t.i1 > t.i0 ? (t.i1 - t.i0 + QT - 1) / QT : 0, count = per * t.heads;  // tiles: heads x queries
-  Staged<T, D, QT> q, g;
+  Staged<T, C, QT> q, g;
   float row_value = 0.f;  // of the first 2 QT threads: lse, D
   const auto load = [&](int n) __attribute__((always_inline)) {
     const int h = t.first + n / per, i = t.i0 + n % per * QT;
@@ -993,35 +1014,35 @@ template <typename T, int D> __global__ __launch_bounds__(kThreads) void k_attn_
     for (int b = 0; b < QT; b += 32) {
       const int p = i + b + t.shift, r = b + 4 * (lane >> 5);
       if (w.any(p, p + 32))
-        dkv_block<T, D, false>(dk, dv, lds, lds + R::bytes(QT), lane_at + R::bytes(b), rows[0] + r, rows[1] + r,
+        dkv_block<T, C>(dk, dv, lds, lds + R::bytes(QT), lane_at + R::bytes(b), rows[0] + r, rows[1] + r,
                                !w.all(p, p + 32), see.from(p), a.scale, c, a.hd, [&](int kk) { return k[kk]; },
                                [&](int kk) { return v[kk]; });
     }
   }
   if (!live) return;
-  store_grad<T, D>(a, t, 0, j, dk, a.hd, lane);
-  store_grad<T, D>(a, t, 1, j, dv, a.hd, lane);
+  store_grad<T, C, kStaged>(a, t, 0, j, dk, a.hd, lane);
+  store_grad<T, C, kStaged>(a, t, 1, j, dv, a.hd, lane);
 }
 
-// Heads that fill the tile, by direct copies.  The accumulators of 32 keys take 128 registers; with the keys and values
+// By direct copies.  The accumulators of 32 keys take 128 registers; with the keys and values
 // beside them a SIMD holds one wave, whose products and exponentials follow each other.  Here they stay in LDS, and 8
 // waves take the same 128 keys, four of them the first 32 queries of a tile of 64 and four the others: two waves a SIMD.
 // The halves' sums are added at the end, the first one's first.
-template <int D> struct Dkv {
+template <int C> struct Dkv {
   static constexpr int W = 8, QT = 64;
-  static constexpr int KEYS = kRows * D * 2, TILE = QT * D * 2;
+  static constexpr int KEYS = RowsOf<bf16_t, C>::bytes(kRows), TILE = RowsOf<bf16_t, C>::bytes(QT);
   static constexpr int BUF = 2 * TILE + 2 * QT * 4;  // queries, dO, lse, D
-  static constexpr int EXCHANGE = W * 64 * (D / 32) * 16 * 4;
+  static constexpr int EXCHANGE = W * 64 * (C / 32) * 16 * 4;
   static constexpr int LDS = 2 * KEYS + 2 * BUF > EXCHANGE ? 2 * KEYS + 2 * BUF : EXCHANGE;
 };
-template <int D> __global__ __launch_bounds__(512, 2) void k_attn_dkv_dma(AttnArgs a) {
+template <int C, int HOW> __global__ __launch_bounds__(512, 2) void k_attn_dkv_dma(AttnArgs a) {
   typedef bf16_t T;
-  typedef Rows<T, D> R;
-  typedef Dkv<D> C;
-  constexpr int QT = C::QT;
+  typedef RowsOf<T, C> R;
+  typedef Dkv<C> P;
+  constexpr int QT = P::QT;
   extern __shared__ __align__(16) char lds[];
-  char *const tk = lds, *const tv = lds + C::KEYS, *const bufs = lds + 2 * C::KEYS;
-  const int lane = threadIdx.x & 63, wave = wave_id(), keys = 32 * (wave & 3), half = wave >> 2;
+  char *const tk = lds, *const tv = lds + P::KEYS, *const bufs = lds + 2 * P::KEYS;
+  const int lane = threadIdx.x & 63, wave = wave_id(), hd = HOW == kWhole ? C : a.hd, keys = 32 * (wave & 3), half = wave >> 2;
   const KeyTile t = key_tile(a, QT);
   if (!t.any) return;
   const Seq& sq = t.sq;
@@ -1030,66 +1051,67 @@ template <int D> __global__ __launch_bounds__(512, 2) void k_attn_dkv_dma(AttnAr
   const Sees see = live ? places_of(a, j, t.shift, sq.nk) : Sees{0, 0};
   const Span w = places_of_wave(a, t.w0 + keys, t);
   const float c = a.scale * kLog2e;
-  f32x16_v dk[D / 32] = {}, dv[D / 32] = {};
+  f32x16_v dk[C / 32] = {}, dv[C / 32] = {};
   const T* Q = static_cast<const T*>(a.Q) + sq.q0 * a.ldq;
   const T* G = static_cast<const T*>(a.dO) + sq.q0 * a.lddo;
   const int64_t at = sq.q0 + (int64_t)t.first * a.q.rows, more = (int64_t)a.heads * a.q.rows;
   const int per = t.i1 > t.i0 ? (t.i1 - t.i0 + QT - 1) / QT : 0, count = per * t.heads;  // tiles: heads x queries
-  const DmaRows<D, QT, C::W> dma(wave);
+  const DmaRows<C, QT, P::W> dma(wave);
   const auto fetch = [&](char* b, int h, int i) __attribute__((always_inline)) {
-    const int64_t col = (int64_t)(t.first + h) * D;
-    dma.copy(b, Q + col, a.ldq, i, sq.nq, wave);
-    dma.copy(b + C::TILE, G + col, a.lddo, i, sq.nq, wave);
+    const int64_t col = (int64_t)(t.first + h) * hd;
+    dma.copy(b, Q + col, a.ldq, i, sq.nq, hd, wave);
+    dma.copy(b + P::TILE, G + col, a.lddo, i, sq.nq, hd, wave);
     if (wave < 2) {  // 64 values each: wave 0 the lse, wave 1 D
       const float* x = a.rows + at + wave * more + (int64_t)h * a.q.rows + min(i + lane, sq.nq - 1);
-      char* to = b + 2 * C::TILE + wave * QT * 4;
+      char* to = b + 2 * P::TILE + wave * QT * 4;
       __builtin_amdgcn_global_load_lds(x, (__attribute__((address_space(3))) void*)to, 4, 0, 0);
     }
   };
   const Lane lane_at = R::lane_at();
   const auto compute = [&](int tile, int i) __attribute__((always_inline)) {
     const int p = i + 32 * half + t.shift;
-    const float* rows = reinterpret_cast<const float*>(lds + tile + 2 * C::TILE) + 32 * half + 4 * (lane >> 5);
+    const float* rows = reinterpret_cast<const float*>(lds + tile + 2 * P::TILE) + 32 * half + 4 * (lane >> 5);
     const Lane at = (lane_at + (tile + R::bytes(32 * half))).here(), keys_at = (lane_at + R::bytes(keys)).here();
     if (w.any(p, p + 32))
-      dkv_block<T, D, true>(dk, dv, lds, lds + C::TILE, at, rows, rows + QT, !w.all(p, p + 32), see.from(p), a.scale,
-                            c, D,
+      dkv_block<T, C>(dk, dv, lds, lds + P::TILE, at, rows, rows + QT, !w.all(p, p + 32), see.from(p), a.scale, c, hd,
                       [&](int kk) { return R::along(tk, keys_at, 0, kk); },
                       [&](int kk) { return R::along(tv, keys_at, 0, kk); });
   };
   if (count > 0) {
-    const DmaRows<D, kRows, C::W> whole(wave);
-    whole.copy(tk, static_cast<const T*>(a.K) + sq.k0 * a.ldk + (int64_t)t.head * D, a.ldk, t.w0, sq.nk, wave);
-    whole.copy(tv, static_cast<const T*>(a.V) + sq.k0 * a.ldv + (int64_t)t.head * D, a.ldv, t.w0, sq.nk, wave);
+    const DmaRows<C, kRows, P::W> whole(wave);
+    whole.copy(tk, static_cast<const T*>(a.K) + sq.k0 * a.ldk + (int64_t)t.head * hd, a.ldk, t.w0, sq.nk, hd, wave);
+    whole.copy(tv, static_cast<const T*>(a.V) + sq.k0 * a.ldv + (int64_t)t.head * hd, a.ldv, t.w0, sq.nk, hd, wave);
     fetch(bufs, 0, t.i0);
+    zero_tail<C>(tk, 2 * kRows, hd, (int)threadIdx.x, 64 * P::W);
+    for (int b = 0; b < 2; ++b) zero_tail<C>(bufs + b * P::BUF, 2 * QT, hd, (int)threadIdx.x, 64 * P::W);
   }
   int h = 0, i = t.i0;
-  for (int n = 0, buf = 0; n < count; ++n, buf ^= C::BUF) {
+  for (int n = 0, buf = 0; n < count; ++n, buf ^= P::BUF) {
     __syncthreads();  // this tile is there, and the other buffer is done with
     const int now = i;
     i += QT;
     if (i >= t.i1) i = t.i0, ++h;
-    if (n + 1 < count) fetch(bufs + (buf ^ C::BUF), h, i);
-    compute(2 * C::KEYS + buf, now);
+    if (n + 1 < count) fetch(bufs + (buf ^ P::BUF), h, i);
+    compute(2 * P::KEYS + buf, now);
   }
   // the waves of the first queries take the others' dK, those of the others the first ones' dV
   __syncthreads();
-  float* mine = reinterpret_cast<float*>(lds) + wave * 64 * (D / 2) + lane;
-  const float* other = reinterpret_cast<const float*>(lds) + (wave ^ 4) * 64 * (D / 2) + lane;
+  float* mine = reinterpret_cast<float*>(lds) + wave * 64 * (C / 2) + lane;
+  const float* other = reinterpret_cast<const float*>(lds) + (wave ^ 4) * 64 * (C / 2) + lane;
 #pragma unroll
-  for (int d = 0; d < D / 32; ++d)
+  for (int d = 0; d < C / 32; ++d)
 #pragma unroll
     for (int e = 0; e < 16; ++e) mine[(16 * d + e) * 64] = half ? dk[d][e] : dv[d][e];
   __syncthreads();
 #pragma unroll
-  for (int d = 0; d < D / 32; ++d)
+  for (int d = 0; d < C / 32; ++d)
 #pragma unroll
     for (int e = 0; e < 16; ++e) {
       const float x = other[(16 * d + e) * 64];
       dk[d][e] = half ? x + dv[d][e] : dk[d][e] + x;
     }
   if (!live) return;
-  store_grad<T, D>(a, t, half, j, dk, D, lane);
+  store_grad<T, C, HOW>(a, t, half, j, dk, hd, lane);
 }
 
 int64_t slots_of(int64_t rows, int batch, int R = kRows) { return rows / R + batch; }
@@ -1108,21 +1130,35 @@ AttnArgs args_of(const AttnDesc& d) {
   return a;
 }
 
-// f.operator()<T, D>() for the type and the head's tile width
+// columns that the kernels are built for
+int width(const AttnDesc& d) { return (int)round_up(d.hd, d.dt == BF16 ? 32 : 64); }
+// f(T(), std::integral_constant<int, C>()) for the type and the width
 template <class F> void pick(const AttnDesc& d, F&& f) {
+  const int c = width(d);
   if (d.dt == BF16) {
-    if (d.hd <= 64) f(bf16_t(), std::integral_constant<int, 64>());
+    if (c == 32) f(bf16_t(), std::integral_constant<int, 32>());
+    else if (c == 64) f(bf16_t(), std::integral_constant<int, 64>());
+    else if (c == 96) f(bf16_t(), std::integral_constant<int, 96>());
     else f(bf16_t(), std::integral_constant<int, 128>());
   } else {
-    if (d.hd <= 64) f(float(), std::integral_constant<int, 64>());
+    if (c == 64) f(float(), std::integral_constant<int, 64>());
     else f(float(), std::integral_constant<int, 128>());
   }
 }
 
 // whether the direct-to-LDS copies take these heads, and these rows
-bool fills_tile(const AttnDesc& d) { return d.dt == BF16 && (d.hd == 64 || d.hd == 128); }
-bool dma_rows(const AttnMat& m) {
+bool direct_heads(const AttnDesc& d) { return d.dt == BF16 && d.hd % 8 == 0; }
+bool direct_rows(const AttnMat& m) {
   return reinterpret_cast<uintptr_t>(m.p) % 16 == 0 && m.ld % 8 == 0 && m.ld <= kDmaLd;
+}
+// f(std::integral_constant<int, HOW>()), direct: they take both
+template <typename T, int C, class F> void pick_how(const AttnDesc& d, bool direct, F&& f) {
+  if constexpr (sizeof(T) == 2) {
+    if constexpr (C % 64 == 0)
+      if (direct && d.hd == C) return f(std::integral_constant<int, kWhole>());
+    if (direct) return f(std::integral_constant<int, kDirect>());
+  }
+  f(std::integral_constant<int, kStaged>());
 }
 
 // The keys of a workgroup in the forward of few rows; 0 where a tile of 32 rows does not hold a sequence's queries on the
@@ -1154,12 +1190,12 @@ bool attn_fits(const AttnDesc& d) {
 size_t attn_fwd_ws_bytes(const AttnDesc& d) {
   const int part = few_part(d);
   if (part == 0 || d.Tk <= part) return 0;  // the latter: no sequence has two parts
-  return (size_t)slots_of(d.Tk, d.batch, part) * d.kv_heads * kFewRows * (2 + (d.hd <= 64 ? 64 : 128)) * 4;
+  return (size_t)slots_of(d.Tk, d.batch, part) * d.kv_heads * kFewRows * (2 + width(d)) * 4;
 }
 static size_t shares_at(const AttnDesc& d) { return (size_t)round_up((int64_t)d.heads * d.Tq * 8, 256); }
 size_t attn_bwd_ws_bytes(const AttnDesc& d) {
   const int n = key_shares(d);
-  return shares_at(d) + (n > 1 ? (size_t)n * 2 * d.kv_heads * d.Tk * (d.hd <= 64 ? 64 : 128) * 4 : 0);
+  return shares_at(d) + (n > 1 ? (size_t)n * 2 * d.kv_heads * d.Tk * width(d) * 4 : 0);
 }
 
 hipError_t attn_fwd(const AttnDesc& d, const AttnMat& Q, const AttnMat& K, const AttnMat& V, void* O, int64_t ldo,
@@ -1169,39 +1205,32 @@ hipError_t attn_fwd(const AttnDesc& d, const AttnMat& Q, const AttnMat& K, const
   a.Q = Q.p, a.ldq = Q.ld, a.K = K.p, a.ldk = K.ld, a.V = V.p, a.ldv = V.ld;
   a.out = O, a.ldout = ldo, a.lse = lse, a.rows = static_cast<float*>(ws);
   a.part = few_part(d);
+  const bool direct = direct_heads(d) && direct_rows(K) && direct_rows(V);
   if (a.part) {
     hipError_t e = hipSuccess;
     const int64_t slots = slots_of(d.Tk, d.batch, a.part);
     a.part_head = 2 * slots * d.kv_heads * kFewRows;
-    pick(d, [&](auto t, auto D) {
+    pick(d, [&](auto t, auto columns) {
       typedef decltype(t) T;
-      constexpr int W = decltype(D)::value;
-      const auto run = [&](auto dma) {
-        typedef Few<T, W, decltype(dma)::value> F;
-        e = px::lds_once<k_attn_few<T, W, decltype(dma)::value>>(F::LDS);
-        if (e != hipSuccess) return;
-        k_attn_few<T, W, decltype(dma)::value><<<dim3((unsigned)(slots * d.kv_heads)), kThreads, F::LDS, s>>>(a);
-      };
-      if constexpr (sizeof(T) == 2) {
-        if (fills_tile(d) && dma_rows(K) && dma_rows(V)) run(std::true_type());
-        else run(std::false_type());
-      } else {
-        run(std::false_type());
-      }
+      constexpr int C = decltype(columns)::value;
+      pick_how<T, C>(d, direct, [&](auto how) {
+        constexpr int HOW = decltype(how)::value, kLds = Few<T, C>::LDS;
+        e = px::lds_once<k_attn_few<T, C, HOW>>(kLds);
+        if (e == hipSuccess)
+          k_attn_few<T, C, HOW><<<dim3((unsigned)(slots * d.kv_heads)), kThreads, kLds, s>>>(a);
+      });
       if (e == hipSuccess && d.Tk > a.part)
-        k_attn_join<T, W><<<dim3(px::cdiv((int64_t)d.Tq * d.heads, kWaves)), kThreads, 0, s>>>(a);
+        k_attn_join<T, C><<<dim3(px::cdiv((int64_t)d.Tq * d.heads, kWaves)), kThreads, 0, s>>>(a);
     });
     return e != hipSuccess ? e : hipGetLastError();
   }
   a.slots = slots_of(d.Tq, d.batch);
-  const bool dma = fills_tile(d) && dma_rows(K) && dma_rows(V);
-  pick(d, [&](auto t, auto D) {
+  pick(d, [&](auto t, auto columns) {
     typedef decltype(t) T;
-    const dim3 grid((unsigned)(a.slots * d.heads));
-    if constexpr (sizeof(T) == 2) {
-      if (dma) return k_attn_fwd<T, decltype(D)::value, true><<<grid, kThreads, 0, s>>>(a);
-    }
-    k_attn_fwd<T, decltype(D)::value, false><<<grid, kThreads, 0, s>>>(a);
+    constexpr int C = decltype(columns)::value;
+    pick_how<T, C>(d, direct, [&](auto how) {
+      k_attn_fwd<T, C, decltype(how)::value><<<dim3((unsigned)(a.slots * d.heads)), kThreads, 0, s>>>(a);
+    });
   });
   return hipGetLastError();
 }
@@ -1209,7 +1238,7 @@ hipError_t attn_fwd(const AttnDesc& d, const AttnMat& Q, const AttnMat& K, const
 hipError_t attn_bwd(const AttnDesc& d, const AttnMat& dO, const AttnMat& Q, const AttnMat& K, const AttnMat& V,
                     const AttnMat& O, const float* lse, void* dQ, int64_t lddq, void* dK, int64_t lddk, void* dV,
                     int64_t lddv, void* ws, hipStream_t s) {
-  const bool full = fills_tile(d);
+  const bool direct = direct_heads(d) && direct_rows(K) && direct_rows(V);
   AttnArgs a = args_of(d);
   a.Q = Q.p, a.ldq = Q.ld, a.K = K.p, a.ldk = K.ld, a.V = V.p, a.ldv = V.ld, a.O = O.p, a.ldo = O.ld;
   a.dO = dO.p, a.lddo = dO.ld;
@@ -1217,14 +1246,12 @@ hipError_t attn_bwd(const AttnDesc& d, const AttnMat& dO, const AttnMat& Q, cons
   if (d.Tq > 0) {
     a.out = dQ, a.ldout = lddq;
     a.slots = slots_of(d.Tq, d.batch);
-    pick(d, [&](auto t, auto D) {
+    pick(d, [&](auto t, auto columns) {
       typedef decltype(t) T;
-      constexpr int W = decltype(D)::value;
-      const dim3 grid((unsigned)(a.slots * d.heads));
-      if constexpr (sizeof(T) == 2) {
-        if (full && dma_rows(K) && dma_rows(V)) return k_attn_dq<T, W, true><<<grid, kThreads, 0, s>>>(a);
-      }
-      k_attn_dq<T, W, false><<<grid, kThreads, 0, s>>>(a);
+      constexpr int C = decltype(columns)::value;
+      pick_how<T, C>(d, direct, [&](auto how) {
+        k_attn_dq<T, C, decltype(how)::value><<<dim3((unsigned)(a.slots * d.heads)), kThreads, 0, s>>>(a);
+      });
     });
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -1235,24 +1262,22 @@ hipError_t attn_bwd(const AttnDesc& d, const AttnMat& dO, const AttnMat& Q, cons
   a.parts = reinterpret_cast<float*>(static_cast<char*>(ws) + shares_at(d));
   a.slots = slots_of(d.Tk, d.batch);
   hipError_t e = hipSuccess;
-  pick(d, [&](auto t, auto D) {
+  pick(d, [&](auto t, auto columns) {
     typedef decltype(t) T;
-    constexpr int W = decltype(D)::value;
+    constexpr int C = decltype(columns)::value;
     const dim3 grid((unsigned)(a.slots * d.kv_heads * a.shares));
-    const auto sum = [&] {
-      const int rows = kThreads / (W / 4);
-      if (e == hipSuccess && a.shares > 1)
-        k_attn_dkv_sum<T, W><<<dim3(px::cdiv(d.Tk * d.kv_heads, rows)), kThreads, 0, s>>>(a);
-    };
-    if constexpr (sizeof(T) == 2) {
-      if (full && dma_rows(Q) && dma_rows(dO) && dma_rows(K) && dma_rows(V)) {
-        e = px::lds_once<k_attn_dkv_dma<W>>(Dkv<W>::LDS);
-        if (e == hipSuccess) k_attn_dkv_dma<W><<<grid, 64 * Dkv<W>::W, Dkv<W>::LDS, s>>>(a);
-        return sum();
+    pick_how<T, C>(d, direct && direct_rows(Q) && direct_rows(dO), [&](auto how) {
+      constexpr int HOW = decltype(how)::value;
+      if constexpr (HOW == kStaged) {
+        k_attn_dkv<T, C><<<grid, kThreads, 0, s>>>(a);
+      } else {
+        e = px::lds_once<k_attn_dkv_dma<C, HOW>>(Dkv<C>::LDS);
+        if (e == hipSuccess) k_attn_dkv_dma<C, HOW><<<grid, 64 * Dkv<C>::W, Dkv<C>::LDS, s>>>(a);
       }
-    }
-    k_attn_dkv<T, W><<<grid, kThreads, 0, s>>>(a);
-    sum();
+    });
+    const int rows = kThreads / (C / 4);  // of a workgroup
+    if (e == hipSuccess && a.shares > 1)
+      k_attn_dkv_sum<T, C><<<dim3(px::cdiv(d.Tk * d.kv_heads, rows)), rows * (C / 4), 0, s>>>(a);
   });
   return e != hipSuccess ? e : hipGetLastError();
 }

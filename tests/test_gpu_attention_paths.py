@@ -159,3 +159,25 @@ def test_workspaces_hold_what_the_calls_write():
                          new(T, top) if top else None, ws, n)
         torch.cuda.synchronize()
         assert (ws[n:] == 0x5A).all()
+
+
+@pytest.mark.parametrize("hd", [8, 24, 32, 40, 56, 72, 88, 96, 104, 120])
+def test_heads_of_a_multiple_of_eight(hd):
+    """Copied straight to LDS without the columns behind the head, which hold zeros whatever was there before."""
+    nan = torch.full((300, 8 * 128), float("nan"), dtype=torch.bfloat16, device="cuda")
+    other = PoetxAttention(8, 8, 128)
+    for lq, lk, causal, window in (([1, 130, 300], [1, 130, 300], True, 0), ([5, 260], [300, 100], False, 70),
+                                   ([1, 1], [700, 40], True, 0)):
+        other.backward(torch.zeros_like(other.forward(nan, nan, nan)))  # not-a-numbers in LDS
+        A.run(6, 2, hd, "bf16", lq, lk, causal, window, seed=hd)
+    A.run(16, 1, hd, "bf16", [200, 33], [200, 33], seed=1)  # query heads shared among workgroups
+
+
+def test_heads_of_a_multiple_of_eight_elsewhere():
+    """The same heads in rows that are no multiple of 16 bytes, or begin at none: through registers."""
+    q, k, v, dO = (A.rows(150, 4 * 40, "bf16", s, 4 * 40 + gap, offset)
+                   for s, gap, offset in ((1, 3, 0), (2, 8, 1), (3, 0, 4), (4, 1, 1)))
+    at = PoetxAttention(4, 4, 40)
+    out = at.forward(q, k, v)
+    A.check(at, O.Attn(4, 4, 40, float(np.float32(at.desc.scale)), True), "bf16", (q, k, v), dO, out, at.saved[4],
+            at.backward(dO), A.cu_of([150]), A.cu_of([150]))
