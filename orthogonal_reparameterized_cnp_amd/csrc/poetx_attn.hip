@@ -71,6 +71,14 @@ template <> PX_DEV f32x8_v to_frag<float>(const f32x16_v& v, int c) {
   return f;
 }
 
+// what the rounding of elements 8 c .. 8 c + 7 to `f` left
+template <typename T> PX_DEV Frag<T> rest_of(const f32x16_v& v, int c, const Frag<T>& f) {
+  f32x16_v r;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) r[i] = v[8 * c + i] - (float)f[i];
+  return to_frag<T>(r, 0);
+}
+
 // row of accumulator element e, in the half of lanes that begins with row 0 (the other's is 4 higher)
 constexpr int acc_row(int e) { return 8 * (e / 4) + e % 4; }
 
@@ -846,6 +854,14 @@ template <typename T, int C, int HOW> __global__ __launch_bounds__(kThreads, HOW
 #pragma unroll
         for (int d = 0; d < C / 32; ++d)
           if (within<T>(32 * d, hd)) mma(acc[d], R::across(tk, at, 32 * b + 16 * h, 32 * d), p);
+        // A tile that a mask cuts is multiplied with what that rounding left too: the queries that see few keys, whose
+        // gradients are the largest, have all or most of theirs there.  dQ of 2 x 4096 causal tokens is 2.30e-3 off in
+        // the norm (1.66e-3 of it rounding dQ itself) instead of 2.51e-3, for 1% of the time.
+        if (sizeof(T) == 2 && masked) {
+          const Frag<T> rest = rest_of<T>(s, h, p);
+#pragma unroll
+          for (int d = 0; d < C / 32; ++d) mma(acc[d], R::across(tk, at, 32 * b + 16 * h, 32 * d), rest);
+        }
       }
     }
   };
