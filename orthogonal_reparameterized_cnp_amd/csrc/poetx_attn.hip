@@ -204,7 +204,24 @@ template <typename T, int C, int N> struct Staged {
 // 16 bytes (pitches of up to kDmaLd).  Rows behind the last repeat it; what is computed from them is masked.  Columns
 // behind the head are left alone: zero_tail() clears them once.
 constexpr int64_t kDmaLd = 1 << 23;  // a tile's rows lie within 32 bits
-template <int C, int N, int W> struct DmaRows {
+// `BYTES` from base + at of each lane to the LDS address t + BYTES * lane.  The compiler holds the builtin for a write to any
+// LDS that the transposing reads may read, and waits in front of those for all copies in flight.  Where that is too early,
+// OWN is assembly, of which it counts nothing: copies_done() or a wait of the kernel's own has to stand before the reads.
+template <int BYTES, bool OWN> PX_DEV void copy_to_lds(char* t, const char* base, uint32_t at) {
+  const auto lds = (__attribute__((address_space(3))) char*)t;
+  if constexpr (!OWN && BYTES == 16)
+    __builtin_amdgcn_global_load_lds(base + at, (__attribute__((address_space(3))) void*)lds, 16, 0, 0);
+  else if constexpr (!OWN)
+    __builtin_amdgcn_global_load_lds(base + at, (__attribute__((address_space(3))) void*)lds, 4, 0, 0);
+  else if constexpr (BYTES == 16)  // with the wait states between writes of the scalar registers and this use of them
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"((uint32_t)(uintptr_t)lds), "v"(at),
+                 "s"(base) : "memory");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, %2" ::"s"((uint32_t)(uintptr_t)lds), "v"(at),
+                 "s"(base) : "memory");
+}
+PX_DEV void copies_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+template <int C, int N, int W, bool OWN> struct DmaRows {
   typedef RowsOf<bf16_t, C> R;
   static constexpr int K = R::CPR, RPW = 64 / K, STEP = W * RPW;  // rows of a wave's copy, of the W waves'
   int r, lane;  // this lane's row in the first copy
@@ -225,9 +242,7 @@ template <int C, int N, int W> struct DmaRows {
         put(t + i * W * 1024, g, (uint32_t)(min(row, last) * pitch + c));
     }
   }
-  static PX_DEV void put(char* t, const char* base, uint32_t at) {
-    __builtin_amdgcn_global_load_lds(base + at, (__attribute__((address_space(3))) void*)t, 16, 0, 0);
-  }
+  static PX_DEV void put(char* t, const char* base, uint32_t at) { copy_to_lds<16, OWN>(t, base, at); }
 };
 // the columns behind the head, of `rows` rows of an LDS tile, by `threads` threads of which this is the x-th
 template <int C> PX_DEV void zero_tail(char* tile, int rows, int hd, int x, int threads) {
@@ -244,6 +259,12 @@ PX_DEV void row_frags(Frag<T> (&f)[C / 16], const T* row, bool there, int hd, in
     load8<HOW>(v, row, there, 16 * kk + 8 * (lane >> 5), hd);
     __builtin_memcpy(&f[kk], v, sizeof(v));
   }
+}
+// The fragments are there: the compiler, which does not count the copies to LDS, waits for all loads in flight where it
+// first needs them, and that has to be before the loop.
+template <typename T, int N> PX_DEV void settle(Frag<T> (&f)[N]) {
+#pragma unroll
+  for (int kk = 0; kk < N; ++kk) asm volatile("" : "+v"(f[kk]));
 }
 // a lane's accumulator column as row elements: 4 consecutive of them at a time
 template <typename T, int C, int HOW>
@@ -425,7 +446,8 @@ PX_DEV int tile_of(const Side& x, int batch, int64_t slots, int64_t n, int R, bo
   return s;
 }
 
-// f(offset of the K tile, which the V tile follows, first key) over the tiles of the keys [j0, j1), which are the same for the whole workgroup
+// f(offset of the K tile, which the V tile follows, first key) over the tiles of the keys [j0, j1), which are the same for
+// the whole workgroup.
 template <typename T, int C, int HOW, int KT, class F>
 PX_DEV void over_tiles(char* lds, const T* K, int64_t ldk, const T* V, int64_t ldv, int n, int hd, int j0, int j1,
                        const F& f) {
@@ -434,7 +456,7 @@ PX_DEV void over_tiles(char* lds, const T* K, int64_t ldk, const T* V, int64_t l
   if constexpr (HOW != kStaged) {
     if (j0 >= j1) return;
     const int wave = wave_id();
-    const DmaRows<C, KT, kWaves> dma(wave);
+    const DmaRows<C, KT, kWaves, false> dma(wave);
     const auto copy = [&](int x, int j) __attribute__((always_inline)) {
       dma.copy(at(x), K, ldk, j, n, hd, wave);
       dma.copy(at(x + 1), V, ldv, j, n, hd, wave);
@@ -573,7 +595,8 @@ template <typename T, int C, int HOW> __global__ __launch_bounds__(kThreads, HOW
 // the card.  Here a tile is 32 rows, a row one query of one of the query heads that share a key head (so that its keys are
 // read once for all of them), and the four waves take 32 keys each of a tile of 128.  By direct copies a wave has its own
 // piece of LDS and waits for nobody: what bounds the kernel is how many bytes are under way, and eight waves a CU that
-// load and compute at different times keep more of them there than two workgroups in step.  A workgroup stands for `part`
+// load and compute at different times keep more of them there than two workgroups in step.  A wave's next keys are copied
+// as soon as these are multiplied, during the softmax, and its next values during the next product.  A workgroup stands for `part`
 // keys of a sequence.  It leaves the maximum, the sum and the unscaled O that they give the sequence's rows, and k_attn_join
 // adds the parts in their order.  Where a sequence has more rows than a tile all the same, its workgroups share the
 // tiles instead, each with all keys.
@@ -629,8 +652,8 @@ template <typename T, int C, int HOW> __global__ __launch_bounds__(kThreads) voi
     f32x16_v acc[C / 32] = {};
     float m = -INFINITY, l = 0.f;
     const Span all = keys_of_rows(a, tile * kFewRows / a.group, last, sq);
-    // 32 keys from j on, whose K and V lie at lds + t and + v behind it
-    const auto step = [&](int t, int v, int j) __attribute__((always_inline)) {
+    // 32 keys from j on, whose K and V lie at lds + t and + v behind it; between() stands between their products
+    const auto step = [&](int t, int v, int j, const auto& between) __attribute__((always_inline)) {
       const Lane at = lane_at + t;
       f32x16_v s = {};
 #pragma unroll
@@ -659,6 +682,7 @@ template <typename T, int C, int HOW> __global__ __launch_bounds__(kThreads) voi
         s[e] = exp2_of((s[e] - base) * c);
         l += s[e];
       }
+      between();
 #pragma unroll
       for (int h = 0; h < 2; ++h) {
         const Frag<T> p = to_frag<T>(s, h);
@@ -670,16 +694,43 @@ template <typename T, int C, int HOW> __global__ __launch_bounds__(kThreads) voi
     if constexpr (HOW != kStaged) {
       const int mine = wave * 2 * R::bytes(32);
       zero_tail<C>(lds + mine, 64, hd, lane, 64);
-      const DmaRows<C, 32, 1> dma(0);
-      for (int j = j0 + 32 * wave; j < j1; j += KT) {
-        dma.copy(lds + mine, K, a.ldk, j, sq.nk, hd, 0);
+      const DmaRows<C, 32, 1, true> dma(0);
+      const auto keys = [&](int j) __attribute__((always_inline)) { dma.copy(lds + mine, K, a.ldk, j, sq.nk, hd, 0); };
+      const auto values = [&](int j) __attribute__((always_inline)) {
         dma.copy(lds + mine + R::bytes(32), V, a.ldv, j, sq.nk, hd, 0);
-        asm volatile("s_waitcnt vmcnt(0)" ::: "memory");  // this wave's own copies
-        step(mine, R::bytes(32), j);
+      };
+      // all of this wave's copies but those of the last 32 rows
+      const auto all_but_last = [] __attribute__((always_inline)) {
+        if constexpr (R::bytes(32) == 8192) asm volatile("s_waitcnt vmcnt(8)" ::: "memory");
+        else asm volatile("s_waitcnt vmcnt(4)" ::: "memory");
+      };
+      static_assert(R::bytes(32) == 8192 || R::bytes(32) == 4096, "1 KB a copy");
+      int j = j0 + 32 * wave;
+      if (j < j1) {
+        keys(j);
+        values(j);
+      }
+      settle<T>(q);
+      for (; j < j1; j += KT) {
+        const bool more = j + KT < j1;
+        all_but_last();
+        step(mine, R::bytes(32), j, [&]() __attribute__((always_inline)) {
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the keys are read
+          if (more) {
+            keys(j + KT);
+            all_but_last();
+          } else {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+          }
+        });
+        if (more) {
+          asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");  // the values are read
+          values(j + KT);
+        }
       }
     } else {
       over_tiles<T, C, HOW, KT>(lds, K, a.ldk, V, a.ldv, sq.nk, hd, j0, j1, [&](int t, int j) __attribute__((always_inline)) {
-        if (j + 32 * wave < j1) step(t + R::bytes(32) * wave, R::bytes(KT), j + 32 * wave);
+        if (j + 32 * wave < j1) step(t + R::bytes(32) * wave, R::bytes(KT), j + 32 * wave, [] {});
       });
     }
     l = sum_halves(l);
@@ -1046,6 +1097,9 @@ template <typename T, int C> __global__ __launch_bounds__(kThreads) void k_attn_
 // The halves' sums are added at the end, the first one's first.
 template <int C> struct Dkv {
   static constexpr int W = 8, QT = 64;
+  // copies that the compiler does not count: 64 columns 564 -> 530 us (2 x 4096, the whole backward), but 96 and 128 are 1%
+  // slower with them
+  static constexpr bool OWN = C <= 64;
   static constexpr int KEYS = RowsOf<bf16_t, C>::bytes(kRows), TILE = RowsOf<bf16_t, C>::bytes(QT);
   static constexpr int BUF = 2 * TILE + 2 * QT * 4;  // queries, dO, lse, D
   static constexpr int EXCHANGE = W * 64 * (C / 32) * 16 * 4;
@@ -1072,15 +1126,15 @@ template <int C, int HOW> __global__ __launch_bounds__(512, 2) void k_attn_dkv_d
   const T* G = static_cast<const T*>(a.dO) + sq.q0 * a.lddo;
   const int64_t at = sq.q0 + (int64_t)t.first * a.q.rows, more = (int64_t)a.heads * a.q.rows;
   const int per = t.i1 > t.i0 ? (t.i1 - t.i0 + QT - 1) / QT : 0, count = per * t.heads;  // tiles: heads x queries
-  const DmaRows<C, QT, P::W> dma(wave);
+  const DmaRows<C, QT, P::W, P::OWN> dma(wave);
   const auto fetch = [&](char* b, int h, int i) __attribute__((always_inline)) {
     const int64_t col = (int64_t)(t.first + h) * hd;
     dma.copy(b, Q + col, a.ldq, i, sq.nq, hd, wave);
     dma.copy(b + P::TILE, G + col, a.lddo, i, sq.nq, hd, wave);
     if (wave < 2) {  // 64 values each: wave 0 the lse, wave 1 D
-      const float* x = a.rows + at + wave * more + (int64_t)h * a.q.rows + min(i + lane, sq.nq - 1);
-      char* to = b + 2 * P::TILE + wave * QT * 4;
-      __builtin_amdgcn_global_load_lds(x, (__attribute__((address_space(3))) void*)to, 4, 0, 0);
+      const float* x = a.rows + at + wave * more + (int64_t)h * a.q.rows;
+      copy_to_lds<4, P::OWN>(b + 2 * P::TILE + wave * QT * 4, reinterpret_cast<const char*>(x + i),
+                     4u * (uint32_t)min(lane, sq.nq - 1 - i));
     }
   };
   const Lane lane_at = R::lane_at();
@@ -1094,7 +1148,7 @@ template <int C, int HOW> __global__ __launch_bounds__(512, 2) void k_attn_dkv_d
                       [&](int kk) { return R::along(tv, keys_at, 0, kk); });
   };
   if (count > 0) {
-    const DmaRows<C, kRows, P::W> whole(wave);
+    const DmaRows<C, kRows, P::W, P::OWN> whole(wave);
     whole.copy(tk, static_cast<const T*>(a.K) + sq.k0 * a.ldk + (int64_t)t.head * hd, a.ldk, t.w0, sq.nk, hd, wave);
     whole.copy(tv, static_cast<const T*>(a.V) + sq.k0 * a.ldv + (int64_t)t.head * hd, a.ldv, t.w0, sq.nk, hd, wave);
     fetch(bufs, 0, t.i0);
@@ -1103,6 +1157,7 @@ template <int C, int HOW> __global__ __launch_bounds__(512, 2) void k_attn_dkv_d
   }
   int h = 0, i = t.i0;
   for (int n = 0, buf = 0; n < count; ++n, buf ^= P::BUF) {
+    if constexpr (P::OWN) copies_done();
     __syncthreads();  // this tile is there, and the other buffer is done with
     const int now = i;
     i += QT;
