@@ -181,21 +181,21 @@ template <int HOW, typename T> PX_DEV void load8(T (&v)[8], const T* row, bool t
   }
 }
 // rows [r0, r0 + N) of a sequence's `n`, into an LDS tile by way of registers: any type, head and alignment
-template <typename T, int C, int N> struct Staged {
-  static constexpr int K = C / 8, ALL = N * K, EACH = (ALL + kThreads - 1) / kThreads;
-  static PX_DEV bool in(int x) { return ALL % kThreads == 0 || x < ALL; }
+template <typename T, int C, int N, int THREADS = kThreads> struct Staged {
+  static constexpr int K = C / 8, ALL = N * K, EACH = (ALL + THREADS - 1) / THREADS;
+  static PX_DEV bool in(int x) { return ALL % THREADS == 0 || x < ALL; }
   T v[EACH][8];
   PX_DEV void load(const T* base, int64_t ld, int r0, int n, int hd) {
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
-      const int x = i * kThreads + (int)threadIdx.x, r = x / K, c = x % K;
+      const int x = i * THREADS + (int)threadIdx.x, r = x / K, c = x % K;
       load8<kStaged>(v[i], base + (int64_t)(r0 + r) * ld, in(x) && r0 + r < n, 8 * c, hd);
     }
   }
   PX_DEV void put(char* tile) const {
 #pragma unroll
     for (int i = 0; i < EACH; ++i) {
-      const int x = i * kThreads + (int)threadIdx.x;
+      const int x = i * THREADS + (int)threadIdx.x;
       if (in(x)) RowsOf<T, C>::put(tile, x / K, x % K, v[i]);
     }
   }
@@ -448,7 +448,7 @@ PX_DEV int tile_of(const Side& x, int batch, int64_t slots, int64_t n, int R, bo
 
 // f(offset of the K tile, which the V tile follows, first key) over the tiles of the keys [j0, j1), which are the same for
 // the whole workgroup.
-template <typename T, int C, int HOW, int KT, class F>
+template <typename T, int C, int HOW, int KT, int THREADS = kThreads, class F>
 PX_DEV void over_tiles(char* lds, const T* K, int64_t ldk, const T* V, int64_t ldv, int n, int hd, int j0, int j1,
                        const F& f) {
   typedef RowsOf<T, C> R;
@@ -470,7 +470,7 @@ PX_DEV void over_tiles(char* lds, const T* K, int64_t ldk, const T* V, int64_t l
     }
   } else if constexpr (KT <= 64) {
     // the next tile's rows come into registers while this one is computed with
-    Staged<T, C, KT> k, v;
+    Staged<T, C, KT, THREADS> k, v;
     const auto load = [&](int j) __attribute__((always_inline)) {
       k.load(K, ldk, j, n, hd);
       v.load(V, ldv, j, n, hd);
@@ -508,11 +508,17 @@ template <typename T> constexpr int kTile = sizeof(T) == 2 ? 64 : 32;  // keys (
 // 2^kSlack, which costs no digits, and the accumulators need no rescaling.
 constexpr float kSlack = 8.f;
 
-template <typename T, int C, int HOW> __global__ __launch_bounds__(kThreads, HOW ? 2 : 1) void k_attn_fwd(AttnArgs a) {
-  constexpr int KT = kTile<T>, NB = KT / 32, BUFS = HOW ? 2 : 1;
+// fp32 has a second group of four waves, which takes the other half of each tile's keys: a wave's products are eight times
+// bf16's, and with one group a SIMD had one wave of them and nobody to work while it staged the next tile and took its
+// softmax (32 heads of 128: 2048 tokens 338 -> 314 us, 2 x 4096 2562 -> 2350; 64 columns 228 -> 171; six sequences of up to
+// 1000 with 9 heads of 75 columns, fewer workgroups than CUs, 72 -> 61).
+template <typename T> constexpr int kFwdGroups = sizeof(T) == 2 ? 1 : 2;
+template <typename T, int C, int HOW>
+__global__ __launch_bounds__(kThreads * kFwdGroups<T>, HOW ? 2 : 1) void k_attn_fwd(AttnArgs a) {
+  constexpr int G = kFwdGroups<T>, PART = kTile<T>, KT = PART * G, NB = PART / 32, BUFS = HOW ? 2 : 1;
   typedef RowsOf<T, C> R;
   __shared__ __align__(16) char lds[BUFS * 2 * R::bytes(KT)];
-  const int lane = threadIdx.x & 63, wave = wave_id(), hd = HOW == kWhole ? C : a.hd;
+  const int lane = threadIdx.x & 63, wave = wave_id() % kWaves, group = wave_id() / kWaves, hd = HOW == kWhole ? C : a.hd;
   const int head = head_of(a, blockIdx.x % a.heads);
   int tile;
   const Seq sq = sequence(a, tile_of(a.q, a.batch, a.slots, blockIdx.x / a.heads, kRows, gridDim.x > kAtOnce, true, &tile));
@@ -578,11 +584,35 @@ template <typename T, int C, int HOW> __global__ __launch_bounds__(kThreads, HOW
           if (within<T>(32 * d, hd)) mma(acc[d], R::across(tv, at, 32 * b + 16 * h, 32 * d), p);
       }
   };
-  over_tiles<T, C, HOW, KT>(lds, K, a.ldk, V, a.ldv, sq.nk, hd, j0, j1,
-                            [&](int tile, int j) __attribute__((always_inline)) {
-                              if (w.all(j, j + KT)) step(tile, j, std::false_type());
-                              else if (w.any(j, j + KT)) step(tile, j, std::true_type());
-                            });
+  over_tiles<T, C, HOW, KT, kThreads * G>(lds, K, a.ldk, V, a.ldv, sq.nk, hd, j0, j1,
+                                          [&](int tile, int j) __attribute__((always_inline)) {
+                                            j += PART * group, tile += R::bytes(PART) * group;
+                                            if (w.all(j, j + PART)) step(tile, j, std::false_type());
+                                            else if (w.any(j, j + PART)) step(tile, j, std::true_type());
+                                          });
+  if constexpr (G == 2) {  // the first group's waves take the second's maxima, sums and O
+    static_assert(kWaves * 64 * (C / 2 + 2) * 4 <= sizeof(lds), "the exchange fits");
+    float* x = reinterpret_cast<float*>(lds) + wave * 64 * (C / 2 + 2) + lane;
+    __syncthreads();
+    if (group == 1) {
+#pragma unroll
+      for (int d = 0; d < C / 32; ++d)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) x[(16 * d + e) * 64] = acc[d][e];
+      x[(C / 2) * 64] = m;
+      x[(C / 2 + 1) * 64] = l;
+    }
+    __syncthreads();
+    if (group == 1) return;
+    const float was = m, other = x[(C / 2) * 64];
+    m = fmaxf(m, other);
+    const float base = m == -INFINITY ? 0.f : m, keep = exp2_of((was - base) * c), more = exp2_of((other - base) * c);
+    l = l * keep + x[(C / 2 + 1) * 64] * more;
+#pragma unroll
+    for (int d = 0; d < C / 32; ++d)
+#pragma unroll
+      for (int e = 0; e < 16; ++e) acc[d][e] = acc[d][e] * keep + x[(16 * d + e) * 64] * more;
+  }
   if (!live) return;
   l = sum_halves(l);
   store_row<T, C, HOW>(static_cast<T*>(a.out) + (sq.q0 + i) * a.ldout + (int64_t)head * hd, acc, l == 0.f ? 0.f : 1.f / l,
@@ -1300,7 +1330,8 @@ hipError_t attn_fwd(const AttnDesc& d, const AttnMat& Q, const AttnMat& K, const
     typedef decltype(t) T;
     constexpr int C = decltype(columns)::value;
     pick_how<T, C>(d, direct, [&](auto how) {
-      k_attn_fwd<T, C, decltype(how)::value><<<dim3((unsigned)(a.slots * d.heads)), kThreads, 0, s>>>(a);
+      k_attn_fwd<T, C, decltype(how)::value>
+          <<<dim3((unsigned)(a.slots * d.heads)), kThreads * kFwdGroups<T>, 0, s>>>(a);
     });
   });
   return hipGetLastError();
