@@ -220,6 +220,8 @@ template <int BYTES, bool OWN> PX_DEV void copy_to_lds(char* t, const char* base
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tglobal_load_lds_dword %1, %2" ::"s"((uint32_t)(uintptr_t)lds), "v"(at),
                  "s"(base) : "memory");
 }
+// This wave's copies.  Not even the builtin's are waited for at a barrier, and a wave that has nothing to compute with a
+// tile would come to the next barrier without having waited anywhere.
 PX_DEV void copies_done() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 template <int C, int N, int W, bool OWN> struct DmaRows {
   typedef RowsOf<bf16_t, C> R;
@@ -464,6 +466,7 @@ PX_DEV void over_tiles(char* lds, const T* K, int64_t ldk, const T* V, int64_t l
     copy(0, j0);
     zero_tail<C>(lds, 4 * KT, hd, (int)threadIdx.x, kThreads);
     for (int j = j0, x = 0; j < j1; j += KT, x ^= 2) {
+      copies_done();
       __syncthreads();  // this tile is there, and the other buffer is done with
       if (j + KT < j1) copy(2 - x, j + KT);
       f(x * R::bytes(KT), j);
@@ -1187,7 +1190,7 @@ template <int C, int HOW> __global__ __launch_bounds__(512, 2) void k_attn_dkv_d
   }
   int h = 0, i = t.i0;
   for (int n = 0, buf = 0; n < count; ++n, buf ^= P::BUF) {
-    if constexpr (P::OWN) copies_done();
+    copies_done();
     __syncthreads();  // this tile is there, and the other buffer is done with
     const int now = i;
     i += QT;
@@ -1284,8 +1287,10 @@ int key_shares(const AttnDesc& d) {
 namespace pxk {
 
 bool attn_fits(const AttnDesc& d) {
-  const double most = (double)((int64_t(1) << 31) - 1);
-  return (double)slots_of(d.Tq, d.batch) * d.heads <= most && (double)slots_of(d.Tk, d.batch) * d.kv_heads <= most;
+  // a launch has fewer than 2^32 threads: 512 a workgroup, and 64 a query and head where parts are joined
+  const int64_t most = (int64_t(1) << 23) - 1;
+  return slots_of(d.Tq, d.batch) * d.heads <= most && slots_of(d.Tk, d.batch) * d.kv_heads <= most &&
+         (few_part(d) == 0 || d.Tq * d.heads < (int64_t(1) << 26));
 }
 
 size_t attn_fwd_ws_bytes(const AttnDesc& d) {

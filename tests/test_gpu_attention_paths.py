@@ -181,3 +181,18 @@ def test_heads_of_a_multiple_of_eight_elsewhere():
     out = at.forward(q, k, v)
     A.check(at, O.Attn(4, 4, 40, float(np.float32(at.desc.scale)), True), "bf16", (q, k, v), dO, out, at.saved[4],
             at.backward(dO), A.cu_of([150]), A.cu_of([150]))
+
+
+@pytest.mark.parametrize("heads,kv,hd,lq,lk,causal,window", [
+    (64, 64, 32, [1000], [1000], True, 20),
+    (64, 64, 128, [1000], [1000], True, 20),
+    (64, 64, 64, [130, 900], [700, 900], True, 0),
+    (32, 32, 96, [130, 900], [700, 900], False, 33),
+])
+def test_waves_with_no_part_in_a_tile(heads, kv, hd, lq, lk, causal, window):
+    """Waves that skip the tiles which their rows do not see have copied a share of them all the same."""
+    at, mats, dO, out, grads, cu_q, cu_k = A.run(heads, kv, hd, "bf16", lq, lk, causal, window)
+    out, grads = out.clone(), [g.clone() for g in grads]
+    for _ in range(10):
+        assert torch.equal(at.forward(*mats, A.dev(cu_q), A.dev(cu_k)), out)
+        assert all(torch.equal(a, b) for a, b in zip(at.backward(dO), grads))
