@@ -122,6 +122,11 @@ struct LogpOut {
   int32_t* ids;
   float* lps;
 };
+// the same from row r on
+LogpOut rows_from(const LogpOut& o, int64_t r, int top) {
+  const auto at = [](auto* p, int64_t n) { return p ? p + n : p; };
+  return LogpOut{at(o.target, r), at(o.logp, r), at(o.lse, r), at(o.entropy, r), at(o.ids, r * top), at(o.lps, r * top)};
+}
 
 // what one row's sums and list say; wave 0 of the workgroup calls it
 template <typename T>
@@ -333,6 +338,7 @@ Cut cut(int64_t T, int V, int least) {
   return Cut{(V + span - 1) / span, span};
 }
 constexpr int kFwdLeast = 2048, kBwdLeast = 4096;
+constexpr int64_t kRowsAtOnce = 1 << 22;  // rows of a launch, whose threads have to stay below 2^32
 
 }  // namespace
 
@@ -352,11 +358,15 @@ static hipError_t fwd(int64_t rows, int V, int top, float scale, const void* Xv,
   const Cut k = cut(rows, V, kFwdLeast);
   float4* sums = static_cast<float4*>(ws);
   uint64_t* keys = reinterpret_cast<uint64_t*>(sums + rows * k.parts);
-  const dim3 grid((unsigned)(rows * k.parts));
-  if (top)
-    k_logp_fwd<T, true><<<grid, kThreads, 0, s>>>(X, ldx, V, top, scale, k.parts, k.span, sums, keys, o);
-  else
-    k_logp_fwd<T, false><<<grid, kThreads, 0, s>>>(X, ldx, V, 0, scale, k.parts, k.span, sums, keys, o);
+  for (int64_t r = 0; r < rows; r += kRowsAtOnce) {  // one launch where there are parts
+    const dim3 grid((unsigned)(std::min(rows - r, kRowsAtOnce) * k.parts));
+    const T* x = X + r * ldx;
+    const LogpOut to = rows_from(o, r, top);
+    if (top)
+      k_logp_fwd<T, true><<<grid, kThreads, 0, s>>>(x, ldx, V, top, scale, k.parts, k.span, sums, keys, to);
+    else
+      k_logp_fwd<T, false><<<grid, kThreads, 0, s>>>(x, ldx, V, 0, scale, k.parts, k.span, sums, keys, to);
+  }
   if (k.parts > 1)
     k_logp_join<T><<<dim3((unsigned)rows), kThreads, 0, s>>>(X, ldx, V, top, scale, k.parts, sums, keys, o);
   return hipGetLastError();
@@ -375,15 +385,18 @@ static hipError_t bwd(int64_t rows, int V, float scale, const void* X, int64_t l
                       const float* lse, const float* entropy, const float* dlogp, const float* dentropy, void* dX,
                       int64_t lddx, hipStream_t s) {
   const Cut k = cut(rows, V, kBwdLeast);
-  const dim3 grid((unsigned)(rows * k.parts));
-  const T* x = static_cast<const T*>(X);
-  T* dx = static_cast<T*>(dX);
-  if (dentropy)
-    k_logp_bwd<T, true><<<grid, kThreads, 0, s>>>(x, ldx, V, scale, k.parts, k.span, target, lse, entropy, dlogp,
-                                                  dentropy, dx, lddx);
-  else
-    k_logp_bwd<T, false><<<grid, kThreads, 0, s>>>(x, ldx, V, scale, k.parts, k.span, target, lse, entropy, dlogp,
-                                                   dentropy, dx, lddx);
+  const auto at = [](auto* p, int64_t r) { return p ? p + r : p; };
+  for (int64_t r = 0; r < rows; r += kRowsAtOnce) {
+    const dim3 grid((unsigned)(std::min(rows - r, kRowsAtOnce) * k.parts));
+    const T* x = static_cast<const T*>(X) + r * ldx;
+    T* dx = static_cast<T*>(dX) + r * lddx;
+    if (dentropy)
+      k_logp_bwd<T, true><<<grid, kThreads, 0, s>>>(x, ldx, V, scale, k.parts, k.span, at(target, r), lse + r,
+                                                    at(entropy, r), at(dlogp, r), at(dentropy, r), dx, lddx);
+    else
+      k_logp_bwd<T, false><<<grid, kThreads, 0, s>>>(x, ldx, V, scale, k.parts, k.span, at(target, r), lse + r,
+                                                     at(entropy, r), at(dlogp, r), at(dentropy, r), dx, lddx);
+  }
   return hipGetLastError();
 }
 

@@ -21,7 +21,7 @@ struct RopeArgs {
   RopeSide side[kRopeSides];
   const int32_t* pos;
   const double* freqs;
-  int64_t T;
+  int64_t T, first;  // first: the launch's first token
   float amplitude, sign;
   int count, hd, rot, tokens;  // tokens of a workgroup
 };
@@ -45,7 +45,7 @@ template <typename T, int W> PX_DEV void store_w(T* p, const float (&f)[W]) {
 template <typename T, int W, bool PAIRS> __global__ __launch_bounds__(kThreads) void k_rope(RopeArgs a) {
   extern __shared__ float2 turn[];  // [tokens][rot / 2]: cos, sin
   const int half = a.rot / 2;
-  const int64_t t0 = (int64_t)blockIdx.x * a.tokens;
+  const int64_t t0 = a.first + (int64_t)blockIdx.x * a.tokens;
   const int nt = (int)min((int64_t)a.tokens, a.T - t0);
   for (int i = threadIdx.x; i < nt * half; i += kThreads) {
     const int t = i / half;
@@ -108,13 +108,16 @@ template <typename T, int W, bool PAIRS> __global__ __launch_bounds__(kThreads) 
   }
 }
 
-template <typename T, int W> hipError_t launch(const RopeArgs& a, bool pairs, hipStream_t s) {
-  const dim3 grid((unsigned)((a.T + a.tokens - 1) / a.tokens));
+template <typename T, int W> hipError_t launch(RopeArgs a, bool pairs, hipStream_t s) {
+  const int64_t most = int64_t(1) << 22;  // workgroups of a launch, whose threads have to stay below 2^32
   const int lds = a.tokens * (a.rot / 2) * (int)sizeof(float2);
-  if (pairs)
-    k_rope<T, W, true><<<grid, kThreads, lds, s>>>(a);
-  else
-    k_rope<T, W, false><<<grid, kThreads, lds, s>>>(a);
+  for (a.first = 0; a.first < a.T; a.first += most * a.tokens) {
+    const dim3 grid((unsigned)std::min(most, (a.T - a.first + a.tokens - 1) / a.tokens));
+    if (pairs)
+      k_rope<T, W, true><<<grid, kThreads, lds, s>>>(a);
+    else
+      k_rope<T, W, false><<<grid, kThreads, lds, s>>>(a);
+  }
   return hipGetLastError();
 }
 

@@ -183,6 +183,29 @@ def test_heads_of_a_multiple_of_eight_elsewhere():
             at.backward(dO), A.cu_of([150]), A.cu_of([150]))
 
 
+def test_more_rows_than_a_launch_holds():
+    """Rows whose workgroups of one launch would have 2^32 threads and more: every 1024 rows give the same bits."""
+    T, n = 2**24 + 1024, 1024
+    op, few = PoetxLogProb(3, top=2), PoetxLogProb(3, top=2)
+    X, t = LP.logits(n, 3, "bf16", 1), LP.targets(n, 3, 2)
+    g, h = (torch.randn(n, device="cuda", generator=torch.Generator("cuda").manual_seed(s)) for s in (3, 4))
+    many = lambda x: x.repeat(T // n, *[1] * (x.dim() - 1))
+    for a, b in zip(op.forward(many(X), many(t)), few.forward(X, t)):
+        assert torch.equal(a.view(T // n, *b.shape), b.expand(T // n, *b.shape))
+    dX = few.backward(g, h)
+    assert torch.equal(op.backward(many(g), many(h)).view(T // n, n, 3), dX.expand(T // n, n, 3))
+
+
+def test_more_tokens_than_a_launch_holds():
+    rope = PoetxRope(512)  # a workgroup a token
+    T, at = 2**22 + 2, [0, 2**22 - 1, 2**22, 2**22 + 1]
+    x = A.rows(1, 512, "bf16", 1)
+    X = x.expand(T, 512).contiguous()
+    rope.forward([X], Ys=[X])
+    want = rope.forward([x.expand(4, 512).contiguous()], torch.tensor(at, dtype=torch.int32, device="cuda"))[0]
+    assert torch.equal(X[at], want)
+
+
 @pytest.mark.parametrize("heads,kv,hd,lq,lk,causal,window", [
     (64, 64, 32, [1000], [1000], True, 20),
     (64, 64, 128, [1000], [1000], True, 20),
