@@ -850,7 +850,7 @@ poetx_status poetx_rope(const poetx_rope_desc* desc, int64_t T, const int32_t* p
  *   - with window w > 0: place - j < w, and j - place < w.
  * A query that sees no key gets O = 0 and lse = -infinity, and no gradient.
  * The scores, the softmax and all sums are fp32.  In bf16 the probabilities
- * (and in the backward their gradients) are rounded to bf16 as operands of the
+ * (and in the backward the scores' gradients) are rounded to bf16 as operands of the
  * products, O and the gradients once at the end; POETX_F32 rounds nothing.
  * An infinity or NaN in a sequence's rows may reach any row of that sequence,
  * and none of another.
@@ -883,6 +883,8 @@ size_t poetx_attn_workspace_size(const poetx_attn_desc* desc, int32_t batch, int
  *   lse    out fp32 [heads][Tq]
  *   ws     >= poetx_attn_workspace_size(desc, batch, Tq, Tk, POETX_OP_FWD)
  *   batch  1 .. 65536;  Tq, Tk  0 .. 2^30.  Tq = 0 is a no-op.
+ * A launch takes all rows: heads (Tq / 128 + batch) and
+ * kv_heads (Tk / 128 + batch) have to be below 2^23.
  * Errors: POETX_E_NULL, POETX_E_SHAPE, POETX_E_DTYPE, POETX_E_WORKSPACE, POETX_E_HIP.
  */
 poetx_status poetx_attn_fwd(const poetx_attn_desc* desc, int32_t batch, int64_t Tq, int64_t Tk, const int32_t* cu_q,

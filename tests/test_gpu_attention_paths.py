@@ -219,3 +219,18 @@ def test_waves_with_no_part_in_a_tile(heads, kv, hd, lq, lk, causal, window):
     for _ in range(10):
         assert torch.equal(at.forward(*mats, A.dev(cu_q), A.dev(cu_k)), out)
         assert all(torch.equal(a, b) for a, b in zip(at.backward(dO), grads))
+
+
+def test_more_joined_rows_than_a_launch_holds():
+    """Many short sequences and a long one behind them, whose parts are joined by a second launch."""
+    heads, n = 512, 15000
+    at = PoetxAttention(heads, heads, 1, causal=False)
+    lq, lk = [3] * n + [3], [2] * n + [600]
+    q, k, v = (A.rows(sum(x), heads, "bf16", s) for x, s in ((lq, 1), (lk, 2), (lk, 3)))
+    dO = A.rows(sum(lq), heads, "bf16", 4)
+    out = at.forward(q, k, v, A.dev(A.cu_of(lq)), A.dev(A.cu_of(lk)))
+    dQ, dK, dV = at.backward(dO)
+    c, lse = O.Attn(heads, heads, 1, float(np.float32(at.desc.scale)), False), at.saved[4]
+    for a, b, x, y in ((0, 3, 0, 2), (-3, None, -600, None)):
+        A.check(at, c, "bf16", (q[a:b], k[x:y], v[x:y]), dO[a:b], out[a:b], lse[:, a:b], (dQ[a:b], dK[x:y], dV[x:y]),
+                A.cu_of([3]), A.cu_of([2 if b else 600]))
