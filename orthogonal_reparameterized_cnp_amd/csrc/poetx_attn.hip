@@ -174,8 +174,8 @@ template <typename T, int C> using RowsOf = Rows<T, sizeof(T) == 4 ? C : C <= 64
 // whether the columns from c on are multiplied with
 template <typename T> PX_DEV bool within(int c, int hd) { return sizeof(T) == 2 || c < hd; }
 
-// How tiles come to LDS: through registers (any type, head and alignment), by direct copies, which take heads of a multiple
-// of 8 columns (96 columns: forward 1300 us through registers, 250 by copies), and by direct copies of heads that fill the
+// How tiles come to LDS: through registers (any type, head and alignment), by direct copies, which take rows of heads of a
+// multiple of 8 columns (96 columns: forward 1300 us through registers, 250 by copies), and by direct copies of heads that fill the
 // rows, which need not ask where the head ends (16 tokens over 20k keys: 39.2 us with the question, 36.3 without).
 enum How { kStaged, kDirect, kWhole };
 
@@ -185,7 +185,7 @@ template <int HOW, typename T> PX_DEV void load8(T (&v)[8], const T* row, bool t
     __builtin_memcpy(v, row + c, sizeof(v));
   } else {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = HOW == kStaged && there && c + i < hd ? row[c + i] : T(0);
+    for (int i = 0; i < 8; ++i) v[i] = HOW != kWhole && there && c + i < hd ? row[c + i] : T(0);
   }
 }
 // rows [r0, r0 + N) of a sequence's `n`, into an LDS tile by way of registers: any type, head and alignment
@@ -289,7 +289,7 @@ PX_DEV void store_row(T* row, const f32x16_v (&acc)[C / 32], float scale, int hd
       for (int i = 0; i < 4; ++i) v[i] = from_f32<T>(acc[d][4 * g + i] * scale);
       if (c + 4 <= hd) {
         __builtin_memcpy(row + c, v, sizeof(v));
-      } else if constexpr (HOW == kStaged) {
+      } else if constexpr (HOW != kWhole) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
           if (c + i < hd) row[c + i] = v[i];
@@ -311,7 +311,8 @@ struct AttnArgs {
                       // maximum and sum and from part_head on their O
   float* parts;       // the shares' dK and dV, [shares][2][kv_heads][Tk][C]
   Side q, k;
-  int batch, heads, group, hd, window;
+  int batch, heads, group, window;
+  int hd, row_hd;  // columns of a head; row_hd: in the rows that are copied straight to LDS, hd or its multiple of 8 above
   int part;    // keys of a workgroup in the forward of few rows
   int shares;  // workgroups that share the query heads of a key head in dK and dV
   bool causal;
@@ -422,8 +423,8 @@ PX_DEV Span keys_of_wave(const AttnArgs& a, int first, const Seq& sq) {
 // 64 sequences the order is exact: with f(k) tiles of the k-th class and above, a lane a class,
 //     f(k) = sum over the sequences of max(tiles - k, 0);
 // more sequences are taken as equal ones, and so are those of a launch that the card takes at once (`order` false), which
-// has nothing to fill (the 60M layer's forward 9.0 us, in order 9.4).  16 sequences of 7 to 2048 tokens, 16 heads: forward 170 -> 151 us, backward 540 -> 522 against
-// equal ones.  Returns the sequence, with *tile < 0 where there is none.
+// has nothing to fill (the 60M layer's forward 9.0 us, in order 9.4).  16 sequences of 7 to 2048 tokens, 16 heads: forward
+// 170 -> 151 us, backward 540 -> 522 against equal ones.  Returns the sequence, with *tile < 0 where there is none.
 PX_DEV int tile_of(const Side& x, int batch, int64_t slots, int64_t n, int R, bool order, bool ends, int* tile) {
   if (!order || batch > 64) {
     const int64_t per = slots / batch, t = n / batch;
@@ -546,8 +547,9 @@ __global__ __launch_bounds__(kThreads * kFwdGroups<T>, HOW ? 2 : 1) void k_attn_
   if (tile < 0 || w0 >= sq.nq) return;
   const int shift = sq.nk - sq.nq, i = w0 + 32 * wave + (lane & 31);  // this lane's query
   const bool live = i < sq.nq;
-  const T* K = static_cast<const T*>(a.K) + sq.k0 * a.ldk + (int64_t)(head / a.group) * hd;
-  const T* V = static_cast<const T*>(a.V) + sq.k0 * a.ldv + (int64_t)(head / a.group) * hd;
+  const int row_hd = HOW == kWhole ? C : a.row_hd;
+  const T* K = static_cast<const T*>(a.K) + sq.k0 * a.ldk + (int64_t)(head / a.group) * row_hd;
+  const T* V = static_cast<const T*>(a.V) + sq.k0 * a.ldv + (int64_t)(head / a.group) * row_hd;
   Frag<T> q[C / 16];
   row_frags<T, C, HOW>(q, static_cast<const T*>(a.Q) + (sq.q0 + i) * a.ldq + (int64_t)head * hd, live, hd, lane);
   const Sees see = live ? keys_of(a, i + shift, sq.nk) : Sees{0, 0};
@@ -604,7 +606,7 @@ __global__ __launch_bounds__(kThreads * kFwdGroups<T>, HOW ? 2 : 1) void k_attn_
           if (within<T>(32 * d, hd)) mma(acc[d], R::across(tv, at, 32 * b + 16 * h, 32 * d), p);
       }
   };
-  over_tiles<T, C, HOW, KT, kThreads * G>(lds, K, a.ldk, V, a.ldv, sq.nk, hd, j0, j1,
+  over_tiles<T, C, HOW, KT, kThreads * G>(lds, K, a.ldk, V, a.ldv, sq.nk, row_hd, j0, j1,
                                           [&](int tile, int j) __attribute__((always_inline)) {
                                             j += PART * group, tile += R::bytes(PART) * group;
                                             if (w.all(j, j + PART)) step(tile, j, std::false_type());
@@ -911,8 +913,9 @@ template <typename T, int C, int HOW> __global__ __launch_bounds__(kThreads, HOW
   if (tile < 0 || w0 >= sq.nq) return;
   const int shift = sq.nk - sq.nq, i = w0 + 32 * wave + (lane & 31);
   const bool live = i < sq.nq;
-  const T* K = static_cast<const T*>(a.K) + sq.k0 * a.ldk + (int64_t)(head / a.group) * hd;
-  const T* V = static_cast<const T*>(a.V) + sq.k0 * a.ldv + (int64_t)(head / a.group) * hd;
+  const int row_hd = HOW == kWhole ? C : a.row_hd;
+  const T* K = static_cast<const T*>(a.K) + sq.k0 * a.ldk + (int64_t)(head / a.group) * row_hd;
+  const T* V = static_cast<const T*>(a.V) + sq.k0 * a.ldv + (int64_t)(head / a.group) * row_hd;
   Frag<T> q[C / 16], g[C / 16];
   row_frags<T, C, HOW>(q, static_cast<const T*>(a.Q) + (sq.q0 + i) * a.ldq + (int64_t)head * hd, live, hd, lane);
   float delta = 0.f;
@@ -977,7 +980,7 @@ template <typename T, int C, int HOW> __global__ __launch_bounds__(kThreads, HOW
       }
     }
   };
-  over_tiles<T, C, HOW, KT>(lds, K, a.ldk, V, a.ldv, sq.nk, hd, j0, j1,
+  over_tiles<T, C, HOW, KT>(lds, K, a.ldk, V, a.ldv, sq.nk, row_hd, j0, j1,
                             [&](int tile, int j) __attribute__((always_inline)) {
                               if (w.any(j, j + KT)) step(tile, j);
                             });
@@ -1177,7 +1180,7 @@ template <int C, int HOW> __global__ __launch_bounds__(512, 2) void k_attn_dkv_d
   constexpr int QT = P::QT;
   extern __shared__ __align__(16) char lds[];
   char *const tk = lds, *const tv = lds + P::KEYS, *const bufs = lds + 2 * P::KEYS;
-  const int lane = threadIdx.x & 63, wave = wave_id(), hd = HOW == kWhole ? C : a.hd;
+  const int lane = threadIdx.x & 63, wave = wave_id(), hd = HOW == kWhole ? C : a.row_hd;
   const int keys = 32 * (wave & 3), half = wave >> 2;
   const KeyTile t = key_tile(a, QT);
   if (!t.any) return;
@@ -1248,7 +1251,29 @@ template <int C, int HOW> __global__ __launch_bounds__(512, 2) void k_attn_dkv_d
       dk[d][e] = half ? x + dv[d][e] : dk[d][e] + x;
     }
   if (!live) return;
-  store_grad<T, C, HOW>(a, t, half, j, dk, hd, lane);
+  store_grad<T, C, HOW>(a, t, half, j, dk, HOW == kWhole ? C : a.hd, lane);
+}
+
+// Rows of heads of any length as rows of heads of a multiple of 8 columns, zeros behind the head: 16 bytes a thread.
+struct Pack {
+  const void* from[4];
+  bf16_t* to[4];
+  int64_t ld[4];
+  Side side[4];
+  int heads[4];
+  int batch, hd, row_hd;
+};
+__global__ __launch_bounds__(kThreads) void k_attn_pack(Pack a) {
+  const int m = blockIdx.y, k = a.row_hd / 8, per = a.heads[m] * k;
+  const int64_t end = first_row(a.side[m], a.batch) * per;
+  for (int64_t x = first_row(a.side[m], 0) * per + (int64_t)blockIdx.x * kThreads + threadIdx.x; x < end;
+       x += (int64_t)gridDim.x * kThreads) {
+    const int64_t row = x / per;
+    const int head = (int)(x - row * per) / k, c = (int)(x - row * per) % k;
+    bf16_t v[8];
+    load8<kStaged>(v, static_cast<const bf16_t*>(a.from[m]) + row * a.ld[m] + (int64_t)head * a.hd, true, 8 * c, a.hd);
+    __builtin_memcpy(a.to[m] + 8 * x, v, sizeof(v));
+  }
 }
 
 int64_t slots_of(int64_t rows, int batch, int R = kRows) { return rows / R + batch; }
@@ -1260,7 +1285,7 @@ AttnArgs args_of(const AttnDesc& d) {
   a.batch = d.batch;
   a.heads = d.heads;
   a.group = d.heads / d.kv_heads;
-  a.hd = d.hd;
+  a.hd = a.row_hd = d.hd;
   a.window = d.window;
   a.causal = d.causal;
   a.scale = d.scale;
@@ -1298,6 +1323,33 @@ template <typename T, int C, class F> void pick_how(const AttnDesc& d, bool dire
   f(std::integral_constant<int, kStaged>());
 }
 
+// bf16 heads of no multiple of 8 columns: whether they are laid out as heads of one first, for the direct copies.  It is a
+// launch more, which sequences of 128 keys on the average make up for.  75 columns, 8 heads over 4, us through registers
+// and laid out first: forward 10.6 and 13.4 at 64 tokens, 19.1 and 15.5 at 256, 51 and 28 at 1024; backward 28.4 and 28.2,
+// 54 and 39, 143 and 78; 2 x 4096 tokens of 32 heads forward 512 and 268, backward 2380 and 870.
+bool packs(const AttnDesc& d) { return d.dt == BF16 && d.hd % 8 != 0 && d.Tk >= 128 * (int64_t)d.batch; }
+int64_t packed_row(const AttnDesc& d, int heads) { return heads * round_up(d.hd, 8); }
+size_t packed_bytes(const AttnDesc& d, int64_t rows, int heads) {
+  return (size_t)round_up(rows * packed_row(d, heads) * 2, 256);
+}
+// `mats` (of the queries or of the keys) laid out at ws, where they are from then on
+void pack(const AttnDesc& d, AttnArgs& a, AttnMat* const* mats, const bool* keys, int count, void* ws, hipStream_t s) {
+  Pack p = {};
+  p.batch = d.batch, p.hd = d.hd, p.row_hd = a.row_hd = (int)round_up(d.hd, 8);
+  char* to = static_cast<char*>(ws);
+  int64_t most = 0;
+  for (int i = 0; i < count; ++i) {
+    const int heads = keys[i] ? d.kv_heads : d.heads;
+    p.side[i] = keys[i] ? a.k : a.q;
+    p.from[i] = mats[i]->p, p.ld[i] = mats[i]->ld, p.heads[i] = heads, p.to[i] = reinterpret_cast<bf16_t*>(to);
+    *mats[i] = AttnMat{to, packed_row(d, heads)};
+    to += packed_bytes(d, p.side[i].rows, heads);
+    most = std::max(most, p.side[i].rows * packed_row(d, heads) / 8);
+  }
+  const unsigned grid = (unsigned)std::min<int64_t>((most + kThreads - 1) / kThreads, 1 << 14);
+  if (grid) k_attn_pack<<<dim3(grid, count), kThreads, 0, s>>>(p);
+}
+
 // The keys of a workgroup in the forward of few rows; 0 where a tile of 32 rows does not hold a sequence's queries on the
 // average, and the tiles of 128 queries are taken (16 tokens over 1 to 8192 keys: 732 us with those).  Parts are as long as
 // leaves the card some 512 workgroups, two a CU (256 to 1024 of them measured the same or slower), and a sequence two.
@@ -1328,23 +1380,34 @@ bool attn_fits(const AttnDesc& d) {
 
 size_t attn_fwd_ws_bytes(const AttnDesc& d) {
   const int part = few_part(d);
+  if (part == 0 && packs(d)) return 2 * packed_bytes(d, d.Tk, d.kv_heads);
   if (part == 0 || d.Tk <= part) return 0;  // the latter: no sequence has two parts
   return (size_t)slots_of(d.Tk, d.batch, part) * d.kv_heads * kFewRows * (2 + width(d)) * 4;
 }
 static size_t shares_at(const AttnDesc& d) { return (size_t)round_up((int64_t)d.heads * d.Tq * 8, 256); }
-size_t attn_bwd_ws_bytes(const AttnDesc& d) {
+static size_t packed_at(const AttnDesc& d) {
   const int n = key_shares(d);
-  return shares_at(d) + (n > 1 ? (size_t)n * 2 * d.kv_heads * d.Tk * width(d) * 4 : 0);
+  return shares_at(d) + (n > 1 ? (size_t)round_up((int64_t)n * 2 * d.kv_heads * d.Tk * width(d) * 4, 256) : 0);
+}
+size_t attn_bwd_ws_bytes(const AttnDesc& d) {
+  return packed_at(d) + (packs(d) ? 2 * packed_bytes(d, d.Tk, d.kv_heads) + 2 * packed_bytes(d, d.Tq, d.heads) : 0);
 }
 
-hipError_t attn_fwd(const AttnDesc& d, const AttnMat& Q, const AttnMat& K, const AttnMat& V, void* O, int64_t ldo,
+hipError_t attn_fwd(const AttnDesc& d, const AttnMat& Q, const AttnMat& K0, const AttnMat& V0, void* O, int64_t ldo,
                     float* lse, void* ws, hipStream_t s) {
   if (d.Tq == 0) return hipSuccess;
   AttnArgs a = args_of(d);
+  AttnMat K = K0, V = V0;
+  const bool packed = few_part(d) == 0 && packs(d);
+  if (packed) {
+    AttnMat* const mats[] = {&K, &V};
+    const bool keys[] = {true, true};
+    pack(d, a, mats, keys, 2, ws, s);
+  }
   a.Q = Q.p, a.ldq = Q.ld, a.K = K.p, a.ldk = K.ld, a.V = V.p, a.ldv = V.ld;
   a.out = O, a.ldout = ldo, a.lse = lse, a.rows = static_cast<float*>(ws);
   a.part = few_part(d);
-  const bool direct = direct_heads(d) && direct_rows(K) && direct_rows(V);
+  const bool direct = packed || (direct_heads(d) && direct_rows(K) && direct_rows(V));
   if (a.part) {
     hipError_t e = hipSuccess;
     const int64_t slots = slots_of(d.Tk, d.batch, a.part);
@@ -1377,13 +1440,21 @@ hipError_t attn_fwd(const AttnDesc& d, const AttnMat& Q, const AttnMat& K, const
   return hipGetLastError();
 }
 
-hipError_t attn_bwd(const AttnDesc& d, const AttnMat& dO, const AttnMat& Q, const AttnMat& K, const AttnMat& V,
+hipError_t attn_bwd(const AttnDesc& d, const AttnMat& dO0, const AttnMat& Q0, const AttnMat& K0, const AttnMat& V0,
                     const AttnMat& O, const float* lse, void* dQ, int64_t lddq, void* dK, int64_t lddk, void* dV,
                     int64_t lddv, void* ws, hipStream_t s) {
-  const bool direct = direct_heads(d) && direct_rows(K) && direct_rows(V);
   AttnArgs a = args_of(d);
-  a.Q = Q.p, a.ldq = Q.ld, a.K = K.p, a.ldk = K.ld, a.V = V.p, a.ldv = V.ld, a.O = O.p, a.ldo = O.ld;
-  a.dO = dO.p, a.lddo = dO.ld;
+  AttnMat dO = dO0, Q = Q0, K = K0, V = V0;
+  const bool packed = packs(d);
+  if (packed) {
+    AttnMat* const mats[] = {&K, &V, &Q, &dO};
+    const bool keys[] = {true, true, false, false};
+    pack(d, a, mats, keys, 4, static_cast<char*>(ws) + packed_at(d), s);
+  }
+  const bool direct = packed || (direct_heads(d) && direct_rows(K) && direct_rows(V));
+  // dQ reads the caller's rows of Q and dO, dK and dV the ones for the copies
+  a.Q = Q0.p, a.ldq = Q0.ld, a.K = K.p, a.ldk = K.ld, a.V = V.p, a.ldv = V.ld, a.O = O.p, a.ldo = O.ld;
+  a.dO = dO0.p, a.lddo = dO0.ld;
   a.lse = const_cast<float*>(lse), a.rows = static_cast<float*>(ws);
   if (d.Tq > 0) {
     a.out = dQ, a.ldout = lddq;
@@ -1400,6 +1471,7 @@ hipError_t attn_bwd(const AttnDesc& d, const AttnMat& dO, const AttnMat& Q, cons
   }
   if (d.Tk == 0) return hipSuccess;
   a.out = dK, a.ldout = lddk, a.out2 = dV, a.ldout2 = lddv;
+  a.Q = Q.p, a.ldq = Q.ld, a.dO = dO.p, a.lddo = dO.ld;
   a.shares = key_shares(d);
   a.parts = reinterpret_cast<float*>(static_cast<char*>(ws) + shares_at(d));
   a.slots = slots_of(d.Tk, d.batch);

@@ -234,3 +234,53 @@ def test_more_joined_rows_than_a_launch_holds():
     for a, b, x, y in ((0, 3, 0, 2), (-3, None, -600, None)):
         A.check(at, c, "bf16", (q[a:b], k[x:y], v[x:y]), dO[a:b], out[a:b], lse[:, a:b], (dQ[a:b], dK[x:y], dV[x:y]),
                 A.cu_of([3]), A.cu_of([2 if b else 600]))
+
+
+@pytest.mark.parametrize("hd", [1, 37, 75, 127])
+def test_heads_that_are_laid_out_first(hd):
+    """bf16 heads of no multiple of 8 columns over longer sequences: rows outside all sequences (not-a-numbers) stay out of
+    it, and a workspace of exactly the bytes asked for holds what the calls write."""
+    A.run(6, 2, hd, "bf16", [1, 130, 300], [150, 130, 300], True, 0, seed=hd, first=3, behind=2)
+    A.run(4, 4, hd, "bf16", [260, 5], [300, 100], False, 70)
+    A.run(16, 1, hd, "bf16", [200, 133], [200, 133], seed=1)  # query heads shared among workgroups
+    heads, kv, lens = 6, 2, [130, 300]
+    cu = A.dev(A.cu_of(lens, 3))
+    T, nq, nk = 435, heads * hd, kv * hd
+    q, k, v, g = (A.rows(T, n, "bf16", s) for n, s in ((nq, 1), (nk, 2), (nk, 3), (nq, 4)))
+    at = PoetxAttention(heads, kv, hd)
+    want = [at.forward(q, k, v, cu)[3:433].clone(), *(x[3:433].clone() for x in at.backward(g))]
+    for x in (q, k, v, g):
+        x[:3] = x[433:] = float("nan")
+    o, lse = torch.zeros_like(q), torch.empty(heads, T, device="cuda")
+    dq, dk, dv = torch.zeros_like(q), torch.zeros_like(k), torch.zeros_like(v)
+    for op in (B.POETX_OP_FWD, B.POETX_OP_BWD):
+        n = B.poetx_attn_workspace_size(at.desc, 2, T, T, op)
+        ws = torch.full((n + 4096,), 0x5A, dtype=torch.uint8, device="cuda")
+        if op == B.POETX_OP_FWD:
+            B.poetx_attn_fwd(at.desc, 2, T, T, cu, cu, q, nq, k, nk, v, nk, o, nq, lse, ws, n)
+        else:
+            B.poetx_attn_bwd(at.desc, 2, T, T, cu, cu, g, nq, q, nq, k, nk, v, nk, o, nq, lse, dq, nq, dk, nk, dv, nk, ws, n)
+        torch.cuda.synchronize()
+        assert (ws[n:] == 0x5A).all()
+    assert all(torch.equal(x[3:433], y) for x, y in zip((o, dq, dk, dv), want))
+    assert not any(x[:3].any() or x[433:].any() for x in (o, dq, dk, dv))
+
+
+def test_heads_that_are_laid_out_first_in_a_graph():
+    at = PoetxAttention(6, 2, 37)
+    q, k, v, g = (A.rows(430, n * 37, "bf16", s) for n, s in ((6, 1), (2, 2), (2, 3), (6, 4)))
+    cu = A.dev(A.cu_of([130, 300]))
+    want = [at.forward(q, k, v, cu), *at.backward(g)]
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = [at.forward(q, k, v, cu), *at.backward(g)]
+    for _ in range(3):
+        for x in got:
+            x.fill_(A.MARK)
+        got[0].zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert all(torch.equal(x, y) for x, y in zip(got, want))
+        assert torch.equal(at.forward(q, k, v, cu), want[0])
+        at.forward(q, k, v, cu)
