@@ -800,7 +800,8 @@ typedef enum {
   POETX_ROPE_BANDS = 3,  /* with r = original f / (2 pi), the turns within the original length: f / factor for r <= low,
                             f for r >= high, and in between the mix that is linear in r */
   POETX_ROPE_RAMP = 4    /* the same with the mix linear in j, between the (real) j that make `low` and `high` turns,
-                            rounded down for high and up for low; amplitude 1 + 0.1 ln(factor) */
+                            rounded down for high and up for low and held within 0 .. rot_dim - 1 (which may lie behind
+                            the last pair); amplitude 1 + 0.1 ln(factor) */
 } poetx_rope_scaling;
 
 typedef struct {

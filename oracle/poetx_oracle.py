@@ -759,9 +759,9 @@ def rope_freqs(rot_dim: int, base: float = 10000.0, scaling: str = "none", facto
         turns = original * f / (2 * np.pi)
         share = np.interp(turns, [low, high], [0.0, 1.0])  # of the unscaled frequency
         return share * f + (1 - share) * f / factor, 1.0
-    # ramp: the pairs where f makes `high` and `low` turns, on whole numbers
+    # ramp: the pairs where f makes `high` and `low` turns, on whole numbers; the end may lie behind the last pair
     at = lambda turns: rot_dim * np.log(original / (2 * np.pi * turns)) / (2 * np.log(base))
-    first, last = max(np.floor(at(high)), 0), min(np.ceil(at(low)), rot_dim // 2 - 1)
+    first, last = max(np.floor(at(high)), 0), min(np.ceil(at(low)), rot_dim - 1)
     last = max(last, first + 1e-3)
     share = 1 - np.clip((j - first) / (last - first), 0, 1)
     return share * f + (1 - share) * f / factor, 1 + 0.1 * np.log(factor)

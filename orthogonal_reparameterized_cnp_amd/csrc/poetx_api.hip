@@ -1937,7 +1937,7 @@ poetx_status poetx_rope_freqs(int32_t rot_dim, const poetx_rope_params* p, doubl
   double j0 = 0.0, j1 = 0.0;
   if (ramp) {
     j0 = std::max(std::floor(pair_of(p->high)), 0.0);
-    j1 = std::min(std::ceil(pair_of(p->low)), rot_dim / 2 - 1.0);
+    j1 = std::min(std::ceil(pair_of(p->low)), rot_dim - 1.0);  // may lie behind the last pair, which is then in the ramp
     j1 = std::max(j1, j0 + 1e-3);  // a step where the two meet
   }
   for (int j = 0; j < rot_dim / 2; ++j) {
