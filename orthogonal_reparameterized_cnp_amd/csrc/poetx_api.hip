@@ -3,6 +3,7 @@
 // poetx_kernels.hip.
 #include <algorithm>
 #include <cmath>
+#include <limits>
 #include <mutex>
 #include <string>
 #include <vector>
@@ -1928,11 +1929,11 @@ poetx_status poetx_rope_freqs(int32_t rot_dim, const poetx_rope_params* p, doubl
       return fail(POETX_E_SHAPE, "low and high must satisfy 0 < low < high");
   }
   const double two_pi = 6.28318530717958647693;
-  double base = p->base;
-  if (p->scaling == POETX_ROPE_BASE) base *= std::pow(p->factor, rot_dim / (rot_dim - 2.0));
-  // the (real) pair that makes `turns` turns within the original length: original base^(-2 j / rot_dim) = 2 pi turns
+  // The (real) pair that makes `turns` turns within the original length: original base^(-2 j / rot_dim) = 2 pi turns.
+  // Where the quotient overflows, its largest value names a pair behind the last one all the same.
   const auto pair_of = [&](double turns) {
-    return 0.5 * rot_dim * std::log(p->original / (two_pi * turns)) / std::log(base);
+    const double ratio = std::min(p->original / (two_pi * turns), std::numeric_limits<double>::max());
+    return 0.5 * rot_dim * std::log(ratio) / std::log(p->base);
   };
   double j0 = 0.0, j1 = 0.0;
   if (ramp) {
@@ -1941,7 +1942,9 @@ poetx_status poetx_rope_freqs(int32_t rot_dim, const poetx_rope_params* p, doubl
     j1 = std::max(j1, j0 + 1e-3);  // a step where the two meet
   }
   for (int j = 0; j < rot_dim / 2; ++j) {
-    const double f = std::pow(base, -2.0 * j / rot_dim);
+    double f = std::pow(p->base, -2.0 * j / rot_dim);
+    // that power of the larger base, which itself may leave a double's range
+    if (p->scaling == POETX_ROPE_BASE) f *= std::pow(p->factor, -2.0 * j / (rot_dim - 2.0));
     double keep = 1.0;  // the share of f that is left unscaled
     if (p->scaling == POETX_ROPE_LINEAR) keep = 0.0;
     if (bands) keep = (p->original * f / two_pi - p->low) / (p->high - p->low);

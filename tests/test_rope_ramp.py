@@ -31,3 +31,18 @@ def test_ramp(N, low, high, share, freqs):
     share = np.array(share, dtype=float)
     np.testing.assert_allclose(f, 4.0 ** -np.arange(4) * (share + (1 - share) / 4), rtol=1e-13)
     assert amp == pytest.approx(1 + 0.1 * np.log(4), rel=1e-7)
+
+
+def test_the_ends_of_the_parameters():
+    """Parameters whose quotients and powers leave the range of a double give the frequencies that the formulas name."""
+    f = 10.0 ** -np.arange(4)  # rot_dim 8, base 10^4
+    for low, high, original in ((1e-310, 1e-309, 1e10), (1e-20, 1e-10, 1e300)):  # every pair makes more than `high` turns
+        for scaling in ("ramp", "bands"):
+            got, _ = LIBRARY(8, base=1e4, scaling=scaling, factor=4.0, original=original, low=low, high=high)
+            np.testing.assert_allclose(got, f, rtol=1e-13)
+    for scaling in ("ramp", "bands"):  # and fewer than `low`
+        got, _ = LIBRARY(8, base=1e4, scaling=scaling, factor=4.0, original=1.0, low=1e307, high=1.7e308)
+        np.testing.assert_allclose(got[scaling == "ramp":], f[scaling == "ramp":] / 4, rtol=1e-13)
+    # the last pair turns `factor` times slower, however large the base that this takes
+    got, _ = LIBRARY(4, base=1e4, scaling="base", factor=1e200)
+    np.testing.assert_allclose(got, [1.0, 1e-202], rtol=1e-13)
