@@ -843,6 +843,8 @@ template <typename T, int C> __global__ __launch_bounds__(kThreads) void k_attn_
   const Seq sq = sequence(a, s);
   const int kv = head / a.group, row = (int)(i - sq.q0) * a.group + head % a.group, parts = parts_of(a, sq);
   if (sq.nq * a.group > kFewRows || parts == 1) return;  // complete
+  // offsets that decrease may name a sequence without this row, whose place among the parts would be outside them
+  if (i < sq.q0 || i >= sq.q0 + sq.nq) return;
   constexpr int kGroup = 16, E = (C + 63) / 64;
   const int64_t slot = (int64_t)((uint32_t)sq.k0 / (uint32_t)a.part) + s;
   const float c = a.scale * kLog2e;
