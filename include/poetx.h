@@ -924,6 +924,9 @@ poetx_status poetx_attn_bwd(const poetx_attn_desc* desc, int32_t batch, int64_t 
  * vocab - 1 asks for nothing: logp = 0, and no gradient through it.  A row of
  * -infinities has lse = -infinity, logp = -infinity (or 0), H = 0 and no gradient;
  * one with a NaN or +infinity gives NaN.  All sums are fp32.
+ * Where scale takes a row's largest finite logit out of fp32's range, logp, H and
+ * the top log probabilities are still those of the differences; lse is held at the
+ * end of the range.
  */
 typedef struct {
   int32_t vocab;     /* columns, 1 .. 2^20 */
@@ -957,8 +960,9 @@ poetx_status poetx_logp_fwd(const poetx_logp_desc* desc, int64_t T, const void* 
  * Backward: the gradient of the logits for upstream gradients of logp and H,
  *     dX_j = scale (dlogp (1[j = target] - p_j) - dentropy p_j (log p_j + H))
  *   lse, entropy  of the forward of these rows (entropy: NULL without dentropy).
- *            log p_j is taken as x_j - lse here: in a row whose largest logit is
- *            2^20 and more in size, p loses the digits that lse has lost.
+ *            log p_j is taken as x_j - lse here (x_j held below fp32's largest
+ *            value as lse is): in a row whose largest scaled logit is 2^20 and more
+ *            in size, p loses the digits that lse has lost.
  *   target, dlogp      NULL for none (both)
  *   dentropy           fp32 [T], or NULL
  *   dX       out [T] pitch lddx; may be X (same pitch), else shares no cell with it

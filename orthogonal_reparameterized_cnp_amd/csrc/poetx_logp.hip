@@ -5,7 +5,8 @@
 // sum s of 2^y and the sum w of y 2^y, y = c (x - m); a new maximum takes both over:
 //     d = c (m - m'):  w' = 2^d (w + d s),  s' = 2^d s.
 // Then lse = scale m + ln 2 log2 s, and the entropy is ln 2 (log2 s - w / s): logits are only subtracted from logits,
-// which is exact near the maximum and does not overflow where a mask holds the type's lowest value.  The row is read once
+// which is exact near the maximum, and the sums do not overflow where a mask holds the type's lowest value (lse may, with a
+// scale above 1, and is held within the range).  The row is read once
 // and nothing is written but a few words, so memory bounds the kernel while there are rows for the whole card: 1024 rows of
 // 128k logits in bf16 (262 MB) 51 to 55 us, 4.8 to 5.1 TB/s; 2.1 GB at 5.5, which is this card's rate of reading.  With
 // fewer, a row is cut into parts whose sums a second launch joins: one row of 131072 with 8 alternatives takes 7.7 + 6.7 us.
@@ -26,6 +27,7 @@ using namespace pxk;
 
 constexpr int kThreads = 256, kWaves = kThreads / 64;
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
+constexpr float kMost = 3.402823466e38f;  // the largest fp32
 
 struct Sums {
   float m, s, w;
@@ -140,7 +142,10 @@ PX_DEV void finish(const Sums& v, const TopList& best, const T* x, int64_t row, 
   const float ls = log2f(v.s);
   const float m = finite_or_0(v.m), log_sum = kLn2 * ls;
   if (lane == 0) {
-    o.lse[row] = m * scale + log_sum;
+    // A scale above 1 takes finite logits out of the range.  Their lse stays at its end: infinities are those of rows
+    // without a finite logit, and the backward tells them apart by that.
+    const float l = m * scale + log_sum;
+    o.lse[row] = v.s > 0.f ? fminf(fmaxf(l, -kMost), kMost) : l;
     if (o.entropy) o.entropy[row] = v.s == 0.f ? 0.f : kLn2 * (ls - v.w / v.s);
     if (o.logp) {
       const int t = o.target[row];
@@ -302,7 +307,7 @@ __global__ __launch_bounds__(kThreads) void k_logp_bwd(const T* X, int64_t ldx, 
   const float a = t >= 0 && !none ? scale * dlogp[row] : 0.f;
   const float b = ENT && !none ? scale * dentropy[row] : 0.f, h = ENT ? entropy[row] : 0.f;
   const auto grad = [&](float f, int at) {
-    const float y = none ? -INFINITY : f * scale - l, p = exp2_of(y * kLog2e);
+    const float y = none ? -INFINITY : fminf(f * scale, kMost) - l, p = exp2_of(y * kLog2e);
     float g = -a * p;
     if (ENT) g -= b * (p * (fmaxf(y, -3e38f) + h));
     return at == t ? g + a : g;
