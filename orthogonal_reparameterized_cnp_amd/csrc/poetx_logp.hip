@@ -303,7 +303,8 @@ __global__ __launch_bounds__(kThreads) void k_logp_bwd(const T* X, int64_t ldx, 
   const float l = lse[row];
   int t = target ? target[row] : -1;
   if (t < 0 || t >= V) t = -1;
-  const bool none = l == -INFINITY;  // no finite logit
+  // no finite logit, or nothing asked for, whose gradient is 0 whatever the row holds (NaN in a batch's padding)
+  const bool none = l == -INFINITY || (!ENT && t < 0);
   const float a = t >= 0 && !none ? scale * dlogp[row] : 0.f;
   const float b = ENT && !none ? scale * dentropy[row] : 0.f, h = ENT ? entropy[row] : 0.f;
   const auto grad = [&](float f, int at) {
