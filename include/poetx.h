@@ -880,8 +880,9 @@ size_t poetx_attn_workspace_size(const poetx_attn_desc* desc, int32_t batch, int
  *          Tq / batch rows (which must be whole).
  *   cu_k   the same for the Tk key rows
  *   Q      [Tq] rows of heads head_dim;  K, V  [Tk] rows of kv_heads head_dim
- *   O      out [Tq] rows of heads head_dim; shares no cell with Q, K or V
- *   lse    out fp32 [heads][Tq]
+ *   O      out [Tq] rows of heads head_dim
+ *   lse    out fp32 [heads][Tq].  O and lse share no cell with an operand or
+ *          one another.
  *   ws     >= poetx_attn_workspace_size(desc, batch, Tq, Tk, POETX_OP_FWD)
  *   batch  1 .. 65536;  Tq, Tk  0 .. 2^30.  Tq = 0 is a no-op.
  * A launch takes all rows: heads (Tq / 128 + batch) and
@@ -949,6 +950,7 @@ size_t poetx_logp_workspace_size(const poetx_logp_desc* desc, int64_t T);
  *   top_ids, top_logp  out int32 and fp32 [T][top]: the `top` largest logits of
  *            each row from the largest down, the lower index first among equal
  *            ones, with x - lse (NaN counts as the largest); NULL with top = 0
+ *            The results share no cell with X, target or one another.
  *   ws       >= poetx_logp_workspace_size(desc, T)
  * T 0 (a no-op) .. 2^30.
  * Errors: POETX_E_NULL, POETX_E_SHAPE, POETX_E_DTYPE, POETX_E_WORKSPACE, POETX_E_HIP.
@@ -966,7 +968,8 @@ poetx_status poetx_logp_fwd(const poetx_logp_desc* desc, int64_t T, const void* 
  *            in size, p loses the digits that lse has lost.
  *   target, dlogp      NULL for none (both)
  *   dentropy           fp32 [T], or NULL
- *   dX       out [T] pitch lddx; may be X (same pitch), else shares no cell with it
+ *   dX       out [T] pitch lddx; may be X (same pitch), else shares no cell with
+ *            it, nor with any other operand
  * desc->top is not used.  Errors: POETX_E_NULL, POETX_E_SHAPE, POETX_E_DTYPE, POETX_E_HIP.
  */
 poetx_status poetx_logp_bwd(const poetx_logp_desc* desc, int64_t T, const void* X, int64_t ldx, const int32_t* target,

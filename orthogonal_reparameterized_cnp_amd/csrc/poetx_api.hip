@@ -1835,15 +1835,17 @@ struct Mat {
   const void* p;
   uint64_t rows, width, pitch;
 };
-// Whether two matrices share a cell.  With one pitch they may lie in each other's gaps (columns of one buffer); with two
-// they must lie apart.
+// `bytes` in one piece, as a matrix of one row
+Mat array(const void* p, uint64_t bytes) { return Mat{p, bytes ? 1u : 0u, bytes, bytes}; }
+// Whether two matrices share a cell.  With one pitch they may lie in each other's gaps (columns of one buffer), and a single
+// row in another's; with two pitches they must lie apart.
 bool share(const Mat& x, const Mat& y) {
   if (!x.p || !y.p || !x.rows || !y.rows) return false;
   const bool swap = reinterpret_cast<uintptr_t>(x.p) > reinterpret_cast<uintptr_t>(y.p);
   const Mat &a = swap ? y : x, &b = swap ? x : y;
   const uint64_t off = reinterpret_cast<uintptr_t>(b.p) - reinterpret_cast<uintptr_t>(a.p);
   if (off >= (a.rows - 1) * a.pitch + a.width) return false;
-  if (a.pitch != b.pitch) return true;
+  if (a.pitch != b.pitch && b.rows > 1) return true;
   // row j of b begins r behind the beginning of a's row q + j
   const uint64_t q = off / a.pitch, r = off % a.pitch;
   return r < a.width || (r + b.width > a.pitch && q + 1 < a.rows);
@@ -1985,8 +1987,7 @@ poetx_status poetx_rope(const poetx_rope_desc* desc, int64_t T, const int32_t* p
     in.push_back(Mat{X[i], (uint64_t)T, cols * es, ldx[i] * es});
     out.push_back(Mat{Y[i], (uint64_t)T, cols * es, ldy[i] * es});
   }
-  const uint64_t pos_bytes = (uint64_t)T * 4, table_bytes = (uint64_t)desc->rot_dim * 4;
-  const Mat places{pos, 1, pos_bytes, pos_bytes}, table{freqs, 1, table_bytes, table_bytes};
+  const Mat places = array(pos, (uint64_t)T * 4), table = array(freqs, (uint64_t)desc->rot_dim * 4);
   for (int i = 0; i < count; ++i) {
     bool bad = share(out[i], places) || share(out[i], table);
     for (int j = 0; j < count; ++j) {
@@ -2026,9 +2027,13 @@ poetx_status poetx_attn_fwd(const poetx_attn_desc* desc, int32_t batch, int64_t 
   }
   if (!lse) return fail(POETX_E_NULL, "lse is NULL");
   const Mat o{O, (uint64_t)Tq, nq * es, ldo * es};
-  if (share(o, Mat{Q, (uint64_t)Tq, nq * es, ldq * es}) || share(o, Mat{K, (uint64_t)Tk, nk * es, ldk * es}) ||
-      share(o, Mat{V, (uint64_t)Tk, nk * es, ldv * es}))
-    return fail(POETX_E_SHAPE, "O must share no cell with Q, K or V");
+  const Mat sums = array(lse, (uint64_t)a.heads * Tq * 4);
+  const uint64_t offsets = ((uint64_t)batch + 1) * 4;
+  bool bad = share(o, sums);
+  for (const Mat& m : {Mat{Q, (uint64_t)Tq, nq * es, ldq * es}, Mat{K, (uint64_t)Tk, nk * es, ldk * es},
+                       Mat{V, (uint64_t)Tk, nk * es, ldv * es}, array(cu_q, offsets), array(cu_k, offsets)})
+    bad |= share(o, m) || share(sums, m);
+  if (bad) return fail(POETX_E_SHAPE, "O and lse must share no cell with Q, K, V, the offsets or one another");
   if ((st = check_ws(ws, ws_bytes, attn_fwd_ws_bytes(a))) != POETX_OK) return st;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   PX_HIP(attn_fwd(a, AttnMat{Q, ldq}, AttnMat{K, ldk}, AttnMat{V, ldv}, O, ldo, lse, ws, s));
@@ -2063,6 +2068,8 @@ poetx_status poetx_attn_bwd(const poetx_attn_desc* desc, int32_t batch, int64_t 
     (o.written ? out : in).push_back(Mat{o.p, (uint64_t)rows, cols * es, o.ld * es});
   }
   if (Tq > 0 && !lse) return fail(POETX_E_NULL, "lse is NULL");
+  in.push_back(array(lse, (uint64_t)a.heads * Tq * 4));
+  for (const int32_t* cu : {cu_q, cu_k}) in.push_back(array(cu, ((uint64_t)batch + 1) * 4));
   for (size_t i = 0; i < out.size(); ++i) {
     bool bad = false;
     for (const Mat& m : in) bad |= share(out[i], m);
@@ -2092,6 +2099,14 @@ poetx_status poetx_logp_fwd(const poetx_logp_desc* desc, int64_t T, const void* 
   if ((target != nullptr) != (logp != nullptr)) return fail(POETX_E_NULL, "logp is written with targets, and only then");
   if ((desc->top > 0) != (top_ids != nullptr) || (desc->top > 0) != (top_logp != nullptr))
     return fail(POETX_E_NULL, "top_ids and top_logp are written with top > 0, and only then");
+  const uint64_t row = desc->vocab * dt_size(desc->act_dtype), each = (uint64_t)T * 4;
+  const Mat out[] = {array(logp, each), array(lse, each), array(entropy, each), array(top_ids, each * desc->top),
+                     array(top_logp, each * desc->top)};
+  for (const Mat& m : out) {
+    bool bad = share(m, Mat{X, (uint64_t)T, row, ldx * dt_size(desc->act_dtype)}) || share(m, array(target, each));
+    for (const Mat* o = out; o != &m; ++o) bad |= share(*o, m);
+    if (bad) return fail(POETX_E_SHAPE, "the results must share no cell with X, the targets or one another");
+  }
   if ((st = check_ws(ws, ws_bytes, poetx_logp_workspace_size(desc, T))) != POETX_OK) return st;
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   PX_HIP(logp_fwd(desc->act_dtype, T, desc->vocab, desc->top, desc->scale, X, ldx, target, logp, lse, entropy, top_ids,
@@ -2114,6 +2129,9 @@ poetx_status poetx_logp_bwd(const poetx_logp_desc* desc, int64_t T, const void* 
   if (X == dX && ldx != lddx) return fail(POETX_E_SHAPE, "dX in place of X must have its pitch");
   if (X != dX && share(Mat{X, (uint64_t)T, width, ldx * es}, Mat{dX, (uint64_t)T, width, lddx * es}))
     return fail(POETX_E_SHAPE, "dX must be X or share no cell with it");
+  for (const void* p : {(const void*)target, (const void*)lse, (const void*)entropy, (const void*)dlogp, (const void*)dentropy})
+    if (share(Mat{dX, (uint64_t)T, width, lddx * es}, array(p, (uint64_t)T * 4)))
+      return fail(POETX_E_SHAPE, "dX must share no cell with the targets, the forward's sums or the upstream gradients");
   hipStream_t s = reinterpret_cast<hipStream_t>(stream);
   PX_HIP(logp_bwd(desc->act_dtype, T, desc->vocab, desc->scale, X, ldx, target, lse, entropy, dlogp, dentropy, dX, lddx,
                   s));
