@@ -1103,7 +1103,8 @@ class PoetxLogProb:
 
     def backward(self, dlogp: Optional[torch.Tensor] = None, dentropy: Optional[torch.Tensor] = None,
                  dX: Optional[torch.Tensor] = None, stream=None) -> torch.Tensor:
-        """The gradient of the last forward's logits, in dX (which may be the logits) or a new tensor."""
+        """The gradient of the last forward's logits, in dX or a new tensor.  dX may be the logits: the saved state ends
+        with them, and the next backward needs a forward first."""
         if self.saved is None:
             raise ValueError("backward before a forward: there is no saved state")
         X, target, lse, entropy = self.saved
@@ -1122,4 +1123,6 @@ class PoetxLogProb:
             B.poetx_logp_bwd(self.desc, T, X, ldx, None if dlogp is None else target, lse, entropy, dlogp, dentropy, dX,
                              lddx)
             _keep(self._saved_on, *[t for t in (X, target, lse, entropy) if t is not None])
+        if T and dX.data_ptr() == X.data_ptr():
+            self.saved = None  # the logits are gone
         return dX
