@@ -692,6 +692,13 @@ def _keep(made_on: Optional[int], *tensors):
         t.record_stream(s)
 
 
+def _keep_given(came_on: Optional[int], *tensors):
+    """_keep for operands of a call on a given stream that the layer keeps: they belong to the stream that was current
+    when the call came (came_on), and the layer may be the last to hold them.  None: no stream was given."""
+    if came_on is not None:
+        _keep(came_on, *[t for t in tensors if t is not None])
+
+
 def _made_on(device: torch.device) -> Optional[int]:
     """The handle of the stream that allocations on `device` belong to now (None on the CPU)."""
     if device.type != "cuda":
@@ -759,6 +766,8 @@ class PoetxNorm:
         ldy = _pitch(Y, "Y", T, d, dt, dev) if Y is not None else d
         lds = _pitch(S, "S", T, d, dt, dev) if S is not None else d
         self._params()
+        came_on = None if stream is None else _made_on(dev)
+        given = X if residual is None else S  # which the norm keeps
         with _on(dev, stream):
             if Y is None:
                 Y = torch.empty(T, d, dtype=dt, device=dev)
@@ -766,6 +775,7 @@ class PoetxNorm:
                 S = torch.empty(T, d, dtype=dt, device=dev)
             stats = torch.empty(2 if self.kind == "layer" else 1, T, dtype=torch.float32, device=dev)
             B.poetx_norm_fwd(self.desc, T, X, ldx, residual, ldr, self.weight, self.bias, S, lds, Y, ldy, stats)
+            _keep_given(came_on, given)
             self._saved_on = B._current_stream()
         self.S, self.stats = (X if S is None else S), stats
         return Y if residual is None else (Y, S)
@@ -1019,6 +1029,7 @@ class PoetxAttention:
                 raise ValueError("cu_q and cu_k must have one entry per sequence and one more")
         elif cu_k is not None:
             raise ValueError("cu_k without cu_q")
+        came_on, given = None if stream is None else _made_on(dev), O
         with _on(dev, stream):
             if O is None:
                 O = (torch.empty if cu_q is None else torch.zeros)(Tq, nq, dtype=dt, device=dev)
@@ -1026,6 +1037,7 @@ class PoetxAttention:
             ws = torch.empty(B.poetx_attn_workspace_size(self.desc, batch, Tq, Tk, B.POETX_OP_FWD), dtype=torch.uint8,
                              device=dev)
             B.poetx_attn_fwd(self.desc, batch, Tq, Tk, cu_q, cu_k, Q, ldq, K, ldk, V, ldv, O, ldo, lse, ws, ws.numel())
+            _keep_given(came_on, Q, K, V, given, cu_q, cu_k)
             self._saved_on = B._current_stream()
         self.saved = (Q, K, V, O, lse, cu_q, cu_k, batch)
         return O
@@ -1089,6 +1101,7 @@ class PoetxLogProb:
         if target is not None:
             _check(target, "target", (T,), torch.int32)
             _check_device(dev, target=target)
+        came_on = None if stream is None else _made_on(dev)
         with _on(dev, stream):
             new = lambda *n, dtype=torch.float32: torch.empty(*n, dtype=dtype, device=dev)
             out = LogProbs(None if target is None else new(T), new(T), new(T),
@@ -1097,6 +1110,7 @@ class PoetxLogProb:
             ws = new(B.poetx_logp_workspace_size(self.desc, T), dtype=torch.uint8)
             B.poetx_logp_fwd(self.desc, T, X, ldx, target, out.logp, out.lse, out.entropy, out.top_ids, out.top_logp, ws,
                              ws.numel())
+            _keep_given(came_on, X, target)
             self._saved_on = B._current_stream()
         self.saved = (X, target, out.lse, out.entropy)
         return out
