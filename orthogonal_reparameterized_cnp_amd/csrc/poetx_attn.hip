@@ -31,7 +31,7 @@ using namespace pxk;
 
 constexpr float kLog2e = 1.44269504088896340736f, kLn2 = 0.69314718055994530942f;
 constexpr int kWaves = 4, kThreads = 64 * kWaves;
-constexpr unsigned kAtOnce = 512;  // workgroups that the card holds of the larger kernels
+constexpr unsigned kAtOnce = 512;  // workgroups that the card holds of the bf16 forward and dQ, two a CU (of dK, dV one)
 constexpr int kRows = 32 * kWaves;  // rows of a workgroup: queries (forward, dQ) or keys (dK, dV), 32 a wave
 
 PX_DEV float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -215,6 +215,8 @@ constexpr int64_t kDmaLd = 1 << 23;  // a tile's rows lie within 32 bits
 // `BYTES` from base + at of each lane to the LDS address t + BYTES * lane.  The compiler holds the builtin for a write to any
 // LDS that the transposing reads may read, and waits in front of those for all copies in flight.  Where that is too early,
 // OWN is assembly, of which it counts nothing: copies_done() or a wait of the kernel's own has to stand before the reads.
+// The assembly changes m0, which the compiler holds for its own and lets no clobber name: a kernel takes all its copies in
+// one of the two ways, and has nothing else that needs m0.
 template <int BYTES, bool OWN> PX_DEV void copy_to_lds(char* t, const char* base, uint32_t at) {
   const auto lds = (__attribute__((address_space(3))) char*)t;
   if constexpr (!OWN && BYTES == 16)
@@ -646,8 +648,10 @@ __global__ __launch_bounds__(kThreads * kFwdGroups<T>, HOW ? 2 : 1) void k_attn_
 // With one or a few queries per sequence the keys are read for little work, and there are too few tiles of 128 queries for
 // the card.  Here a tile is 32 rows, a row one query of one of the query heads that share a key head (so that its keys are
 // read once for all of them), and the four waves take 32 keys each of a tile of 128.  By direct copies a wave has its own
-// piece of LDS and waits for nobody: what bounds the kernel is how many bytes are under way, and eight waves a CU that
-// load and compute at different times keep more of them there than two workgroups in step.  A wave's next keys are copied
+// piece of LDS and waits for nobody: what bounds the kernel is how many bytes are under way, and waves that load and
+// compute at different times keep more of them there than workgroups in step.  (Heads of 128 columns take 264 to 296
+// registers in bf16 and 323 in fp32, so that one workgroup stands on a CU; up to 96 columns, in fp32 64, it is two or
+// three.)  A wave's next keys are copied
 // as soon as these are multiplied, during the softmax, and its next values during the next product (64 tokens over 2048
 // keys each 145 -> 130 us).  A workgroup stands for `part` keys of a sequence.  It leaves the maximum, the sum and the
 // unscaled O that they give the sequence's rows, and k_attn_join adds the parts in their order.  Where a sequence has more
@@ -655,7 +659,8 @@ __global__ __launch_bounds__(kThreads * kFwdGroups<T>, HOW ? 2 : 1) void k_attn_
 //
 // HBM bounds it, from some 100 MB of keys on: 64 tokens over 8192 keys each (8 key heads of 128, 2.1 GB) 430 us, 5.0 TB/s,
 // what reading alone reaches; 16 over 1 to 8192 (112 MB) 33.5 us with the join (5), one over 100000 91 us, where the start
-// and end of a launch and parts of unequal sequences count.
+// and end of a launch and parts of unequal sequences count.  fp32, which stages the keys through registers: 16 over 4096
+// each (537 MB) 183 us, 2.9 TB/s, and one over 100000 (819 MB) 259.
 constexpr int kFewRows = 32, kFewKeys = 32 * kWaves;
 template <typename T, int C> struct Few {
   static constexpr int TILES = 2 * RowsOf<T, C>::bytes(kFewKeys);
@@ -1353,8 +1358,10 @@ void pack(const AttnDesc& d, AttnArgs& a, AttnMat* const* mats, const bool* keys
 }
 
 // The keys of a workgroup in the forward of few rows; 0 where a tile of 32 rows does not hold a sequence's queries on the
-// average, and the tiles of 128 queries are taken (16 tokens over 1 to 8192 keys: 732 us with those).  Parts are as long as
-// leaves the card some 512 workgroups, two a CU (256 to 1024 of them measured the same or slower), and a sequence two.
+// average, and the tiles of 128 queries are taken (16 tokens over 1 to 8192 keys: 732 us with those).  The average is the
+// call's, since the host knows no length: a prompt among single tokens goes the way of the most (128 tokens over 4096 keys
+// each, 444 us, with a prompt of 900, 27 us, take 1430 us in one call).  Parts are as long as leaves the card some 512
+// workgroups (256 to 1024 measured the same or slower; heads of 128 columns run them in two turns), and a sequence two.
 int few_part(const AttnDesc& d) {
   if (d.Tq * (d.heads / d.kv_heads) > (int64_t)kFewRows * d.batch) return 0;
   return (int)std::max<int64_t>(256, round_up(std::min(d.Tk * d.kv_heads / 512, d.Tk / (2 * d.batch)), kFewKeys));

@@ -5,17 +5,18 @@
 // sum s of 2^y and the sum w of y 2^y, y = c (x - m); a new maximum takes both over:
 //     d = c (m - m'):  w' = 2^d (w + d s),  s' = 2^d s.
 // Then lse = scale m + ln 2 log2 s, and the entropy is ln 2 (log2 s - w / s): logits are only subtracted from logits,
-// which is exact near the maximum, and the sums do not overflow where a mask holds the type's lowest value (lse may, with a
-// scale above 1, and is held within the range).  The row is read once
-// and nothing is written but a few words, so memory bounds the kernel while there are rows for the whole card: 1024 rows of
-// 128k logits in bf16 (262 MB) 51 to 55 us, 4.8 to 5.1 TB/s; 2.1 GB at 5.5, which is this card's rate of reading.  With
-// fewer, a row is cut into parts whose sums a second launch joins: one row of 131072 with 8 alternatives takes 7.7 + 6.7 us.
+// which is exact near the maximum, and the sums do not overflow where a mask holds the type's lowest value (lse may,
+// with a scale above 1, and is held within the range).  The row is read once and nothing is written but a few words, so
+// memory bounds the kernel while there are rows for the whole card: 4096 rows of 32000 logits in bf16 (262 MB) 47 to 55
+// us, 4.8 to 5.5 TB/s; 2.1 GB at 5.5, which is this card's rate of reading.  With fewer, a row is cut into parts whose
+// sums a second launch joins: one row of 131072 with 8 alternatives takes 7.7 + 6.7 us.
 //
-// The top alternatives come from the same pass.  A logit and its index make one 64-bit key, larger for larger logits and
-// for lower indexes among equal ones; lane i of a wave keeps the wave's i-th largest key so far.  A key that beats the
-// last of them is put in by one ballot (its place) and one shift; of n keys in any order about top (1 + ln(n / top))
-// do, so nearly all of them cost one comparison.  The first keys would all do: they are held against the top-th largest of
-// the lanes' maxima first (23.5 -> 15.6 us for that row).
+// The top alternatives come from the same pass.  A logit and its index make one 64-bit key, larger for larger logits
+// and for lower indexes among equal ones; lane i of a wave keeps the wave's i-th largest key so far.  A key that beats
+// the last of them is put in by one ballot (its place) and one shift; of n keys in any order about top (1 + ln(n /
+// top)) do, so nearly all of them cost one comparison (those that do follow each other: 8 alternatives of the 4096 rows
+// 106 us).  The first keys would all do: they are held against the top-th largest of the lanes' maxima first (23.5 ->
+// 15.6 us for that row).
 #include <algorithm>
 
 #include "common.h"

@@ -989,7 +989,8 @@ class PoetxAttention:
     forward, once that stream waits for the forward's.
 
     cu_q, cu_k: int32 [sequences + 1], the first rows of the sequences (cu_k None: those of cu_q); or neither, and
-    `batch` equal sequences.  Rows that belong to no sequence are not written; a new tensor holds zeros there."""
+    `batch` equal sequences.  Rows that belong to no sequence are not written; with offsets a new tensor is filled with zeros
+    for their sake, which a given O, dQ, dK and dV spare (16 tokens over 112 MB of keys: 39 us, 36 with a given O)."""
 
     def __init__(self, heads: int, kv_heads: int, head_dim: int, act: str = "bf16", causal: bool = True, window: int = 0,
                  scale: Optional[float] = None, device: str = "cuda"):
