@@ -308,8 +308,12 @@ __global__ __launch_bounds__(kThreads) void k_logp_bwd(const T* X, int64_t ldx, 
   const bool none = l == -INFINITY || (!ENT && t < 0);
   const float a = t >= 0 && !none ? scale * dlogp[row] : 0.f;
   const float b = ENT && !none ? scale * dentropy[row] : 0.f, h = ENT ? entropy[row] : 0.f;
+  // log p of logits beyond the range in a row whose lse is held at its end; others keep what the fma gives
+  const float most = l == kMost ? 0.f : INFINITY;
   const auto grad = [&](float f, int at) {
-    const float y = none ? -INFINITY : fminf(f * scale, kMost) - l, p = exp2_of(y * kLog2e);
+    float y = none ? -INFINITY : f * scale - l;
+    y = y > most ? most : y;  // NaN stays
+    const float p = exp2_of(y * kLog2e);
     float g = -a * p;
     if (ENT) g -= b * (p * (fmaxf(y, -3e38f) + h));
     return at == t ? g + a : g;
