@@ -922,10 +922,10 @@ poetx_status poetx_attn_bwd(const poetx_attn_desc* desc, int32_t batch, int64_t 
  *     lse = log sum_j exp(x_j),  logp = x_target - lse
  *     H = -sum_j p_j log p_j,  p_j = exp(x_j - lse)
  * A logit of -infinity has p = 0 and adds nothing.  A target outside 0 ..
- * vocab - 1 asks for nothing: logp = 0, and no gradient through it (0 without
- * dentropy, whatever the row holds).  A row of -infinities has lse = -infinity,
- * logp = -infinity (or 0), H = 0 and no gradient; one with a NaN or +infinity
- * gives NaN for what is asked of it.  All sums are fp32.
+ * vocab - 1 asks for nothing: logp = 0, and no gradient through it.  A row of
+ * -infinities has lse = -infinity, logp = -infinity (or 0), H = 0 and no gradient;
+ * one with a NaN or +infinity gives NaN, but a gradient of 0 where nothing is asked
+ * of it (no target or dlogp = 0, and no dentropy or dentropy = 0).  All sums are fp32.
  * Where scale takes a row's largest finite logit out of fp32's range, logp, H and
  * the top log probabilities are still those of the differences; lse is held at the
  * end of the range.

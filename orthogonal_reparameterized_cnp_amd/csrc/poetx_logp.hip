@@ -301,13 +301,14 @@ __global__ __launch_bounds__(kThreads) void k_logp_bwd(const T* X, int64_t ldx, 
   const T* x = X + row * ldx;
   T* dx = dX + row * lddx;
   const int c0 = part * span, c1 = min(V, c0 + span);
-  const float l = lse[row];
+  // the row's values on the way together, none behind a test of another
+  const float l = lse[row], H = ENT ? entropy[row] : 0.f, dh = ENT ? dentropy[row] : 0.f, dl = target ? dlogp[row] : 0.f;
   int t = target ? target[row] : -1;
   if (t < 0 || t >= V) t = -1;
-  // no finite logit, or nothing asked for, whose gradient is 0 whatever the row holds (NaN in a batch's padding)
-  const bool none = l == -INFINITY || (!ENT && t < 0);
-  const float a = t >= 0 && !none ? scale * dlogp[row] : 0.f;
-  const float b = ENT && !none ? scale * dentropy[row] : 0.f, h = ENT ? entropy[row] : 0.f;
+  const float a = t >= 0 && l != -INFINITY ? scale * dl : 0.f, b = ENT && l != -INFINITY ? scale * dh : 0.f;
+  // no finite logit, or nothing asked for: the gradient is 0 whatever the row holds (NaN in a batch's padding)
+  const bool none = a == 0.f && b == 0.f;
+  const float h = none ? 0.f : H;
   // log p of logits beyond the range in a row whose lse is held at its end; others keep what the fma gives
   const float most = l == kMost ? 0.f : INFINITY;
   const auto grad = [&](float f, int at) {

@@ -36,3 +36,21 @@ def test_ignored_rows_have_no_gradient(act, T, V):
     # no targets at all
     op.forward(X)
     assert not op.backward().any()
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("T,V", [(6, 5001), (1200, 300)])
+def test_rows_of_no_upstream_gradient_have_none(act, T, V):
+    """Padding that is masked in the loss: upstream gradients of 0, with targets like any others."""
+    op = PoetxLogProb(V, act)
+    X, t = LP.logits(T, V, act, 2), torch.zeros(T, dtype=torch.int32, device="cuda")
+    a, b = torch.full((T,), 0.5, device="cuda"), torch.full((T,), 0.25, device="cuda")
+    a[:3], b[:3] = 0, 0
+    a[1], t[2] = -0.0, -1
+    op.forward(X, t)
+    want, only = op.backward(a, b), op.backward(None, b)
+    Y = X.clone()
+    Y[0], Y[1, 5], Y[2, 7] = float("nan"), float("inf"), float("nan")
+    op.forward(Y, t)
+    for dX, ref in ((op.backward(a, b), want), (op.backward(None, b), only)):
+        assert not dX[:3].any() and torch.equal(dX[3:], ref[3:]) and ref[3:].any() and torch.isfinite(ref).all()
